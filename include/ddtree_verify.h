@@ -63,6 +63,7 @@ struct CUevent_st;                   /* cudaEvent_t  == struct CUevent_st*  */
 #define DDTREE_MAX_NODES 64          /* ancestor sets are one 64-bit mask */
 #define DDTREE_MAX_HEADS 128
 #define DDTREE_MAX_BATCH 1024
+#define DDTREE_MAX_PAGE_SIZE 65536   /* tokens of a page, where caches have pages */
 
 enum ddtree_status {
   DDTREE_OK = 0,
@@ -81,6 +82,7 @@ enum ddtree_status {
 #define DDTREE_ST_TIMEOUT     0x8u   /* a bounded wait in a kernel expired    */
 #define DDTREE_ST_OVERLAP     0x10u  /* relocation: a destination row is busy  */
 #define DDTREE_ST_BAD_MASK    0x20u  /* a custom mask that is not a tree mask  */
+#define DDTREE_ST_NO_PAGES    0x40u  /* step maps: the free list runs out      */
 
 /* Kernel variants of the split-KV partial stage. */
 #define DDTREE_KERNEL_AUTO 0

@@ -30,6 +30,14 @@ DDTREE_ST_BAD_LENGTH = 0x4
 DDTREE_ST_TIMEOUT = 0x8
 DDTREE_ST_OVERLAP = 0x10
 DDTREE_ST_BAD_MASK = 0x20
+DDTREE_ST_NO_PAGES = 0x40
+
+DDTREE_ROPE_PLAIN = 0
+DDTREE_ROPE_LINEAR = 1
+DDTREE_ROPE_YARN = 2
+
+DDTREE_BF16 = 0
+DDTREE_FP16 = 1
 
 DDTREE_KERNEL_AUTO = 0
 DDTREE_KERNEL_SIMT = 1
@@ -42,7 +50,8 @@ EXPORTS = (
     "ddtree_verify_mla_check", "ddtree_status_str", "ddtree_verify_mla_batched_timed",
     "ddtree_verify_mla_noalloc", "ddtree_accept_greedy_workspace_size", "ddtree_accept_greedy",
     "ddtree_relocate_kv_workspace_size", "ddtree_relocate_kv",
-    "ddtree_tree_from_mask_workspace_size", "ddtree_tree_from_mask",
+    "ddtree_tree_from_mask_workspace_size", "ddtree_tree_from_mask", "ddtree_step_maps",
+    "ddtree_rope_init", "ddtree_mla_append", "ddtree_draft_append",
 )
 
 
@@ -61,6 +70,19 @@ class Plan(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {k: getattr(self, k) for k, _ in self._fields_ if k != "reserved"}
+
+
+class Rope(ctypes.Structure):
+    """A rotation (ddtree_rope_t), made by ddtree_rope_init."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 128)]
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 class DDTreeError(RuntimeError):
@@ -108,6 +130,16 @@ def library() -> ctypes.CDLL:
     L.ddtree_tree_from_mask_workspace_size.restype = sz
     L.ddtree_tree_from_mask.argtypes = [i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
     L.ddtree_tree_from_mask.restype = i32
+    L.ddtree_step_maps.argtypes = [i32, i32, i32, i64, vp, i32, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp,
+                                   vp, vp, i64, vp, vp, vp, vp, vp, vp]
+    L.ddtree_step_maps.restype = i32
+    f64 = ctypes.c_double
+    L.ddtree_rope_init.argtypes = [i32, i32, f64, i32, f64, i32, f64, f64, f64, vp]
+    L.ddtree_rope_init.restype = i32
+    L.ddtree_mla_append.argtypes = [i64, i32, vp, vp, i64, vp, f32, vp, i64, i64, vp, vp, vp, i64, vp, i64, i64, vp, vp]
+    L.ddtree_mla_append.restype = i32
+    L.ddtree_draft_append.argtypes = [i64, i32, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, vp, vp, i64, vp, vp]
+    L.ddtree_draft_append.restype = i32
     for name in ("ddtree_verify_mla_plan", "ddtree_verify_mla_plan_ex", "ddtree_verify_mla",
                  "ddtree_verify_mla_batched", "ddtree_build_ancestor_mask", "ddtree_verify_mla_check",
                  "ddtree_verify_mla_batched_timed", "ddtree_verify_mla_noalloc"):
@@ -365,3 +397,211 @@ def ddtree_tree_from_mask(custom_mask: torch.Tensor, mask_indptr: torch.Tensor, 
         _dev(prefix_lens, torch.int32, "prefix_lens"), _dev(tree_parent, torch.int32, "tree_parent"),
         None if anc_bits is None else _dev(anc_bits, torch.int64, "anc_bits"),
         _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "tree_from_mask")
+
+
+class _Bound:
+    """A call whose arguments are checked and marshalled once, for callers
+    whose buffers stay the same (see BoundVerify).  Calling the object launches
+    on `stream`, with the device of the buffers current.  It keeps references
+    to the tensors; they must not be resized or moved in place while the object
+    is used."""
+    _entry = ""
+
+    def _bind(self, args, keep) -> None:
+        self._args, self._keep = args, keep
+        self._fn = getattr(library(), self._entry)
+        self._device = torch.cuda.current_device()
+
+    def __call__(self, stream=None) -> None:
+        if torch.cuda.current_device() != self._device:
+            raise ValueError(f"{self._entry}: bound on cuda:{self._device}, which is not the current device")
+        _check(self._fn(*self._args, _stream(stream)), self._entry)
+
+
+def _opt(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, numel: Optional[int] = None,
+         device: Optional[int] = None) -> Optional[int]:
+    return None if t is None else _dev(t, dtype, name, numel, device=device)
+
+
+def _maps_args(page_table, prefix_lens, max_new, page_size, n_pages, kv_indptr, kv_indices, new_slots, positions,
+               table_row, new_lens, tree_parent, pages_held, free_pages, free_head, pages_held_out, free_head_out,
+               new_indptr, token_rows, status):
+    i32 = torch.int32
+    table = _dev(page_table, i32, "page_table")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [rows, pages of a row]")
+    d = page_table.get_device()
+    b, t = int(prefix_lens.numel()), int(max_new)
+    n_free = 0 if free_pages is None else int(free_pages.numel())
+    return (b, t, int(page_size), int(n_pages), table, int(page_table.shape[0]), int(page_table.shape[1]),
+            _opt(table_row, i32, "table_row", b, d), _dev(prefix_lens, i32, "prefix_lens", device=d),
+            _opt(new_lens, i32, "new_lens", b, d), _opt(tree_parent, i32, "tree_parent", b * t, d),
+            _opt(pages_held, i32, "pages_held", b, d), _opt(free_pages, i32, "free_pages", device=d), n_free,
+            _opt(free_head, i32, "free_head", 1, d), _opt(pages_held_out, i32, "pages_held_out", b, d),
+            _opt(free_head_out, i32, "free_head_out", 1, d), _dev(kv_indptr, i32, "kv_indptr", b + 1, device=d),
+            _opt(kv_indices, i32, "kv_indices", device=d), 0 if kv_indices is None else int(kv_indices.numel()),
+            _opt(new_indptr, i32, "new_indptr", b + 1, d), _dev(new_slots, i32, "new_slots", b * t, device=d),
+            _dev(positions, i32, "positions", b * t, device=d), _opt(token_rows, i32, "token_rows", b * t, d),
+            _opt(status, i32, "status", 1, d))
+
+
+def ddtree_step_maps(page_table: torch.Tensor, prefix_lens: torch.Tensor, max_new: int, page_size: int, n_pages: int,
+                     kv_indptr: torch.Tensor, kv_indices: Optional[torch.Tensor], new_slots: torch.Tensor,
+                     positions: torch.Tensor, *, table_row: Optional[torch.Tensor] = None,
+                     new_lens: Optional[torch.Tensor] = None, tree_parent: Optional[torch.Tensor] = None,
+                     pages_held: Optional[torch.Tensor] = None, free_pages: Optional[torch.Tensor] = None,
+                     free_head: Optional[torch.Tensor] = None, pages_held_out: Optional[torch.Tensor] = None,
+                     free_head_out: Optional[torch.Tensor] = None, new_indptr: Optional[torch.Tensor] = None,
+                     token_rows: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """Page-table growth, verify index layout, slots and positions of a step
+    from the requests' lengths (include/ddtree_maps.h).  page_table int32
+    [rows, pages of a row], grown in place; the batch is prefix_lens.numel()."""
+    _check(library().ddtree_step_maps(
+        *_maps_args(page_table, prefix_lens, max_new, page_size, n_pages, kv_indptr, kv_indices, new_slots, positions,
+                    table_row, new_lens, tree_parent, pages_held, free_pages, free_head, pages_held_out,
+                    free_head_out, new_indptr, token_rows, status), _stream(stream)), "ddtree_step_maps")
+
+
+class BoundStepMaps(_Bound):
+    """ddtree_step_maps with its arguments checked and marshalled once."""
+    _entry = "ddtree_step_maps"
+
+    def __init__(self, page_table, prefix_lens, max_new: int, page_size: int, n_pages: int, kv_indptr, kv_indices,
+                 new_slots, positions, *, table_row=None, new_lens=None, tree_parent=None, pages_held=None,
+                 free_pages=None, free_head=None, pages_held_out=None, free_head_out=None, new_indptr=None,
+                 token_rows=None, status=None):
+        a = (page_table, prefix_lens, max_new, page_size, n_pages, kv_indptr, kv_indices, new_slots, positions,
+             table_row, new_lens, tree_parent, pages_held, free_pages, free_head, pages_held_out, free_head_out,
+             new_indptr, token_rows, status)
+        self._bind(_maps_args(*a), a)
+
+
+def ddtree_rope_init(rot_dim: int, *, theta: float, interleaved: bool = False, scaling: int = DDTREE_ROPE_PLAIN,
+                     factor: float = 1.0, original_positions: int = 1, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     mscale: float = 0.0) -> Rope:
+    """A rotation for the append calls (include/ddtree_append.h); host only."""
+    rope = Rope()
+    _check(library().ddtree_rope_init(int(rot_dim), int(bool(interleaved)), float(theta), int(scaling), float(factor),
+                                      int(original_positions), float(beta_fast), float(beta_slow), float(mscale),
+                                      ctypes.addressof(rope)), "ddtree_rope_init")
+    return rope
+
+
+def _rows(t: torch.Tensor, dtype: torch.dtype, name: str, shape: tuple, device: int) -> int:
+    """Pointer of a strided tensor of `shape` whose last dimension is dense."""
+    p = _dev(t, dtype, name, contiguous=False, device=device)
+    if tuple(t.shape) != shape or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be {list(shape)} with unit-stride columns, got {list(t.shape)}")
+    return p
+
+
+def _step(t: torch.Tensor, d: int, least: int) -> int:
+    """Stride of dimension d; a dimension of one element has none of its own."""
+    return int(t.stride(d)) if t.shape[d] > 1 else least
+
+
+def _mla_append_args(rope, kv_new, positions, slots, kv_pool, latent_weight, eps, q_rope, q_out, status):
+    bf, i32 = torch.bfloat16, torch.int32
+    if kv_new.dim() != 2 or kv_pool.dim() != 2 or kv_pool.shape[1] != 576:
+        raise ValueError("kv_new must be [tokens, 576] and kv_pool [rows, 576]")
+    pool = _dev(kv_pool, bf, "kv_pool")
+    d, n = kv_pool.get_device(), int(kv_new.shape[0])
+    kv = _rows(kv_new, bf, "kv_new", (n, 576), d)
+    heads, q, o = 0, (None, 64, 64), (None, 64, 64)
+    if (q_rope is None) != (q_out is None):
+        raise ValueError("q_rope and q_out come together")
+    if q_rope is not None and q_rope.numel() > 0:
+        heads = int(q_rope.shape[1])
+        q = (_rows(q_rope, bf, "q_rope", (n, heads, 64), d), _step(q_rope, 0, 64), _step(q_rope, 1, 64))
+        o = (_rows(q_out, bf, "q_out", (n, heads, 64), d), _step(q_out, 0, 64), _step(q_out, 1, 64))
+    return (n, heads, ctypes.addressof(rope), kv, _step(kv_new, 0, 576),
+            _opt(latent_weight, bf, "latent_weight", 512, d), float(eps), *q,
+            _dev(positions, i32, "positions", n, device=d), _dev(slots, i32, "slots", n, device=d), pool,
+            int(kv_pool.shape[0]), *o, _opt(status, i32, "status", 1, d))
+
+
+def ddtree_mla_append(rope: Rope, kv_new: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                      kv_pool: torch.Tensor, *, latent_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      q_rope: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Norm, rotation and pool rows of new tokens, and their queries' rope part
+    (include/ddtree_append.h).  kv_new [N, 576] (rows may be strided), q_rope
+    and q_out [N, H, 64] (tokens and heads may be strided; q_out may be q_rope)."""
+    _check(library().ddtree_mla_append(
+        *_mla_append_args(rope, kv_new, positions, slots, kv_pool, latent_weight, eps, q_rope, q_out, status),
+        _stream(stream)), "ddtree_mla_append")
+
+
+class BoundMlaAppend(_Bound):
+    """ddtree_mla_append with its arguments checked and marshalled once."""
+    _entry = "ddtree_mla_append"
+
+    def __init__(self, rope: Rope, kv_new, positions, slots, kv_pool, *, latent_weight=None, eps: float = 1e-6,
+                 q_rope=None, q_out=None, status=None):
+        a = (rope, kv_new, positions, slots, kv_pool, latent_weight, eps, q_rope, q_out, status)
+        self._bind(_mla_append_args(*a), a)
+
+
+class DraftCache:
+    """The drafter's paged cache (ddtree_draft_cache_t): k and v are
+    [pages, page_size, kv_heads, head_dim] tensors of one dtype (bf16 or fp16)
+    and equal strides; a view with the heads outside the tokens serves too."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        dtype = {torch.bfloat16: DDTREE_BF16, torch.float16: DDTREE_FP16}.get(k.dtype)
+        if dtype is None:
+            raise TypeError(f"a draft cache is bfloat16 or float16, got {k.dtype}")
+        if k.dim() != 4:
+            raise ValueError("a draft cache is [pages, page_size, kv_heads, head_dim]")
+        kp = _rows(k, k.dtype, "k cache", tuple(k.shape), torch.cuda.current_device())
+        vp = _rows(v, k.dtype, "v cache", tuple(k.shape), k.get_device())
+        step = [_step(k, d, int(k.shape[3])) for d in range(3)]
+        if step != [_step(v, d, int(k.shape[3])) for d in range(3)]:
+            raise ValueError("the key and value caches must have equal strides")
+        self.k, self.v = k, v
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = (int(x) for x in k.shape)
+        self.struct = _CacheStruct(kp, vp, self.n_pages, *step, self.page_size, self.n_kv_heads, self.head_dim, dtype)
+
+
+def _draft_append_args(cache, rope, q, k, v, positions, slots, q_out, q_weight, k_weight, eps, status):
+    dt, i32, d = cache.k.dtype, torch.int32, cache.k.get_device()
+    if cache.k.get_device() != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {cache.k.device}, not the current device")
+    n, dim, kvh = int(k.shape[0]), cache.head_dim, cache.n_kv_heads
+
+    def heads(t, name, h):
+        p = _rows(t, dt, name, (n, h, dim), d)
+        if h > 1 and n and t.stride(1) != dim:
+            raise ValueError(f"{name}: heads must be {dim} elements apart")
+        return p, _step(t, 0, h * dim)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    h = int(q.shape[1]) if q is not None else 0
+    qa, oa = (heads(q, "q", h), heads(q_out, "q_out", h)) if h else ((None, 0), (None, 0))
+    return (n, h, ctypes.addressof(cache.struct), ctypes.addressof(rope), *qa, *heads(k, "k", kvh), *heads(v, "v", kvh),
+            _opt(q_weight, dt, "q_weight", dim, d), _opt(k_weight, dt, "k_weight", dim, d), float(eps),
+            _dev(positions, i32, "positions", n, device=d), _dev(slots, i32, "slots", n, device=d), *oa,
+            _opt(status, i32, "status", 1, d))
+
+
+def ddtree_draft_append(cache: DraftCache, rope: Rope, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                        positions: torch.Tensor, slots: torch.Tensor, q_out: Optional[torch.Tensor], *,
+                        q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                        eps: float = 1e-6, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Head norms, rotation and cache rows of the drafter's new tokens
+    (include/ddtree_append.h).  q [N, H, D], k and v [N, Hkv, D] (tokens may be
+    strided, as parts of one projection); q_out [N, H, D], which may be q."""
+    _check(library().ddtree_draft_append(
+        *_draft_append_args(cache, rope, q, k, v, positions, slots, q_out, q_weight, k_weight, eps, status),
+        _stream(stream)), "ddtree_draft_append")
+
+
+class BoundDraftAppend(_Bound):
+    """ddtree_draft_append with its arguments checked and marshalled once."""
+    _entry = "ddtree_draft_append"
+
+    def __init__(self, cache: DraftCache, rope: Rope, q, k, v, positions, slots, q_out, *, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, status=None):
+        a = (cache, rope, q, k, v, positions, slots, q_out, q_weight, k_weight, eps, status)
+        self._bind(_draft_append_args(*a), a)

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/ddtree_append.h"
 #include "../../include/ddtree_verify.h"
 
 namespace ddtree {
@@ -212,7 +213,73 @@ struct MaskArgs {
   int batch, n_nodes, num_sms;
 };
 
+// Everything the step maps need (see include/ddtree_maps.h).
+struct MapsArgs {
+  int32_t* table;            // [table_rows, table_stride], grown in place
+  const int32_t* table_row;  // [batch] or null: row b
+  const int32_t* prefix_lens;
+  const int32_t* new_lens;   // [batch] or null: max_new each
+  const int32_t* parent;     // [batch, max_new] or null: a chain
+  const int32_t* held;       // [batch] or null: nothing is taken
+  const int32_t* free_pages; // [n_free]
+  const int32_t* free_head;  // [1]
+  int32_t* held_out;         // [batch]
+  int32_t* free_head_out;    // [1]
+  int32_t* kv_indptr;        // [batch+1]
+  int32_t* kv_indices;       // [capacity] or null
+  int32_t* new_indptr;       // [batch+1] or null
+  int32_t* new_slots;        // [batch*max_new]
+  int32_t* positions;        // [batch*max_new]
+  int32_t* token_rows;       // [batch*max_new] or null
+  uint32_t* status;          // or null
+  int64_t n_pages, capacity;
+  int32_t batch, max_new, page_size, table_rows, table_stride, n_free;
+};
+
+// What a rotation needs (see include/ddtree_append.h): by value in a launch.
+struct RopeArgs {
+  int32_t rot_dim, interleaved;
+  float mscale;
+  uint64_t turns[DDTREE_ROPE_MAX_PAIRS];
+};
+
+// Everything the latent append needs.
+struct MlaAppendArgs {
+  const uint16_t* kv;        // [n, 576], rows kv_stride apart
+  const uint16_t* weight;    // [512] or null
+  const uint16_t* q;         // [n, heads, 64]; may be q_out itself
+  const int32_t* positions;
+  const int32_t* slots;
+  uint16_t* pool;            // [pool_rows, 576]
+  uint16_t* q_out;
+  uint32_t* status;          // or null
+  int64_t kv_stride, q_token, q_head, o_token, o_head, pool_rows;
+  float eps;
+  int32_t n_tokens, n_heads;
+  RopeArgs rope;
+};
+
+// Everything the drafter's append needs.
+struct DraftAppendArgs {
+  const uint16_t *q, *k, *v; // tokens *_stride apart, heads head_dim apart; q may be q_out itself
+  const uint16_t *q_weight, *k_weight;
+  const int32_t* positions;
+  const int32_t* slots;
+  uint16_t* q_out;
+  uint16_t *k_cache, *v_cache;
+  uint32_t* status;          // or null
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int64_t page_stride, token_stride, head_stride;
+  int64_t total_slots;       // n_pages * page_size
+  float eps;
+  int32_t n_tokens, n_heads, n_kv_heads, head_dim, page_size, dtype;
+  RopeArgs rope;
+};
+
 // ---- launchers (one per .cu file) ----
+cudaError_t launch_mla_append(const MlaAppendArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_draft_append(const DraftAppendArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_maps(const MapsArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_mask(const MaskArgs& a, cudaStream_t stream);
 cudaError_t launch_relocate(const RelocateArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream);
