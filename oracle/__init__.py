@@ -15,3 +15,4 @@ from .relocate_oracle import relocate, relocation_errors  # noqa: F401
 from .mask_oracle import tree_from_mask, trees_from_flat_mask  # noqa: F401
 from .maps_oracle import step_maps  # noqa: F401
 from . import append_oracle  # noqa: F401
+from .draft_oracle import draft_attention, visible_keys  # noqa: F401

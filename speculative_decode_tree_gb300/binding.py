@@ -52,6 +52,7 @@ EXPORTS = (
     "ddtree_relocate_kv_workspace_size", "ddtree_relocate_kv",
     "ddtree_tree_from_mask_workspace_size", "ddtree_tree_from_mask", "ddtree_step_maps",
     "ddtree_rope_init", "ddtree_mla_append", "ddtree_draft_append",
+    "ddtree_draft_attention_plan", "ddtree_draft_attention_workspace_size", "ddtree_draft_attention",
 )
 
 
@@ -83,6 +84,13 @@ class _CacheStruct(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class DraftPlan(ctypes.Structure):
+    """ddtree_draft_plan_t (include/ddtree_draft.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_heads", "n_kv_heads", "head_dim", "dtype", "page_size",
+                                              "window", "n_sinks", "row_tile", "tile_keys", "n_shares", "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "out_stride", "workspace_bytes")]
 
 
 class DDTreeError(RuntimeError):
@@ -140,6 +148,12 @@ def library() -> ctypes.CDLL:
     L.ddtree_mla_append.restype = i32
     L.ddtree_draft_append.argtypes = [i64, i32, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, vp, vp, i64, vp, vp]
     L.ddtree_draft_append.restype = i32
+    L.ddtree_draft_attention_plan.argtypes = [i32, i32, vp, i32, i32, i32, vp]
+    L.ddtree_draft_attention_plan.restype = i32
+    L.ddtree_draft_attention_workspace_size.argtypes = [vp]
+    L.ddtree_draft_attention_workspace_size.restype = sz
+    L.ddtree_draft_attention.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, f32, vp, vp, vp, sz, vp]
+    L.ddtree_draft_attention.restype = i32
     for name in ("ddtree_verify_mla_plan", "ddtree_verify_mla_plan_ex", "ddtree_verify_mla",
                  "ddtree_verify_mla_batched", "ddtree_build_ancestor_mask", "ddtree_verify_mla_check",
                  "ddtree_verify_mla_batched_timed", "ddtree_verify_mla_noalloc"):
@@ -605,3 +619,58 @@ class BoundDraftAppend(_Bound):
                  eps: float = 1e-6, status=None):
         a = (cache, rope, q, k, v, positions, slots, q_out, q_weight, k_weight, eps, status)
         self._bind(_draft_append_args(*a), a)
+
+
+def ddtree_draft_attention_plan(n_tokens: int, n_heads: int, cache: DraftCache, window: int = 0, n_sinks: int = 0,
+                                num_sms: int = 0) -> DraftPlan:
+    """Plan of the drafter's attention (include/ddtree_draft.h): one for all lengths."""
+    plan = DraftPlan()
+    _check(library().ddtree_draft_attention_plan(int(n_tokens), int(n_heads), ctypes.addressof(cache.struct), int(window),
+                                                 int(n_sinks), int(num_sms), ctypes.addressof(plan)), "draft_attention_plan")
+    return plan
+
+
+def ddtree_draft_attention_workspace_size(plan: DraftPlan) -> int:
+    return int(library().ddtree_draft_attention_workspace_size(ctypes.addressof(plan)))
+
+
+def _draft_attention_args(plan, q, cache, page_table, positions, sm_scale, out, workspace, token_rows, lse):
+    dt, i32, d = cache.k.dtype, torch.int32, cache.k.get_device()
+    n, h, dim = plan.n_tokens, plan.n_heads, plan.head_dim
+    if cache.head_dim != dim:
+        raise ValueError("the plan was made for another cache")
+
+    def heads(t, name, stride):
+        p = _rows(t, dt, name, (n, h, dim), d)
+        if (h > 1 and t.stride(1) != dim) or (n > 1 and t.stride(0) != (stride or h * dim)):
+            raise ValueError(f"{name}: heads must be {dim} and tokens {stride or h * dim} elements apart (plan q_stride, out_stride)")
+        return p
+    table = _dev(page_table, i32, "page_table")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [rows, pages of a row]")
+    return (ctypes.addressof(plan), heads(q, "q", plan.q_stride), ctypes.addressof(cache.struct), table,
+            int(page_table.shape[0]), int(page_table.shape[1]), _opt(token_rows, i32, "token_rows", n, d),
+            _dev(positions, i32, "positions", n, device=d), float(sm_scale), heads(out, "out", plan.out_stride),
+            _opt(lse, torch.float32, "lse", n * h, d),
+            _dev(workspace, torch.uint8, "workspace", plan.workspace_bytes, device=d), int(workspace.numel()))
+
+
+def ddtree_draft_attention(plan: DraftPlan, q: torch.Tensor, cache: DraftCache, page_table: torch.Tensor,
+                           positions: torch.Tensor, sm_scale: float, out: torch.Tensor, workspace: torch.Tensor, *,
+                           token_rows: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                           stream=None) -> None:
+    """The drafter's attention of one new token per request over its paged
+    cache (include/ddtree_draft.h).  q and out [N, H, D], lse [N, H]."""
+    _check(library().ddtree_draft_attention(
+        *_draft_attention_args(plan, q, cache, page_table, positions, sm_scale, out, workspace, token_rows, lse),
+        _stream(stream)), "ddtree_draft_attention")
+
+
+class BoundDraftAttention(_Bound):
+    """ddtree_draft_attention with its arguments checked and marshalled once."""
+    _entry = "ddtree_draft_attention"
+
+    def __init__(self, plan: DraftPlan, q, cache: DraftCache, page_table, positions, sm_scale: float, out, workspace, *,
+                 token_rows=None, lse=None):
+        a = (plan, q, cache, page_table, positions, sm_scale, out, workspace, token_rows, lse)
+        self._bind(_draft_attention_args(*a), a)

@@ -276,7 +276,28 @@ struct DraftAppendArgs {
   RopeArgs rope;
 };
 
+// Everything the drafter's attention needs (see include/ddtree_draft.h).
+struct DraftAttnArgs {
+  const uint16_t* q;         // tokens q_stride apart
+  const uint16_t *k, *v;     // paged cache
+  const int32_t* table;      // [table_rows, table_stride]
+  const int32_t* token_rows; // [n_tokens] or null: row n
+  const int32_t* positions;  // [n_tokens]
+  uint16_t* out;             // tokens out_stride apart
+  float* lse;                // [n_tokens, n_heads] or null
+  uint8_t* ws;               // workspace: status block, then partial results
+  int64_t q_stride, out_stride, page_stride, token_stride, head_stride, n_pages;
+  float scale_log2;          // sm_scale * log2(e)
+  int32_t n_tokens, n_heads, n_kv_heads, group, head_dim, dtype, page_size;
+  int32_t window, n_sinks, table_rows, table_stride;
+  int32_t row_tile, n_shares;
+};
+
 // ---- launchers (one per .cu file) ----
+int draft_tile_keys(int head_dim);
+int64_t draft_workspace_bytes(int row_tile, int head_dim, int n_shares);
+cudaError_t launch_draft_attention(const DraftAttnArgs& a, cudaStream_t stream);
+bool draft_cache_ok(const ddtree_draft_cache_t* cache);
 cudaError_t launch_mla_append(const MlaAppendArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_draft_append(const DraftAppendArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_maps(const MapsArgs& a, int num_sms, cudaStream_t stream);
