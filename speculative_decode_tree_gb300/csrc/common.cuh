@@ -295,6 +295,7 @@ struct DraftAttnArgs {
 
 // ---- launchers (one per .cu file) ----
 int draft_tile_keys(int head_dim);
+int draft_shares(int head_dim, int num_sms);
 int64_t draft_workspace_bytes(int row_tile, int head_dim, int n_shares);
 cudaError_t launch_draft_attention(const DraftAttnArgs& a, cudaStream_t stream);
 bool draft_cache_ok(const ddtree_draft_cache_t* cache);

@@ -63,7 +63,7 @@ extern "C" int ddtree_draft_attention_plan(int n_tokens, int n_heads, const ddtr
   p.n_sinks = n_sinks;
   p.row_tile = row_tile_for(n_heads / cache->n_kv_heads);
   p.tile_keys = draft_tile_keys(p.head_dim);
-  p.n_shares = 2 * num_sms;
+  p.n_shares = draft_shares(p.head_dim, num_sms);
   p.workspace_bytes = draft_workspace_bytes(p.row_tile, p.head_dim, p.n_shares);
   *plan = p;
   return DDTREE_OK;

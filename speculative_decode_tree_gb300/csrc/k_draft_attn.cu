@@ -1,115 +1,585 @@
 // The drafter's attention of one new token per request over its paged cache
 // (include/ddtree_draft.h).
 //
-// One CTA per (token, query head); its warps take the visible keys in turn,
-// each with a running maximum and sum in 32 bits, and join at the end.  The
-// visible keys are numbered without gaps: the sinks that lie before the
-// window, then the window.
+//   s_j = scale <q, k_j>,  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)
+//
+// The work is a stream of keys: 4 D bytes for 4 D flops per query head of the
+// group, so a group of up to 64 heads stays below the ridge and HBM is the
+// bound.  The kernel is built to keep loads in flight on every SM:
+//
+//  - Equal shares.  The visible keys of a (token, key head) unit are numbered
+//    without gaps (the sinks that lie before the window, then the window) and
+//    cut into tiles; all units' tiles form one list, and share c of G takes
+//    tiles [c T/G, (c+1) T/G).  One CTA per share, all resident at once, so
+//    every SM streams the same number of bytes whatever the lengths are.  The
+//    list exists only as sums over the tokens, which every CTA takes for itself.
+//  - A ring of stages in shared memory, filled by 16-byte cp.async across unit
+//    borders: the next unit's first tiles and its queries are under way while
+//    the last unit finishes.  Page lookups run one tile ahead of the copies and
+//    leave row offsets and a validity bit per key in a small ring; a key that is
+//    not there is filled with zeros and masked.
+//  - The group's query heads are the rows of the matrix instruction (16 rows,
+//    padded), so a key row read once serves them all.  Rows are few, and a
+//    unit's keys are split over the warps instead, each with its own running
+//    maximum and sum in 32 bits; they join through the stage just consumed.
+//    This is mma.sync and not tcgen05: with 4 to 16 useful rows of a 128-row
+//    tile the tensor pipe is no bound, and the fragments stay in registers.
+//  - A unit that lies within a share is finished there.  One that crosses into
+//    other shares leaves its maximum, sum and unnormalised rows per share (at
+//    most two per share), and a second small grid, launched ahead of time with
+//    programmatic dependence, joins them in share order.
 #include "rope.cuh"
+#include "tc_ptx.cuh"
 
 namespace ddtree {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kRing = 4;  // offset slots: the tile in use, those in flight, and the next
+
+template <int kDim, int kWM>
+struct Config {
+  static constexpr int kKeys = kDim == 64 ? 128 : 64;       // keys of a tile
+  static constexpr int kWK = kWarps / kWM;                  // warps along the keys
+  static constexpr int kWarpKeys = kKeys / kWK;
+  static constexpr int kBlock = kDim == 256 ? 16 : (kWarpKeys < 32 ? kWarpKeys : 32);  // keys of one softmax step
+  static constexpr int kRows = 16 * kWM;
+  static constexpr int kRowBytes = kDim * 2;
+  static constexpr int kTileBytes = kKeys * kRowBytes;      // of K, and of V
+  static constexpr int kQBytes = kRows * kRowBytes;
+  // Two CTAs per SM for the narrower heads, one for 256 columns.
+  static constexpr int kStages = kWM == 1 || (kDim == 64 && kWM == 2) ? 3 : 2;
+  static constexpr int kSmem = kStages * (2 * kTileBytes + kQBytes);
+  // The joined rows of all warps fit the stage they replace.
+  static_assert(kWarps * 16 * kDim * 4 <= 2 * kTileBytes, "merge buffer");
+  static_assert(kRing >= kStages + 1, "offset ring");
+};
+
+struct Record {     // of a share whose last unit goes on in later shares
+  int32_t token, kv_head, last_share, pad;
+};
+
+// Workspace: status block, per share a status word and a record, then the
+// (maximum, sum) pairs and the rows of two partial units per share.
+struct Layout {
+  int64_t words, records, sums, rows, total;
+};
+__host__ __device__ inline Layout layout_of(int row_tile, int dim, int shares) {
+  Layout l;
+  l.words = 256;
+  l.records = l.words + ((int64_t)shares * 4 + 255) / 256 * 256;
+  l.sums = l.records + ((int64_t)shares * 16 + 255) / 256 * 256;
+  l.rows = l.sums + ((int64_t)shares * 2 * row_tile * 8 + 255) / 256 * 256;
+  l.total = l.rows + (int64_t)shares * 2 * row_tile * dim * 4;
+  return l;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <bool kHalf>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (kHalf) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+
+// What a token sees, from its position and table row.
+struct Token {
+  int pos, row, lo, first, tiles;  // window start, sinks before it, tiles per key head (0: padding)
+  int64_t seen;                    // visible keys (0 of a token whose data is bad: one empty tile)
+};
+__device__ __forceinline__ Token token_of(const DraftAttnArgs& a, int n, int tile_keys) {
+  Token t;
+  t.pos = __ldg(a.positions + n);
+  t.row = a.token_rows ? __ldg(a.token_rows + n) : n;
+  const bool ok = t.pos >= 0 && t.row >= 0 && t.row < a.table_rows && t.pos / a.page_size < a.table_stride;
+  t.lo = ok && a.window > 0 ? max(0, t.pos - a.window + 1) : 0;
+  t.first = min(a.n_sinks, t.lo);
+  t.seen = ok ? (int64_t)t.first + t.pos - t.lo + 1 : 0;
+  t.tiles = t.pos == -1 ? 0 : ok ? (int)((t.seen + tile_keys - 1) / tile_keys) : 1;
+  return t;
+}
+
+// A tile as the copies and the arithmetic need it.
+struct Tile {
+  int32_t token, kv_head;
+  int32_t unit;   // ordinal within the share: its queries' place in the ring
+  int32_t flags;
+};
+enum { kFirst = 1, kLast = 2, kBegun = 4, kGoesOn = 8 };
+
+template <bool kHalf, int kDim, int kWM>
+__global__ void __launch_bounds__(kThreads) draft_attn_kernel(const DraftAttnArgs a) {
+  using C = Config<kDim, kWM>;
+  constexpr int kChunks = kDim / 8;  // 16-byte chunks of a row
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t offsets[kRing][C::kKeys];   // element offset of a key's row, -1: not there
+  __shared__ uint32_t there[kRing][C::kKeys / 32];
+  __shared__ Tile tiles[kRing];
+  __shared__ float top_s[C::kWK][C::kRows], sum_s[C::kWK][C::kRows];
+  __shared__ int64_t warp_sum[kWarps];
+  __shared__ int start_token;
+  __shared__ int64_t start_at;
+  __shared__ uint32_t bits;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int share = blockIdx.x;
+  const Layout ws = layout_of(C::kRows, kDim, a.n_shares);
+  Record* records = reinterpret_cast<Record*>(a.ws + ws.records);
+  uint32_t* words = reinterpret_cast<uint32_t*>(a.ws + ws.words);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- the list of tiles: sums over the tokens, a run of tokens per thread
+  const int per = (a.n_tokens + kThreads - 1) / kThreads;
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int n = tid * per + i;
+    if (n < a.n_tokens) mine += (int64_t)token_of(a, n, C::kKeys).tiles * a.n_kv_heads;
+  }
+  int64_t inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  if (tid == 0) bits = 0;
+  __syncthreads();
+  int64_t before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  const int64_t shares = total < a.n_shares ? total : a.n_shares;
+  if (share >= shares) {
+    if (tid == 0) {
+      records[share].token = -1;
+      words[share] = 0;
+    }
+    return;
+  }
+  const int64_t begin = share * total / shares, end = (share + 1) * total / shares;
+  if (before <= begin && begin < before + mine) {
+    int n = tid * per;
+    int64_t at = begin - before;
+    for (;; ++n) {
+      const int64_t here = (int64_t)token_of(a, n, C::kKeys).tiles * a.n_kv_heads;
+      if (at < here) break;
+      at -= here;
+    }
+    start_token = n;
+    start_at = at;
+  }
+  __syncthreads();
+  const int count = (int)(end - begin);
+
+  // ---- the next tile to look up; the same in every thread
+  int cur = start_token, unit = 0;
+  Token tok = token_of(a, cur, C::kKeys);
+  int kv_head = (int)(start_at / tok.tiles);
+  int tile = (int)(start_at - (int64_t)kv_head * tok.tiles);
+  bool begun = tile > 0;
+  if (share + 1 == shares && tid == 0) records[share].token = -1;  // its last unit cannot go on
+
+  // First half of a lookup: the page of this thread's key.  -2: no such key.
+  auto page_of_key = [&](int i) {
+    if (i >= count || tid >= C::kKeys) return -2;
+    const int64_t x = (int64_t)tile * C::kKeys + tid;
+    if (x >= tok.seen) return -2;
+    const int j = (int)(x < tok.first ? x : x - tok.first + tok.lo);
+    return __ldg(a.table + (int64_t)tok.row * a.table_stride + j / a.page_size);
+  };
+  // Second half: the row's offset and the tile's description; then one tile on.
+  auto finish_lookup = [&](int i, int page) {
+    if (i >= count) return;
+    const int slot = i % kRing;
+    if (tid < C::kKeys) {
+      const bool good = page >= 0 && page < a.n_pages;
+      if (page != -2 && !good) atomicOr(&bits, DDTREE_ST_BAD_INDEX);
+      int64_t off = -1;
+      if (good) {
+        const int64_t x = (int64_t)tile * C::kKeys + tid;
+        const int j = (int)(x < tok.first ? x : x - tok.first + tok.lo);
+        off = page * a.page_stride + (j % a.page_size) * a.token_stride + kv_head * a.head_stride;
+      }
+      offsets[slot][tid] = off;
+      const uint32_t have = __ballot_sync(0xffffffffu, good);
+      if (lane == 0) there[slot][warp] = have;
+    }
+    const bool unit_ends = tile + 1 == tok.tiles, range_ends = i + 1 == count;
+    if (tid == 0) {
+      Tile t;
+      t.token = cur;
+      t.kv_head = kv_head;
+      t.unit = unit;
+      t.flags = (tile == 0 || i == 0 ? kFirst : 0) | (unit_ends || range_ends ? kLast : 0) | (begun ? kBegun : 0) |
+                (unit_ends ? 0 : kGoesOn);
+      tiles[slot] = t;
+      if (tok.seen == 0) atomicOr(&bits, DDTREE_ST_BAD_LENGTH);
+      if (range_ends && share + 1 < shares) {
+        Record r;
+        r.token = unit_ends || begun ? -1 : cur;
+        r.kv_head = kv_head;
+        const int64_t last = end - 1 + (tok.tiles - 1 - tile);  // the unit's last tile in the list
+        r.last_share = (int)(((last + 1) * shares - 1) / total);
+        r.pad = 0;
+        records[share] = r;
+      }
+    }
+    if (unit_ends && !range_ends) {
+      tile = 0;
+      begun = false;
+      ++unit;
+      if (++kv_head == a.n_kv_heads) {
+        kv_head = 0;
+        do tok = token_of(a, ++cur, C::kKeys);
+        while (tok.tiles == 0);
+      }
+    } else {
+      ++tile;
+    }
+  };
+
+  const uint32_t ring = ptx::smem_u32(smem);
+  const uint32_t q_ring = ring + C::kStages * 2 * C::kTileBytes;
+  auto swizzled = [](int row, int chunk) { return (uint32_t)(row * C::kRowBytes + ((chunk ^ (row & 7)) << 4)); };
+  // Starts the copies of tile i (every thread commits a group, empty or not).
+  auto start_copies = [&](int i) {
+    if (i < count) {
+      const int slot = i % kRing;
+      const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes, v_at = k_at + C::kTileBytes;
+      constexpr int kRowsPerStep = kThreads / kChunks;
+      const int c = tid % kChunks, r0 = tid / kChunks;
+#pragma unroll 8
+      for (int r = r0; r < C::kKeys; r += kRowsPerStep) {
+        const int64_t off = offsets[slot][r];
+        const uint32_t size = off >= 0 ? 16u : 0u;
+        const int64_t from = off >= 0 ? off + 8 * c : 0;
+        ptx::cp_async16_zfill(k_at + swizzled(r, c), a.k + from, size);
+        ptx::cp_async16_zfill(v_at + swizzled(r, c), a.v + from, size);
+      }
+      const Tile t = tiles[slot];
+      if (t.flags & kFirst) {
+        const uint32_t q_at = q_ring + (t.unit % C::kStages) * C::kQBytes;
+        const uint16_t* q = a.q + t.token * a.q_stride + (int64_t)t.kv_head * a.group * kDim;
+#pragma unroll
+        for (int r = r0; r < C::kRows; r += kRowsPerStep)
+          ptx::cp_async16_zfill(q_at + swizzled(r, c), r < a.group ? q + r * kDim + 8 * c : a.q, r < a.group ? 16u : 0u);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  for (int i = 0; i < C::kStages; ++i) finish_lookup(i, page_of_key(i));
+  __syncthreads();
+  for (int i = 0; i < C::kStages - 1; ++i) start_copies(i);
+
+  // ---- this warp's rows (16 of the group) and keys of every tile
+  const int wm = warp % kWM, wk = warp / kWM;
+  constexpr bool kHoldQ = kDim <= 128;  // query fragments in registers; wider heads read them again per tile
+  uint32_t qf[kHoldQ ? kDim / 16 : 1][4];
+  float o[kDim / 8][4], top[2], sum[2];
+  // Probabilities meet V in the cache's type.  fp16 holds nothing below 2^-24,
+  // so there they carry a factor of 2^10: a key counts down to 2^-34 of the
+  // largest, and the factor leaves with the division by the sum.
+  constexpr float kShift = kHalf ? 10.f : 0.f;
+
+  for (int i = 0; i < count; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+    __syncthreads();
+    start_copies(i + C::kStages - 1);
+    const int next_page = page_of_key(i + C::kStages);
+    const int slot = i % kRing;
+    const Tile t = tiles[slot];
+    const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes, v_at = k_at + C::kTileBytes;
+    const uint32_t q_at = q_ring + (t.unit % C::kStages) * C::kQBytes;
+    const int q_row = wm * 16 + (lane & 15), q_chunk = lane >> 4;
+    if (t.flags & kFirst) {
+      if constexpr (kHoldQ) {
+#pragma unroll
+        for (int ks = 0; ks < kDim / 16; ++ks) ldsm4(q_at + swizzled(q_row, 2 * ks + q_chunk), qf[ks]);
+      }
+#pragma unroll
+      for (int d = 0; d < kDim / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+      top[0] = top[1] = -INFINITY;
+      sum[0] = sum[1] = 0.f;
+    }
+#pragma unroll 1
+    for (int block = 0; block < C::kWarpKeys; block += C::kBlock) {
+      const int key0 = wk * C::kWarpKeys + block;
+      float s[C::kBlock / 8][4];
+#pragma unroll
+      for (int x = 0; x < C::kBlock / 8; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < kDim / 16; ++ks) {
+        uint32_t again[4];
+        if constexpr (!kHoldQ) ldsm4(q_at + swizzled(q_row, 2 * ks + q_chunk), again);
+        const uint32_t(&af)[4] = kHoldQ ? qf[kHoldQ ? ks : 0] : again;
+#pragma unroll
+        for (int x = 0; x < C::kBlock / 16; ++x) {
+          uint32_t b[4];
+          ldsm4(k_at + swizzled(key0 + 16 * x + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)), b);
+          mma<kHalf>(s[2 * x], af, b[0], b[1]);
+          mma<kHalf>(s[2 * x + 1], af, b[2], b[3]);
+        }
+      }
+      // Scores in base 2, keys that are not there at -inf.
+      const uint32_t mask = there[slot][key0 >> 5] >> (key0 & 31);
+      constexpr uint32_t kAll = C::kBlock == 32 ? 0xffffffffu : (1u << (C::kBlock & 31)) - 1;
+      float high[2] = {top[0], top[1]};
+#pragma unroll
+      for (int x = 0; x < C::kBlock / 8; ++x) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[x][e] *= a.scale_log2;
+      }
+      if ((mask & kAll) != kAll) {
+#pragma unroll
+        for (int x = 0; x < C::kBlock / 8; ++x) {
+          const uint32_t two = mask >> (8 * x + 2 * (lane & 3));
+          if (!(two & 1)) s[x][0] = s[x][2] = -INFINITY;
+          if (!(two & 2)) s[x][1] = s[x][3] = -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < C::kBlock / 8; ++x) {
+        high[0] = fmaxf(high[0], fmaxf(s[x][0], s[x][1]));
+        high[1] = fmaxf(high[1], fmaxf(s[x][2], s[x][3]));
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        high[r] = fmaxf(high[r], __shfl_xor_sync(0xffffffffu, high[r], 1));
+        high[r] = fmaxf(high[r], __shfl_xor_sync(0xffffffffu, high[r], 2));
+      }
+      if (__any_sync(0xffffffffu, high[0] > top[0] || high[1] > top[1])) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float keep = top[r] == -INFINITY ? 0.f : exp2f(top[r] - high[r]);
+          sum[r] *= keep;
+          top[r] = high[r];
+#pragma unroll
+          for (int d = 0; d < kDim / 8; ++d) {
+            o[d][2 * r] *= keep;
+            o[d][2 * r + 1] *= keep;
+          }
+        }
+      }
+      const float base[2] = {top[0] == -INFINITY ? 0.f : top[0] - kShift, top[1] == -INFINITY ? 0.f : top[1] - kShift};
+#pragma unroll
+      for (int x = 0; x < C::kBlock / 8; ++x) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[x][e] = exp2f(s[x][e] - base[e >> 1]);
+        sum[0] += s[x][0] + s[x][1];
+        sum[1] += s[x][2] + s[x][3];
+      }
+#pragma unroll
+      for (int x = 0; x < C::kBlock / 16; ++x) {
+        const uint32_t p[4] = {pack2<kHalf>(s[2 * x][0], s[2 * x][1]), pack2<kHalf>(s[2 * x][2], s[2 * x][3]),
+                               pack2<kHalf>(s[2 * x + 1][0], s[2 * x + 1][1]), pack2<kHalf>(s[2 * x + 1][2], s[2 * x + 1][3])};
+#pragma unroll
+        for (int d = 0; d < kDim / 16; ++d) {
+          uint32_t b[4];
+          ldsm4_trans(v_at + swizzled(key0 + 16 * x + (lane & 15), 2 * d + (lane >> 4)), b);
+          mma<kHalf>(o[2 * d], p, b[0], b[1]);
+          mma<kHalf>(o[2 * d + 1], p, b[2], b[3]);
+        }
+      }
+    }
+    finish_lookup(i + C::kStages, next_page);
+    if (!(t.flags & kLast)) continue;
+
+    // ---- the unit ends here: join the warps' rows through this tile's stage
+    __syncthreads();  // every warp is done with the tile
+    float* rows = reinterpret_cast<float*>(smem + (i % C::kStages) * 2 * C::kTileBytes);
+    // Row r of key part w; the exchange of column groups keeps the four rows that lanes write at once on other banks.
+    auto cell = [&](int w, int r, int col) { return rows + (w * C::kRows + r) * kDim + (col ^ ((r & 3) << 3)); };
+    const int g = lane >> 2;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+      const int row = wm * 16 + g + 8 * r;
+      if ((lane & 3) == 0) {
+        top_s[wk][row] = top[r];
+        sum_s[wk][row] = sum[r];
+      }
+      if (row < a.group) {
+#pragma unroll
+        for (int d = 0; d < kDim / 8; ++d)
+          *reinterpret_cast<float2*>(cell(wk, row, 8 * d + 2 * (lane & 3))) = make_float2(o[d][2 * r], o[d][2 * r + 1]);
+      }
+    }
+    __syncthreads();
+    const bool whole = !(t.flags & (kBegun | kGoesOn));
+    const int64_t part = 2 * share + (t.flags & kBegun ? 0 : 1);
+    for (int e = tid; e < a.group * (kDim / 8); e += kThreads) {
+      const int row = e / (kDim / 8), col = (e - row * (kDim / 8)) * 8;
+      float m = -INFINITY, l = 0.f, w[C::kWK];
+#pragma unroll
+      for (int k = 0; k < C::kWK; ++k) m = fmaxf(m, top_s[k][row]);
+      const float from = m == -INFINITY ? 0.f : m;
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < C::kWK; ++k) {
+        w[k] = exp2f(top_s[k][row] - from);
+        l += w[k] * sum_s[k][row];
+        const float4 u = *reinterpret_cast<const float4*>(cell(k, row, col)), v = *reinterpret_cast<const float4*>(cell(k, row, col + 4));
+        x[0] += w[k] * u.x; x[1] += w[k] * u.y; x[2] += w[k] * u.z; x[3] += w[k] * u.w;
+        x[4] += w[k] * v.x; x[5] += w[k] * v.y; x[6] += w[k] * v.z; x[7] += w[k] * v.w;
+      }
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] *= inv;
+        const int head = t.kv_head * a.group + row;
+        *reinterpret_cast<uint4*>(a.out + t.token * a.out_stride + (int64_t)head * kDim + col) = pack8<kHalf>(x);
+        if (a.lse && col == 0)
+          a.lse[(int64_t)t.token * a.n_heads + head] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
+      } else {
+        float4* to = reinterpret_cast<float4*>(a.ws + ws.rows) + (part * C::kRows + row) * (kDim / 4) + col / 4;
+        to[0] = make_float4(x[0], x[1], x[2], x[3]);
+        to[1] = make_float4(x[4], x[5], x[6], x[7]);
+        if (col == 0) reinterpret_cast<float2*>(a.ws + ws.sums)[part * C::kRows + row] = make_float2(m, l);
+      }
+    }
+    // The next iteration's barrier comes before this stage is filled again.
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  if (tid == 0) words[share] = bits;
+}
+
+// Joins the shares' parts of every unit that crosses shares, a CTA per share
+// that such a unit starts in and row; CTA (0, 0) gathers the status words.
+template <bool kHalf, int kDim>
+__global__ void __launch_bounds__(kThreads) draft_join_kernel(const DraftAttnArgs a) {
+  constexpr int kLanes = kDim / 4;               // threads of a row, a float4 each
+  constexpr int kParts = kThreads / kLanes;      // parts taken at once
+  __shared__ float4 acc[kParts][kLanes];
+  __shared__ float high_s[kWarps], total_s[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Layout ws = layout_of(a.row_tile, kDim, a.n_shares);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    uint32_t b = 0;
+    for (int s = tid; s < a.n_shares; s += kThreads) b |= reinterpret_cast<const uint32_t*>(a.ws + ws.words)[s];
+    b = __reduce_or_sync(0xffffffffu, b);
+    __shared__ uint32_t all[kWarps];
+    if (lane == 0) all[warp] = b;
+    __syncthreads();
+    if (tid == 0) *reinterpret_cast<uint32_t*>(a.ws) = all[0] | all[1] | all[2] | all[3];
+  }
+  const Record r = reinterpret_cast<const Record*>(a.ws + ws.records)[blockIdx.x];
+  if (r.token < 0) return;
+  const int first = blockIdx.x, parts = r.last_share - first + 1;
+  const float2* sums = reinterpret_cast<const float2*>(a.ws + ws.sums);
+  const float4* rows = reinterpret_cast<const float4*>(a.ws + ws.rows);
+  // Part p of the unit: the second place of its first share, the first place of the others.
+  auto place = [&](int p, int row) { return ((int64_t)2 * (first + p) + (p == 0)) * a.row_tile + row; };
+  for (int row = blockIdx.y; row < a.group; row += gridDim.y) {
+    float high = -INFINITY;
+    for (int p = tid; p < parts; p += kThreads) high = fmaxf(high, sums[place(p, row)].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+    if (lane == 0) high_s[warp] = high;
+    __syncthreads();
+    high = fmaxf(fmaxf(high_s[0], high_s[1]), fmaxf(high_s[2], high_s[3]));
+    const float from = high == -INFINITY ? 0.f : high;
+    float l = 0.f;
+    for (int p = tid; p < parts; p += kThreads) {
+      const float2 s = sums[place(p, row)];
+      l += exp2f(s.x - from) * s.y;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (lane == 0) total_s[warp] = l;
+    const int c = tid % kLanes;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = tid / kLanes; p < parts; p += kParts) {
+      const float w = exp2f(sums[place(p, row)].x - from);
+      const float4 v = rows[place(p, row) * kLanes + c];
+      x.x += w * v.x; x.y += w * v.y; x.z += w * v.z; x.w += w * v.w;
+    }
+    acc[tid / kLanes][c] = x;
+    __syncthreads();
+    if (tid < kLanes) {
+      const float total = total_s[0] + total_s[1] + total_s[2] + total_s[3];
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+      for (int k = 1; k < kParts; ++k) {
+        x.x += acc[k][c].x; x.y += acc[k][c].y; x.z += acc[k][c].z; x.w += acc[k][c].w;
+      }
+      const int head = r.kv_head * a.group + row;
+      *reinterpret_cast<uint2*>(a.out + r.token * a.out_stride + (int64_t)head * kDim + 4 * c) =
+          make_uint2(pack2<kHalf>(x.x * inv, x.y * inv), pack2<kHalf>(x.z * inv, x.w * inv));
+      constexpr float kShift = kHalf ? 10.f : 0.f;
+      if (a.lse && c == 0)
+        a.lse[(int64_t)r.token * a.n_heads + head] = total == 0.f ? -INFINITY : (high - kShift + log2f(total)) * 0.6931471805599453f;
+    }
+    __syncthreads();
+  }
+}
+
+template <bool kHalf, int kDim, int kWM>
+cudaError_t launch(const DraftAttnArgs& a, cudaStream_t stream) {
+  using C = Config<kDim, kWM>;
+  cudaError_t e = cudaFuncSetAttribute(draft_attn_kernel<kHalf, kDim, kWM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  draft_attn_kernel<kHalf, kDim, kWM><<<a.n_shares, kThreads, C::kSmem, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.n_shares, std::min(a.group, 8));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, draft_join_kernel<kHalf, kDim>, a);
+}
 
 template <bool kHalf, int kDim>
-__global__ void __launch_bounds__(kThreads) draft_attn_kernel(const DraftAttnArgs a) {
-  constexpr int kPer = kDim / 32;
-  __shared__ float acc[kWarps][kDim];
-  __shared__ float ms[kWarps], ls[kWarps];
-  const int n = blockIdx.x / a.n_heads, h = blockIdx.x - n * a.n_heads, kh = h / a.group;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t* status = reinterpret_cast<uint32_t*>(a.ws);
-  const int pos = __ldg(a.positions + n);
-  if (pos == -1) return;
-  const int row = a.token_rows ? __ldg(a.token_rows + n) : n;
-  const bool ok = pos >= 0 && row >= 0 && row < a.table_rows && pos / a.page_size < a.table_stride;
-  const int lo = ok && a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  const int first = min(a.n_sinks, lo);
-  const int64_t seen = ok ? (int64_t)first + pos - lo + 1 : 0;
-  if (!ok && threadIdx.x == 0) atomicOr(status, DDTREE_ST_BAD_LENGTH);
-  float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-  const uint16_t* qp = a.q + n * a.q_stride + h * kDim;
-#pragma unroll
-  for (int i = 0; i < kPer / 2; ++i) {
-    const float2 p = unpack2<kHalf>(reinterpret_cast<const uint32_t*>(qp)[lane * (kPer / 2) + i]);
-    q[2 * i] = p.x;
-    q[2 * i + 1] = p.y;
-  }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-  for (int64_t x = warp; x < seen; x += kWarps) {
-    const int j = (int)(x < first ? x : x - first + lo);
-    const int page = __ldg(a.table + (int64_t)row * a.table_stride + j / a.page_size);
-    if (page < 0 || page >= a.n_pages) {
-      if (lane == 0) atomicOr(status, DDTREE_ST_BAD_INDEX);
-      continue;
-    }
-    const int64_t at = page * a.page_stride + (j % a.page_size) * a.token_stride + kh * a.head_stride;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer / 2; ++i) {
-      const float2 p = unpack2<kHalf>(reinterpret_cast<const uint32_t*>(a.k + at)[lane * (kPer / 2) + i]);
-      s += q[2 * i] * p.x + q[2 * i + 1] * p.y;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= a.scale_log2;
-    const float top = fmaxf(m, s), keep = exp2f(m - top), p = exp2f(s - top);
-    m = top;
-    l = l * keep + p;
-#pragma unroll
-    for (int i = 0; i < kPer / 2; ++i) {
-      const float2 v = unpack2<kHalf>(reinterpret_cast<const uint32_t*>(a.v + at)[lane * (kPer / 2) + i]);
-      o[2 * i] = o[2 * i] * keep + p * v.x;
-      o[2 * i + 1] = o[2 * i + 1] * keep + p * v.y;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[warp][lane * kPer + i] = o[i];
-  ms[warp] = m;
-  ls[warp] = l;
-  __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ms[w]);
-  for (int w = 0; w < kWarps; ++w) sum += ms[w] == -INFINITY ? 0.f : ls[w] * exp2f(ms[w] - top);
-  for (int c = threadIdx.x; c < kDim / 2; c += kThreads) {
-    float x = 0.f, y = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ms[w] == -INFINITY ? 0.f : exp2f(ms[w] - top);
-      x += f * acc[w][2 * c];
-      y += f * acc[w][2 * c + 1];
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    reinterpret_cast<uint32_t*>(a.out + n * a.out_stride + h * kDim)[c] = pack2<kHalf>(x * inv, y * inv);
-  }
-  if (threadIdx.x == 0 && a.lse)
-    a.lse[(int64_t)n * a.n_heads + h] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+cudaError_t launch_rows(const DraftAttnArgs& a, cudaStream_t stream) {
+  return a.row_tile == 16   ? launch<kHalf, kDim, 1>(a, stream)
+         : a.row_tile == 32 ? launch<kHalf, kDim, 2>(a, stream)
+                            : launch<kHalf, kDim, 4>(a, stream);
+}
+
+template <bool kHalf>
+cudaError_t launch_dim(const DraftAttnArgs& a, cudaStream_t stream) {
+  return a.head_dim == 64    ? launch_rows<kHalf, 64>(a, stream)
+         : a.head_dim == 128 ? launch_rows<kHalf, 128>(a, stream)
+                             : launch_rows<kHalf, 256>(a, stream);
 }
 
 }  // namespace
 
-int draft_tile_keys(int head_dim) { return head_dim == 256 ? 32 : 64; }
+int draft_tile_keys(int head_dim) { return head_dim == 64 ? 128 : 64; }
 
-int64_t draft_workspace_bytes(int row_tile, int head_dim, int n_shares) { return 256; }
+int draft_shares(int head_dim, int num_sms) { return (head_dim == 256 ? 1 : 2) * num_sms; }
+
+int64_t draft_workspace_bytes(int row_tile, int head_dim, int n_shares) {
+  return (layout_of(row_tile, head_dim, n_shares).total + 255) / 256 * 256;
+}
 
 cudaError_t launch_draft_attention(const DraftAttnArgs& a, cudaStream_t stream) {
-  cudaError_t e = cudaMemsetAsync(a.ws, 0, 256, stream);
-  if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)(a.n_tokens * a.n_heads);
-#define RUN(H, D) draft_attn_kernel<H, D><<<grid, kThreads, 0, stream>>>(a)
-  if (a.dtype == DDTREE_FP16) {
-    if (a.head_dim == 64) RUN(true, 64);
-    else if (a.head_dim == 128) RUN(true, 128);
-    else RUN(true, 256);
-  } else {
-    if (a.head_dim == 64) RUN(false, 64);
-    else if (a.head_dim == 128) RUN(false, 128);
-    else RUN(false, 256);
-  }
-#undef RUN
-  return cudaGetLastError();
+  return a.dtype == DDTREE_FP16 ? launch_dim<true>(a, stream) : launch_dim<false>(a, stream);
 }
 
 }  // namespace ddtree
