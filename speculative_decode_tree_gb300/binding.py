@@ -205,8 +205,15 @@ def _q(t: torch.Tensor, name: str, rows: int, width: int, row_stride: int, devic
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (0.2 us instead
+# of 3 us of host time); the public call where torch has no such function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -422,14 +429,22 @@ class _Bound:
     _entry = ""
 
     def _bind(self, args, keep) -> None:
-        self._args, self._keep = args, keep
-        self._fn = getattr(library(), self._entry)
+        lib = library()
+        # Arguments are converted here, not at every call: a function object of
+        # its own without argument types takes the converted ones as they are
+        # (1.2 us instead of 2.8 us for 26 arguments).
+        types = getattr(lib, self._entry).argtypes
+        self._args, self._keep = tuple(t.from_param(v) for t, v in zip(types, args, strict=False)), keep
+        self._fn = lib[self._entry]
+        self._fn.restype = ctypes.c_int
         self._device = torch.cuda.current_device()
 
     def __call__(self, stream=None) -> None:
         if torch.cuda.current_device() != self._device:
             raise ValueError(f"{self._entry}: bound on cuda:{self._device}, which is not the current device")
-        _check(self._fn(*self._args, _stream(stream)), self._entry)
+        rc = self._fn(*self._args, ctypes.c_void_p(_stream(stream)))
+        if rc != DDTREE_OK:
+            raise DDTreeError(rc, self._entry)
 
 
 def _opt(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, numel: Optional[int] = None,

@@ -1,12 +1,14 @@
 // The drafter's new queries, keys and values (include/ddtree_append.h): head
 // norms, rotation of the leading columns, cache writes.
 //
-// A CTA takes a few tokens and treats all their heads (query, key, value) as
-// one list of 16-byte chunks, a chunk per thread and step.  A head's chunks lie
-// on neighbouring lanes of one warp, so its mean square is a shuffle sum and
-// the second element of a pair in the half layout comes from another lane by
-// shuffle.  Sine and cosine are computed once per token and pair into shared
-// memory and serve all heads; the loads of the chunks are issued before that.
+// A warp takes a token, or a slice of its heads where tokens are few, and
+// treats query, key and value heads as one list.  A lane keeps the same 16-byte
+// chunk of every head it meets (8, 4, 2 or 1 heads per step for 32 lanes of 8
+// columns), so the sines and cosines of its pairs stay in its registers: each
+// lane computes a few of the token's pairs and the warp hands them round by
+// shuffles once.  A head's mean square is a shuffle sum over its lanes, and in
+// the half layout the other element of a pair comes from its lane by shuffle.
+// No shared memory, no barrier; kUnroll steps' loads are in flight together.
 // Every value is read once, rounded once and written once: HBM-bound for long
 // prompts, latency-bound for a decode step.
 #include "rope.cuh"
@@ -15,112 +17,126 @@ namespace ddtree {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;        // chunks per thread whose loads are in flight together
-constexpr int kMaxTokens = 16;    // tokens per CTA
+constexpr int kUnroll = 4;
 
-template <bool kHalf, int kDim>
-__global__ void __launch_bounds__(kThreads) draft_append_kernel(const __grid_constant__ DraftAppendArgs a,
-                                                                int tokens_per_cta) {
-  constexpr int kChunks = kDim / 8;  // per head: 8, 16 or 32, a divisor of the warp
-  __shared__ float2 table[kMaxTokens][kDim / 2];
+template <bool kHalf, int kDim, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) draft_append_kernel(const __grid_constant__ DraftAppendArgs a, int slices,
+                                                                int slice_heads) {
+  constexpr int kChunks = kDim / 8;              // lanes of a head: 8, 16 or 32
+  constexpr int kHeadsPerStep = 32 / kChunks;
+  constexpr int kPairsPerLane = kDim / 64;       // pairs a lane computes: dim / 2 over 32 lanes
+  constexpr int kTurns = kInterleaved ? 4 : 8;   // pairs with elements in a chunk
   const int lane = threadIdx.x & 31;
-  const int heads = a.n_heads + 2 * a.n_kv_heads;
+  const int c = lane % kChunks, sub = lane / kChunks;
+  const int nq = a.n_heads, nk = a.n_kv_heads, heads = nq + 2 * nk;
   const int pairs = a.rope.rot_dim / 2;
-  const int groups = (a.n_tokens + tokens_per_cta - 1) / tokens_per_cta;
-  for (int group = blockIdx.x; group < groups; group += gridDim.x) {
-    const int t0 = group * tokens_per_cta;
-    const int nt = min(tokens_per_cta, a.n_tokens - t0);
-    const int total = nt * heads * kChunks;
-    for (int base = 0; base < total; base += kThreads * kUnroll) {
-      uint4 v[kUnroll];
+  // Half layout: the chunk that holds the other elements of this chunk's pairs.
+  const int half = a.rope.rot_dim / 16;
+  const bool turned = 8 * c < a.rope.rot_dim;
+  const int other = !turned ? c : c < half ? c + half : c - half;
+  const int other_lane = (lane & ~(kChunks - 1)) + other;
+  const int pair0 = kInterleaved ? 4 * c : 8 * (c < half ? c : other);
+  const bool norms = a.q_weight || a.k_weight;
+  const uint4 one = make_uint4(0, 0, 0, 0);
+  const uint4 wq = a.q_weight ? __ldg(reinterpret_cast<const uint4*>(a.q_weight) + c) : one;
+  const uint4 wk = a.k_weight ? __ldg(reinterpret_cast<const uint4*>(a.k_weight) + c) : one;
+
+  const uint32_t items = (uint32_t)a.n_tokens * (uint32_t)slices;
+  const uint32_t stride = gridDim.x * (kThreads / 32);
+  for (uint32_t item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); item < items; item += stride) {
+    const uint32_t n = item / (uint32_t)slices;
+    const int h_begin = (int)(item - n * (uint32_t)slices) * slice_heads;
+    const int h_end = min(h_begin + slice_heads, heads);
+    const int64_t token = n;
+    const int32_t pos = __ldg(a.positions + n);
+    const int32_t slot = __ldg(a.slots + n);
+    float2 cs[kTurns];
+    const uint16_t *q = a.q + token * a.q_stride, *k = a.k + token * a.k_stride, *v = a.v + token * a.v_stride;
+    for (int base = h_begin; base < h_end; base += kHeadsPerStep * kUnroll) {
+      uint4 in[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int i = base + u * kThreads + (int)threadIdx.x;
-        v[u] = make_uint4(0, 0, 0, 0);
-        if (i >= total) continue;
-        const int c = i % kChunks, hh = i / kChunks, t = hh / heads, h = hh - t * heads;
-        const int64_t token = t0 + t;
-        const uint16_t* src = h < a.n_heads ? a.q + token * a.q_stride + h * kDim
-                              : h < a.n_heads + a.n_kv_heads
-                                  ? a.k + token * a.k_stride + (h - a.n_heads) * kDim
-                                  : a.v + token * a.v_stride + (h - a.n_heads - a.n_kv_heads) * kDim;
-        v[u] = reinterpret_cast<const uint4*>(src)[c];  // plain loads: q_out may be q
+        const int h = base + u * kHeadsPerStep + sub;
+        const uint16_t* src = h < nq ? q + h * kDim : h < nq + nk ? k + (h - nq) * kDim : v + (h - nq - nk) * kDim;
+        in[u] = h < h_end ? reinterpret_cast<const uint4*>(src)[c] : one;  // plain loads: q_out may be q
       }
-      if (base == 0) {
-        __syncthreads();  // the last group's rotations are done with the table
-        for (int e = threadIdx.x; e < nt * pairs; e += kThreads) {
-          const int t = e / pairs, p = e - t * pairs;
-          table[t][p] = turn(a.rope.turns[p], max(__ldg(a.positions + t0 + t), 0), a.rope.mscale);
+      if (base == h_begin) {
+        if (pos < 0) {
+          if (pos < -1 && a.status && h_begin == 0 && lane == 0) atomicOr(a.status, DDTREE_ST_BAD_LENGTH);
+          break;
         }
-        __syncthreads();
+        if (slot < -1 || slot >= a.total_slots) {
+          if (a.status && lane == 0) atomicOr(a.status, DDTREE_ST_BAD_INDEX);
+        }
+        // Pair p is computed by lane p % 32 as its (p / 32)-th.
+        float2 mine[kPairsPerLane];
+#pragma unroll
+        for (int j = 0; j < kPairsPerLane; ++j) {
+          const int p = lane + 32 * j;
+          mine[j] = p < pairs ? turn(a.rope.turns[p], pos, a.rope.mscale) : make_float2(1.f, 0.f);
+        }
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+          const int p = pair0 + t;
+          cs[t] = mine[0];
+#pragma unroll
+          for (int j = 0; j < kPairsPerLane; ++j) {
+            const float x = __shfl_sync(0xffffffffu, mine[j].x, p & 31), y = __shfl_sync(0xffffffffu, mine[j].y, p & 31);
+            if (p >> 5 == j) cs[t] = make_float2(x, y);
+          }
+          // Half layout: a first element is x cos - y sin, a second one x cos + y sin with y its partner.
+          if (!kInterleaved && c < half) cs[t].y = -cs[t].y;
+        }
       }
+      const bool write_kv = slot >= 0 && slot < a.total_slots;
+      const int page = write_kv ? slot / a.page_size : 0, off = write_kv ? slot - page * a.page_size : 0;
+      const int64_t row = page * a.page_stride + off * a.token_stride;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int i = base + u * kThreads + (int)threadIdx.x;
-        const bool in = i < total;
-        const int c = in ? i % kChunks : 0, hh = in ? i / kChunks : 0, t = hh / heads, h = hh - t * heads;
-        const bool is_q = h < a.n_heads, is_v = h >= a.n_heads + a.n_kv_heads;
-        const uint16_t* weight = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
-        float x[8];
-        unpack8<kHalf>(v[u], x);
-        float sum = 0.f;
+        if (base + u * kHeadsPerStep >= h_end) break;  // the same in the whole warp
+        const int h = base + u * kHeadsPerStep + sub;
+        const bool is_q = h < nq, is_v = h >= nq + nk;
+        // Values are copied as they came.  A step of value heads alone leaves the arithmetic out.
+        if (base + u * kHeadsPerStep < nq + nk) {
+          float x[8];
+          unpack8<kHalf>(in[u], x);
+          if (norms) {
+            float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
+            for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
 #pragma unroll
-        for (int d = kChunks / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (weight) {
-          float w[8];
-          unpack8<kHalf>(__ldg(reinterpret_cast<const uint4*>(weight) + c), w);
-          const float scale = rsqrtf(sum * (1.f / kDim) + a.eps);
+            for (int d = kChunks / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
+              const float scale = rsqrtf(sum * (1.f / kDim) + a.eps);
+              float w[8];
+              unpack8<kHalf>(is_q ? wq : wk, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = x[j] * scale * w[j];
-        }
-        if (a.rope.interleaved) {
-          if (!is_v && 8 * c < a.rope.rot_dim) {
+              for (int j = 0; j < 8; ++j) x[j] = x[j] * scale * w[j];
+            }
+          }
+          if constexpr (kInterleaved) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 cs = table[t][4 * c + j];
               const float e = x[2 * j], o = x[2 * j + 1];
-              x[2 * j] = e * cs.x - o * cs.y;
-              x[2 * j + 1] = e * cs.y + o * cs.x;
+              x[2 * j] = turned ? e * cs[j].x - o * cs[j].y : e;
+              x[2 * j + 1] = turned ? e * cs[j].y + o * cs[j].x : o;
             }
-          }
-        } else {
-          // The chunk that holds the other elements of this chunk's pairs.
-          const int half = a.rope.rot_dim / 16;
-          const int other = c < half ? c + half : c < 2 * half ? c - half : c;
-          const int src = (lane & ~(kChunks - 1)) + other;
+          } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float y = __shfl_sync(0xffffffffu, x[j], src);
-            if (!is_v && c < 2 * half) {
-              const float2 cs = table[t][8 * (c < half ? c : other) + j];
-              x[j] = c < half ? x[j] * cs.x - y * cs.y : y * cs.y + x[j] * cs.x;
+            for (int j = 0; j < 8; ++j) {
+              const float y = __shfl_sync(0xffffffffu, x[j], other_lane);
+              if (turned) x[j] = x[j] * cs[j].x + y * cs[j].y;
             }
           }
+          if (!is_v) in[u] = pack8<kHalf>(x);
         }
-        if (!in) continue;
-        const int64_t token = t0 + t;
-        const int32_t pos = __ldg(a.positions + token);
-        if (pos < 0) {
-          if (pos < -1 && a.status && h == 0 && c == 0) atomicOr(a.status, DDTREE_ST_BAD_LENGTH);
-          continue;
-        }
-        uint16_t* dst;
+        if (h >= h_end) continue;
         if (is_q) {
-          dst = a.q_out + token * a.q_out_stride + h * kDim;
-        } else {
-          const int64_t slot = __ldg(a.slots + token);
-          if (slot < 0 || slot >= a.total_slots) {
-            if (slot != -1 && a.status && c == 0) atomicOr(a.status, DDTREE_ST_BAD_INDEX);
-            continue;
-          }
-          const int page = (int)slot / a.page_size, off = (int)slot - page * a.page_size;
-          const int kh = h - a.n_heads - (is_v ? a.n_kv_heads : 0);
-          dst = (is_v ? a.v_cache : a.k_cache) + page * a.page_stride + off * a.token_stride + kh * a.head_stride;
+          reinterpret_cast<uint4*>(a.q_out + token * a.q_out_stride + h * kDim)[c] = in[u];
+        } else if (write_kv) {
+          uint16_t* dst = (is_v ? a.v_cache + (h - nq - nk) * a.head_stride : a.k_cache + (h - nq) * a.head_stride) + row;
+          reinterpret_cast<uint4*>(dst)[c] = in[u];
         }
-        // Values are copied as they came.
-        reinterpret_cast<uint4*>(dst)[c] = is_v ? v[u] : pack8<kHalf>(x);
       }
     }
   }
@@ -128,12 +144,19 @@ __global__ void __launch_bounds__(kThreads) draft_append_kernel(const __grid_con
 
 template <bool kHalf, int kDim>
 cudaError_t launch(const DraftAppendArgs& a, int num_sms, cudaStream_t stream) {
-  // About one unrolled step of chunks per CTA, but tokens on every SM first.
-  const int chunks = (a.n_heads + 2 * a.n_kv_heads) * (kDim / 8);
-  int per = std::max(1, std::min(kMaxTokens, kThreads * kUnroll / chunks));
-  per = std::max(1, std::min(per, a.n_tokens / num_sms));
-  const int64_t blocks = ((int64_t)a.n_tokens + per - 1) / per;
-  draft_append_kernel<kHalf, kDim><<<(unsigned)std::min<int64_t>(blocks, (int64_t)num_sms * 64), kThreads, 0, stream>>>(a, per);
+  // A token is one warp's work where tokens fill the SMs with 32 warps each;
+  // fewer tokens are cut into slices, down to one step of heads.
+  constexpr int kHeadsPerStep = 32 / (kDim / 8);
+  const int heads = a.n_heads + 2 * a.n_kv_heads;
+  const int steps = (heads + kHeadsPerStep - 1) / kHeadsPerStep;
+  const int64_t want = ((int64_t)num_sms * 32 + a.n_tokens - 1) / a.n_tokens;
+  const int slice_steps = (int)std::max<int64_t>(1, steps / std::min<int64_t>(want, steps));
+  const int slices = (steps + slice_steps - 1) / slice_steps;
+  const int64_t blocks = ((int64_t)a.n_tokens * slices + kThreads / 32 - 1) / (kThreads / 32);
+  const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)num_sms * 64);
+  const int slice_heads = slice_steps * kHeadsPerStep;
+  if (a.rope.interleaved) draft_append_kernel<kHalf, kDim, true><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);
+  else draft_append_kernel<kHalf, kDim, false><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);
   return cudaGetLastError();
 }
 

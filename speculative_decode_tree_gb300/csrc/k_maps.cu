@@ -4,11 +4,13 @@
 // One launch.  Every CTA takes the exclusive sums over the batch (at most 1024
 // requests: four per thread) of keys, new tokens and pages to take, into its
 // own shared memory: the same integers everywhere, so each CTA reaches the
-// all-or-nothing verdict by itself and no CTA waits for another.  Then the
-// CTAs share out three flat lists by element: the pages to take, the new
-// tokens (a warp per request, so that depths come by pointer doubling over the
-// lanes), and kv_indices, where each thread writes four consecutive entries
-// with one 16-byte store and finds its request by bisection of the sums.
+// all-or-nothing verdict by itself and no CTA waits for another.  The first
+// CTAs then write the lists of tokens and pages (a warp per request, so that
+// depths come by pointer doubling over the lanes), the others kv_indices: each
+// warp a contiguous share of the whole list, four consecutive entries per lane
+// and 16-byte store.  A lane finds its request by bisection once and then only
+// walks forward; page and place in the page advance by additions, and several
+// steps' table loads are in flight together.
 // A page of a request comes from the table below `held` and from the free list
 // above, so no thread reads a table entry that this launch writes.
 //
@@ -22,6 +24,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = DDTREE_MAX_BATCH / kThreads;
+constexpr int kSteps = 4;  // steps of kv_indices whose table loads are in flight together
 
 struct Shared {
   int32_t ptr[DDTREE_MAX_BATCH + 1];   // exclusive sums of P + n
@@ -58,21 +61,37 @@ __device__ __forceinline__ int request_of(const int32_t* sums, int batch, int g)
   return lo;
 }
 
-// Page k of request b, or -1 (and BAD_INDEX) when it lies outside the pool.
-__device__ __forceinline__ int page_of(const MapsArgs& a, const Shared& s, int head, int b, int k) {
-  const int page = k < s.held[b] ? a.table[(int64_t)s.row[b] * a.table_stride + k]
-                                 : __ldg(a.free_pages + head + s.off[b] + (k - s.held[b]));
-  if (page >= 0 && page < a.n_pages) return page;
+// The pages of one request: from the table below `held`, from the free list
+// above.
+struct Pages {
+  const int32_t* table;  // its row
+  const int32_t* fresh;  // such that fresh[k] is page k >= held
+  int held;
+  __device__ __forceinline__ int operator[](int k) const { return k < held ? table[k] : __ldg(fresh + k); }
+};
+__device__ __forceinline__ Pages pages_of(const MapsArgs& a, const Shared& s, int head, int b) {
+  Pages p;
+  p.held = s.held[b];
+  p.table = a.table + (int64_t)s.row[b] * a.table_stride;
+  p.fresh = a.free_pages + ((int64_t)head + s.off[b] - p.held);
+  return p;
+}
+// A page's row for a place in it, or -1 (and BAD_INDEX) when it lies outside the pool.
+__device__ __forceinline__ int row_of(const MapsArgs& a, int page, int in) {
+  if ((uint32_t)page < (uint32_t)a.n_pages) return page * a.page_size + in;
   flag(a, DDTREE_ST_BAD_INDEX);
   return -1;
 }
 
-__global__ void __launch_bounds__(kThreads) maps_kernel(const MapsArgs a) {
+// The first token_ctas CTAs write the token and page lists, the others kv_indices.
+template <bool kSinglePage>  // page_size 1: every entry is a table entry
+__global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ MapsArgs a, int token_ctas) {
   __shared__ Shared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.batch, ps = a.page_size;
 
   // ---- sums over the batch
+  const int head = a.held ? __ldg(a.free_head) : 0;
   long long keys[kPer], need[kPer];
   int fresh[kPer];
   long long keys_sum = 0, need_sum = 0;
@@ -126,7 +145,6 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const MapsArgs a) {
     total_need += s.warp_need[w];
     total_new += s.warp_new[w];
   }
-  const int head = a.held ? __ldg(a.free_head) : 0;
   bad = bad || total > INT32_MAX || (a.kv_indices && total > a.capacity);
   const bool dry = !bad && a.held && (head < 0 || head > a.n_free || total_need > a.n_free - head);
   const bool ok = !bad && !dry;
@@ -161,119 +179,186 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const MapsArgs a) {
   }
   __syncthreads();
 
-  const int64_t gtid = (int64_t)blockIdx.x * kThreads + tid;
-  const int64_t threads = (int64_t)gridDim.x * kThreads;
-  // ---- entries behind the last token (all of them when the call does nothing)
-  for (int64_t t = (ok ? total_new : 0) + gtid; t < (int64_t)B * a.max_new; t += threads) {
-    a.new_slots[t] = -1;
-    a.positions[t] = -1;
-    if (a.token_rows) a.token_rows[t] = -1;
-  }
-  if (!ok) return;
-
-  // ---- pages to take
-  for (int64_t e = gtid; e < total_need; e += threads) {
-    const int b = request_of(s.off, B, (int)e);
-    const int page = __ldg(a.free_pages + head + e);
-    a.table[(int64_t)s.row[b] * a.table_stride + s.held[b] + ((int)e - s.off[b])] = page;
-    if (page < 0 || page >= a.n_pages) flag(a, DDTREE_ST_BAD_INDEX);
-  }
-
-  // ---- new tokens: a warp per request, two nodes per lane
-  for (int b = blockIdx.x * kWarps + warp; b < B; b += gridDim.x * kWarps) {
-    const int t0 = s.nptr[b], n = s.nptr[b + 1] - t0;
-    const int P = s.ptr[b + 1] - s.ptr[b] - n;
-    int up[2], depth[2];  // next ancestor not yet counted, and the steps counted
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = lane + 32 * r;
-      up[r] = i - 1;
-      depth[r] = i;
-      if (a.parent) {
-        int p = i < n ? __ldg(a.parent + (int64_t)b * a.max_new + i) : -1;
-        if (p < -1 || p >= i) {
-          flag(a, DDTREE_ST_BAD_PARENT);
-          p = -1;
-        }
-        up[r] = p;
-        depth[r] = p >= 0;
-      }
+  if ((int)blockIdx.x < token_ctas) {
+    const int gtid = blockIdx.x * kThreads + tid, threads = token_ctas * kThreads;
+    // ---- entries behind the last token (all of them when the call does nothing)
+    for (int t = (ok ? total_new : 0) + gtid; t < B * a.max_new; t += threads) {
+      a.new_slots[t] = -1;
+      a.positions[t] = -1;
+      if (a.token_rows) a.token_rows[t] = -1;
     }
-    if (a.parent) {
+    if (!ok) return;
+
+    // ---- new tokens: a warp per request, two nodes per lane
+    for (int b = blockIdx.x * kWarps + warp; b < B; b += token_ctas * kWarps) {
+      const int t0 = s.nptr[b], n = s.nptr[b + 1] - t0;
+      const int P = s.ptr[b + 1] - s.ptr[b] - n;
+      const Pages pages = pages_of(a, s, head, b);
+      int page[2], up[2], depth[2];  // up: next ancestor not yet counted, depth: the steps counted
 #pragma unroll
-      for (int step = 0; step < 6; ++step) {  // ancestors of a 64-node tree: 2^6 steps
-        int d[2], u[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int src = up[r] & 31;
-          const int d0 = __shfl_sync(0xffffffffu, depth[0], src), d1 = __shfl_sync(0xffffffffu, depth[1], src);
-          const int u0 = __shfl_sync(0xffffffffu, up[0], src), u1 = __shfl_sync(0xffffffffu, up[1], src);
-          d[r] = up[r] < 32 ? d0 : d1;
-          u[r] = up[r] < 32 ? u0 : u1;
+      for (int r = 0; r < 2; ++r) {
+        const int i = lane + 32 * r;
+        page[r] = i < n ? pages[(P + i) / ps] : -1;
+        up[r] = i - 1;
+        depth[r] = i;
+        if (a.parent) {
+          int p = i < n ? __ldg(a.parent + (int64_t)b * a.max_new + i) : -1;
+          if (p < -1 || p >= i) {
+            flag(a, DDTREE_ST_BAD_PARENT);
+            p = -1;
+          }
+          up[r] = p;
+          depth[r] = p >= 0;
         }
+      }
+      if (a.parent) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (up[r] >= 0) {
-            depth[r] += d[r];
-            up[r] = u[r];
+        for (int step = 0; step < 6; ++step) {  // ancestors of a 64-node tree: 2^6 steps
+          int d[2], u[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int src = up[r] & 31;
+            const int d0 = __shfl_sync(0xffffffffu, depth[0], src), d1 = __shfl_sync(0xffffffffu, depth[1], src);
+            const int u0 = __shfl_sync(0xffffffffu, up[0], src), u1 = __shfl_sync(0xffffffffu, up[1], src);
+            d[r] = up[r] < 32 ? d0 : d1;
+            u[r] = up[r] < 32 ? u0 : u1;
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if (up[r] >= 0) {
+              depth[r] += d[r];
+              up[r] = u[r];
+            }
           }
         }
       }
-    }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = lane + 32 * r;
-      if (i >= n) continue;
-      const int page = page_of(a, s, head, b, (P + i) / ps);
-      a.new_slots[t0 + i] = page < 0 ? -1 : page * ps + (P + i) % ps;
-      a.positions[t0 + i] = P + depth[r];
-      if (a.token_rows) a.token_rows[t0 + i] = s.row[b];
-    }
-  }
-
-  // ---- the verify index layout, four entries per thread
-  if (!a.kv_indices) return;
-  const bool vec = ((uintptr_t)a.kv_indices & 15) == 0;
-  for (int64_t g0 = 4 * gtid; g0 < total; g0 += 4 * threads) {
-    int b = request_of(s.ptr, B, (int)g0);
-    int end = s.ptr[b + 1];
-    unsigned j = (unsigned)((int)g0 - s.ptr[b]);
-    unsigned k = j / (unsigned)ps, in = j - k * (unsigned)ps;
-    int page = page_of(a, s, head, b, k);
-    int out[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      out[e] = page < 0 ? -1 : page * ps + (int)in;
-      if (e == 3) break;
-      if (g0 + e + 1 >= total) break;
-      const int g = (int)(g0 + e + 1);
-      if (g >= end) {
-        do ++b;  // requests without keys own no entry
-        while (s.ptr[b + 1] <= g);
-        end = s.ptr[b + 1];
-        k = in = 0;
-        page = page_of(a, s, head, b, 0);
-      } else if (++in == (unsigned)ps) {
-        in = 0;
-        page = page_of(a, s, head, b, ++k);
+      for (int r = 0; r < 2; ++r) {
+        const int i = lane + 32 * r;
+        if (i >= n) continue;
+        a.new_slots[t0 + i] = row_of(a, page[r], (P + i) % ps);
+        a.positions[t0 + i] = P + depth[r];
+        if (a.token_rows) a.token_rows[t0 + i] = s.row[b];
       }
     }
-    if (vec && g0 + 4 <= total) {
-      *reinterpret_cast<int4*>(a.kv_indices + g0) = make_int4(out[0], out[1], out[2], out[3]);
-    } else {
-      for (int e = 0; e < 4 && g0 + e < total; ++e) a.kv_indices[g0 + e] = out[e];
+
+    // ---- pages to take
+    for (int64_t e = gtid; e < total_need; e += threads) {
+      const int b = request_of(s.off, B, (int)e);
+      const int page = __ldg(a.free_pages + head + e);
+      a.table[(int64_t)s.row[b] * a.table_stride + s.held[b] + ((int)e - s.off[b])] = page;
+      if (page < 0 || page >= a.n_pages) flag(a, DDTREE_ST_BAD_INDEX);
     }
+    return;
+  }
+
+  // ---- the verify index layout
+  if (!ok) return;
+  const int64_t warps = (int64_t)(gridDim.x - token_ctas) * kWarps;
+  const int64_t part = ((total + warps - 1) / warps + 127) / 128 * 128;  // whole steps of 32 lanes x 4 entries
+  const int64_t begin = ((int64_t)(blockIdx.x - token_ctas) * kWarps + warp) * part;
+  const int64_t end = begin + part < total ? begin + part : total;
+  if (begin + 4 * lane >= end) return;
+  const bool vec = ((uintptr_t)a.kv_indices & 15) == 0;
+  int64_t g0 = begin + 4 * lane;
+  int b = request_of(s.ptr, B, (int)g0);
+  Pages pages = pages_of(a, s, head, b);
+  int first = s.ptr[b], last = s.ptr[b + 1];  // the request's entries
+  // k: page of entry g0, in: its place there; a step moves them by whole pages and a rest.
+  int k = ((int)g0 - first) / ps, in = ((int)g0 - first) - k * ps;
+  const int step_pages = 128 / ps, step_in = 128 - step_pages * ps;
+  // One step: the row numbers of four entries, from the pages that were loaded for them.
+  auto store = [&](int64_t g, const int (&row)[4]) {
+    if (vec && g + 4 <= total) {
+      *reinterpret_cast<int4*>(a.kv_indices + g) = make_int4(row[0], row[1], row[2], row[3]);
+    } else {
+      for (int e = 0; e < 4 && g + e < total; ++e) a.kv_indices[g + e] = row[e];
+    }
+  };
+  auto forward = [&]() {
+    g0 += 128;
+    k += step_pages;
+    in += step_in;
+    if (in >= ps) {
+      in -= ps;
+      ++k;
+    }
+  };
+  while (g0 < end) {
+    if (g0 >= last) {
+      do ++b;  // requests without keys own no entry
+      while (s.ptr[b + 1] <= (int)g0);
+      pages = pages_of(a, s, head, b);
+      first = s.ptr[b];
+      last = s.ptr[b + 1];
+      k = ((int)g0 - first) / ps;
+      in = ((int)g0 - first) - k * ps;
+    }
+    if ((kSinglePage || ps >= 4) && g0 + 128 * (kSteps - 1) + 4 <= last && g0 + 128 * (kSteps - 1) < end) {
+      // The request's entries for kSteps steps: at most two pages a step, or four pages of one entry.
+      int page[kSteps][kSinglePage ? 4 : 2], at[kSteps];
+      int64_t g[kSteps];
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        g[u] = g0;
+        at[u] = in;
+        if constexpr (kSinglePage) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) page[u][e] = pages[k + e];
+        } else {
+          page[u][0] = pages[k];
+          page[u][1] = in + 4 > ps ? pages[k + 1] : 0;
+        }
+        forward();
+      }
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        int row[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (kSinglePage) row[e] = row_of(a, page[u][e], 0);
+          else row[e] = at[u] + e < ps ? row_of(a, page[u][0], at[u] + e) : row_of(a, page[u][1], at[u] + e - ps);
+        }
+        store(g[u], row);
+      }
+      continue;
+    }
+    // Near a request's end, or pages of two and three entries: entry by entry.
+    int row[4];
+    int bb = b, kk = k, ii = in, stop = last;
+    Pages pp = pages;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (g0 + e >= total) break;
+      const int g = (int)(g0 + e);
+      if (g >= stop) {
+        do ++bb;
+        while (s.ptr[bb + 1] <= g);
+        pp = pages_of(a, s, head, bb);
+        stop = s.ptr[bb + 1];
+        kk = ii = 0;
+      }
+      row[e] = row_of(a, pp[kk], ii);
+      if (++ii == ps) {
+        ii = 0;
+        ++kk;
+      }
+    }
+    store(g0, row);
+    forward();
   }
 }
 
 }  // namespace
 
 cudaError_t launch_maps(const MapsArgs& a, int num_sms, cudaStream_t stream) {
-  // One CTA per 2048 index entries (two 16-byte stores a thread), up to four
-  // per SM; without indices the token lists size the grid.
-  const int64_t work = std::max<int64_t>(a.capacity, (int64_t)a.batch * a.max_new * 4);
-  const int64_t blocks = std::min<int64_t>((work + 2047) / 2048, (int64_t)num_sms * 4);
-  maps_kernel<<<(unsigned)std::max<int64_t>(blocks, 1), kThreads, 0, stream>>>(a);
+  // A warp per request for the lists, one step of 1024 index entries per CTA
+  // at least, four CTAs per SM at most.
+  const int64_t tokens = std::min<int64_t>((a.batch + kWarps - 1) / kWarps, num_sms);
+  const int64_t index = a.kv_indices ? std::min<int64_t>((a.capacity + 1023) / 1024, (int64_t)num_sms * 4) : 0;
+  const unsigned grid = (unsigned)(tokens + index);
+  if (a.page_size == 1) maps_kernel<true><<<grid, kThreads, 0, stream>>>(a, (int)tokens);
+  else maps_kernel<false><<<grid, kThreads, 0, stream>>>(a, (int)tokens);
   return cudaGetLastError();
 }
 

@@ -1,36 +1,37 @@
 // Latent rows and rotated queries of new tokens (include/ddtree_append.h):
 //   pool[slot] = [ norm(latent) * w | R(p) k_rope ],   q_out = R(p) q_rope.
 //
-// One warp per piece of a token: piece 0 is its pool row (64 sixteen-byte
-// chunks of latent, two per lane, and the rope part on four lanes), every
-// further piece eight query heads (four lanes a head, eight pairs a lane).
-// Each lane computes the sine and cosine of one of the 32 pairs and the warp
-// hands them round by shuffles, so nothing is staged in shared memory and no
-// warp waits for another.  The mean square is one warp sum over values that
-// stay in registers; every value is read once, rounded once and written once,
-// so the kernel is bound by HBM when there are many tokens and by its two
-// dependent loads when there are few.
+// A warp takes a token, or where tokens are few a slice of it: slice 0 has the
+// pool row (64 sixteen-byte chunks of latent, two per lane, and the rope part
+// on four lanes) and the first query heads, further slices eight heads each
+// (four lanes a head, eight pairs a lane).  Each lane computes the sine and
+// cosine of one of the 32 pairs and the warp hands them round by shuffles, so
+// nothing is staged in shared memory and no warp waits for another.  The loads
+// of the row and of the first sixteen heads are in flight together.  The mean
+// square is one warp sum over values that stay in registers; every value is
+// read once, rounded once and written once: HBM-bound for many tokens, bound by
+// two dependent loads for few.
 #include "rope.cuh"
 
 namespace ddtree {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeadsPerPiece = 8;
+constexpr int kHeadsPerStep = 8;
+constexpr int kUnroll = 2;  // steps of heads whose loads are in flight together
 
-// Rotates the eight pairs of group g (of four): chunk a holds first elements
-// and chunk b second ones (half layout), or a and b hold whole pairs in a row.
-// cs is the calling lane's own pair; every lane of the warp takes part.
-__device__ __forceinline__ void rotate_group(uint4& a, uint4& b, int g, float2 cs, bool interleaved) {
+// Rotates eight pairs: chunk a holds their first elements and chunk b the
+// second ones (half layout), or a and b hold whole pairs one after the other.
+template <bool kInterleaved>
+__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2 (&cs)[8]) {
   float x[8], y[8];
   unpack8<false>(a, x);
   unpack8<false>(b, y);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float c = __shfl_sync(0xffffffffu, cs.x, 8 * g + i), s = __shfl_sync(0xffffffffu, cs.y, 8 * g + i);
-    float& u = interleaved ? (i < 4 ? x[2 * (i & 3)] : y[2 * (i & 3)]) : x[i];
-    float& v = interleaved ? (i < 4 ? x[2 * (i & 3) + 1] : y[2 * (i & 3) + 1]) : y[i];
-    const float r = u * c - v * s, t = u * s + v * c;
+    float& u = kInterleaved ? (i < 4 ? x[2 * (i & 3)] : y[2 * (i & 3)]) : x[i];
+    float& v = kInterleaved ? (i < 4 ? x[2 * (i & 3) + 1] : y[2 * (i & 3) + 1]) : y[i];
+    const float r = u * cs[i].x - v * cs[i].y, t = u * cs[i].y + v * cs[i].x;
     u = r;
     v = t;
   }
@@ -39,31 +40,61 @@ __device__ __forceinline__ void rotate_group(uint4& a, uint4& b, int g, float2 c
 }
 
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) mla_append_kernel(const __grid_constant__ MlaAppendArgs a, int pieces) {
+__global__ void __launch_bounds__(kThreads) mla_append_kernel(const __grid_constant__ MlaAppendArgs a, int slices,
+                                                              int slice_heads) {
   const int lane = threadIdx.x & 31;
-  const uint32_t items = (uint32_t)a.n_tokens * (uint32_t)pieces;
+  const int g = lane & 3, sub = lane >> 2;
+  const int c0 = kInterleaved ? 2 * g : g, c1 = kInterleaved ? 2 * g + 1 : g + 4;
+  const uint64_t freq = a.rope.turns[lane];
+  const uint32_t items = (uint32_t)a.n_tokens * (uint32_t)slices;
   const uint32_t stride = gridDim.x * (kThreads / 32);
   for (uint32_t item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); item < items; item += stride) {
-    const uint32_t token = item / (uint32_t)pieces;
-    const int piece = (int)(item - token * (uint32_t)pieces);
-    const int32_t pos = __ldg(a.positions + token);
+    const uint32_t n = item / (uint32_t)slices;
+    const int slice = (int)(item - n * (uint32_t)slices);
+    const int64_t token = n;
+    const int32_t pos = __ldg(a.positions + n);
+    const int64_t slot = __ldg(a.slots + n);
+    const bool has_row = slice == 0;  // what the loads below can be issued for without waiting for pos and slot
+    uint4 v[2], w[2], r0, r1;
+    if (has_row) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.kv + token * a.kv_stride);
+      v[0] = __ldg(src + lane);
+      v[1] = __ldg(src + lane + 32);
+      r0 = __ldg(src + kLatent / 8 + c0);  // lanes 4..31 repeat 0..3
+      r1 = __ldg(src + kLatent / 8 + c1);
+      if (a.weight) {
+        w[0] = __ldg(reinterpret_cast<const uint4*>(a.weight) + lane);
+        w[1] = __ldg(reinterpret_cast<const uint4*>(a.weight) + lane + 32);
+      }
+    }
+    const int h_begin = slice * slice_heads, h_end = min(h_begin + slice_heads, a.n_heads);
+    uint4 q0[kUnroll], q1[kUnroll];
+    auto load_heads = [&](int base) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int h = base + u * kHeadsPerStep + sub;
+        q0[u] = q1[u] = make_uint4(0, 0, 0, 0);
+        if (h < h_end) {  // plain loads: q_out may be the same buffer
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + token * a.q_token + (int64_t)h * a.q_head);
+          q0[u] = src[c0];
+          q1[u] = src[c1];
+        }
+      }
+    };
+    load_heads(h_begin);
     if (pos < 0) {
-      if (pos < -1 && piece == 0 && lane == 0 && a.status) atomicOr(a.status, DDTREE_ST_BAD_LENGTH);
+      if (pos < -1 && has_row && lane == 0 && a.status) atomicOr(a.status, DDTREE_ST_BAD_LENGTH);
       continue;
     }
-    const int g = lane & 3;
-    const int c0 = kInterleaved ? 2 * g : g, c1 = kInterleaved ? 2 * g + 1 : g + 4;
-    if (piece == 0) {
-      const int64_t slot = __ldg(a.slots + token);
-      if (slot < 0 || slot >= a.pool_rows) {
-        if (slot != -1 && lane == 0 && a.status) atomicOr(a.status, DDTREE_ST_BAD_INDEX);
-        continue;
-      }
-      const uint4* src = reinterpret_cast<const uint4*>(a.kv + (int64_t)token * a.kv_stride);
+    const float2 mine = turn(freq, pos, a.rope.mscale);
+    float2 cs[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      cs[i] = make_float2(__shfl_sync(0xffffffffu, mine.x, 8 * g + i), __shfl_sync(0xffffffffu, mine.y, 8 * g + i));
+    if (has_row && (slot < 0 || slot >= a.pool_rows)) {
+      if (slot != -1 && lane == 0 && a.status) atomicOr(a.status, DDTREE_ST_BAD_INDEX);
+    } else if (has_row) {
       uint4* dst = reinterpret_cast<uint4*>(a.pool + slot * kRow);
-      uint4 v[2] = {__ldg(src + lane), __ldg(src + lane + 32)};
-      uint4 r0 = __ldg(src + kLatent / 8 + c0), r1 = __ldg(src + kLatent / 8 + c1);  // lanes 4..31 repeat 0..3
-      const float2 cs = turn(a.rope.turns[lane], pos, a.rope.mscale);
       if (a.weight) {
         float x[2][8], sum = 0.f;
 #pragma unroll
@@ -77,35 +108,31 @@ __global__ void __launch_bounds__(kThreads) mla_append_kernel(const __grid_const
         const float scale = rsqrtf(sum * (1.f / kLatent) + a.eps);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float w[8];
-          unpack8<false>(__ldg(reinterpret_cast<const uint4*>(a.weight) + lane + 32 * j), w);
+          float y[8];
+          unpack8<false>(w[j], y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[j][i] = x[j][i] * scale * w[i];
+          for (int i = 0; i < 8; ++i) x[j][i] = x[j][i] * scale * y[i];
           v[j] = pack8<false>(x[j]);
         }
       }
-      rotate_group(r0, r1, g, cs, kInterleaved);
+      rotate<kInterleaved>(r0, r1, cs);
       dst[lane] = v[0];
       dst[lane + 32] = v[1];
       if (lane < 4) {
         dst[kLatent / 8 + c0] = r0;
         dst[kLatent / 8 + c1] = r1;
       }
-    } else {
-      const int head = (piece - 1) * kHeadsPerPiece + (lane >> 2);
-      const bool have = head < a.n_heads;
-      uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
-      if (have) {  // plain loads: q_out may be the same buffer
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)token * a.q_token + (int64_t)head * a.q_head);
-        r0 = src[c0];
-        r1 = src[c1];
-      }
-      const float2 cs = turn(a.rope.turns[lane], pos, a.rope.mscale);
-      rotate_group(r0, r1, g, cs, kInterleaved);
-      if (have) {
-        uint4* dst = reinterpret_cast<uint4*>(a.q_out + (int64_t)token * a.o_token + (int64_t)head * a.o_head);
-        dst[c0] = r0;
-        dst[c1] = r1;
+    }
+    for (int base = h_begin; base < h_end; base += kHeadsPerStep * kUnroll) {
+      if (base != h_begin) load_heads(base);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int h = base + u * kHeadsPerStep + sub;
+        if (h >= h_end) continue;
+        rotate<kInterleaved>(q0[u], q1[u], cs);
+        uint4* dst = reinterpret_cast<uint4*>(a.q_out + token * a.o_token + (int64_t)h * a.o_head);
+        dst[c0] = q0[u];
+        dst[c1] = q1[u];
       }
     }
   }
@@ -115,11 +142,17 @@ __global__ void __launch_bounds__(kThreads) mla_append_kernel(const __grid_const
 
 cudaError_t launch_mla_append(const MlaAppendArgs& a, int num_sms, cudaStream_t stream) {
   if (a.n_tokens == 0) return cudaSuccess;
-  const int pieces = 1 + (a.n_heads + kHeadsPerPiece - 1) / kHeadsPerPiece;
-  const int64_t blocks = ((int64_t)a.n_tokens * pieces + kThreads / 32 - 1) / (kThreads / 32);
+  // A token is one warp's work where tokens fill the SMs with 32 warps each;
+  // fewer tokens are cut into slices, down to eight heads.
+  const int steps = std::max(1, (a.n_heads + kHeadsPerStep - 1) / kHeadsPerStep);
+  const int64_t want = ((int64_t)num_sms * 32 + a.n_tokens - 1) / a.n_tokens;
+  const int slice_steps = (int)std::max<int64_t>(1, steps / std::min<int64_t>(want, steps));
+  const int slices = (steps + slice_steps - 1) / slice_steps;
+  const int64_t blocks = ((int64_t)a.n_tokens * slices + kThreads / 32 - 1) / (kThreads / 32);
   const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)num_sms * 64);
-  if (a.rope.interleaved) mla_append_kernel<true><<<grid, kThreads, 0, stream>>>(a, pieces);
-  else mla_append_kernel<false><<<grid, kThreads, 0, stream>>>(a, pieces);
+  const int slice_heads = slice_steps * kHeadsPerStep;
+  if (a.rope.interleaved) mla_append_kernel<true><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);
+  else mla_append_kernel<false><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);
   return cudaGetLastError();
 }
 
