@@ -276,6 +276,21 @@ struct DraftAppendArgs {
   RopeArgs rope;
 };
 
+// Quotients of numbers below 2^31 by one divisor (1 .. 65536): a product with
+// ceil(2^(31+l) / d), 2^(l-1) < d <= 2^l, is exact for them.
+struct Divider {
+  uint32_t d, mul, shift;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int quotient(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> shift); }
+#endif
+};
+inline Divider make_divider(int d) {
+  uint32_t l = 0;
+  while ((1u << l) < (uint32_t)d) ++l;
+  const uint64_t one = 1ull << (31 + l);
+  return Divider{(uint32_t)d, (uint32_t)((one + d - 1) / d), 31 + l};
+}
+
 // Everything the drafter's attention needs (see include/ddtree_draft.h).
 struct DraftAttnArgs {
   const uint16_t* q;         // tokens q_stride apart
@@ -288,6 +303,7 @@ struct DraftAttnArgs {
   uint8_t* ws;               // workspace: status block, then partial results
   int64_t q_stride, out_stride, page_stride, token_stride, head_stride, n_pages;
   float scale_log2;          // sm_scale * log2(e)
+  Divider page;              // by the tokens of a page
   int32_t n_tokens, n_heads, n_kv_heads, group, head_dim, dtype, page_size;
   int32_t window, n_sinks, table_rows, table_stride;
   int32_t row_tile, n_shares;

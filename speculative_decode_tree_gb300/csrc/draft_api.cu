@@ -119,6 +119,7 @@ extern "C" int ddtree_draft_attention(const ddtree_draft_plan_t* plan, const voi
   a.head_dim = plan->head_dim;
   a.dtype = plan->dtype;
   a.page_size = plan->page_size;
+  a.page = make_divider(plan->page_size);
   a.window = plan->window;
   a.n_sinks = plan->n_sinks;
   a.table_rows = table_rows;

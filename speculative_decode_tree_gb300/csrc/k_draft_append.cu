@@ -16,11 +16,11 @@
 namespace ddtree {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kThreads = 128;
+constexpr int kUnroll = 3;
 
 template <bool kHalf, int kDim, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) draft_append_kernel(const __grid_constant__ DraftAppendArgs a, int slices,
+__global__ void __launch_bounds__(kThreads, 8) draft_append_kernel(const __grid_constant__ DraftAppendArgs a, int slices,
                                                                 int slice_heads) {
   constexpr int kChunks = kDim / 8;              // lanes of a head: 8, 16 or 32
   constexpr int kHeadsPerStep = 32 / kChunks;
@@ -153,7 +153,7 @@ cudaError_t launch(const DraftAppendArgs& a, int num_sms, cudaStream_t stream) {
   const int slice_steps = (int)std::max<int64_t>(1, steps / std::min<int64_t>(want, steps));
   const int slices = (steps + slice_steps - 1) / slice_steps;
   const int64_t blocks = ((int64_t)a.n_tokens * slices + kThreads / 32 - 1) / (kThreads / 32);
-  const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)num_sms * 64);
+  const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)num_sms * 8);
   const int slice_heads = slice_steps * kHeadsPerStep;
   if (a.rope.interleaved) draft_append_kernel<kHalf, kDim, true><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);
   else draft_append_kernel<kHalf, kDim, false><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);

@@ -28,32 +28,40 @@
 //    other shares leaves its maximum, sum and unnormalised rows per share (at
 //    most two per share), and a second small grid, launched ahead of time with
 //    programmatic dependence, joins them in share order.
+#include <atomic>
+
 #include "rope.cuh"
 #include "tc_ptx.cuh"
 
 namespace ddtree {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = 4;
 constexpr int kRing = 4;  // offset slots: the tile in use, those in flight, and the next
 
 template <int kDim, int kWM>
 struct Config {
   static constexpr int kKeys = kDim == 64 ? 128 : 64;       // keys of a tile
-  static constexpr int kWK = kWarps / kWM;                  // warps along the keys
+  // Warps along the rows, the keys and the columns of V.  Two warps share keys
+  // and halve the columns (both take the scores) where one would need the
+  // registers of a whole row: more warps to hide each other's latency.
+  static constexpr int kWN = kDim == 256 || (kDim == 128 && kWM > 1) ? 2 : 1;
+  static constexpr int kWK = (kDim == 64 ? 8 : 4) / kWM;
+  static constexpr int kWarps = kWM * kWN * kWK;
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kWarpKeys = kKeys / kWK;
-  static constexpr int kBlock = kDim == 256 ? 16 : (kWarpKeys < 32 ? kWarpKeys : 32);  // keys of one softmax step
+  static constexpr int kBlock = kDim == 256 || kWarpKeys < 32 ? 16 : 32;  // keys of one softmax step
+  static constexpr int kCols = kDim / kWN;                  // columns of a warp
   static constexpr int kRows = 16 * kWM;
   static constexpr int kRowBytes = kDim * 2;
   static constexpr int kTileBytes = kKeys * kRowBytes;      // of K, and of V
   static constexpr int kQBytes = kRows * kRowBytes;
-  // Two CTAs per SM for the narrower heads, one for 256 columns.
+  static constexpr int kCtas = kDim == 256 ? 1 : 2;         // per SM
   static constexpr int kStages = kWM == 1 || (kDim == 64 && kWM == 2) ? 3 : 2;
   static constexpr int kSmem = kStages * (2 * kTileBytes + kQBytes);
-  // The joined rows of all warps fit the stage they replace.
-  static_assert(kWarps * 16 * kDim * 4 <= 2 * kTileBytes, "merge buffer");
+  // The rows of all key parts fit the stage they replace.
+  static_assert(kWK * kRows * kDim * 4 <= 2 * kTileBytes, "merge buffer");
   static_assert(kRing >= kStages + 1, "offset ring");
+  static_assert(kThreads >= kKeys, "a thread per key looks its page up");
 };
 
 struct Record {     // of a share whose last unit goes on in later shares
@@ -96,6 +104,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
   }
 }
 
+// 2^x; results below the normal range become zero.
+__device__ __forceinline__ float power2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // What a token sees, from its position and table row.
 struct Token {
   int pos, row, lo, first, tiles;  // window start, sinks before it, tiles per key head (0: padding)
@@ -105,7 +120,7 @@ __device__ __forceinline__ Token token_of(const DraftAttnArgs& a, int n, int til
   Token t;
   t.pos = __ldg(a.positions + n);
   t.row = a.token_rows ? __ldg(a.token_rows + n) : n;
-  const bool ok = t.pos >= 0 && t.row >= 0 && t.row < a.table_rows && t.pos / a.page_size < a.table_stride;
+  const bool ok = t.pos >= 0 && t.row >= 0 && t.row < a.table_rows && a.page.quotient(t.pos) < a.table_stride;
   t.lo = ok && a.window > 0 ? max(0, t.pos - a.window + 1) : 0;
   t.first = min(a.n_sinks, t.lo);
   t.seen = ok ? (int64_t)t.first + t.pos - t.lo + 1 : 0;
@@ -122,12 +137,14 @@ struct Tile {
 enum { kFirst = 1, kLast = 2, kBegun = 4, kGoesOn = 8 };
 
 template <bool kHalf, int kDim, int kWM>
-__global__ void __launch_bounds__(kThreads) draft_attn_kernel(const DraftAttnArgs a) {
+__global__ void __launch_bounds__(Config<kDim, kWM>::kThreads, Config<kDim, kWM>::kCtas)
+draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   using C = Config<kDim, kWM>;
+  constexpr int kThreads = C::kThreads, kWarps = C::kWarps;
   constexpr int kChunks = kDim / 8;  // 16-byte chunks of a row
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t offsets[kRing][C::kKeys];   // element offset of a key's row, -1: not there
-  __shared__ uint32_t there[kRing][C::kKeys / 32];
+  __shared__ int64_t offsets[kRing][C::kKeys];   // element offset of a key's row
+  __shared__ uint32_t there[kRing][C::kKeys / 32];  // a bit per key that exists
   __shared__ Tile tiles[kRing];
   __shared__ float top_s[C::kWK][C::kRows], sum_s[C::kWK][C::kRows];
   __shared__ int64_t warp_sum[kWarps];
@@ -195,27 +212,24 @@ __global__ void __launch_bounds__(kThreads) draft_attn_kernel(const DraftAttnArg
   bool begun = tile > 0;
   if (share + 1 == shares && tid == 0) records[share].token = -1;  // its last unit cannot go on
 
-  // First half of a lookup: the page of this thread's key.  -2: no such key.
-  auto page_of_key = [&](int i) {
+  // First half of a lookup: the page of this thread's key (-2: no such key) and its place there.
+  auto page_of_key = [&](int i, int& in) {
     if (i >= count || tid >= C::kKeys) return -2;
     const int64_t x = (int64_t)tile * C::kKeys + tid;
     if (x >= tok.seen) return -2;
     const int j = (int)(x < tok.first ? x : x - tok.first + tok.lo);
-    return __ldg(a.table + (int64_t)tok.row * a.table_stride + j / a.page_size);
+    const int k = a.page.quotient(j);
+    in = j - k * a.page_size;
+    return __ldg(a.table + (int64_t)tok.row * a.table_stride + k);
   };
   // Second half: the row's offset and the tile's description; then one tile on.
-  auto finish_lookup = [&](int i, int page) {
+  auto finish_lookup = [&](int i, int page, int in) {
     if (i >= count) return;
     const int slot = i % kRing;
     if (tid < C::kKeys) {
       const bool good = page >= 0 && page < a.n_pages;
       if (page != -2 && !good) atomicOr(&bits, DDTREE_ST_BAD_INDEX);
-      int64_t off = -1;
-      if (good) {
-        const int64_t x = (int64_t)tile * C::kKeys + tid;
-        const int j = (int)(x < tok.first ? x : x - tok.first + tok.lo);
-        off = page * a.page_stride + (j % a.page_size) * a.token_stride + kv_head * a.head_stride;
-      }
+      const int64_t off = good ? page * a.page_stride + in * a.token_stride + kv_head * a.head_stride : 0;
       offsets[slot][tid] = off;
       const uint32_t have = __ballot_sync(0xffffffffu, good);
       if (lane == 0) there[slot][warp] = have;
@@ -258,83 +272,132 @@ __global__ void __launch_bounds__(kThreads) draft_attn_kernel(const DraftAttnArg
   const uint32_t q_ring = ring + C::kStages * 2 * C::kTileBytes;
   auto swizzled = [](int row, int chunk) { return (uint32_t)(row * C::kRowBytes + ((chunk ^ (row & 7)) << 4)); };
   // Starts the copies of tile i (every thread commits a group, empty or not).
+  // A thread copies one chunk of every kRowsPerStep-th row: the swizzle of its
+  // rows is the same, so shared addresses advance by a constant.
+  constexpr int kRowsPerStep = kThreads / kChunks;
+  static_assert(C::kKeys % kRowsPerStep == 0 && kRowsPerStep % 8 == 0, "copy steps");
+  const int copy_chunk = tid % kChunks, copy_row = tid / kChunks;
+  const uint32_t copy_at = swizzled(copy_row, copy_chunk);
+  const uint16_t *copy_k = a.k + 8 * copy_chunk, *copy_v = a.v + 8 * copy_chunk;
   auto start_copies = [&](int i) {
     if (i < count) {
       const int slot = i % kRing;
-      const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes, v_at = k_at + C::kTileBytes;
-      constexpr int kRowsPerStep = kThreads / kChunks;
-      const int c = tid % kChunks, r0 = tid / kChunks;
-#pragma unroll 8
-      for (int r = r0; r < C::kKeys; r += kRowsPerStep) {
-        const int64_t off = offsets[slot][r];
-        const uint32_t size = off >= 0 ? 16u : 0u;
-        const int64_t from = off >= 0 ? off + 8 * c : 0;
-        ptx::cp_async16_zfill(k_at + swizzled(r, c), a.k + from, size);
-        ptx::cp_async16_zfill(v_at + swizzled(r, c), a.v + from, size);
+      const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes + copy_at, v_at = k_at + C::kTileBytes;
+      uint32_t full = 0xffffffffu;
+#pragma unroll
+      for (int w = 0; w < C::kKeys / 32; ++w) full &= there[slot][w];
+      if (full == 0xffffffffu) {
+#pragma unroll
+        for (int r = 0; r < C::kKeys; r += kRowsPerStep) {
+          const int64_t off = offsets[slot][copy_row + r];
+          ptx::cp_async16(k_at + r * C::kRowBytes, copy_k + off);
+          ptx::cp_async16(v_at + r * C::kRowBytes, copy_v + off);
+        }
+      } else {
+#pragma unroll 2
+        for (int r = 0; r < C::kKeys; r += kRowsPerStep) {
+          const int64_t off = offsets[slot][copy_row + r];
+          const int key = copy_row + r;
+          const uint32_t size = (there[slot][key >> 5] >> (key & 31)) & 1 ? 16u : 0u;
+          ptx::cp_async16_zfill(k_at + r * C::kRowBytes, copy_k + off, size);
+          ptx::cp_async16_zfill(v_at + r * C::kRowBytes, copy_v + off, size);
+        }
       }
       const Tile t = tiles[slot];
       if (t.flags & kFirst) {
         const uint32_t q_at = q_ring + (t.unit % C::kStages) * C::kQBytes;
         const uint16_t* q = a.q + t.token * a.q_stride + (int64_t)t.kv_head * a.group * kDim;
 #pragma unroll
-        for (int r = r0; r < C::kRows; r += kRowsPerStep)
-          ptx::cp_async16_zfill(q_at + swizzled(r, c), r < a.group ? q + r * kDim + 8 * c : a.q, r < a.group ? 16u : 0u);
+        for (int r = copy_row; r < C::kRows; r += kRowsPerStep)
+          ptx::cp_async16_zfill(q_at + swizzled(r, copy_chunk), r < a.group ? q + r * kDim + 8 * copy_chunk : a.q,
+                                r < a.group ? 16u : 0u);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
-  for (int i = 0; i < C::kStages; ++i) finish_lookup(i, page_of_key(i));
+#pragma unroll 1
+  for (int i = 0; i < C::kStages; ++i) {
+    int in = 0;
+    const int page = page_of_key(i, in);
+    finish_lookup(i, page, in);
+  }
   __syncthreads();
+#pragma unroll 1
   for (int i = 0; i < C::kStages - 1; ++i) start_copies(i);
 
   // ---- this warp's rows (16 of the group) and keys of every tile
-  const int wm = warp % kWM, wk = warp / kWM;
+  const int wm = warp % kWM, wn = warp / kWM % C::kWN, wk = warp / (kWM * C::kWN);
   constexpr bool kHoldQ = kDim <= 128;  // query fragments in registers; wider heads read them again per tile
   uint32_t qf[kHoldQ ? kDim / 16 : 1][4];
-  float o[kDim / 8][4], top[2], sum[2];
+  float o[C::kCols / 8][4], top[2], sum[2];
   // Probabilities meet V in the cache's type.  fp16 holds nothing below 2^-24,
   // so there they carry a factor of 2^10: a key counts down to 2^-34 of the
   // largest, and the factor leaves with the division by the sum.
   constexpr float kShift = kHalf ? 10.f : 0.f;
 
+  // Fragment addresses.  A row's chunks are exchanged by its low three bits,
+  // which are the lane's in every matrix it addresses, so four offsets serve
+  // all columns and the rest is constant.
+  uint32_t k_off[4], v_off[4], q_off[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    k_off[j] = swizzled(wk * C::kWarpKeys + (lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1));
+    v_off[j] = swizzled(wk * C::kWarpKeys + (lane & 15), 2 * j + (lane >> 4)) + wn * C::kCols * 2;
+    q_off[j] = swizzled(wm * 16 + (lane & 15), 2 * j + (lane >> 4));
+  }
+
   for (int i = 0; i < count; ++i) {
     asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
     __syncthreads();
     start_copies(i + C::kStages - 1);
-    const int next_page = page_of_key(i + C::kStages);
+    int next_in = 0;
+    const int next_page = page_of_key(i + C::kStages, next_in);
     const int slot = i % kRing;
     const Tile t = tiles[slot];
     const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes, v_at = k_at + C::kTileBytes;
     const uint32_t q_at = q_ring + (t.unit % C::kStages) * C::kQBytes;
-    const int q_row = wm * 16 + (lane & 15), q_chunk = lane >> 4;
     if (t.flags & kFirst) {
       if constexpr (kHoldQ) {
 #pragma unroll
-        for (int ks = 0; ks < kDim / 16; ++ks) ldsm4(q_at + swizzled(q_row, 2 * ks + q_chunk), qf[ks]);
+        for (int ks = 0; ks < kDim / 16; ++ks) ldsm4(q_at + q_off[ks & 3] + (ks >> 2) * 128, qf[ks]);
       }
 #pragma unroll
-      for (int d = 0; d < kDim / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+      for (int d = 0; d < C::kCols / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
       top[0] = top[1] = -INFINITY;
       sum[0] = sum[1] = 0.f;
     }
 #pragma unroll 1
     for (int block = 0; block < C::kWarpKeys; block += C::kBlock) {
       const int key0 = wk * C::kWarpKeys + block;
-      float s[C::kBlock / 8][4];
+      const uint32_t k_blk = k_at + block * C::kRowBytes, v_blk = v_at + block * C::kRowBytes;
+      // Short blocks sum even and odd column steps apart: twice the independent products.
+      constexpr int kSets = C::kBlock == 16 ? 2 : 1;
+      float part[kSets][C::kBlock / 8][4];
 #pragma unroll
-      for (int x = 0; x < C::kBlock / 8; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+      for (int y = 0; y < kSets; ++y) {
+#pragma unroll
+        for (int x = 0; x < C::kBlock / 8; ++x) part[y][x][0] = part[y][x][1] = part[y][x][2] = part[y][x][3] = 0.f;
+      }
 #pragma unroll
       for (int ks = 0; ks < kDim / 16; ++ks) {
         uint32_t again[4];
-        if constexpr (!kHoldQ) ldsm4(q_at + swizzled(q_row, 2 * ks + q_chunk), again);
+        if constexpr (!kHoldQ) ldsm4(q_at + q_off[ks & 3] + (ks >> 2) * 128, again);
         const uint32_t(&af)[4] = kHoldQ ? qf[kHoldQ ? ks : 0] : again;
 #pragma unroll
         for (int x = 0; x < C::kBlock / 16; ++x) {
           uint32_t b[4];
-          ldsm4(k_at + swizzled(key0 + 16 * x + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)), b);
-          mma<kHalf>(s[2 * x], af, b[0], b[1]);
-          mma<kHalf>(s[2 * x + 1], af, b[2], b[3]);
+          ldsm4(k_blk + k_off[ks & 3] + (ks >> 2) * 128 + x * 16 * C::kRowBytes, b);
+          mma<kHalf>(part[ks % kSets][2 * x], af, b[0], b[1]);
+          mma<kHalf>(part[ks % kSets][2 * x + 1], af, b[2], b[3]);
+        }
+      }
+      float(&s)[C::kBlock / 8][4] = part[0];
+      if constexpr (kSets == 2) {
+#pragma unroll
+        for (int x = 0; x < C::kBlock / 8; ++x) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[x][e] += part[kSets - 1][x][e];
         }
       }
       // Scores in base 2, keys that are not there at -inf.
@@ -371,7 +434,7 @@ __global__ void __launch_bounds__(kThreads) draft_attn_kernel(const DraftAttnArg
           sum[r] *= keep;
           top[r] = high[r];
 #pragma unroll
-          for (int d = 0; d < kDim / 8; ++d) {
+          for (int d = 0; d < C::kCols / 8; ++d) {
             o[d][2 * r] *= keep;
             o[d][2 * r + 1] *= keep;
           }
@@ -381,7 +444,7 @@ __global__ void __launch_bounds__(kThreads) draft_attn_kernel(const DraftAttnArg
 #pragma unroll
       for (int x = 0; x < C::kBlock / 8; ++x) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] = exp2f(s[x][e] - base[e >> 1]);
+        for (int e = 0; e < 4; ++e) s[x][e] = power2(s[x][e] - base[e >> 1]);
         sum[0] += s[x][0] + s[x][1];
         sum[1] += s[x][2] + s[x][3];
       }
@@ -390,15 +453,15 @@ __global__ void __launch_bounds__(kThreads) draft_attn_kernel(const DraftAttnArg
         const uint32_t p[4] = {pack2<kHalf>(s[2 * x][0], s[2 * x][1]), pack2<kHalf>(s[2 * x][2], s[2 * x][3]),
                                pack2<kHalf>(s[2 * x + 1][0], s[2 * x + 1][1]), pack2<kHalf>(s[2 * x + 1][2], s[2 * x + 1][3])};
 #pragma unroll
-        for (int d = 0; d < kDim / 16; ++d) {
+        for (int d = 0; d < C::kCols / 16; ++d) {
           uint32_t b[4];
-          ldsm4_trans(v_at + swizzled(key0 + 16 * x + (lane & 15), 2 * d + (lane >> 4)), b);
+          ldsm4_trans(v_blk + v_off[d & 3] + (d >> 2) * 128 + x * 16 * C::kRowBytes, b);
           mma<kHalf>(o[2 * d], p, b[0], b[1]);
           mma<kHalf>(o[2 * d + 1], p, b[2], b[3]);
         }
       }
     }
-    finish_lookup(i + C::kStages, next_page);
+    finish_lookup(i + C::kStages, next_page, next_in);
     if (!(t.flags & kLast)) continue;
 
     // ---- the unit ends here: join the warps' rows through this tile's stage
@@ -412,14 +475,14 @@ __global__ void __launch_bounds__(kThreads) draft_attn_kernel(const DraftAttnArg
       sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
       sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
       const int row = wm * 16 + g + 8 * r;
-      if ((lane & 3) == 0) {
+      if ((lane & 3) == 0 && wn == 0) {
         top_s[wk][row] = top[r];
         sum_s[wk][row] = sum[r];
       }
       if (row < a.group) {
 #pragma unroll
-        for (int d = 0; d < kDim / 8; ++d)
-          *reinterpret_cast<float2*>(cell(wk, row, 8 * d + 2 * (lane & 3))) = make_float2(o[d][2 * r], o[d][2 * r + 1]);
+        for (int d = 0; d < C::kCols / 8; ++d)
+          *reinterpret_cast<float2*>(cell(wk, row, wn * C::kCols + 8 * d + 2 * (lane & 3))) = make_float2(o[d][2 * r], o[d][2 * r + 1]);
       }
     }
     __syncthreads();
@@ -464,8 +527,11 @@ __global__ void __launch_bounds__(kThreads) draft_attn_kernel(const DraftAttnArg
 
 // Joins the shares' parts of every unit that crosses shares, a CTA per share
 // that such a unit starts in and row; CTA (0, 0) gathers the status words.
+constexpr int kJoinThreads = 128;
+
 template <bool kHalf, int kDim>
-__global__ void __launch_bounds__(kThreads) draft_join_kernel(const DraftAttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) draft_join_kernel(const __grid_constant__ DraftAttnArgs a) {
+  constexpr int kThreads = kJoinThreads, kWarps = kThreads / 32;
   constexpr int kLanes = kDim / 4;               // threads of a row, a float4 each
   constexpr int kParts = kThreads / kLanes;      // parts taken at once
   __shared__ float4 acc[kParts][kLanes];
@@ -537,14 +603,23 @@ __global__ void __launch_bounds__(kThreads) draft_join_kernel(const DraftAttnArg
 template <bool kHalf, int kDim, int kWM>
 cudaError_t launch(const DraftAttnArgs& a, cudaStream_t stream) {
   using C = Config<kDim, kWM>;
-  cudaError_t e = cudaFuncSetAttribute(draft_attn_kernel<kHalf, kDim, kWM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  // The shared-memory limit belongs to the kernel on a device: set once on each.
+  static std::atomic<uint64_t> have{0};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
-  draft_attn_kernel<kHalf, kDim, kWM><<<a.n_shares, kThreads, C::kSmem, stream>>>(a);
+  const uint64_t bit = 1ull << (device & 63);
+  if (!(have.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(draft_attn_kernel<kHalf, kDim, kWM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    have.fetch_or(bit, std::memory_order_release);
+  }
+  draft_attn_kernel<kHalf, kDim, kWM><<<a.n_shares, C::kThreads, C::kSmem, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.n_shares, std::min(a.group, 8));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -7,10 +7,11 @@
 // all-or-nothing verdict by itself and no CTA waits for another.  The first
 // CTAs then write the lists of tokens and pages (a warp per request, so that
 // depths come by pointer doubling over the lanes), the others kv_indices: each
-// warp a contiguous share of the whole list, four consecutive entries per lane
-// and 16-byte store.  A lane finds its request by bisection once and then only
-// walks forward; page and place in the page advance by additions, and several
-// steps' table loads are in flight together.
+// warp a contiguous share of the whole list, eight consecutive entries per lane
+// and 32-byte store (four and 16 where every entry is a table entry).  A lane finds its request by bisection once and then only
+// walks forward; page and place in the page advance by additions.  (Two and four
+// steps' table loads in flight together took 27 and 31 us where one takes 24,
+// 1024 requests of 21M entries: registers cost more warps than they gain.)
 // A page of a request comes from the table below `held` and from the free list
 // above, so no thread reads a table entry that this launch writes.
 //
@@ -24,7 +25,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = DDTREE_MAX_BATCH / kThreads;
-constexpr int kSteps = 4;  // steps of kv_indices whose table loads are in flight together
 
 struct Shared {
   int32_t ptr[DDTREE_MAX_BATCH + 1];   // exclusive sums of P + n
@@ -67,7 +67,7 @@ struct Pages {
   const int32_t* table;  // its row
   const int32_t* fresh;  // such that fresh[k] is page k >= held
   int held;
-  __device__ __forceinline__ int operator[](int k) const { return k < held ? table[k] : __ldg(fresh + k); }
+  __device__ __forceinline__ int operator[](int k) const { return (k < held ? table : fresh)[k]; }
 };
 __device__ __forceinline__ Pages pages_of(const MapsArgs& a, const Shared& s, int head, int b) {
   Pages p;
@@ -254,29 +254,39 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ 
 
   // ---- the verify index layout
   if (!ok) return;
-  const int64_t warps = (int64_t)(gridDim.x - token_ctas) * kWarps;
-  const int64_t part = ((total + warps - 1) / warps + 127) / 128 * 128;  // whole steps of 32 lanes x 4 entries
-  const int64_t begin = ((int64_t)(blockIdx.x - token_ctas) * kWarps + warp) * part;
-  const int64_t end = begin + part < total ? begin + part : total;
-  if (begin + 4 * lane >= end) return;
-  const bool vec = ((uintptr_t)a.kv_indices & 15) == 0;
-  int64_t g0 = begin + 4 * lane;
+  constexpr int kEntries = kSinglePage ? 4 : 8;  // consecutive entries of a lane: one 16- or 32-byte store
+  constexpr uint32_t kStep = 32 * kEntries;
+  const uint32_t entries = (uint32_t)total;      // below 2^31, so sums with a few steps stay in 32 bits
+  const uint32_t warps = (gridDim.x - token_ctas) * kWarps;
+  const uint32_t part = ((entries + warps - 1) / warps + kStep - 1) / kStep * kStep;  // whole steps
+  const uint64_t part0 = (uint64_t)((blockIdx.x - token_ctas) * kWarps + warp) * part;
+  if (part0 + kEntries * lane >= entries) return;
+  uint32_t g0 = (uint32_t)part0 + kEntries * lane;
+  const uint32_t end = min((uint32_t)part0 + part, entries);
+  const bool vec = ((uintptr_t)a.kv_indices & (4 * kEntries - 1)) == 0;
   int b = request_of(s.ptr, B, (int)g0);
   Pages pages = pages_of(a, s, head, b);
-  int first = s.ptr[b], last = s.ptr[b + 1];  // the request's entries
+  uint32_t first = s.ptr[b], last = s.ptr[b + 1];  // the request's entries
   // k: page of entry g0, in: its place there; a step moves them by whole pages and a rest.
-  int k = ((int)g0 - first) / ps, in = ((int)g0 - first) - k * ps;
-  const int step_pages = 128 / ps, step_in = 128 - step_pages * ps;
-  // One step: the row numbers of four entries, from the pages that were loaded for them.
-  auto store = [&](int64_t g, const int (&row)[4]) {
-    if (vec && g + 4 <= total) {
-      *reinterpret_cast<int4*>(a.kv_indices + g) = make_int4(row[0], row[1], row[2], row[3]);
+  int k = (int)(g0 - first) / ps, in = (int)(g0 - first) - k * ps;
+  const int step_pages = (int)kStep / ps, step_in = (int)kStep - step_pages * ps;
+  auto store = [&](uint32_t g, const int (&row)[kEntries]) {
+    if (vec && g + kEntries <= entries) {
+      if constexpr (kSinglePage) {
+        *reinterpret_cast<int4*>(a.kv_indices + g) = make_int4(row[0], row[1], row[2], row[3]);
+      } else {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a.kv_indices + g), "r"(row[0]),
+                     "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(row[4]), "r"(row[5]), "r"(row[6]), "r"(row[7])
+                     : "memory");
+      }
     } else {
-      for (int e = 0; e < 4 && g + e < total; ++e) a.kv_indices[g + e] = row[e];
+#pragma unroll
+      for (int e = 0; e < kEntries; ++e)
+        if (g + e < entries) a.kv_indices[g + e] = row[e];
     }
   };
   auto forward = [&]() {
-    g0 += 128;
+    g0 += kStep;
     k += step_pages;
     in += step_in;
     if (in >= ps) {
@@ -287,53 +297,51 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ 
   while (g0 < end) {
     if (g0 >= last) {
       do ++b;  // requests without keys own no entry
-      while (s.ptr[b + 1] <= (int)g0);
+      while ((uint32_t)s.ptr[b + 1] <= g0);
       pages = pages_of(a, s, head, b);
       first = s.ptr[b];
       last = s.ptr[b + 1];
-      k = ((int)g0 - first) / ps;
-      in = ((int)g0 - first) - k * ps;
+      k = (int)(g0 - first) / ps;
+      in = (int)(g0 - first) - k * ps;
     }
-    if ((kSinglePage || ps >= 4) && g0 + 128 * (kSteps - 1) + 4 <= last && g0 + 128 * (kSteps - 1) < end) {
-      // The request's entries for kSteps steps: at most two pages a step, or four pages of one entry.
-      int page[kSteps][kSinglePage ? 4 : 2], at[kSteps];
-      int64_t g[kSteps];
+    if ((kSinglePage || ps >= kEntries) && g0 + kEntries <= last) {
+      // All of one request: at most two pages, or four pages of one entry.
+      int row[kEntries];
+      if constexpr (kSinglePage) {
+        int page[kEntries];
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        g[u] = g0;
-        at[u] = in;
-        if constexpr (kSinglePage) {
+        for (int e = 0; e < kEntries; ++e) page[e] = pages[k + e];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) page[u][e] = pages[k + e];
-        } else {
-          page[u][0] = pages[k];
-          page[u][1] = in + 4 > ps ? pages[k + 1] : 0;
+        for (int e = 0; e < kEntries; ++e) row[e] = row_of(a, page[e], 0);
+      } else {
+        // Rows count on within a page: one product per page, then additions.
+        const int left = ps - in;
+        const int p0 = pages[k], p1 = left < kEntries ? pages[k + 1] : p0;
+        const int from = p0 * ps + in, then = p1 * ps - left;
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) row[e] = (e < left ? from : then) + e;
+        if (max((uint32_t)p0, (uint32_t)p1) >= (uint32_t)a.n_pages) {
+#pragma unroll
+          for (int e = 0; e < kEntries; ++e) row[e] = e < left ? row_of(a, p0, in + e) : row_of(a, p1, e - left);
         }
-        forward();
       }
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        int row[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (kSinglePage) row[e] = row_of(a, page[u][e], 0);
-          else row[e] = at[u] + e < ps ? row_of(a, page[u][0], at[u] + e) : row_of(a, page[u][1], at[u] + e - ps);
-        }
-        store(g[u], row);
-      }
+      store(g0, row);
+      forward();
       continue;
     }
-    // Near a request's end, or pages of two and three entries: entry by entry.
-    int row[4];
-    int bb = b, kk = k, ii = in, stop = last;
+    // Near a request's end, or short pages: entry by entry.
+    int row[kEntries];
+    int bb = b, kk = k, ii = in;
+    uint32_t stop = last;
     Pages pp = pages;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (g0 + e >= total) break;
-      const int g = (int)(g0 + e);
+    for (int e = 0; e < kEntries; ++e) {
+      row[e] = -1;
+      const uint32_t g = g0 + e;
+      if (g >= entries) continue;
       if (g >= stop) {
         do ++bb;
-        while (s.ptr[bb + 1] <= g);
+        while ((uint32_t)s.ptr[bb + 1] <= g);
         pp = pages_of(a, s, head, bb);
         stop = s.ptr[bb + 1];
         kk = ii = 0;

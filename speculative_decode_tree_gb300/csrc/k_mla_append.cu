@@ -16,7 +16,7 @@
 namespace ddtree {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kHeadsPerStep = 8;
 constexpr int kUnroll = 2;  // steps of heads whose loads are in flight together
 
@@ -142,14 +142,14 @@ __global__ void __launch_bounds__(kThreads) mla_append_kernel(const __grid_const
 
 cudaError_t launch_mla_append(const MlaAppendArgs& a, int num_sms, cudaStream_t stream) {
   if (a.n_tokens == 0) return cudaSuccess;
-  // A token is one warp's work where tokens fill the SMs with 32 warps each;
+  // A token is one warp's work where tokens fill the SMs with 8 warps each;
   // fewer tokens are cut into slices, down to eight heads.
   const int steps = std::max(1, (a.n_heads + kHeadsPerStep - 1) / kHeadsPerStep);
-  const int64_t want = ((int64_t)num_sms * 32 + a.n_tokens - 1) / a.n_tokens;
+  const int64_t want = ((int64_t)num_sms * 8 + a.n_tokens - 1) / a.n_tokens;
   const int slice_steps = (int)std::max<int64_t>(1, steps / std::min<int64_t>(want, steps));
   const int slices = (steps + slice_steps - 1) / slice_steps;
   const int64_t blocks = ((int64_t)a.n_tokens * slices + kThreads / 32 - 1) / (kThreads / 32);
-  const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)num_sms * 64);
+  const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)num_sms * 128);
   const int slice_heads = slice_steps * kHeadsPerStep;
   if (a.rope.interleaved) mla_append_kernel<true><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);
   else mla_append_kernel<false><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);
