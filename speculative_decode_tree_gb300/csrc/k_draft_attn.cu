@@ -27,7 +27,7 @@
 //  - A unit that lies within a share is finished there.  One that crosses into
 //    other shares leaves its maximum, sum and unnormalised rows per share (at
 //    most two per share), and a second small grid, launched ahead of time with
-//    programmatic dependence, joins them in share order.
+//    programmatic dependence, joins them in a fixed order.
 #include <atomic>
 
 #include "rope.cuh"
@@ -56,7 +56,7 @@ struct Config {
   static constexpr int kTileBytes = kKeys * kRowBytes;      // of K, and of V
   static constexpr int kQBytes = kRows * kRowBytes;
   static constexpr int kCtas = kDim == 256 ? 1 : 2;         // per SM
-  static constexpr int kStages = kWM == 1 || (kDim == 64 && kWM == 2) ? 3 : 2;
+  static constexpr int kStages = kWM == 1 ? 3 : 2;
   static constexpr int kSmem = kStages * (2 * kTileBytes + kQBytes);
   // The rows of all key parts fit the stage they replace.
   static_assert(kWK * kRows * kDim * 4 <= 2 * kTileBytes, "merge buffer");
@@ -64,9 +64,13 @@ struct Config {
   static_assert(kThreads >= kKeys, "a thread per key looks its page up");
 };
 
-struct Record {     // of a share whose last unit goes on in later shares
-  int32_t token, kv_head, last_share, pad;
+// A unit that goes on from one share to others: where its parts lie.  There is
+// a record per unit where units are no more than shares, else one per share,
+// for the unit that starts there and goes on; token -1: nothing to join.
+struct Record {
+  int32_t token, kv_head, first_share, last_share;
 };
+__host__ __device__ inline bool by_unit(const DraftAttnArgs& a) { return (int64_t)a.n_tokens * a.n_kv_heads <= a.n_shares; }
 
 // Workspace: status block, per share a status word and a record, then the
 // (maximum, sum) pairs and the rows of two partial units per share.
@@ -182,9 +186,10 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     total += warp_sum[w];
   }
   const int64_t shares = total < a.n_shares ? total : a.n_shares;
+  const bool unit_records = by_unit(a);
   if (share >= shares) {
     if (tid == 0) {
-      records[share].token = -1;
+      if (!unit_records) records[share].token = -1;
       words[share] = 0;
     }
     return;
@@ -210,7 +215,6 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   int kv_head = (int)(start_at / tok.tiles);
   int tile = (int)(start_at - (int64_t)kv_head * tok.tiles);
   bool begun = tile > 0;
-  if (share + 1 == shares && tid == 0) records[share].token = -1;  // its last unit cannot go on
 
   // First half of a lookup: the page of this thread's key (-2: no such key) and its place there.
   auto page_of_key = [&](int i, int& in) {
@@ -244,14 +248,16 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
                 (unit_ends ? 0 : kGoesOn);
       tiles[slot] = t;
       if (tok.seen == 0) atomicOr(&bits, DDTREE_ST_BAD_LENGTH);
-      if (range_ends && share + 1 < shares) {
+      // The unit's record, where it starts; without units' own, the share's, where the share ends.
+      const bool goes_on = range_ends && !unit_ends && !begun;
+      if (unit_records ? !begun && (unit_ends || range_ends) : range_ends) {
         Record r;
-        r.token = unit_ends || begun ? -1 : cur;
+        r.token = goes_on ? cur : -1;
         r.kv_head = kv_head;
+        r.first_share = share;
         const int64_t last = end - 1 + (tok.tiles - 1 - tile);  // the unit's last tile in the list
         r.last_share = (int)(((last + 1) * shares - 1) / total);
-        r.pad = 0;
-        records[share] = r;
+        records[unit_records ? cur * a.n_kv_heads + kv_head : share] = r;
       }
     }
     if (unit_ends && !range_ends) {
@@ -335,6 +341,9 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   // so there they carry a factor of 2^10: a key counts down to 2^-34 of the
   // largest, and the factor leaves with the division by the sum.
   constexpr float kShift = kHalf ? 10.f : 0.f;
+  // A negative scale turns the products' signs instead; zero becomes a factor
+  // that no product survives, so that absent keys stay at -inf.
+  const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
 
   // Fragment addresses.  A row's chunks are exchanged by its low three bits,
   // which are the lane's in every matrix it addresses, so four offsets serve
@@ -400,14 +409,17 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
           for (int e = 0; e < 4; ++e) s[x][e] += part[kSets - 1][x][e];
         }
       }
-      // Scores in base 2, keys that are not there at -inf.
+      // Products as they are, keys that are not there at -inf; the scale (made
+      // positive, see below) enters with the maximum in one multiply-add.
       const uint32_t mask = there[slot][key0 >> 5] >> (key0 & 31);
       constexpr uint32_t kAll = C::kBlock == 32 ? 0xffffffffu : (1u << (C::kBlock & 31)) - 1;
       float high[2] = {top[0], top[1]};
+      if (a.scale_log2 < 0.f) {
 #pragma unroll
-      for (int x = 0; x < C::kBlock / 8; ++x) {
+        for (int x = 0; x < C::kBlock / 8; ++x) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] *= a.scale_log2;
+          for (int e = 0; e < 4; ++e) s[x][e] = -s[x][e];
+        }
       }
       if ((mask & kAll) != kAll) {
 #pragma unroll
@@ -430,7 +442,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       if (__any_sync(0xffffffffu, high[0] > top[0] || high[1] > top[1])) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float keep = top[r] == -INFINITY ? 0.f : exp2f(top[r] - high[r]);
+          const float keep = top[r] == -INFINITY ? 0.f : power2((top[r] - high[r]) * scale);
           sum[r] *= keep;
           top[r] = high[r];
 #pragma unroll
@@ -440,11 +452,11 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
           }
         }
       }
-      const float base[2] = {top[0] == -INFINITY ? 0.f : top[0] - kShift, top[1] == -INFINITY ? 0.f : top[1] - kShift};
+      const float base[2] = {top[0] == -INFINITY ? 0.f : kShift - top[0] * scale, top[1] == -INFINITY ? 0.f : kShift - top[1] * scale};
 #pragma unroll
       for (int x = 0; x < C::kBlock / 8; ++x) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] = power2(s[x][e] - base[e >> 1]);
+        for (int e = 0; e < 4; ++e) s[x][e] = power2(fmaf(s[x][e], scale, base[e >> 1]));
         sum[0] += s[x][0] + s[x][1];
         sum[1] += s[x][2] + s[x][3];
       }
@@ -476,7 +488,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
       const int row = wm * 16 + g + 8 * r;
       if ((lane & 3) == 0 && wn == 0) {
-        top_s[wk][row] = top[r];
+        top_s[wk][row] = top[r] == -INFINITY ? top[r] : top[r] * scale;  // from here on in base 2
         sum_s[wk][row] = sum[r];
       }
       if (row < a.group) {
@@ -497,7 +509,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < C::kWK; ++k) {
-        w[k] = exp2f(top_s[k][row] - from);
+        w[k] = power2(top_s[k][row] - from);
         l += w[k] * sum_s[k][row];
         const float4 u = *reinterpret_cast<const float4*>(cell(k, row, col)), v = *reinterpret_cast<const float4*>(cell(k, row, col + 4));
         x[0] += w[k] * u.x; x[1] += w[k] * u.y; x[2] += w[k] * u.z; x[3] += w[k] * u.w;
@@ -525,78 +537,104 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   if (tid == 0) words[share] = bits;
 }
 
-// Joins the shares' parts of every unit that crosses shares, a CTA per share
-// that such a unit starts in and row; CTA (0, 0) gathers the status words.
-constexpr int kJoinThreads = 128;
-
+// Joins the parts of the units that go on across shares: a CTA per record (x)
+// and slice of the group's rows (y); the last x gathers the status words.
+// Eight teams of kDim / 4 threads, a float4 each.  With many parts several
+// teams share a row, with few parts a team takes a row alone; every team keeps
+// its own running maximum, so sums and rows are loaded together.
 template <bool kHalf, int kDim>
-__global__ void __launch_bounds__(kJoinThreads) draft_join_kernel(const __grid_constant__ DraftAttnArgs a) {
-  constexpr int kThreads = kJoinThreads, kWarps = kThreads / 32;
-  constexpr int kLanes = kDim / 4;               // threads of a row, a float4 each
-  constexpr int kParts = kThreads / kLanes;      // parts taken at once
-  __shared__ float4 acc[kParts][kLanes];
-  __shared__ float high_s[kWarps], total_s[kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__global__ void __launch_bounds__(2 * kDim) draft_join_kernel(const __grid_constant__ DraftAttnArgs a, int row_slices) {
+  constexpr int kTeams = 8, kLanes = kDim / 4, kUnroll = 8;
+  constexpr int kThreads = kTeams * kLanes;
+  __shared__ float4 acc[kTeams][kLanes];
+  __shared__ float2 team_sum[kTeams];
+  const int tid = threadIdx.x;
   const Layout ws = layout_of(a.row_tile, kDim, a.n_shares);
+  const int x = blockIdx.x / row_slices, slice = blockIdx.x - x * row_slices;
+  const int records = by_unit(a) ? a.n_tokens * a.n_kv_heads : a.n_shares;
+  // Inputs of the call, not of the first grid: no need to wait for them.
+  const bool padding = by_unit(a) && x < records && __ldg(a.positions + x / a.n_kv_heads) == -1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
+  if (x == records) {
     uint32_t b = 0;
     for (int s = tid; s < a.n_shares; s += kThreads) b |= reinterpret_cast<const uint32_t*>(a.ws + ws.words)[s];
-    b = __reduce_or_sync(0xffffffffu, b);
-    __shared__ uint32_t all[kWarps];
-    if (lane == 0) all[warp] = b;
+    __shared__ uint32_t all;
+    if (tid == 0) all = 0;
     __syncthreads();
-    if (tid == 0) *reinterpret_cast<uint32_t*>(a.ws) = all[0] | all[1] | all[2] | all[3];
+    if (b) atomicOr(&all, b);
+    __syncthreads();
+    if (tid == 0) *reinterpret_cast<uint32_t*>(a.ws) = all;
+    return;
   }
-  const Record r = reinterpret_cast<const Record*>(a.ws + ws.records)[blockIdx.x];
+  if (padding) return;  // no share has this unit: nobody wrote its record
+  const Record r = reinterpret_cast<const Record*>(a.ws + ws.records)[x];
   if (r.token < 0) return;
-  const int first = blockIdx.x, parts = r.last_share - first + 1;
+  const int first = r.first_share, parts = r.last_share - first + 1;
   const float2* sums = reinterpret_cast<const float2*>(a.ws + ws.sums);
   const float4* rows = reinterpret_cast<const float4*>(a.ws + ws.rows);
   // Part p of the unit: the second place of its first share, the first place of the others.
   auto place = [&](int p, int row) { return ((int64_t)2 * (first + p) + (p == 0)) * a.row_tile + row; };
-  for (int row = blockIdx.y; row < a.group; row += gridDim.y) {
-    float high = -INFINITY;
-    for (int p = tid; p < parts; p += kThreads) high = fmaxf(high, sums[place(p, row)].x);
+  const int per_row = parts > 16 ? 8 : parts > 8 ? 4 : parts > 4 ? 2 : 1;  // teams of a row
+  const int team = tid / kLanes, c = tid - team * kLanes;
+  const int row_begin = a.group * slice / row_slices, row_end = a.group * (slice + 1) / row_slices;
+  for (int row0 = row_begin; row0 < row_end; row0 += kTeams / per_row) {
+    const int row = row0 + team / per_row;
+    float high = -INFINITY, total = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = team % per_row; p0 < parts && row < row_end; p0 += per_row * kUnroll) {
+      float2 s[kUnroll];
+      float4 v[kUnroll];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
-    if (lane == 0) high_s[warp] = high;
-    __syncthreads();
-    high = fmaxf(fmaxf(high_s[0], high_s[1]), fmaxf(high_s[2], high_s[3]));
-    const float from = high == -INFINITY ? 0.f : high;
-    float l = 0.f;
-    for (int p = tid; p < parts; p += kThreads) {
-      const float2 s = sums[place(p, row)];
-      l += exp2f(s.x - from) * s.y;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (lane == 0) total_s[warp] = l;
-    const int c = tid % kLanes;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = tid / kLanes; p < parts; p += kParts) {
-      const float w = exp2f(sums[place(p, row)].x - from);
-      const float4 v = rows[place(p, row) * kLanes + c];
-      x.x += w * v.x; x.y += w * v.y; x.z += w * v.z; x.w += w * v.w;
-    }
-    acc[tid / kLanes][c] = x;
-    __syncthreads();
-    if (tid < kLanes) {
-      const float total = total_s[0] + total_s[1] + total_s[2] + total_s[3];
-      const float inv = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
-      for (int k = 1; k < kParts; ++k) {
-        x.x += acc[k][c].x; x.y += acc[k][c].y; x.z += acc[k][c].z; x.w += acc[k][c].w;
+      for (int u = 0; u < kUnroll; ++u) {
+        const int p = p0 + u * per_row;
+        s[u] = make_float2(-INFINITY, 0.f);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p < parts) {
+          s[u] = sums[place(p, row)];
+          v[u] = rows[place(p, row) * kLanes + c];
+        }
       }
+      float top = high;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) top = fmaxf(top, s[u].x);
+      const float from = top == -INFINITY ? 0.f : top, keep = power2(high - from);
+      total *= keep;
+      o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
+      high = top;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const float w = power2(s[u].x - from);
+        total += w * s[u].y;
+        o.x += w * v[u].x; o.y += w * v[u].y; o.z += w * v[u].z; o.w += w * v[u].w;
+      }
+    }
+    if (per_row > 1) {  // the same in the whole CTA
+      acc[team][c] = o;
+      if (c == 0) team_sum[team] = make_float2(high, total);
+      __syncthreads();
+      if (team % per_row == 0) {
+        for (int k = 0; k < per_row; ++k) high = fmaxf(high, team_sum[team + k].x);
+        const float from = high == -INFINITY ? 0.f : high;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        total = 0.f;
+        for (int k = 0; k < per_row; ++k) {
+          const float w = power2(team_sum[team + k].x - from);
+          const float4 v = acc[team + k][c];
+          total += w * team_sum[team + k].y;
+          o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+        }
+      }
+      __syncthreads();
+    }
+    if (team % per_row == 0 && row < row_end) {
+      const float inv = total == 0.f ? 0.f : 1.f / total;
       const int head = r.kv_head * a.group + row;
       *reinterpret_cast<uint2*>(a.out + r.token * a.out_stride + (int64_t)head * kDim + 4 * c) =
-          make_uint2(pack2<kHalf>(x.x * inv, x.y * inv), pack2<kHalf>(x.z * inv, x.w * inv));
+          make_uint2(pack2<kHalf>(o.x * inv, o.y * inv), pack2<kHalf>(o.z * inv, o.w * inv));
       constexpr float kShift = kHalf ? 10.f : 0.f;
       if (a.lse && c == 0)
         a.lse[(int64_t)r.token * a.n_heads + head] = total == 0.f ? -INFINITY : (high - kShift + log2f(total)) * 0.6931471805599453f;
     }
-    __syncthreads();
   }
 }
 
@@ -618,15 +656,19 @@ cudaError_t launch(const DraftAttnArgs& a, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.n_shares, std::min(a.group, 8));
-  cfg.blockDim = dim3(kJoinThreads);
+  // Rows get CTAs of their own where records are few (their units have many
+  // parts); many records have few parts each, and one CTA takes all rows.
+  const int records = by_unit(a) ? a.n_tokens * a.n_kv_heads : a.n_shares;
+  const int slices = std::max(1, std::min(a.group, a.n_shares / records));
+  cfg.gridDim = dim3(records * slices + 1);
+  cfg.blockDim = dim3(2 * kDim);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, draft_join_kernel<kHalf, kDim>, a);
+  return cudaLaunchKernelEx(&cfg, draft_join_kernel<kHalf, kDim>, a, slices);
 }
 
 template <bool kHalf, int kDim>
