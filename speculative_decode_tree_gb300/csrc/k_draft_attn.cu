@@ -15,9 +15,9 @@
 //    list exists only as sums over the tokens, which every CTA takes for itself.
 //  - A ring of stages in shared memory, filled by 16-byte cp.async across unit
 //    borders: the next unit's first tiles and its queries are under way while
-//    the last unit finishes.  Page lookups run one tile ahead of the copies and
-//    leave row offsets and a validity bit per key in a small ring; a key that is
-//    not there is filled with zeros and masked.
+//    the last unit finishes.  A warp of its own runs the page lookups one tile
+//    ahead of the copies and leaves row offsets and a validity bit per key in a
+//    small ring; a key that is not there is filled with zeros and masked.
 //  - The group's query heads are the rows of the matrix instruction (16 rows,
 //    padded), so a key row read once serves them all.  Rows are few, and a
 //    unit's keys are split over the warps instead, each with its own running
@@ -41,13 +41,17 @@ constexpr int kRing = 4;  // offset slots: the tile in use, those in flight, and
 template <int kDim, int kWM>
 struct Config {
   static constexpr int kKeys = kDim == 64 ? 128 : 64;       // keys of a tile
-  // Warps along the rows, the keys and the columns of V.  Two warps share keys
-  // and halve the columns (both take the scores) where one would need the
-  // registers of a whole row: more warps to hide each other's latency.
-  static constexpr int kWN = kDim == 256 || (kDim == 128 && kWM > 1) ? 2 : 1;
-  static constexpr int kWK = (kDim == 64 ? 8 : 4) / kWM;
+  // Warps along the rows, the keys and the columns of V.  256 columns are
+  // halved between two warps (both take the scores): a whole row's registers
+  // would leave too few warps to hide each other's latency.
+  static constexpr int kWN = kDim == 256 ? 2 : 1;
+  static constexpr int kWK = kDim == 256 || (kDim == 128 && kWM == 1) ? 4 / kWM : 8 / kWM;
   static constexpr int kWarps = kWM * kWN * kWK;
-  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kThreads = 32 * kWarps;              // that compute
+  // One more warp looks the keys up, where its registers leave room for the
+  // other warps' (17 warps on an SM get 96 each); else warp 0 does.
+  static constexpr bool kLookupWarp = kDim != 128 || kWM == 1;
+  static constexpr int kAllThreads = kThreads + (kLookupWarp ? 32 : 0);
   static constexpr int kWarpKeys = kKeys / kWK;
   static constexpr int kBlock = kDim == 256 || kWarpKeys < 32 ? 16 : 32;  // keys of one softmax step
   static constexpr int kCols = kDim / kWN;                  // columns of a warp
@@ -57,11 +61,14 @@ struct Config {
   static constexpr int kQBytes = kRows * kRowBytes;
   static constexpr int kCtas = kDim == 256 ? 1 : 2;         // per SM
   static constexpr int kStages = kWM == 1 ? 3 : 2;
+  // Query fragments in registers for the whole unit, or read again per tile.
+  static constexpr bool kHoldQ = kDim == 64 || (kDim == 128 && kWM == 1);
   static constexpr int kSmem = kStages * (2 * kTileBytes + kQBytes);
-  // The rows of all key parts fit the stage they replace.
-  static_assert(kWK * kRows * kDim * 4 <= 2 * kTileBytes, "merge buffer");
+  // Columns joined at a time: the rows of all key parts fit the stage they replace.
+  static constexpr int kRounds = kWK * kRows * kDim * 4 <= 2 * kTileBytes ? 1 : 2;
+  static constexpr int kRoundCols = kDim / kRounds;
+  static_assert(kWK * kRows * kRoundCols * 4 <= 2 * kTileBytes, "merge buffer");
   static_assert(kRing >= kStages + 1, "offset ring");
-  static_assert(kThreads >= kKeys, "a thread per key looks its page up");
 };
 
 // A unit that goes on from one share to others: where its parts lie.  There is
@@ -141,17 +148,17 @@ struct Tile {
 enum { kFirst = 1, kLast = 2, kBegun = 4, kGoesOn = 8 };
 
 template <bool kHalf, int kDim, int kWM>
-__global__ void __launch_bounds__(Config<kDim, kWM>::kThreads, Config<kDim, kWM>::kCtas)
+__global__ void __launch_bounds__(Config<kDim, kWM>::kAllThreads, Config<kDim, kWM>::kCtas)
 draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   using C = Config<kDim, kWM>;
-  constexpr int kThreads = C::kThreads, kWarps = C::kWarps;
+  constexpr int kThreads = C::kThreads, kWarps = C::kWarps;  // without the lookup warp
   constexpr int kChunks = kDim / 8;  // 16-byte chunks of a row
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t offsets[kRing][C::kKeys];   // element offset of a key's row
   __shared__ uint32_t there[kRing][C::kKeys / 32];  // a bit per key that exists
   __shared__ Tile tiles[kRing];
   __shared__ float top_s[C::kWK][C::kRows], sum_s[C::kWK][C::kRows];
-  __shared__ int64_t warp_sum[kWarps];
+  __shared__ int64_t warp_sum[C::kAllThreads / 32];
   __shared__ int start_token;
   __shared__ int64_t start_at;
   __shared__ uint32_t bits;
@@ -164,7 +171,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- the list of tiles: sums over the tokens, a run of tokens per thread
-  const int per = (a.n_tokens + kThreads - 1) / kThreads;
+  const int per = (a.n_tokens + C::kAllThreads - 1) / C::kAllThreads;
   int64_t mine = 0;
   for (int i = 0; i < per; ++i) {
     const int n = tid * per + i;
@@ -181,7 +188,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   __syncthreads();
   int64_t before = inc - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < C::kAllThreads / 32; ++w) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
@@ -209,37 +216,30 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   __syncthreads();
   const int count = (int)(end - begin);
 
-  // ---- the next tile to look up; the same in every thread
+  // ---- lookups: kStages tiles ahead of the arithmetic, by one warp, two or four keys a lane
+  constexpr int kPerLane = C::kKeys / 32;
   int cur = start_token, unit = 0;
   Token tok = token_of(a, cur, C::kKeys);
   int kv_head = (int)(start_at / tok.tiles);
   int tile = (int)(start_at - (int64_t)kv_head * tok.tiles);
   bool begun = tile > 0;
-
-  // First half of a lookup: the page of this thread's key (-2: no such key) and its place there.
-  auto page_of_key = [&](int i, int& in) {
-    if (i >= count || tid >= C::kKeys) return -2;
-    const int64_t x = (int64_t)tile * C::kKeys + tid;
-    if (x >= tok.seen) return -2;
-    const int j = (int)(x < tok.first ? x : x - tok.first + tok.lo);
-    const int k = a.page.quotient(j);
-    in = j - k * a.page_size;
-    return __ldg(a.table + (int64_t)tok.row * a.table_stride + k);
-  };
-  // Second half: the row's offset and the tile's description; then one tile on.
-  auto finish_lookup = [&](int i, int page, int in) {
-    if (i >= count) return;
+  auto look_up = [&](int i) {
     const int slot = i % kRing;
-    if (tid < C::kKeys) {
-      const bool good = page >= 0 && page < a.n_pages;
-      if (page != -2 && !good) atomicOr(&bits, DDTREE_ST_BAD_INDEX);
-      const int64_t off = good ? page * a.page_stride + in * a.token_stride + kv_head * a.head_stride : 0;
-      offsets[slot][tid] = off;
-      const uint32_t have = __ballot_sync(0xffffffffu, good);
-      if (lane == 0) there[slot][warp] = have;
+    int page[kPerLane], in[kPerLane];
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const int64_t x = (int64_t)tile * C::kKeys + 32 * k + lane;
+      page[k] = -2;  // no such key
+      in[k] = 0;
+      if (x < tok.seen) {
+        const int j = (int)(x < tok.first ? x : x - tok.first + tok.lo);
+        const int number = a.page.quotient(j);
+        in[k] = j - number * a.page_size;
+        page[k] = __ldg(a.table + (int64_t)tok.row * a.table_stride + number);
+      }
     }
     const bool unit_ends = tile + 1 == tok.tiles, range_ends = i + 1 == count;
-    if (tid == 0) {
+    if (lane == 0) {
       Tile t;
       t.token = cur;
       t.kv_head = kv_head;
@@ -260,6 +260,14 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
         records[unit_records ? cur * a.n_kv_heads + kv_head : share] = r;
       }
     }
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const bool good = page[k] >= 0 && page[k] < a.n_pages;
+      if (page[k] != -2 && !good) atomicOr(&bits, DDTREE_ST_BAD_INDEX);
+      offsets[slot][32 * k + lane] = good ? page[k] * a.page_stride + in[k] * a.token_stride + kv_head * a.head_stride : 0;
+      const uint32_t have = __ballot_sync(0xffffffffu, good);
+      if (lane == 0) there[slot][k] = have;
+    }
     if (unit_ends && !range_ends) {
       tile = 0;
       begun = false;
@@ -273,6 +281,19 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       ++tile;
     }
   };
+  if (warp == (C::kLookupWarp ? kWarps : 0)) {
+    for (int i = 0; i < C::kStages && i < count; ++i) look_up(i);
+  }
+  if (C::kLookupWarp && warp == kWarps) {
+    __syncthreads();
+    for (int i = 0; i < count; ++i) {
+      __syncthreads();  // tile i's slot is in use, the one of tile i + kStages free
+      if (i + C::kStages < count) look_up(i + C::kStages);
+    }
+    __syncthreads();
+    if (lane == 0) words[share] = bits;
+    return;
+  }
 
   const uint32_t ring = ptx::smem_u32(smem);
   const uint32_t q_ring = ring + C::kStages * 2 * C::kTileBytes;
@@ -322,19 +343,16 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
-#pragma unroll 1
-  for (int i = 0; i < C::kStages; ++i) {
-    int in = 0;
-    const int page = page_of_key(i, in);
-    finish_lookup(i, page, in);
-  }
   __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < C::kStages - 1; ++i) start_copies(i);
 
+  auto computing_warps = [] { asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads) : "memory"); };
+
   // ---- this warp's rows (16 of the group) and keys of every tile
   const int wm = warp % kWM, wn = warp / kWM % C::kWN, wk = warp / (kWM * C::kWN);
-  constexpr bool kHoldQ = kDim <= 128;  // query fragments in registers; wider heads read them again per tile
+  constexpr bool kHoldQ = C::kHoldQ;
+  const bool idle = wm * 16 >= a.group;  // rows of the tile that no head fills
   uint32_t qf[kHoldQ ? kDim / 16 : 1][4];
   float o[C::kCols / 8][4], top[2], sum[2];
   // Probabilities meet V in the cache's type.  fp16 holds nothing below 2^-24,
@@ -360,8 +378,6 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
     __syncthreads();
     start_copies(i + C::kStages - 1);
-    int next_in = 0;
-    const int next_page = page_of_key(i + C::kStages, next_in);
     const int slot = i % kRing;
     const Tile t = tiles[slot];
     const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes, v_at = k_at + C::kTileBytes;
@@ -377,7 +393,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       sum[0] = sum[1] = 0.f;
     }
 #pragma unroll 1
-    for (int block = 0; block < C::kWarpKeys; block += C::kBlock) {
+    for (int block = 0; block < (idle ? 0 : C::kWarpKeys); block += C::kBlock) {
       const int key0 = wk * C::kWarpKeys + block;
       const uint32_t k_blk = k_at + block * C::kRowBytes, v_blk = v_at + block * C::kRowBytes;
       // Short blocks sum even and odd column steps apart: twice the independent products.
@@ -473,15 +489,17 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
         }
       }
     }
-    finish_lookup(i + C::kStages, next_page, next_in);
+    if (!C::kLookupWarp && warp == 0 && i + C::kStages < count) look_up(i + C::kStages);
     if (!(t.flags & kLast)) continue;
 
     // ---- the unit ends here: join the warps' rows through this tile's stage
-    __syncthreads();  // every warp is done with the tile
+    computing_warps();  // every warp is done with the tile
     float* rows = reinterpret_cast<float*>(smem + (i % C::kStages) * 2 * C::kTileBytes);
     // Row r of key part w; the exchange of column groups keeps the four rows that lanes write at once on other banks.
-    auto cell = [&](int w, int r, int col) { return rows + (w * C::kRows + r) * kDim + (col ^ ((r & 3) << 3)); };
+    auto cell = [&](int w, int r, int col) { return rows + (w * C::kRows + r) * C::kRoundCols + (col ^ ((r & 3) << 3)); };
     const int g = lane >> 2;
+    const bool whole = !(t.flags & (kBegun | kGoesOn));
+    const int64_t part = 2 * share + (t.flags & kBegun ? 0 : 1);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
@@ -491,50 +509,59 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
         top_s[wk][row] = top[r] == -INFINITY ? top[r] : top[r] * scale;  // from here on in base 2
         sum_s[wk][row] = sum[r];
       }
-      if (row < a.group) {
-#pragma unroll
-        for (int d = 0; d < C::kCols / 8; ++d)
-          *reinterpret_cast<float2*>(cell(wk, row, wn * C::kCols + 8 * d + 2 * (lane & 3))) = make_float2(o[d][2 * r], o[d][2 * r + 1]);
-      }
     }
-    __syncthreads();
-    const bool whole = !(t.flags & (kBegun | kGoesOn));
-    const int64_t part = 2 * share + (t.flags & kBegun ? 0 : 1);
-    for (int e = tid; e < a.group * (kDim / 8); e += kThreads) {
-      const int row = e / (kDim / 8), col = (e - row * (kDim / 8)) * 8;
-      float m = -INFINITY, l = 0.f, w[C::kWK];
 #pragma unroll
-      for (int k = 0; k < C::kWK; ++k) m = fmaxf(m, top_s[k][row]);
-      const float from = m == -INFINITY ? 0.f : m;
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int round = 0; round < C::kRounds; ++round) {
+      const int col0 = round * C::kRoundCols;
+      if (round > 0) computing_warps();
 #pragma unroll
-      for (int k = 0; k < C::kWK; ++k) {
-        w[k] = power2(top_s[k][row] - from);
-        l += w[k] * sum_s[k][row];
-        const float4 u = *reinterpret_cast<const float4*>(cell(k, row, col)), v = *reinterpret_cast<const float4*>(cell(k, row, col + 4));
-        x[0] += w[k] * u.x; x[1] += w[k] * u.y; x[2] += w[k] * u.z; x[3] += w[k] * u.w;
-        x[4] += w[k] * v.x; x[5] += w[k] * v.y; x[6] += w[k] * v.z; x[7] += w[k] * v.w;
+      for (int r = 0; r < 2; ++r) {
+        const int row = wm * 16 + g + 8 * r;
+        if (row >= a.group) continue;
+#pragma unroll
+        for (int d = 0; d < C::kCols / 8; ++d) {
+          const int col = wn * C::kCols + 8 * d - col0;
+          if (C::kRounds == 1 || (col >= 0 && col < C::kRoundCols))
+            *reinterpret_cast<float2*>(cell(wk, row, col + 2 * (lane & 3))) = make_float2(o[d][2 * r], o[d][2 * r + 1]);
+        }
       }
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+      computing_warps();
+      for (int e = tid; e < a.group * (C::kRoundCols / 8); e += kThreads) {
+        const int row = e / (C::kRoundCols / 8), at = (e - row * (C::kRoundCols / 8)) * 8, col = col0 + at;
+        float m = -INFINITY, l = 0.f, w[C::kWK];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] *= inv;
-        const int head = t.kv_head * a.group + row;
-        *reinterpret_cast<uint4*>(a.out + t.token * a.out_stride + (int64_t)head * kDim + col) = pack8<kHalf>(x);
-        if (a.lse && col == 0)
-          a.lse[(int64_t)t.token * a.n_heads + head] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
-      } else {
-        float4* to = reinterpret_cast<float4*>(a.ws + ws.rows) + (part * C::kRows + row) * (kDim / 4) + col / 4;
-        to[0] = make_float4(x[0], x[1], x[2], x[3]);
-        to[1] = make_float4(x[4], x[5], x[6], x[7]);
-        if (col == 0) reinterpret_cast<float2*>(a.ws + ws.sums)[part * C::kRows + row] = make_float2(m, l);
+        for (int k = 0; k < C::kWK; ++k) m = fmaxf(m, top_s[k][row]);
+        const float from = m == -INFINITY ? 0.f : m;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < C::kWK; ++k) {
+          w[k] = power2(top_s[k][row] - from);
+          l += w[k] * sum_s[k][row];
+          const float4 u = *reinterpret_cast<const float4*>(cell(k, row, at)), v = *reinterpret_cast<const float4*>(cell(k, row, at + 4));
+          x[0] += w[k] * u.x; x[1] += w[k] * u.y; x[2] += w[k] * u.z; x[3] += w[k] * u.w;
+          x[4] += w[k] * v.x; x[5] += w[k] * v.y; x[6] += w[k] * v.z; x[7] += w[k] * v.w;
+        }
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] *= inv;
+          const int head = t.kv_head * a.group + row;
+          *reinterpret_cast<uint4*>(a.out + t.token * a.out_stride + (int64_t)head * kDim + col) = pack8<kHalf>(x);
+          if (a.lse && col == 0)
+            a.lse[(int64_t)t.token * a.n_heads + head] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
+        } else {
+          float4* to = reinterpret_cast<float4*>(a.ws + ws.rows) + (part * C::kRows + row) * (kDim / 4) + col / 4;
+          to[0] = make_float4(x[0], x[1], x[2], x[3]);
+          to[1] = make_float4(x[4], x[5], x[6], x[7]);
+          if (col == 0) reinterpret_cast<float2*>(a.ws + ws.sums)[part * C::kRows + row] = make_float2(m, l);
+        }
       }
     }
     // The next iteration's barrier comes before this stage is filled again.
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  if (tid == 0) words[share] = bits;
+  if (!C::kLookupWarp && tid == 0) words[share] = bits;
 }
 
 // Joins the parts of the units that go on across shares: a CTA per record (x)
@@ -652,7 +679,7 @@ cudaError_t launch(const DraftAttnArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     have.fetch_or(bit, std::memory_order_release);
   }
-  draft_attn_kernel<kHalf, kDim, kWM><<<a.n_shares, C::kThreads, C::kSmem, stream>>>(a);
+  draft_attn_kernel<kHalf, kDim, kWM><<<a.n_shares, C::kAllThreads, C::kSmem, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
