@@ -307,7 +307,32 @@ struct DraftAttnArgs {
   int32_t n_tokens, n_heads, n_kv_heads, group, head_dim, dtype, page_size;
   int32_t window, n_sinks, table_rows, table_stride;
   int32_t row_tile, n_shares;
+  int32_t bundle;            // key heads that shares take side by side (divides them all)
 };
+
+// Launches that may begin while the stream's last kernel is still running
+// (programmatic dependence): the kernel waits for it with await_grid() before
+// it touches memory, in every thread block, and lets the next such launch
+// begin with release_grid().  After any other kernel the wait is the usual one.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                                Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void await_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void release_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
 
 // ---- launchers (one per .cu file) ----
 int draft_tile_keys(int head_dim);

@@ -26,6 +26,8 @@ __global__ void __launch_bounds__(kThreads, 8) draft_append_kernel(const __grid_
   constexpr int kHeadsPerStep = 32 / kChunks;
   constexpr int kPairsPerLane = kDim / 64;       // pairs a lane computes: dim / 2 over 32 lanes
   constexpr int kTurns = kInterleaved ? 4 : 8;   // pairs with elements in a chunk
+  release_grid();
+  await_grid();
   const int lane = threadIdx.x & 31;
   const int c = lane % kChunks, sub = lane / kChunks;
   const int nq = a.n_heads, nk = a.n_kv_heads, heads = nq + 2 * nk;
@@ -155,9 +157,8 @@ cudaError_t launch(const DraftAppendArgs& a, int num_sms, cudaStream_t stream) {
   const int64_t blocks = ((int64_t)a.n_tokens * slices + kThreads / 32 - 1) / (kThreads / 32);
   const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)num_sms * 8);
   const int slice_heads = slice_steps * kHeadsPerStep;
-  if (a.rope.interleaved) draft_append_kernel<kHalf, kDim, true><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);
-  else draft_append_kernel<kHalf, kDim, false><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);
-  return cudaGetLastError();
+  return launch_early(a.rope.interleaved ? draft_append_kernel<kHalf, kDim, true> : draft_append_kernel<kHalf, kDim, false>,
+                      grid, kThreads, 0, stream, a, slices, slice_heads);
 }
 
 }  // namespace

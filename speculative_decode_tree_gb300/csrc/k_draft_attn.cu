@@ -9,10 +9,13 @@
 //
 //  - Equal shares.  The visible keys of a (token, key head) unit are numbered
 //    without gaps (the sinks that lie before the window, then the window) and
-//    cut into tiles; all units' tiles form one list, and share c of G takes
-//    tiles [c T/G, (c+1) T/G).  One CTA per share, all resident at once, so
-//    every SM streams the same number of bytes whatever the lengths are.  The
-//    list exists only as sums over the tokens, which every CTA takes for itself.
+//    cut into tiles; all units' tiles form one list, and every share takes an
+//    equal run of it.  One CTA per share, all resident at once, so every SM
+//    streams the same number of bytes whatever the lengths are.  The list exists
+//    only as sums over the tokens, which every CTA takes for itself.
+//    Up to eight key heads go through the list side by side, one per share:
+//    where a token's heads lie next to each other, their shares read the same
+//    stretch of memory at the same time.
 //  - A ring of stages in shared memory, filled by 16-byte cp.async across unit
 //    borders: the next unit's first tiles and its queries are under way while
 //    the last unit finishes.  A warp of its own runs the page lookups one tile
@@ -122,6 +125,11 @@ __device__ __forceinline__ float power2(float x) {
   return y;
 }
 
+// Most lists are short enough for 32 bits, where a quotient takes a tenth of the time.
+__device__ __forceinline__ int64_t quotient(int64_t x, uint32_t d) {
+  return (x >> 32) == 0 ? (int64_t)((uint32_t)x / d) : (int64_t)((uint64_t)x / d);
+}
+
 // What a token sees, from its position and table row.
 struct Token {
   int pos, row, lo, first, tiles;  // window start, sinks before it, tiles per key head (0: padding)
@@ -164,18 +172,20 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   __shared__ uint32_t bits;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int share = blockIdx.x;
+  const int share = blockIdx.x, range = share / a.bundle, sub = share - range * a.bundle;
+  const int bundles = a.n_kv_heads / a.bundle;
   const Layout ws = layout_of(C::kRows, kDim, a.n_shares);
   Record* records = reinterpret_cast<Record*>(a.ws + ws.records);
   uint32_t* words = reinterpret_cast<uint32_t*>(a.ws + ws.words);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  release_grid();
+  await_grid();
 
   // ---- the list of tiles: sums over the tokens, a run of tokens per thread
   const int per = (a.n_tokens + C::kAllThreads - 1) / C::kAllThreads;
   int64_t mine = 0;
   for (int i = 0; i < per; ++i) {
     const int n = tid * per + i;
-    if (n < a.n_tokens) mine += (int64_t)token_of(a, n, C::kKeys).tiles * a.n_kv_heads;
+    if (n < a.n_tokens) mine += (int64_t)token_of(a, n, C::kKeys).tiles * bundles;
   }
   int64_t inc = mine;
 #pragma unroll
@@ -192,21 +202,23 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  const int64_t shares = total < a.n_shares ? total : a.n_shares;
+  const int64_t ranges = min(total, (int64_t)(a.n_shares / a.bundle));
   const bool unit_records = by_unit(a);
-  if (share >= shares) {
+  if (range >= ranges) {
     if (tid == 0) {
       if (!unit_records) records[share].token = -1;
       words[share] = 0;
     }
     return;
   }
-  const int64_t begin = share * total / shares, end = (share + 1) * total / shares;
+  // The first `longer` ranges have one tile more than the others.
+  const int64_t base = quotient(total, (uint32_t)ranges), longer = total - base * ranges;
+  const int64_t begin = range * base + min((int64_t)range, longer), end = begin + base + (range < longer);
   if (before <= begin && begin < before + mine) {
     int n = tid * per;
     int64_t at = begin - before;
     for (;; ++n) {
-      const int64_t here = (int64_t)token_of(a, n, C::kKeys).tiles * a.n_kv_heads;
+      const int64_t here = (int64_t)token_of(a, n, C::kKeys).tiles * bundles;
       if (at < here) break;
       at -= here;
     }
@@ -220,8 +232,9 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   constexpr int kPerLane = C::kKeys / 32;
   int cur = start_token, unit = 0;
   Token tok = token_of(a, cur, C::kKeys);
-  int kv_head = (int)(start_at / tok.tiles);
-  int tile = (int)(start_at - (int64_t)kv_head * tok.tiles);
+  const int first_bundle = (int)quotient(start_at, (uint32_t)tok.tiles);
+  int tile = (int)(start_at - (int64_t)first_bundle * tok.tiles);
+  int kv_head = first_bundle * a.bundle + sub;
   bool begun = tile > 0;
   auto look_up = [&](int i) {
     const int slot = i % kRing;
@@ -256,7 +269,8 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
         r.kv_head = kv_head;
         r.first_share = share;
         const int64_t last = end - 1 + (tok.tiles - 1 - tile);  // the unit's last tile in the list
-        r.last_share = (int)(((last + 1) * shares - 1) / total);
+        const int64_t in_longer = longer * (base + 1);
+        r.last_share = (int)(last < in_longer ? last / (base + 1) : longer + (last - in_longer) / base) * a.bundle + sub;
         records[unit_records ? cur * a.n_kv_heads + kv_head : share] = r;
       }
     }
@@ -272,8 +286,9 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       tile = 0;
       begun = false;
       ++unit;
-      if (++kv_head == a.n_kv_heads) {
-        kv_head = 0;
+      kv_head += a.bundle;
+      if (kv_head >= a.n_kv_heads) {
+        kv_head = sub;
         do tok = token_of(a, ++cur, C::kKeys);
         while (tok.tiles == 0);
       }
@@ -579,9 +594,10 @@ __global__ void __launch_bounds__(2 * kDim) draft_join_kernel(const __grid_const
   const Layout ws = layout_of(a.row_tile, kDim, a.n_shares);
   const int x = blockIdx.x / row_slices, slice = blockIdx.x - x * row_slices;
   const int records = by_unit(a) ? a.n_tokens * a.n_kv_heads : a.n_shares;
-  // Inputs of the call, not of the first grid: no need to wait for them.
+  release_grid();
+  await_grid();
+  // A padding token's units are in no share: nobody wrote their records.
   const bool padding = by_unit(a) && x < records && __ldg(a.positions + x / a.n_kv_heads) == -1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (x == records) {
     uint32_t b = 0;
     for (int s = tid; s < a.n_shares; s += kThreads) b |= reinterpret_cast<const uint32_t*>(a.ws + ws.words)[s];
@@ -593,14 +609,14 @@ __global__ void __launch_bounds__(2 * kDim) draft_join_kernel(const __grid_const
     if (tid == 0) *reinterpret_cast<uint32_t*>(a.ws) = all;
     return;
   }
-  if (padding) return;  // no share has this unit: nobody wrote its record
+  if (padding) return;
   const Record r = reinterpret_cast<const Record*>(a.ws + ws.records)[x];
   if (r.token < 0) return;
-  const int first = r.first_share, parts = r.last_share - first + 1;
+  const int first = r.first_share, parts = (r.last_share - first) / a.bundle + 1;
   const float2* sums = reinterpret_cast<const float2*>(a.ws + ws.sums);
   const float4* rows = reinterpret_cast<const float4*>(a.ws + ws.rows);
-  // Part p of the unit: the second place of its first share, the first place of the others.
-  auto place = [&](int p, int row) { return ((int64_t)2 * (first + p) + (p == 0)) * a.row_tile + row; };
+  // Part p of the unit, in every bundle-th share: the second place of the first one, the first place of the others.
+  auto place = [&](int p, int row) { return ((int64_t)2 * (first + p * a.bundle) + (p == 0)) * a.row_tile + row; };
   const int per_row = parts > 16 ? 8 : parts > 8 ? 4 : parts > 4 ? 2 : 1;  // teams of a row
   const int team = tid / kLanes, c = tid - team * kLanes;
   const int row_begin = a.group * slice / row_slices, row_end = a.group * (slice + 1) / row_slices;
@@ -679,23 +695,13 @@ cudaError_t launch(const DraftAttnArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     have.fetch_or(bit, std::memory_order_release);
   }
-  draft_attn_kernel<kHalf, kDim, kWM><<<a.n_shares, C::kAllThreads, C::kSmem, stream>>>(a);
-  e = cudaGetLastError();
+  e = launch_early(draft_attn_kernel<kHalf, kDim, kWM>, a.n_shares, C::kAllThreads, C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
   // Rows get CTAs of their own where records are few (their units have many
   // parts); many records have few parts each, and one CTA takes all rows.
   const int records = by_unit(a) ? a.n_tokens * a.n_kv_heads : a.n_shares;
   const int slices = std::max(1, std::min(a.group, a.n_shares / records));
-  cfg.gridDim = dim3(records * slices + 1);
-  cfg.blockDim = dim3(2 * kDim);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, draft_join_kernel<kHalf, kDim>, a, slices);
+  return launch_early(draft_join_kernel<kHalf, kDim>, records * slices + 1, 2 * kDim, 0, stream, a, slices);
 }
 
 template <bool kHalf, int kDim>

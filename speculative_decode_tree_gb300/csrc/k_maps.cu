@@ -89,6 +89,8 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ 
   __shared__ Shared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.batch, ps = a.page_size;
+  release_grid();
+  await_grid();
 
   // ---- sums over the batch
   const int head = a.held ? __ldg(a.free_head) : 0;
@@ -365,9 +367,7 @@ cudaError_t launch_maps(const MapsArgs& a, int num_sms, cudaStream_t stream) {
   const int64_t tokens = std::min<int64_t>((a.batch + kWarps - 1) / kWarps, num_sms);
   const int64_t index = a.kv_indices ? std::min<int64_t>((a.capacity + 1023) / 1024, (int64_t)num_sms * 4) : 0;
   const unsigned grid = (unsigned)(tokens + index);
-  if (a.page_size == 1) maps_kernel<true><<<grid, kThreads, 0, stream>>>(a, (int)tokens);
-  else maps_kernel<false><<<grid, kThreads, 0, stream>>>(a, (int)tokens);
-  return cudaGetLastError();
+  return launch_early(a.page_size == 1 ? maps_kernel<true> : maps_kernel<false>, grid, kThreads, 0, stream, a, (int)tokens);
 }
 
 }  // namespace ddtree

@@ -42,6 +42,8 @@ __device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2 (&cs)[8]
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) mla_append_kernel(const __grid_constant__ MlaAppendArgs a, int slices,
                                                               int slice_heads) {
+  release_grid();
+  await_grid();
   const int lane = threadIdx.x & 31;
   const int g = lane & 3, sub = lane >> 2;
   const int c0 = kInterleaved ? 2 * g : g, c1 = kInterleaved ? 2 * g + 1 : g + 4;
@@ -151,9 +153,8 @@ cudaError_t launch_mla_append(const MlaAppendArgs& a, int num_sms, cudaStream_t 
   const int64_t blocks = ((int64_t)a.n_tokens * slices + kThreads / 32 - 1) / (kThreads / 32);
   const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)num_sms * 128);
   const int slice_heads = slice_steps * kHeadsPerStep;
-  if (a.rope.interleaved) mla_append_kernel<true><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);
-  else mla_append_kernel<false><<<grid, kThreads, 0, stream>>>(a, slices, slice_heads);
-  return cudaGetLastError();
+  return launch_early(a.rope.interleaved ? mla_append_kernel<true> : mla_append_kernel<false>, grid, kThreads, 0, stream, a,
+                      slices, slice_heads);
 }
 
 }  // namespace ddtree
