@@ -101,3 +101,56 @@ class DeviceAccept:
                 "commit_indices": self.commit_indices.cpu().numpy(),
                 "freed_indices": self.freed_indices.cpu().numpy()}
 
+
+
+class DeviceStep:
+    """Static buffers of one decode step of the target model around verify
+    attention, each call marshalled once: step maps (page growth, index layout,
+    slots, positions), latent append (pool rows, rotated queries), verify.
+
+    The caller fills `prefix_lens`, `tree_parent`, `pages_held`, `free_head`,
+    `kv_new` [B*T, 576], `q` [B*T, H, 576] (latent part as absorbed, rope part
+    not yet rotated) and calls `run`; `out` and `lse` are the verify outputs and
+    `pages_held_out`, `free_head_out` what the step took.  `run` can be captured
+    into a graph and replayed with other contents up to `max_prefix`."""
+
+    def __init__(self, batch: int, n_nodes: int, n_heads: int, max_prefix: int, page_size: int, kv_pool: torch.Tensor,
+                 page_table: torch.Tensor, free_pages: torch.Tensor, rope: B.Rope, sm_scale: float,
+                 latent_weight: Optional[torch.Tensor] = None):
+        dev, i32, bf = kv_pool.device, torch.int32, torch.bfloat16
+        n_pages, n = int(kv_pool.shape[0]) // page_size, batch * n_nodes
+
+        def ints(*shape):
+            return torch.zeros(*shape, dtype=i32, device=dev)
+        self.prefix_lens, self.tree_parent = ints(batch), ints(batch, n_nodes)
+        self.pages_held, self.free_head = ints(batch), ints(1)
+        self.pages_held_out, self.free_head_out = ints(batch), ints(1)
+        self.kv_indptr, self.kv_indices = ints(batch + 1), ints(batch * (max_prefix + n_nodes))
+        self.new_slots, self.positions, self.status_word = ints(n), ints(n), ints(1)
+        self.kv_new = torch.zeros(n, 576, dtype=bf, device=dev)
+        self.q = torch.zeros(n, n_heads, 576, dtype=bf, device=dev)
+        self.out = torch.empty(n, n_heads, 512, dtype=bf, device=dev)
+        self.lse = torch.empty(n, n_heads, dtype=torch.float32, device=dev)
+        self.plan = B.ddtree_verify_mla_plan(batch, n_nodes, n_heads, [max_prefix] * batch, int(kv_pool.shape[0]))
+        self.plan.q_latent_row_stride = self.plan.q_rope_row_stride = 576
+        self.workspace = torch.empty(B.ddtree_verify_mla_workspace_size(self.plan), dtype=torch.uint8, device=dev)
+        q_rope = self.q[..., 512:]
+        self._calls = (
+            B.BoundStepMaps(page_table, self.prefix_lens, n_nodes, page_size, n_pages, self.kv_indptr, self.kv_indices,
+                            self.new_slots, self.positions, tree_parent=self.tree_parent, pages_held=self.pages_held,
+                            free_pages=free_pages, free_head=self.free_head, pages_held_out=self.pages_held_out,
+                            free_head_out=self.free_head_out, status=self.status_word),
+            B.BoundMlaAppend(rope, self.kv_new, self.positions, self.new_slots, kv_pool, latent_weight=latent_weight,
+                             q_rope=q_rope, q_out=q_rope, status=self.status_word),
+            B.BoundVerify(self.plan, self.q[..., :512], q_rope, kv_pool, self.kv_indices, self.kv_indptr,
+                          self.prefix_lens, self.tree_parent, sm_scale, self.out, self.lse, self.workspace))
+
+    def run(self, stream=None) -> None:
+        for call in self._calls:
+            call(stream)
+
+    def status(self, stream=None) -> int:
+        """Status bits of the last run (synchronises); clears those of the maps and the append."""
+        bits = B.ddtree_verify_mla_check(self.workspace, stream) | int(self.status_word)
+        self.status_word.zero_()
+        return bits
