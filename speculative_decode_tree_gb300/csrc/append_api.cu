@@ -185,6 +185,7 @@ extern "C" int ddtree_draft_append(int64_t n_tokens, int n_heads, const ddtree_d
   a.n_kv_heads = cache->n_kv_heads;
   a.head_dim = cache->head_dim;
   a.page_size = cache->page_size;
+  a.page = make_divider(cache->page_size);
   a.dtype = cache->dtype;
   copy_rope(rope, &a.rope);
   if (launch_draft_append(a, info.sms, (cudaStream_t)stream) != cudaSuccess) {

@@ -213,6 +213,21 @@ struct MaskArgs {
   int batch, n_nodes, num_sms;
 };
 
+// Quotients of numbers below 2^31 by one divisor (1 .. 65536): a product with
+// ceil(2^(31+l) / d), 2^(l-1) < d <= 2^l, is exact for them.
+struct Divider {
+  uint32_t d, mul, shift;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int quotient(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> shift); }
+#endif
+};
+inline Divider make_divider(int d) {
+  uint32_t l = 0;
+  while ((1u << l) < (uint32_t)d) ++l;
+  const uint64_t one = 1ull << (31 + l);
+  return Divider{(uint32_t)d, (uint32_t)((one + d - 1) / d), 31 + l};
+}
+
 // Everything the step maps need (see include/ddtree_maps.h).
 struct MapsArgs {
   int32_t* table;            // [table_rows, table_stride], grown in place
@@ -233,6 +248,7 @@ struct MapsArgs {
   int32_t* token_rows;       // [batch*max_new] or null
   uint32_t* status;          // or null
   int64_t n_pages, capacity;
+  Divider page;              // by the tokens of a page
   int32_t batch, max_new, page_size, table_rows, table_stride, n_free;
 };
 
@@ -271,25 +287,11 @@ struct DraftAppendArgs {
   int64_t q_stride, k_stride, v_stride, q_out_stride;
   int64_t page_stride, token_stride, head_stride;
   int64_t total_slots;       // n_pages * page_size
+  Divider page;              // by the tokens of a page
   float eps;
   int32_t n_tokens, n_heads, n_kv_heads, head_dim, page_size, dtype;
   RopeArgs rope;
 };
-
-// Quotients of numbers below 2^31 by one divisor (1 .. 65536): a product with
-// ceil(2^(31+l) / d), 2^(l-1) < d <= 2^l, is exact for them.
-struct Divider {
-  uint32_t d, mul, shift;
-#ifdef __CUDACC__
-  __device__ __forceinline__ int quotient(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> shift); }
-#endif
-};
-inline Divider make_divider(int d) {
-  uint32_t l = 0;
-  while ((1u << l) < (uint32_t)d) ++l;
-  const uint64_t one = 1ull << (31 + l);
-  return Divider{(uint32_t)d, (uint32_t)((one + d - 1) / d), 31 + l};
-}
 
 // Everything the drafter's attention needs (see include/ddtree_draft.h).
 struct DraftAttnArgs {

@@ -26,7 +26,6 @@ __global__ void __launch_bounds__(kThreads, 8) draft_append_kernel(const __grid_
   constexpr int kHeadsPerStep = 32 / kChunks;
   constexpr int kPairsPerLane = kDim / 64;       // pairs a lane computes: dim / 2 over 32 lanes
   constexpr int kTurns = kInterleaved ? 4 : 8;   // pairs with elements in a chunk
-  release_grid();
   await_grid();
   const int lane = threadIdx.x & 31;
   const int c = lane % kChunks, sub = lane / kChunks;
@@ -91,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 8) draft_append_kernel(const __grid_
         }
       }
       const bool write_kv = slot >= 0 && slot < a.total_slots;
-      const int page = write_kv ? slot / a.page_size : 0, off = write_kv ? slot - page * a.page_size : 0;
+      const int page = write_kv ? a.page.quotient(slot) : 0, off = write_kv ? slot - page * a.page_size : 0;
       const int64_t row = page * a.page_stride + off * a.token_stride;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {

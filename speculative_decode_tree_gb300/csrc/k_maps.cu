@@ -89,7 +89,6 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ 
   __shared__ Shared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.batch, ps = a.page_size;
-  release_grid();
   await_grid();
 
   // ---- sums over the batch
@@ -110,11 +109,11 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ 
       const int row = a.table_row ? __ldg(a.table_row + b) : b;
       const int held = a.held ? __ldg(a.held + b) : a.table_stride;
       const long long L = (long long)P + n;
-      const long long pages = (L + ps - 1) / ps;
-      if (P < 0 || n < 0 || n > a.max_new || row < 0 || row >= a.table_rows || held < 0 || held > a.table_stride ||
-          pages > a.table_stride) {
+      if (P < 0 || L > INT32_MAX || n < 0 || n > a.max_new || row < 0 || row >= a.table_rows || held < 0 || held > a.table_stride) {
         bad = true;
       } else {
+        const int pages = L > 0 ? a.page.quotient((int)L - 1) + 1 : 0;
+        bad = bad || pages > a.table_stride;
         keys[i] = L;
         fresh[i] = n;
         need[i] = pages > held ? pages - held : 0;
@@ -196,11 +195,12 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ 
       const int t0 = s.nptr[b], n = s.nptr[b + 1] - t0;
       const int P = s.ptr[b + 1] - s.ptr[b] - n;
       const Pages pages = pages_of(a, s, head, b);
-      int page[2], up[2], depth[2];  // up: next ancestor not yet counted, depth: the steps counted
+      int page[2], number[2], up[2], depth[2];  // up: next ancestor not yet counted, depth: the steps counted
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int i = lane + 32 * r;
-        page[r] = i < n ? pages[(P + i) / ps] : -1;
+        number[r] = a.page.quotient(P + min(i, max(n - 1, 0)));
+        page[r] = i < n ? pages[number[r]] : -1;
         up[r] = i - 1;
         depth[r] = i;
         if (a.parent) {
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ 
       for (int r = 0; r < 2; ++r) {
         const int i = lane + 32 * r;
         if (i >= n) continue;
-        a.new_slots[t0 + i] = row_of(a, page[r], (P + i) % ps);
+        a.new_slots[t0 + i] = row_of(a, page[r], P + i - number[r] * ps);
         a.positions[t0 + i] = P + depth[r];
         if (a.token_rows) a.token_rows[t0 + i] = s.row[b];
       }
@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ 
   Pages pages = pages_of(a, s, head, b);
   uint32_t first = s.ptr[b], last = s.ptr[b + 1];  // the request's entries
   // k: page of entry g0, in: its place there; a step moves them by whole pages and a rest.
-  int k = (int)(g0 - first) / ps, in = (int)(g0 - first) - k * ps;
-  const int step_pages = (int)kStep / ps, step_in = (int)kStep - step_pages * ps;
+  int k = a.page.quotient((int)(g0 - first)), in = (int)(g0 - first) - k * ps;
+  const int step_pages = a.page.quotient((int)kStep), step_in = (int)kStep - step_pages * ps;
   auto store = [&](uint32_t g, const int (&row)[kEntries]) {
     if (vec && g + kEntries <= entries) {
       if constexpr (kSinglePage) {
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ 
       pages = pages_of(a, s, head, b);
       first = s.ptr[b];
       last = s.ptr[b + 1];
-      k = (int)(g0 - first) / ps;
+      k = a.page.quotient((int)(g0 - first));
       in = (int)(g0 - first) - k * ps;
     }
     if ((kSinglePage || ps >= kEntries) && g0 + kEntries <= last) {
@@ -363,9 +363,9 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ 
 
 cudaError_t launch_maps(const MapsArgs& a, int num_sms, cudaStream_t stream) {
   // A warp per request for the lists, one step of 1024 index entries per CTA
-  // at least, four CTAs per SM at most.
+  // at least, as many CTAs as an SM holds at most.
   const int64_t tokens = std::min<int64_t>((a.batch + kWarps - 1) / kWarps, num_sms);
-  const int64_t index = a.kv_indices ? std::min<int64_t>((a.capacity + 1023) / 1024, (int64_t)num_sms * 4) : 0;
+  const int64_t index = a.kv_indices ? std::min<int64_t>((a.capacity + 1023) / 1024, (int64_t)num_sms * 5) : 0;
   const unsigned grid = (unsigned)(tokens + index);
   return launch_early(a.page_size == 1 ? maps_kernel<true> : maps_kernel<false>, grid, kThreads, 0, stream, a, (int)tokens);
 }

@@ -42,7 +42,6 @@ __device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2 (&cs)[8]
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) mla_append_kernel(const __grid_constant__ MlaAppendArgs a, int slices,
                                                               int slice_heads) {
-  release_grid();
   await_grid();
   const int lane = threadIdx.x & 31;
   const int g = lane & 3, sub = lane >> 2;

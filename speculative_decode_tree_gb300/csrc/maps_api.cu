@@ -68,6 +68,7 @@ extern "C" int ddtree_step_maps(int batch, int max_new, int page_size, int64_t n
   a.batch = batch;
   a.max_new = max_new;
   a.page_size = page_size;
+  a.page = make_divider(page_size);
   a.table_rows = table_rows;
   a.table_stride = table_stride;
   a.n_free = n_free;
