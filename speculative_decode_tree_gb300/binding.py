@@ -440,9 +440,11 @@ class _Bound:
         self._device = torch.cuda.current_device()
 
     def __call__(self, stream=None) -> None:
-        if torch.cuda.current_device() != self._device:
+        device = torch.cuda.current_device()
+        if device != self._device:
             raise ValueError(f"{self._entry}: bound on cuda:{self._device}, which is not the current device")
-        rc = self._fn(*self._args, ctypes.c_void_p(_stream(stream)))
+        handle = _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
+        rc = self._fn(*self._args, ctypes.c_void_p(handle))
         if rc != DDTREE_OK:
             raise DDTreeError(rc, self._entry)
 

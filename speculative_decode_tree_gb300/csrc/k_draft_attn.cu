@@ -56,7 +56,7 @@ struct Config {
   static constexpr bool kLookupWarp = kDim != 128 || kWM == 1;
   static constexpr int kAllThreads = kThreads + (kLookupWarp ? 32 : 0);
   static constexpr int kWarpKeys = kKeys / kWK;
-  static constexpr int kBlock = kDim == 256 || kWarpKeys < 32 ? 16 : 32;  // keys of one softmax step
+  static constexpr int kBlock = kWarpKeys < 32 ? 16 : 32;    // keys of one softmax step
   static constexpr int kCols = kDim / kWN;                  // columns of a warp
   static constexpr int kRows = 16 * kWM;
   static constexpr int kRowBytes = kDim * 2;
@@ -135,16 +135,20 @@ struct Token {
   int pos, row, lo, first, tiles;  // window start, sinks before it, tiles per key head (0: padding)
   int64_t seen;                    // visible keys (0 of a token whose data is bad: one empty tile)
 };
-__device__ __forceinline__ Token token_of(const DraftAttnArgs& a, int n, int tile_keys) {
+__device__ __forceinline__ int row_index(const DraftAttnArgs& a, int n) { return a.token_rows ? __ldg(a.token_rows + n) : n; }
+__device__ __forceinline__ Token token_at(const DraftAttnArgs& a, int pos, int row, int tile_keys) {
   Token t;
-  t.pos = __ldg(a.positions + n);
-  t.row = a.token_rows ? __ldg(a.token_rows + n) : n;
+  t.pos = pos;
+  t.row = row;
   const bool ok = t.pos >= 0 && t.row >= 0 && t.row < a.table_rows && a.page.quotient(t.pos) < a.table_stride;
   t.lo = ok && a.window > 0 ? max(0, t.pos - a.window + 1) : 0;
   t.first = min(a.n_sinks, t.lo);
   t.seen = ok ? (int64_t)t.first + t.pos - t.lo + 1 : 0;
   t.tiles = t.pos == -1 ? 0 : ok ? (int)((t.seen + tile_keys - 1) / tile_keys) : 1;
   return t;
+}
+__device__ __forceinline__ Token token_of(const DraftAttnArgs& a, int n, int tile_keys) {
+  return token_at(a, __ldg(a.positions + n), row_index(a, n), tile_keys);
 }
 
 // A tile as the copies and the arithmetic need it.
@@ -236,6 +240,16 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   int tile = (int)(start_at - (int64_t)first_bundle * tok.tiles);
   int kv_head = first_bundle * a.bundle + sub;
   bool begun = tile > 0;
+  // The token after the current one, loaded when the current one is entered:
+  // short contexts change tokens with every tile.
+  int next_pos = -1, next_row = 0;
+  auto fetch_next = [&] {
+    if (cur + 1 < a.n_tokens) {
+      next_pos = __ldg(a.positions + cur + 1);
+      next_row = row_index(a, cur + 1);
+    }
+  };
+  fetch_next();
   auto look_up = [&](int i) {
     const int slot = i % kRing;
     int page[kPerLane], in[kPerLane];
@@ -289,8 +303,11 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       kv_head += a.bundle;
       if (kv_head >= a.n_kv_heads) {
         kv_head = sub;
-        do tok = token_of(a, ++cur, C::kKeys);
-        while (tok.tiles == 0);
+        do {
+          ++cur;
+          tok = token_at(a, next_pos, next_row, C::kKeys);
+          fetch_next();
+        } while (tok.tiles == 0);
       }
     } else {
       ++tile;
@@ -411,14 +428,9 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     for (int block = 0; block < (idle ? 0 : C::kWarpKeys); block += C::kBlock) {
       const int key0 = wk * C::kWarpKeys + block;
       const uint32_t k_blk = k_at + block * C::kRowBytes, v_blk = v_at + block * C::kRowBytes;
-      // Short blocks sum even and odd column steps apart: twice the independent products.
-      constexpr int kSets = C::kBlock == 16 ? 2 : 1;
-      float part[kSets][C::kBlock / 8][4];
+      float s[C::kBlock / 8][4];
 #pragma unroll
-      for (int y = 0; y < kSets; ++y) {
-#pragma unroll
-        for (int x = 0; x < C::kBlock / 8; ++x) part[y][x][0] = part[y][x][1] = part[y][x][2] = part[y][x][3] = 0.f;
-      }
+      for (int x = 0; x < C::kBlock / 8; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < kDim / 16; ++ks) {
         uint32_t again[4];
@@ -428,16 +440,8 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
         for (int x = 0; x < C::kBlock / 16; ++x) {
           uint32_t b[4];
           ldsm4(k_blk + k_off[ks & 3] + (ks >> 2) * 128 + x * 16 * C::kRowBytes, b);
-          mma<kHalf>(part[ks % kSets][2 * x], af, b[0], b[1]);
-          mma<kHalf>(part[ks % kSets][2 * x + 1], af, b[2], b[3]);
-        }
-      }
-      float(&s)[C::kBlock / 8][4] = part[0];
-      if constexpr (kSets == 2) {
-#pragma unroll
-        for (int x = 0; x < C::kBlock / 8; ++x) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[x][e] += part[kSets - 1][x][e];
+          mma<kHalf>(s[2 * x], af, b[0], b[1]);
+          mma<kHalf>(s[2 * x + 1], af, b[2], b[3]);
         }
       }
       // Products as they are, keys that are not there at -inf; the scale (made
