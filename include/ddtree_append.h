@@ -67,7 +67,8 @@ DDTREE_API int ddtree_rope_init(int rot_dim, int interleaved, double theta, int 
  *   q_out[n, h]     = R(positions[n]) q_rope[n, h]
  * with norm(x) = x / sqrt(mean(x^2) + eps) * latent_weight (x itself when
  * latent_weight is NULL).
- *   n_tokens      0 .. DDTREE_APPEND_MAX_TOKENS;  n_heads 0 .. DDTREE_MAX_HEADS
+ *   n_tokens      0 .. DDTREE_APPEND_MAX_TOKENS (0: nothing happens, and the
+ *                 tokens' pointers may be NULL);  n_heads 0 .. DDTREE_MAX_HEADS
  *                 (0: rows only, q_rope and q_out may be NULL)
  *   rope          rot_dim must be 64
  *   kv_new        bf16, 576 columns, rows kv_stride elements apart
@@ -118,9 +119,9 @@ typedef struct ddtree_draft_cache {
  *   v cache [slots[n], h] = v[n, h]
  * norm over the head's head_dim columns as above, left out where the weight is
  * NULL; R turns the first rope->rot_dim columns.
- *   n_tokens      0 .. DDTREE_APPEND_MAX_TOKENS;  n_heads query heads, 0 ..
- *                 DDTREE_DRAFT_MAX_HEADS (0: keys and values only, q and q_out
- *                 may be NULL)
+ *   n_tokens      0 .. DDTREE_APPEND_MAX_TOKENS, as above;  n_heads query heads,
+ *                 0 .. DDTREE_DRAFT_MAX_HEADS (0: keys and values only, q and
+ *                 q_out may be NULL)
  *   rope          rot_dim <= head_dim, a multiple of 16
  *   q, k, v       cache->dtype; tokens *_stride elements apart, heads head_dim
  *                 apart (e.g. parts of one fused projection)

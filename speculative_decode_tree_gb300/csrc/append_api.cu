@@ -94,9 +94,14 @@ extern "C" int ddtree_mla_append(int64_t n_tokens, int n_heads, const ddtree_rop
                                  int64_t q_out_head_stride, uint32_t* status, struct CUstream_st* stream) {
   if (n_tokens < 0 || n_tokens > DDTREE_APPEND_MAX_TOKENS || n_heads < 0 || n_heads > DDTREE_MAX_HEADS) return DDTREE_EINVAL;
   if (!rope_ok(rope) || rope->rot_dim != kRope || !(eps >= 0.f) || !isfinite(eps)) return DDTREE_EINVAL;
-  if (!row_ok(kv_new) || !row_ok(kv_pool) || !aligned(latent_weight, 16) || !stride_ok(kv_stride, kRow)) return DDTREE_EINVAL;
-  if (!positions || !aligned(positions, 4) || !slots || !aligned(slots, 4) || !aligned(status, 4)) return DDTREE_EINVAL;
-  if (pool_rows < 1 || pool_rows > INT32_MAX) return DDTREE_EINVAL;
+  if (!row_ok(kv_pool) || pool_rows < 1 || pool_rows > INT32_MAX || !aligned(latent_weight, 16) || !aligned(status, 4))
+    return DDTREE_EINVAL;
+  if (n_tokens == 0) {  // nothing to read: the tokens' pointers are not looked at
+    DevInfo info;
+    return device_ok(&info);
+  }
+  if (!row_ok(kv_new) || !stride_ok(kv_stride, kRow)) return DDTREE_EINVAL;
+  if (!positions || !aligned(positions, 4) || !slots || !aligned(slots, 4)) return DDTREE_EINVAL;
   if (n_heads > 0) {
     if (!row_ok(q_rope) || !row_ok(q_out) || !stride_ok(q_token_stride, kRope) || !stride_ok(q_head_stride, kRope) ||
         !stride_ok(q_out_token_stride, kRope) || !stride_ok(q_out_head_stride, kRope))
@@ -145,11 +150,14 @@ extern "C" int ddtree_draft_append(int64_t n_tokens, int n_heads, const ddtree_d
   if (!draft_cache_ok(cache) || !rope_ok(rope) || rope->rot_dim > cache->head_dim || rope->rot_dim % 16 ||
       !(eps >= 0.f) || !isfinite(eps))
     return DDTREE_EINVAL;
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(status, 4)) return DDTREE_EINVAL;
+  if (n_tokens == 0) {  // nothing to read: the tokens' pointers are not looked at
+    DevInfo info;
+    return device_ok(&info);
+  }
   const int64_t kv_width = (int64_t)cache->n_kv_heads * cache->head_dim, q_width = (int64_t)n_heads * cache->head_dim;
-  if (!row_ok(k) || !row_ok(v) || !stride_ok(k_stride, kv_width) || !stride_ok(v_stride, kv_width) ||
-      !aligned(q_weight, 16) || !aligned(k_weight, 16))
-    return DDTREE_EINVAL;
-  if (!positions || !aligned(positions, 4) || !slots || !aligned(slots, 4) || !aligned(status, 4)) return DDTREE_EINVAL;
+  if (!row_ok(k) || !row_ok(v) || !stride_ok(k_stride, kv_width) || !stride_ok(v_stride, kv_width)) return DDTREE_EINVAL;
+  if (!positions || !aligned(positions, 4) || !slots || !aligned(slots, 4)) return DDTREE_EINVAL;
   if (n_heads > 0) {
     if (!row_ok(q) || !row_ok(q_out) || !stride_ok(q_stride, q_width) || !stride_ok(q_out_stride, q_width)) return DDTREE_EINVAL;
     if (q == q_out && q_stride != q_out_stride) return DDTREE_EINVAL;

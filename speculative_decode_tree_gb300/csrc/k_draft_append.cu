@@ -163,7 +163,6 @@ cudaError_t launch(const DraftAppendArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_draft_append(const DraftAppendArgs& a, int num_sms, cudaStream_t stream) {
-  if (a.n_tokens == 0) return cudaSuccess;
   if (a.dtype == DDTREE_FP16) {
     return a.head_dim == 64    ? launch<true, 64>(a, num_sms, stream)
            : a.head_dim == 128 ? launch<true, 128>(a, num_sms, stream)

@@ -218,6 +218,13 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   // The first `longer` ranges have one tile more than the others.
   const int64_t base = quotient(total, (uint32_t)ranges), longer = total - base * ranges;
   const int64_t begin = range * base + min((int64_t)range, longer), end = begin + base + (range < longer);
+  if (base >= INT32_MAX) {  // more tiles than a share counts (over 10^13 bytes): refused as a whole
+    if (tid == 0) {
+      if (!unit_records) records[share].token = -1;
+      words[share] = DDTREE_ST_BAD_LENGTH;
+    }
+    return;
+  }
   if (before <= begin && begin < before + mine) {
     int n = tid * per;
     int64_t at = begin - before;
@@ -615,7 +622,10 @@ __global__ void __launch_bounds__(2 * kDim) draft_join_kernel(const __grid_const
   }
   if (padding) return;
   const Record r = reinterpret_cast<const Record*>(a.ws + ws.records)[x];
-  if (r.token < 0) return;
+  // (Bounds hold for every record that was written; a refused call writes none.)
+  if (r.token < 0 || r.token >= a.n_tokens || r.kv_head < 0 || r.kv_head >= a.n_kv_heads || r.first_share < 0 ||
+      r.last_share < r.first_share || r.last_share >= a.n_shares)
+    return;
   const int first = r.first_share, parts = (r.last_share - first) / a.bundle + 1;
   const float2* sums = reinterpret_cast<const float2*>(a.ws + ws.sums);
   const float4* rows = reinterpret_cast<const float4*>(a.ws + ws.rows);

@@ -142,7 +142,6 @@ __global__ void __launch_bounds__(kThreads) mla_append_kernel(const __grid_const
 }  // namespace
 
 cudaError_t launch_mla_append(const MlaAppendArgs& a, int num_sms, cudaStream_t stream) {
-  if (a.n_tokens == 0) return cudaSuccess;
   // A token is one warp's work where tokens fill the SMs with 8 warps each;
   // fewer tokens are cut into slices, down to eight heads.
   const int steps = std::max(1, (a.n_heads + kHeadsPerStep - 1) / kHeadsPerStep);

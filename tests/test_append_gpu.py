@@ -131,11 +131,17 @@ def test_mla_padding_and_bad_slots():
 
 def test_mla_no_tokens_and_a_row_far_into_the_pool():
     rope = _rope(64, True, "plain")[0]
-    none = torch.empty(0, 576, dtype=torch.bfloat16, device="cuda")
+    bf = dict(dtype=torch.bfloat16, device="cuda")
     ints = torch.empty(0, dtype=I32, device="cuda")
-    pool = torch.ones(4, 576, dtype=torch.bfloat16, device="cuda")
-    B.ddtree_mla_append(rope, torch.empty(1, 576, dtype=torch.bfloat16, device="cuda")[:0], ints, ints, pool) if none.data_ptr() else None
-    assert bool((pool == 1).all())
+    pool = torch.ones(4, 576, **bf)
+    B.ddtree_mla_append(rope, torch.empty(0, 576, **bf), ints, ints, pool)
+    B.ddtree_mla_append(rope, torch.empty(0, 576, **bf), ints, ints, pool, q_rope=torch.empty(0, 8, 64, **bf),
+                        q_out=torch.empty(0, 8, 64, **bf), latent_weight=torch.ones(512, **bf))
+    cache = B.DraftCache(torch.ones(2, 4, 2, 64, **bf), torch.ones(2, 4, 2, 64, **bf))
+    empty = [torch.empty(0, h, 64, **bf) for h in (4, 2, 2, 4)]
+    B.ddtree_draft_append(cache, rope, *empty[:3], ints, ints, empty[3])
+    torch.cuda.synchronize()
+    assert bool((pool == 1).all()) and bool((cache.k == 1).all()) and bool((cache.v == 1).all())
     rows = 4_000_000  # byte offsets past 2^32
     pool = torch.zeros(rows, 576, dtype=torch.bfloat16, device="cuda")
     kv = torch.randn(2, 576, device="cuda").to(torch.bfloat16)

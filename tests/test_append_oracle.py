@@ -98,6 +98,17 @@ BAD_CACHES = [dict(k=None), dict(v=(1 << 12) + 8), dict(n_pages=0), dict(n_pages
               dict(n_kv_heads=129), dict(head_dim=96), dict(dtype=2)]
 
 
+def test_no_tokens_need_no_pointers(lib):
+    rope, cache = B.ddtree_rope_init(64, theta=1e4), _cache()
+    rc = lib.ddtree_mla_append(0, 8, ctypes.addressof(rope), None, 0, None, 0.0, None, 0, 0, None, None, P, 9, None, 0, 0, None, None)
+    assert rc in (B.DDTREE_OK, B.DDTREE_EUNSUPPORTED)  # without a device there is nothing to run on
+    rc = lib.ddtree_draft_append(0, 8, ctypes.addressof(cache), ctypes.addressof(rope), None, 0, None, 0, None, 0, None, None, 0.0,
+                                 None, None, None, 0, None, None)
+    assert rc in (B.DDTREE_OK, B.DDTREE_EUNSUPPORTED)
+    assert lib.ddtree_mla_append(0, 8, ctypes.addressof(rope), None, 0, None, 0.0, None, 0, 0, None, None, None, 9, None, 0, 0, None,
+                                 None) == B.DDTREE_EINVAL
+
+
 def test_draft_append_refusals(lib):
     rope = B.ddtree_rope_init(64, theta=1e4)
     big = B.ddtree_rope_init(128, theta=1e4)
