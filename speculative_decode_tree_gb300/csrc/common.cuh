@@ -309,7 +309,7 @@ struct DraftAttnArgs {
   int32_t n_tokens, n_heads, n_kv_heads, group, head_dim, dtype, page_size;
   int32_t window, n_sinks, table_rows, table_stride;
   int32_t row_tile, n_shares;
-  int32_t bundle;            // key heads that shares take side by side (divides them all)
+  int32_t bundle_log2;       // key heads that shares take side by side: 1, 2, 4 or 8, a divisor of them all
 };
 
 // Launches that may begin while the stream's last kernel is still running
@@ -317,10 +317,10 @@ struct DraftAttnArgs {
 // it touches memory, in every thread block, and lets the next such launch
 // begin with release_grid().  After any other kernel the wait is the usual one.
 template <typename... Params, typename... Args>
-inline cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+inline cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream,
                                 Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

