@@ -58,7 +58,8 @@ DDTREE_API int ddtree_draft_attention_plan(int n_tokens, int n_heads, const ddtr
 
 /* Workspace bytes for a plan (a multiple of 256; 256-byte aligned buffer): the
  * 256-byte status block (read with ddtree_verify_mla_check), then the shares'
- * partial results.  It keeps nothing between calls.  0 for a null plan. */
+ * partial results.  It keeps nothing between calls; calls that may overlap on
+ * the GPU need a workspace each.  0 for a null plan. */
 DDTREE_API size_t ddtree_draft_attention_workspace_size(const ddtree_draft_plan_t* plan);
 
 /*

@@ -143,6 +143,33 @@ def test_many_tokens():
     _check([r.randint(0, 20) for _ in range(4096)], 2, 1, 64, page=4, seed=4)
 
 
+@pytest.mark.parametrize("kvh,dim", [(3, 64), (5, 128), (6, 64), (12, 128), (16, 64), (24, 64), (10, 256), (128, 64)])
+def test_key_heads_that_shares_take_side_by_side(kvh, dim):
+    _check([700, 3, -1, 129, 2500], 2 * kvh, kvh, dim, seed=kvh)
+    _check([40] * 33, kvh, kvh, dim, page=8, seed=kvh + 1)
+
+
+def test_one_long_request_among_many_short_ones():
+    # More units than shares: the long request's units cross shares, the short ones' do not.
+    _check([9000] + [10, 60, 200, 127, 128] * 20, 8, 4, 64, seed=41)
+    _check([30] * 70 + [6000, 100], 48, 8, 128, seed=42)
+
+
+def test_strided_outputs_and_caches_of_one_tensor():
+    c = Case([300, 5, 77], 8, 2, 64, seed=43)
+    c.device()
+    both = torch.stack([c.k_dev, c.v_dev], 1)                   # [pages, 2, page, heads, dim]
+    cache = B.DraftCache(both[:, 0], both[:, 1])
+    wide = torch.full((3, 11, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    plan = B.ddtree_draft_attention_plan(3, 8, cache)
+    plan.out_stride = 11 * 64
+    B.ddtree_draft_attention(plan, c.q_dev, cache, *c.args[3:6], wide[:, 2:10], c.ws, **c.kw)
+    torch.cuda.synchronize()
+    c.out = wide[:, 2:10].contiguous()
+    c.compare()
+    assert bool((wide[:, :2] == 7.0).all()) and bool((wide[:, 10:] == 7.0).all())
+
+
 def test_padding_tokens_are_left_alone():
     _check([-1, 100, -1, -1, 7, -1], 8, 2, 128, seed=5)
     _check([-1, -1], 8, 2, 128, seed=6)
