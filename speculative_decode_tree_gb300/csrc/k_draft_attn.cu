@@ -33,10 +33,10 @@
 //    programmatic dependence, joins them in a fixed order.
 //
 // Measured, calls back to back in a graph, bf16 unless noted: eight requests of
-// 1k to 185k tokens, 8 key heads of 128 columns, 206 to 209 us (7.05 TB/s of
-// K and V, 1.04 of the measured copy rate); one of 185k with 2 heads of 256
-// columns 69.2 us (5.6 TB/s; some 8 us are start, join and launch); 61 fp16
-// requests of 511 to 16k, 8 heads of 64 columns, 93 us (6.2 TB/s); a
+// 1k to 185k tokens, 8 key heads of 128 columns, 205 to 209 us (7.1 TB/s of
+// K and V, 1.05 of the measured copy rate); one of 185k with 2 heads of 256
+// columns 66.9 us (5.8 TB/s; some 8 us are start, join and launch); 61 fp16
+// requests of 511 to 16k, 8 heads of 64 columns, 92 us (6.3 TB/s); a
 // window of 2,048 at 65k 7.8 us, a chain of dependent steps (positions, page
 // numbers, keys, product, join) with almost no bytes.  Groups above 16 rows are
 // bound by the matrix instruction and its operand loads instead: 64 rows of 128
