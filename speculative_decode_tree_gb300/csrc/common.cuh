@@ -216,7 +216,7 @@ struct MaskArgs {
 // Quotients of numbers below 2^31 by one divisor (1 .. 65536): a product with
 // ceil(2^(31+l) / d), 2^(l-1) < d <= 2^l, is exact for them.
 struct Divider {
-  uint32_t d, mul, shift;
+  uint32_t mul, shift;
 #ifdef __CUDACC__
   __device__ __forceinline__ int quotient(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> shift); }
 #endif
@@ -225,7 +225,7 @@ inline Divider make_divider(int d) {
   uint32_t l = 0;
   while ((1u << l) < (uint32_t)d) ++l;
   const uint64_t one = 1ull << (31 + l);
-  return Divider{(uint32_t)d, (uint32_t)((one + d - 1) / d), 31 + l};
+  return Divider{(uint32_t)((one + d - 1) / d), 31 + l};
 }
 
 // Everything the step maps need (see include/ddtree_maps.h).

@@ -4,8 +4,9 @@
 //   s_j = scale <q, k_j>,  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)
 //
 // The work is a stream of keys: 4 D bytes for 4 D flops per query head of the
-// group, so a group of up to 64 heads stays below the ridge and HBM is the
-// bound.  The kernel is built to keep loads in flight on every SM:
+// group, far below the ridge of some 280 flops a byte, so HBM is the bound (for
+// groups above 16 heads see the end).  The kernel is built to keep loads in
+// flight on every SM:
 //
 //  - Equal shares.  The visible keys of a (token, key head) unit are numbered
 //    without gaps (the sinks that lie before the window, then the window) and
@@ -39,8 +40,9 @@
 // requests of 511 to 16k, 8 heads of 64 columns, 92 us (6.3 TB/s); a
 // window of 2,048 at 65k 7.8 us, a chain of dependent steps (positions, page
 // numbers, keys, product, join) with almost no bytes.  Groups above 16 rows are
-// bound by the matrix instruction and its operand loads instead: 64 rows of 128
-// columns stream 4.0 TB/s.  Token-granular pages of 64 columns, 128 bytes at
+// bound by shared memory instead, since every tile of 16 rows loads the keys'
+// fragments for itself: 64 rows of 128 columns stream 4.0 TB/s (two row tiles a
+// warp halve those loads, but leave eight warps on an SM: 3.8 TB/s).  Token-granular pages of 64 columns, 128 bytes at
 // scattered places, stream 5.2 TB/s.
 #include <atomic>
 
