@@ -74,7 +74,9 @@ DDTREE_API size_t ddtree_draft_attention_workspace_size(const ddtree_draft_plan_
  * Device-data errors set status bits instead of faulting: a position below -1,
  * a row outside the table or a position past its pages: DDTREE_ST_BAD_LENGTH,
  * out 0 and lse -inf; a page outside [0, n_pages): DDTREE_ST_BAD_INDEX, its
- * keys are dropped (out 0 and lse -inf when none is left).
+ * keys are dropped (out 0 and lse -inf when none is left); a bounded wait
+ * inside the kernel that expired: DDTREE_ST_TIMEOUT, and the outputs are not
+ * valid.
  * Errors: DDTREE_EINVAL (also a plan that was made for another cache shape),
  * DDTREE_EWORKSPACE, DDTREE_EUNSUPPORTED, DDTREE_ELAUNCH.
  */

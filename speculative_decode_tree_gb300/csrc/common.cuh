@@ -337,6 +337,7 @@ __device__ __forceinline__ void release_grid() { asm volatile("griddepcontrol.la
 #endif
 
 // ---- launchers (one per .cu file) ----
+int draft_row_tile(int group, int head_dim);
 int draft_tile_keys(int head_dim);
 int draft_shares(int head_dim, int num_sms);
 int64_t draft_workspace_bytes(int row_tile, int head_dim, int n_shares);

@@ -11,10 +11,6 @@ namespace {
 
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// Query rows of a work item: the group of one key head, padded to 16 rows of
-// the matrix instruction per warp row.
-int row_tile_for(int group) { return group <= 16 ? 16 : group <= 32 ? 32 : 64; }
-
 bool sizes_ok(int n_tokens, int n_heads, int n_kv_heads, int head_dim, int dtype, int page_size, int window, int n_sinks) {
   return n_tokens >= 1 && n_tokens <= DDTREE_DRAFT_MAX_TOKENS && n_kv_heads >= 1 && n_kv_heads <= DDTREE_MAX_HEADS &&
          n_heads >= n_kv_heads && n_heads % n_kv_heads == 0 && n_heads / n_kv_heads <= DDTREE_DRAFT_MAX_GROUP &&
@@ -25,7 +21,7 @@ bool sizes_ok(int n_tokens, int n_heads, int n_kv_heads, int head_dim, int dtype
 bool plan_ok(const ddtree_draft_plan_t* p) {
   if (!p || !sizes_ok(p->n_tokens, p->n_heads, p->n_kv_heads, p->head_dim, p->dtype, p->page_size, p->window, p->n_sinks))
     return false;
-  if (p->row_tile != row_tile_for(p->n_heads / p->n_kv_heads) || p->tile_keys != draft_tile_keys(p->head_dim) ||
+  if (p->row_tile != draft_row_tile(p->n_heads / p->n_kv_heads, p->head_dim) || p->tile_keys != draft_tile_keys(p->head_dim) ||
       p->n_shares < 1 || p->n_shares > 65535)
     return false;
   if (p->workspace_bytes != draft_workspace_bytes(p->row_tile, p->head_dim, p->n_shares)) return false;
@@ -61,7 +57,7 @@ extern "C" int ddtree_draft_attention_plan(int n_tokens, int n_heads, const ddtr
   p.page_size = cache->page_size;
   p.window = window;
   p.n_sinks = n_sinks;
-  p.row_tile = row_tile_for(n_heads / cache->n_kv_heads);
+  p.row_tile = draft_row_tile(n_heads / cache->n_kv_heads, p.head_dim);
   p.tile_keys = draft_tile_keys(p.head_dim);
   p.n_shares = draft_shares(p.head_dim, num_sms);
   p.workspace_bytes = draft_workspace_bytes(p.row_tile, p.head_dim, p.n_shares);

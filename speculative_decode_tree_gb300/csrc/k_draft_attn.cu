@@ -4,9 +4,8 @@
 //   s_j = scale <q, k_j>,  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)
 //
 // The work is a stream of keys: 4 D bytes for 4 D flops per query head of the
-// group, far below the ridge of some 280 flops a byte, so HBM is the bound (for
-// groups above 16 heads see the end).  The kernel is built to keep loads in
-// flight on every SM:
+// group, far below the ridge of some 280 flops a byte, so HBM is the bound.  The
+// kernel is built to keep loads in flight on every SM:
 //
 //  - Equal shares.  The visible keys of a (token, key head) unit are numbered
 //    without gaps (the sinks that lie before the window, then the window) and
@@ -28,6 +27,7 @@
 //    maximum and sum in 32 bits; they join through the stage just consumed.
 //    This is mma.sync and not tcgen05: with 4 to 16 useful rows of a 128-row
 //    tile the tensor pipe is no bound, and the fragments stay in registers.
+//    Wide groups take tcgen05 (tensor_tiles, and the rule at Config).
 //  - A unit that lies within a share is finished there.  One that crosses into
 //    other shares leaves its maximum, sum and unnormalised rows per share (at
 //    most two per share), and a second small grid, launched ahead of time with
@@ -39,11 +39,9 @@
 // columns 66.9 us (5.8 TB/s; some 8 us are start, join and launch); 61 fp16
 // requests of 511 to 16k, 8 heads of 64 columns, 92 us (6.3 TB/s); a
 // window of 2,048 at 65k 7.8 us, a chain of dependent steps (positions, page
-// numbers, keys, product, join) with almost no bytes.  Groups above 16 rows are
-// bound by shared memory instead, since every tile of 16 rows loads the keys'
-// fragments for itself: 64 rows of 128 columns stream 4.0 TB/s (two row tiles a
-// warp halve those loads, but leave eight warps on an SM: 3.8 TB/s).  Token-granular pages of 64 columns, 128 bytes at
-// scattered places, stream 5.2 TB/s.
+// numbers, keys, product, join) with almost no bytes.  64 heads a group stream
+// 4.6, 5.5 and 4.2 TB/s at 64, 128 and 256 columns.  Token-granular pages of 64
+// columns, 128 bytes at scattered places, stream 5.2 TB/s.
 #include <atomic>
 
 #include "rope.cuh"
@@ -56,36 +54,41 @@ constexpr int kRing = 4;  // offset slots: the tile in use, those in flight, and
 
 template <int kDim, int kWM>
 struct Config {
+  // Up to 16 rows, 32 where the columns are 64 or 256, go through registers;
+  // 64 rows, and more than 16 of 128 columns, through the tensor memory
+  // (tensor_tiles): in registers every tile of 16 rows loads the keys' fragments
+  // for itself, which 64 rows of 128 columns pay with shared memory's whole
+  // bandwidth.  us per GB (256 columns: per 537 MB), registers and tensor memory:
+  // 64 rows of 64, 128, 256 columns 259, 269, 198 and 233, 194, 129; 24 rows 180,
+  // 204, 115 and 231, 191, 127.
+  static constexpr bool kTensor = kWM == 4;
+  static_assert(kWM != 2 || kDim != 128, "see draft_row_tile");
   static constexpr int kKeys = kDim == 64 ? 128 : 64;       // keys of a tile
   // Warps along the rows, the keys and the columns of V.  256 columns are
   // halved between two warps (both take the scores): a whole row's registers
   // would leave too few warps to hide each other's latency.
   static constexpr int kWN = kDim == 256 ? 2 : 1;
-  static constexpr int kWK = kDim == 256 || (kDim == 128 && kWM == 1) ? 4 / kWM : 8 / kWM;
-  static constexpr int kWarps = kWM * kWN * kWK;
+  static constexpr int kWK = kTensor ? 2 : kDim == 64 ? 8 / kWM : 4 / kWM;
+  static constexpr int kWarps = kTensor ? 8 : kWM * kWN * kWK;
   static constexpr int kThreads = 32 * kWarps;              // that compute
-  // One more warp looks the keys up (185k single 70.8 us instead of 84.8, batch
-  // of 61 110 instead of 119), unless its registers take the others' away: more
-  // than 16 rows of 128 columns need more than the 96 each that 18 warps on an
-  // SM get (64 rows 380 us per GB instead of 273), and there warp 0 does it.
-  static constexpr bool kLookupWarp = kDim != 128 || kWM == 1;
-  static constexpr int kAllThreads = kThreads + (kLookupWarp ? 32 : 0);
-  static constexpr int kWarpKeys = kKeys / kWK;
-  static constexpr int kBlock = kWarpKeys < 32 ? 16 : 32;    // keys of one softmax step
-  static constexpr int kCols = kDim / kWN;                  // columns of a warp
+  // One more warp looks the keys up (185k single 70.8 us instead of 84.8 when
+  // one of the others did, batch of 61 110 instead of 119).
+  static constexpr int kAllThreads = kThreads + 32;
   static constexpr int kRows = 16 * kWM;
   static constexpr int kRowBytes = kDim * 2;
   static constexpr int kTileBytes = kKeys * kRowBytes;      // of K, and of V
   static constexpr int kQBytes = kRows * kRowBytes;
   static constexpr int kCtas = kDim == 256 ? 1 : 2;         // per SM
   static constexpr int kStages = kWM == 1 ? 3 : 2;
-  // Query fragments in registers for the whole unit, or read again per tile.
-  static constexpr bool kHoldQ = kDim == 64 || (kDim == 128 && kWM == 1);
-  static constexpr int kSmem = kStages * (2 * kTileBytes + kQBytes);
+  // Shared memory: probabilities (kTensor), queries, tiles.  The tensor core
+  // reads 128 rows of an operand whose first 64 count: behind the last of the
+  // probabilities lie queries and behind those tiles, so it stays inside.
+  static constexpr int kPBytes = kTensor ? kRows * kKeys * 2 : 0;
+  static constexpr int kSmem = (kTensor ? 1024 : 0) + kPBytes + kStages * (2 * kTileBytes + kQBytes);
   // Columns joined at a time: the rows of all key parts fit the stage they replace.
   static constexpr int kRounds = kWK * kRows * kDim * 4 <= 2 * kTileBytes ? 1 : 2;
   static constexpr int kRoundCols = kDim / kRounds;
-  static_assert(kWK * kRows * kRoundCols * 4 <= 2 * kTileBytes, "merge buffer");
+  static_assert(kTensor || kWK * kRows * kRoundCols * 4 <= 2 * kTileBytes, "merge buffer");
   static_assert(kRing >= kStages + 1, "offset ring");
 };
 
@@ -171,6 +174,227 @@ struct Tile {
 };
 enum { kFirst = 1, kLast = 2, kBegun = 4, kGoesOn = 8 };
 
+// ---- 64 rows: scores and sums in tensor memory
+//
+// One thread issues the products: S = Q K^T (128 x tile keys, rows 64.. unused)
+// and O += P V (128 x columns).  Four warps take the softmax, a row and half of
+// the tile's keys per thread: two threads of a row exchange their maxima through
+// shared memory, keep one reference m that moves only when the maximum has
+// grown by more than 2^8 (the rows of O are then rescaled in place), and leave
+// P in shared memory in the cache's type.  All eight warps copy.  Within a CTA
+// the steps of a tile follow each other; the two CTAs of an SM fill each other's
+// gaps (256 columns: one CTA, twice the keys' bytes per step).
+// Waits are bounded (2 s): an expired one sets TIMEOUT and leaves its tile's
+// number, and behind the next tile's barrier all warps see it and stop.  (The
+// number and not a flag: a warp that is late behind a barrier must not stop for
+// what another has set since.)
+struct TensorShared {
+  uint64_t scores, values;  // barriers: S of a tile complete, O of a tile complete
+  uint32_t base;            // tensor memory
+  int32_t expired;          // tile in which a wait ran out, else INT32_MAX
+};
+constexpr int kAllocWarp = 3, kIssueWarp = 2;
+constexpr uint64_t kWaitNs = 2000000000ull;
+// Columns: S at 0, O behind; a power of two.
+__host__ __device__ constexpr int o_col(int dim) { return dim == 256 ? 256 : 128; }
+__host__ __device__ constexpr int tmem_cols(int dim) { return dim == 256 ? 512 : 256; }
+// Instruction descriptor: 32-bit sums, A and B both fp16 or both bf16, A K-major.
+__host__ __device__ constexpr uint32_t product_desc(int n, bool b_mn_major, bool half) {
+  return half ? ptx::idesc_bf16_f32(128, n, false, b_mn_major) & ~((1u << 7) | (1u << 10))
+              : ptx::idesc_bf16_f32(128, n, false, b_mn_major);
+}
+
+template <bool kHalf, int kDim, typename Copies>
+__device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layout& ws, TensorShared& sh, uint32_t p_at,
+                                             uint32_t q_ring, uint32_t ring, const Tile* tiles,
+                                             const uint32_t (*there)[Config<kDim, 4>::kKeys / 32], float (*top_s)[64],
+                                             float (*sum_s)[64], uint32_t* bits, int count, int share, Copies& start_copies) {
+  using namespace ptx;
+  using C = Config<kDim, 4>;
+  constexpr int kHalfKeys = C::kKeys / 2, kHalfCols = kDim / 2;
+  constexpr int kSlab = C::kKeys * 128, kRowSlab = 64 * 128;  // 64 columns of a tile, and of 64 rows
+  constexpr float kShift = kHalf ? 10.f : 0.f;
+  constexpr float kGrowth = kHalf ? 4.f : 8.f;  // fp16: 2^(10 + 4) is the largest probability
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // Warps 0, 1 and 4, 5 reach the lanes of rows 0..63.
+  const bool softmax = (warp & 3) < 2;
+  const int row = (warp & 1) * 32 + lane, half = warp >> 2;
+  const uint32_t my_lane = (uint32_t)((warp & 3) * 32) << 16;
+  const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);  // as for fewer rows
+  float m = -INFINITY, l = 0.f;
+  tc_fence_after();  // the base was written before the last barrier
+  const uint32_t s_mem = sh.base, o_mem = sh.base + o_col(kDim);
+  auto rows_barrier = [] { asm volatile("bar.sync 3, 128;" ::: "memory"); };
+  auto wait = [&](uint64_t* bar, uint32_t parity, int i) {
+    if (!mbar_wait(bar, parity, kWaitNs)) {
+      *(volatile int32_t*)&sh.expired = i;
+      atomicOr(bits, DDTREE_ST_TIMEOUT);
+    }
+  };
+
+  for (int i = 0; i < count; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+    fence_async_smem();  // this thread's copies, before the tensor core reads them
+    tc_fence_before();
+    __syncthreads();
+    if (*(volatile int32_t*)&sh.expired < i) break;
+    const int slot = i % kRing;
+    const Tile t = tiles[slot];
+    const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes, v_at = k_at + C::kTileBytes;
+    if (warp == kIssueWarp && lane == 0) {
+      tc_fence_after();
+      const uint32_t q_at = q_ring + (t.unit % C::kStages) * C::kQBytes;
+#pragma unroll
+      for (int c = 0; c < kDim / 64; ++c)
+        mma_ss_x4<2, 2>(s_mem, desc_sw128(q_at + c * kRowSlab, 16, 1024), desc_sw128(k_at + c * kSlab, 16, 1024),
+                        product_desc(C::kKeys, false, kHalf), c > 0);
+      mma_commit(&sh.scores);
+    }
+    // The last tile's stage and probabilities are free once its O is complete.
+    if (i > 0) wait(&sh.values, (i - 1) & 1, i);
+    start_copies(i + C::kStages - 1);
+    if (softmax) {
+      wait(&sh.scores, i & 1, i);
+      __syncwarp();
+      tc_fence_after();
+      uint32_t x[kHalfKeys / 32][32];
+#pragma unroll
+      for (int q = 0; q < kHalfKeys / 32; ++q) tmem_ld32(s_mem + my_lane + half * kHalfKeys + 32 * q, x[q]);
+      if (a.scale_log2 < 0.f) {
+#pragma unroll
+        for (int k = 0; k < kHalfKeys; ++k) x[k >> 5][k & 31] ^= 0x80000000u;
+      }
+#pragma unroll
+      for (int q = 0; q < kHalfKeys / 32; ++q) {
+        const uint32_t mask = there[slot][half * (kHalfKeys / 32) + q];
+        if (mask != 0xffffffffu) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!((mask >> k) & 1)) x[q][k] = 0xff800000u;  // -inf
+        }
+      }
+      float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < kHalfKeys; ++k) high[k & 3] = fmaxf(high[k & 3], __uint_as_float(x[k >> 5][k & 31]));
+      const float mine = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
+      top_s[half][row] = mine;
+      rows_barrier();
+      const float top = fmaxf(mine, top_s[half ^ 1][row]);
+      if (t.flags & kFirst) {
+        m = -INFINITY;
+        l = 0.f;
+      }
+      float keep = 1.f;
+      if ((top - m) * scale > kGrowth) {  // also the first finite maximum
+        keep = m == -INFINITY ? 0.f : power2((m - top) * scale);
+        m = top;
+      }
+      l *= keep;
+      // The rows of O so far, whose last product is complete (the wait above).
+      if (!(t.flags & kFirst) && __any_sync(0xffffffffu, keep != 1.f)) {
+        __syncwarp();
+        tc_fence_after();
+        uint32_t v[16];
+#pragma unroll 1
+        for (int c = 0; c < kHalfCols; c += 16) {
+          tmem_ld16(o_mem + my_lane + half * kHalfCols + c, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * keep);
+          tmem_st16(o_mem + my_lane + half * kHalfCols + c, v);
+        }
+        tmem_st_wait();
+      }
+      const float base = m == -INFINITY ? 0.f : kShift - m * scale;
+      const uint32_t p_row = p_at + row * 128;
+      float sums[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < kHalfKeys / 8; ++c) {  // 16-byte chunks of eight keys
+        uint32_t packed[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = 8 * c + 2 * e;
+          const float u = power2(fmaf(__uint_as_float(x[k >> 5][k & 31]), scale, base));
+          const float w = power2(fmaf(__uint_as_float(x[k >> 5][(k & 31) + 1]), scale, base));
+          sums[e] += u + w;
+          packed[e] = pack2<kHalf>(u, w);
+        }
+        const int chunk = half * (kHalfKeys / 8) + c;  // of the tile: slab chunk / 8
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + (chunk >> 3) * kRowSlab +
+                                                                       (((chunk & 7) ^ (row & 7)) << 4)),
+                     "r"(packed[0]), "r"(packed[1]), "r"(packed[2]), "r"(packed[3])
+                     : "memory");
+      }
+      l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+      fence_async_smem();
+      tc_fence_before();
+    }
+    // P is written and O rescaled; and every warp has seen the last O complete,
+    // so the barrier of the values never runs two phases ahead of a waiter.
+    asm volatile("bar.sync 2, %0;" ::"n"(C::kThreads) : "memory");
+    if (warp == kIssueWarp && lane == 0) {
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < C::kKeys / 64; ++c)
+        mma_ss_x4<2, 128>(o_mem, desc_sw128(p_at + c * kRowSlab, 16, 1024), desc_sw128(v_at + c * 64 * 128, kSlab, 1024),
+                          product_desc(kDim, true, kHalf), c > 0 || !(t.flags & kFirst));
+      mma_commit(&sh.values);
+    }
+    if (!(t.flags & kLast) || !softmax) continue;
+
+    // ---- the unit ends here: a thread has half of a row's columns
+    sum_s[half][row] = l;
+    rows_barrier();
+    const float total = l + sum_s[half ^ 1][row];
+    wait(&sh.values, i & 1, i);
+    __syncwarp();
+    tc_fence_after();
+    const bool whole = !(t.flags & (kBegun | kGoesOn));
+    const int64_t part = 2 * share + (t.flags & kBegun ? 0 : 1);
+    const int head = t.kv_head * a.group + row;
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    uint16_t* out = a.out + t.token * a.out_stride + (int64_t)head * kDim + half * kHalfCols;
+    float4* rows = reinterpret_cast<float4*>(a.ws + ws.rows) + (part * C::kRows + row) * (kDim / 4) + half * (kHalfCols / 4);
+#pragma unroll 1
+    for (int c = 0; c < kHalfCols; c += 16) {
+      uint32_t v[16];
+      tmem_ld16(o_mem + my_lane + half * kHalfCols + c, v);  // the whole warp; the rows that count are stored
+      if (row < a.group) {
+        float f[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(v[e]);
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            *reinterpret_cast<uint4*>(out + c + e) =
+                make_uint4(pack2<kHalf>(f[e] * inv, f[e + 1] * inv), pack2<kHalf>(f[e + 2] * inv, f[e + 3] * inv),
+                           pack2<kHalf>(f[e + 4] * inv, f[e + 5] * inv), pack2<kHalf>(f[e + 6] * inv, f[e + 7] * inv));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) rows[(c + e) / 4] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        }
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    if (row < a.group && half == 0) {
+      const float top = m == -INFINITY ? m : m * scale;
+      if (!whole) reinterpret_cast<float2*>(a.ws + ws.sums)[part * C::kRows + row] = make_float2(top, total);
+      else if (a.lse)
+        a.lse[(int64_t)t.token * a.n_heads + head] = total == 0.f ? -INFINITY : (top - kShift + log2f(total)) * 0.6931471805599453f;
+    }
+  }
+  // Nothing of the tensor core's is in flight after a complete list (its last
+  // tile ends a unit); after an expired wait, give what is a last chance.
+  if (warp == kIssueWarp && lane == 0) {
+    __shared__ uint64_t drained;
+    mbar_init(&drained, 1);
+    fence_mbar_init();
+    mma_commit(&drained);
+    mbar_wait(&drained, 0, kWaitNs);
+  }
+  tc_fence_before();
+}
+
 template <bool kHalf, int kDim, int kWM>
 __global__ void __launch_bounds__(Config<kDim, kWM>::kAllThreads, Config<kDim, kWM>::kCtas)
 draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
@@ -186,6 +410,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   __shared__ int start_token;
   __shared__ int64_t start_at;
   __shared__ uint32_t bits;
+  __shared__ TensorShared tensor;  // of the tensor form only
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int share = blockIdx.x, range = share >> a.bundle_log2, sub = share - (range << a.bundle_log2);
@@ -210,7 +435,10 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     if (lane >= d) inc += o;
   }
   if (lane == 31) warp_sum[warp] = inc;
-  if (tid == 0) bits = 0;
+  if (tid == 0) {
+    bits = 0;
+    tensor.expired = INT32_MAX;
+  }
   __syncthreads();
   int64_t before = inc - mine, total = 0;
 #pragma unroll
@@ -332,13 +560,23 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       ++tile;
     }
   };
-  if (warp == (C::kLookupWarp ? kWarps : 0)) {
-    for (int i = 0; i < C::kStages && i < count; ++i) look_up(i);
+  if constexpr (C::kTensor) {
+    if (tid == 0) {
+      ptx::mbar_init(&tensor.scores, 1);
+      ptx::mbar_init(&tensor.values, 1);
+      ptx::fence_mbar_init();
+    }
+    if (warp == kAllocWarp) {
+      ptx::tmem_alloc(&tensor.base, tmem_cols(kDim));
+      ptx::tmem_relinquish();
+    }
   }
-  if (C::kLookupWarp && warp == kWarps) {
+  if (warp == kWarps) {
+    for (int i = 0; i < C::kStages && i < count; ++i) look_up(i);
     __syncthreads();
     for (int i = 0; i < count; ++i) {
       __syncthreads();  // tile i's slot is in use, the one of tile i + kStages free
+      if (C::kTensor && *(volatile int32_t*)&tensor.expired < i) break;
       if (i + C::kStages < count) look_up(i + C::kStages);
     }
     __syncthreads();
@@ -346,16 +584,23 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     return;
   }
 
-  const uint32_t ring = ptx::smem_u32(smem);
-  const uint32_t q_ring = ring + C::kStages * 2 * C::kTileBytes;
-  auto swizzled = [](int row, int chunk) { return (uint32_t)(row * C::kRowBytes + ((chunk ^ (row & 7)) << 4)); };
+  // Operands of the tensor core are 64-column slabs of 128-byte rows, swizzled
+  // from a 1024-byte border; for ldmatrix a row lies whole.
+  const uint32_t p_at = C::kTensor ? (ptx::smem_u32(smem) + 1023) & ~1023u : ptx::smem_u32(smem);
+  const uint32_t q_ring = C::kTensor ? p_at + C::kPBytes : p_at + C::kStages * 2 * C::kTileBytes;
+  const uint32_t ring = C::kTensor ? q_ring + C::kStages * C::kQBytes : p_at;
+  constexpr int kPitch = C::kTensor ? 128 : C::kRowBytes;
+  auto swizzled = [](int row, int chunk, int rows) {
+    if constexpr (C::kTensor) return (uint32_t)((chunk >> 3) * rows * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+    else return (uint32_t)(row * C::kRowBytes + ((chunk ^ (row & 7)) << 4));
+  };
   // Starts the copies of tile i (every thread commits a group, empty or not).
   // A thread copies one chunk of every kRowsPerStep-th row: the swizzle of its
   // rows is the same, so shared addresses advance by a constant.
   constexpr int kRowsPerStep = kThreads / kChunks;
   static_assert(C::kKeys % kRowsPerStep == 0 && kRowsPerStep % 8 == 0, "copy steps");
   const int copy_chunk = tid % kChunks, copy_row = tid / kChunks;
-  const uint32_t copy_at = swizzled(copy_row, copy_chunk);
+  const uint32_t copy_at = swizzled(copy_row, copy_chunk, C::kKeys);
   const uint16_t *copy_k = a.k + 8 * copy_chunk, *copy_v = a.v + 8 * copy_chunk;
   auto start_copies = [&](int i) {
     if (i < count) {
@@ -368,8 +613,8 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
 #pragma unroll
         for (int r = 0; r < C::kKeys; r += kRowsPerStep) {
           const int64_t off = offsets[slot][copy_row + r];
-          ptx::cp_async16(k_at + r * C::kRowBytes, copy_k + off);
-          ptx::cp_async16(v_at + r * C::kRowBytes, copy_v + off);
+          ptx::cp_async16(k_at + r * kPitch, copy_k + off);
+          ptx::cp_async16(v_at + r * kPitch, copy_v + off);
         }
       } else {
 #pragma unroll 2
@@ -377,8 +622,8 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
           const int64_t off = offsets[slot][copy_row + r];
           const int key = copy_row + r;
           const uint32_t size = (there[slot][key >> 5] >> (key & 31)) & 1 ? 16u : 0u;
-          ptx::cp_async16_zfill(k_at + r * C::kRowBytes, copy_k + off, size);
-          ptx::cp_async16_zfill(v_at + r * C::kRowBytes, copy_v + off, size);
+          ptx::cp_async16_zfill(k_at + r * kPitch, copy_k + off, size);
+          ptx::cp_async16_zfill(v_at + r * kPitch, copy_v + off, size);
         }
       }
       const Tile t = tiles[slot];
@@ -387,7 +632,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
         const uint16_t* q = a.q + t.token * a.q_stride + (int64_t)t.kv_head * a.group * kDim;
 #pragma unroll
         for (int r = copy_row; r < C::kRows; r += kRowsPerStep)
-          ptx::cp_async16_zfill(q_at + swizzled(r, copy_chunk), r < a.group ? q + r * kDim + 8 * copy_chunk : a.q,
+          ptx::cp_async16_zfill(q_at + swizzled(r, copy_chunk, C::kRows), r < a.group ? q + r * kDim + 8 * copy_chunk : a.q,
                                 r < a.group ? 16u : 0u);
       }
     }
@@ -398,222 +643,232 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
 #pragma unroll 1
   for (int i = 0; i < C::kStages - 1; ++i) start_copies(i);
 
-  auto computing_warps = [] { asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads) : "memory"); };
+  if constexpr (C::kTensor) {
+    tensor_tiles<kHalf, kDim>(a, ws, tensor, p_at, q_ring, ring, tiles, there, top_s, sum_s, &bits, count, share, start_copies);
+  } else {
+    auto computing_warps = [] { asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads) : "memory"); };
 
-  // ---- this warp's rows (16 of the group) and keys of every tile
-  const int wm = warp % kWM, wn = warp / kWM % C::kWN, wk = warp / (kWM * C::kWN);
-  constexpr bool kHoldQ = C::kHoldQ;
-  const bool idle = wm * 16 >= a.group;  // rows of the tile that no head fills
-  uint32_t qf[kHoldQ ? kDim / 16 : 1][4];
-  float o[C::kCols / 8][4], top[2], sum[2];
-  // Probabilities meet V in the cache's type.  fp16 holds nothing below 2^-24,
-  // so there they carry a factor of 2^10: a key counts down to 2^-34 of the
-  // largest, and the factor leaves with the division by the sum.
-  constexpr float kShift = kHalf ? 10.f : 0.f;
-  // A negative scale turns the products' signs instead; zero becomes a factor
-  // that no product survives, so that absent keys stay at -inf.
-  const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
+    // ---- this warp's rows (16 of the group) and keys of every tile
+    const int wm = warp % kWM, wn = warp / kWM % C::kWN, wk = warp / (kWM * C::kWN);
+    constexpr int kWarpKeys = C::kKeys / C::kWK;
+    constexpr int kBlock = kWarpKeys < 32 ? 16 : 32;  // keys of one softmax step
+    constexpr int kCols = kDim / C::kWN;              // columns of a warp
+    // Query fragments in registers for the whole unit, or read again per tile.
+    constexpr bool kHoldQ = kDim <= 128;
+    const bool idle = wm * 16 >= a.group;  // rows of the tile that no head fills
+    uint32_t qf[kHoldQ ? kDim / 16 : 1][4];
+    float o[kCols / 8][4], top[2], sum[2];
+    // Probabilities meet V in the cache's type.  fp16 holds nothing below 2^-24,
+    // so there they carry a factor of 2^10: a key counts down to 2^-34 of the
+    // largest, and the factor leaves with the division by the sum.
+    constexpr float kShift = kHalf ? 10.f : 0.f;
+    // A negative scale turns the products' signs instead; zero becomes a factor
+    // that no product survives, so that absent keys stay at -inf.
+    const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
 
-  // Fragment addresses.  A row's chunks are exchanged by its low three bits,
-  // which are the lane's in every matrix it addresses, so four offsets serve
-  // all columns and the rest is constant.
-  uint32_t k_off[4], v_off[4], q_off[4];
+    // Fragment addresses.  A row's chunks are exchanged by its low three bits,
+    // which are the lane's in every matrix it addresses, so four offsets serve
+    // all columns and the rest is constant.
+    uint32_t k_off[4], v_off[4], q_off[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    k_off[j] = swizzled(wk * C::kWarpKeys + (lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1));
-    v_off[j] = swizzled(wk * C::kWarpKeys + (lane & 15), 2 * j + (lane >> 4)) + wn * C::kCols * 2;
-    q_off[j] = swizzled(wm * 16 + (lane & 15), 2 * j + (lane >> 4));
-  }
-
-  for (int i = 0; i < count; ++i) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-    __syncthreads();
-    start_copies(i + C::kStages - 1);
-    const int slot = i % kRing;
-    const Tile t = tiles[slot];
-    const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes, v_at = k_at + C::kTileBytes;
-    const uint32_t q_at = q_ring + (t.unit % C::kStages) * C::kQBytes;
-    if (t.flags & kFirst) {
-      if constexpr (kHoldQ) {
-#pragma unroll
-        for (int ks = 0; ks < kDim / 16; ++ks) ldsm4(q_at + q_off[ks & 3] + (ks >> 2) * 128, qf[ks]);
-      }
-#pragma unroll
-      for (int d = 0; d < C::kCols / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
-      top[0] = top[1] = -INFINITY;
-      sum[0] = sum[1] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+      k_off[j] = swizzled(wk * kWarpKeys + (lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1), C::kKeys);
+      v_off[j] = swizzled(wk * kWarpKeys + (lane & 15), 2 * j + (lane >> 4), C::kKeys) + wn * kCols * 2;
+      q_off[j] = swizzled(wm * 16 + (lane & 15), 2 * j + (lane >> 4), C::kRows);
     }
+
+    for (int i = 0; i < count; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+      __syncthreads();
+      start_copies(i + C::kStages - 1);
+      const int slot = i % kRing;
+      const Tile t = tiles[slot];
+      const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes, v_at = k_at + C::kTileBytes;
+      const uint32_t q_at = q_ring + (t.unit % C::kStages) * C::kQBytes;
+      if (t.flags & kFirst) {
+        if constexpr (kHoldQ) {
+#pragma unroll
+          for (int ks = 0; ks < kDim / 16; ++ks) ldsm4(q_at + q_off[ks & 3] + (ks >> 2) * 128, qf[ks]);
+        }
+#pragma unroll
+        for (int d = 0; d < kCols / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+        top[0] = top[1] = -INFINITY;
+        sum[0] = sum[1] = 0.f;
+      }
 #pragma unroll 1
-    for (int block = 0; block < (idle ? 0 : C::kWarpKeys); block += C::kBlock) {
-      const int key0 = wk * C::kWarpKeys + block;
-      const uint32_t k_blk = k_at + block * C::kRowBytes, v_blk = v_at + block * C::kRowBytes;
-      float s[C::kBlock / 8][4];
+      for (int block = 0; block < (idle ? 0 : kWarpKeys); block += kBlock) {
+        const int key0 = wk * kWarpKeys + block;
+        const uint32_t k_blk = k_at + block * C::kRowBytes, v_blk = v_at + block * C::kRowBytes;
+        float s[kBlock / 8][4];
 #pragma unroll
-      for (int x = 0; x < C::kBlock / 8; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+        for (int x = 0; x < kBlock / 8; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < kDim / 16; ++ks) {
-        uint32_t again[4];
-        if constexpr (!kHoldQ) ldsm4(q_at + q_off[ks & 3] + (ks >> 2) * 128, again);
-        const uint32_t(&af)[4] = kHoldQ ? qf[kHoldQ ? ks : 0] : again;
+        for (int ks = 0; ks < kDim / 16; ++ks) {
+          uint32_t again[4];
+          if constexpr (!kHoldQ) ldsm4(q_at + q_off[ks & 3] + (ks >> 2) * 128, again);
+          const uint32_t(&af)[4] = kHoldQ ? qf[kHoldQ ? ks : 0] : again;
 #pragma unroll
-        for (int x = 0; x < C::kBlock / 16; ++x) {
-          uint32_t b[4];
-          ldsm4(k_blk + k_off[ks & 3] + (ks >> 2) * 128 + x * 16 * C::kRowBytes, b);
-          mma<kHalf>(s[2 * x], af, b[0], b[1]);
-          mma<kHalf>(s[2 * x + 1], af, b[2], b[3]);
+          for (int x = 0; x < kBlock / 16; ++x) {
+            uint32_t b[4];
+            ldsm4(k_blk + k_off[ks & 3] + (ks >> 2) * 128 + x * 16 * C::kRowBytes, b);
+            mma<kHalf>(s[2 * x], af, b[0], b[1]);
+            mma<kHalf>(s[2 * x + 1], af, b[2], b[3]);
+          }
         }
-      }
-      // Products as they are, keys that are not there at -inf; the scale (made
-      // positive, see below) enters with the maximum in one multiply-add.
-      const uint32_t mask = there[slot][key0 >> 5] >> (key0 & 31);
-      constexpr uint32_t kAll = C::kBlock == 32 ? 0xffffffffu : (1u << (C::kBlock & 31)) - 1;
-      float high[2] = {top[0], top[1]};
-      if (a.scale_log2 < 0.f) {
+        // Products as they are, keys that are not there at -inf; the scale (made
+        // positive, see below) enters with the maximum in one multiply-add.
+        const uint32_t mask = there[slot][key0 >> 5] >> (key0 & 31);
+        constexpr uint32_t kAll = kBlock == 32 ? 0xffffffffu : (1u << (kBlock & 31)) - 1;
+        float high[2] = {top[0], top[1]};
+        if (a.scale_log2 < 0.f) {
 #pragma unroll
-        for (int x = 0; x < C::kBlock / 8; ++x) {
+          for (int x = 0; x < kBlock / 8; ++x) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[x][e] = -s[x][e];
+            for (int e = 0; e < 4; ++e) s[x][e] = -s[x][e];
+          }
         }
-      }
-      if ((mask & kAll) != kAll) {
+        if ((mask & kAll) != kAll) {
 #pragma unroll
-        for (int x = 0; x < C::kBlock / 8; ++x) {
-          const uint32_t two = mask >> (8 * x + 2 * (lane & 3));
-          if (!(two & 1)) s[x][0] = s[x][2] = -INFINITY;
-          if (!(two & 2)) s[x][1] = s[x][3] = -INFINITY;
+          for (int x = 0; x < kBlock / 8; ++x) {
+            const uint32_t two = mask >> (8 * x + 2 * (lane & 3));
+            if (!(two & 1)) s[x][0] = s[x][2] = -INFINITY;
+            if (!(two & 2)) s[x][1] = s[x][3] = -INFINITY;
+          }
         }
-      }
 #pragma unroll
-      for (int x = 0; x < C::kBlock / 8; ++x) {
-        high[0] = fmaxf(high[0], fmaxf(s[x][0], s[x][1]));
-        high[1] = fmaxf(high[1], fmaxf(s[x][2], s[x][3]));
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        high[r] = fmaxf(high[r], __shfl_xor_sync(0xffffffffu, high[r], 1));
-        high[r] = fmaxf(high[r], __shfl_xor_sync(0xffffffffu, high[r], 2));
-      }
-      if (__any_sync(0xffffffffu, high[0] > top[0] || high[1] > top[1])) {
+        for (int x = 0; x < kBlock / 8; ++x) {
+          high[0] = fmaxf(high[0], fmaxf(s[x][0], s[x][1]));
+          high[1] = fmaxf(high[1], fmaxf(s[x][2], s[x][3]));
+        }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float keep = top[r] == -INFINITY ? 0.f : power2((top[r] - high[r]) * scale);
-          sum[r] *= keep;
-          top[r] = high[r];
+          high[r] = fmaxf(high[r], __shfl_xor_sync(0xffffffffu, high[r], 1));
+          high[r] = fmaxf(high[r], __shfl_xor_sync(0xffffffffu, high[r], 2));
+        }
+        if (__any_sync(0xffffffffu, high[0] > top[0] || high[1] > top[1])) {
 #pragma unroll
-          for (int d = 0; d < C::kCols / 8; ++d) {
-            o[d][2 * r] *= keep;
-            o[d][2 * r + 1] *= keep;
+          for (int r = 0; r < 2; ++r) {
+            const float keep = top[r] == -INFINITY ? 0.f : power2((top[r] - high[r]) * scale);
+            sum[r] *= keep;
+            top[r] = high[r];
+#pragma unroll
+            for (int d = 0; d < kCols / 8; ++d) {
+              o[d][2 * r] *= keep;
+              o[d][2 * r + 1] *= keep;
+            }
+          }
+        }
+        const float base[2] = {top[0] == -INFINITY ? 0.f : kShift - top[0] * scale, top[1] == -INFINITY ? 0.f : kShift - top[1] * scale};
+#pragma unroll
+        for (int x = 0; x < kBlock / 8; ++x) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[x][e] = power2(fmaf(s[x][e], scale, base[e >> 1]));
+          sum[0] += s[x][0] + s[x][1];
+          sum[1] += s[x][2] + s[x][3];
+        }
+#pragma unroll
+        for (int x = 0; x < kBlock / 16; ++x) {
+          const uint32_t p[4] = {pack2<kHalf>(s[2 * x][0], s[2 * x][1]), pack2<kHalf>(s[2 * x][2], s[2 * x][3]),
+                                 pack2<kHalf>(s[2 * x + 1][0], s[2 * x + 1][1]), pack2<kHalf>(s[2 * x + 1][2], s[2 * x + 1][3])};
+#pragma unroll
+          for (int d = 0; d < kCols / 16; ++d) {
+            uint32_t b[4];
+            ldsm4_trans(v_blk + v_off[d & 3] + (d >> 2) * 128 + x * 16 * C::kRowBytes, b);
+            mma<kHalf>(o[2 * d], p, b[0], b[1]);
+            mma<kHalf>(o[2 * d + 1], p, b[2], b[3]);
           }
         }
       }
-      const float base[2] = {top[0] == -INFINITY ? 0.f : kShift - top[0] * scale, top[1] == -INFINITY ? 0.f : kShift - top[1] * scale};
-#pragma unroll
-      for (int x = 0; x < C::kBlock / 8; ++x) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] = power2(fmaf(s[x][e], scale, base[e >> 1]));
-        sum[0] += s[x][0] + s[x][1];
-        sum[1] += s[x][2] + s[x][3];
-      }
-#pragma unroll
-      for (int x = 0; x < C::kBlock / 16; ++x) {
-        const uint32_t p[4] = {pack2<kHalf>(s[2 * x][0], s[2 * x][1]), pack2<kHalf>(s[2 * x][2], s[2 * x][3]),
-                               pack2<kHalf>(s[2 * x + 1][0], s[2 * x + 1][1]), pack2<kHalf>(s[2 * x + 1][2], s[2 * x + 1][3])};
-#pragma unroll
-        for (int d = 0; d < C::kCols / 16; ++d) {
-          uint32_t b[4];
-          ldsm4_trans(v_blk + v_off[d & 3] + (d >> 2) * 128 + x * 16 * C::kRowBytes, b);
-          mma<kHalf>(o[2 * d], p, b[0], b[1]);
-          mma<kHalf>(o[2 * d + 1], p, b[2], b[3]);
-        }
-      }
-    }
-    if (!C::kLookupWarp && warp == 0 && i + C::kStages < count) look_up(i + C::kStages);
-    if (!(t.flags & kLast)) continue;
+      if (!(t.flags & kLast)) continue;
 
-    // ---- the unit ends here: join the warps' rows through this tile's stage
-    computing_warps();  // every warp is done with the tile
-    float* rows = reinterpret_cast<float*>(smem + (i % C::kStages) * 2 * C::kTileBytes);
-    // Row r of key part w; the exchange of column groups keeps the four rows that lanes write at once on other banks.
-    auto cell = [&](int w, int r, int col) { return rows + (w * C::kRows + r) * C::kRoundCols + (col ^ ((r & 3) << 3)); };
-    const int g = lane >> 2;
-    const bool whole = !(t.flags & (kBegun | kGoesOn));
-    const int64_t part = 2 * share + (t.flags & kBegun ? 0 : 1);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-      const int row = wm * 16 + g + 8 * r;
-      if ((lane & 3) == 0 && wn == 0) {
-        top_s[wk][row] = top[r] == -INFINITY ? top[r] : top[r] * scale;  // from here on in base 2
-        sum_s[wk][row] = sum[r];
-      }
-    }
-#pragma unroll
-    for (int round = 0; round < C::kRounds; ++round) {
-      const int col0 = round * C::kRoundCols;
-      if (round > 0) computing_warps();
+      // ---- the unit ends here: join the warps' rows through this tile's stage
+      computing_warps();  // every warp is done with the tile
+      float* rows = reinterpret_cast<float*>(smem + (i % C::kStages) * 2 * C::kTileBytes);
+      // Row r of key part w; the exchange of column groups keeps the four rows that lanes write at once on other banks.
+      auto cell = [&](int w, int r, int col) { return rows + (w * C::kRows + r) * C::kRoundCols + (col ^ ((r & 3) << 3)); };
+      const int g = lane >> 2;
+      const bool whole = !(t.flags & (kBegun | kGoesOn));
+      const int64_t part = 2 * share + (t.flags & kBegun ? 0 : 1);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
         const int row = wm * 16 + g + 8 * r;
-        if (row >= a.group) continue;
-#pragma unroll
-        for (int d = 0; d < C::kCols / 8; ++d) {
-          const int col = wn * C::kCols + 8 * d - col0;
-          if (C::kRounds == 1 || (col >= 0 && col < C::kRoundCols))
-            *reinterpret_cast<float2*>(cell(wk, row, col + 2 * (lane & 3))) = make_float2(o[d][2 * r], o[d][2 * r + 1]);
+        if ((lane & 3) == 0 && wn == 0) {
+          top_s[wk][row] = top[r] == -INFINITY ? top[r] : top[r] * scale;  // from here on in base 2
+          sum_s[wk][row] = sum[r];
         }
       }
-      computing_warps();
-      // Columns of a thread: few where many threads share a small group's rows
-      // (185k single 69.3 -> 67.1 us with four of 256; with 128 threads four
-      // spill where eight do not: 1024 requests of 100 keys 109 us instead of 92).
-      constexpr int kVec = kThreads == 128 ? 8 : 4;
-      for (int e = tid; e < a.group * (C::kRoundCols / kVec); e += kThreads) {
-        const int row = e / (C::kRoundCols / kVec), at = (e - row * (C::kRoundCols / kVec)) * kVec, col = col0 + at;
-        float m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int k = 0; k < C::kWK; ++k) m = fmaxf(m, top_s[k][row]);
-        const float from = m == -INFINITY ? 0.f : m;
-        float4 x[kVec / 4];
+      for (int round = 0; round < C::kRounds; ++round) {
+        const int col0 = round * C::kRoundCols;
+        if (round > 0) computing_warps();
 #pragma unroll
-        for (int q = 0; q < kVec / 4; ++q) x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < 2; ++r) {
+          const int row = wm * 16 + g + 8 * r;
+          if (row >= a.group) continue;
 #pragma unroll
-        for (int k = 0; k < C::kWK; ++k) {
-          const float w = power2(top_s[k][row] - from);
-          l += w * sum_s[k][row];
-#pragma unroll
-          for (int q = 0; q < kVec / 4; ++q) {
-            const float4 u = *reinterpret_cast<const float4*>(cell(k, row, at + 4 * q));
-            x[q].x += w * u.x; x[q].y += w * u.y; x[q].z += w * u.z; x[q].w += w * u.w;
+          for (int d = 0; d < kCols / 8; ++d) {
+            const int col = wn * kCols + 8 * d - col0;
+            if (C::kRounds == 1 || (col >= 0 && col < C::kRoundCols))
+              *reinterpret_cast<float2*>(cell(wk, row, col + 2 * (lane & 3))) = make_float2(o[d][2 * r], o[d][2 * r + 1]);
           }
         }
-        if (whole) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          const int head = t.kv_head * a.group + row;
-          uint32_t packed[kVec / 2];
+        computing_warps();
+        // Columns of a thread: few where many threads share a small group's rows
+        // (185k single 69.3 -> 67.1 us with four of 256; with 128 threads four
+        // spill where eight do not: 1024 requests of 100 keys 109 us instead of 92).
+        constexpr int kVec = kThreads == 128 ? 8 : 4;
+        for (int e = tid; e < a.group * (C::kRoundCols / kVec); e += kThreads) {
+          const int row = e / (C::kRoundCols / kVec), at = (e - row * (C::kRoundCols / kVec)) * kVec, col = col0 + at;
+          float m = -INFINITY, l = 0.f;
 #pragma unroll
-          for (int q = 0; q < kVec / 4; ++q) {
-            packed[2 * q] = pack2<kHalf>(x[q].x * inv, x[q].y * inv);
-            packed[2 * q + 1] = pack2<kHalf>(x[q].z * inv, x[q].w * inv);
+          for (int k = 0; k < C::kWK; ++k) m = fmaxf(m, top_s[k][row]);
+          const float from = m == -INFINITY ? 0.f : m;
+          float4 x[kVec / 4];
+#pragma unroll
+          for (int q = 0; q < kVec / 4; ++q) x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < C::kWK; ++k) {
+            const float w = power2(top_s[k][row] - from);
+            l += w * sum_s[k][row];
+#pragma unroll
+            for (int q = 0; q < kVec / 4; ++q) {
+              const float4 u = *reinterpret_cast<const float4*>(cell(k, row, at + 4 * q));
+              x[q].x += w * u.x; x[q].y += w * u.y; x[q].z += w * u.z; x[q].w += w * u.w;
+            }
           }
-          uint16_t* to = a.out + t.token * a.out_stride + (int64_t)head * kDim + col;
-          if constexpr (kVec == 8) *reinterpret_cast<uint4*>(to) = make_uint4(packed[0], packed[1], packed[kVec / 2 - 2], packed[kVec / 2 - 1]);
-          else *reinterpret_cast<uint2*>(to) = make_uint2(packed[0], packed[1]);
-          if (a.lse && col == 0)
-            a.lse[(int64_t)t.token * a.n_heads + head] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
-        } else {
-          float4* to = reinterpret_cast<float4*>(a.ws + ws.rows) + (part * C::kRows + row) * (kDim / 4) + col / 4;
+          if (whole) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int head = t.kv_head * a.group + row;
+            uint32_t packed[kVec / 2];
 #pragma unroll
-          for (int q = 0; q < kVec / 4; ++q) to[q] = x[q];
-          if (col == 0) reinterpret_cast<float2*>(a.ws + ws.sums)[part * C::kRows + row] = make_float2(m, l);
+            for (int q = 0; q < kVec / 4; ++q) {
+              packed[2 * q] = pack2<kHalf>(x[q].x * inv, x[q].y * inv);
+              packed[2 * q + 1] = pack2<kHalf>(x[q].z * inv, x[q].w * inv);
+            }
+            uint16_t* to = a.out + t.token * a.out_stride + (int64_t)head * kDim + col;
+            if constexpr (kVec == 8) *reinterpret_cast<uint4*>(to) = make_uint4(packed[0], packed[1], packed[kVec / 2 - 2], packed[kVec / 2 - 1]);
+            else *reinterpret_cast<uint2*>(to) = make_uint2(packed[0], packed[1]);
+            if (a.lse && col == 0)
+              a.lse[(int64_t)t.token * a.n_heads + head] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
+          } else {
+            float4* to = reinterpret_cast<float4*>(a.ws + ws.rows) + (part * C::kRows + row) * (kDim / 4) + col / 4;
+#pragma unroll
+            for (int q = 0; q < kVec / 4; ++q) to[q] = x[q];
+            if (col == 0) reinterpret_cast<float2*>(a.ws + ws.sums)[part * C::kRows + row] = make_float2(m, l);
+          }
         }
       }
+      // The next iteration's barrier comes before this stage is filled again.
     }
-    // The next iteration's barrier comes before this stage is filled again.
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  if (!C::kLookupWarp && tid == 0) words[share] = bits;
+  if constexpr (C::kTensor) {
+    ptx::tc_fence_after();
+    if (warp == kAllocWarp) ptx::tmem_dealloc(tensor.base, tmem_cols(kDim));
+  }
 }
 
 // Joins the parts of the units that go on across shares: a CTA per record (x)
@@ -752,9 +1007,11 @@ cudaError_t launch(const DraftAttnArgs& a, cudaStream_t stream) {
 
 template <bool kHalf, int kDim>
 cudaError_t launch_rows(const DraftAttnArgs& a, cudaStream_t stream) {
-  return a.row_tile == 16   ? launch<kHalf, kDim, 1>(a, stream)
-         : a.row_tile == 32 ? launch<kHalf, kDim, 2>(a, stream)
-                            : launch<kHalf, kDim, 4>(a, stream);
+  if (a.row_tile == 16) return launch<kHalf, kDim, 1>(a, stream);
+  if constexpr (kDim != 128) {
+    if (a.row_tile == 32) return launch<kHalf, kDim, 2>(a, stream);
+  }
+  return launch<kHalf, kDim, 4>(a, stream);
 }
 
 template <bool kHalf>
@@ -765,6 +1022,8 @@ cudaError_t launch_dim(const DraftAttnArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+int draft_row_tile(int group, int head_dim) { return group <= 16 ? 16 : group <= 32 && head_dim != 128 ? 32 : 64; }
 
 int draft_tile_keys(int head_dim) { return head_dim == 64 ? 128 : 64; }
 
