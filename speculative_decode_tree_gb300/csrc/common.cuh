@@ -338,8 +338,8 @@ __device__ __forceinline__ void release_grid() { asm volatile("griddepcontrol.la
 
 // ---- launchers (one per .cu file) ----
 int draft_row_tile(int group, int head_dim);
-int draft_tile_keys(int head_dim);
-int draft_shares(int head_dim, int num_sms);
+int draft_tile_keys(int row_tile, int head_dim);
+int draft_shares(int row_tile, int head_dim, int num_sms);
 int64_t draft_workspace_bytes(int row_tile, int head_dim, int n_shares);
 cudaError_t launch_draft_attention(const DraftAttnArgs& a, cudaStream_t stream);
 bool draft_cache_ok(const ddtree_draft_cache_t* cache);

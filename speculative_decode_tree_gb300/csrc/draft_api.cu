@@ -21,7 +21,7 @@ bool sizes_ok(int n_tokens, int n_heads, int n_kv_heads, int head_dim, int dtype
 bool plan_ok(const ddtree_draft_plan_t* p) {
   if (!p || !sizes_ok(p->n_tokens, p->n_heads, p->n_kv_heads, p->head_dim, p->dtype, p->page_size, p->window, p->n_sinks))
     return false;
-  if (p->row_tile != draft_row_tile(p->n_heads / p->n_kv_heads, p->head_dim) || p->tile_keys != draft_tile_keys(p->head_dim) ||
+  if (p->row_tile != draft_row_tile(p->n_heads / p->n_kv_heads, p->head_dim) || p->tile_keys != draft_tile_keys(p->row_tile, p->head_dim) ||
       p->n_shares < 1 || p->n_shares > 65535)
     return false;
   if (p->workspace_bytes != draft_workspace_bytes(p->row_tile, p->head_dim, p->n_shares)) return false;
@@ -58,8 +58,8 @@ extern "C" int ddtree_draft_attention_plan(int n_tokens, int n_heads, const ddtr
   p.window = window;
   p.n_sinks = n_sinks;
   p.row_tile = draft_row_tile(n_heads / cache->n_kv_heads, p.head_dim);
-  p.tile_keys = draft_tile_keys(p.head_dim);
-  p.n_shares = draft_shares(p.head_dim, num_sms);
+  p.tile_keys = draft_tile_keys(p.row_tile, p.head_dim);
+  p.n_shares = draft_shares(p.row_tile, p.head_dim, num_sms);
   p.workspace_bytes = draft_workspace_bytes(p.row_tile, p.head_dim, p.n_shares);
   *plan = p;
   return DDTREE_OK;

@@ -50,7 +50,11 @@
 namespace ddtree {
 namespace {
 
-constexpr int kRing = 4;  // offset slots: the tile in use, those in flight, and the next
+// Keys of a tile and CTAs per SM, by rows and columns.
+__host__ __device__ constexpr int keys_of(int row_tile, int dim) {
+  return row_tile == 64 ? (dim == 256 ? 32 : 64) : dim == 64 ? 128 : 64;
+}
+__host__ __device__ constexpr int ctas_of(int row_tile, int dim) { return dim == 64 || (dim == 128 && row_tile < 64) ? 2 : 1; }
 
 template <int kDim, int kWM>
 struct Config {
@@ -63,28 +67,35 @@ struct Config {
   // 204, 115 and 231, 191, 127.
   static constexpr bool kTensor = kWM == 4;
   static_assert(kWM != 2 || kDim != 128, "see draft_row_tile");
-  static constexpr int kKeys = kDim == 64 ? 128 : 64;       // keys of a tile
+  static constexpr int kKeys = keys_of(16 * kWM, kDim);     // keys of a tile
   // Warps along the rows, the keys and the columns of V.  256 columns are
   // halved between two warps (both take the scores): a whole row's registers
   // would leave too few warps to hide each other's latency.
   static constexpr int kWN = kDim == 256 ? 2 : 1;
   static constexpr int kWK = kTensor ? 2 : kDim == 64 ? 8 / kWM : 4 / kWM;
-  static constexpr int kWarps = kTensor ? 8 : kWM * kWN * kWK;
+  static constexpr int kWarps = kTensor ? 12 : kWM * kWN * kWK;
   static constexpr int kThreads = 32 * kWarps;              // that compute
   // One more warp looks the keys up (185k single 70.8 us instead of 84.8 when
   // one of the others did, batch of 61 110 instead of 119).
-  static constexpr int kAllThreads = kThreads + 32;
+  static constexpr int kAllThreads = kThreads + (kTensor ? 64 : 32);
   static constexpr int kRows = 16 * kWM;
   static constexpr int kRowBytes = kDim * 2;
   static constexpr int kTileBytes = kKeys * kRowBytes;      // of K, and of V
   static constexpr int kQBytes = kRows * kRowBytes;
-  static constexpr int kCtas = kDim == 256 ? 1 : 2;         // per SM
-  static constexpr int kStages = kWM == 1 ? 3 : 2;
+  static constexpr int kCtas = ctas_of(16 * kWM, kDim);     // per SM
+  static constexpr int kStages = kTensor ? (kDim == 256 ? 4 : 5) : kWM == 1 ? 3 : 2;
+  static constexpr int kQSlots = kTensor ? 2 : kStages;     // units whose queries are held
+  static constexpr int kRing = kTensor ? 8 : 4;             // offset slots: the tile in use, those in flight, and the next
+  static constexpr int kCopyThreads = kTensor ? 128 : kThreads;
   // Shared memory: probabilities (kTensor), queries, tiles.  The tensor core
   // reads 128 rows of an operand whose first 64 count: behind the last of the
   // probabilities lie queries and behind those tiles, so it stays inside.
-  static constexpr int kPBytes = kTensor ? kRows * kKeys * 2 : 0;
-  static constexpr int kSmem = (kTensor ? 1024 : 0) + kPBytes + kStages * (2 * kTileBytes + kQBytes);
+  static constexpr int kPBytes = kTensor ? kRows * 128 : 0;
+  static constexpr int kQAt = kTensor ? kPBytes : kStages * 2 * kTileBytes;  // from the first byte used
+  static constexpr int kRingAt = kTensor ? kPBytes + kQSlots * kQBytes : 0;
+  static constexpr int kUsed = kPBytes + kQSlots * kQBytes + kStages * 2 * kTileBytes;
+  static constexpr int kSmem = (kTensor ? 1024 : 0) + kUsed;
+  static_assert(kQAt + kQSlots * kQBytes <= kUsed && kRingAt + kStages * 2 * kTileBytes <= kUsed, "shared memory");
   // Columns joined at a time: the rows of all key parts fit the stage they replace.
   static constexpr int kRounds = kWK * kRows * kDim * 4 <= 2 * kTileBytes ? 1 : 2;
   static constexpr int kRoundCols = kDim / kRounds;
@@ -176,221 +187,271 @@ enum { kFirst = 1, kLast = 2, kBegun = 4, kGoesOn = 8 };
 
 // ---- 64 rows: scores and sums in tensor memory
 //
-// One thread issues the products: S = Q K^T (128 x tile keys, rows 64.. unused)
-// and O += P V (128 x columns).  Four warps take the softmax, a row and half of
-// the tile's keys per thread: two threads of a row exchange their maxima through
-// shared memory, keep one reference m that moves only when the maximum has
-// grown by more than 2^8 (the rows of O are then rescaled in place), and leave
-// P in shared memory in the cache's type.  All eight warps copy.  Within a CTA
-// the steps of a tile follow each other; the two CTAs of an SM fill each other's
-// gaps (256 columns: one CTA, twice the keys' bytes per step).
-// Waits are bounded (2 s): an expired one sets TIMEOUT and leaves its tile's
-// number, and behind the next tile's barrier all warps see it and stop.  (The
-// number and not a flag: a warp that is late behind a barrier must not stop for
-// what another has set since.)
+// Roles: four warps copy, one looks keys up, one issues the products S = Q K^T
+// (64 x tile keys) and O += P V (64 x columns), eight take the softmax: two warps
+// share 16 rows, a half of the tile's keys each, exchange their maxima through
+// shared memory, keep one reference m that moves only when the maximum has grown
+// by more than 2^8 (the rows of O are then rescaled in place), and leave P in
+// shared memory in the cache's type.
+// The first three meet at a barrier per tile (feeders_barrier); the softmax warps
+// follow them through the products' barriers only.  The scores of the next tile
+// are issued before the softmax of this one, so a tile costs its softmax and the
+// way through the P barrier, and copies are in flight for all but three of the
+// stages.  Queries are copied two tiles ahead, into two slots.
+// One elected thread of the converged warp issues: with a thread chosen by its
+// lane the descriptors go through vector registers, and a product of 16 columns
+// of K took 100 cycles to issue instead of 35.
+// Waits are bounded (2 s): a warp whose wait expires sets TIMEOUT and goes on
+// without waiting, so that every barrier is still met.
 struct TensorShared {
-  uint64_t scores, values;  // barriers: S of a tile complete, O of a tile complete
-  uint32_t base;            // tensor memory
-  int32_t expired;          // tile in which a wait ran out, else INT32_MAX
+  uint64_t scores[2], values[2];  // barriers of even and odd tiles: S complete, O complete
+  uint32_t base;                  // tensor memory
 };
-constexpr int kAllocWarp = 3, kIssueWarp = 2;
+constexpr int kAllocWarp = 3, kIssueWarp = 13;
 constexpr uint64_t kWaitNs = 2000000000ull;
-// Columns: S at 0, O behind; a power of two.
+// Columns: two S at 0, O behind; a power of two.
 __host__ __device__ constexpr int o_col(int dim) { return dim == 256 ? 256 : 128; }
 __host__ __device__ constexpr int tmem_cols(int dim) { return dim == 256 ? 512 : 256; }
 // Instruction descriptor: 32-bit sums, A and B both fp16 or both bf16, A K-major.
 __host__ __device__ constexpr uint32_t product_desc(int n, bool b_mn_major, bool half) {
-  return half ? ptx::idesc_bf16_f32(128, n, false, b_mn_major) & ~((1u << 7) | (1u << 10))
-              : ptx::idesc_bf16_f32(128, n, false, b_mn_major);
+  return half ? ptx::idesc_bf16_f32(64, n, false, b_mn_major) & ~((1u << 7) | (1u << 10))
+              : ptx::idesc_bf16_f32(64, n, false, b_mn_major);
 }
 
-template <bool kHalf, int kDim, typename Copies>
+// Warps 0 to 7 take the softmax, 8 to 11 copy.
+__device__ __forceinline__ bool copies_tiles(int warp) { return (warp & ~3) == 8; }
+
+// The copying warps, the lookup warp and the issuing warp.
+__device__ __forceinline__ void feeders_barrier() { asm volatile("bar.sync 1, 192;" ::: "memory"); }
+
+template <bool kHalf, int kDim, typename Copies, typename Queries>
 __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layout& ws, TensorShared& sh, uint32_t p_at,
                                              uint32_t q_ring, uint32_t ring, const Tile* tiles,
-                                             const uint32_t (*there)[Config<kDim, 4>::kKeys / 32], float (*top_s)[64],
-                                             float (*sum_s)[64], uint32_t* bits, int count, int share, Copies& start_copies) {
+                                             const uint32_t (*there)[Config<kDim, 4>::kKeys / 32], float (*top_s)[64], float (*sum_s)[64],
+                                             uint32_t* bits, int count, int share, Copies& start_copies, Queries& start_queries) {
   using namespace ptx;
   using C = Config<kDim, 4>;
-  constexpr int kHalfKeys = C::kKeys / 2, kHalfCols = kDim / 2;
+  constexpr int kBlocks = C::kKeys / 16;  // of eight keys, half a tile's
+  constexpr int kHalfCols = kDim / 2;
   constexpr int kSlab = C::kKeys * 128, kRowSlab = 64 * 128;  // 64 columns of a tile, and of 64 rows
   constexpr float kShift = kHalf ? 10.f : 0.f;
   constexpr float kGrowth = kHalf ? 4.f : 8.f;  // fp16: 2^(10 + 4) is the largest probability
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // Warps 0, 1 and 4, 5 reach the lanes of rows 0..63.
-  const bool softmax = (warp & 3) < 2;
-  const int row = (warp & 1) * 32 + lane, half = warp >> 2;
-  const uint32_t my_lane = (uint32_t)((warp & 3) * 32) << 16;
-  const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);  // as for fewer rows
-  float m = -INFINITY, l = 0.f;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   tc_fence_after();  // the base was written before the last barrier
   const uint32_t s_mem = sh.base, o_mem = sh.base + o_col(kDim);
-  auto rows_barrier = [] { asm volatile("bar.sync 3, 128;" ::: "memory"); };
-  auto wait = [&](uint64_t* bar, uint32_t parity, int i) {
-    if (!mbar_wait(bar, parity, kWaitNs)) {
-      *(volatile int32_t*)&sh.expired = i;
+  bool late = false;
+  auto wait = [&](uint64_t (&bars)[2], int tile) {  // by a whole warp
+    if (!late && !__all_sync(0xffffffffu, mbar_wait(&bars[tile & 1], (tile >> 1) & 1, kWaitNs))) {
+      late = true;
       atomicOr(bits, DDTREE_ST_TIMEOUT);
     }
   };
+  auto stage_of = [&](int i) { return ring + (i % C::kStages) * 2 * C::kTileBytes; };
 
-  for (int i = 0; i < count; ++i) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-    fence_async_smem();  // this thread's copies, before the tensor core reads them
-    tc_fence_before();
-    __syncthreads();
-    if (*(volatile int32_t*)&sh.expired < i) break;
-    const int slot = i % kRing;
-    const Tile t = tiles[slot];
-    const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes, v_at = k_at + C::kTileBytes;
-    if (warp == kIssueWarp && lane == 0) {
-      tc_fence_after();
-      const uint32_t q_at = q_ring + (t.unit % C::kStages) * C::kQBytes;
+  if (copies_tiles(warp)) {
+    for (int i = 0; i < count; ++i) {
+      // The next tile is here; its queries, where a unit starts, came with the last copies.
+      if (i > 0 && i + 1 < count && (tiles[(i + 1) % C::kRing].flags & kFirst)) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      else asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 3) : "memory");
+      fence_async_smem();  // this thread's copies, before the tensor core reads them
+      __syncwarp();
+      feeders_barrier();
+      // The last tile's stage is free once its O is complete, and with it this
+      // tile's queries, whose scores were issued before.
+      if (i > 0) wait(sh.values, i - 1);
+      else wait(sh.scores, 0);
+      start_queries(i + 2);
+      start_copies(i + C::kStages - 1);
+    }
+    return;
+  }
+
+  if (warp == kIssueWarp) {
+    auto score = [&](int i) {
+      const uint32_t q_at = q_ring + (tiles[i % C::kRing].unit % C::kQSlots) * C::kQBytes, k_at = stage_of(i);
 #pragma unroll
       for (int c = 0; c < kDim / 64; ++c)
-        mma_ss_x4<2, 2>(s_mem, desc_sw128(q_at + c * kRowSlab, 16, 1024), desc_sw128(k_at + c * kSlab, 16, 1024),
-                        product_desc(C::kKeys, false, kHalf), c > 0);
-      mma_commit(&sh.scores);
-    }
-    // The last tile's stage and probabilities are free once its O is complete.
-    if (i > 0) wait(&sh.values, (i - 1) & 1, i);
-    start_copies(i + C::kStages - 1);
-    if (softmax) {
-      wait(&sh.scores, i & 1, i);
+        mma_ss_x4<2, 2>(s_mem + (i & 1) * C::kKeys, desc_sw128(q_at + c * kRowSlab, 16, 1024),
+                        desc_sw128(k_at + c * kSlab, 16, 1024), product_desc(C::kKeys, false, kHalf), c > 0);
+      mma_commit(&sh.scores[i & 1]);
+    };
+    for (int i = 0; i < count; ++i) {
       __syncwarp();
+      feeders_barrier();
       tc_fence_after();
-      uint32_t x[kHalfKeys / 32][32];
-#pragma unroll
-      for (int q = 0; q < kHalfKeys / 32; ++q) tmem_ld32(s_mem + my_lane + half * kHalfKeys + 32 * q, x[q]);
-      if (a.scale_log2 < 0.f) {
-#pragma unroll
-        for (int k = 0; k < kHalfKeys; ++k) x[k >> 5][k & 31] ^= 0x80000000u;
+      if (elect_one()) {
+        if (i == 0) score(0);
+        if (i + 1 < count) score(i + 1);
       }
-#pragma unroll
-      for (int q = 0; q < kHalfKeys / 32; ++q) {
-        const uint32_t mask = there[slot][half * (kHalfKeys / 32) + q];
-        if (mask != 0xffffffffu) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (!((mask >> k) & 1)) x[q][k] = 0xff800000u;  // -inf
-        }
-      }
-      float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int k = 0; k < kHalfKeys; ++k) high[k & 3] = fmaxf(high[k & 3], __uint_as_float(x[k >> 5][k & 31]));
-      const float mine = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
-      top_s[half][row] = mine;
-      rows_barrier();
-      const float top = fmaxf(mine, top_s[half ^ 1][row]);
-      if (t.flags & kFirst) {
-        m = -INFINITY;
-        l = 0.f;
-      }
-      float keep = 1.f;
-      if ((top - m) * scale > kGrowth) {  // also the first finite maximum
-        keep = m == -INFINITY ? 0.f : power2((m - top) * scale);
-        m = top;
-      }
-      l *= keep;
-      // The rows of O so far, whose last product is complete (the wait above).
-      if (!(t.flags & kFirst) && __any_sync(0xffffffffu, keep != 1.f)) {
-        __syncwarp();
-        tc_fence_after();
-        uint32_t v[16];
-#pragma unroll 1
-        for (int c = 0; c < kHalfCols; c += 16) {
-          tmem_ld16(o_mem + my_lane + half * kHalfCols + c, v);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * keep);
-          tmem_st16(o_mem + my_lane + half * kHalfCols + c, v);
-        }
-        tmem_st_wait();
-      }
-      const float base = m == -INFINITY ? 0.f : kShift - m * scale;
-      const uint32_t p_row = p_at + row * 128;
-      float sums[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < kHalfKeys / 8; ++c) {  // 16-byte chunks of eight keys
-        uint32_t packed[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int k = 8 * c + 2 * e;
-          const float u = power2(fmaf(__uint_as_float(x[k >> 5][k & 31]), scale, base));
-          const float w = power2(fmaf(__uint_as_float(x[k >> 5][(k & 31) + 1]), scale, base));
-          sums[e] += u + w;
-          packed[e] = pack2<kHalf>(u, w);
-        }
-        const int chunk = half * (kHalfKeys / 8) + c;  // of the tile: slab chunk / 8
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + (chunk >> 3) * kRowSlab +
-                                                                       (((chunk & 7) ^ (row & 7)) << 4)),
-                     "r"(packed[0]), "r"(packed[1]), "r"(packed[2]), "r"(packed[3])
-                     : "memory");
-      }
-      l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
-      fence_async_smem();
-      tc_fence_before();
-    }
-    // P is written and O rescaled; and every warp has seen the last O complete,
-    // so the barrier of the values never runs two phases ahead of a waiter.
-    asm volatile("bar.sync 2, %0;" ::"n"(C::kThreads) : "memory");
-    if (warp == kIssueWarp && lane == 0) {
+      __syncwarp();
+      asm volatile("bar.sync 2, 288;" ::: "memory");  // P is written and O rescaled
       tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < C::kKeys / 64; ++c)
-        mma_ss_x4<2, 128>(o_mem, desc_sw128(p_at + c * kRowSlab, 16, 1024), desc_sw128(v_at + c * 64 * 128, kSlab, 1024),
-                          product_desc(kDim, true, kHalf), c > 0 || !(t.flags & kFirst));
-      mma_commit(&sh.values);
+      if (elect_one()) {
+        const uint32_t v_at = stage_of(i) + C::kTileBytes;
+        const bool more = !(tiles[i % C::kRing].flags & kFirst);
+        if constexpr (C::kKeys == 64)
+          mma_ss_x4<2, 128>(o_mem, desc_sw128(p_at, 16, 1024), desc_sw128(v_at, kSlab, 1024), product_desc(kDim, true, kHalf), more);
+        else
+          mma_ss_x2<2, 128>(o_mem, desc_sw128(p_at, 16, 1024), desc_sw128(v_at, kSlab, 1024), product_desc(kDim, true, kHalf), more);
+        mma_commit(&sh.values[i & 1]);
+      }
     }
-    if (!(t.flags & kLast) || !softmax) continue;
+    // Nothing is in flight once the softmax warps are through (the last tile
+    // ends a unit); after an expired wait, give what is a last chance.
+    if (elect_one()) {
+      __shared__ uint64_t drained;
+      mbar_init(&drained, 1);
+      fence_mbar_init();
+      mma_commit(&drained);
+      mbar_wait(&drained, 0, kWaitNs);
+    }
+    return;
+  }
 
-    // ---- the unit ends here: a thread has half of a row's columns
-    sum_s[half][row] = l;
-    rows_barrier();
-    const float total = l + sum_s[half ^ 1][row];
-    wait(&sh.values, i & 1, i);
+  // Row 16 w + r of a product with 64 rows is lane 32 w + r of the tensor memory.
+  // A thread has rows row and row + 8, keys (columns) 2 quad and 2 quad + 1 of every eight.
+  const int row = (warp & 3) * 16 + (lane >> 2), quad = lane & 3;
+  const int half = warp >> 2;  // of the tile's keys and O's columns
+  const uint32_t my_lane = (uint32_t)((warp & 3) * 32) << 16;
+  const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);  // as for fewer rows
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  auto rows_barrier = [&] {  // the two warps of the same rows
     __syncwarp();
+    asm volatile("bar.sync %0, 64;" ::"r"(3 + (warp & 3)) : "memory");
+  };
+  for (int i = 0; i < count; ++i) {
+    const int slot = i % C::kRing;
+    wait(sh.scores, i);
+    tc_fence_after();
+    const Tile t = tiles[slot];
+    uint32_t x[4 * kBlocks];
+    if constexpr (kBlocks == 4) tmem_ld_frag32(s_mem + my_lane + (i & 1) * C::kKeys + half * 32, x);
+    else tmem_ld_frag16(s_mem + my_lane + (i & 1) * C::kKeys + half * 16, x);
+    if (a.scale_log2 < 0.f) {
+#pragma unroll
+      for (int k = 0; k < 4 * kBlocks; ++k) x[k] ^= 0x80000000u;
+    }
+    const uint32_t mask = there[slot][half * kBlocks / 4] >> (half * kBlocks * 8 % 32);
+    if (~mask << (32 - 8 * kBlocks)) {
+#pragma unroll
+      for (int k = 0; k < 4 * kBlocks; ++k)
+        if (!((mask >> (8 * (k >> 2) + 2 * quad + (k & 1))) & 1)) x[k] = 0xff800000u;  // -inf
+    }
+    float tops[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float high[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < kBlocks; ++j) {
+        high[0] = fmaxf(high[0], __uint_as_float(x[4 * j + 2 * h]));
+        high[1] = fmaxf(high[1], __uint_as_float(x[4 * j + 2 * h + 1]));
+      }
+      tops[h] = fmaxf(high[0], high[1]);
+      tops[h] = fmaxf(tops[h], __shfl_xor_sync(0xffffffffu, tops[h], 1));
+      tops[h] = fmaxf(tops[h], __shfl_xor_sync(0xffffffffu, tops[h], 2));
+      if (quad == 0) top_s[2 * (i & 1) + half][row + 8 * h] = tops[h];
+    }
+    rows_barrier();
+    float keep[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float top = fmaxf(tops[h], top_s[2 * (i & 1) + (half ^ 1)][row + 8 * h]);
+      if (t.flags & kFirst) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+      }
+      keep[h] = 1.f;
+      if ((top - m[h]) * scale > kGrowth) {  // also the first finite maximum
+        keep[h] = m[h] == -INFINITY ? 0.f : power2((m[h] - top) * scale);
+        m[h] = top;
+      }
+      l[h] *= keep[h];
+    }
+    // The last product: P may be written again, and the rows of O are complete.
+    if (i > 0) wait(sh.values, i - 1);
+    if (!(t.flags & kFirst) && __any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
+      tc_fence_after();
+      uint32_t v[16];
+#pragma unroll 1
+      for (int c = half * kHalfCols; c < (half + 1) * kHalfCols; c += 32) {
+        tmem_ld_frag32(o_mem + my_lane + c, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * keep[(e >> 1) & 1]);
+        tmem_st_frag32(o_mem + my_lane + c, v);
+      }
+      tmem_st_wait();
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float base = m[h] == -INFINITY ? 0.f : kShift - m[h] * scale;
+      const uint32_t p_row = p_at + (row + 8 * h) * 128 + 4 * quad;
+      float sums[2] = {0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < kBlocks; ++j) {
+        const float u = power2(fmaf(__uint_as_float(x[4 * j + 2 * h]), scale, base));
+        const float w = power2(fmaf(__uint_as_float(x[4 * j + 2 * h + 1]), scale, base));
+        sums[j & 1] += u + w;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(p_row + (((half * kBlocks + j) ^ (row & 7)) << 4)), "r"(pack2<kHalf>(u, w)) : "memory");
+      }
+      l[h] += sums[0] + sums[1];
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    // A warp cannot be here again before the others were: it waits for the values.
+    if (late) asm volatile("bar.sync 2, 288;" ::: "memory");
+    else asm volatile("bar.arrive 2, 288;" ::: "memory");
+    if (!(t.flags & kLast)) continue;
+
+    // ---- the unit ends here
+    wait(sh.values, i);
     tc_fence_after();
     const bool whole = !(t.flags & (kBegun | kGoesOn));
     const int64_t part = 2 * share + (t.flags & kBegun ? 0 : 1);
     const int head = t.kv_head * a.group + row;
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    uint16_t* out = a.out + t.token * a.out_stride + (int64_t)head * kDim + half * kHalfCols;
-    float4* rows = reinterpret_cast<float4*>(a.ws + ws.rows) + (part * C::kRows + row) * (kDim / 4) + half * (kHalfCols / 4);
+    float total[2], inv[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      total[h] = l[h] + __shfl_xor_sync(0xffffffffu, l[h], 1);
+      total[h] += __shfl_xor_sync(0xffffffffu, total[h], 2);
+      if (quad == 0) sum_s[half][row + 8 * h] = total[h];
+    }
+    rows_barrier();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      total[h] = sum_s[0][row + 8 * h] + sum_s[1][row + 8 * h];
+      inv[h] = total[h] == 0.f ? 0.f : 1.f / total[h];
+    }
+    uint16_t* out = a.out + t.token * a.out_stride + (int64_t)head * kDim + 2 * quad;
+    float* rows = reinterpret_cast<float*>(a.ws + ws.rows) + (part * C::kRows + row) * kDim + 2 * quad;
 #pragma unroll 1
-    for (int c = 0; c < kHalfCols; c += 16) {
+    for (int c = half * kHalfCols; c < (half + 1) * kHalfCols; c += 32) {
       uint32_t v[16];
-      tmem_ld16(o_mem + my_lane + half * kHalfCols + c, v);  // the whole warp; the rows that count are stored
-      if (row < a.group) {
-        float f[16];
+      tmem_ld_frag32(o_mem + my_lane + c, v);  // the whole warp; the rows that count are stored
 #pragma unroll
-        for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(v[e]);
-        if (whole) {
+      for (int h = 0; h < 2; ++h) {
+        if (row + 8 * h < a.group) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 8)
-            *reinterpret_cast<uint4*>(out + c + e) =
-                make_uint4(pack2<kHalf>(f[e] * inv, f[e + 1] * inv), pack2<kHalf>(f[e + 2] * inv, f[e + 3] * inv),
-                           pack2<kHalf>(f[e + 4] * inv, f[e + 5] * inv), pack2<kHalf>(f[e + 6] * inv, f[e + 7] * inv));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) rows[(c + e) / 4] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+          for (int j = 0; j < 4; ++j) {
+            const float u = __uint_as_float(v[4 * j + 2 * h]), w = __uint_as_float(v[4 * j + 2 * h + 1]);
+            if (whole) *reinterpret_cast<uint32_t*>(out + 8 * h * kDim + c + 8 * j) = pack2<kHalf>(u * inv[h], w * inv[h]);
+            else *reinterpret_cast<float2*>(rows + 8 * h * kDim + c + 8 * j) = make_float2(u, w);
+          }
         }
       }
       __syncwarp();
     }
     tc_fence_before();
-    if (row < a.group && half == 0) {
-      const float top = m == -INFINITY ? m : m * scale;
-      if (!whole) reinterpret_cast<float2*>(a.ws + ws.sums)[part * C::kRows + row] = make_float2(top, total);
-      else if (a.lse)
-        a.lse[(int64_t)t.token * a.n_heads + head] = total == 0.f ? -INFINITY : (top - kShift + log2f(total)) * 0.6931471805599453f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (row + 8 * h < a.group && quad == 0 && half == 0) {
+        const float top = m[h] == -INFINITY ? m[h] : m[h] * scale;
+        if (!whole) reinterpret_cast<float2*>(a.ws + ws.sums)[part * C::kRows + row + 8 * h] = make_float2(top, total[h]);
+        else if (a.lse)
+          a.lse[(int64_t)t.token * a.n_heads + head + 8 * h] =
+              total[h] == 0.f ? -INFINITY : (top - kShift + log2f(total[h])) * 0.6931471805599453f;
+      }
     }
-  }
-  // Nothing of the tensor core's is in flight after a complete list (its last
-  // tile ends a unit); after an expired wait, give what is a last chance.
-  if (warp == kIssueWarp && lane == 0) {
-    __shared__ uint64_t drained;
-    mbar_init(&drained, 1);
-    fence_mbar_init();
-    mma_commit(&drained);
-    mbar_wait(&drained, 0, kWaitNs);
   }
   tc_fence_before();
 }
@@ -402,10 +463,10 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   constexpr int kThreads = C::kThreads, kWarps = C::kWarps;  // without the lookup warp
   constexpr int kChunks = kDim / 8;  // 16-byte chunks of a row
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t offsets[kRing][C::kKeys];   // element offset of a key's row
-  __shared__ uint32_t there[kRing][C::kKeys / 32];  // a bit per key that exists
-  __shared__ Tile tiles[kRing];
-  __shared__ float top_s[C::kWK][C::kRows], sum_s[C::kWK][C::kRows];
+  __shared__ int64_t offsets[C::kRing][C::kKeys];   // element offset of a key's row
+  __shared__ uint32_t there[C::kRing][C::kKeys / 32];  // a bit per key that exists
+  __shared__ Tile tiles[C::kRing];
+  __shared__ float top_s[C::kTensor ? 4 : C::kWK][C::kRows], sum_s[C::kWK][C::kRows];  // kTensor: maxima of even and odd tiles
   __shared__ int64_t warp_sum[C::kAllThreads / 32];
   __shared__ int start_token;
   __shared__ int64_t start_at;
@@ -435,10 +496,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     if (lane >= d) inc += o;
   }
   if (lane == 31) warp_sum[warp] = inc;
-  if (tid == 0) {
-    bits = 0;
-    tensor.expired = INT32_MAX;
-  }
+  if (tid == 0) bits = 0;
   __syncthreads();
   int64_t before = inc - mine, total = 0;
 #pragma unroll
@@ -498,7 +556,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   };
   fetch_next();
   auto look_up = [&](int i) {
-    const int slot = i % kRing;
+    const int slot = i % C::kRing;
     int page[kPerLane], in[kPerLane];
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
@@ -562,8 +620,10 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   };
   if constexpr (C::kTensor) {
     if (tid == 0) {
-      ptx::mbar_init(&tensor.scores, 1);
-      ptx::mbar_init(&tensor.values, 1);
+      for (int k = 0; k < 2; ++k) {
+        ptx::mbar_init(&tensor.scores[k], 1);
+        ptx::mbar_init(&tensor.values[k], 1);
+      }
       ptx::fence_mbar_init();
     }
     if (warp == kAllocWarp) {
@@ -575,8 +635,9 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     for (int i = 0; i < C::kStages && i < count; ++i) look_up(i);
     __syncthreads();
     for (int i = 0; i < count; ++i) {
-      __syncthreads();  // tile i's slot is in use, the one of tile i + kStages free
-      if (C::kTensor && *(volatile int32_t*)&tensor.expired < i) break;
+      // Tile i's slot is in use, the one of tile i + kStages free.
+      if constexpr (C::kTensor) feeders_barrier();
+      else __syncthreads();
       if (i + C::kStages < count) look_up(i + C::kStages);
     }
     __syncthreads();
@@ -587,8 +648,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   // Operands of the tensor core are 64-column slabs of 128-byte rows, swizzled
   // from a 1024-byte border; for ldmatrix a row lies whole.
   const uint32_t p_at = C::kTensor ? (ptx::smem_u32(smem) + 1023) & ~1023u : ptx::smem_u32(smem);
-  const uint32_t q_ring = C::kTensor ? p_at + C::kPBytes : p_at + C::kStages * 2 * C::kTileBytes;
-  const uint32_t ring = C::kTensor ? q_ring + C::kStages * C::kQBytes : p_at;
+  const uint32_t q_ring = p_at + C::kQAt, ring = p_at + C::kRingAt;
   constexpr int kPitch = C::kTensor ? 128 : C::kRowBytes;
   auto swizzled = [](int row, int chunk, int rows) {
     if constexpr (C::kTensor) return (uint32_t)((chunk >> 3) * rows * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
@@ -596,15 +656,28 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   };
   // Starts the copies of tile i (every thread commits a group, empty or not).
   // A thread copies one chunk of every kRowsPerStep-th row: the swizzle of its
-  // rows is the same, so shared addresses advance by a constant.
-  constexpr int kRowsPerStep = kThreads / kChunks;
-  static_assert(C::kKeys % kRowsPerStep == 0 && kRowsPerStep % 8 == 0, "copy steps");
-  const int copy_chunk = tid % kChunks, copy_row = tid / kChunks;
+  // rows is the same, so shared addresses advance by a constant (steps of four
+  // rows: the third bit of the row alternates).
+  constexpr int kRowsPerStep = C::kCopyThreads / kChunks;
+  static_assert(C::kKeys % kRowsPerStep == 0 && kRowsPerStep % 4 == 0, "copy steps");
+  const int copy_tid = C::kTensor ? tid & 127 : tid;
+  const int copy_chunk = copy_tid % kChunks, copy_row = copy_tid / kChunks;
   const uint32_t copy_at = swizzled(copy_row, copy_chunk, C::kKeys);
   const uint16_t *copy_k = a.k + 8 * copy_chunk, *copy_v = a.v + 8 * copy_chunk;
+  auto start_queries = [&](int i) {
+    if (i >= count) return;
+    const Tile t = tiles[i % C::kRing];
+    if (!(t.flags & kFirst)) return;
+    const uint32_t q_at = q_ring + (t.unit % C::kQSlots) * C::kQBytes;
+    const uint16_t* q = a.q + t.token * a.q_stride + (int64_t)t.kv_head * a.group * kDim;
+#pragma unroll
+    for (int r = copy_row; r < C::kRows; r += kRowsPerStep)
+      ptx::cp_async16_zfill(q_at + swizzled(r, copy_chunk, C::kRows), r < a.group ? q + r * kDim + 8 * copy_chunk : a.q,
+                            r < a.group ? 16u : 0u);
+  };
   auto start_copies = [&](int i) {
     if (i < count) {
-      const int slot = i % kRing;
+      const int slot = i % C::kRing;
       const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes + copy_at, v_at = k_at + C::kTileBytes;
       uint32_t full = 0xffffffffu;
 #pragma unroll
@@ -613,8 +686,8 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
 #pragma unroll
         for (int r = 0; r < C::kKeys; r += kRowsPerStep) {
           const int64_t off = offsets[slot][copy_row + r];
-          ptx::cp_async16(k_at + r * kPitch, copy_k + off);
-          ptx::cp_async16(v_at + r * kPitch, copy_v + off);
+          ptx::cp_async16((k_at ^ ((r & 4) << 4)) + r * kPitch, copy_k + off);
+          ptx::cp_async16((v_at ^ ((r & 4) << 4)) + r * kPitch, copy_v + off);
         }
       } else {
 #pragma unroll 2
@@ -622,29 +695,28 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
           const int64_t off = offsets[slot][copy_row + r];
           const int key = copy_row + r;
           const uint32_t size = (there[slot][key >> 5] >> (key & 31)) & 1 ? 16u : 0u;
-          ptx::cp_async16_zfill(k_at + r * kPitch, copy_k + off, size);
-          ptx::cp_async16_zfill(v_at + r * kPitch, copy_v + off, size);
+          ptx::cp_async16_zfill((k_at ^ ((r & 4) << 4)) + r * kPitch, copy_k + off, size);
+          ptx::cp_async16_zfill((v_at ^ ((r & 4) << 4)) + r * kPitch, copy_v + off, size);
         }
       }
-      const Tile t = tiles[slot];
-      if (t.flags & kFirst) {
-        const uint32_t q_at = q_ring + (t.unit % C::kStages) * C::kQBytes;
-        const uint16_t* q = a.q + t.token * a.q_stride + (int64_t)t.kv_head * a.group * kDim;
-#pragma unroll
-        for (int r = copy_row; r < C::kRows; r += kRowsPerStep)
-          ptx::cp_async16_zfill(q_at + swizzled(r, copy_chunk, C::kRows), r < a.group ? q + r * kDim + 8 * copy_chunk : a.q,
-                                r < a.group ? 16u : 0u);
-      }
+      if constexpr (!C::kTensor) start_queries(i);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   __syncthreads();
+  if (!C::kTensor || copies_tiles(warp)) {
+    if constexpr (C::kTensor) {
+      start_queries(0);
+      start_queries(1);
+    }
 #pragma unroll 1
-  for (int i = 0; i < C::kStages - 1; ++i) start_copies(i);
+    for (int i = 0; i < C::kStages - 1; ++i) start_copies(i);
+  }
 
   if constexpr (C::kTensor) {
-    tensor_tiles<kHalf, kDim>(a, ws, tensor, p_at, q_ring, ring, tiles, there, top_s, sum_s, &bits, count, share, start_copies);
+    tensor_tiles<kHalf, kDim>(a, ws, tensor, p_at, q_ring, ring, tiles, there, top_s, sum_s, &bits, count, share, start_copies,
+                              start_queries);
   } else {
     auto computing_warps = [] { asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads) : "memory"); };
 
@@ -681,7 +753,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
       __syncthreads();
       start_copies(i + C::kStages - 1);
-      const int slot = i % kRing;
+      const int slot = i % C::kRing;
       const Tile t = tiles[slot];
       const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes, v_at = k_at + C::kTileBytes;
       const uint32_t q_at = q_ring + (t.unit % C::kStages) * C::kQBytes;
@@ -1025,9 +1097,9 @@ cudaError_t launch_dim(const DraftAttnArgs& a, cudaStream_t stream) {
 
 int draft_row_tile(int group, int head_dim) { return group <= 16 ? 16 : group <= 32 && head_dim != 128 ? 32 : 64; }
 
-int draft_tile_keys(int head_dim) { return head_dim == 64 ? 128 : 64; }
+int draft_tile_keys(int row_tile, int head_dim) { return keys_of(row_tile, head_dim); }
 
-int draft_shares(int head_dim, int num_sms) { return (head_dim == 256 ? 1 : 2) * num_sms; }
+int draft_shares(int row_tile, int head_dim, int num_sms) { return ctas_of(row_tile, head_dim) * num_sms; }
 
 int64_t draft_workspace_bytes(int row_tile, int head_dim, int n_shares) {
   return (layout_of(row_tile, head_dim, n_shares).total + 255) / 256 * 256;
