@@ -40,7 +40,7 @@
 // requests of 511 to 16k, 8 heads of 64 columns, 92 us (6.3 TB/s); a
 // window of 2,048 at 65k 7.8 us, a chain of dependent steps (positions, page
 // numbers, keys, product, join) with almost no bytes.  64 heads a group stream
-// 4.6, 5.5 and 4.2 TB/s at 64, 128 and 256 columns.  Token-granular pages of 64
+// 5.2, 6.2 and 5.3 TB/s at 64, 128 and 256 columns.  Token-granular pages of 64
 // columns, 128 bytes at scattered places, stream 5.2 TB/s.
 #include <atomic>
 
@@ -52,21 +52,20 @@ namespace {
 
 // Keys of a tile and CTAs per SM, by rows and columns.
 __host__ __device__ constexpr int keys_of(int row_tile, int dim) {
-  return row_tile == 64 ? (dim == 256 ? 32 : 64) : dim == 64 ? 128 : 64;
+  return row_tile == 64 ? 8192 / dim : dim == 64 ? 128 : 64;
 }
-__host__ __device__ constexpr int ctas_of(int row_tile, int dim) { return dim == 64 || (dim == 128 && row_tile < 64) ? 2 : 1; }
+__host__ __device__ constexpr int ctas_of(int row_tile, int dim) { return row_tile == 64 || dim == 256 ? 1 : 2; }
 
 template <int kDim, int kWM>
 struct Config {
-  // Up to 16 rows, 32 where the columns are 64 or 256, go through registers;
-  // 64 rows, and more than 16 of 128 columns, through the tensor memory
-  // (tensor_tiles): in registers every tile of 16 rows loads the keys' fragments
-  // for itself, which 64 rows of 128 columns pay with shared memory's whole
-  // bandwidth.  us per GB (256 columns: per 537 MB), registers and tensor memory:
-  // 64 rows of 64, 128, 256 columns 259, 269, 198 and 233, 194, 129; 24 rows 180,
-  // 204, 115 and 231, 191, 127.
+  // Up to 16 rows, 32 of 64 columns, go through registers, more through the tensor
+  // memory (tensor_tiles): in registers every tile of 16 rows loads the keys'
+  // fragments for itself, which 64 rows of 128 columns pay with shared memory's
+  // whole bandwidth.  us per GB (256 columns: per 537 MB), registers and tensor
+  // memory: 64 rows of 64, 128, 256 columns 259, 269, 198 and 208, 173, 101; 24
+  // rows 181, 204, 114 and 205, 167, 97.
   static constexpr bool kTensor = kWM == 4;
-  static_assert(kWM != 2 || kDim != 128, "see draft_row_tile");
+  static_assert(kWM != 2 || kDim == 64, "see draft_row_tile");
   static constexpr int kKeys = keys_of(16 * kWM, kDim);     // keys of a tile
   // Warps along the rows, the keys and the columns of V.  256 columns are
   // halved between two warps (both take the scores): a whole row's registers
@@ -87,10 +86,8 @@ struct Config {
   static constexpr int kQSlots = kTensor ? 2 : kStages;     // units whose queries are held
   static constexpr int kRing = kTensor ? 8 : 4;             // offset slots: the tile in use, those in flight, and the next
   static constexpr int kCopyThreads = kTensor ? 128 : kThreads;
-  // Shared memory: probabilities (kTensor), queries, tiles.  The tensor core
-  // reads 128 rows of an operand whose first 64 count: behind the last of the
-  // probabilities lie queries and behind those tiles, so it stays inside.
-  static constexpr int kPBytes = kTensor ? kRows * 128 : 0;
+  // Shared memory: probabilities (kTensor), queries, tiles.
+  static constexpr int kTileP = kRows * 128 * (kKeys > 64 ? 2 : 1), kPBytes = kTensor ? 2 * kTileP : 0;
   static constexpr int kQAt = kTensor ? kPBytes : kStages * 2 * kTileBytes;  // from the first byte used
   static constexpr int kRingAt = kTensor ? kPBytes + kQSlots * kQBytes : 0;
   static constexpr int kUsed = kPBytes + kQSlots * kQBytes + kStages * 2 * kTileBytes;
@@ -100,7 +97,7 @@ struct Config {
   static constexpr int kRounds = kWK * kRows * kDim * 4 <= 2 * kTileBytes ? 1 : 2;
   static constexpr int kRoundCols = kDim / kRounds;
   static_assert(kTensor || kWK * kRows * kRoundCols * 4 <= 2 * kTileBytes, "merge buffer");
-  static_assert(kRing >= kStages + 1, "offset ring");
+  static_assert(kRing >= kStages + (kTensor ? 3 : 1), "offset ring");
 };
 
 // A unit that goes on from one share to others: where its parts lie.  There is
@@ -183,35 +180,36 @@ struct Tile {
   int32_t unit;   // ordinal within the share: its queries' place in the ring
   int32_t flags;
 };
-enum { kFirst = 1, kLast = 2, kBegun = 4, kGoesOn = 8 };
+enum { kFirst = 1, kLast = 2, kBegun = 4, kGoesOn = 8, kNextLast = 16 };
 
 // ---- 64 rows: scores and sums in tensor memory
 //
 // Roles: four warps copy, one looks keys up, one issues the products S = Q K^T
-// (64 x tile keys) and O += P V (64 x columns), eight take the softmax: two warps
-// share 16 rows, a half of the tile's keys each, exchange their maxima through
-// shared memory, keep one reference m that moves only when the maximum has grown
-// by more than 2^8 (the rows of O are then rescaled in place), and leave P in
-// shared memory in the cache's type.
-// The first three meet at a barrier per tile (feeders_barrier); the softmax warps
-// follow them through the products' barriers only.  The scores of the next tile
-// are issued before the softmax of this one, so a tile costs its softmax and the
-// way through the P barrier, and copies are in flight for all but three of the
-// stages.  Queries are copied two tiles ahead, into two slots.
+// (64 x tile keys) and O += P V (64 x columns), eight take the softmax: four the
+// even tiles and four the odd ones, so that one group's exponentials run beside
+// the other's loads and maxima.  They hand each row's reference m from tile to
+// tile; it moves only when the maximum has grown by more than 2^8 (the rows of O
+// are then rescaled in place).  Each group has its own sum, joined where the unit
+// ends, and leaves P in shared memory in the cache's type.
+// Barriers of stages, tiles and units tie the roles together, so each runs ahead
+// as far as its buffers go: copies by the ring's stages, scores by one tile,
+// queries by one unit.
 // One elected thread of the converged warp issues: with a thread chosen by its
 // lane the descriptors go through vector registers, and a product of 16 columns
 // of K took 100 cycles to issue instead of 35.
 // Waits are bounded (2 s): a warp whose wait expires sets TIMEOUT and goes on
-// without waiting, so that every barrier is still met.
+// without waiting, so that every barrier between warps is still met.
 struct TensorShared {
-  uint64_t scores[2], values[2];  // barriers of even and odd tiles: S complete, O complete
+  // Barriers.  Of a stage: copies landed, O of its tile complete.  Of even and odd
+  // tiles: S complete.  Of even and odd units: the last S with their queries complete.
+  uint64_t full[5], values[5], scores[2], queries[2];
   uint32_t base;                  // tensor memory
 };
 constexpr int kAllocWarp = 3, kIssueWarp = 13;
 constexpr uint64_t kWaitNs = 2000000000ull;
 // Columns: two S at 0, O behind; a power of two.
-__host__ __device__ constexpr int o_col(int dim) { return dim == 256 ? 256 : 128; }
-__host__ __device__ constexpr int tmem_cols(int dim) { return dim == 256 ? 512 : 256; }
+__host__ __device__ constexpr int o_col(int dim) { return dim == 128 ? 128 : 256; }
+__host__ __device__ constexpr int tmem_cols(int dim) { return dim == 128 ? 256 : 512; }
 // Instruction descriptor: 32-bit sums, A and B both fp16 or both bf16, A K-major.
 __host__ __device__ constexpr uint32_t product_desc(int n, bool b_mn_major, bool half) {
   return half ? ptx::idesc_bf16_f32(64, n, false, b_mn_major) & ~((1u << 7) | (1u << 10))
@@ -221,18 +219,17 @@ __host__ __device__ constexpr uint32_t product_desc(int n, bool b_mn_major, bool
 // Warps 0 to 7 take the softmax, 8 to 11 copy.
 __device__ __forceinline__ bool copies_tiles(int warp) { return (warp & ~3) == 8; }
 
-// The copying warps, the lookup warp and the issuing warp.
-__device__ __forceinline__ void feeders_barrier() { asm volatile("bar.sync 1, 192;" ::: "memory"); }
+// The copying warps and the lookup warp.
+__device__ __forceinline__ void copies_barrier() { asm volatile("bar.sync 1, 160;" ::: "memory"); }
 
 template <bool kHalf, int kDim, typename Copies, typename Queries>
 __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layout& ws, TensorShared& sh, uint32_t p_at,
                                              uint32_t q_ring, uint32_t ring, const Tile* tiles,
-                                             const uint32_t (*there)[Config<kDim, 4>::kKeys / 32], float (*top_s)[64], float (*sum_s)[64],
+                                             const uint32_t (*there)[Config<kDim, 4>::kKeys / 32], float* reference, float2* others,
                                              uint32_t* bits, int count, int share, Copies& start_copies, Queries& start_queries) {
   using namespace ptx;
   using C = Config<kDim, 4>;
-  constexpr int kBlocks = C::kKeys / 16;  // of eight keys, half a tile's
-  constexpr int kHalfCols = kDim / 2;
+  constexpr int kBlocks = C::kKeys / 8;  // of eight keys
   constexpr int kSlab = C::kKeys * 128, kRowSlab = 64 * 128;  // 64 columns of a tile, and of 64 rows
   constexpr float kShift = kHalf ? 10.f : 0.f;
   constexpr float kGrowth = kHalf ? 4.f : 8.f;  // fp16: 2^(10 + 4) is the largest probability
@@ -240,61 +237,69 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
   tc_fence_after();  // the base was written before the last barrier
   const uint32_t s_mem = sh.base, o_mem = sh.base + o_col(kDim);
   bool late = false;
-  auto wait = [&](uint64_t (&bars)[2], int tile) {  // by a whole warp
-    if (!late && !__all_sync(0xffffffffu, mbar_wait(&bars[tile & 1], (tile >> 1) & 1, kWaitNs))) {
+  auto wait = [&](uint64_t* bar, int phase) {  // by a whole warp
+    if (!late && !__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, kWaitNs))) {
       late = true;
       atomicOr(bits, DDTREE_ST_TIMEOUT);
     }
   };
+  auto wait_values = [&](int i) { wait(&sh.values[i % C::kStages], i / C::kStages); };
   auto stage_of = [&](int i) { return ring + (i % C::kStages) * 2 * C::kTileBytes; };
 
   if (copies_tiles(warp)) {
     for (int i = 0; i < count; ++i) {
-      // The next tile is here; its queries, where a unit starts, came with the last copies.
-      if (i > 0 && i + 1 < count && (tiles[(i + 1) % C::kRing].flags & kFirst)) asm volatile("cp.async.wait_group 0;" ::: "memory");
-      else asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 3) : "memory");
-      fence_async_smem();  // this thread's copies, before the tensor core reads them
       __syncwarp();
-      feeders_barrier();
-      // The last tile's stage is free once its O is complete, and with it this
-      // tile's queries, whose scores were issued before.
-      if (i > 0) wait(sh.values, i - 1);
-      else wait(sh.scores, 0);
-      start_queries(i + 2);
-      start_copies(i + C::kStages - 1);
+      copies_barrier();  // the tile's keys are looked up
+      if (i >= C::kStages) wait_values(i - C::kStages);
+      const Tile t = tiles[i % C::kRing];
+      if (t.flags & kFirst) {
+        if (t.unit >= 2) wait(&sh.queries[t.unit & 1], t.unit / 2 - 1);
+        start_queries(i);
+      }
+      start_copies(i);
+      cp_async_mbar_arrive(&sh.full[i % C::kStages]);
+      if ((threadIdx.x & 127) == 0) mbar_arrive(&sh.full[i % C::kStages]);  // what the lookup wrote goes along
     }
     return;
   }
 
   if (warp == kIssueWarp) {
     auto score = [&](int i) {
-      const uint32_t q_at = q_ring + (tiles[i % C::kRing].unit % C::kQSlots) * C::kQBytes, k_at = stage_of(i);
+      wait(&sh.full[i % C::kStages], i / C::kStages);
+      fence_async_smem();  // what the copies wrote, before the tensor core reads it
+      tc_fence_after();
+      if (elect_one()) {
+        const Tile t = tiles[i % C::kRing];
+        const uint32_t q_at = q_ring + (t.unit % C::kQSlots) * C::kQBytes, k_at = stage_of(i);
 #pragma unroll
-      for (int c = 0; c < kDim / 64; ++c)
-        mma_ss_x4<2, 2>(s_mem + (i & 1) * C::kKeys, desc_sw128(q_at + c * kRowSlab, 16, 1024),
-                        desc_sw128(k_at + c * kSlab, 16, 1024), product_desc(C::kKeys, false, kHalf), c > 0);
-      mma_commit(&sh.scores[i & 1]);
+        for (int c = 0; c < kDim / 64; ++c)
+          mma_ss_x4<2, 2>(s_mem + (i & 1) * C::kKeys, desc_sw128(q_at + c * kRowSlab, 16, 1024),
+                          desc_sw128(k_at + c * kSlab, 16, 1024), product_desc(C::kKeys, false, kHalf), c > 0);
+        mma_commit(&sh.scores[i & 1]);
+        if (t.flags & kLast) mma_commit(&sh.queries[t.unit & 1]);
+      }
+      __syncwarp();
     };
+    score(0);
     for (int i = 0; i < count; ++i) {
-      __syncwarp();
-      feeders_barrier();
+      if (i + 1 < count) score(i + 1);
+      asm volatile("bar.sync %0, 160;" ::"r"(2 + (i & 1)) : "memory");  // P is written and O rescaled
       tc_fence_after();
       if (elect_one()) {
-        if (i == 0) score(0);
-        if (i + 1 < count) score(i + 1);
-      }
-      __syncwarp();
-      asm volatile("bar.sync 2, 288;" ::: "memory");  // P is written and O rescaled
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t v_at = stage_of(i) + C::kTileBytes;
+        const uint32_t p_tile = p_at + (i & 1) * C::kTileP, v_at = stage_of(i) + C::kTileBytes;
         const bool more = !(tiles[i % C::kRing].flags & kFirst);
-        if constexpr (C::kKeys == 64)
-          mma_ss_x4<2, 128>(o_mem, desc_sw128(p_at, 16, 1024), desc_sw128(v_at, kSlab, 1024), product_desc(kDim, true, kHalf), more);
-        else
-          mma_ss_x2<2, 128>(o_mem, desc_sw128(p_at, 16, 1024), desc_sw128(v_at, kSlab, 1024), product_desc(kDim, true, kHalf), more);
-        mma_commit(&sh.values[i & 1]);
+        if constexpr (C::kKeys >= 64) {
+#pragma unroll
+          for (int c = 0; c < C::kKeys / 64; ++c)
+            mma_ss_x4<2, 128>(o_mem, desc_sw128(p_tile + c * kRowSlab, 16, 1024), desc_sw128(v_at + c * 64 * 128, kSlab, 1024),
+                              product_desc(kDim, true, kHalf), c > 0 || more);
+        } else {
+          mma_ss_x2<2, 128>(o_mem, desc_sw128(p_tile, 16, 1024), desc_sw128(v_at, kSlab, 1024), product_desc(kDim, true, kHalf),
+                            more);
+        }
+        mma_commit(&sh.values[i % C::kStages]);
       }
+      __syncwarp();
     }
     // Nothing is in flight once the softmax warps are through (the last tile
     // ends a unit); after an expired wait, give what is a last chance.
@@ -310,34 +315,37 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
 
   // Row 16 w + r of a product with 64 rows is lane 32 w + r of the tensor memory.
   // A thread has rows row and row + 8, keys (columns) 2 quad and 2 quad + 1 of every eight.
-  const int row = (warp & 3) * 16 + (lane >> 2), quad = lane & 3;
-  const int half = warp >> 2;  // of the tile's keys and O's columns
-  const uint32_t my_lane = (uint32_t)((warp & 3) * 32) << 16;
+  const int quarter = warp & 3, row = quarter * 16 + (lane >> 2), quad = lane & 3;
+  const int mine = warp >> 2;  // even tiles or odd ones
+  const uint32_t my_lane = (uint32_t)(quarter * 32) << 16;
   const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);  // as for fewer rows
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  auto rows_barrier = [&] {  // the two warps of the same rows
-    __syncwarp();
-    asm volatile("bar.sync %0, 64;" ::"r"(3 + (warp & 3)) : "memory");
-  };
-  for (int i = 0; i < count; ++i) {
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // as of this group's last tile
+  int unit = -1;
+  for (int i = mine; i < count; i += 2) {
     const int slot = i % C::kRing;
-    wait(sh.scores, i);
+    wait(&sh.scores[i & 1], i >> 1);
     tc_fence_after();
     const Tile t = tiles[slot];
     uint32_t x[4 * kBlocks];
-    if constexpr (kBlocks == 4) tmem_ld_frag32(s_mem + my_lane + (i & 1) * C::kKeys + half * 32, x);
-    else tmem_ld_frag16(s_mem + my_lane + (i & 1) * C::kKeys + half * 16, x);
+    const uint32_t x_mem = s_mem + my_lane + (i & 1) * C::kKeys;
+    if constexpr (kBlocks == 4) tmem_ld_frag32(x_mem, x);
+    else
+#pragma unroll
+      for (int c = 0; c < kBlocks / 8; ++c) tmem_ld_frag64(x_mem + 64 * c, reinterpret_cast<uint32_t(&)[32]>(x[32 * c]));
     if (a.scale_log2 < 0.f) {
 #pragma unroll
       for (int k = 0; k < 4 * kBlocks; ++k) x[k] ^= 0x80000000u;
     }
-    const uint32_t mask = there[slot][half * kBlocks / 4] >> (half * kBlocks * 8 % 32);
-    if (~mask << (32 - 8 * kBlocks)) {
 #pragma unroll
-      for (int k = 0; k < 4 * kBlocks; ++k)
-        if (!((mask >> (8 * (k >> 2) + 2 * quad + (k & 1))) & 1)) x[k] = 0xff800000u;  // -inf
+    for (int w = 0; w < kBlocks / 4; ++w) {
+      const uint32_t mask = there[slot][w];
+      if (mask != 0xffffffffu) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (!((mask >> (8 * (k >> 2) + 2 * quad + (k & 1))) & 1)) x[16 * w + k] = 0xff800000u;  // -inf
+      }
     }
-    float tops[2];
+    float top[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float high[2] = {-INFINITY, -INFINITY};
@@ -346,34 +354,44 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
         high[0] = fmaxf(high[0], __uint_as_float(x[4 * j + 2 * h]));
         high[1] = fmaxf(high[1], __uint_as_float(x[4 * j + 2 * h + 1]));
       }
-      tops[h] = fmaxf(high[0], high[1]);
-      tops[h] = fmaxf(tops[h], __shfl_xor_sync(0xffffffffu, tops[h], 1));
-      tops[h] = fmaxf(tops[h], __shfl_xor_sync(0xffffffffu, tops[h], 2));
-      if (quad == 0) top_s[2 * (i & 1) + half][row + 8 * h] = tops[h];
+      top[h] = fmaxf(high[0], high[1]);
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
     }
-    rows_barrier();
-    float keep[2];
+    // The reference goes from tile to tile, and so from group to group; where a
+    // unit ends, after its rows were read: the next tile's product writes over them.
+    if (i > 0) asm volatile("bar.sync %0, 64;" ::"r"(8 - 4 * mine + quarter) : "memory");
+    bool raised = false;
+    float keep[2], before[2] = {-INFINITY, -INFINITY};
+    if (!(t.flags & kFirst)) {
+      before[0] = reference[row];
+      before[1] = reference[row + 8];
+    }
+    __syncwarp();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float top = fmaxf(tops[h], top_s[2 * (i & 1) + (half ^ 1)][row + 8 * h]);
-      if (t.flags & kFirst) {
-        m[h] = -INFINITY;
-        l[h] = 0.f;
-      }
+      float now = before[h];
       keep[h] = 1.f;
-      if ((top - m[h]) * scale > kGrowth) {  // also the first finite maximum
-        keep[h] = m[h] == -INFINITY ? 0.f : power2((m[h] - top) * scale);
-        m[h] = top;
+      if ((top[h] - now) * scale > kGrowth) {  // also the first finite maximum
+        keep[h] = now == -INFINITY ? 0.f : power2((now - top[h]) * scale);
+        raised = true;
+        now = top[h];
       }
-      l[h] *= keep[h];
+      if (unit != t.unit) l[h] = 0.f;
+      else if (m[h] != now) l[h] *= m[h] == -INFINITY ? 0.f : power2((m[h] - now) * scale);
+      m[h] = now;
+      if (quad == 0) reference[row + 8 * h] = now;
     }
-    // The last product: P may be written again, and the rows of O are complete.
-    if (i > 0) wait(sh.values, i - 1);
-    if (!(t.flags & kFirst) && __any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
+    unit = t.unit;
+    __syncwarp();
+    const bool unit_ends = t.flags & kLast;
+    if (!unit_ends) asm volatile("bar.arrive %0, 64;" ::"r"(4 + 4 * mine + quarter) : "memory");
+    if (!(t.flags & kFirst) && __any_sync(0xffffffffu, raised)) {
+      wait_values(i - 1);  // the rows of O are complete
       tc_fence_after();
       uint32_t v[16];
 #pragma unroll 1
-      for (int c = half * kHalfCols; c < (half + 1) * kHalfCols; c += 32) {
+      for (int c = 0; c < kDim; c += 32) {
         tmem_ld_frag32(o_mem + my_lane + c, v);
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * keep[(e >> 1) & 1]);
@@ -381,51 +399,60 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
       }
       tmem_st_wait();
     }
+    if (i > 1) wait_values(i - 2);  // these probabilities' place is free
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float base = m[h] == -INFINITY ? 0.f : kShift - m[h] * scale;
-      const uint32_t p_row = p_at + (row + 8 * h) * 128 + 4 * quad;
+      const uint32_t p_row = p_at + mine * C::kTileP + (row + 8 * h) * 128 + 4 * quad;
       float sums[2] = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < kBlocks; ++j) {
         const float u = power2(fmaf(__uint_as_float(x[4 * j + 2 * h]), scale, base));
         const float w = power2(fmaf(__uint_as_float(x[4 * j + 2 * h + 1]), scale, base));
         sums[j & 1] += u + w;
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(p_row + (((half * kBlocks + j) ^ (row & 7)) << 4)), "r"(pack2<kHalf>(u, w)) : "memory");
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(p_row + (j >> 3) * kRowSlab + (((j & 7) ^ (row & 7)) << 4)),
+                     "r"(pack2<kHalf>(u, w))
+                     : "memory");
       }
       l[h] += sums[0] + sums[1];
+    }
+    float total[2] = {l[0], l[1]};
+    if (t.flags & (kLast | kNextLast)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        total[h] += __shfl_xor_sync(0xffffffffu, total[h], 1);
+        total[h] += __shfl_xor_sync(0xffffffffu, total[h], 2);
+        // For the group that ends the unit: this one's sum and its reference.
+        if (!unit_ends && quad == 0) others[row + 8 * h] = make_float2(total[h], m[h]);
+      }
     }
     fence_async_smem();
     tc_fence_before();
     __syncwarp();
-    // A warp cannot be here again before the others were: it waits for the values.
-    if (late) asm volatile("bar.sync 2, 288;" ::: "memory");
-    else asm volatile("bar.arrive 2, 288;" ::: "memory");
-    if (!(t.flags & kLast)) continue;
+    // A warp cannot be here again before the others of its group were: it waits for the values.
+    if (late) asm volatile("bar.sync %0, 160;" ::"r"(2 + mine) : "memory");
+    else asm volatile("bar.arrive %0, 160;" ::"r"(2 + mine) : "memory");
+    if (!unit_ends) continue;
 
-    // ---- the unit ends here
-    wait(sh.values, i);
+    // ---- the unit ends here; the product before this tile's came after the other group's sums
+    wait_values(i);
     tc_fence_after();
     const bool whole = !(t.flags & (kBegun | kGoesOn));
     const int64_t part = 2 * share + (t.flags & kBegun ? 0 : 1);
     const int head = t.kv_head * a.group + row;
-    float total[2], inv[2];
+    float inv[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      total[h] = l[h] + __shfl_xor_sync(0xffffffffu, l[h], 1);
-      total[h] += __shfl_xor_sync(0xffffffffu, total[h], 2);
-      if (quad == 0) sum_s[half][row + 8 * h] = total[h];
-    }
-    rows_barrier();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      total[h] = sum_s[0][row + 8 * h] + sum_s[1][row + 8 * h];
+      if (!(t.flags & kFirst)) {
+        const float2 other = others[row + 8 * h];
+        if (other.x != 0.f) total[h] += other.x * power2((other.y - m[h]) * scale);
+      }
       inv[h] = total[h] == 0.f ? 0.f : 1.f / total[h];
     }
     uint16_t* out = a.out + t.token * a.out_stride + (int64_t)head * kDim + 2 * quad;
     float* rows = reinterpret_cast<float*>(a.ws + ws.rows) + (part * C::kRows + row) * kDim + 2 * quad;
 #pragma unroll 1
-    for (int c = half * kHalfCols; c < (half + 1) * kHalfCols; c += 32) {
+    for (int c = 0; c < kDim; c += 32) {
       uint32_t v[16];
       tmem_ld_frag32(o_mem + my_lane + c, v);  // the whole warp; the rows that count are stored
 #pragma unroll
@@ -444,7 +471,7 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
     tc_fence_before();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (row + 8 * h < a.group && quad == 0 && half == 0) {
+      if (row + 8 * h < a.group && quad == 0) {
         const float top = m[h] == -INFINITY ? m[h] : m[h] * scale;
         if (!whole) reinterpret_cast<float2*>(a.ws + ws.sums)[part * C::kRows + row + 8 * h] = make_float2(top, total[h]);
         else if (a.lse)
@@ -452,6 +479,8 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
               total[h] == 0.f ? -INFINITY : (top - kShift + log2f(total[h])) * 0.6931471805599453f;
       }
     }
+    __syncwarp();
+    if (i + 1 < count) asm volatile("bar.arrive %0, 64;" ::"r"(4 + 4 * mine + quarter) : "memory");
   }
   tc_fence_before();
 }
@@ -466,7 +495,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   __shared__ int64_t offsets[C::kRing][C::kKeys];   // element offset of a key's row
   __shared__ uint32_t there[C::kRing][C::kKeys / 32];  // a bit per key that exists
   __shared__ Tile tiles[C::kRing];
-  __shared__ float top_s[C::kTensor ? 4 : C::kWK][C::kRows], sum_s[C::kWK][C::kRows];  // kTensor: maxima of even and odd tiles
+  __shared__ __align__(8) float top_s[C::kWK][C::kRows], sum_s[C::kWK][C::kRows];  // kTensor: one maximum, one (sum, maximum)
   __shared__ int64_t warp_sum[C::kAllThreads / 32];
   __shared__ int start_token;
   __shared__ int64_t start_at;
@@ -555,9 +584,8 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     }
   };
   fetch_next();
-  auto look_up = [&](int i) {
-    const int slot = i % C::kRing;
-    int page[kPerLane], in[kPerLane];
+  int page[kPerLane], in[kPerLane];
+  auto load_pages = [&] {  // of the current tile
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
       const int64_t x = (int64_t)tile * C::kKeys + 32 * k + lane;
@@ -570,6 +598,10 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
         page[k] = __ldg(a.table + (int64_t)tok.row * a.table_stride + number);
       }
     }
+  };
+  // The next tile's page numbers are loaded as a tile is done.
+  auto look_up = [&](int i) {
+    const int slot = i % C::kRing;
     const bool unit_ends = tile + 1 == tok.tiles, range_ends = i + 1 == count;
     if (lane == 0) {
       Tile t;
@@ -578,6 +610,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       t.unit = unit;
       t.flags = (tile == 0 || i == 0 ? kFirst : 0) | (unit_ends || range_ends ? kLast : 0) | (begun ? kBegun : 0) |
                 (unit_ends ? 0 : kGoesOn);
+      if (C::kTensor && !unit_ends && !range_ends && (tile + 2 == tok.tiles || i + 2 == count)) t.flags |= kNextLast;
       tiles[slot] = t;
       if (tok.seen == 0) atomicOr(&bits, DDTREE_ST_BAD_LENGTH);
       // The unit's record, where it starts; without units' own, the share's, where the share ends.
@@ -617,12 +650,17 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     } else {
       ++tile;
     }
+    if (!range_ends) load_pages();
   };
   if constexpr (C::kTensor) {
     if (tid == 0) {
+      for (int k = 0; k < C::kStages; ++k) {
+        ptx::mbar_init(&tensor.full[k], C::kCopyThreads + 1);
+        ptx::mbar_init(&tensor.values[k], 1);
+      }
       for (int k = 0; k < 2; ++k) {
         ptx::mbar_init(&tensor.scores[k], 1);
-        ptx::mbar_init(&tensor.values[k], 1);
+        ptx::mbar_init(&tensor.queries[k], 1);
       }
       ptx::fence_mbar_init();
     }
@@ -632,13 +670,22 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     }
   }
   if (warp == kWarps) {
-    for (int i = 0; i < C::kStages && i < count; ++i) look_up(i);
-    __syncthreads();
-    for (int i = 0; i < count; ++i) {
-      // Tile i's slot is in use, the one of tile i + kStages free.
-      if constexpr (C::kTensor) feeders_barrier();
-      else __syncthreads();
-      if (i + C::kStages < count) look_up(i + C::kStages);
+    load_pages();
+    if constexpr (C::kTensor) {
+      __syncthreads();
+      look_up(0);
+      for (int i = 0; i < count; ++i) {
+        __syncwarp();
+        copies_barrier();  // tile i's copies start; those of tile i - kStages are used up but for one
+        if (i + 1 < count) look_up(i + 1);
+      }
+    } else {
+      for (int i = 0; i < C::kStages && i < count; ++i) look_up(i);
+      __syncthreads();
+      for (int i = 0; i < count; ++i) {
+        __syncthreads();  // tile i's slot is in use, the one of tile i + kStages free
+        if (i + C::kStages < count) look_up(i + C::kStages);
+      }
     }
     __syncthreads();
     if (lane == 0) words[share] = bits;
@@ -654,7 +701,8 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     if constexpr (C::kTensor) return (uint32_t)((chunk >> 3) * rows * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
     else return (uint32_t)(row * C::kRowBytes + ((chunk ^ (row & 7)) << 4));
   };
-  // Starts the copies of tile i (every thread commits a group, empty or not).
+  // Starts the copies of tile i (kTensor: the barrier follows; else every thread
+  // commits a group, empty or not).
   // A thread copies one chunk of every kRowsPerStep-th row: the swizzle of its
   // rows is the same, so shared addresses advance by a constant (steps of four
   // rows: the third bit of the row alternates).
@@ -701,21 +749,17 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       }
       if constexpr (!C::kTensor) start_queries(i);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    if constexpr (!C::kTensor) asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   __syncthreads();
-  if (!C::kTensor || copies_tiles(warp)) {
-    if constexpr (C::kTensor) {
-      start_queries(0);
-      start_queries(1);
-    }
+  if constexpr (!C::kTensor) {
 #pragma unroll 1
     for (int i = 0; i < C::kStages - 1; ++i) start_copies(i);
   }
 
   if constexpr (C::kTensor) {
-    tensor_tiles<kHalf, kDim>(a, ws, tensor, p_at, q_ring, ring, tiles, there, top_s, sum_s, &bits, count, share, start_copies,
+    tensor_tiles<kHalf, kDim>(a, ws, tensor, p_at, q_ring, ring, tiles, there, &top_s[0][0], reinterpret_cast<float2*>(&sum_s[0][0]), &bits, count, share, start_copies,
                               start_queries);
   } else {
     auto computing_warps = [] { asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads) : "memory"); };
@@ -1080,7 +1124,7 @@ cudaError_t launch(const DraftAttnArgs& a, cudaStream_t stream) {
 template <bool kHalf, int kDim>
 cudaError_t launch_rows(const DraftAttnArgs& a, cudaStream_t stream) {
   if (a.row_tile == 16) return launch<kHalf, kDim, 1>(a, stream);
-  if constexpr (kDim != 128) {
+  if constexpr (kDim == 64) {
     if (a.row_tile == 32) return launch<kHalf, kDim, 2>(a, stream);
   }
   return launch<kHalf, kDim, 4>(a, stream);
@@ -1095,7 +1139,7 @@ cudaError_t launch_dim(const DraftAttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int draft_row_tile(int group, int head_dim) { return group <= 16 ? 16 : group <= 32 && head_dim != 128 ? 32 : 64; }
+int draft_row_tile(int group, int head_dim) { return group <= 16 ? 16 : group <= 32 && head_dim == 64 ? 32 : 64; }
 
 int draft_tile_keys(int row_tile, int head_dim) { return keys_of(row_tile, head_dim); }
 

@@ -55,9 +55,10 @@ def test_plans(lib):
     for h, tile in ((2, 16), (32, 16), (34, 32), (64, 32), (66, 64), (128, 64)):
         assert make(h=h) == 0 and plan.row_tile == tile and plan.n_heads == h
         assert B.ddtree_draft_attention_workspace_size(plan) == plan.workspace_bytes and plan.workspace_bytes % 256 == 0
-    wide = _cache(n_kv_heads=2, head_dim=128, head_stride=128, token_stride=256, page_stride=16 * 256)
-    for h, tile in ((32, 16), (34, 64), (128, 64)):
-        assert make(h=h, cache=wide) == 0 and plan.row_tile == tile
+    for dim in (128, 256):
+        wide = _cache(n_kv_heads=2, head_dim=dim, head_stride=dim, token_stride=2 * dim, page_stride=32 * dim)
+        for h, tile in ((32, 16), (34, 64), (128, 64)):
+            assert make(h=h, cache=wide) == 0 and plan.row_tile == tile
     assert make(n=4096) == 0 and make(sinks=2 ** 31 - 1, window=1) == 0
     for bad in (dict(n=0), dict(n=4097), dict(h=0), dict(h=7), dict(h=130), dict(cache=None), dict(window=-1), dict(sinks=-1),
                 dict(sms=-1), dict(sms=4097)):
