@@ -40,7 +40,7 @@
 // requests of 511 to 16k, 8 heads of 64 columns, 92 us (6.3 TB/s); a
 // window of 2,048 at 65k 7.8 us, a chain of dependent steps (positions, page
 // numbers, keys, product, join) with almost no bytes.  64 heads a group stream
-// 5.2, 6.2 and 5.3 TB/s at 64, 128 and 256 columns.  Token-granular pages of 64
+// 5.4, 6.2 and 5.3 TB/s at 64, 128 and 256 columns.  Token-granular pages of 64
 // columns, 128 bytes at scattered places, stream 5.2 TB/s.
 #include <atomic>
 
@@ -62,8 +62,8 @@ struct Config {
   // memory (tensor_tiles): in registers every tile of 16 rows loads the keys'
   // fragments for itself, which 64 rows of 128 columns pay with shared memory's
   // whole bandwidth.  us per GB (256 columns: per 537 MB), registers and tensor
-  // memory: 64 rows of 64, 128, 256 columns 259, 269, 198 and 208, 173, 101; 24
-  // rows 181, 204, 114 and 205, 167, 97.
+  // memory: 64 rows of 64, 128, 256 columns 259, 269, 198 and 198, 173, 101; 24
+  // rows 181, 204, 114 and 195, 167, 96.
   static constexpr bool kTensor = kWM == 4;
   static_assert(kWM != 2 || kDim == 64, "see draft_row_tile");
   static constexpr int kKeys = keys_of(16 * kWM, kDim);     // keys of a tile
@@ -85,6 +85,7 @@ struct Config {
   static constexpr int kStages = kTensor ? (kDim == 256 ? 4 : 5) : kWM == 1 ? 3 : 2;
   static constexpr int kQSlots = kTensor ? 2 : kStages;     // units whose queries are held
   static constexpr int kRing = kTensor ? 8 : 4;             // offset slots: the tile in use, those in flight, and the next
+  static constexpr int kTileRing = kTensor ? 16 : kRing;    // its tiles, begun one ahead of the offsets
   static constexpr int kCopyThreads = kTensor ? 128 : kThreads;
   // Shared memory: probabilities (kTensor), queries, tiles.
   static constexpr int kTileP = kRows * 128 * (kKeys > 64 ? 2 : 1), kPBytes = kTensor ? 2 * kTileP : 0;
@@ -193,7 +194,9 @@ enum { kFirst = 1, kLast = 2, kBegun = 4, kGoesOn = 8, kNextLast = 16 };
 // ends, and leaves P in shared memory in the cache's type.
 // Barriers of stages, tiles and units tie the roles together, so each runs ahead
 // as far as its buffers go: copies by the ring's stages, scores by one tile,
-// queries by one unit.
+// queries by one unit.  What a tile costs now is its copies (32 KB of 16-byte
+// copies take an SM some 1,300 of 1,530 cycles at 128 columns), at 64 columns the
+// way from scores to product (1,750), at 256 the 18 products (1,740).
 // One elected thread of the converged warp issues: with a thread chosen by its
 // lane the descriptors go through vector registers, and a product of 16 columns
 // of K took 100 cycles to issue instead of 35.
@@ -251,7 +254,7 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
       __syncwarp();
       copies_barrier();  // the tile's keys are looked up
       if (i >= C::kStages) wait_values(i - C::kStages);
-      const Tile t = tiles[i % C::kRing];
+      const Tile t = tiles[i % C::kTileRing];
       if (t.flags & kFirst) {
         if (t.unit >= 2) wait(&sh.queries[t.unit & 1], t.unit / 2 - 1);
         start_queries(i);
@@ -269,7 +272,7 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
       fence_async_smem();  // what the copies wrote, before the tensor core reads it
       tc_fence_after();
       if (elect_one()) {
-        const Tile t = tiles[i % C::kRing];
+        const Tile t = tiles[i % C::kTileRing];
         const uint32_t q_at = q_ring + (t.unit % C::kQSlots) * C::kQBytes, k_at = stage_of(i);
 #pragma unroll
         for (int c = 0; c < kDim / 64; ++c)
@@ -287,7 +290,7 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
       tc_fence_after();
       if (elect_one()) {
         const uint32_t p_tile = p_at + (i & 1) * C::kTileP, v_at = stage_of(i) + C::kTileBytes;
-        const bool more = !(tiles[i % C::kRing].flags & kFirst);
+        const bool more = !(tiles[i % C::kTileRing].flags & kFirst);
         if constexpr (C::kKeys >= 64) {
 #pragma unroll
           for (int c = 0; c < C::kKeys / 64; ++c)
@@ -325,7 +328,7 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
     const int slot = i % C::kRing;
     wait(&sh.scores[i & 1], i >> 1);
     tc_fence_after();
-    const Tile t = tiles[slot];
+    const Tile t = tiles[i % C::kTileRing];
     uint32_t x[4 * kBlocks];
     const uint32_t x_mem = s_mem + my_lane + (i & 1) * C::kKeys;
     if constexpr (kBlocks == 4) tmem_ld_frag32(x_mem, x);
@@ -494,7 +497,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t offsets[C::kRing][C::kKeys];   // element offset of a key's row
   __shared__ uint32_t there[C::kRing][C::kKeys / 32];  // a bit per key that exists
-  __shared__ Tile tiles[C::kRing];
+  __shared__ Tile tiles[C::kTileRing];
   __shared__ __align__(8) float top_s[C::kWK][C::kRows], sum_s[C::kWK][C::kRows];  // kTensor: one maximum, one (sum, maximum)
   __shared__ int64_t warp_sum[C::kAllThreads / 32];
   __shared__ int start_token;
@@ -584,24 +587,24 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     }
   };
   fetch_next();
-  int page[kPerLane], in[kPerLane];
-  auto load_pages = [&] {  // of the current tile
+  // A tile in two steps, so that the page numbers can be under way meanwhile.
+  struct Pages {
+    int page[kPerLane];
+    int64_t at[kPerLane];  // of the key's row in its page
+  };
+  auto begin_tile = [&](int i, Pages& p) {
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
       const int64_t x = (int64_t)tile * C::kKeys + 32 * k + lane;
-      page[k] = -2;  // no such key
-      in[k] = 0;
+      p.page[k] = -2;  // no such key
+      p.at[k] = 0;
       if (x < tok.seen) {
         const int j = (int)(x < tok.first ? x : x - tok.first + tok.lo);
         const int number = a.page.quotient(j);
-        in[k] = j - number * a.page_size;
-        page[k] = __ldg(a.table + (int64_t)tok.row * a.table_stride + number);
+        p.at[k] = (j - number * a.page_size) * a.token_stride + kv_head * a.head_stride;
+        p.page[k] = __ldg(a.table + (int64_t)tok.row * a.table_stride + number);
       }
     }
-  };
-  // The next tile's page numbers are loaded as a tile is done.
-  auto look_up = [&](int i) {
-    const int slot = i % C::kRing;
     const bool unit_ends = tile + 1 == tok.tiles, range_ends = i + 1 == count;
     if (lane == 0) {
       Tile t;
@@ -611,7 +614,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       t.flags = (tile == 0 || i == 0 ? kFirst : 0) | (unit_ends || range_ends ? kLast : 0) | (begun ? kBegun : 0) |
                 (unit_ends ? 0 : kGoesOn);
       if (C::kTensor && !unit_ends && !range_ends && (tile + 2 == tok.tiles || i + 2 == count)) t.flags |= kNextLast;
-      tiles[slot] = t;
+      tiles[i % C::kTileRing] = t;
       if (tok.seen == 0) atomicOr(&bits, DDTREE_ST_BAD_LENGTH);
       // The unit's record, where it starts; without units' own, the share's, where the share ends.
       const bool goes_on = range_ends && !unit_ends && !begun;
@@ -625,14 +628,6 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
         r.last_share = (int)(last < in_longer ? last / (base + 1) : longer + (last - in_longer) / base) * (1 << a.bundle_log2) + sub;
         records[unit_records ? cur * a.n_kv_heads + kv_head : share] = r;
       }
-    }
-#pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-      const bool good = page[k] >= 0 && page[k] < a.n_pages;
-      if (page[k] != -2 && !good) atomicOr(&bits, DDTREE_ST_BAD_INDEX);
-      offsets[slot][32 * k + lane] = good ? page[k] * a.page_stride + in[k] * a.token_stride + kv_head * a.head_stride : 0;
-      const uint32_t have = __ballot_sync(0xffffffffu, good);
-      if (lane == 0) there[slot][k] = have;
     }
     if (unit_ends && !range_ends) {
       tile = 0;
@@ -650,7 +645,17 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     } else {
       ++tile;
     }
-    if (!range_ends) load_pages();
+  };
+  auto end_tile = [&](int i, const Pages& p) {
+    const int slot = i % C::kRing;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const bool good = p.page[k] >= 0 && p.page[k] < a.n_pages;
+      if (p.page[k] != -2 && !good) atomicOr(&bits, DDTREE_ST_BAD_INDEX);
+      offsets[slot][32 * k + lane] = good ? p.page[k] * a.page_stride + p.at[k] : 0;
+      const uint32_t have = __ballot_sync(0xffffffffu, good);
+      if (lane == 0) there[slot][k] = have;
+    }
   };
   if constexpr (C::kTensor) {
     if (tid == 0) {
@@ -670,16 +675,31 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     }
   }
   if (warp == kWarps) {
-    load_pages();
+    Pages even, odd;
     if constexpr (C::kTensor) {
-      __syncthreads();
-      look_up(0);
-      for (int i = 0; i < count; ++i) {
+      // Page numbers are loaded two tiles ahead of the copies: beside those a
+      // load takes some 1,000 cycles, about what a tile has (64 rows of 64 columns
+      // 206 -> 198 us per GB; four of 131k on pages of one token, 128 columns, 60
+      // -> 56; 64 requests of 512 keys 0.5 us slower).
+      auto step = [&](int i, Pages& mine, Pages& other) {
         __syncwarp();
-        copies_barrier();  // tile i's copies start; those of tile i - kStages are used up but for one
-        if (i + 1 < count) look_up(i + 1);
+        copies_barrier();  // the copies of tile i start; at most kStages + 1 tiles before it are in use
+        if (i + 2 < count) begin_tile(i + 2, mine);
+        if (i + 1 < count) end_tile(i + 1, other);
+      };
+      __syncthreads();
+      begin_tile(0, even);
+      if (count > 1) begin_tile(1, odd);
+      end_tile(0, even);
+      for (int i = 0; i < count; i += 2) {
+        step(i, even, odd);
+        if (i + 1 < count) step(i + 1, odd, even);
       }
     } else {
+      auto look_up = [&](int i) {
+        begin_tile(i, even);
+        end_tile(i, even);
+      };
       for (int i = 0; i < C::kStages && i < count; ++i) look_up(i);
       __syncthreads();
       for (int i = 0; i < count; ++i) {
@@ -714,7 +734,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   const uint16_t *copy_k = a.k + 8 * copy_chunk, *copy_v = a.v + 8 * copy_chunk;
   auto start_queries = [&](int i) {
     if (i >= count) return;
-    const Tile t = tiles[i % C::kRing];
+    const Tile t = tiles[i % C::kTileRing];
     if (!(t.flags & kFirst)) return;
     const uint32_t q_at = q_ring + (t.unit % C::kQSlots) * C::kQBytes;
     const uint16_t* q = a.q + t.token * a.q_stride + (int64_t)t.kv_head * a.group * kDim;
@@ -798,7 +818,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       __syncthreads();
       start_copies(i + C::kStages - 1);
       const int slot = i % C::kRing;
-      const Tile t = tiles[slot];
+      const Tile t = tiles[i % C::kTileRing];
       const uint32_t k_at = ring + (i % C::kStages) * 2 * C::kTileBytes, v_at = k_at + C::kTileBytes;
       const uint32_t q_at = q_ring + (t.unit % C::kStages) * C::kQBytes;
       if (t.flags & kFirst) {
