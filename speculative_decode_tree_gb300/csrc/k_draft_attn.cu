@@ -596,8 +596,8 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
       const int64_t x = (int64_t)tile * C::kKeys + 32 * k + lane;
-      p.page[k] = -2;  // no such key
-      p.at[k] = 0;
+      p.page[k] = -1;
+      p.at[k] = -1;  // no such key
       if (x < tok.seen) {
         const int j = (int)(x < tok.first ? x : x - tok.first + tok.lo);
         const int number = a.page.quotient(j);
@@ -651,7 +651,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
       const bool good = p.page[k] >= 0 && p.page[k] < a.n_pages;
-      if (p.page[k] != -2 && !good) atomicOr(&bits, DDTREE_ST_BAD_INDEX);
+      if (p.at[k] >= 0 && !good) atomicOr(&bits, DDTREE_ST_BAD_INDEX);
       offsets[slot][32 * k + lane] = good ? p.page[k] * a.page_stride + p.at[k] : 0;
       const uint32_t have = __ballot_sync(0xffffffffu, good);
       if (lane == 0) there[slot][k] = have;

@@ -320,3 +320,12 @@ def test_python_refusals():
         a[i] = bad
         with pytest.raises((TypeError, ValueError)):
             B.ddtree_draft_attention(*a, **c.kw)
+
+
+@pytest.mark.parametrize("heads,kvh,dim", [(8, 2, 64), (66, 2, 64), (40, 1, 128), (64, 1, 256)])
+@pytest.mark.parametrize("entry", [-2, -2 ** 31, 2 ** 31 - 1])
+def test_every_table_entry_outside_the_cache_is_reported(entry, heads, kvh, dim):
+    c = Case([100, 50, 20], heads, kvh, dim, seed=45)
+    c.table[c.token_rows[0], 2] = entry
+    assert c.run() == B.DDTREE_ST_BAD_INDEX
+    c.compare()
