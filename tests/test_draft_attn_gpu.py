@@ -329,3 +329,79 @@ def test_every_table_entry_outside_the_cache_is_reported(entry, heads, kvh, dim)
     c.table[c.token_rows[0], 2] = entry
     assert c.run() == B.DDTREE_ST_BAD_INDEX
     c.compare()
+
+
+WIDE = [(d, t) for d in (64, 128, 256) for t in (torch.bfloat16, torch.float16)]
+
+
+@pytest.mark.parametrize("dim,dtype", WIDE)
+def test_wide_groups_over_many_tiles_a_share(dim, dtype):
+    # 20 to 40 tiles a share: every ring of the kernel goes round more than once.
+    n = {64: 50000, 128: 25000, 256: 15000}[dim]
+    _check([n, n - 77, 3], 4 * 33, 4, dim, dtype=dtype, seed=46)
+
+
+@pytest.mark.parametrize("dim,dtype", WIDE)
+def test_wide_groups_of_many_short_requests(dim, dtype):
+    r = random.Random(47)
+    _check([r.choice([0, -1, 31, 32, 63, 64, 127, 128, r.randint(0, 300)]) for _ in range(331)], 66, 2, dim, dtype=dtype, seed=47)
+    _check([3000] + [r.randint(0, 70) for _ in range(90)], 40, 1, dim, dtype=dtype, page=1, seed=48)
+
+
+@pytest.mark.parametrize("dim,dtype", WIDE)
+@pytest.mark.parametrize("page,window,sinks", [(1, 1, 0), (3, 100, 70), (16, 1000, 33), (64, 64, 4), (16, 7, 2 ** 31 - 1)])
+def test_wide_groups_with_windows(page, window, sinks, dim, dtype):
+    _check([0, 3, 99, 640, 2049], 40, 1, dim, dtype=dtype, page=page, window=window, sinks=sinks, heads_first=page == 16, seed=49)
+
+
+@pytest.mark.parametrize("dim,dtype", WIDE)
+@pytest.mark.parametrize("step", [0.05, -0.05, 0.004])
+def test_wide_groups_whose_scores_rise_or_fall_along_the_keys(step, dim, dtype):
+    c = Case([2500, 140], 33, 1, dim, dtype=dtype, page=16, freed=False, seed=50, scale=1.0)
+    c.q.zero_(), c.k_raw.zero_()
+    c.q[:, :, 0] = 4.0
+    c.q_dev.copy_(c.q)
+    for p, row in zip(c.positions, c.token_rows):
+        for j in range(p + 1):
+            c.k_raw[c.table[row, j // 16], j % 16, 0, 0] = step * j
+    assert c.run() == 0
+    c.compare()
+
+
+@pytest.mark.parametrize("dim,dtype", WIDE)
+def test_wide_groups_with_other_scales_strides_and_padding(dim, dtype):
+    _check([300, -1, 500], 40, 1, dim, dtype=dtype, wide=True, seed=51)
+    _check([300, 500], 66, 2, dim, dtype=dtype, q_scale=30.0, seed=52)
+    _check([300, 500], 40, 1, dim, dtype=dtype, scale=-0.2, seed=53)
+    _check([300, 500], 40, 1, dim, dtype=dtype, scale=0.0, seed=54)
+    c = Case([100, 50, 20, 77], 40, 1, dim, dtype=dtype, seed=55)
+    c.positions[3] = 16 * c.table.shape[1]
+    c.table[c.token_rows[2], :] = -7      # nothing left to see
+    assert c.run() == B.DDTREE_ST_BAD_INDEX | B.DDTREE_ST_BAD_LENGTH
+    c.compare()
+    assert bool((c.out[2:] == 0).all())
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_wide_groups_see_nothing_else_and_replay_equal_bits(dim):
+    base = Case([100, 37, 4000], 34, 1, dim, window=64, sinks=3, freed=False, seed=56)
+    assert base.run() == 0
+    base.compare()
+    c = Case([100, 37, 4000], 34, 1, dim, window=64, sinks=3, freed=False, seed=56)
+    keep = torch.zeros(c.k_raw.shape[:2], dtype=torch.bool)
+    for p, row in zip(c.positions, c.token_rows):
+        for j in range(p + 1):
+            if j > p - 64 or j < 3:
+                keep[c.table[row, j // 16], j % 16] = True
+    c.k_raw[~keep], c.v_raw[~keep] = float("nan"), float("inf")
+    assert c.run() == 0
+    assert torch.equal(c.out, base.out) and torch.equal(c.lse, base.lse)
+    bound = B.BoundDraftAttention(*c.args, **c.kw)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            bound()
+    c.out.zero_(), c.lse.zero_(), c.ws.fill_(0x3C)
+    g.replay(), g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, base.out) and torch.equal(c.lse, base.lse)
