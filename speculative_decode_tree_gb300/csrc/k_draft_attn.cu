@@ -94,10 +94,8 @@ struct Config {
   static constexpr int kUsed = kPBytes + kQSlots * kQBytes + kStages * 2 * kTileBytes;
   static constexpr int kSmem = (kTensor ? 1024 : 0) + kUsed;
   static_assert(kQAt + kQSlots * kQBytes <= kUsed && kRingAt + kStages * 2 * kTileBytes <= kUsed, "shared memory");
-  // Columns joined at a time: the rows of all key parts fit the stage they replace.
-  static constexpr int kRounds = kWK * kRows * kDim * 4 <= 2 * kTileBytes ? 1 : 2;
-  static constexpr int kRoundCols = kDim / kRounds;
-  static_assert(kTensor || kWK * kRows * kRoundCols * 4 <= 2 * kTileBytes, "merge buffer");
+  // The rows of all key parts are joined in the stage that they replace.
+  static_assert(kTensor || kWK * kRows * kDim * 4 <= 2 * kTileBytes, "merge buffer");
   static_assert(kRing >= kStages + (kTensor ? 3 : 1), "offset ring");
 };
 
@@ -791,7 +789,6 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     constexpr int kCols = kDim / C::kWN;              // columns of a warp
     // Query fragments in registers for the whole unit, or read again per tile.
     constexpr bool kHoldQ = kDim <= 128;
-    const bool idle = wm * 16 >= a.group;  // rows of the tile that no head fills
     uint32_t qf[kHoldQ ? kDim / 16 : 1][4];
     float o[kCols / 8][4], top[2], sum[2];
     // Probabilities meet V in the cache's type.  fp16 holds nothing below 2^-24,
@@ -832,7 +829,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
         sum[0] = sum[1] = 0.f;
       }
 #pragma unroll 1
-      for (int block = 0; block < (idle ? 0 : kWarpKeys); block += kBlock) {
+      for (int block = 0; block < kWarpKeys; block += kBlock) {
         const int key0 = wk * kWarpKeys + block;
         const uint32_t k_blk = k_at + block * C::kRowBytes, v_blk = v_at + block * C::kRowBytes;
         float s[kBlock / 8][4];
@@ -921,7 +918,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
       computing_warps();  // every warp is done with the tile
       float* rows = reinterpret_cast<float*>(smem + (i % C::kStages) * 2 * C::kTileBytes);
       // Row r of key part w; the exchange of column groups keeps the four rows that lanes write at once on other banks.
-      auto cell = [&](int w, int r, int col) { return rows + (w * C::kRows + r) * C::kRoundCols + (col ^ ((r & 3) << 3)); };
+      auto cell = [&](int w, int r, int col) { return rows + (w * C::kRows + r) * kDim + (col ^ ((r & 3) << 3)); };
       const int g = lane >> 2;
       const bool whole = !(t.flags & (kBegun | kGoesOn));
       const int64_t part = 2 * share + (t.flags & kBegun ? 0 : 1);
@@ -936,64 +933,58 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
         }
       }
 #pragma unroll
-      for (int round = 0; round < C::kRounds; ++round) {
-        const int col0 = round * C::kRoundCols;
-        if (round > 0) computing_warps();
+      for (int r = 0; r < 2; ++r) {
+        const int row = wm * 16 + g + 8 * r;
+        if (row >= a.group) continue;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = wm * 16 + g + 8 * r;
-          if (row >= a.group) continue;
+        for (int d = 0; d < kCols / 8; ++d) {
+          const int col = wn * kCols + 8 * d;
+          *reinterpret_cast<float2*>(cell(wk, row, col + 2 * (lane & 3))) = make_float2(o[d][2 * r], o[d][2 * r + 1]);
+        }
+      }
+      computing_warps();
+      // Columns of a thread: few where many threads share a small group's rows
+      // (185k single 69.3 -> 67.1 us with four of 256; with 128 threads four
+      // spill where eight do not: 1024 requests of 100 keys 109 us instead of 92).
+      constexpr int kVec = kThreads == 128 ? 8 : 4;
+      for (int e = tid; e < a.group * (kDim / kVec); e += kThreads) {
+        const int row = e / (kDim / kVec), col = (e - row * (kDim / kVec)) * kVec;
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-          for (int d = 0; d < kCols / 8; ++d) {
-            const int col = wn * kCols + 8 * d - col0;
-            if (C::kRounds == 1 || (col >= 0 && col < C::kRoundCols))
-              *reinterpret_cast<float2*>(cell(wk, row, col + 2 * (lane & 3))) = make_float2(o[d][2 * r], o[d][2 * r + 1]);
+        for (int k = 0; k < C::kWK; ++k) m = fmaxf(m, top_s[k][row]);
+        const float from = m == -INFINITY ? 0.f : m;
+        float4 x[kVec / 4];
+#pragma unroll
+        for (int q = 0; q < kVec / 4; ++q) x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < C::kWK; ++k) {
+          const float w = power2(top_s[k][row] - from);
+          l += w * sum_s[k][row];
+#pragma unroll
+          for (int q = 0; q < kVec / 4; ++q) {
+            const float4 u = *reinterpret_cast<const float4*>(cell(k, row, col + 4 * q));
+            x[q].x += w * u.x; x[q].y += w * u.y; x[q].z += w * u.z; x[q].w += w * u.w;
           }
         }
-        computing_warps();
-        // Columns of a thread: few where many threads share a small group's rows
-        // (185k single 69.3 -> 67.1 us with four of 256; with 128 threads four
-        // spill where eight do not: 1024 requests of 100 keys 109 us instead of 92).
-        constexpr int kVec = kThreads == 128 ? 8 : 4;
-        for (int e = tid; e < a.group * (C::kRoundCols / kVec); e += kThreads) {
-          const int row = e / (C::kRoundCols / kVec), at = (e - row * (C::kRoundCols / kVec)) * kVec, col = col0 + at;
-          float m = -INFINITY, l = 0.f;
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int head = t.kv_head * a.group + row;
+          uint32_t packed[kVec / 2];
 #pragma unroll
-          for (int k = 0; k < C::kWK; ++k) m = fmaxf(m, top_s[k][row]);
-          const float from = m == -INFINITY ? 0.f : m;
-          float4 x[kVec / 4];
-#pragma unroll
-          for (int q = 0; q < kVec / 4; ++q) x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < C::kWK; ++k) {
-            const float w = power2(top_s[k][row] - from);
-            l += w * sum_s[k][row];
-#pragma unroll
-            for (int q = 0; q < kVec / 4; ++q) {
-              const float4 u = *reinterpret_cast<const float4*>(cell(k, row, at + 4 * q));
-              x[q].x += w * u.x; x[q].y += w * u.y; x[q].z += w * u.z; x[q].w += w * u.w;
-            }
+          for (int q = 0; q < kVec / 4; ++q) {
+            packed[2 * q] = pack2<kHalf>(x[q].x * inv, x[q].y * inv);
+            packed[2 * q + 1] = pack2<kHalf>(x[q].z * inv, x[q].w * inv);
           }
-          if (whole) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int head = t.kv_head * a.group + row;
-            uint32_t packed[kVec / 2];
+          uint16_t* to = a.out + t.token * a.out_stride + (int64_t)head * kDim + col;
+          if constexpr (kVec == 8) *reinterpret_cast<uint4*>(to) = make_uint4(packed[0], packed[1], packed[kVec / 2 - 2], packed[kVec / 2 - 1]);
+          else *reinterpret_cast<uint2*>(to) = make_uint2(packed[0], packed[1]);
+          if (a.lse && col == 0)
+            a.lse[(int64_t)t.token * a.n_heads + head] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
+        } else {
+          float4* to = reinterpret_cast<float4*>(a.ws + ws.rows) + (part * C::kRows + row) * (kDim / 4) + col / 4;
 #pragma unroll
-            for (int q = 0; q < kVec / 4; ++q) {
-              packed[2 * q] = pack2<kHalf>(x[q].x * inv, x[q].y * inv);
-              packed[2 * q + 1] = pack2<kHalf>(x[q].z * inv, x[q].w * inv);
-            }
-            uint16_t* to = a.out + t.token * a.out_stride + (int64_t)head * kDim + col;
-            if constexpr (kVec == 8) *reinterpret_cast<uint4*>(to) = make_uint4(packed[0], packed[1], packed[kVec / 2 - 2], packed[kVec / 2 - 1]);
-            else *reinterpret_cast<uint2*>(to) = make_uint2(packed[0], packed[1]);
-            if (a.lse && col == 0)
-              a.lse[(int64_t)t.token * a.n_heads + head] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
-          } else {
-            float4* to = reinterpret_cast<float4*>(a.ws + ws.rows) + (part * C::kRows + row) * (kDim / 4) + col / 4;
-#pragma unroll
-            for (int q = 0; q < kVec / 4; ++q) to[q] = x[q];
-            if (col == 0) reinterpret_cast<float2*>(a.ws + ws.sums)[part * C::kRows + row] = make_float2(m, l);
-          }
+          for (int q = 0; q < kVec / 4; ++q) to[q] = x[q];
+          if (col == 0) reinterpret_cast<float2*>(a.ws + ws.sums)[part * C::kRows + row] = make_float2(m, l);
         }
       }
       // The next iteration's barrier comes before this stage is filled again.
