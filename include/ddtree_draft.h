@@ -33,15 +33,18 @@ extern "C" {
 #define DDTREE_DRAFT_MAX_TOKENS 4096
 #define DDTREE_DRAFT_MAX_GROUP 64     /* query heads of one key head */
 
-/* Fields are outputs of ddtree_draft_attention_plan except q_stride and
- * out_stride, which the caller may set afterwards (0: contiguous tokens). */
+/* Fields are outputs of ddtree_draft_attention_plan except wait_limit_us,
+ * q_stride and out_stride, which the caller may set afterwards (0: 2 s,
+ * contiguous tokens). */
 typedef struct ddtree_draft_plan {
   int32_t n_tokens, n_heads, n_kv_heads, head_dim, dtype, page_size;
   int32_t window, n_sinks;   /* window 0: no window                              */
   int32_t row_tile;          /* query rows of a work item: 16, 32 or 64          */
   int32_t tile_keys;         /* keys of an inner tile                            */
   int32_t n_shares;          /* CTAs, each with an equal share of all key tiles  */
-  int32_t reserved;
+  int32_t wait_limit_us;     /* bound of each wait inside the kernel of wide groups, in
+                                microseconds; one that expires sets DDTREE_ST_TIMEOUT and
+                                the call ends without it (e.g. to test that path)   */
   int64_t q_stride, out_stride;   /* elements between tokens, multiples of 8     */
   int64_t workspace_bytes;
 } ddtree_draft_plan_t;

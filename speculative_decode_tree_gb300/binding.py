@@ -89,7 +89,7 @@ class _CacheStruct(ctypes.Structure):
 class DraftPlan(ctypes.Structure):
     """ddtree_draft_plan_t (include/ddtree_draft.h)."""
     _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_heads", "n_kv_heads", "head_dim", "dtype", "page_size",
-                                              "window", "n_sinks", "row_tile", "tile_keys", "n_shares", "reserved")] + \
+                                              "window", "n_sinks", "row_tile", "tile_keys", "n_shares", "wait_limit_us")] + \
                [(n, ctypes.c_int64) for n in ("q_stride", "out_stride", "workspace_bytes")]
 
 

@@ -305,6 +305,7 @@ struct DraftAttnArgs {
   uint8_t* ws;               // workspace: status block, then partial results
   int64_t q_stride, out_stride, page_stride, token_stride, head_stride, n_pages;
   float scale_log2;          // sm_scale * log2(e)
+  uint64_t wait_ns;          // bound of every wait of the tensor-memory form
   Divider page;              // by the tokens of a page
   int32_t n_tokens, n_heads, n_kv_heads, group, head_dim, dtype, page_size;
   int32_t window, n_sinks, table_rows, table_stride;

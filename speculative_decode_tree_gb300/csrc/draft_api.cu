@@ -22,7 +22,7 @@ bool plan_ok(const ddtree_draft_plan_t* p) {
   if (!p || !sizes_ok(p->n_tokens, p->n_heads, p->n_kv_heads, p->head_dim, p->dtype, p->page_size, p->window, p->n_sinks))
     return false;
   if (p->row_tile != draft_row_tile(p->n_heads / p->n_kv_heads, p->head_dim) || p->tile_keys != draft_tile_keys(p->row_tile, p->head_dim) ||
-      p->n_shares < 1 || p->n_shares > 65535)
+      p->n_shares < 1 || p->n_shares > 65535 || p->wait_limit_us < 0)
     return false;
   if (p->workspace_bytes != draft_workspace_bytes(p->row_tile, p->head_dim, p->n_shares)) return false;
   const int64_t width = (int64_t)p->n_heads * p->head_dim;
@@ -108,6 +108,7 @@ extern "C" int ddtree_draft_attention(const ddtree_draft_plan_t* plan, const voi
   a.head_stride = cache->head_stride;
   a.n_pages = cache->n_pages;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.wait_ns = plan->wait_limit_us > 0 ? (uint64_t)plan->wait_limit_us * 1000ull : 2000000000ull;
   a.n_tokens = plan->n_tokens;
   a.n_heads = plan->n_heads;
   a.n_kv_heads = plan->n_kv_heads;

@@ -198,8 +198,18 @@ enum { kFirst = 1, kLast = 2, kBegun = 4, kGoesOn = 8, kNextLast = 16 };
 // One elected thread of the converged warp issues: with a thread chosen by its
 // lane the descriptors go through vector registers, and a product of 16 columns
 // of K took 100 cycles to issue instead of 35.
-// Waits are bounded (2 s): a warp whose wait expires sets TIMEOUT and goes on
-// without waiting, so that every barrier between warps is still met.
+// Waits are bounded (the plan's wait_limit_us): a warp whose wait expires sets
+// TIMEOUT and goes on without waiting for copies and products, but meets every
+// named barrier, each once a tile and in order, so that all warps come to the end:
+//  - P is handed over at four of them in turn (tile & 3).  A warp arrives without
+//    waiting there and runs ahead; from an expired wait on it waits there, at a
+//    barrier whose last use was over before its tile's scores were issued.  With
+//    two in turn it could arrive for the next tile before a slower warp had
+//    arrived for this one, and the count would never come out again.
+//  - Tiles that other warps take from it may not have been looked up yet; their
+//    places hold a valid token from the start, so nothing is read or written out of
+//    range.  A softmax warp takes each for a unit's end and leaves its rows in the
+//    workspace: what a tile owes to the next one is then the same for every tile.
 struct TensorShared {
   // Barriers.  Of a stage: copies landed, O of its tile complete.  Of even and odd
   // tiles: S complete.  Of even and odd units: the last S with their queries complete.
@@ -207,7 +217,14 @@ struct TensorShared {
   uint32_t base;                  // tensor memory
 };
 constexpr int kAllocWarp = 3, kIssueWarp = 13;
-constexpr uint64_t kWaitNs = 2000000000ull;
+// Named barriers: 0 of all warps, 1 of the copies, eight for the reference of a
+// quarter of the rows (from even to odd tiles and back), four for P.
+constexpr int kReferenceBarrier = 2, kPBarrier = 10;
+constexpr uint64_t kDrainNs = 2000000000ull;  // for products in flight where the kernel ends
+// Bounds below this one have a kernel of their own that polls (kShort): a try may
+// suspend a warp for longer, and polls beside the tries make the kernel's code so
+// long that 64 rows of 64 columns took 309 us per GB instead of 223.
+constexpr uint64_t kShortNs = 1000000ull;
 // Columns: two S at 0, O behind; a power of two.
 __host__ __device__ constexpr int o_col(int dim) { return dim == 128 ? 128 : 256; }
 __host__ __device__ constexpr int tmem_cols(int dim) { return dim == 128 ? 256 : 512; }
@@ -223,7 +240,7 @@ __device__ __forceinline__ bool copies_tiles(int warp) { return (warp & ~3) == 8
 // The copying warps and the lookup warp.
 __device__ __forceinline__ void copies_barrier() { asm volatile("bar.sync 1, 160;" ::: "memory"); }
 
-template <bool kHalf, int kDim, typename Copies, typename Queries>
+template <bool kHalf, int kDim, bool kShort, typename Copies, typename Queries>
 __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layout& ws, TensorShared& sh, uint32_t p_at,
                                              uint32_t q_ring, uint32_t ring, const Tile* tiles,
                                              const uint32_t (*there)[Config<kDim, 4>::kKeys / 32], float* reference, float2* others,
@@ -239,7 +256,9 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
   const uint32_t s_mem = sh.base, o_mem = sh.base + o_col(kDim);
   bool late = false;
   auto wait = [&](uint64_t* bar, int phase) {  // by a whole warp
-    if (!late && !__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, kWaitNs))) {
+    if (late) return;
+    const bool done = kShort ? mbar_poll(bar, phase & 1, a.wait_ns) : mbar_wait(bar, phase & 1, a.wait_ns);
+    if (!__all_sync(0xffffffffu, done)) {
       late = true;
       atomicOr(bits, DDTREE_ST_TIMEOUT);
     }
@@ -284,7 +303,7 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
     score(0);
     for (int i = 0; i < count; ++i) {
       if (i + 1 < count) score(i + 1);
-      asm volatile("bar.sync %0, 160;" ::"r"(2 + (i & 1)) : "memory");  // P is written and O rescaled
+      asm volatile("bar.sync %0, 160;" ::"r"(kPBarrier + (i & 3)) : "memory");  // P is written and O rescaled
       tc_fence_after();
       if (elect_one()) {
         const uint32_t p_tile = p_at + (i & 1) * C::kTileP, v_at = stage_of(i) + C::kTileBytes;
@@ -309,7 +328,7 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
       mbar_init(&drained, 1);
       fence_mbar_init();
       mma_commit(&drained);
-      mbar_wait(&drained, 0, kWaitNs);
+      mbar_wait(&drained, 0, kDrainNs);
     }
     return;
   }
@@ -326,7 +345,8 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
     const int slot = i % C::kRing;
     wait(&sh.scores[i & 1], i >> 1);
     tc_fence_after();
-    const Tile t = tiles[i % C::kTileRing];
+    Tile t = tiles[i % C::kTileRing];
+    if (late) t.flags = kLast | kGoesOn;  // the lookup may not have been here
     uint32_t x[4 * kBlocks];
     const uint32_t x_mem = s_mem + my_lane + (i & 1) * C::kKeys;
     if constexpr (kBlocks == 4) tmem_ld_frag32(x_mem, x);
@@ -361,7 +381,7 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
     }
     // The reference goes from tile to tile, and so from group to group; where a
     // unit ends, after its rows were read: the next tile's product writes over them.
-    if (i > 0) asm volatile("bar.sync %0, 64;" ::"r"(8 - 4 * mine + quarter) : "memory");
+    if (i > 0) asm volatile("bar.sync %0, 64;" ::"r"(kReferenceBarrier + 4 - 4 * mine + quarter) : "memory");
     bool raised = false;
     float keep[2], before[2] = {-INFINITY, -INFINITY};
     if (!(t.flags & kFirst)) {
@@ -386,7 +406,7 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
     unit = t.unit;
     __syncwarp();
     const bool unit_ends = t.flags & kLast;
-    if (!unit_ends) asm volatile("bar.arrive %0, 64;" ::"r"(4 + 4 * mine + quarter) : "memory");
+    if (!unit_ends) asm volatile("bar.arrive %0, 64;" ::"r"(kReferenceBarrier + 4 * mine + quarter) : "memory");
     if (!(t.flags & kFirst) && __any_sync(0xffffffffu, raised)) {
       wait_values(i - 1);  // the rows of O are complete
       tc_fence_after();
@@ -430,9 +450,8 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
     fence_async_smem();
     tc_fence_before();
     __syncwarp();
-    // A warp cannot be here again before the others of its group were: it waits for the values.
-    if (late) asm volatile("bar.sync %0, 160;" ::"r"(2 + mine) : "memory");
-    else asm volatile("bar.arrive %0, 160;" ::"r"(2 + mine) : "memory");
+    if (late) asm volatile("bar.sync %0, 160;" ::"r"(kPBarrier + (i & 3)) : "memory");
+    else asm volatile("bar.arrive %0, 160;" ::"r"(kPBarrier + (i & 3)) : "memory");
     if (!unit_ends) continue;
 
     // ---- the unit ends here; the product before this tile's came after the other group's sums
@@ -481,12 +500,12 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
       }
     }
     __syncwarp();
-    if (i + 1 < count) asm volatile("bar.arrive %0, 64;" ::"r"(4 + 4 * mine + quarter) : "memory");
+    if (i + 1 < count) asm volatile("bar.arrive %0, 64;" ::"r"(kReferenceBarrier + 4 * mine + quarter) : "memory");
   }
   tc_fence_before();
 }
 
-template <bool kHalf, int kDim, int kWM>
+template <bool kHalf, int kDim, int kWM, bool kShort>
 __global__ void __launch_bounds__(Config<kDim, kWM>::kAllThreads, Config<kDim, kWM>::kCtas)
 draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   using C = Config<kDim, kWM>;
@@ -656,6 +675,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     }
   };
   if constexpr (C::kTensor) {
+    if (tid < C::kTileRing) tiles[tid] = Tile{start_token, 0, 0, 0};
     if (tid == 0) {
       for (int k = 0; k < C::kStages; ++k) {
         ptx::mbar_init(&tensor.full[k], C::kCopyThreads + 1);
@@ -777,7 +797,7 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
   }
 
   if constexpr (C::kTensor) {
-    tensor_tiles<kHalf, kDim>(a, ws, tensor, p_at, q_ring, ring, tiles, there, &top_s[0][0], reinterpret_cast<float2*>(&sum_s[0][0]), &bits, count, share, start_copies,
+    tensor_tiles<kHalf, kDim, kShort>(a, ws, tensor, p_at, q_ring, ring, tiles, there, &top_s[0][0], reinterpret_cast<float2*>(&sum_s[0][0]), &bits, count, share, start_copies,
                               start_queries);
   } else {
     auto computing_warps = [] { asm volatile("bar.sync 1, %0;" ::"n"(C::kThreads) : "memory"); };
@@ -1105,7 +1125,7 @@ __global__ void __launch_bounds__(2 * kDim) draft_join_kernel(const __grid_const
   }
 }
 
-template <bool kHalf, int kDim, int kWM>
+template <bool kHalf, int kDim, int kWM, bool kShort = false>
 cudaError_t launch(const DraftAttnArgs& a, cudaStream_t stream) {
   using C = Config<kDim, kWM>;
   // The shared-memory limit belongs to the kernel on a device: set once on each.
@@ -1115,11 +1135,11 @@ cudaError_t launch(const DraftAttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (device & 63);
   if (!(have.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(draft_attn_kernel<kHalf, kDim, kWM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(draft_attn_kernel<kHalf, kDim, kWM, kShort>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     have.fetch_or(bit, std::memory_order_release);
   }
-  e = launch_early(draft_attn_kernel<kHalf, kDim, kWM>, a.n_shares, C::kAllThreads, C::kSmem, stream, a);
+  e = launch_early(draft_attn_kernel<kHalf, kDim, kWM, kShort>, a.n_shares, C::kAllThreads, C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
   // Rows get CTAs of their own where records are few, for their units have many
   // parts (one CTA for all rows: window 12.0 us instead of 8.0, 185k single 85.6
@@ -1138,7 +1158,7 @@ cudaError_t launch_rows(const DraftAttnArgs& a, cudaStream_t stream) {
   if constexpr (kDim == 64) {
     if (a.row_tile == 32) return launch<kHalf, kDim, 2>(a, stream);
   }
-  return launch<kHalf, kDim, 4>(a, stream);
+  return a.wait_ns < kShortNs ? launch<kHalf, kDim, 4, true>(a, stream) : launch<kHalf, kDim, 4>(a, stream);
 }
 
 template <bool kHalf>
