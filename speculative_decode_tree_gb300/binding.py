@@ -595,10 +595,16 @@ class DraftCache:
         self.struct = _CacheStruct(kp, vp, self.n_pages, *step, self.page_size, self.n_kv_heads, self.head_dim, dtype)
 
 
-def _draft_append_args(cache, rope, q, k, v, positions, slots, q_out, q_weight, k_weight, eps, status):
-    dt, i32, d = cache.k.dtype, torch.int32, cache.k.get_device()
-    if cache.k.get_device() != torch.cuda.current_device():
+def _cache_device(cache: DraftCache) -> int:
+    """The cache's device, which must be the current one: the call launches there."""
+    d = cache.k.get_device()
+    if d != torch.cuda.current_device():
         raise ValueError(f"the cache is on {cache.k.device}, not the current device")
+    return d
+
+
+def _draft_append_args(cache, rope, q, k, v, positions, slots, q_out, q_weight, k_weight, eps, status):
+    dt, i32, d = cache.k.dtype, torch.int32, _cache_device(cache)
     n, dim, kvh = int(k.shape[0]), cache.head_dim, cache.n_kv_heads
 
     def heads(t, name, h):
@@ -652,7 +658,7 @@ def ddtree_draft_attention_workspace_size(plan: DraftPlan) -> int:
 
 
 def _draft_attention_args(plan, q, cache, page_table, positions, sm_scale, out, workspace, token_rows, lse):
-    dt, i32, d = cache.k.dtype, torch.int32, cache.k.get_device()
+    dt, i32, d = cache.k.dtype, torch.int32, _cache_device(cache)
     n, h, dim = plan.n_tokens, plan.n_heads, plan.head_dim
     if cache.head_dim != dim:
         raise ValueError("the plan was made for another cache")
@@ -662,7 +668,7 @@ def _draft_attention_args(plan, q, cache, page_table, positions, sm_scale, out, 
         if (h > 1 and t.stride(1) != dim) or (n > 1 and t.stride(0) != (stride or h * dim)):
             raise ValueError(f"{name}: heads must be {dim} and tokens {stride or h * dim} elements apart (plan q_stride, out_stride)")
         return p
-    table = _dev(page_table, i32, "page_table")
+    table = _dev(page_table, i32, "page_table", device=d)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [rows, pages of a row]")
     return (ctypes.addressof(plan), heads(q, "q", plan.q_stride), ctypes.addressof(cache.struct), table,
