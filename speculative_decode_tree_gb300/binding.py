@@ -7,6 +7,7 @@ fallback, and loading fails loudly when the library has not been built.
 """
 from __future__ import annotations
 
+import copy
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -425,7 +426,8 @@ class _Bound:
     whose buffers stay the same (see BoundVerify).  Calling the object launches
     on `stream`, with the device of the buffers current.  It keeps references
     to the tensors; they must not be resized or moved in place while the object
-    is used."""
+    is used.  Plans, rotations and a cache's layout are kept as they were when
+    they were checked: later changes of the caller's do not reach the call."""
     _entry = ""
 
     def _bind(self, args, keep) -> None:
@@ -447,6 +449,15 @@ class _Bound:
         rc = self._fn(*self._args, ctypes.c_void_p(handle))
         if rc != DDTREE_OK:
             raise DDTreeError(rc, self._entry)
+
+
+def _kept(x):
+    """A copy of a plan, a rotation or a cache (whose tensors stay the same)."""
+    if isinstance(x, DraftCache):
+        own = copy.copy(x)
+        own.struct = _kept(x.struct)
+        return own
+    return type(x).from_buffer_copy(x)
 
 
 def _opt(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, numel: Optional[int] = None,
@@ -570,7 +581,7 @@ class BoundMlaAppend(_Bound):
 
     def __init__(self, rope: Rope, kv_new, positions, slots, kv_pool, *, latent_weight=None, eps: float = 1e-6,
                  q_rope=None, q_out=None, status=None):
-        a = (rope, kv_new, positions, slots, kv_pool, latent_weight, eps, q_rope, q_out, status)
+        a = (_kept(rope), kv_new, positions, slots, kv_pool, latent_weight, eps, q_rope, q_out, status)
         self._bind(_mla_append_args(*a), a)
 
 
@@ -640,7 +651,7 @@ class BoundDraftAppend(_Bound):
 
     def __init__(self, cache: DraftCache, rope: Rope, q, k, v, positions, slots, q_out, *, q_weight=None, k_weight=None,
                  eps: float = 1e-6, status=None):
-        a = (cache, rope, q, k, v, positions, slots, q_out, q_weight, k_weight, eps, status)
+        a = (_kept(cache), _kept(rope), q, k, v, positions, slots, q_out, q_weight, k_weight, eps, status)
         self._bind(_draft_append_args(*a), a)
 
 
@@ -695,5 +706,5 @@ class BoundDraftAttention(_Bound):
 
     def __init__(self, plan: DraftPlan, q, cache: DraftCache, page_table, positions, sm_scale: float, out, workspace, *,
                  token_rows=None, lse=None):
-        a = (plan, q, cache, page_table, positions, sm_scale, out, workspace, token_rows, lse)
+        a = (_kept(plan), q, _kept(cache), page_table, positions, sm_scale, out, workspace, token_rows, lse)
         self._bind(_draft_attention_args(*a), a)

@@ -1,0 +1,47 @@
+"""Calls through the binding that its objects and checks have to hold for."""
+import pytest
+import torch
+
+from speculative_decode_tree_gb300 import binding as B
+from test_draft_attn_gpu import Case
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+
+
+def test_bound_attention_keeps_the_plan_it_checked():
+    # The strides that were checked against `out` count, whatever becomes of the plan.  (Every place that either
+    # stride reaches lies inside the buffer.)
+    c = Case([300, 5, 77], 8, 2, 64, seed=71)
+    c.device()
+    wide = torch.full((3, 16, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.plan.out_stride = 16 * 64
+    bound = B.BoundDraftAttention(c.plan, c.q_dev, c.cache, *c.args[3:6], wide[:, :8], c.ws, **c.kw)
+    c.plan.out_stride = 0
+    bound()
+    torch.cuda.synchronize()
+    assert bool((wide[:, 8:] == 7.0).all())
+    c.out = wide[:, :8].contiguous()
+    c.compare()
+
+
+def test_bound_appends_keep_their_rotation():
+    g = torch.Generator().manual_seed(72)
+    kv, q = torch.randn(5, 576, generator=g).to(torch.bfloat16).cuda(), torch.randn(5, 3, 64, generator=g).to(torch.bfloat16).cuda()
+    pos, slots = torch.arange(1, 6, dtype=I32, device="cuda"), torch.arange(5, dtype=I32, device="cuda")
+    pools, outs = [torch.zeros(5, 576, dtype=torch.bfloat16, device="cuda") for _ in range(2)], [torch.zeros_like(q) for _ in range(2)]
+    rope = B.ddtree_rope_init(64, theta=1e4, interleaved=True)
+    B.ddtree_mla_append(rope, kv, pos, slots, pools[0], q_rope=q, q_out=outs[0])
+    bound = B.BoundMlaAppend(rope, kv, pos, slots, pools[1], q_rope=q, q_out=outs[1])
+    rope.interleaved = 0
+    bound()
+    assert torch.equal(pools[0], pools[1]) and torch.equal(outs[0], outs[1])
+
+    caches = [B.DraftCache(torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16, device="cuda"),
+                           torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16, device="cuda")) for _ in range(2)]
+    rope = B.ddtree_rope_init(64, theta=1e4, interleaved=True)
+    B.ddtree_draft_append(caches[0], rope, q, q, q, pos, slots, outs[0])
+    bound = B.BoundDraftAppend(caches[1], rope, q, q, q, pos, slots, outs[1])
+    rope.interleaved = 0
+    bound()
+    assert torch.equal(caches[0].k, caches[1].k) and torch.equal(outs[0], outs[1])
