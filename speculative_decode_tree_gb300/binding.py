@@ -475,13 +475,17 @@ def _maps_args(page_table, prefix_lens, max_new, page_size, n_pages, kv_indptr, 
     d = page_table.get_device()
     b, t = int(prefix_lens.numel()), int(max_new)
     n_free = 0 if free_pages is None else int(free_pages.numel())
+    indptr = _dev(kv_indptr, i32, "kv_indptr", b + 1, device=d)
+    indices = _opt(kv_indices, i32, "kv_indices", device=d)
+    if kv_indices is not None and kv_indices.numel() == 0:
+        indices = indptr  # an empty list has no address, and a null one asks for none; nothing is written there
     return (b, t, int(page_size), int(n_pages), table, int(page_table.shape[0]), int(page_table.shape[1]),
             _opt(table_row, i32, "table_row", b, d), _dev(prefix_lens, i32, "prefix_lens", device=d),
             _opt(new_lens, i32, "new_lens", b, d), _opt(tree_parent, i32, "tree_parent", b * t, d),
             _opt(pages_held, i32, "pages_held", b, d), _opt(free_pages, i32, "free_pages", device=d), n_free,
             _opt(free_head, i32, "free_head", 1, d), _opt(pages_held_out, i32, "pages_held_out", b, d),
-            _opt(free_head_out, i32, "free_head_out", 1, d), _dev(kv_indptr, i32, "kv_indptr", b + 1, device=d),
-            _opt(kv_indices, i32, "kv_indices", device=d), 0 if kv_indices is None else int(kv_indices.numel()),
+            _opt(free_head_out, i32, "free_head_out", 1, d), indptr,
+            indices, 0 if kv_indices is None else int(kv_indices.numel()),
             _opt(new_indptr, i32, "new_indptr", b + 1, d), _dev(new_slots, i32, "new_slots", b * t, device=d),
             _dev(positions, i32, "positions", b * t, device=d), _opt(token_rows, i32, "token_rows", b * t, d),
             _opt(status, i32, "status", 1, d))

@@ -45,3 +45,22 @@ def test_bound_appends_keep_their_rotation():
     rope.interleaved = 0
     bound()
     assert torch.equal(caches[0].k, caches[1].k) and torch.equal(outs[0], outs[1])
+
+
+def test_an_empty_index_list_is_too_small_for_any_key():
+    def call(prefix):
+        table = torch.tensor([[0, -1, -1]], dtype=I32, device="cuda")
+        o = {n: torch.full((s,), -9, dtype=I32, device="cuda") for n, s in
+             (("indptr", 2), ("slots", 2), ("pos", 2), ("held", 1), ("head", 1))}
+        status = torch.zeros(1, dtype=I32, device="cuda")
+        new = torch.tensor([2 if prefix else 0], dtype=I32, device="cuda")
+        B.ddtree_step_maps(table, torch.tensor([prefix], dtype=I32, device="cuda"), 2, 4, 8, o["indptr"],
+                           torch.empty(0, dtype=I32, device="cuda"), o["slots"], o["pos"], new_lens=new,
+                           pages_held=torch.ones(1, dtype=I32, device="cuda"),
+                           free_pages=torch.arange(1, 8, dtype=I32, device="cuda"),
+                           free_head=torch.zeros(1, dtype=I32, device="cuda"), pages_held_out=o["held"],
+                           free_head_out=o["head"], status=status)
+        return table.tolist(), o["indptr"].tolist(), o["held"].tolist(), o["head"].tolist(), int(status)
+
+    assert call(3) == ([[0, -1, -1]], [0, 0], [1], [0], B.DDTREE_ST_BAD_LENGTH)
+    assert call(0) == ([[0, -1, -1]], [0, 0], [1], [0], 0)
