@@ -64,3 +64,32 @@ def test_an_empty_index_list_is_too_small_for_any_key():
 
     assert call(3) == ([[0, -1, -1]], [0, 0], [1], [0], B.DDTREE_ST_BAD_LENGTH)
     assert call(0) == ([[0, -1, -1]], [0, 0], [1], [0], 0)
+
+
+def test_reading_a_step_status_leaves_the_next_steps_bits(monkeypatch):
+    from speculative_decode_tree_gb300.runner import DeviceStep
+    pool = torch.zeros(64, 576, dtype=torch.bfloat16, device="cuda")
+    table = torch.full((1, 40), -1, dtype=I32, device="cuda")
+    free = torch.arange(8, dtype=I32, device="cuda")
+    step = DeviceStep(1, 4, 2, 30, 1, pool, table, free, B.ddtree_rope_init(64, theta=1e4), 0.1)
+    step.tree_parent.fill_(-1)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    step.run(side)
+    assert step.status(side) == 0
+
+    # A slow clear, and a step that runs out of pages right behind it on the other stream.
+    clear = torch.Tensor.zero_
+
+    def slow(t):
+        torch.cuda._sleep(200_000_000)
+        return clear(t)
+    step.free_head.fill_(6)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch.Tensor, "zero_", slow)
+    assert step.status(side) == 0
+    step.run(side)
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert step.status(side) & B.DDTREE_ST_NO_PAGES
+    assert step.status(side) & B.DDTREE_ST_NO_PAGES == 0
