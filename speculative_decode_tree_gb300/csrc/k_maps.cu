@@ -324,9 +324,10 @@ __global__ void __launch_bounds__(kThreads) maps_kernel(const __grid_constant__ 
         // Rows count on within a page: one product per page, then additions.
         const int left = ps - in;
         const int p0 = pages[k], p1 = left < kEntries ? pages[k + 1] : p0;
-        const int from = p0 * ps + in, then = p1 * ps - left;
+        // Without a sign: a page outside the pool may overflow, and is replaced below.
+        const uint32_t from = (uint32_t)p0 * (uint32_t)ps + (uint32_t)in, then = (uint32_t)p1 * (uint32_t)ps - (uint32_t)left;
 #pragma unroll
-        for (int e = 0; e < kEntries; ++e) row[e] = (e < left ? from : then) + e;
+        for (int e = 0; e < kEntries; ++e) row[e] = (int)((e < left ? from : then) + (uint32_t)e);
         if (max((uint32_t)p0, (uint32_t)p1) >= (uint32_t)a.n_pages) {
 #pragma unroll
           for (int e = 0; e < kEntries; ++e) row[e] = e < left ? row_of(a, p0, in + e) : row_of(a, p1, e - left);

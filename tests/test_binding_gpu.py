@@ -93,3 +93,12 @@ def test_reading_a_step_status_leaves_the_next_steps_bits(monkeypatch):
     torch.cuda.synchronize()
     assert step.status(side) & B.DDTREE_ST_NO_PAGES
     assert step.status(side) & B.DDTREE_ST_NO_PAGES == 0
+
+
+@pytest.mark.parametrize("page", [16, 48, 8])
+@pytest.mark.parametrize("entry", [2 ** 31 - 1, -2 ** 31, -1, 70_000_000])
+def test_index_rows_of_table_entries_far_outside_the_pool(page, entry):
+    from test_maps_gpu import _case, _check
+    c = _case(21 + page, [page * 9 + 5, page * 4], 6, page, grow=False)
+    c["table"][0][2] = c["table"][1][1] = c["table"][0][9] = entry
+    assert _check(c)["bad_index"]
