@@ -338,7 +338,7 @@ __device__ __forceinline__ void tensor_tiles(const DraftAttnArgs& a, const Layou
   const int quarter = warp & 3, row = quarter * 16 + (lane >> 2), quad = lane & 3;
   const int mine = warp >> 2;  // even tiles or odd ones
   const uint32_t my_lane = (uint32_t)(quarter * 32) << 16;
-  const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);  // as for fewer rows
+  const float scale = fmaxf(fabsf(a.scale_log2), 1.4e-45f);  // as for fewer rows
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // as of this group's last tile
   int unit = -1;
   for (int i = mine; i < count; i += 2) {
@@ -815,9 +815,9 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     // so there they carry a factor of 2^10: a key counts down to 2^-34 of the
     // largest, and the factor leaves with the division by the sum.
     constexpr float kShift = kHalf ? 10.f : 0.f;
-    // A negative scale turns the products' signs instead; zero becomes a factor
-    // that no product survives, so that absent keys stay at -inf.
-    const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
+    // A negative scale turns the products' signs instead; zero becomes the least
+    // number, which no product survives, so that absent keys stay at -inf.
+    const float scale = fmaxf(fabsf(a.scale_log2), 1.4e-45f);
 
     // Fragment addresses.  A row's chunks are exchanged by its low three bits,
     // which are the lane's in every matrix it addresses, so four offsets serve

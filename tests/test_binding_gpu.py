@@ -102,3 +102,14 @@ def test_index_rows_of_table_entries_far_outside_the_pool(page, entry):
     c = _case(21 + page, [page * 9 + 5, page * 4], 6, page, grow=False)
     c["table"][0][2] = c["table"][1][1] = c["table"][0][9] = entry
     assert _check(c)["bad_index"]
+
+
+@pytest.mark.parametrize("heads,kvh,dim", [(8, 2, 64), (24, 1, 64), (8, 1, 256), (40, 1, 128)])
+@pytest.mark.parametrize("scale", [0.0, 1e-38, -1e-42])
+def test_scales_that_no_score_survives(scale, heads, kvh, dim):
+    # Scores up to 1e38: what little the scale leaves of them must not become a weight.
+    c = Case([700, 30], heads, kvh, dim, seed=73, scale=scale)
+    c.q.mul_(1e17), c.k_raw.mul_(1e17)
+    c.q_dev.copy_(c.q)
+    assert c.run() == 0
+    c.compare()
