@@ -52,7 +52,8 @@ typedef struct ddtree_rope {
 
 /*
  * rot_dim 2 .. 256, even; theta > 1; factor >= 1 (ignored by PLAIN); the next
- * three are read by YARN only: original_positions >= 1, beta_fast > beta_slow > 0.
+ * three are read by YARN only: beta_fast > beta_slow > 0, original_positions >
+ * 2 pi beta_slow (with fewer no pair turns beta_slow times over them).
  * mscale > 0, or 0 for the method's own: 0.1 ln(factor) + 1 for YARN, else 1.
  * Host only.  Errors: DDTREE_EINVAL.
  */

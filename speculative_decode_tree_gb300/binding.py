@@ -526,7 +526,8 @@ class BoundStepMaps(_Bound):
 def ddtree_rope_init(rot_dim: int, *, theta: float, interleaved: bool = False, scaling: int = DDTREE_ROPE_PLAIN,
                      factor: float = 1.0, original_positions: int = 1, beta_fast: float = 32.0, beta_slow: float = 1.0,
                      mscale: float = 0.0) -> Rope:
-    """A rotation for the append calls (include/ddtree_append.h); host only."""
+    """A rotation for the append calls (include/ddtree_append.h); host only.
+    DDTREE_ROPE_YARN needs `factor` and `original_positions`."""
     rope = Rope()
     _check(library().ddtree_rope_init(int(rot_dim), int(bool(interleaved)), float(theta), int(scaling), float(factor),
                                       int(original_positions), float(beta_fast), float(beta_slow), float(mscale),

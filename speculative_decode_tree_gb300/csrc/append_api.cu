@@ -60,6 +60,7 @@ extern "C" int ddtree_rope_init(int rot_dim, int interleaved, double theta, int 
     return DDTREE_EINVAL;
   if (!(mscale >= 0.0) || !isfinite((float)mscale)) return DDTREE_EINVAL;
   constexpr double kTwoPi = 6.283185307179586476925286766559;
+  if (scaling == DDTREE_ROPE_YARN && !(original_positions > kTwoPi * beta_slow)) return DDTREE_EINVAL;
   // Pair index at which a pair makes `beta` turns over the original length.
   auto index_of = [&](double beta) {
     return rot_dim * log(original_positions / (beta * kTwoPi)) / (2.0 * log(theta));
