@@ -74,6 +74,7 @@ DDTREE_API size_t ddtree_draft_attention_workspace_size(const ddtree_draft_plan_
  *   out         [n_tokens, n_heads, head_dim] dtype, tokens plan->out_stride apart;
  *               it must not overlap q
  *   lse         [n_tokens, n_heads] fp32, contiguous, or NULL
+ *   sm_scale    any number that times log2(e) is finite; negative and 0 too
  * Device-data errors set status bits instead of faulting: a position below -1,
  * a row outside the table or a position past its pages: DDTREE_ST_BAD_LENGTH,
  * out 0 and lse -inf; a page outside [0, n_pages): DDTREE_ST_BAD_INDEX, its

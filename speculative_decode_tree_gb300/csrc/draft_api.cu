@@ -81,8 +81,10 @@ extern "C" int ddtree_draft_attention(const ddtree_draft_plan_t* plan, const voi
   if (!q || !aligned(q, 16) || !page_table || !aligned(page_table, 4) || !aligned(token_rows, 4) || !positions ||
       !aligned(positions, 4) || !out || !aligned(out, 16) || !aligned(lse, 4) || !workspace || !aligned(workspace, 256))
     return DDTREE_EINVAL;
-  if (table_rows < 1 || table_stride < 1 || (!token_rows && table_rows < plan->n_tokens) || q == out || !isfinite(sm_scale))
+  if (table_rows < 1 || table_stride < 1 || (!token_rows && table_rows < plan->n_tokens) || q == out)
     return DDTREE_EINVAL;
+  const float scale_log2 = sm_scale * 1.4426950408889634f;
+  if (!isfinite(scale_log2)) return DDTREE_EINVAL;
   if ((int64_t)workspace_bytes < plan->workspace_bytes) return DDTREE_EWORKSPACE;
   DevInfo info;
   const int rc = current_device_info(&info);
@@ -107,7 +109,7 @@ extern "C" int ddtree_draft_attention(const ddtree_draft_plan_t* plan, const voi
   a.token_stride = cache->token_stride;
   a.head_stride = cache->head_stride;
   a.n_pages = cache->n_pages;
-  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.wait_ns = plan->wait_limit_us > 0 ? (uint64_t)plan->wait_limit_us * 1000ull : 2000000000ull;
   a.n_tokens = plan->n_tokens;
   a.n_heads = plan->n_heads;

@@ -26,3 +26,12 @@ def test_wait_limit(lib):
     for limit, code in ((0, B.DDTREE_EWORKSPACE), (1, B.DDTREE_EWORKSPACE), (2 ** 31 - 1, B.DDTREE_EWORKSPACE), (-1, B.DDTREE_EINVAL)):
         plan.wait_limit_us = limit
         assert call() == code, limit
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_scales_whose_product_with_log2_e_overflows(lib, scale):
+    c, plan = _cache(), B.DraftPlan()
+    assert lib.ddtree_draft_attention_plan(4, 8, ctypes.addressof(c), 0, 0, 152, ctypes.addressof(plan)) == 0
+    for s, code in ((scale, B.DDTREE_EINVAL), (scale / 2, B.DDTREE_EWORKSPACE)):
+        assert lib.ddtree_draft_attention(ctypes.addressof(plan), P, ctypes.addressof(c), P, 4, 8, None, P, s, Q, P, P,
+                                          plan.workspace_bytes - 1, None) == code
