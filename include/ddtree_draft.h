@@ -14,6 +14,12 @@
  * Table entries of pages that no visible key lies in are never read, so pages
  * behind the window may have been released.
  *
+ * Scores, the softmax's maxima and sums and the products' sums are held in 32
+ * bits.  A probability is rounded to the cache's type (half a step of it) where
+ * it meets V, as in the verify kernels, while the sums take it unrounded; fp16
+ * probabilities carry a factor of 2^10 there, so that keys down to 2^-34 of the
+ * largest count.  An output is rounded once.
+ *
  * The work is split over the tokens' lengths in equal shares for the SMs, read
  * on the device: a plan depends on no length, and a captured call replays with
  * any.  Partial results are joined in a fixed order: equal inputs give equal

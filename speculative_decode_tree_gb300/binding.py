@@ -699,7 +699,8 @@ def ddtree_draft_attention(plan: DraftPlan, q: torch.Tensor, cache: DraftCache, 
                            token_rows: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                            stream=None) -> None:
     """The drafter's attention of one new token per request over its paged
-    cache (include/ddtree_draft.h).  q and out [N, H, D], lse [N, H]."""
+    cache (include/ddtree_draft.h).  q and out [N, H, D], lse [N, H].
+    Probabilities meet V in the cache's type; everything else is in 32 bits."""
     _check(library().ddtree_draft_attention(
         *_draft_attention_args(plan, q, cache, page_table, positions, sm_scale, out, workspace, token_rows, lse),
         _stream(stream)), "ddtree_draft_attention")

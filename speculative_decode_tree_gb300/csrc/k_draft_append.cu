@@ -11,10 +11,14 @@
 // No shared memory, no barrier; kUnroll steps' loads are in flight together.
 // Every value is read once, rounded once and written once.  Calls back to back
 // in a graph: 8 tokens of 48 heads 3.1 us (launch and two dependent loads);
-// 32,749 tokens of 24 64-column heads 35 us (5.75 TB/s, 0.85 of the measured
-// copy rate), bound by the memory system: half of the cache rows' bytes go out
-// as 128-byte pieces at scattered places, and neither more loads in flight
-// (unroll 4 and 6: 36.7 and 35.5 us) nor more warps (unroll 2: 35.7) change it.
+// 32,749 tokens of 24 64-column heads, interleaved and without norms, 35 us (5.75
+// TB/s, 0.85 of the measured copy rate), bound by the memory system: half of the
+// cache rows' bytes go out as 128-byte pieces at scattered places, and neither
+// more loads in flight (unroll 4 and 6: 36.7 and 35.5 us) nor more warps (unroll
+// 2: 35.7) change it.  With norms 40 us, in the half layout 38 and 44.5 (128 and
+// 256 columns of the same bytes 47.6 and 49.1): the arithmetic and the exchanges
+// between lanes bound those, and 64 registers spill 16 to 24 bytes in the half
+// layout.
 // The grid holds one wave: 45 us with a CTA per eight tokens.
 #include "rope.cuh"
 

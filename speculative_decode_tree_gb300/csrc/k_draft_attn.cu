@@ -62,7 +62,7 @@ struct Config {
   // memory (tensor_tiles): in registers every tile of 16 rows loads the keys'
   // fragments for itself, which 64 rows of 128 columns pay with shared memory's
   // whole bandwidth.  us per GB (256 columns: per 537 MB), registers and tensor
-  // memory: 64 rows of 64, 128, 256 columns 259, 269, 198 and 198, 173, 101; 24
+  // memory: 64 rows of 64, 128, 256 columns 259, 269, 198 and 197, 172, 101; 24
   // rows 181, 204, 114 and 195, 167, 96.
   static constexpr bool kTensor = kWM == 4;
   static_assert(kWM != 2 || kDim == 64, "see draft_row_tile");
@@ -811,7 +811,10 @@ draft_attn_kernel(const __grid_constant__ DraftAttnArgs a) {
     constexpr bool kHoldQ = kDim <= 128;
     uint32_t qf[kHoldQ ? kDim / 16 : 1][4];
     float o[kCols / 8][4], top[2], sum[2];
-    // Probabilities meet V in the cache's type.  fp16 holds nothing below 2^-24,
+    // Probabilities meet V in the cache's type: half a step of it each, in exchange
+    // for one matrix instruction per product (error of bf16 outputs against 64 bits
+    // 0.00164 -> 0.00175, most of it the outputs' own rounding).  The sum takes them
+    // unrounded, so the logarithm does not see it.  fp16 holds nothing below 2^-24,
     // so there they carry a factor of 2^10: a key counts down to 2^-34 of the
     // largest, and the factor leaves with the division by the sum.
     constexpr float kShift = kHalf ? 10.f : 0.f;

@@ -18,9 +18,9 @@
 // above, so no thread reads a table entry that this launch writes.
 //
 // Integer work.  Calls back to back in a graph: one request 2.4 us and eight
-// requests of 448,768 entries 4.2 us (a launch and two dependent loads); 1024
-// requests of 21M entries 23.7 us, of which the 84 MB of writes alone take 13.4
-// (0.57 of the measured copy rate).  The rest there is latency: the sums, which
+// requests of 359,739 entries 4.2 us (a launch and two dependent loads); 1024
+// requests of 21.5M entries 23.7 us (0.57 of the measured copy rate), of which the
+// 86 MB of writes alone take 12.7.  The rest there is latency: the sums, which
 // every CTA takes, some 5 us, and a table load per step of 256 entries.
 #include "common.cuh"
 
