@@ -48,9 +48,10 @@ typedef struct ddtree_draft_plan {
   int32_t row_tile;          /* query rows of a work item: 16, 32 or 64          */
   int32_t tile_keys;         /* keys of an inner tile                            */
   int32_t n_shares;          /* CTAs, each with an equal share of all key tiles  */
-  int32_t wait_limit_us;     /* bound of each wait inside the kernel of wide groups, in
-                                microseconds; one that expires sets DDTREE_ST_TIMEOUT and
-                                the call ends without it (e.g. to test that path)   */
+  int32_t wait_limit_us;     /* bound of each wait inside the kernel of wide groups
+                                (row_tile 64), in microseconds; one that expires sets
+                                DDTREE_ST_TIMEOUT, and the call ends without it (e.g.
+                                to test that path)                              */
   int64_t q_stride, out_stride;   /* elements between tokens, multiples of 8     */
   int64_t workspace_bytes;
 } ddtree_draft_plan_t;

@@ -150,8 +150,8 @@ class DeviceStep:
             call(stream)
 
     def status(self, stream=None) -> int:
-        """Status bits of the last run, on `stream` as it was (synchronises); clears those of
-        the maps and the append.  Nothing of it is left to do when it returns, so a run that
+        """Status bits of the last run, which `stream` was given to (synchronises); clears those
+        of the maps and the append.  The clear is over when this returns, so a run that
         follows, on whatever stream, keeps its bits."""
         bits = B.ddtree_verify_mla_check(self.workspace, stream) | int(self.status_word)
         self.status_word.zero_()
