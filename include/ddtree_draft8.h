@@ -1,0 +1,106 @@
+/*
+ * The drafter's cache in 8 bits: quantised as it is written, and read back ("Chunk 66.0", magik.net seg_66/chunk_0: a drafter with KV
+ * caching proposes the trees; its one-token attention is bound by the bytes
+ * of its cache, and 8 bits halve them).
+ *
+ * An element of the cache is an e4m3 number c (1 sign, 4 exponent and 3
+ * mantissa bits, largest 448) and stands for c * scale, with a scale for each
+ * block of tokens and key head, of keys and of values.  Token t of a page lies
+ * in its block t / block_tokens; a page's last block may be a short one.
+ * Scales are 32-bit numbers in [DDTREE_DRAFT8_SCALE_MIN, _MAX]; the append
+ * writes powers of two, so a block that moves to a larger scale keeps its
+ * numbers but for those that become subnormal.
+ *
+ * Conventions as in ddtree_verify.h.
+ */
+#ifndef DDTREE_DRAFT8_H_
+#define DDTREE_DRAFT8_H_
+
+#include "ddtree_append.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define DDTREE_DRAFT8_MAX_BLOCK 4096          /* block_tokens * head_dim */
+#define DDTREE_DRAFT8_SCALE_MIN 5.4210108624275222e-20f  /* 2^-64 */
+#define DDTREE_DRAFT8_SCALE_MAX 7.9228162514264338e28f   /* 2^96 */
+
+/* Element (page, token, head, column) of k and of v lies page * page_stride +
+ * token * token_stride + head * head_stride + column bytes behind the pointer;
+ * its scale is number (page * blocks + token / block_tokens) * n_kv_heads +
+ * head of k_scale or v_scale, with blocks = ceil(page_size / block_tokens). */
+typedef struct ddtree_draft8_cache {
+  void* k;               /* 16-byte aligned, e4m3 codes                           */
+  void* v;
+  float* k_scale;        /* [n_pages, blocks, n_kv_heads], contiguous             */
+  float* v_scale;
+  int64_t n_pages;       /* n_pages * page_size <= 2^31 - 1                       */
+  int64_t page_stride;   /* bytes, multiples of 16                                */
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t page_size;     /* tokens of a page, 1 .. DDTREE_MAX_PAGE_SIZE, any number */
+  int32_t n_kv_heads;    /* 1 .. DDTREE_MAX_HEADS                                 */
+  int32_t head_dim;      /* 64, 128 or 256                                        */
+  int32_t block_tokens;  /* 1 .. DDTREE_DRAFT8_MAX_BLOCK / head_dim, any number up to page_size */
+} ddtree_draft8_cache_t;
+
+/*
+ * Queries, keys and values of n_tokens new tokens, as ddtree_draft_append, the
+ * keys and values quantised:
+ *   q_out[n, h]                 = R(positions[n]) norm(q[n, h], q_weight)
+ *   k cache, scales [slots[n]]  = quantised R(positions[n]) norm(k[n, h], k_weight)
+ *   v cache, scales [slots[n]]  = quantised v[n, h]
+ * Keys are quantised from their 32-bit values.  Per key head, with m the
+ * largest finite magnitude of the rows that the call writes to a block:
+ *   - A block whose first token is among them starts afresh: its scale is the
+ *     least power of two s with m <= 448 s (from 2^-64 to 2^96; 1 where m is
+ *     0), and its other tokens hold nothing from then on.
+ *   - Otherwise the block keeps its scale if m <= 448 times that; if not, it
+ *     takes the one that the rows need, and the tokens that it holds already
+ *     are quantised again with it.  A scale that is no number from 2^-64 to
+ *     2^96 counts as none: the block starts afresh.
+ * Codes are rounded to the nearest, ties to even; what lies beyond 448 becomes
+ * 448 (infinities too), NaN stays NaN.
+ * So a request's tokens are to be written in order, as ddtree_step_maps lays
+ * them out, and in a call tokens of the same block must follow one another
+ * in the list, nothing between them, no padding token either: of a block that a
+ * call names in several places, or of a slot that it names twice, the contents
+ * would be a mixture (of that block alone).  Tokens of rejected drafts may be
+ * overwritten; their block's scale stays.
+ *   dtype          DDTREE_BF16 or DDTREE_FP16, of q, k, v, weights and q_out
+ *   n_tokens, n_heads, rope, strides, positions, slots, status as in
+ *   ddtree_draft_append; slot = page * page_size + token in page
+ * Errors: DDTREE_EINVAL, DDTREE_EUNSUPPORTED, DDTREE_ELAUNCH.
+ */
+DDTREE_API int ddtree_draft8_append(int64_t n_tokens, int n_heads, int dtype, const ddtree_draft8_cache_t* cache,
+                                    const ddtree_rope_t* rope, const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* v, int64_t v_stride, const void* q_weight,
+                                    const void* k_weight, float eps, const int32_t* positions, const int32_t* slots,
+                                    void* q_out, int64_t q_out_stride, uint32_t* status, struct CUstream_st* stream);
+
+/*
+ * Rows of the cache read back: k_out[n, h] = k cache[slots[n], h] in 16 bits,
+ * v_out likewise; a product is rounded once (exact in bf16 where the scale is
+ * a power of two; fp16 holds less range, and what lies beyond it becomes an
+ * infinity).
+ *   n_rows        0 .. DDTREE_APPEND_MAX_TOKENS (0: nothing happens)
+ *   slots         [n_rows] int32; -1: the row is left as it is.  Others outside
+ *                 the cache: DDTREE_ST_BAD_INDEX, left as they are.  A slot may
+ *                 be named any number of times.
+ *   k_out, v_out  dtype, rows *_stride elements apart (multiples of 8), heads
+ *                 head_dim apart; one of them may be NULL
+ *   status        uint32, OR-ed (the caller clears it), or NULL.  A scale that
+ *                 is no number from 2^-64 to 2^96 sets DDTREE_ST_BAD_SCALE, and
+ *                 its rows are 0.
+ * Errors: DDTREE_EINVAL, DDTREE_EUNSUPPORTED, DDTREE_ELAUNCH.
+ */
+DDTREE_API int ddtree_draft8_read(int64_t n_rows, int dtype, const ddtree_draft8_cache_t* cache, const int32_t* slots,
+                                  void* k_out, int64_t k_out_stride, void* v_out, int64_t v_out_stride,
+                                  uint32_t* status, struct CUstream_st* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DDTREE_DRAFT8_H_ */

@@ -83,6 +83,7 @@ enum ddtree_status {
 #define DDTREE_ST_OVERLAP     0x10u  /* relocation: a destination row is busy  */
 #define DDTREE_ST_BAD_MASK    0x20u  /* a custom mask that is not a tree mask  */
 #define DDTREE_ST_NO_PAGES    0x40u  /* step maps: the free list runs out      */
+#define DDTREE_ST_BAD_SCALE   0x80u  /* 8-bit cache: a scale out of its range  */
 
 /* Kernel variants of the split-KV partial stage. */
 #define DDTREE_KERNEL_AUTO 0

@@ -32,6 +32,7 @@ DDTREE_ST_TIMEOUT = 0x8
 DDTREE_ST_OVERLAP = 0x10
 DDTREE_ST_BAD_MASK = 0x20
 DDTREE_ST_NO_PAGES = 0x40
+DDTREE_ST_BAD_SCALE = 0x80
 
 DDTREE_ROPE_PLAIN = 0
 DDTREE_ROPE_LINEAR = 1
@@ -54,6 +55,7 @@ EXPORTS = (
     "ddtree_tree_from_mask_workspace_size", "ddtree_tree_from_mask", "ddtree_step_maps",
     "ddtree_rope_init", "ddtree_mla_append", "ddtree_draft_append",
     "ddtree_draft_attention_plan", "ddtree_draft_attention_workspace_size", "ddtree_draft_attention",
+    "ddtree_draft8_append", "ddtree_draft8_read",
 )
 
 
@@ -85,6 +87,12 @@ class _CacheStruct(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class _Cache8Struct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + \
+               [(n, ctypes.c_int64) for n in ("n_pages", "page_stride", "token_stride", "head_stride")] + \
+               [(n, ctypes.c_int32) for n in ("page_size", "n_kv_heads", "head_dim", "block_tokens")]
 
 
 class DraftPlan(ctypes.Structure):
@@ -155,6 +163,10 @@ def library() -> ctypes.CDLL:
     L.ddtree_draft_attention_workspace_size.restype = sz
     L.ddtree_draft_attention.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, f32, vp, vp, vp, sz, vp]
     L.ddtree_draft_attention.restype = i32
+    L.ddtree_draft8_append.argtypes = [i64, i32, i32, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, vp, vp, i64, vp, vp]
+    L.ddtree_draft8_append.restype = i32
+    L.ddtree_draft8_read.argtypes = [i64, i32, vp, vp, vp, i64, vp, i64, vp, vp]
+    L.ddtree_draft8_read.restype = i32
     for name in ("ddtree_verify_mla_plan", "ddtree_verify_mla_plan_ex", "ddtree_verify_mla",
                  "ddtree_verify_mla_batched", "ddtree_build_ancestor_mask", "ddtree_verify_mla_check",
                  "ddtree_verify_mla_batched_timed", "ddtree_verify_mla_noalloc"):
@@ -453,7 +465,7 @@ class _Bound:
 
 def _kept(x):
     """A copy of a plan, a rotation or a cache (whose tensors stay the same)."""
-    if isinstance(x, DraftCache):
+    if isinstance(x, (DraftCache, Draft8Cache)):
         own = copy.copy(x)
         own.struct = _kept(x.struct)
         return own
@@ -714,3 +726,119 @@ class BoundDraftAttention(_Bound):
                  token_rows=None, lse=None):
         a = (_kept(plan), q, _kept(cache), page_table, positions, sm_scale, out, workspace, token_rows, lse)
         self._bind(_draft_attention_args(*a), a)
+
+
+_DTYPES = {torch.bfloat16: DDTREE_BF16, torch.float16: DDTREE_FP16}
+
+
+def _dtype_code(dtype: torch.dtype) -> int:
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"the type must be bfloat16 or float16, got {dtype}")
+    return code
+
+
+class Draft8Cache:
+    """The drafter's paged cache in 8 bits (ddtree_draft8_cache_t): k and v are
+    [pages, page_size, kv_heads, head_dim] tensors of float8_e4m3fn (or their
+    bytes, uint8) with equal strides, as in DraftCache; k_scale and v_scale
+    are contiguous [pages, ceil(page_size / block_tokens), kv_heads] float32
+    tensors.  Scales of zero are blocks that nothing was written to."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, block_tokens: int):
+        if k.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise TypeError(f"an 8-bit draft cache is float8_e4m3fn or uint8, got {k.dtype}")
+        if k.dim() != 4:
+            raise ValueError("a draft cache is [pages, page_size, kv_heads, head_dim]")
+        kp = _rows(k, k.dtype, "k cache", tuple(k.shape), torch.cuda.current_device())
+        d = k.get_device()
+        vp = _rows(v, k.dtype, "v cache", tuple(k.shape), d)
+        step = [_step(k, i, -(-int(k.shape[3]) // 16) * 16) for i in range(3)]
+        if step != [_step(v, i, -(-int(k.shape[3]) // 16) * 16) for i in range(3)]:
+            raise ValueError("the key and value caches must have equal strides")
+        self.k, self.v, self.k_scale, self.v_scale, self.block_tokens = k, v, k_scale, v_scale, int(block_tokens)
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = (int(x) for x in k.shape)
+        if self.block_tokens < 1:
+            raise ValueError("block_tokens must be at least 1")
+        shape = (self.n_pages, -(-self.page_size // self.block_tokens), self.n_kv_heads)
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _dev(t, torch.float32, name, device=d)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        self.struct = _Cache8Struct(kp, vp, k_scale.data_ptr(), v_scale.data_ptr(), self.n_pages, *step, self.page_size,
+                                    self.n_kv_heads, self.head_dim, self.block_tokens)
+
+
+def _head_rows(t, dtype, name, n, h, dim, device):
+    """Pointer and row stride of a [n, h, dim] tensor whose heads lie next to each other."""
+    p = _rows(t, dtype, name, (n, h, dim), device)
+    if h > 1 and n and t.stride(1) != dim:
+        raise ValueError(f"{name}: heads must be {dim} elements apart")
+    return p, _step(t, 0, h * dim)
+
+
+def _draft8_append_args(cache, rope, q, k, v, positions, slots, q_out, q_weight, k_weight, eps, status):
+    dt, i32, d = k.dtype, torch.int32, _cache_device(cache)
+    n, dim, kvh = int(k.shape[0]), cache.head_dim, cache.n_kv_heads
+    code = _dtype_code(dt)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    h = int(q.shape[1]) if q is not None else 0
+    qa, oa = (None, 0), (None, 0)
+    if h:
+        qa, oa = _head_rows(q, dt, "q", n, h, dim, d), _head_rows(q_out, dt, "q_out", n, h, dim, d)
+    return (n, h, code, ctypes.addressof(cache.struct), ctypes.addressof(rope), *qa, *_head_rows(k, dt, "k", n, kvh, dim, d),
+            *_head_rows(v, dt, "v", n, kvh, dim, d), _opt(q_weight, dt, "q_weight", dim, d), _opt(k_weight, dt, "k_weight", dim, d),
+            float(eps), _dev(positions, i32, "positions", n, device=d), _dev(slots, i32, "slots", n, device=d), *oa,
+            _opt(status, i32, "status", 1, d))
+
+
+def ddtree_draft8_append(cache: Draft8Cache, rope: Rope, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                         positions: torch.Tensor, slots: torch.Tensor, q_out: Optional[torch.Tensor], *,
+                         q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                         eps: float = 1e-6, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Head norms and rotation of the drafter's new tokens, keys and values
+    quantised into their blocks (include/ddtree_draft8.h).  Tensors as in
+    ddtree_draft_append; tokens of one block follow one another."""
+    _check(library().ddtree_draft8_append(
+        *_draft8_append_args(cache, rope, q, k, v, positions, slots, q_out, q_weight, k_weight, eps, status),
+        _stream(stream)), "ddtree_draft8_append")
+
+
+class BoundDraft8Append(_Bound):
+    """ddtree_draft8_append with its arguments checked and marshalled once."""
+    _entry = "ddtree_draft8_append"
+
+    def __init__(self, cache: Draft8Cache, rope: Rope, q, k, v, positions, slots, q_out, *, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, status=None):
+        a = (_kept(cache), _kept(rope), q, k, v, positions, slots, q_out, q_weight, k_weight, eps, status)
+        self._bind(_draft8_append_args(*a), a)
+
+
+def _draft8_read_args(cache, slots, k_out, v_out, status):
+    d = _cache_device(cache)
+    one = k_out if k_out is not None else v_out
+    if one is None:
+        raise ValueError("one of k_out and v_out at least")
+    n, code = int(one.shape[0]), _dtype_code(one.dtype)
+    outs = [(None, 0) if t is None else _head_rows(t, one.dtype, name, n, cache.n_kv_heads, cache.head_dim, d)
+            for t, name in ((k_out, "k_out"), (v_out, "v_out"))]
+    return (n, code, ctypes.addressof(cache.struct), _dev(slots, torch.int32, "slots", n, device=d), *outs[0], *outs[1],
+            _opt(status, torch.int32, "status", 1, d))
+
+
+def ddtree_draft8_read(cache: Draft8Cache, slots: torch.Tensor, k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor], *,
+                       status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rows of the 8-bit cache in 16 bits (include/ddtree_draft8.h): k_out and
+    v_out [N, Hkv, D], bf16 or fp16 (rows may be strided), either may be None."""
+    _check(library().ddtree_draft8_read(*_draft8_read_args(cache, slots, k_out, v_out, status), _stream(stream)),
+           "ddtree_draft8_read")
+
+
+class BoundDraft8Read(_Bound):
+    """ddtree_draft8_read with its arguments checked and marshalled once."""
+    _entry = "ddtree_draft8_read"
+
+    def __init__(self, cache: Draft8Cache, slots, k_out, v_out, *, status=None):
+        a = (_kept(cache), slots, k_out, v_out, status)
+        self._bind(_draft8_read_args(*a), a)

@@ -313,6 +313,37 @@ struct DraftAttnArgs {
   int32_t bundle_log2;       // key heads that shares take side by side: 1, 2, 4 or 8, a divisor of them all
 };
 
+// Everything the 8-bit append needs (see include/ddtree_draft8.h).
+struct Draft8AppendArgs {
+  const uint16_t *q, *k, *v; // tokens *_stride apart, heads head_dim apart; q may be q_out itself
+  const uint16_t *q_weight, *k_weight;
+  const int32_t* positions;
+  const int32_t* slots;
+  uint16_t* q_out;
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;  // [pages, blocks, n_kv_heads]
+  uint32_t* status;          // or null
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int64_t page_stride, token_stride, head_stride;
+  int64_t total_slots;       // n_pages * page_size
+  Divider page, block;       // by the tokens of a page, of a block
+  float eps;
+  int32_t n_tokens, n_heads, n_kv_heads, head_dim, page_size, block_tokens, blocks, dtype;
+  RopeArgs rope;
+};
+
+// Everything the read of 8-bit rows needs.
+struct Draft8ReadArgs {
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int32_t* slots;
+  uint16_t *k_out, *v_out;   // rows *_stride apart; one may be null
+  uint32_t* status;          // or null
+  int64_t k_out_stride, v_out_stride, page_stride, token_stride, head_stride, total_slots;
+  Divider page, block;
+  int32_t n_rows, row_pieces, n_kv_heads, head_dim, page_size, blocks, dtype;
+};
+
 // Launches that may begin while the stream's last kernel is still running
 // (programmatic dependence): the kernel waits for it with await_grid() before
 // it touches memory, in every thread block, and lets the next such launch
@@ -346,6 +377,8 @@ cudaError_t launch_draft_attention(const DraftAttnArgs& a, cudaStream_t stream);
 bool draft_cache_ok(const ddtree_draft_cache_t* cache);
 cudaError_t launch_mla_append(const MlaAppendArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_draft_append(const DraftAppendArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_draft8_append(const Draft8AppendArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_draft8_read(const Draft8ReadArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_maps(const MapsArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_mask(const MaskArgs& a, cudaStream_t stream);
 cudaError_t launch_relocate(const RelocateArgs& a, int num_sms, cudaStream_t stream);
