@@ -1,5 +1,6 @@
 /*
- * The drafter's cache in 8 bits: quantised as it is written, and read back ("Chunk 66.0", magik.net seg_66/chunk_0: a drafter with KV
+ * The drafter's cache in 8 bits: quantised as it is written, read back, and
+ * attended to ("Chunk 66.0", magik.net seg_66/chunk_0: a drafter with KV
  * caching proposes the trees; its one-token attention is bound by the bytes
  * of its cache, and 8 bits halve them).
  *
@@ -16,7 +17,7 @@
 #ifndef DDTREE_DRAFT8_H_
 #define DDTREE_DRAFT8_H_
 
-#include "ddtree_append.h"
+#include "ddtree_draft.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -98,6 +99,46 @@ DDTREE_API int ddtree_draft8_append(int64_t n_tokens, int n_heads, int dtype, co
 DDTREE_API int ddtree_draft8_read(int64_t n_rows, int dtype, const ddtree_draft8_cache_t* cache, const int32_t* slots,
                                   void* k_out, int64_t k_out_stride, void* v_out, int64_t v_out_stride,
                                   uint32_t* status, struct CUstream_st* stream);
+
+/* Fields are outputs of ddtree_draft8_attention_plan except q_stride and
+ * out_stride, which the caller may set afterwards (0: contiguous tokens). */
+typedef struct ddtree_draft8_plan {
+  int32_t n_tokens, n_heads, n_kv_heads, head_dim, dtype, page_size, block_tokens;
+  int32_t window, n_sinks;   /* window 0: no window                              */
+  int32_t row_tiles;         /* work items of a key head: each 16 query heads    */
+  int32_t tile_keys;         /* keys of an inner tile                            */
+  int32_t n_shares;          /* CTAs, each with an equal share of all key tiles  */
+  int64_t q_stride, out_stride;   /* elements between tokens, multiples of 8     */
+  int64_t workspace_bytes;
+} ddtree_draft8_plan_t;
+
+/* As ddtree_draft_attention_plan; dtype: of q and out. */
+DDTREE_API int ddtree_draft8_attention_plan(int n_tokens, int n_heads, const ddtree_draft8_cache_t* cache, int dtype,
+                                            int window, int n_sinks, int num_sms, ddtree_draft8_plan_t* plan);
+
+/* As ddtree_draft_attention_workspace_size. */
+DDTREE_API size_t ddtree_draft8_attention_workspace_size(const ddtree_draft8_plan_t* plan);
+
+/*
+ * ddtree_draft_attention over the 8-bit cache: the same visible keys, page
+ * table, outputs and data errors.  Besides, a key with a scale that is no
+ * number from 2^-64 to 2^96 (of its key or its value) sets DDTREE_ST_BAD_SCALE
+ * and is dropped.
+ *
+ * e4m3 numbers are exact in fp16, and products run there: a query row is moved
+ * by a power of two so that its largest element fills fp16's range (what is
+ * 2^-39 of it or less is lost), scores, maxima and sums are in 32 bits, and the
+ * weight p_j vscale_j of a value row is rounded to fp16 (half a step of it,
+ * 2^-11) relative to the unit's largest: a row counts down to 2^-38 of that.
+ * The sums take p_j unrounded, and an output is rounded once.  Equal inputs
+ * give equal bits.
+ * Errors: as ddtree_draft_attention.
+ */
+DDTREE_API int ddtree_draft8_attention(const ddtree_draft8_plan_t* plan, const void* q,
+                                       const ddtree_draft8_cache_t* cache, const int32_t* page_table, int table_rows,
+                                       int table_stride, const int32_t* token_rows, const int32_t* positions,
+                                       float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                       struct CUstream_st* stream);
 
 #ifdef __cplusplus
 }

@@ -103,3 +103,45 @@ def read_rows(codes, scales, block: int, slots: Sequence[int], out: torch.Tensor
             out[n] = torch.where(ok[:, None], row, torch.zeros_like(row))
     return out
 
+
+
+def attention(q, k_codes, v_codes, k_scale, v_scale, block: int, page_table, token_rows, positions, window: int, n_sinks: int,
+              sm_scale: float, out, lse):
+    """The drafter's attention over the dequantised cache, as
+    draft_oracle.draft_attention gives it: (out, lse) in float64 from the given
+    buffers, the sum of |p_j v_j| of every output and the largest sum of
+    |scaled product| terms.  Keys whose scale is out of range are dropped."""
+    out, lse = out.to(torch.float64), lse.to(torch.float64)
+    mass, terms = torch.zeros_like(out), torch.zeros_like(lse)
+    pages, page, kvh = k_codes.shape[:3]
+    k_all, v_all = dequantised(k_codes, k_scale, block), dequantised(v_codes, v_scale, block)
+    at = torch.arange(page) // block
+    good = [(s >= 2.0 ** -64) & (s <= 2.0 ** 96) for s in (k_scale.to(torch.float64)[:, at], v_scale.to(torch.float64)[:, at])]
+    good = good[0] & good[1]
+    group = q.shape[1] // kvh
+    for n, pos in enumerate(positions):
+        if pos == -1:
+            continue
+        row = n if token_rows is None else int(token_rows[n])
+        out[n], lse[n] = 0.0, -math.inf
+        if pos < -1 or not 0 <= row < page_table.shape[0] or pos // page >= page_table.shape[1]:
+            continue
+        seen = torch.tensor([j for j in range(pos + 1) if window == 0 or j > pos - window or j < n_sinks])
+        where = page_table[row][seen // page].long()
+        here = (where >= 0) & (where < pages)
+        seen, where = seen[here], where[here]
+        for h in range(q.shape[1]):
+            kh = h // group
+            live = good[where, seen % page, kh]
+            if not bool(live.any()):
+                continue
+            k, v = (c[where[live], seen[live] % page, kh] for c in (k_all, v_all))
+            qh = q[n, h].to(torch.float64)
+            s = sm_scale * (k @ qh)
+            p = torch.exp(s - s.max())
+            total = p.sum()
+            lse[n, h] = s.max() + torch.log(total)
+            out[n, h] = (p / total) @ v
+            mass[n, h] = (p / total) @ v.abs()
+            terms[n, h] = abs(sm_scale) * float((k.abs() @ qh.abs()).max())
+    return out, lse, mass, terms

@@ -56,6 +56,7 @@ EXPORTS = (
     "ddtree_rope_init", "ddtree_mla_append", "ddtree_draft_append",
     "ddtree_draft_attention_plan", "ddtree_draft_attention_workspace_size", "ddtree_draft_attention",
     "ddtree_draft8_append", "ddtree_draft8_read",
+    "ddtree_draft8_attention_plan", "ddtree_draft8_attention_workspace_size", "ddtree_draft8_attention",
 )
 
 
@@ -99,6 +100,13 @@ class DraftPlan(ctypes.Structure):
     """ddtree_draft_plan_t (include/ddtree_draft.h)."""
     _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_heads", "n_kv_heads", "head_dim", "dtype", "page_size",
                                               "window", "n_sinks", "row_tile", "tile_keys", "n_shares", "wait_limit_us")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "out_stride", "workspace_bytes")]
+
+
+class Draft8Plan(ctypes.Structure):
+    """ddtree_draft8_plan_t (include/ddtree_draft8.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_heads", "n_kv_heads", "head_dim", "dtype", "page_size", "block_tokens",
+                                              "window", "n_sinks", "row_tiles", "tile_keys", "n_shares")] + \
                [(n, ctypes.c_int64) for n in ("q_stride", "out_stride", "workspace_bytes")]
 
 
@@ -167,6 +175,12 @@ def library() -> ctypes.CDLL:
     L.ddtree_draft8_append.restype = i32
     L.ddtree_draft8_read.argtypes = [i64, i32, vp, vp, vp, i64, vp, i64, vp, vp]
     L.ddtree_draft8_read.restype = i32
+    L.ddtree_draft8_attention_plan.argtypes = [i32, i32, vp, i32, i32, i32, i32, vp]
+    L.ddtree_draft8_attention_plan.restype = i32
+    L.ddtree_draft8_attention_workspace_size.argtypes = [vp]
+    L.ddtree_draft8_attention_workspace_size.restype = sz
+    L.ddtree_draft8_attention.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, f32, vp, vp, vp, sz, vp]
+    L.ddtree_draft8_attention.restype = i32
     for name in ("ddtree_verify_mla_plan", "ddtree_verify_mla_plan_ex", "ddtree_verify_mla",
                  "ddtree_verify_mla_batched", "ddtree_build_ancestor_mask", "ddtree_verify_mla_check",
                  "ddtree_verify_mla_batched_timed", "ddtree_verify_mla_noalloc"):
@@ -842,3 +856,64 @@ class BoundDraft8Read(_Bound):
     def __init__(self, cache: Draft8Cache, slots, k_out, v_out, *, status=None):
         a = (_kept(cache), slots, k_out, v_out, status)
         self._bind(_draft8_read_args(*a), a)
+
+
+def ddtree_draft8_attention_plan(n_tokens: int, n_heads: int, cache: Draft8Cache, dtype: torch.dtype, window: int = 0,
+                                 n_sinks: int = 0, num_sms: int = 0) -> Draft8Plan:
+    """Plan of the drafter's attention over its 8-bit cache (include/ddtree_draft8.h):
+    one for all lengths.  dtype: of q and out, bf16 or fp16."""
+    plan = Draft8Plan()
+    _check(library().ddtree_draft8_attention_plan(int(n_tokens), int(n_heads), ctypes.addressof(cache.struct), _dtype_code(dtype),
+                                                  int(window), int(n_sinks), int(num_sms), ctypes.addressof(plan)),
+           "draft8_attention_plan")
+    return plan
+
+
+def ddtree_draft8_attention_workspace_size(plan: Draft8Plan) -> int:
+    return int(library().ddtree_draft8_attention_workspace_size(ctypes.addressof(plan)))
+
+
+def _plan_rows(t, dtype, name, n, h, dim, stride, device, fields):
+    """Pointer of a [n, h, dim] tensor laid out as a plan says (stride 0: contiguous rows)."""
+    p = _rows(t, dtype, name, (n, h, dim), device)
+    if (h > 1 and t.stride(1) != dim) or (n > 1 and t.stride(0) != (stride or h * dim)):
+        raise ValueError(f"{name}: heads must be {dim} and rows {stride or h * dim} elements apart (plan {fields})")
+    return p
+
+
+def _draft8_attention_args(plan, q, cache, page_table, positions, sm_scale, out, workspace, token_rows, lse):
+    dt, i32, d = q.dtype, torch.int32, _cache_device(cache)
+    n, h, dim = plan.n_tokens, plan.n_heads, plan.head_dim
+    if cache.head_dim != dim:
+        raise ValueError("the plan was made for another cache")
+    if _dtype_code(dt) != plan.dtype:
+        raise TypeError(f"the plan was made for another type than {dt}")
+    table = _dev(page_table, i32, "page_table", device=d)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [rows, pages of a row]")
+    return (ctypes.addressof(plan), _plan_rows(q, dt, "q", n, h, dim, plan.q_stride, d, "q_stride"),
+            ctypes.addressof(cache.struct), table, int(page_table.shape[0]), int(page_table.shape[1]),
+            _opt(token_rows, i32, "token_rows", n, d), _dev(positions, i32, "positions", n, device=d), float(sm_scale),
+            _plan_rows(out, dt, "out", n, h, dim, plan.out_stride, d, "out_stride"), _opt(lse, torch.float32, "lse", n * h, d),
+            _dev(workspace, torch.uint8, "workspace", plan.workspace_bytes, device=d), int(workspace.numel()))
+
+
+def ddtree_draft8_attention(plan: Draft8Plan, q: torch.Tensor, cache: Draft8Cache, page_table: torch.Tensor,
+                            positions: torch.Tensor, sm_scale: float, out: torch.Tensor, workspace: torch.Tensor, *,
+                            token_rows: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                            stream=None) -> None:
+    """ddtree_draft_attention over the 8-bit cache (include/ddtree_draft8.h).
+    q and out [N, H, D], lse [N, H]."""
+    _check(library().ddtree_draft8_attention(
+        *_draft8_attention_args(plan, q, cache, page_table, positions, sm_scale, out, workspace, token_rows, lse),
+        _stream(stream)), "ddtree_draft8_attention")
+
+
+class BoundDraft8Attention(_Bound):
+    """ddtree_draft8_attention with its arguments checked and marshalled once."""
+    _entry = "ddtree_draft8_attention"
+
+    def __init__(self, plan: Draft8Plan, q, cache: Draft8Cache, page_table, positions, sm_scale: float, out, workspace, *,
+                 token_rows=None, lse=None):
+        a = (_kept(plan), q, _kept(cache), page_table, positions, sm_scale, out, workspace, token_rows, lse)
+        self._bind(_draft8_attention_args(*a), a)

@@ -344,6 +344,27 @@ struct Draft8ReadArgs {
   int32_t n_rows, row_pieces, n_kv_heads, head_dim, page_size, blocks, dtype;
 };
 
+// Everything the attention over the 8-bit cache needs.
+struct Draft8AttnArgs {
+  const uint16_t* q;         // tokens q_stride apart
+  const uint8_t *k, *v;      // paged cache
+  const float *k_scale, *v_scale;
+  const int32_t* table;      // [table_rows, table_stride]
+  const int32_t* token_rows; // [n_tokens] or null: row n
+  const int32_t* positions;  // [n_tokens]
+  uint16_t* out;             // tokens out_stride apart
+  float* lse;                // [n_tokens, n_heads] or null
+  uint8_t* ws;               // workspace: status block, then partial results
+  int64_t q_stride, out_stride, page_stride, token_stride, head_stride, n_pages;
+  float scale_log2;          // sm_scale * log2(e)
+  Divider page, block;       // by the tokens of a page, of a block
+  int32_t n_tokens, n_heads, n_kv_heads, group, head_dim, dtype, page_size, blocks;
+  int32_t row_tiles;         // units of a key head: each up to 16 of its query heads
+  int32_t unit_heads;        // n_kv_heads * row_tiles
+  int32_t window, n_sinks, table_rows, table_stride, n_shares;
+  int32_t bundle_log2;       // of the unit heads that shares take side by side: 1, 2, 4 or 8
+};
+
 // Launches that may begin while the stream's last kernel is still running
 // (programmatic dependence): the kernel waits for it with await_grid() before
 // it touches memory, in every thread block, and lets the next such launch
@@ -379,6 +400,10 @@ cudaError_t launch_mla_append(const MlaAppendArgs& a, int num_sms, cudaStream_t 
 cudaError_t launch_draft_append(const DraftAppendArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_draft8_append(const Draft8AppendArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_draft8_read(const Draft8ReadArgs& a, int num_sms, cudaStream_t stream);
+int draft8_tile_keys(int head_dim);
+int draft8_shares(int head_dim, int num_sms);
+int64_t draft8_workspace_bytes(int head_dim, int n_shares);
+cudaError_t launch_draft8_attention(const Draft8AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_maps(const MapsArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_mask(const MaskArgs& a, cudaStream_t stream);
 cudaError_t launch_relocate(const RelocateArgs& a, int num_sms, cudaStream_t stream);

@@ -113,3 +113,34 @@ def test_host_tensors_are_refused():
     if not torch.cuda.is_available():
         with pytest.raises((TypeError, RuntimeError, AssertionError)):
             B.Draft8Cache(k, k, s, s, 8)
+
+
+def test_attention_plan_and_refusals(lib):
+    cache, plan = cache8(), B.Draft8Plan()
+    make = lambda n=4, h=8, c=cache, dtype=0, w=0, s=0, sms=152: lib.ddtree_draft8_attention_plan(  # noqa: E731
+        n, h, ctypes.addressof(c), dtype, w, s, sms, ctypes.addressof(plan))
+    for kw in (dict(n=0), dict(n=4097), dict(h=7), dict(h=130), dict(h=0), dict(dtype=2), dict(w=-1), dict(s=-1), dict(sms=-1), dict(sms=4097)):
+        assert make(**kw) == B.DDTREE_EINVAL, kw
+    for bad in BAD_CACHES:
+        assert make(c=cache8(**bad)) == B.DDTREE_EINVAL, bad
+    assert make(h=128) == 0 and plan.row_tiles == 4
+    assert make() == 0 and plan.row_tiles == 1 and plan.n_shares == 2 * 152
+    assert B.ddtree_draft8_attention_workspace_size(plan) == plan.workspace_bytes > 0 and plan.workspace_bytes % 256 == 0
+    ok = dict(plan=ctypes.addressof(plan), q=P, cache=ctypes.addressof(cache), table=P, rows=4, stride=8, of=None, pos=P, scale=0.1, out=Q,
+              lse=None, ws=P, wsb=plan.workspace_bytes)
+
+    def call(**kw):
+        a = dict(ok, **kw)
+        return lib.ddtree_draft8_attention(*[a[k] for k in ok], None)
+    for bad in (dict(plan=None), dict(q=None), dict(q=OFF), dict(cache=None), dict(table=None), dict(table=ODD), dict(rows=0), dict(rows=3),
+                dict(stride=0), dict(of=ODD), dict(pos=None), dict(pos=ODD), dict(scale=float("nan")), dict(scale=3e38), dict(out=None),
+                dict(out=OFF), dict(out=P), dict(lse=ODD), dict(ws=None), dict(ws=OFF)):
+        assert call(**bad) == B.DDTREE_EINVAL, bad
+    assert call(wsb=plan.workspace_bytes - 1) == B.DDTREE_EWORKSPACE
+    for other in (dict(head_dim=128, page_stride=4096, token_stride=256, head_stride=128), dict(page_size=8), dict(block_tokens=4), dict(n_kv_heads=4)):
+        assert call(cache=ctypes.addressof(cache8(**other))) == B.DDTREE_EINVAL, other
+    for field, value in (("row_tiles", 2), ("tile_keys", 64), ("n_shares", 0), ("workspace_bytes", 256), ("q_stride", 8), ("out_stride", 516)):
+        kept = getattr(plan, field)
+        setattr(plan, field, value)
+        assert call() == B.DDTREE_EINVAL, field
+        setattr(plan, field, kept)
