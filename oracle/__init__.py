@@ -17,3 +17,4 @@ from .maps_oracle import step_maps  # noqa: F401
 from . import append_oracle  # noqa: F401
 from .draft_oracle import draft_attention, visible_keys  # noqa: F401
 from . import draft8_oracle  # noqa: F401
+from .prompt_oracle import prompt_attention  # noqa: F401

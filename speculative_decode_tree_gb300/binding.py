@@ -57,6 +57,7 @@ EXPORTS = (
     "ddtree_draft_attention_plan", "ddtree_draft_attention_workspace_size", "ddtree_draft_attention",
     "ddtree_draft8_append", "ddtree_draft8_read",
     "ddtree_draft8_attention_plan", "ddtree_draft8_attention_workspace_size", "ddtree_draft8_attention",
+    "ddtree_prompt_attention_plan", "ddtree_prompt_attention_workspace_size", "ddtree_prompt_attention",
 )
 
 
@@ -108,6 +109,13 @@ class Draft8Plan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_heads", "n_kv_heads", "head_dim", "dtype", "page_size", "block_tokens",
                                               "window", "n_sinks", "row_tiles", "tile_keys", "n_shares")] + \
                [(n, ctypes.c_int64) for n in ("q_stride", "out_stride", "workspace_bytes")]
+
+
+class PromptPlan(ctypes.Structure):
+    """ddtree_prompt_plan_t (include/ddtree_prompt.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "n_heads", "n_kv_heads", "head_dim", "dtype", "window", "n_sinks", "q_rows", "k_rows",
+                                              "wait_limit_us", "tile_tokens", "max_items")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "out_stride", "workspace_bytes")]
 
 
 class DDTreeError(RuntimeError):
@@ -181,6 +189,12 @@ def library() -> ctypes.CDLL:
     L.ddtree_draft8_attention_workspace_size.restype = sz
     L.ddtree_draft8_attention.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, f32, vp, vp, vp, sz, vp]
     L.ddtree_draft8_attention.restype = i32
+    L.ddtree_prompt_attention_plan.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32, vp]
+    L.ddtree_prompt_attention_plan.restype = i32
+    L.ddtree_prompt_attention_workspace_size.argtypes = [vp]
+    L.ddtree_prompt_attention_workspace_size.restype = sz
+    L.ddtree_prompt_attention.argtypes = [vp, vp, vp, vp, vp, vp, f32, vp, vp, vp, sz, vp]
+    L.ddtree_prompt_attention.restype = i32
     for name in ("ddtree_verify_mla_plan", "ddtree_verify_mla_plan_ex", "ddtree_verify_mla",
                  "ddtree_verify_mla_batched", "ddtree_build_ancestor_mask", "ddtree_verify_mla_check",
                  "ddtree_verify_mla_batched_timed", "ddtree_verify_mla_noalloc"):
@@ -917,3 +931,63 @@ class BoundDraft8Attention(_Bound):
                  token_rows=None, lse=None):
         a = (_kept(plan), q, _kept(cache), page_table, positions, sm_scale, out, workspace, token_rows, lse)
         self._bind(_draft8_attention_args(*a), a)
+
+
+def ddtree_prompt_attention_plan(batch: int, q_rows: int, k_rows: int, n_heads: int, n_kv_heads: int, head_dim: int, dtype: torch.dtype,
+                                 window: int = 0, n_sinks: int = 0) -> PromptPlan:
+    """Plan of the attention over whole prompts (include/ddtree_prompt.h), for
+    packed buffers of q_rows and k_rows rows and up to `batch` sequences of
+    any lengths; host only."""
+    plan = PromptPlan()
+    _check(library().ddtree_prompt_attention_plan(int(batch), int(q_rows), int(k_rows), int(n_heads), int(n_kv_heads), int(head_dim),
+                                                  _dtype_code(dtype), int(window), int(n_sinks), ctypes.addressof(plan)),
+           "prompt_attention_plan")
+    return plan
+
+
+def ddtree_prompt_attention_workspace_size(plan: PromptPlan) -> int:
+    return int(library().ddtree_prompt_attention_workspace_size(ctypes.addressof(plan)))
+
+
+def _prompt_attention_args(plan, q, k, v, q_indptr, k_indptr, sm_scale, out, workspace, lse):
+    dt, i32, f = q.dtype, torch.int32, torch.cuda.current_device()
+    if _dtype_code(dt) != plan.dtype:
+        raise TypeError(f"the plan was made for another type than {dt}")
+    h, kvh, dim = plan.n_heads, plan.n_kv_heads, plan.head_dim
+    plan = type(plan).from_buffer_copy(plan)  # the call's own: strides are the tensors' where the plan leaves them out
+    pointers = []
+    for t, name, rows, heads in ((q, "q", plan.q_rows, h), (k, "k", plan.k_rows, kvh), (v, "v", plan.k_rows, kvh), (out, "out", plan.q_rows, h)):
+        p = _rows(t, dt, name, (rows, heads, dim), f)
+        if heads > 1 and t.stride(1) != dim:
+            raise ValueError(f"{name}: heads must be {dim} elements apart")
+        field = f"{name}_stride"
+        if getattr(plan, field) == 0:
+            setattr(plan, field, _step(t, 0, heads * dim))
+        elif rows > 1 and t.stride(0) != getattr(plan, field):
+            raise ValueError(f"{name}: rows must be {getattr(plan, field)} elements apart (plan {field})")
+        pointers.append(p)
+    args = (ctypes.addressof(plan), *pointers[:3], _dev(q_indptr, i32, "q_indptr", plan.batch + 1, device=f),
+            _opt(k_indptr, i32, "k_indptr", plan.batch + 1, f), float(sm_scale), pointers[3],
+            _opt(lse, torch.float32, "lse", plan.q_rows * h, f),
+            _dev(workspace, torch.uint8, "workspace", plan.workspace_bytes, device=f), int(workspace.numel()))
+    return args, plan
+
+
+def ddtree_prompt_attention(plan: PromptPlan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_indptr: torch.Tensor,
+                            k_indptr: Optional[torch.Tensor], sm_scale: float, out: torch.Tensor, workspace: torch.Tensor, *,
+                            lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Causal attention over packed prompts (include/ddtree_prompt.h).  q and
+    out [q_rows, H, D], k and v [k_rows, Hkv, D] (rows may be strided, as parts
+    of one projection), q_indptr and k_indptr [batch + 1] (None: the same),
+    lse [q_rows, H]."""
+    args, plan = _prompt_attention_args(plan, q, k, v, q_indptr, k_indptr, sm_scale, out, workspace, lse)
+    _check(library().ddtree_prompt_attention(*args, _stream(stream)), "ddtree_prompt_attention")
+
+
+class BoundPromptAttention(_Bound):
+    """ddtree_prompt_attention with its arguments checked and marshalled once."""
+    _entry = "ddtree_prompt_attention"
+
+    def __init__(self, plan: PromptPlan, q, k, v, q_indptr, k_indptr, sm_scale: float, out, workspace, *, lse=None):
+        args, kept = _prompt_attention_args(plan, q, k, v, q_indptr, k_indptr, sm_scale, out, workspace, lse)
+        self._bind(args, (kept, q, k, v, q_indptr, k_indptr, out, workspace, lse))

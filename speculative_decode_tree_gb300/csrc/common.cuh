@@ -365,6 +365,22 @@ struct Draft8AttnArgs {
   int32_t bundle_log2;       // of the unit heads that shares take side by side: 1, 2, 4 or 8
 };
 
+// Everything the prompt attention needs (see include/ddtree_prompt.h).
+struct PromptArgs {
+  const uint16_t *q, *k, *v;   // rows *_stride apart, heads head_dim apart
+  const int32_t *q_indptr, *k_indptr;
+  uint16_t* out;
+  float* lse;                  // [q_rows, n_heads] or null
+  uint32_t* status;            // workspace offset 0
+  uint32_t* words;             // [max_items]: status bits of an item, and kPromptAgain
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  float scale_log2;            // sm_scale * log2(e)
+  uint64_t wait_ns;            // bound of every wait
+  int32_t batch, n_heads, n_kv_heads, group, head_dim, dtype, window, n_sinks;
+  int32_t q_rows, k_rows, tile_tokens, max_items;
+};
+constexpr uint32_t kPromptAgain = 0x80000000u;  // the item goes row by row
+
 // Launches that may begin while the stream's last kernel is still running
 // (programmatic dependence): the kernel waits for it with await_grid() before
 // it touches memory, in every thread block, and lets the next such launch
@@ -404,6 +420,9 @@ int draft8_tile_keys(int head_dim);
 int draft8_shares(int head_dim, int num_sms);
 int64_t draft8_workspace_bytes(int head_dim, int n_shares);
 cudaError_t launch_draft8_attention(const Draft8AttnArgs& a, cudaStream_t stream);
+int prompt_tile_tokens(int group, int head_dim);
+cudaError_t launch_prompt(const PromptArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_prompt_rows(const PromptArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_maps(const MapsArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_mask(const MaskArgs& a, cudaStream_t stream);
 cudaError_t launch_relocate(const RelocateArgs& a, int num_sms, cudaStream_t stream);
