@@ -1,15 +1,480 @@
-// The prompt attention: which items go row by row (all of them).
+// Causal attention over packed prompts (include/ddtree_prompt.h) on the tensor
+// cores.
+//
+//   S = Q K^T,  P = 2^(scale S - m),  O = sum P V,  l = sum P,  out = O / l
+//
+// 4 D flops a visible pair and head, and next to nothing to read: the tensor
+// pipe is the bound, and everything else has to run beside it.
+//
+//  - An item is a run of query tokens of one sequence with the heads of one key
+//    head: 128 rows (a token's heads next to each other) are one product tile, so
+//    a key tile serves the whole group, and short sequences of many heads fill
+//    tiles too.  Two tiles (A and B) share every key tile; while the softmax of
+//    one works on its scores, the products of the other run: in order A's PV of key
+//    tile i, A's QK of i + 1, then B's.  256 columns take one tile, whose scores
+//    have two buffers: QK of i + 1 runs beside the softmax of i.
+//  - Roles: a warp that loads (TMA boxes of 64 columns, 128-byte swizzle), a warp
+//    that issues the products, and four warps for each tile's softmax, a row a
+//    thread: no exchange between threads.  S, P (in place of S) and O live in the
+//    tensor memory; P is an operand there.
+//  - The reference m moves only when a row's maximum has grown by more than 2^8
+//    (2^4 for fp16, whose probabilities carry 2^10); O is then scaled in place by
+//    the softmax warps.
+//  - Key tiles that no row sees are skipped; those that some rows see in part are
+//    masked by bits.  What is masked has probability 0, and 0 times a NaN or an
+//    infinity in V is a NaN: a row whose result is no number marks its item, and a
+//    second grid, placed ahead of time, does marked items row by row
+//    (k_prompt_rows.cu).  So only inputs that hold such values pay for them.
+//  - Waits are bounded (the plan's wait_limit_us).  A role whose wait expires sets
+//    TIMEOUT, goes on without waiting and comes to its end; products in flight are
+//    waited for before the tensor memory is given back, copies before the CTA ends.
+#include <cuda.h>
+#include <string.h>
+
+#include <atomic>
+
 #include "prompt_list.cuh"
+#include "rope.cuh"
+#include "tc_ptx.cuh"
 
 namespace ddtree {
 namespace {
 
-__global__ void __launch_bounds__(128) prompt_all_kernel(const __grid_constant__ PromptArgs a) {
-  __shared__ int scratch[12];
+using namespace ptx;
+
+struct PromptMaps {
+  CUtensorMap q, k, v;
+};
+
+template <int kDim>
+struct Config {
+  static constexpr int kTiles = kDim == 256 ? 1 : 2;        // of 128 rows
+  static constexpr int kKeys = kDim == 256 ? 64 : 128;      // of a key tile
+  static constexpr int kSlabs = kDim / 64;                  // of 64 columns
+  static constexpr int kQBytes = 128 * kDim * 2;
+  static constexpr int kStageBytes = kKeys * kDim * 2;      // a tile of K or of V
+  static constexpr int kStages = kDim == 64 ? 10 : 5;
+  static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStageBytes;
+  static constexpr int kLoadWarp = 4 * kTiles, kIssueWarp = kLoadWarp + 1;
+  static constexpr int kThreads = 32 * (kIssueWarp + 1);
+  // Tensor memory: two buffers of S, then O of each tile.
+  static constexpr int kOCol = 256;
+};
+constexpr uint64_t kDrainNs = 2000000000ull;  // for products and copies in flight where the kernel ends
+
+__host__ __device__ constexpr uint32_t product_desc(int n, bool b_mn_major, bool half) {
+  return half ? idesc_bf16_f32(128, n, false, b_mn_major) & ~((1u << 7) | (1u << 10)) : idesc_bf16_f32(128, n, false, b_mn_major);
+}
+
+__device__ __forceinline__ void load_box(const CUtensorMap* map, uint32_t dst, int col, int head, int row, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(col), "r"(head), "r"(row), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// (x, y) * s + t and (x, y) += (u, v), two numbers an instruction.
+__device__ __forceinline__ void fma_pair(float& x, float& y, float s, float t) {
+  asm("{ .reg .b64 a, b, c;\n"
+      "  mov.b64 a, {%0, %1}; mov.b64 b, {%2, %2}; mov.b64 c, {%3, %3};\n"
+      "  fma.rn.f32x2 a, a, b, c;\n"
+      "  mov.b64 {%0, %1}, a; }"
+      : "+f"(x), "+f"(y)
+      : "f"(s), "f"(t));
+}
+__device__ __forceinline__ void add_pair(float& x, float& y, float u, float v) {
+  asm("{ .reg .b64 a, b;\n"
+      "  mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3};\n"
+      "  add.rn.f32x2 a, a, b;\n"
+      "  mov.b64 {%0, %1}, a; }"
+      : "+f"(x), "+f"(y)
+      : "f"(u), "f"(v));
+}
+
+// Bits 0 .. h of a word of 32.
+__device__ __forceinline__ uint32_t bits_to(int h) { return h < 0 ? 0u : h >= 31 ? 0xffffffffu : (2u << h) - 1u; }
+
+struct Shared {
+  uint64_t full[10], empty[10];      // stages: landed, used
+  uint64_t queries;
+  uint64_t scores[2];                // S of a buffer is complete
+  uint64_t weights[2];               // P is written
+  uint64_t products;                 // 256 columns: PV of a key tile is complete
+  uint64_t result[2];                // O of a tile is complete
+  uint64_t drained;
+  uint32_t base, word;
+  int scratch[20];
+};
+
+template <bool kHalf, int kDim>
+__global__ void __launch_bounds__(Config<kDim>::kThreads, 1) prompt_kernel(const __grid_constant__ PromptArgs a,
+                                                                          const __grid_constant__ PromptMaps maps) {
+  using C = Config<kDim>;
+  extern __shared__ uint8_t smem[];
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const int kv = blockIdx.x % a.n_kv_heads;
+  release_grid();
   await_grid();
   PromptItem it;
-  const int got = find_prompt_item<128>(a, blockIdx.x / a.n_kv_heads, scratch, it);
-  if (threadIdx.x == 0) a.words[blockIdx.x] = got == 2 ? DDTREE_ST_BAD_LENGTH : got == 0 ? kPromptAgain : 0;
+  const int got = find_prompt_item<C::kThreads>(a, blockIdx.x / a.n_kv_heads, sh.scratch, it);
+  if (got) {
+    if (tid == 0) a.words[blockIdx.x] = got == 2 ? DDTREE_ST_BAD_LENGTH : 0;
+    return;
+  }
+
+  // ---- the key tiles: sinks before every row's window, then from the first row's window on
+  const int tile_tokens = a.tile_tokens / C::kTiles;
+  const int lo_min = a.window > 0 ? max(0, it.pos - a.window + 1) : 0, sinks = min(a.n_sinks, lo_min);
+  const int sink_tiles = (sinks + C::kKeys - 1) / C::kKeys;
+  auto tiles_of = [&](int t) {  // key tiles of product tile t
+    const int last = it.pos + min((t + 1) * tile_tokens, it.tokens) - 1;
+    return t * tile_tokens >= it.tokens || last < 0 ? 0 : sink_tiles + (last - lo_min + C::kKeys) / C::kKeys;
+  };
+  auto start_of = [&](int i) { return i < sink_tiles ? i * C::kKeys : lo_min + (i - sink_tiles) * C::kKeys; };
+  const int n_of[2] = {tiles_of(0), C::kTiles == 2 ? tiles_of(1) : 0};
+  const int count = max(n_of[0], n_of[1]), present = C::kTiles == 2 && n_of[1] > 0 ? 2 : 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    mbar_init(&sh.queries, 1);
+    mbar_init(&sh.products, 1);
+    mbar_init(&sh.drained, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.scores[i], 1);
+      mbar_init(&sh.weights[i], 4);
+      mbar_init(&sh.result[i], 1);
+    }
+    fence_mbar_init();
+    sh.word = 0;
+  }
+  if (warp == C::kLoadWarp) {
+    tmem_alloc(&sh.base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.base;
+  const uint32_t q_at = (smem_u32(smem) + 1023) & ~1023u, ring = q_at + C::kTiles * C::kQBytes;
+  bool late = false;
+  auto wait = [&](uint64_t* bar, int phase) {  // by a whole warp
+    if (late) return;
+    const bool done = mbar_wait(bar, phase & 1, a.wait_ns);
+    if (!__all_sync(0xffffffffu, done)) {
+      late = true;
+      atomicOr(&sh.word, DDTREE_ST_TIMEOUT);
+    }
+  };
+
+  if (warp == C::kLoadWarp) {
+    if (count > 0 && elect_one()) {
+      mbar_arrive_expect_tx(&sh.queries, present * C::kSlabs * tile_tokens * a.group * 128);
+      for (int t = 0; t < present; ++t)
+        for (int s = 0; s < C::kSlabs; ++s)
+          load_box(&maps.q, q_at + t * C::kQBytes + s * 16384, 64 * s, kv * a.group, it.q0 + t * tile_tokens, &sh.queries);
+    }
+    __syncwarp();
+    int n = 0;
+    for (; n < 2 * count; ++n) {  // K of tile 0, V of tile 0, K of tile 1, ...
+      const int stage = n % C::kStages;
+      if (n >= C::kStages) wait(&sh.empty[stage], n / C::kStages - 1);
+      if (late) break;  // a stage that may be on its way is not filled again
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&sh.full[stage], C::kStageBytes);
+        const int row = it.k0 + start_of(n >> 1);
+#pragma unroll
+        for (int s = 0; s < C::kSlabs; ++s)
+          load_box(n & 1 ? &maps.v : &maps.k, ring + stage * C::kStageBytes + s * C::kKeys * 128, 64 * s, kv, row, &sh.full[stage]);
+      }
+      __syncwarp();
+    }
+    // Nothing of this may be on its way when the CTA ends.
+    if (count > 0) mbar_wait(&sh.queries, 0, kDrainNs);
+    for (int i = max(0, n - C::kStages); i < n; ++i) mbar_wait(&sh.full[i % C::kStages], (i / C::kStages) & 1, kDrainNs);
+  } else if (warp == C::kIssueWarp) {
+    auto stage_of = [&](int n) { return ring + (n % C::kStages) * C::kStageBytes; };
+    auto landed = [&](int n) {
+      wait(&sh.full[n % C::kStages], n / C::kStages);
+      tc_fence_after();
+    };
+    // By one thread: scores of tile t (into its buffer) with key tile i, its sums with the values of key tile i.
+    auto score = [&](int t, int buffer, int i) {
+      const uint32_t k_at = stage_of(2 * i);
+#pragma unroll
+      for (int s = 0; s < C::kSlabs; ++s)
+        mma_ss_x4<2, 2>(tmem + buffer * C::kKeys, desc_sw128(q_at + t * C::kQBytes + s * 16384, 16, 1024),
+                        desc_sw128(k_at + s * C::kKeys * 128, 16, 1024), product_desc(C::kKeys, false, kHalf), s > 0);
+      mma_commit(&sh.scores[buffer]);
+    };
+    auto accumulate = [&](int t, int buffer, int i) {
+      const uint32_t v_at = stage_of(2 * i + 1);
+#pragma unroll
+      for (int c = 0; c < C::kKeys / 64; ++c)
+        mma_ts_x4_step<128>(tmem + C::kOCol + t * kDim, tmem + buffer * C::kKeys + 32 * c, desc_sw128(v_at + c * 64 * 128, C::kKeys * 128, 1024),
+                            product_desc(kDim, true, kHalf), c > 0 || i > 0);
+    };
+    if (count > 0) {
+      wait(&sh.queries, 0);
+      landed(0);
+      if (elect_one()) {
+        for (int t = 0; t < present; ++t)
+          if (n_of[t] > 0) score(t, t, 0);
+        mma_commit(&sh.empty[0]);
+      }
+      __syncwarp();
+    }
+    if constexpr (C::kTiles == 2) {
+      for (int i = 0; i < count; ++i) {
+        landed(2 * i + 1);
+        if (i + 1 < count) landed(2 * i + 2);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (i >= n_of[t]) continue;
+          wait(&sh.weights[t], i);
+          tc_fence_after();
+          if (elect_one()) {
+            accumulate(t, t, i);
+            if (t == present - 1) mma_commit(&sh.empty[(2 * i + 1) % C::kStages]);
+            if (i + 1 < n_of[t]) score(t, t, i + 1);
+            else mma_commit(&sh.result[t]);
+            if (t == present - 1 && i + 1 < count) mma_commit(&sh.empty[(2 * i + 2) % C::kStages]);
+          }
+          __syncwarp();
+        }
+      }
+    } else {
+      for (int i = 0; i < count; ++i) {
+        if (i + 1 < count) {
+          landed(2 * i + 2);
+          if (elect_one()) {
+            score(0, (i + 1) & 1, i + 1);
+            mma_commit(&sh.empty[(2 * i + 2) % C::kStages]);
+          }
+          __syncwarp();
+        }
+        landed(2 * i + 1);
+        wait(&sh.weights[i & 1], i >> 1);
+        tc_fence_after();
+        if (elect_one()) {
+          accumulate(0, i & 1, i);
+          mma_commit(&sh.empty[(2 * i + 1) % C::kStages]);
+          mma_commit(&sh.products);
+          if (i + 1 == count) mma_commit(&sh.result[0]);
+        }
+        __syncwarp();
+      }
+    }
+    // After an expired wait products may be in flight still.
+    if (elect_one()) {
+      mma_commit(&sh.drained);
+      mbar_wait(&sh.drained, 0, kDrainNs);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: a row a thread
+    const int t = C::kTiles == 2 ? warp >> 2 : 0, quarter = warp & 3, row = quarter * 32 + lane;
+    const int n = n_of[t], token = t * tile_tokens + row / a.group, head = kv * a.group + row % a.group;
+    const bool valid = row < tile_tokens * a.group && token < it.tokens;
+    // Rows that are none are computed like the last one, and not stored.
+    const int pos = it.pos + (valid ? token : it.tokens - 1);
+    const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+    const uint32_t my_lane = (uint32_t)(quarter * 32) << 16, o_mem = tmem + C::kOCol + t * kDim + my_lane;
+    constexpr float kShift = kHalf ? 10.f : 0.f, kGrowth = kHalf ? 4.f : 8.f;
+    const float scale = fmaxf(fabsf(a.scale_log2), 1.4e-45f);  // its sign goes to the scores; zero becomes the least number
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < n; ++i) {
+      const int buffer = C::kTiles == 2 ? t : i & 1;
+      wait(&sh.scores[buffer], C::kTiles == 2 ? i : i >> 1);
+      tc_fence_after();
+      const uint32_t s_mem = tmem + buffer * C::kKeys + my_lane;
+      uint32_t x[C::kKeys];
+      if constexpr (C::kKeys == 128) tmem_ld128(s_mem, x);
+      else tmem_ld64(s_mem, x);
+      if (a.scale_log2 < 0.f) {
+#pragma unroll
+        for (int c = 0; c < C::kKeys; ++c) x[c] ^= 0x80000000u;
+      }
+      // Columns up to `high`, and of those the ones from `low` on or below `sink`.
+      const int start = start_of(i);
+      const int high = min(pos, (i < sink_tiles ? sinks : it.keys) - 1) - start;
+      const int low = i < sink_tiles ? 0 : lo - start, sink = a.n_sinks - start;
+      if (__any_sync(0xffffffffu, high < C::kKeys - 1 || (low > 0 && sink < min(low, C::kKeys)))) {
+#pragma unroll
+        for (int w = 0; w < C::kKeys / 32; ++w) {
+          const uint32_t seen = bits_to(high - 32 * w) & (~bits_to(low - 1 - 32 * w) | bits_to(max(sink, 0) - 1 - 32 * w));
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!(seen >> c & 1)) x[32 * w + c] = 0xff800000u;  // -inf
+        }
+      }
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < C::kKeys; c += 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
+      }
+      const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      bool raised = false;
+      float keep = 1.f;
+      if (valid && (most - m) * scale > kGrowth) {  // also the first finite maximum
+        keep = m == -INFINITY ? 0.f : ex2_approx((m - most) * scale);
+        raised = true;
+        m = most;
+        l *= keep;
+      }
+      if (i > 0 && __any_sync(0xffffffffu, raised)) {
+        // Two tiles: these scores came after the last product, which is complete.
+        if constexpr (C::kTiles == 1) {
+          wait(&sh.products, i - 1);
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int c = 0; c < kDim; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(o_mem + c, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * keep);
+          tmem_st32(o_mem + c, v);
+        }
+      }
+      const float from = m == -INFINITY ? 0.f : kShift - m * scale;
+      // A tile's sum first, then the row's: tens of thousands of equal terms one by
+      // one would lose four digits.
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int half = 0; half < C::kKeys / 64; ++half) {
+        uint32_t p[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float u = __uint_as_float(x[64 * half + 2 * c]), w = __uint_as_float(x[64 * half + 2 * c + 1]);
+          fma_pair(u, w, scale, from);
+          u = ex2_approx(u);
+          w = ex2_approx(w);
+          add_pair(part[2 * (c & 1)], part[2 * (c & 1) + 1], u, w);
+          p[c] = pack2<kHalf>(u, w);
+        }
+        tmem_st32(s_mem + 32 * half, p);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.weights[buffer]);
+      l += (part[0] + part[1]) + (part[2] + part[3]);
+    }
+    // ---- the rows
+    const float by = l == 0.f ? 0.f : 1.f / l;
+    const int64_t to = it.q0 + token;
+    uint16_t* out = a.out + to * a.out_stride + (int64_t)head * kDim;
+    bool odd = !(fabsf(l) < INFINITY);
+    if (n > 0) {
+      wait(&sh.result[t], 0);
+      tc_fence_after();
+    }
+#pragma unroll 1
+    for (int c = 0; c < kDim; c += 32) {
+      uint32_t v[32];
+      if (n > 0) {
+        tmem_ld32(o_mem + c, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = 0;
+      }
+      if (valid) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          float y[8];
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            y[d] = __uint_as_float(v[e + d]);
+            odd |= !(fabsf(y[d]) < INFINITY);
+            y[d] *= by;
+          }
+          *reinterpret_cast<uint4*>(out + c + e) = pack8<kHalf>(y);
+        }
+      }
+      __syncwarp();
+    }
+    if (valid) {
+      if (a.lse) a.lse[to * a.n_heads + head] = l == 0.f ? -INFINITY : (m * scale - kShift + log2f(l)) * 0.6931471805599453f;
+      if (odd) atomicOr(&sh.word, kPromptAgain);
+    }
+    tc_fence_before();
+    __syncwarp();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == C::kLoadWarp) tmem_dealloc(tmem, 512);
+  if (tid == 0) a.words[blockIdx.x] = sh.word;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                  CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static std::atomic<EncodeTiledFn> fn{nullptr};
+  EncodeTiledFn f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+      f = reinterpret_cast<EncodeTiledFn>(p);
+      fn.store(f, std::memory_order_release);
+    } else {
+      cudaGetLastError();
+    }
+  }
+  return f;
+}
+
+// [rows, heads, kDim] with boxes of 64 columns; rows past the buffer read as zeros.
+bool make_map(CUtensorMap* map, const uint16_t* base, int dtype, int dim, int heads, int rows, int64_t stride, int box_heads, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
+  return enc(map, dtype == DDTREE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<uint16_t*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kHalf, int kDim>
+cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
+  using C = Config<kDim>;
+  static_assert(C::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
+  PromptMaps maps;
+  if (!make_map(&maps.q, a.q, a.dtype, kDim, a.n_heads, a.q_rows, a.q_stride, a.group, a.tile_tokens / C::kTiles) ||
+      !make_map(&maps.k, a.k, a.dtype, kDim, a.n_kv_heads, a.k_rows, a.k_stride, 1, C::kKeys) ||
+      !make_map(&maps.v, a.v, a.dtype, kDim, a.n_kv_heads, a.k_rows, a.v_stride, 1, C::kKeys))
+    return cudaErrorInvalidValue;
+  // The shared-memory limit belongs to the kernel on a device: set once on each.
+  static std::atomic<uint64_t> have{0};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (device & 63);
+  if (!(have.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(prompt_kernel<kHalf, kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    have.fetch_or(bit, std::memory_order_release);
+  }
+  return launch_early(prompt_kernel<kHalf, kDim>, a.max_items, C::kThreads, C::kSmem, stream, a, maps);
+}
+
+template <bool kHalf>
+cudaError_t launch_dim(const PromptArgs& a, cudaStream_t stream) {
+  return a.head_dim == 64 ? launch<kHalf, 64>(a, stream) : a.head_dim == 128 ? launch<kHalf, 128>(a, stream) : launch<kHalf, 256>(a, stream);
 }
 
 }  // namespace
@@ -17,7 +482,7 @@ __global__ void __launch_bounds__(128) prompt_all_kernel(const __grid_constant__
 int prompt_tile_tokens(int group, int head_dim) { return 128 / group * (head_dim == 256 ? 1 : 2); }
 
 cudaError_t launch_prompt(const PromptArgs& a, int num_sms, cudaStream_t stream) {
-  const cudaError_t e = launch_early(prompt_all_kernel, a.max_items, 128, 0, stream, a);
+  const cudaError_t e = a.dtype == DDTREE_FP16 ? launch_dim<true>(a, stream) : launch_dim<false>(a, stream);
   return e != cudaSuccess ? e : launch_prompt_rows(a, num_sms, stream);
 }
 
