@@ -34,26 +34,24 @@
 namespace ddtree {
 namespace {
 
-__host__ __device__ constexpr int keys_of(int dim) { return dim == 64 ? 128 : 64; }
-__host__ __device__ constexpr int ctas_of(int dim) { return dim == 256 ? 1 : 2; }
+constexpr int kWarps = 4;       // of a CTA, each with keys of its own
+constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16;       // query heads of a unit
 constexpr float kShift = 14.f;  // log2 of the factor of a probability in fp16
 
 template <int kDim>
 struct Config {
-  static constexpr int kKeys = keys_of(kDim);
-  static constexpr int kWK = 4;                         // warps along the keys of a tile
-  static constexpr int kWN = kDim == 256 ? 2 : 1;       // warps along the columns of V (all take the scores)
-  static constexpr int kThreads = 32 * kWK * kWN;       // that compute
-  static constexpr int kAllThreads = kThreads + 32;
-  static constexpr int kStages = kDim == 256 ? 5 : 4;
-  static constexpr int kTileBytes = kKeys * kDim;       // of K, and of V
-  static constexpr int kQBytes = kRows * kDim * 2;
-  static constexpr int kSmem = kStages * (2 * kTileBytes + kQBytes);
-  static constexpr int kTileRing = kStages + 2;
-  static constexpr int kCols = kDim / kWN;              // columns of a warp
-  // The warps' rows are joined in the stage just consumed, so many columns at a time.
-  static constexpr int kJoinCols = 2 * kTileBytes / (kWK * kRows * 4) < kDim ? 2 * kTileBytes / (kWK * kRows * 4) : kDim;
+  static constexpr int kWarpKeys = kDim == 256 ? 16 : 32;   // of a tile, for each warp
+  static constexpr int kKeys = kWarps * kWarpKeys;
+  static constexpr int kCtas = kDim == 64 ? 4 : kDim == 128 ? 3 : 2;  // per SM
+  static constexpr int kStages = kDim == 64 ? 3 : 2;
+  static constexpr int kHalfBytes = kWarpKeys * kDim;       // a warp's K of a tile, and its V
+  static constexpr int kStageBytes = 2 * kHalfBytes;
+  static constexpr int kSmem = kWarps * kStages * kStageBytes;
+  // Query fragments in registers for the whole unit, or read again per tile.
+  static constexpr bool kHoldQ = kDim <= 128;
+  // The warps' rows are joined in the stages just consumed, so many columns at a time.
+  static constexpr int kJoinCols = kStageBytes / (kRows * 4) < kDim ? kStageBytes / (kRows * 4) : kDim;
 };
 
 // A unit that goes on from one share to others: where its parts lie (a record
@@ -141,13 +139,6 @@ __device__ __forceinline__ Token token_of(const Draft8AttnArgs& a, int n, int ti
   return token_at(a, __ldg(a.positions + n), row_index(a, n), tile_keys);
 }
 
-struct Tile {
-  int32_t token, head;  // head: of the list, key head and 16 of its query heads
-  int32_t unit;         // ordinal within the share: its queries' place
-  int32_t flags;
-};
-enum { kFirst = 1, kLast = 2, kBegun = 4, kGoesOn = 8 };
-
 // Query heads of a unit: the first one, and how many.
 __device__ __forceinline__ int first_head(const Draft8AttnArgs& a, int head, int& rows) {
   const int kv = head / a.row_tiles, part = head - kv * a.row_tiles;
@@ -156,17 +147,16 @@ __device__ __forceinline__ int first_head(const Draft8AttnArgs& a, int head, int
 }
 
 template <bool kHalf, int kDim>
-__global__ void __launch_bounds__(Config<kDim>::kAllThreads, ctas_of(kDim)) draft8_attn_kernel(const __grid_constant__ Draft8AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_kernel(const __grid_constant__ Draft8AttnArgs a) {
   using C = Config<kDim>;
-  constexpr int kThreads = C::kThreads, kLookup = kThreads / 32;
+  constexpr int kStages = C::kStages, kWarpKeys = C::kWarpKeys;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t offsets[C::kStages][C::kKeys];              // byte offset of a key's row, -1: none
-  __shared__ __align__(16) float2 scales[C::kStages][C::kKeys];  // scale of K, log2 of that of V
-  __shared__ __align__(16) float inverse[C::kStages][C::kKeys];  // 1 / scale of V
-  __shared__ uint32_t dropped[C::kStages][C::kKeys / 32];               // keys whose scale is none
-  __shared__ Tile tiles[C::kTileRing];
-  __shared__ float top_s[C::kWK][kRows], sum_s[C::kWK][kRows];
-  __shared__ int64_t warp_sum[C::kAllThreads / 32];
+  __shared__ int64_t offsets[kWarps][32];                  // byte offset of a key's row
+  __shared__ __align__(16) float2 scales[kWarps][32];      // scale of K, log2 of that of V
+  __shared__ __align__(16) float inverse[kWarps][32];      // 1 / scale of V
+  __shared__ __align__(16) uint32_t queries[C::kHoldQ ? 1 : kDim / 16 * 32 * 4];  // fragments, lane by lane
+  __shared__ float top_s[kWarps][kRows], sum_s[kWarps][kRows];
+  __shared__ int64_t warp_sum[kWarps];
   __shared__ int start_token;
   __shared__ int64_t start_at;
   __shared__ uint32_t bits;
@@ -181,7 +171,7 @@ __global__ void __launch_bounds__(Config<kDim>::kAllThreads, ctas_of(kDim)) draf
   await_grid();
 
   // ---- the list of tiles: sums over the tokens, a run of tokens per thread
-  const int per = (a.n_tokens + C::kAllThreads - 1) / C::kAllThreads;
+  const int per = (a.n_tokens + kThreads - 1) / kThreads;
   int64_t mine = 0;
   for (int i = 0; i < per; ++i) {
     const int n = tid * per + i;
@@ -198,7 +188,7 @@ __global__ void __launch_bounds__(Config<kDim>::kAllThreads, ctas_of(kDim)) draf
   __syncthreads();
   int64_t before = inc - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < C::kAllThreads / 32; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
@@ -235,211 +225,147 @@ __global__ void __launch_bounds__(Config<kDim>::kAllThreads, ctas_of(kDim)) draf
   __syncthreads();
   const int count = (int)(end - begin);
 
-  // ---- lookups by a warp of their own, two or four keys a lane, in three steps a
-  // tile each: page numbers, then row offsets and the scales' loads, then the scales.
-  // Each step's loads are under way until the next tile's turn.
-  constexpr int kStages = C::kStages;
-  if (warp == kLookup) {
-    constexpr int kPerLane = C::kKeys / 32;
-    int cur = start_token, unit = 0;
-    Token tok = token_of(a, cur, C::kKeys);
-    const int first_bundle = (int)((uint64_t)start_at / (uint32_t)tok.tiles);
-    int tile = (int)(start_at - (int64_t)first_bundle * tok.tiles);
-    int head = (first_bundle << a.bundle_log2) + sub;
-    bool begun = tile > 0;
-    int next_pos = -1, next_row = 0;  // of the next token, loaded when the current one is entered
-    auto fetch_next = [&] {
-      if (cur + 1 < a.n_tokens) {
-        next_pos = __ldg(a.positions + cur + 1);
-        next_row = row_index(a, cur + 1);
+  // ---- the walk along the list, by every warp for itself: a tile is found some
+  // turns before it is computed, first its keys' page numbers, then, when they are
+  // here, its rows' offsets, the copies and the loads of the scales
+  struct Spot {                       // the next tile to be found
+    int token, head, tile;
+    Token tok;
+  } at;
+  at.token = start_token;
+  at.tok = token_of(a, at.token, C::kKeys);
+  {
+    const int first_bundle = (int)((uint64_t)start_at / (uint32_t)at.tok.tiles);
+    at.tile = (int)(start_at - (int64_t)first_bundle * at.tok.tiles);
+    at.head = (first_bundle << a.bundle_log2) + sub;
+  }
+  int next_pos = -1, next_row = 0;    // of the token behind it, loaded when it is entered
+  auto fetch_next = [&] {
+    if (at.token + 1 < a.n_tokens) {
+      next_pos = __ldg(a.positions + at.token + 1);
+      next_row = row_index(a, at.token + 1);
+    }
+  };
+  fetch_next();
+  const int key_lane = warp * kWarpKeys + (lane & (kWarpKeys - 1));  // this lane's key of a tile
+  int page = -1, place = -1, kv_head = 0;  // of the tile found last; place -1: no such key
+  auto find = [&] {
+    kv_head = at.head / a.row_tiles;
+    const uint32_t x = (uint32_t)at.tile * C::kKeys + key_lane;  // below 2^31 + kKeys
+    place = -1;
+    page = -1;
+    if ((int64_t)x < at.tok.seen) {
+      const int j = (int)x < at.tok.first ? (int)x : (int)x - at.tok.first + at.tok.lo;
+      const int number = a.page.quotient(j);
+      place = j - number * a.page_size;
+      page = __ldg(a.table + (int64_t)at.tok.row * a.table_stride + number);
+    }
+    if (at.tok.seen == 0 && tid == 0) atomicOr(&bits, DDTREE_ST_BAD_LENGTH);
+    if (++at.tile == at.tok.tiles) {
+      at.tile = 0;
+      at.head += 1 << a.bundle_log2;
+      if (at.head >= a.unit_heads) {
+        at.head = sub;
+        do {
+          if (++at.token >= a.n_tokens) break;  // behind the list's end nothing is found any more
+          at.tok = token_at(a, next_pos, next_row, C::kKeys);
+          fetch_next();
+        } while (at.tok.tiles == 0);
       }
-    };
-    fetch_next();
-    struct Look {
-      int page[kPerLane], place[kPerLane], kv_head;  // place -1: no such key
-      float ks[kPerLane], vs[kPerLane];
-      uint32_t have;                                 // a bit per key that has a row
-    };
-    auto begin_tile = [&](int i, Look& p) {
-      p.kv_head = head / a.row_tiles;
+    }
+  };
+  const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * C::kStageBytes;
+  constexpr int kChunks = kDim / 16, kRowsPerStep = 32 / kChunks;
+  const int copy_chunk = lane % kChunks, copy_row = lane / kChunks;
+  const uint8_t *k_src = a.k + 16 * copy_chunk, *v_src = a.v + 16 * copy_chunk;
+  // Scales of the tiles under way (0: no key), newest last.
+  float ks[kStages], vs[kStages];
+  bool has[kStages];
+  auto start = [&](int slot) {  // the copies of the tile found last
+    const bool good = page >= 0 && page < a.n_pages;
+    if (place >= 0 && !good) atomicOr(&bits, DDTREE_ST_BAD_INDEX);
+    ks[kStages - 1] = vs[kStages - 1] = 0.f;
+    has[kStages - 1] = good;
+    int64_t off = -1;
+    if (good) {
+      off = page * a.page_stride + place * a.token_stride + kv_head * a.head_stride;
+      const int64_t s = ((int64_t)page * a.blocks + a.block.quotient(place)) * a.n_kv_heads + kv_head;
+      ks[kStages - 1] = a.k_scale[s];
+      vs[kStages - 1] = a.v_scale[s];
+    }
+    __syncwarp();  // the offsets of the last tile are used, and its stage
+    offsets[warp][lane] = off;
+    const bool full = __all_sync(0xffffffffu, good);
+    __syncwarp();
+    const uint32_t stage = ring + slot * C::kStageBytes;
 #pragma unroll
-      for (int k = 0; k < kPerLane; ++k) {
-        const int64_t x = (int64_t)tile * C::kKeys + 32 * k + lane;
-        p.page[k] = -1;
-        p.place[k] = -1;
-        if (x < tok.seen) {
-          const int j = (int)(x < tok.first ? x : x - tok.first + tok.lo);
-          const int number = a.page.quotient(j);
-          p.place[k] = j - number * a.page_size;
-          p.page[k] = __ldg(a.table + (int64_t)tok.row * a.table_stride + number);
-        }
-      }
-      const bool unit_ends = tile + 1 == tok.tiles, range_ends = i + 1 == count;
-      if (lane == 0) {
-        Tile t;
-        t.token = cur;
-        t.head = head;
-        t.unit = unit;
-        t.flags = (tile == 0 || i == 0 ? kFirst : 0) | (unit_ends || range_ends ? kLast : 0) | (begun ? kBegun : 0) |
-                  (unit_ends ? 0 : kGoesOn);
-        tiles[i % C::kTileRing] = t;
-        if (tok.seen == 0) atomicOr(&bits, DDTREE_ST_BAD_LENGTH);
-        // The unit's record, where it starts; without units' own, the share's, where the share ends.
-        const bool goes_on = range_ends && !unit_ends && !begun;
-        if (unit_records ? !begun && (unit_ends || range_ends) : range_ends) {
-          Record r;
-          r.token = goes_on ? cur : -1;
-          r.head = head;
-          r.first_share = share;
-          const int64_t last = end - 1 + (tok.tiles - 1 - tile);  // the unit's last tile in the list
-          const int64_t in_longer = longer * (base + 1);
-          r.last_share = (int)(last < in_longer ? last / (base + 1) : longer + (last - in_longer) / base) * (1 << a.bundle_log2) + sub;
-          records[unit_records ? cur * a.unit_heads + head : share] = r;
-        }
-      }
-      if (unit_ends && !range_ends) {
-        tile = 0;
-        begun = false;
-        ++unit;
-        head += 1 << a.bundle_log2;
-        if (head >= a.unit_heads) {
-          head = sub;
-          do {
-            ++cur;
-            tok = token_at(a, next_pos, next_row, C::kKeys);
-            fetch_next();
-          } while (tok.tiles == 0);
-        }
+    for (int r = 0; r < kWarpKeys; r += kRowsPerStep) {
+      const int row = r + copy_row;
+      const uint32_t k_to = stage + k_at<kDim>(row, copy_chunk), v_to = stage + C::kHalfBytes + v_at<kDim>(row, copy_chunk);
+      const int64_t o = offsets[warp][row];
+      if (full) {
+        ptx::cp_async16(k_to, k_src + o);
+        ptx::cp_async16(v_to, v_src + o);
       } else {
-        ++tile;
+        ptx::cp_async16_zfill(k_to, k_src + (o < 0 ? 0 : o), o < 0 ? 0u : 16u);
+        ptx::cp_async16_zfill(v_to, v_src + (o < 0 ? 0 : o), o < 0 ? 0u : 16u);
       }
-    };
-    auto place_tile = [&](int i, Look& p) {
-      p.have = 0;
-#pragma unroll
-      for (int k = 0; k < kPerLane; ++k) {
-        const bool good = p.page[k] >= 0 && p.page[k] < a.n_pages;
-        if (p.place[k] >= 0 && !good) atomicOr(&bits, DDTREE_ST_BAD_INDEX);
-        offsets[i % kStages][32 * k + lane] =
-            good ? p.page[k] * a.page_stride + p.place[k] * a.token_stride + p.kv_head * a.head_stride : -1;
-        p.ks[k] = p.vs[k] = 0.f;
-        if (good) {
-          const int64_t s = ((int64_t)p.page[k] * a.blocks + a.block.quotient(p.place[k])) * a.n_kv_heads + p.kv_head;
-          p.ks[k] = a.k_scale[s];
-          p.vs[k] = a.v_scale[s];
-          p.have |= 1u << k;
-        }
-      }
-    };
-    auto scale_tile = [&](int i, const Look& p) {
-      const int slot = i % kStages;
-#pragma unroll
-      for (int k = 0; k < kPerLane; ++k) {
-        const bool good = p.ks[k] >= 0x1p-64f && p.ks[k] <= 0x1p96f && p.vs[k] >= 0x1p-64f && p.vs[k] <= 0x1p96f;
-        scales[slot][32 * k + lane] = good ? make_float2(p.ks[k], log2f(p.vs[k])) : make_float2(0.f, -INFINITY);
-        inverse[slot][32 * k + lane] = good ? 1.f / p.vs[k] : 0.f;
-        const uint32_t out = __ballot_sync(0xffffffffu, (p.have >> k & 1) && !good);
-        if (lane == 0) {
-          dropped[slot][k] = out;
-          if (out) atomicOr(&bits, DDTREE_ST_BAD_SCALE);
-        }
-      }
-    };
-    Look placed, ahead;
-    {
-      Look first[kStages];
-#pragma unroll
-      for (int i = 0; i < kStages; ++i)
-        if (i < count) begin_tile(i, first[i]);
-#pragma unroll
-      for (int i = 0; i < kStages; ++i)
-        if (i < count) place_tile(i, first[i]);
-      if (kStages < count) begin_tile(kStages, ahead);
-      __syncthreads();  // the copies of tiles 0 .. kStages - 2 may start
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i)
-        if (i < count) scale_tile(i, first[i]);
-      placed = first[kStages - 1];
     }
-    for (int i = 0; i < count; ++i) {
-      __syncthreads();  // tile i is computed, the copies of tile i + kStages - 1 start
-      if (i + kStages - 1 < count) scale_tile(i + kStages - 1, placed);
-      if (i + kStages < count) {
-        place_tile(i + kStages, ahead);
-        placed = ahead;
-      }
-      if (i + kStages + 1 < count) begin_tile(i + kStages + 1, ahead);
+  };
+  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+  auto all_warps = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
+
+  // The tile that is computed, apart from the one that is found.
+  int token = at.token, head = at.head, tile = at.tile;
+  Token now = at.tok;
+  bool begun = tile > 0;
+  // Each turn's copies need the page numbers found a turn before.
+  find();
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) {
+#pragma unroll
+    for (int k = 0; k + 1 < kStages; ++k) {
+      ks[k] = ks[k + 1];
+      vs[k] = vs[k + 1];
+      has[k] = has[k + 1];
     }
-    __syncthreads();
-    if (lane == 0) words[share] = bits;
-    return;
+    if (i < count) start(i);
+    commit();
+    if (i + 1 < count) find();
   }
 
-  // ---- copies: a thread has one 16-byte chunk of every kRowsPerStep-th key
-  const uint32_t ring = ptx::smem_u32(smem), q_ring = ring + kStages * 2 * C::kTileBytes;
-  constexpr int kChunks = kDim / 16, kRowsPerStep = kThreads / kChunks;
-  static_assert(C::kKeys % kRowsPerStep == 0 && kRowsPerStep % 8 == 0, "copy steps");
-  const int copy_chunk = tid % kChunks, copy_row = tid / kChunks;
-  // Steps of eight rows leave the exchange of chunks as it is.
-  const uint32_t copy_k = k_at<kDim>(copy_row, copy_chunk), copy_v = C::kTileBytes + v_at<kDim>(copy_row, copy_chunk);
-  const uint8_t *k_src = a.k + 16 * copy_chunk, *v_src = a.v + 16 * copy_chunk;
-  auto start_copies = [&](int i) {
-    if (i < count) {
-      const uint32_t stage = ring + (i % kStages) * 2 * C::kTileBytes;
-#pragma unroll
-      for (int r = 0; r < C::kKeys; r += kRowsPerStep) {
-        const int64_t off = offsets[i % kStages][copy_row + r];
-        const uint32_t size = off < 0 ? 0u : 16u;
-        ptx::cp_async16_zfill(stage + copy_k + r * kDim, k_src + (off < 0 ? 0 : off), size);
-        ptx::cp_async16_zfill(stage + copy_v + r * kDim, v_src + (off < 0 ? 0 : off), size);
-      }
-      const Tile t = tiles[i % C::kTileRing];
-      if (t.flags & kFirst) {
-        int rows;
-        const uint16_t* q = a.q + t.token * a.q_stride + (int64_t)first_head(a, t.head, rows) * kDim;
-        const uint32_t q_at = q_ring + (t.unit % kStages) * C::kQBytes;
-#pragma unroll
-        for (int e = tid; e < kRows * (kDim / 8); e += kThreads) {
-          const int r = e / (kDim / 8);
-          ptx::cp_async16_zfill(q_at + e * 16, r < rows ? q + e * 8 : a.q, r < rows ? 16u : 0u);
-        }
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-
-  __syncthreads();
-#pragma unroll 1
-  for (int i = 0; i < kStages - 1; ++i) start_copies(i);
-
-  auto computing_warps = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
-  // ---- this warp's keys of every tile, and its columns of V
-  const int wn = warp % C::kWN, wk = warp / C::kWN, g = lane >> 2, q4 = lane & 3;
-  constexpr int kWarpKeys = C::kKeys / C::kWK, kGroups = kWarpKeys / 8;  // of eight keys
-  constexpr int kChunkCols = C::kCols / 8;                               // columns of V that a lane reads: 16 or 8
-  constexpr int kTilesN = C::kCols / 8;                                  // product tiles of eight columns
-  const int key0 = wk * kWarpKeys;
-  uint32_t qf[kDim / 16][4];
+  // ---- this warp's keys of every tile
+  const int g = lane >> 2, q4 = lane & 3;
+  constexpr int kGroups = kWarpKeys / 8;     // of eight keys
+  constexpr int kChunkCols = kDim == 64 ? 8 : 16;  // columns of V that a lane reads at once
+  constexpr int kParts = kDim == 256 ? 2 : 1;      // times so many
+  constexpr int kTilesN = kDim / 8;          // product tiles of eight columns
+  uint32_t qf[C::kHoldQ ? kDim / 16 : 1][4];
   float o[kTilesN][4], top[2], sum[2], factor[2];
+  bool first = true;
+  int rows = 0, head0 = 0;
 
   for (int i = 0; i < count; ++i) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    __syncthreads();
-    start_copies(i + kStages - 1);
     const int slot = i % kStages;
-    const Tile t = tiles[i % C::kTileRing];
-    const uint32_t k_tile = ring + slot * 2 * C::kTileBytes, v_tile = k_tile + C::kTileBytes;
-    if (t.flags & kFirst) {
-      // Columns 16 q4 .. 16 q4 + 15 of every 64, of rows g and g + 8: four of them an instruction.
+    const bool unit_ends = tile + 1 == now.tiles, last = unit_ends || i + 1 == count;
+    if (first) {
+      // Queries: columns 16 q4 .. 16 q4 + 15 of every 64, of rows g and g + 8, four of them an instruction.
+      head0 = first_head(a, head, rows);
+      const uint16_t* q = a.q + token * a.q_stride + (int64_t)head0 * kDim;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const uint32_t q_at = q_ring + (t.unit % kStages) * C::kQBytes + (g + 8 * r) * kDim * 2 + q4 * 32;
+        const uint4* src = reinterpret_cast<const uint4*>(q + (int64_t)(g + 8 * r) * kDim) + 2 * q4;
+        const bool live = g + 8 * r < rows;
+        uint4 v[kDim / 32];
         float most = 0.f;
 #pragma unroll
         for (int b = 0; b < kDim / 32; ++b) {
-          const uint4 v = lds128(q_at + (b >> 1) * 128 + (b & 1) * 16);
+          v[b] = live ? src[(b >> 1) * 8 + (b & 1)] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int b = 0; b < kDim / 32; ++b) {
           float x[8];
-          unpack8<kHalf>(v, x);
+          unpack8<kHalf>(v[b], x);
 #pragma unroll
           for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
         }
@@ -451,26 +377,45 @@ __global__ void __launch_bounds__(Config<kDim>::kAllThreads, ctas_of(kDim)) draf
         factor[r] = __uint_as_float((uint32_t)(127 - up) << 23) * a.scale_log2;
 #pragma unroll
         for (int b = 0; b < kDim / 32; ++b) {
-          const uint4 v = lds128(q_at + (b >> 1) * 128 + (b & 1) * 16);
           float x[8];
-          unpack8<kHalf>(v, x);
+          unpack8<kHalf>(v[b], x);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            qf[2 * b + e][r] = pack2<true>(x[4 * e] * by, x[4 * e + 1] * by);
-            qf[2 * b + e][2 + r] = pack2<true>(x[4 * e + 2] * by, x[4 * e + 3] * by);
+            const uint32_t lo = pack2<true>(x[4 * e] * by, x[4 * e + 1] * by), hi = pack2<true>(x[4 * e + 2] * by, x[4 * e + 3] * by);
+            if constexpr (C::kHoldQ) {
+              qf[2 * b + e][r] = lo;
+              qf[2 * b + e][2 + r] = hi;
+            } else if (warp == 0) {
+              queries[((2 * b + e) * 32 + lane) * 4 + r] = lo;
+              queries[((2 * b + e) * 32 + lane) * 4 + 2 + r] = hi;
+            }
           }
         }
       }
+      if constexpr (!C::kHoldQ) all_warps();
 #pragma unroll
       for (int d = 0; d < kTilesN; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
       top[0] = top[1] = -INFINITY;
       sum[0] = sum[1] = 0.f;
     }
-    // Keys without a scale may hold anything: their rows become zeros.
-    uint32_t out = dropped[slot][key0 >> 5] >> (key0 & 31) & (kWarpKeys == 32 ? 0xffffffffu : (1u << (kWarpKeys & 31)) - 1);
+    // Scales, a key a lane; they came with the copies before the last ones.
+    uint32_t out;
+    __syncwarp();  // those of the last tile are used
+    {
+      const bool good = ks[0] >= 0x1p-64f && ks[0] <= 0x1p96f && vs[0] >= 0x1p-64f && vs[0] <= 0x1p96f;
+      scales[warp][lane] = good ? make_float2(ks[0], log2f(vs[0])) : make_float2(0.f, -INFINITY);
+      inverse[warp][lane] = good ? __frcp_rn(vs[0]) : 0.f;
+      out = __ballot_sync(0xffffffffu, i < count && has[0] && !good);
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    __syncwarp();
+    const uint32_t k_tile = ring + slot * C::kStageBytes, v_tile = k_tile + C::kHalfBytes;
     if (out) {
+      // Keys without a scale may hold anything: their rows become zeros.
+      if (lane == 0) atomicOr(&bits, DDTREE_ST_BAD_SCALE);
+      if (kWarpKeys < 32) out &= (1u << (kWarpKeys & 31)) - 1;
       for (; out; out &= out - 1) {
-        const int key = key0 + __ffs(out) - 1;
+        const int key = __ffs(out) - 1;
         if (lane < kChunks) {
           asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(k_tile + k_at<kDim>(key, lane)), "r"(0) : "memory");
           asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_tile + v_at<kDim>(key, lane)), "r"(0) : "memory");
@@ -484,15 +429,23 @@ __global__ void __launch_bounds__(Config<kDim>::kAllThreads, ctas_of(kDim)) draf
     for (int x = 0; x < kGroups; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
 #pragma unroll
     for (int b = 0; b < kDim / 64; ++b) {
+      uint32_t again[C::kHoldQ ? 1 : 4][4];
+      if constexpr (!C::kHoldQ) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 v = *reinterpret_cast<const uint4*>(&queries[((4 * b + e) * 32 + lane) * 4]);
+          again[e][0] = v.x; again[e][1] = v.y; again[e][2] = v.z; again[e][3] = v.w;
+        }
+      }
 #pragma unroll
       for (int x = 0; x < kGroups; ++x) {
-        const uint4 codes = lds128(k_tile + k_at<kDim>(key0 + 8 * x + g, 4 * b + q4));
+        const uint4 codes = lds128(k_tile + k_at<kDim>(8 * x + g, 4 * b + q4));
         const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint32_t lo, hi;
           from_codes(c[e], lo, hi);
-          mma(s[x], qf[4 * b + e], lo, hi);
+          mma(s[x], C::kHoldQ ? qf[C::kHoldQ ? 4 * b + e : 0] : again[C::kHoldQ ? 0 : e], lo, hi);
         }
       }
     }
@@ -500,8 +453,8 @@ __global__ void __launch_bounds__(Config<kDim>::kAllThreads, ctas_of(kDim)) draf
     float inv[kGroups][2], high[2] = {top[0], top[1]};
 #pragma unroll
     for (int x = 0; x < kGroups; ++x) {
-      const float4 f = *reinterpret_cast<const float4*>(&scales[slot][key0 + 8 * x + 2 * q4]);
-      const float2 w = *reinterpret_cast<const float2*>(&inverse[slot][key0 + 8 * x + 2 * q4]);
+      const float4 f = *reinterpret_cast<const float4*>(&scales[warp][8 * x + 2 * q4]);
+      const float2 w = *reinterpret_cast<const float2*>(&inverse[warp][8 * x + 2 * q4]);
       inv[x][0] = w.x;
       inv[x][1] = w.y;
       s[x][0] = fmaf(s[x][0] * factor[0], f.x, f.y);
@@ -544,98 +497,139 @@ __global__ void __launch_bounds__(Config<kDim>::kAllThreads, ctas_of(kDim)) draf
       const uint32_t p[4] = {pack2<true>(s[2 * x][0], s[2 * x][1]), pack2<true>(s[2 * x][2], s[2 * x][3]),
                              pack2<true>(s[2 * x + 1][0], s[2 * x + 1][1]), pack2<true>(s[2 * x + 1][2], s[2 * x + 1][3])};
       constexpr int kWords4 = kChunkCols / 4;
-      uint32_t c[4][kWords4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = key0 + 16 * x + 2 * q4 + (e & 1) + 8 * (e >> 1);
-        if constexpr (kChunkCols == 16) {
-          const uint4 v = lds128(v_tile + v_at<kDim>(key, wn * 8 + g));
-          c[e][0] = v.x; c[e][1] = v.y; c[e][2] = v.z; c[e][3] = v.w;
-        } else {
-          const uint2 v = lds64(v_tile + v_at<kDim>(key, g >> 1) + (g & 1) * 8);
-          c[e][0] = v.x; c[e][1] = v.y;
+      for (int part = 0; part < kParts; ++part) {
+        uint32_t c[4][kWords4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = 16 * x + 2 * q4 + (e & 1) + 8 * (e >> 1);
+          if constexpr (kChunkCols == 16) {
+            const uint4 v = lds128(v_tile + v_at<kDim>(key, part * 8 + g));
+            c[e][0] = v.x; c[e][1] = v.y; c[e][2] = v.z; c[e][3] = v.w;
+          } else {
+            const uint2 v = lds64(v_tile + v_at<kDim>(key, g >> 1) + (g & 1) * 8);
+            c[e][0] = v.x; c[e][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kWords4; ++w) {
+          uint32_t b0[4], b1[4];
+          from_codes(__byte_perm(c[0][w], c[1][w], 0x5140), b0[0], b0[1]);
+          from_codes(__byte_perm(c[0][w], c[1][w], 0x7362), b0[2], b0[3]);
+          from_codes(__byte_perm(c[2][w], c[3][w], 0x5140), b1[0], b1[1]);
+          from_codes(__byte_perm(c[2][w], c[3][w], 0x7362), b1[2], b1[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mma(o[(part * kWords4 + w) * 4 + e], p, b0[e], b1[e]);
         }
       }
-#pragma unroll
-      for (int w = 0; w < kWords4; ++w) {
-        uint32_t b0[4], b1[4];
-        from_codes(__byte_perm(c[0][w], c[1][w], 0x5140), b0[0], b0[1]);
-        from_codes(__byte_perm(c[0][w], c[1][w], 0x7362), b0[2], b0[3]);
-        from_codes(__byte_perm(c[2][w], c[3][w], 0x5140), b1[0], b1[1]);
-        from_codes(__byte_perm(c[2][w], c[3][w], 0x7362), b1[2], b1[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mma(o[4 * w + e], p, b0[e], b1[e]);
-      }
     }
-    if (!(t.flags & kLast)) continue;
-
-    // ---- the unit ends here: the warps' rows are joined through this tile's stage
-    const bool whole = !(t.flags & (kBegun | kGoesOn));
-    const int64_t part = 2 * share + (t.flags & kBegun ? 0 : 1);
-    int rows;
-    const int head = first_head(a, t.head, rows);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-      if (q4 == 0 && wn == 0) {
-        top_s[wk][g + 8 * r] = top[r];
-        sum_s[wk][g + 8 * r] = sum[r];
+    if (last) {
+      // ---- the unit ends here: the warps' rows are joined through this tile's stages
+      const bool whole = unit_ends && !begun;
+      const int64_t piece = 2 * share + (begun ? 0 : 1);
+      // The unit's record, where it starts; without units' own, the share's, where the share ends.
+      if (tid == 0 && (unit_records ? !begun : i + 1 == count)) {
+        Record r;
+        r.token = !unit_ends && !begun ? token : -1;
+        r.head = head;
+        r.first_share = share;
+        const int64_t final_tile = end - 1 + (now.tiles - 1 - tile);  // the unit's last tile in the list
+        const int64_t in_longer = longer * (base + 1);
+        r.last_share =
+            (int)(final_tile < in_longer ? final_tile / (base + 1) : longer + (final_tile - in_longer) / base) * (1 << a.bundle_log2) + sub;
+        records[unit_records ? token * a.unit_heads + head : share] = r;
       }
-    }
-    float4* buffer = reinterpret_cast<float4*>(smem + slot * 2 * C::kTileBytes);
-    constexpr int kVecs = C::kJoinCols / 4;
-    // The exchange keeps the rows and columns that eight lanes write at once on other banks.
-    auto cell = [&](int w, int r, int c4) { return buffer + (w * kRows + r) * kVecs + (c4 ^ ((r ^ ((c4 >> 3) << 1)) & 7)); };
 #pragma unroll
-    for (int pass = 0; pass < kDim / C::kJoinCols; ++pass) {
-      computing_warps();  // the stage is free: every warp is done with the tile, or with the last columns
-      // A lane has columns wn kCols + 2 q4 kChunkCols ... twice kChunkCols of them.
-      const int col0 = wn * C::kCols + 2 * q4 * kChunkCols - pass * C::kJoinCols;
-      if (col0 >= 0 && col0 < C::kJoinCols) {
+      for (int r = 0; r < 2; ++r) {
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+        if (q4 == 0) {
+          top_s[warp][g + 8 * r] = top[r];
+          sum_s[warp][g + 8 * r] = sum[r];
+        }
+      }
+      constexpr int kVecs = C::kJoinCols / 4;
+      // The exchange keeps the rows and columns that eight lanes write at once on other banks.
+      auto cell = [&](int w, int r, int c4) {
+        return reinterpret_cast<float4*>(smem + (w * kStages + slot) * C::kStageBytes) + r * kVecs + (c4 ^ ((r ^ ((c4 >> 3) << 1)) & 7));
+      };
+#pragma unroll
+      for (int pass = 0; pass < kDim / C::kJoinCols; ++pass) {
+        if (pass > 0) all_warps();  // the last columns are joined
+        __syncwarp();               // this warp is done with the stage
+        // Of every part a lane has the columns 2 q4 kChunkCols ..., twice kChunkCols of them.
+        static_assert(kParts == kDim / C::kJoinCols, "a part a pass");
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           if (g + 8 * r >= rows) continue;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int d = 0; d < kChunkCols / 4; ++d)
-              *cell(wk, g + 8 * r, (col0 + h * kChunkCols) / 4 + d) =
-                  make_float4(o[4 * d][2 * r + h], o[4 * d + 1][2 * r + h], o[4 * d + 2][2 * r + h], o[4 * d + 3][2 * r + h]);
+            for (int d = 0; d < kChunkCols / 4; ++d) {
+              const int t = pass * kChunkCols + 4 * d;
+              *cell(warp, g + 8 * r, ((2 * q4 + h) * kChunkCols) / 4 + d) =
+                  make_float4(o[t][2 * r + h], o[t + 1][2 * r + h], o[t + 2][2 * r + h], o[t + 3][2 * r + h]);
+            }
+          }
+        }
+        all_warps();
+        for (int e = tid; e < rows * kVecs; e += kThreads) {
+          const int row = e / kVecs, c4 = e - row * kVecs, col = pass * C::kJoinCols + 4 * c4;
+          float m = -INFINITY, l = 0.f;
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) m = fmaxf(m, top_s[k][row]);
+          const float ref = m == -INFINITY ? 0.f : m;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) {
+            const float w = power2(top_s[k][row] - ref);
+            const float4 u = *cell(k, row, c4);
+            l += w * sum_s[k][row];
+            x.x += w * u.x; x.y += w * u.y; x.z += w * u.z; x.w += w * u.w;
+          }
+          if (whole) {
+            const float by = l == 0.f ? 0.f : 1.f / l;
+            *reinterpret_cast<uint2*>(a.out + token * a.out_stride + (int64_t)(head0 + row) * kDim + col) =
+                make_uint2(pack2<kHalf>(x.x * by, x.y * by), pack2<kHalf>(x.z * by, x.w * by));
+            if (a.lse && col == 0)
+              a.lse[(int64_t)token * a.n_heads + head0 + row] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
+          } else {
+            reinterpret_cast<float4*>(a.ws + ws.rows)[(piece * kRows + row) * (kDim / 4) + col / 4] = x;
+            if (col == 0) reinterpret_cast<float2*>(a.ws + ws.sums)[piece * kRows + row] = make_float2(m, l);
           }
         }
       }
-      computing_warps();
-      for (int e = tid; e < rows * kVecs; e += kThreads) {
-        const int row = e / kVecs, c4 = e - row * kVecs, col = pass * C::kJoinCols + 4 * c4;
-        float m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int k = 0; k < C::kWK; ++k) m = fmaxf(m, top_s[k][row]);
-        const float ref = m == -INFINITY ? 0.f : m;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < C::kWK; ++k) {
-          const float w = power2(top_s[k][row] - ref);
-          const float4 u = *cell(k, row, c4);
-          l += w * sum_s[k][row];
-          x.x += w * u.x; x.y += w * u.y; x.z += w * u.z; x.w += w * u.w;
-        }
-        if (whole) {
-          const float by = l == 0.f ? 0.f : 1.f / l;
-          *reinterpret_cast<uint2*>(a.out + t.token * a.out_stride + (int64_t)(head + row) * kDim + col) =
-              make_uint2(pack2<kHalf>(x.x * by, x.y * by), pack2<kHalf>(x.z * by, x.w * by));
-          if (a.lse && col == 0)
-            a.lse[(int64_t)t.token * a.n_heads + head + row] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
-        } else {
-          reinterpret_cast<float4*>(a.ws + ws.rows)[(part * kRows + row) * (kDim / 4) + col / 4] = x;
-          if (col == 0) reinterpret_cast<float2*>(a.ws + ws.sums)[part * kRows + row] = make_float2(m, l);
-        }
-      }
+      all_warps();  // the stages are free again
     }
-    // The next iteration's barrier comes before this stage is filled again.
+    // ---- the next tile of this stage
+#pragma unroll
+    for (int k = 0; k + 1 < kStages; ++k) {
+      ks[k] = ks[k + 1];
+      vs[k] = vs[k + 1];
+      has[k] = has[k + 1];
+    }
+    if (i + kStages < count) start(slot);
+    commit();
+    if (i + kStages + 1 < count) find();
+    // ---- and the tile after this one
+    first = last;
+    if (unit_ends) {
+      tile = 0;
+      begun = false;
+      head += 1 << a.bundle_log2;
+      if (head >= a.unit_heads && i + 1 < count) {
+        head = sub;
+        do {
+          now = token_of(a, ++token, C::kKeys);
+        } while (now.tiles == 0);
+      }
+    } else {
+      ++tile;
+    }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
+  if (tid == 0) words[share] = bits;
 }
 
 // Joins the parts of the units that go on across shares, as the 16-bit kernel's
@@ -755,7 +749,7 @@ cudaError_t launch(const Draft8AttnArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     have.fetch_or(bit, std::memory_order_release);
   }
-  e = launch_early(draft8_attn_kernel<kHalf, kDim>, a.n_shares, C::kAllThreads, C::kSmem, stream, a);
+  e = launch_early(draft8_attn_kernel<kHalf, kDim>, a.n_shares, kThreads, C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
   // Rows get CTAs of their own where records are few, for their units have many parts.
   const int records = by_unit(a) ? a.n_tokens * a.unit_heads : a.n_shares;
@@ -773,9 +767,11 @@ cudaError_t launch_dim(const Draft8AttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int draft8_tile_keys(int head_dim) { return keys_of(head_dim); }
+int draft8_tile_keys(int head_dim) { return head_dim == 256 ? Config<256>::kKeys : Config<128>::kKeys; }
 
-int draft8_shares(int head_dim, int num_sms) { return ctas_of(head_dim) * num_sms; }
+int draft8_shares(int head_dim, int num_sms) {
+  return num_sms * (head_dim == 64 ? Config<64>::kCtas : head_dim == 128 ? Config<128>::kCtas : Config<256>::kCtas);
+}
 
 int64_t draft8_workspace_bytes(int head_dim, int n_shares) { return (layout_of(head_dim, n_shares).total + 255) / 256 * 256; }
 

