@@ -37,7 +37,7 @@ typedef struct ddtree_draft8_cache {
   float* k_scale;        /* [n_pages, blocks, n_kv_heads], contiguous             */
   float* v_scale;
   int64_t n_pages;       /* n_pages * page_size <= 2^31 - 1                       */
-  int64_t page_stride;   /* bytes, multiples of 16                                */
+  int64_t page_stride;   /* bytes, multiples of 16 below 2^36                     */
   int64_t token_stride;
   int64_t head_stride;
   int32_t page_size;     /* tokens of a page, 1 .. DDTREE_MAX_PAGE_SIZE, any number */
@@ -129,7 +129,7 @@ DDTREE_API size_t ddtree_draft8_attention_workspace_size(const ddtree_draft8_pla
  * by a power of two so that its largest element fills fp16's range (what is
  * 2^-39 of it or less is lost), scores, maxima and sums are in 32 bits, and the
  * weight p_j vscale_j of a value row is rounded to fp16 (half a step of it,
- * 2^-11) relative to the unit's largest: a row counts down to 2^-38 of that.
+ * 2^-11) relative to the unit's largest: a row counts down to 2^-34 of that.
  * The sums take p_j unrounded, and an output is rounded once.  Equal inputs
  * give equal bits.
  * Errors: as ddtree_draft_attention.

@@ -355,7 +355,9 @@ struct Draft8AttnArgs {
   uint16_t* out;             // tokens out_stride apart
   float* lse;                // [n_tokens, n_heads] or null
   uint8_t* ws;               // workspace: status block, then partial results
-  int64_t q_stride, out_stride, page_stride, token_stride, head_stride, n_pages;
+  int64_t q_stride, out_stride;
+  uint32_t page_step, token_step, head_step;  // of the cache, in 16 bytes
+  int32_t n_pages;
   float scale_log2;          // sm_scale * log2(e)
   Divider page, block;       // by the tokens of a page, of a block
   int32_t n_tokens, n_heads, n_kv_heads, group, head_dim, dtype, page_size, blocks;

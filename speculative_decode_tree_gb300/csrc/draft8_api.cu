@@ -24,7 +24,7 @@ bool cache_ok(const ddtree_draft8_cache_t* c) {
   if (c->block_tokens < 1 || c->block_tokens > c->page_size || c->block_tokens > DDTREE_DRAFT8_MAX_BLOCK / c->head_dim)
     return false;
   for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
-    if (s < c->head_dim || s % 16) return false;
+    if (s < c->head_dim || s % 16 || s / 16 > UINT32_MAX) return false;
   return true;
 }
 
@@ -255,10 +255,10 @@ extern "C" int ddtree_draft8_attention(const ddtree_draft8_plan_t* plan, const v
   a.ws = static_cast<uint8_t*>(workspace);
   a.q_stride = plan->q_stride ? plan->q_stride : width;
   a.out_stride = plan->out_stride ? plan->out_stride : width;
-  a.page_stride = cache->page_stride;
-  a.token_stride = cache->token_stride;
-  a.head_stride = cache->head_stride;
-  a.n_pages = cache->n_pages;
+  a.page_step = (uint32_t)(cache->page_stride / 16);
+  a.token_step = (uint32_t)(cache->token_stride / 16);
+  a.head_step = (uint32_t)(cache->head_stride / 16);
+  a.n_pages = (int32_t)cache->n_pages;
   a.scale_log2 = scale_log2;
   a.page = make_divider(cache->page_size);
   a.block = make_divider(cache->block_tokens);

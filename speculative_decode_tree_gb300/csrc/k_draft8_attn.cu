@@ -23,9 +23,12 @@
 //  - Scales stay out of the products.  ks_j multiplies a score; vs_j goes into
 //    the exponent: with x_j = s_j + log2 vs_j (in base 2), M = max x_j,
 //    O = sum 2^(x_j - M) vc_j,  l = sum 2^(x_j - M) / vs_j,  out = O / l.
-//    So what is rounded to fp16 is a row's weight in the result, at most 1 times
-//    a factor of 2^14, whatever the scales are.  A key that is not there has
-//    ks = 0, log2 vs = -inf and 1 / vs = 0, and needs no mask.
+//    So what is rounded to fp16 is a row's weight in the result, whatever the
+//    scales are.  A key that is not there has ks = 0, log2 vs = -inf and
+//    1 / vs = 0, and needs no mask.
+//  - What costs now is instructions: two for a pair of codes (K 1.5), and per key
+//    its lookup, scales and softmax.  Pairs of scores go through two-number
+//    instructions, and O is scaled only when a maximum has grown well.
 #include <atomic>
 
 #include "rope.cuh"
@@ -37,7 +40,10 @@ namespace {
 constexpr int kWarps = 4;       // of a CTA, each with keys of its own
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16;       // query heads of a unit
-constexpr float kShift = 14.f;  // log2 of the factor of a probability in fp16
+// A weight carries a factor of 2^kShift in fp16, and the maximum that it is
+// relative to moves only when it has grown by more than 2^kGrowth: 2^15 is the
+// largest weight, and one counts down to 2^-34 of it.
+constexpr float kShift = 10.f, kGrowth = 5.f;
 
 template <int kDim>
 struct Config {
@@ -102,6 +108,37 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   return v;
 }
 __device__ __forceinline__ float power2(float x) { return ptx::ex2_approx(x); }
+// Two numbers in 64 bits, and instructions on both.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 apart(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 // Byte offset of a 16-byte chunk of a key in its tile.  128-byte lines keep
 // their chunks exchanged so that the eight lanes of a load's quarter meet eight
@@ -152,8 +189,8 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
   constexpr int kStages = C::kStages, kWarpKeys = C::kWarpKeys;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t offsets[kWarps][32];                  // byte offset of a key's row
-  __shared__ __align__(16) float2 scales[kWarps][32];      // scale of K, log2 of that of V
-  __shared__ __align__(16) float inverse[kWarps][32];      // 1 / scale of V
+  // Of a tile's keys: scale of K, log2 of that of V, its inverse.
+  __shared__ __align__(16) float k_scales[kWarps][32], v_log2[kWarps][32], v_inverse[kWarps][32];
   __shared__ __align__(16) uint32_t queries[C::kHoldQ ? 1 : kDim / 16 * 32 * 4];  // fragments, lane by lane
   __shared__ float top_s[kWarps][kRows], sum_s[kWarps][kRows];
   __shared__ int64_t warp_sum[kWarps];
@@ -249,8 +286,10 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
   fetch_next();
   const int key_lane = warp * kWarpKeys + (lane & (kWarpKeys - 1));  // this lane's key of a tile
   int page = -1, place = -1, kv_head = 0;  // of the tile found last; place -1: no such key
+  uint64_t head_at = 0;                    // its key head's place in a token, in 16 bytes
   auto find = [&] {
-    kv_head = at.head / a.row_tiles;
+    kv_head = a.row_tiles == 1 ? at.head : at.head / a.row_tiles;
+    head_at = (uint64_t)(uint32_t)kv_head * a.head_step;
     const uint32_t x = (uint32_t)at.tile * C::kKeys + key_lane;  // below 2^31 + kKeys
     place = -1;
     page = -1;
@@ -288,8 +327,9 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
     has[kStages - 1] = good;
     int64_t off = -1;
     if (good) {
-      off = page * a.page_stride + place * a.token_stride + kv_head * a.head_stride;
-      const int64_t s = ((int64_t)page * a.blocks + a.block.quotient(place)) * a.n_kv_heads + kv_head;
+      off = ((uint64_t)(uint32_t)page * a.page_step + (uint64_t)(uint32_t)place * a.token_step + head_at) << 4;
+      const uint32_t block = (uint32_t)page * a.blocks + a.block.quotient(place);  // below n_pages * page_size
+      const uint64_t s = (uint64_t)block * (uint32_t)a.n_kv_heads + kv_head;
       ks[kStages - 1] = a.k_scale[s];
       vs[kStages - 1] = a.v_scale[s];
     }
@@ -341,7 +381,8 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
   constexpr int kParts = kDim == 256 ? 2 : 1;      // times so many
   constexpr int kTilesN = kDim / 8;          // product tiles of eight columns
   uint32_t qf[C::kHoldQ ? kDim / 16 : 1][4];
-  float o[kTilesN][4], top[2], sum[2], factor[2];
+  float o[kTilesN][4], top[2], factor[2];
+  uint64_t sum[2];
   bool first = true;
   int rows = 0, head0 = 0;
 
@@ -396,15 +437,16 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
 #pragma unroll
       for (int d = 0; d < kTilesN; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
       top[0] = top[1] = -INFINITY;
-      sum[0] = sum[1] = 0.f;
+      sum[0] = sum[1] = 0;
     }
     // Scales, a key a lane; they came with the copies before the last ones.
     uint32_t out;
     __syncwarp();  // those of the last tile are used
     {
       const bool good = ks[0] >= 0x1p-64f && ks[0] <= 0x1p96f && vs[0] >= 0x1p-64f && vs[0] <= 0x1p96f;
-      scales[warp][lane] = good ? make_float2(ks[0], log2f(vs[0])) : make_float2(0.f, -INFINITY);
-      inverse[warp][lane] = good ? __frcp_rn(vs[0]) : 0.f;
+      k_scales[warp][lane] = good ? ks[0] : 0.f;
+      v_log2[warp][lane] = good ? __log2f(vs[0]) : -INFINITY;
+      v_inverse[warp][lane] = good ? __fdividef(1.f, vs[0]) : 0.f;
       out = __ballot_sync(0xffffffffu, i < count && has[0] && !good);
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
@@ -450,31 +492,33 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
       }
     }
     // ---- weights: scores in base 2 plus log2 of the value's scale
-    float inv[kGroups][2], high[2] = {top[0], top[1]};
+    uint64_t y[kGroups][2], inv[kGroups];  // keys 2 q4 and 2 q4 + 1 of every eight, of both rows
+    const uint64_t by0 = pair(factor[0], factor[0]), by1 = pair(factor[1], factor[1]);
+    float high[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int x = 0; x < kGroups; ++x) {
-      const float4 f = *reinterpret_cast<const float4*>(&scales[warp][8 * x + 2 * q4]);
-      const float2 w = *reinterpret_cast<const float2*>(&inverse[warp][8 * x + 2 * q4]);
-      inv[x][0] = w.x;
-      inv[x][1] = w.y;
-      s[x][0] = fmaf(s[x][0] * factor[0], f.x, f.y);
-      s[x][1] = fmaf(s[x][1] * factor[0], f.z, f.w);
-      s[x][2] = fmaf(s[x][2] * factor[1], f.x, f.y);
-      s[x][3] = fmaf(s[x][3] * factor[1], f.z, f.w);
-      high[0] = fmaxf(high[0], fmaxf(s[x][0], s[x][1]));
-      high[1] = fmaxf(high[1], fmaxf(s[x][2], s[x][3]));
+      const uint64_t kf = *reinterpret_cast<const uint64_t*>(&k_scales[warp][8 * x + 2 * q4]);
+      const uint64_t vf = *reinterpret_cast<const uint64_t*>(&v_log2[warp][8 * x + 2 * q4]);
+      inv[x] = *reinterpret_cast<const uint64_t*>(&v_inverse[warp][8 * x + 2 * q4]);
+      y[x][0] = fma2(mul2(pair(s[x][0], s[x][1]), by0), kf, vf);
+      y[x][1] = fma2(mul2(pair(s[x][2], s[x][3]), by1), kf, vf);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 v = apart(y[x][r]);
+        high[r] = max3(high[r], v.x, v.y);
+      }
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       high[r] = fmaxf(high[r], __shfl_xor_sync(0xffffffffu, high[r], 1));
       high[r] = fmaxf(high[r], __shfl_xor_sync(0xffffffffu, high[r], 2));
     }
-    if (__any_sync(0xffffffffu, high[0] > top[0] || high[1] > top[1])) {
+    if (__any_sync(0xffffffffu, high[0] - top[0] > kGrowth || high[1] - top[1] > kGrowth)) {  // also the first finite ones
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float keep = top[r] == -INFINITY ? 0.f : power2(top[r] - high[r]);
-        sum[r] *= keep;
-        top[r] = high[r];
+        const float to = fmaxf(high[r], top[r]), keep = top[r] == -INFINITY ? 0.f : power2(top[r] - to);
+        sum[r] = mul2(sum[r], pair(keep, keep));
+        top[r] = to;
 #pragma unroll
         for (int d = 0; d < kTilesN; ++d) {
           o[d][2 * r] *= keep;
@@ -482,13 +526,15 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
         }
       }
     }
-    const float from[2] = {top[0] == -INFINITY ? 0.f : kShift - top[0], top[1] == -INFINITY ? 0.f : kShift - top[1]};
+    const float from0 = top[0] == -INFINITY ? 0.f : kShift - top[0], from1 = top[1] == -INFINITY ? 0.f : kShift - top[1];
 #pragma unroll
     for (int x = 0; x < kGroups; ++x) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[x][e] = power2(s[x][e] + from[e >> 1]);
-        sum[e >> 1] = fmaf(s[x][e], inv[x][e & 1], sum[e >> 1]);
+      for (int r = 0; r < 2; ++r) {
+        const float2 v = apart(add2(y[x][r], r ? pair(from1, from1) : pair(from0, from0)));
+        s[x][2 * r] = power2(v.x);
+        s[x][2 * r + 1] = power2(v.y);
+        sum[r] = fma2(pair(s[x][2 * r], s[x][2 * r + 1]), inv[x], sum[r]);
       }
     }
     // ---- O += P V: sixteen keys an instruction, of which the lane has 2 q4, 2 q4 + 1 and the same plus 8
@@ -541,11 +587,13 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+        const float2 both = apart(sum[r]);
+        float l = both.x + both.y;
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
         if (q4 == 0) {
           top_s[warp][g + 8 * r] = top[r];
-          sum_s[warp][g + 8 * r] = sum[r];
+          sum_s[warp][g + 8 * r] = l;
         }
       }
       constexpr int kVecs = C::kJoinCols / 4;

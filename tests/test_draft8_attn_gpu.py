@@ -3,7 +3,7 @@ oracle on the dequantised cache.
 
 Bound of an output: half a step of its type for the final rounding; half a step
 of fp16 (2^-11) of every weight p_j vscale_j: 2^-11 of sum |p v|; where a weight
-is subnormal in fp16 2^-25 of 2^14 units of the largest weight, so 2^-39 of
+is subnormal in fp16 2^-25, with 2^10 at least for the largest weight, so 2^-35 of
 the largest scale times the number of keys times 448; and for the 32-bit work, as
 in the 16-bit tests, two sums of D terms (codes times a query in fp16 are exact
 products) and 64 units for the sums over keys, besides 8 units of the largest
@@ -85,7 +85,7 @@ class Case:
         exponent = 8 * U * float(vs.log2().abs().max())
         score = self.dim * U * terms + exponent
         keys = max(max(self.positions), 0) + 1
-        ob = ref.abs() * half + mass * (2.0 ** -11 + 2 * (2 * score + 64 * U)[..., None]) + keys * 448 * 2.0 ** -39 * float(vs.max()) + \
+        ob = ref.abs() * half + mass * (2.0 ** -11 + 2 * (2 * score + 64 * U)[..., None]) + keys * 448 * 2.0 ** -35 * float(vs.max()) + \
             (2.0 ** -25 if self.dtype == torch.float16 else 0)
         lb = score + 8 * U * lse.abs() + 64 * U
         out, got = self.out.cpu().double(), self.lse.cpu().double()
