@@ -268,9 +268,18 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
   struct Spot {                       // the next tile to be found
     int token, head, tile;
     Token tok;
+    const int32_t* pages;
+    uint32_t seen;
+    int behind;                       // keys between the sinks and the window
   } at;
+  auto enter = [&](const Token& t) {
+    at.tok = t;
+    at.pages = a.table + (uint64_t)(uint32_t)t.row * (uint32_t)a.table_stride;
+    at.seen = (uint32_t)t.seen;
+    at.behind = t.lo - t.first;
+  };
   at.token = start_token;
-  at.tok = token_of(a, at.token, C::kKeys);
+  enter(token_of(a, at.token, C::kKeys));
   {
     const int first_bundle = (int)((uint64_t)start_at / (uint32_t)at.tok.tiles);
     at.tile = (int)(start_at - (int64_t)first_bundle * at.tok.tiles);
@@ -293,11 +302,11 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
     const uint32_t x = (uint32_t)at.tile * C::kKeys + key_lane;  // below 2^31 + kKeys
     place = -1;
     page = -1;
-    if ((int64_t)x < at.tok.seen) {
-      const int j = (int)x < at.tok.first ? (int)x : (int)x - at.tok.first + at.tok.lo;
+    if (x < at.seen) {
+      const int j = (int)x + ((int)x < at.tok.first ? 0 : at.behind);
       const int number = a.page.quotient(j);
       place = j - number * a.page_size;
-      page = __ldg(a.table + (int64_t)at.tok.row * a.table_stride + number);
+      page = __ldg(at.pages + number);
     }
     if (at.tok.seen == 0 && tid == 0) atomicOr(&bits, DDTREE_ST_BAD_LENGTH);
     if (++at.tile == at.tok.tiles) {
@@ -307,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
         at.head = sub;
         do {
           if (++at.token >= a.n_tokens) break;  // behind the list's end nothing is found any more
-          at.tok = token_at(a, next_pos, next_row, C::kKeys);
+          enter(token_at(a, next_pos, next_row, C::kKeys));
           fetch_next();
         } while (at.tok.tiles == 0);
       }
@@ -317,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
   constexpr int kChunks = kDim / 16, kRowsPerStep = 32 / kChunks;
   const int copy_chunk = lane % kChunks, copy_row = lane / kChunks;
   const uint8_t *k_src = a.k + 16 * copy_chunk, *v_src = a.v + 16 * copy_chunk;
+  const uint32_t copy_k = ring + k_at<kDim>(copy_row, copy_chunk), copy_v = ring + C::kHalfBytes + v_at<kDim>(copy_row, copy_chunk);
+  static_assert(kDim > 64 || kRowsPerStep == 8, "copy steps");
   // Scales of the tiles under way (0: no key), newest last.
   float ks[kStages], vs[kStages];
   bool has[kStages];
@@ -337,12 +348,13 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
     offsets[warp][lane] = off;
     const bool full = __all_sync(0xffffffffu, good);
     __syncwarp();
-    const uint32_t stage = ring + slot * C::kStageBytes;
+    // Steps of eight rows leave the exchange of chunks as it is, those of fewer turn one or two of its bits.
+    const uint32_t k_here = copy_k + slot * C::kStageBytes, v_here = copy_v + slot * C::kStageBytes;
 #pragma unroll
     for (int r = 0; r < kWarpKeys; r += kRowsPerStep) {
-      const int row = r + copy_row;
-      const uint32_t k_to = stage + k_at<kDim>(row, copy_chunk), v_to = stage + C::kHalfBytes + v_at<kDim>(row, copy_chunk);
-      const int64_t o = offsets[warp][row];
+      const uint32_t k_to = (k_here ^ (kDim > 64 ? (r & 1) << 6 : 0)) + r * kDim;
+      const uint32_t v_to = (v_here ^ (kDim > 64 ? (r & 6) << 4 : 0)) + r * kDim;
+      const int64_t o = offsets[warp][r + copy_row];
       if (full) {
         ptx::cp_async16(k_to, k_src + o);
         ptx::cp_async16(v_to, v_src + o);
@@ -381,6 +393,8 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
   constexpr int kParts = kDim == 256 ? 2 : 1;      // times so many
   constexpr int kTilesN = kDim / 8;          // product tiles of eight columns
   uint32_t qf[C::kHoldQ ? kDim / 16 : 1][4];
+  // Where this lane's codes lie in a stage; chunks of the other half of 128 bytes are 64 away, either way.
+  const uint32_t k_lane = ring + k_at<kDim>(g, q4), v_lane = ring + C::kHalfBytes + (kDim == 64 ? v_at<64>(2 * q4, g >> 1) + (g & 1) * 8 : v_at<kDim>(2 * q4, g));
   float o[kTilesN][4], top[2], factor[2];
   uint64_t sum[2];
   bool first = true;
@@ -465,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
       }
       __syncwarp();
     }
+    const uint32_t k_first = k_lane + slot * C::kStageBytes, v_first = v_lane + slot * C::kStageBytes;
     // ---- scores
     float s[kGroups][4];
 #pragma unroll
@@ -481,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
       }
 #pragma unroll
       for (int x = 0; x < kGroups; ++x) {
-        const uint4 codes = lds128(k_tile + k_at<kDim>(8 * x + g, 4 * b + q4));
+        const uint4 codes = lds128((k_first ^ (b & 1) << 6) + (b >> 1) * 128 + 8 * x * kDim);
         const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -548,12 +563,11 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
         uint32_t c[4][kWords4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int key = 16 * x + 2 * q4 + (e & 1) + 8 * (e >> 1);
           if constexpr (kChunkCols == 16) {
-            const uint4 v = lds128(v_tile + v_at<kDim>(key, part * 8 + g));
+            const uint4 v = lds128(v_first + (16 * x + (e & 1) + 8 * (e >> 1)) * kDim + part * 128);
             c[e][0] = v.x; c[e][1] = v.y; c[e][2] = v.z; c[e][3] = v.w;
           } else {
-            const uint2 v = lds64(v_tile + v_at<kDim>(key, g >> 1) + (g & 1) * 8);
+            const uint2 v = lds64((v_first ^ (e & 1) << 6) + (16 * x + 8 * (e >> 1)) * kDim);
             c[e][0] = v.x; c[e][1] = v.y;
           }
         }
