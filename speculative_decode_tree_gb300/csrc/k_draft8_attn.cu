@@ -47,17 +47,16 @@ constexpr float kShift = 10.f, kGrowth = 5.f;
 
 template <int kDim>
 struct Config {
-  static constexpr int kWarpKeys = kDim == 256 ? 16 : 32;   // of a tile, for each warp
-  static constexpr int kKeys = kWarps * kWarpKeys;
-  static constexpr int kCtas = kDim == 64 ? 4 : kDim == 128 ? 3 : 2;  // per SM
+  // 256 columns are halved between two warps, which add up their halves of the scores.
+  static constexpr int kHalves = kDim == 256 ? 2 : 1, kCols = kDim / kHalves;
+  static constexpr int kWarpKeys = 32;                      // of a tile, for each warp or pair
+  static constexpr int kParts = kWarps / kHalves, kKeys = kParts * kWarpKeys;
+  static constexpr int kCtas = kDim == 64 ? 4 : 3;          // per SM
   static constexpr int kStages = kDim == 64 ? 3 : 2;
-  static constexpr int kHalfBytes = kWarpKeys * kDim;       // a warp's K of a tile, and its V
+  static constexpr int kHalfBytes = kWarpKeys * kCols;      // a warp's K of a tile, and its V
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kSmem = kWarps * kStages * kStageBytes;
-  // Query fragments in registers for the whole unit, or read again per tile.
-  static constexpr bool kHoldQ = kDim <= 128;
-  // The warps' rows are joined in the stages just consumed, so many columns at a time.
-  static constexpr int kJoinCols = kStageBytes / (kRows * 4) < kDim ? kStageBytes / (kRows * 4) : kDim;
+  static_assert(kStageBytes == kRows * kCols * 4, "a warp's rows are joined in the stage just consumed");
 };
 
 // A unit that goes on from one share to others: where its parts lie (a record
@@ -186,13 +185,12 @@ __device__ __forceinline__ int first_head(const Draft8AttnArgs& a, int head, int
 template <bool kHalf, int kDim>
 __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_kernel(const __grid_constant__ Draft8AttnArgs a) {
   using C = Config<kDim>;
-  constexpr int kStages = C::kStages, kWarpKeys = C::kWarpKeys;
+  constexpr int kStages = C::kStages, kWarpKeys = C::kWarpKeys, kCols = C::kCols;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t offsets[kWarps][32];                  // byte offset of a key's row
   // Of a tile's keys: scale of K, log2 of that of V, its inverse.
   __shared__ __align__(16) float k_scales[kWarps][32], v_log2[kWarps][32], v_inverse[kWarps][32];
-  __shared__ __align__(16) uint32_t queries[C::kHoldQ ? 1 : kDim / 16 * 32 * 4];  // fragments, lane by lane
-  __shared__ float top_s[kWarps][kRows], sum_s[kWarps][kRows];
+  __shared__ float top_s[C::kParts][kRows], sum_s[C::kParts][kRows];
   __shared__ int64_t warp_sum[kWarps];
   __shared__ int start_token;
   __shared__ int64_t start_at;
@@ -293,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
     }
   };
   fetch_next();
-  const int key_lane = warp * kWarpKeys + (lane & (kWarpKeys - 1));  // this lane's key of a tile
+  const int part = warp / C::kHalves, half = warp % C::kHalves;  // keys and columns of this warp
+  const int key_lane = part * kWarpKeys + lane;                    // this lane's key of a tile
   int page = -1, place = -1, kv_head = 0;  // of the tile found last; place -1: no such key
   uint64_t head_at = 0;                    // its key head's place in a token, in 16 bytes
   auto find = [&] {
@@ -323,11 +322,10 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
     }
   };
   const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * C::kStageBytes;
-  constexpr int kChunks = kDim / 16, kRowsPerStep = 32 / kChunks;
+  constexpr int kChunks = kCols / 16, kRowsPerStep = 32 / kChunks;
   const int copy_chunk = lane % kChunks, copy_row = lane / kChunks;
-  const uint8_t *k_src = a.k + 16 * copy_chunk, *v_src = a.v + 16 * copy_chunk;
-  const uint32_t copy_k = ring + k_at<kDim>(copy_row, copy_chunk), copy_v = ring + C::kHalfBytes + v_at<kDim>(copy_row, copy_chunk);
-  static_assert(kDim > 64 || kRowsPerStep == 8, "copy steps");
+  const uint8_t *k_src = a.k + half * kCols + 16 * copy_chunk, *v_src = a.v + half * kCols + 16 * copy_chunk;
+  const uint32_t copy_k = ring + k_at<kCols>(copy_row, copy_chunk), copy_v = ring + C::kHalfBytes + v_at<kCols>(copy_row, copy_chunk);
   // Scales of the tiles under way (0: no key), newest last.
   float ks[kStages], vs[kStages];
   bool has[kStages];
@@ -348,23 +346,30 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
     offsets[warp][lane] = off;
     const bool full = __all_sync(0xffffffffu, good);
     __syncwarp();
-    // Steps of eight rows leave the exchange of chunks as it is, those of fewer turn one or two of its bits.
-    const uint32_t k_here = copy_k + slot * C::kStageBytes, v_here = copy_v + slot * C::kStageBytes;
+    // Steps of four rows turn one bit of the exchange of chunks of V, steps of eight leave it as it is.
+    const uint32_t k_to = copy_k + slot * C::kStageBytes, v_to = copy_v + slot * C::kStageBytes;
+    constexpr int kSteps = kWarpKeys / kRowsPerStep;
+    int64_t o[kSteps];
 #pragma unroll
-    for (int r = 0; r < kWarpKeys; r += kRowsPerStep) {
-      const uint32_t k_to = (k_here ^ (kDim > 64 ? (r & 1) << 6 : 0)) + r * kDim;
-      const uint32_t v_to = (v_here ^ (kDim > 64 ? (r & 6) << 4 : 0)) + r * kDim;
-      const int64_t o = offsets[warp][r + copy_row];
-      if (full) {
-        ptx::cp_async16(k_to, k_src + o);
-        ptx::cp_async16(v_to, v_src + o);
-      } else {
-        ptx::cp_async16_zfill(k_to, k_src + (o < 0 ? 0 : o), o < 0 ? 0u : 16u);
-        ptx::cp_async16_zfill(v_to, v_src + (o < 0 ? 0 : o), o < 0 ? 0u : 16u);
+    for (int r = 0; r < kSteps; ++r) o[r] = offsets[warp][r * kRowsPerStep + copy_row];
+    if (full) {
+#pragma unroll
+      for (int r = 0; r < kSteps; ++r) {
+        const uint32_t turned = kCols > 64 ? (r * kRowsPerStep & 4) << 4 : 0;
+        ptx::cp_async16(k_to + r * kRowsPerStep * kCols, k_src + o[r]);
+        ptx::cp_async16((v_to ^ turned) + r * kRowsPerStep * kCols, v_src + o[r]);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < kSteps; ++r) {
+        const uint32_t turned = kCols > 64 ? (r * kRowsPerStep & 4) << 4 : 0, size = o[r] < 0 ? 0u : 16u;
+        ptx::cp_async16_zfill(k_to + r * kRowsPerStep * kCols, k_src + (o[r] < 0 ? 0 : o[r]), size);
+        ptx::cp_async16_zfill((v_to ^ turned) + r * kRowsPerStep * kCols, v_src + (o[r] < 0 ? 0 : o[r]), size);
       }
     }
   };
   auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+  auto pair_of_warps = [&] { asm volatile("bar.sync %0, 64;" ::"r"(2 + part) : "memory"); };
   auto all_warps = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
 
   // The tile that is computed, apart from the one that is found.
@@ -389,12 +394,12 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
   // ---- this warp's keys of every tile
   const int g = lane >> 2, q4 = lane & 3;
   constexpr int kGroups = kWarpKeys / 8;     // of eight keys
-  constexpr int kChunkCols = kDim == 64 ? 8 : 16;  // columns of V that a lane reads at once
-  constexpr int kParts = kDim == 256 ? 2 : 1;      // times so many
-  constexpr int kTilesN = kDim / 8;          // product tiles of eight columns
-  uint32_t qf[C::kHoldQ ? kDim / 16 : 1][4];
+  constexpr int kChunkCols = kCols / 8;      // columns of V that a lane reads at once
+  constexpr int kTilesN = kCols / 8;         // product tiles of eight columns
+  uint32_t qf[kCols / 16][4];
   // Where this lane's codes lie in a stage; chunks of the other half of 128 bytes are 64 away, either way.
-  const uint32_t k_lane = ring + k_at<kDim>(g, q4), v_lane = ring + C::kHalfBytes + (kDim == 64 ? v_at<64>(2 * q4, g >> 1) + (g & 1) * 8 : v_at<kDim>(2 * q4, g));
+  const uint32_t k_lane = ring + k_at<kCols>(g, q4);
+  const uint32_t v_lane = ring + C::kHalfBytes + (kCols == 64 ? v_at<kCols>(2 * q4, g >> 1) + (g & 1) * 8 : v_at<kCols>(2 * q4, g));
   float o[kTilesN][4], top[2], factor[2];
   uint64_t sum[2];
   bool first = true;
@@ -414,9 +419,7 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
         uint4 v[kDim / 32];
         float most = 0.f;
 #pragma unroll
-        for (int b = 0; b < kDim / 32; ++b) {
-          v[b] = live ? src[(b >> 1) * 8 + (b & 1)] : make_uint4(0, 0, 0, 0);
-        }
+        for (int b = 0; b < kDim / 32; ++b) v[b] = live ? src[(b >> 1) * 8 + (b & 1)] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int b = 0; b < kDim / 32; ++b) {
           float x[8];
@@ -431,23 +434,17 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
         const float by = __uint_as_float((uint32_t)(up + 127) << 23);
         factor[r] = __uint_as_float((uint32_t)(127 - up) << 23) * a.scale_log2;
 #pragma unroll
-        for (int b = 0; b < kDim / 32; ++b) {
+        for (int b = 0; b < kCols / 32; ++b) {
           float x[8];
-          unpack8<kHalf>(v[b], x);
+          if constexpr (C::kHalves == 2) unpack8<kHalf>(half ? v[b + kCols / 32] : v[b], x);
+          else unpack8<kHalf>(v[b], x);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t lo = pack2<true>(x[4 * e] * by, x[4 * e + 1] * by), hi = pack2<true>(x[4 * e + 2] * by, x[4 * e + 3] * by);
-            if constexpr (C::kHoldQ) {
-              qf[2 * b + e][r] = lo;
-              qf[2 * b + e][2 + r] = hi;
-            } else if (warp == 0) {
-              queries[((2 * b + e) * 32 + lane) * 4 + r] = lo;
-              queries[((2 * b + e) * 32 + lane) * 4 + 2 + r] = hi;
-            }
+            qf[2 * b + e][r] = pack2<true>(x[4 * e] * by, x[4 * e + 1] * by);
+            qf[2 * b + e][2 + r] = pack2<true>(x[4 * e + 2] * by, x[4 * e + 3] * by);
           }
         }
       }
-      if constexpr (!C::kHoldQ) all_warps();
 #pragma unroll
       for (int d = 0; d < kTilesN; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
       top[0] = top[1] = -INFINITY;
@@ -469,12 +466,11 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
     if (out) {
       // Keys without a scale may hold anything: their rows become zeros.
       if (lane == 0) atomicOr(&bits, DDTREE_ST_BAD_SCALE);
-      if (kWarpKeys < 32) out &= (1u << (kWarpKeys & 31)) - 1;
       for (; out; out &= out - 1) {
         const int key = __ffs(out) - 1;
         if (lane < kChunks) {
-          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(k_tile + k_at<kDim>(key, lane)), "r"(0) : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_tile + v_at<kDim>(key, lane)), "r"(0) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(k_tile + k_at<kCols>(key, lane)), "r"(0) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_tile + v_at<kCols>(key, lane)), "r"(0) : "memory");
         }
       }
       __syncwarp();
@@ -485,25 +481,31 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
 #pragma unroll
     for (int x = 0; x < kGroups; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
 #pragma unroll
-    for (int b = 0; b < kDim / 64; ++b) {
-      uint32_t again[C::kHoldQ ? 1 : 4][4];
-      if constexpr (!C::kHoldQ) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint4 v = *reinterpret_cast<const uint4*>(&queries[((4 * b + e) * 32 + lane) * 4]);
-          again[e][0] = v.x; again[e][1] = v.y; again[e][2] = v.z; again[e][3] = v.w;
-        }
-      }
+    for (int b = 0; b < kCols / 64; ++b) {
 #pragma unroll
       for (int x = 0; x < kGroups; ++x) {
-        const uint4 codes = lds128((k_first ^ (b & 1) << 6) + (b >> 1) * 128 + 8 * x * kDim);
+        const uint4 codes = lds128((k_first ^ b << 6) + 8 * x * kCols);
         const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint32_t lo, hi;
           from_codes(c[e], lo, hi);
-          mma(s[x], C::kHoldQ ? qf[C::kHoldQ ? 4 * b + e : 0] : again[C::kHoldQ ? 0 : e], lo, hi);
+          mma(s[x], qf[4 * b + e], lo, hi);
         }
+      }
+    }
+    if constexpr (C::kHalves == 2) {
+      // The pair's halves add up, through where this tile's K was.
+      float4* here = reinterpret_cast<float4*>(smem + (warp * kStages + slot) * C::kStageBytes) + lane;
+      const float4* there = here + (half ? -1 : 1) * (kStages * C::kStageBytes / 16);
+      __syncwarp();
+#pragma unroll
+      for (int x = 0; x < kGroups; ++x) here[32 * x] = make_float4(s[x][0], s[x][1], s[x][2], s[x][3]);
+      pair_of_warps();
+#pragma unroll
+      for (int x = 0; x < kGroups; ++x) {
+        const float4 v = there[32 * x];
+        s[x][0] += v.x; s[x][1] += v.y; s[x][2] += v.z; s[x][3] += v.w;
       }
     }
     // ---- weights: scores in base 2 plus log2 of the value's scale
@@ -558,29 +560,26 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
       const uint32_t p[4] = {pack2<true>(s[2 * x][0], s[2 * x][1]), pack2<true>(s[2 * x][2], s[2 * x][3]),
                              pack2<true>(s[2 * x + 1][0], s[2 * x + 1][1]), pack2<true>(s[2 * x + 1][2], s[2 * x + 1][3])};
       constexpr int kWords4 = kChunkCols / 4;
+      uint32_t c[4][kWords4];
 #pragma unroll
-      for (int part = 0; part < kParts; ++part) {
-        uint32_t c[4][kWords4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (kChunkCols == 16) {
-            const uint4 v = lds128(v_first + (16 * x + (e & 1) + 8 * (e >> 1)) * kDim + part * 128);
-            c[e][0] = v.x; c[e][1] = v.y; c[e][2] = v.z; c[e][3] = v.w;
-          } else {
-            const uint2 v = lds64((v_first ^ (e & 1) << 6) + (16 * x + 8 * (e >> 1)) * kDim);
-            c[e][0] = v.x; c[e][1] = v.y;
-          }
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (kChunkCols == 16) {
+          const uint4 v = lds128(v_first + (16 * x + (e & 1) + 8 * (e >> 1)) * kCols);
+          c[e][0] = v.x; c[e][1] = v.y; c[e][2] = v.z; c[e][3] = v.w;
+        } else {
+          const uint2 v = lds64((v_first ^ (e & 1) << 6) + (16 * x + 8 * (e >> 1)) * kCols);
+          c[e][0] = v.x; c[e][1] = v.y;
         }
+      }
 #pragma unroll
-        for (int w = 0; w < kWords4; ++w) {
-          uint32_t b0[4], b1[4];
-          from_codes(__byte_perm(c[0][w], c[1][w], 0x5140), b0[0], b0[1]);
-          from_codes(__byte_perm(c[0][w], c[1][w], 0x7362), b0[2], b0[3]);
-          from_codes(__byte_perm(c[2][w], c[3][w], 0x5140), b1[0], b1[1]);
-          from_codes(__byte_perm(c[2][w], c[3][w], 0x7362), b1[2], b1[3]);
+      for (int w = 0; w < kWords4; ++w) {
+        uint32_t b0[4], b1[4];
+        from_codes(__byte_perm(c[0][w], c[1][w], 0x5140), b0[0], b0[1]);
+        from_codes(__byte_perm(c[0][w], c[1][w], 0x7362), b0[2], b0[3]);
+        from_codes(__byte_perm(c[2][w], c[3][w], 0x5140), b1[0], b1[1]);
+        from_codes(__byte_perm(c[2][w], c[3][w], 0x7362), b1[2], b1[3]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma(o[(part * kWords4 + w) * 4 + e], p, b0[e], b1[e]);
-        }
+        for (int e = 0; e < 4; ++e) mma(o[4 * w + e], p, b0[e], b1[e]);
       }
     }
     if (last) {
@@ -605,65 +604,62 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
         float l = both.x + both.y;
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (q4 == 0) {
-          top_s[warp][g + 8 * r] = top[r];
-          sum_s[warp][g + 8 * r] = l;
+        if (q4 == 0 && half == 0) {
+          top_s[part][g + 8 * r] = top[r];
+          sum_s[part][g + 8 * r] = l;
         }
       }
-      constexpr int kVecs = C::kJoinCols / 4;
+      constexpr int kVecs = kCols / 4;
       // The exchange keeps the rows and columns that eight lanes write at once on other banks.
       auto cell = [&](int w, int r, int c4) {
         return reinterpret_cast<float4*>(smem + (w * kStages + slot) * C::kStageBytes) + r * kVecs + (c4 ^ ((r ^ ((c4 >> 3) << 1)) & 7));
       };
+      if constexpr (C::kHalves == 2) pair_of_warps();  // the other one has read the scores
+      else __syncwarp();
+      // A lane has the columns 2 q4 kChunkCols ..., twice kChunkCols of them.
 #pragma unroll
-      for (int pass = 0; pass < kDim / C::kJoinCols; ++pass) {
-        if (pass > 0) all_warps();  // the last columns are joined
-        __syncwarp();               // this warp is done with the stage
-        // Of every part a lane has the columns 2 q4 kChunkCols ..., twice kChunkCols of them.
-        static_assert(kParts == kDim / C::kJoinCols, "a part a pass");
+      for (int r = 0; r < 2; ++r) {
+        if (g + 8 * r >= rows) continue;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (g + 8 * r >= rows) continue;
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int d = 0; d < kChunkCols / 4; ++d) {
-              const int t = pass * kChunkCols + 4 * d;
-              *cell(warp, g + 8 * r, ((2 * q4 + h) * kChunkCols) / 4 + d) =
-                  make_float4(o[t][2 * r + h], o[t + 1][2 * r + h], o[t + 2][2 * r + h], o[t + 3][2 * r + h]);
-            }
-          }
+          for (int t = 0; t < kChunkCols; t += 4)
+            *cell(warp, g + 8 * r, ((2 * q4 + h) * kChunkCols + t) / 4) =
+                make_float4(o[t][2 * r + h], o[t + 1][2 * r + h], o[t + 2][2 * r + h], o[t + 3][2 * r + h]);
         }
-        all_warps();
-        for (int e = tid; e < rows * kVecs; e += kThreads) {
-          const int row = e / kVecs, c4 = e - row * kVecs, col = pass * C::kJoinCols + 4 * c4;
-          float m = -INFINITY, l = 0.f;
+      }
+      all_warps();
+      for (int e = tid; e < rows * (kDim / 4); e += kThreads) {
+        const int row = e / (kDim / 4), vec = e - row * (kDim / 4), col = 4 * vec;
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-          for (int k = 0; k < kWarps; ++k) m = fmaxf(m, top_s[k][row]);
-          const float ref = m == -INFINITY ? 0.f : m;
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < C::kParts; ++k) m = fmaxf(m, top_s[k][row]);
+        const float ref = m == -INFINITY ? 0.f : m;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < kWarps; ++k) {
-            const float w = power2(top_s[k][row] - ref);
-            const float4 u = *cell(k, row, c4);
-            l += w * sum_s[k][row];
-            x.x += w * u.x; x.y += w * u.y; x.z += w * u.z; x.w += w * u.w;
-          }
-          if (whole) {
-            const float by = l == 0.f ? 0.f : 1.f / l;
-            *reinterpret_cast<uint2*>(a.out + token * a.out_stride + (int64_t)(head0 + row) * kDim + col) =
-                make_uint2(pack2<kHalf>(x.x * by, x.y * by), pack2<kHalf>(x.z * by, x.w * by));
-            if (a.lse && col == 0)
-              a.lse[(int64_t)token * a.n_heads + head0 + row] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
-          } else {
-            reinterpret_cast<float4*>(a.ws + ws.rows)[(piece * kRows + row) * (kDim / 4) + col / 4] = x;
-            if (col == 0) reinterpret_cast<float2*>(a.ws + ws.sums)[piece * kRows + row] = make_float2(m, l);
-          }
+        for (int k = 0; k < C::kParts; ++k) {
+          const float w = power2(top_s[k][row] - ref);
+          const float4 u = *cell(k * C::kHalves + vec / kVecs, row, vec % kVecs);
+          l += w * sum_s[k][row];
+          x.x += w * u.x; x.y += w * u.y; x.z += w * u.z; x.w += w * u.w;
+        }
+        if (whole) {
+          const float by = l == 0.f ? 0.f : 1.f / l;
+          *reinterpret_cast<uint2*>(a.out + token * a.out_stride + (int64_t)(head0 + row) * kDim + col) =
+              make_uint2(pack2<kHalf>(x.x * by, x.y * by), pack2<kHalf>(x.z * by, x.w * by));
+          if (a.lse && col == 0)
+            a.lse[(int64_t)token * a.n_heads + head0 + row] = l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
+        } else {
+          reinterpret_cast<float4*>(a.ws + ws.rows)[(piece * kRows + row) * (kDim / 4) + vec] = x;
+          if (col == 0) reinterpret_cast<float2*>(a.ws + ws.sums)[piece * kRows + row] = make_float2(m, l);
         }
       }
       all_warps();  // the stages are free again
     }
     // ---- the next tile of this stage
+    if constexpr (C::kHalves == 2) {
+      if (!last) pair_of_warps();  // the other one has read the scores
+    }
 #pragma unroll
     for (int k = 0; k + 1 < kStages; ++k) {
       ks[k] = ks[k + 1];
@@ -829,10 +825,12 @@ cudaError_t launch_dim(const Draft8AttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
+static_assert(Config<256>::kCtas == Config<128>::kCtas && Config<64>::kKeys == Config<128>::kKeys, "below");
+
 int draft8_tile_keys(int head_dim) { return head_dim == 256 ? Config<256>::kKeys : Config<128>::kKeys; }
 
 int draft8_shares(int head_dim, int num_sms) {
-  return num_sms * (head_dim == 64 ? Config<64>::kCtas : head_dim == 128 ? Config<128>::kCtas : Config<256>::kCtas);
+  return num_sms * (head_dim == 64 ? Config<64>::kCtas : Config<128>::kCtas);
 }
 
 int64_t draft8_workspace_bytes(int head_dim, int n_shares) { return (layout_of(head_dim, n_shares).total + 255) / 256 * 256; }
