@@ -422,7 +422,7 @@ int draft8_tile_keys(int head_dim);
 int draft8_shares(int head_dim, int num_sms);
 int64_t draft8_workspace_bytes(int head_dim, int n_shares);
 cudaError_t launch_draft8_attention(const Draft8AttnArgs& a, cudaStream_t stream);
-int prompt_tile_tokens(int group, int head_dim);
+int prompt_tile_tokens(int batch, int q_rows, int group, int head_dim);
 cudaError_t launch_prompt(const PromptArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_prompt_rows(const PromptArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_maps(const MapsArgs& a, int num_sms, cudaStream_t stream);

@@ -31,6 +31,7 @@
 //    instructions, and O is scaled only when a maximum has grown well.
 #include <atomic>
 
+#include "f32x2.cuh"
 #include "rope.cuh"
 #include "tc_ptx.cuh"
 
@@ -107,38 +108,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   return v;
 }
 __device__ __forceinline__ float power2(float x) { return ptx::ex2_approx(x); }
-// Two numbers in 64 bits, and instructions on both.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 apart(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // Byte offset of a 16-byte chunk of a key in its tile.  128-byte lines keep
 // their chunks exchanged so that the eight lanes of a load's quarter meet eight
 // different ones: for K, lanes with four chunks of two neighbouring keys; for V,

@@ -16,7 +16,8 @@
 //  - Roles: a warp that loads (TMA boxes of 64 columns, 128-byte swizzle), a warp
 //    that issues the products, and four warps for each tile's softmax, a row a
 //    thread: no exchange between threads.  S, P (in place of S) and O live in the
-//    tensor memory; P is an operand there.
+//    tensor memory; P is an operand there, and its first half is multiplied while
+//    the second is made.
 //  - The reference m moves only when a row's maximum has grown by more than 2^8
 //    (2^4 for fp16, whose probabilities carry 2^10); O is then scaled in place by
 //    the softmax warps.
@@ -33,6 +34,7 @@
 
 #include <atomic>
 
+#include "f32x2.cuh"
 #include "prompt_list.cuh"
 #include "rope.cuh"
 #include "tc_ptx.cuh"
@@ -46,20 +48,30 @@ struct PromptMaps {
   CUtensorMap q, k, v;
 };
 
-template <int kDim>
+// kTiles: product tiles of a CTA.  One tile of 64 or 128 columns leaves room for two
+// CTAs on an SM: short sequences, where a CTA's start and end are most of its time.
+template <int kDim, int kTiles>
 struct Config {
-  static constexpr int kTiles = kDim == 256 ? 1 : 2;        // of 128 rows
+  static constexpr bool kSmall = kTiles == 1 && kDim < 256;
+  static constexpr int kCtas = kSmall ? 2 : 1;              // per SM
   static constexpr int kKeys = kDim == 256 ? 64 : 128;      // of a key tile
   static constexpr int kSlabs = kDim / 64;                  // of 64 columns
   static constexpr int kQBytes = 128 * kDim * 2;
   static constexpr int kStageBytes = kKeys * kDim * 2;      // a tile of K or of V
-  static constexpr int kStages = kDim == 64 ? 10 : 5;
+  static constexpr int kStages = kDim == 64 ? (kSmall ? 4 : 10) : kSmall ? 2 : kDim == 128 ? 4 : 5;
   static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStageBytes;
-  static constexpr int kLoadWarp = 4 * kTiles, kIssueWarp = kLoadWarp + 1;
-  static constexpr int kThreads = 32 * (kIssueWarp + 1);
-  // Tensor memory: two buffers of S, then O of each tile.
-  static constexpr int kOCol = 256;
+  // Tensor memory: S of each tile (256 columns: two buffers), O of each tile.
+  static constexpr int kBuffers = kDim == 256 ? 2 : 1;      // of S, for each tile
+  static constexpr int kColumns = kSmall ? 256 : 512;
+  static constexpr int kOCol = kDim == 256 ? 256 : kTiles * kKeys;
+  static_assert(kOCol + kTiles * kDim <= kColumns, "tensor memory");
+  // Threads of a row.  With two product tiles one is enough, and the softmax warps
+  // take registers from the others; few warps are helped by two.
+  static constexpr int kSplit = kSmall ? 2 : 1, kMyKeys = kKeys / kSplit;
+  static constexpr int kLoadWarp = 4 * kTiles * kSplit, kIssueWarp = kLoadWarp + 1;
+  static constexpr int kThreads = 32 * (kTiles == 2 ? kLoadWarp + 4 : kIssueWarp + 1);
 };
+constexpr int kShortRows = 1024;
 constexpr uint64_t kDrainNs = 2000000000ull;  // for products and copies in flight where the kernel ends
 
 __host__ __device__ constexpr uint32_t product_desc(int n, bool b_mn_major, bool half) {
@@ -73,63 +85,67 @@ __device__ __forceinline__ void load_box(const CUtensorMap* map, uint32_t dst, i
       : "memory");
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-// (x, y) * s + t and (x, y) += (u, v), two numbers an instruction.
-__device__ __forceinline__ void fma_pair(float& x, float& y, float s, float t) {
-  asm("{ .reg .b64 a, b, c;\n"
-      "  mov.b64 a, {%0, %1}; mov.b64 b, {%2, %2}; mov.b64 c, {%3, %3};\n"
-      "  fma.rn.f32x2 a, a, b, c;\n"
-      "  mov.b64 {%0, %1}, a; }"
-      : "+f"(x), "+f"(y)
-      : "f"(s), "f"(t));
-}
-__device__ __forceinline__ void add_pair(float& x, float& y, float u, float v) {
-  asm("{ .reg .b64 a, b;\n"
-      "  mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3};\n"
-      "  add.rn.f32x2 a, a, b;\n"
-      "  mov.b64 {%0, %1}, a; }"
-      : "+f"(x), "+f"(y)
-      : "f"(u), "f"(v));
-}
-
 // Bits 0 .. h of a word of 32.
 __device__ __forceinline__ uint32_t bits_to(int h) { return h < 0 ? 0u : h >= 31 ? 0xffffffffu : (2u << h) - 1u; }
 
+template <int kTiles, int kSplit>
 struct Shared {
-  uint64_t full[10], empty[10];      // stages: landed, used
+  uint64_t full[10], empty[10];      // stages: landed, used by every tile
   uint64_t queries;
-  uint64_t scores[2];                // S of a buffer is complete
-  uint64_t weights[2];               // P is written
+  uint64_t scores[2];                // S of a tile (256 columns: of a buffer) is complete
+  uint64_t weights[2][2];            // 64 keys of P are written, by each half's threads
   uint64_t products;                 // 256 columns: PV of a key tile is complete
   uint64_t result[2];                // O of a tile is complete
   uint64_t drained;
+  float tops[2][kTiles][2][kSplit == 2 ? 128 : 1];  // of even and odd key tiles, of both halves: the rows' maxima; at the end their sums
   uint32_t base, word;
-  int scratch[20];
+  int scratch[28];
 };
 
-template <bool kHalf, int kDim>
-__global__ void __launch_bounds__(Config<kDim>::kThreads, 1) prompt_kernel(const __grid_constant__ PromptArgs a,
-                                                                          const __grid_constant__ PromptMaps maps) {
-  using C = Config<kDim>;
+template <bool kHalf, int kDim, int kTiles>
+__global__ void __launch_bounds__(Config<kDim, kTiles>::kThreads, Config<kDim, kTiles>::kCtas)
+prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps) {
+  using C = Config<kDim, kTiles>;
+  constexpr int kSplit = C::kSplit;
   extern __shared__ uint8_t smem[];
-  __shared__ Shared sh;
+  __shared__ Shared<kTiles, kSplit> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int kv = blockIdx.x % a.n_kv_heads;
+  // What needs no data comes before the wait for the stream's last kernel.
+  if (warp == C::kLoadWarp) {
+    if (elect_one()) {
+      for (const CUtensorMap* m : {&maps.q, &maps.k, &maps.v}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
+    __syncwarp();
+    tmem_alloc(&sh.base, C::kColumns);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    sh.word = 0;
+    mbar_init(&sh.queries, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.scores[i], 1);
+      for (int h = 0; h < 2; ++h) mbar_init(&sh.weights[i][h], 4);
+      mbar_init(&sh.result[i], 1);
+    }
+    mbar_init(&sh.products, 1);
+    mbar_init(&sh.drained, 1);
+  }
   release_grid();
   await_grid();
+  tc_fence_before();
   PromptItem it;
   const int got = find_prompt_item<C::kThreads>(a, blockIdx.x / a.n_kv_heads, sh.scratch, it);
+  tc_fence_after();
+  const uint32_t tmem = sh.base;
   if (got) {
     if (tid == 0) a.words[blockIdx.x] = got == 2 ? DDTREE_ST_BAD_LENGTH : 0;
+    if (warp == C::kLoadWarp) tmem_dealloc(tmem, C::kColumns);
     return;
   }
 
   // ---- the key tiles: sinks before every row's window, then from the first row's window on
-  const int tile_tokens = a.tile_tokens / C::kTiles;
+  const int tile_tokens = a.tile_tokens / kTiles;
   const int lo_min = a.window > 0 ? max(0, it.pos - a.window + 1) : 0, sinks = min(a.n_sinks, lo_min);
   const int sink_tiles = (sinks + C::kKeys - 1) / C::kKeys;
   auto tiles_of = [&](int t) {  // key tiles of product tile t
@@ -137,34 +153,17 @@ __global__ void __launch_bounds__(Config<kDim>::kThreads, 1) prompt_kernel(const
     return t * tile_tokens >= it.tokens || last < 0 ? 0 : sink_tiles + (last - lo_min + C::kKeys) / C::kKeys;
   };
   auto start_of = [&](int i) { return i < sink_tiles ? i * C::kKeys : lo_min + (i - sink_tiles) * C::kKeys; };
-  const int n_of[2] = {tiles_of(0), C::kTiles == 2 ? tiles_of(1) : 0};
-  const int count = max(n_of[0], n_of[1]), present = C::kTiles == 2 && n_of[1] > 0 ? 2 : 1;
-
+  const int n_of[2] = {tiles_of(0), kTiles == 2 ? tiles_of(1) : 0};
+  const int count = max(n_of[0], n_of[1]), present = n_of[1] > 0 ? 2 : 1;
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
-    mbar_init(&sh.queries, 1);
-    mbar_init(&sh.products, 1);
-    mbar_init(&sh.drained, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.scores[i], 1);
-      mbar_init(&sh.weights[i], 4);
-      mbar_init(&sh.result[i], 1);
-    }
     fence_mbar_init();
-    sh.word = 0;
   }
-  if (warp == C::kLoadWarp) {
-    tmem_alloc(&sh.base, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.base;
-  const uint32_t q_at = (smem_u32(smem) + 1023) & ~1023u, ring = q_at + C::kTiles * C::kQBytes;
+  const uint32_t q_at = (smem_u32(smem) + 1023) & ~1023u, ring = q_at + kTiles * C::kQBytes;
   bool late = false;
   auto wait = [&](uint64_t* bar, int phase) {  // by a whole warp
     if (late) return;
@@ -175,141 +174,154 @@ __global__ void __launch_bounds__(Config<kDim>::kThreads, 1) prompt_kernel(const
     }
   };
 
-  if (warp == C::kLoadWarp) {
-    if (count > 0 && elect_one()) {
-      mbar_arrive_expect_tx(&sh.queries, present * C::kSlabs * tile_tokens * a.group * 128);
-      for (int t = 0; t < present; ++t)
-        for (int s = 0; s < C::kSlabs; ++s)
-          load_box(&maps.q, q_at + t * C::kQBytes + s * 16384, 64 * s, kv * a.group, it.q0 + t * tile_tokens, &sh.queries);
-    }
-    __syncwarp();
-    int n = 0;
-    for (; n < 2 * count; ++n) {  // K of tile 0, V of tile 0, K of tile 1, ...
-      const int stage = n % C::kStages;
-      if (n >= C::kStages) wait(&sh.empty[stage], n / C::kStages - 1);
-      if (late) break;  // a stage that may be on its way is not filled again
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&sh.full[stage], C::kStageBytes);
-        const int row = it.k0 + start_of(n >> 1);
-#pragma unroll
-        for (int s = 0; s < C::kSlabs; ++s)
-          load_box(n & 1 ? &maps.v : &maps.k, ring + stage * C::kStageBytes + s * C::kKeys * 128, 64 * s, kv, row, &sh.full[stage]);
-      }
-      __syncwarp();
-    }
-    // Nothing of this may be on its way when the CTA ends.
-    if (count > 0) mbar_wait(&sh.queries, 0, kDrainNs);
-    for (int i = max(0, n - C::kStages); i < n; ++i) mbar_wait(&sh.full[i % C::kStages], (i / C::kStages) & 1, kDrainNs);
-  } else if (warp == C::kIssueWarp) {
-    auto stage_of = [&](int n) { return ring + (n % C::kStages) * C::kStageBytes; };
-    auto landed = [&](int n) {
-      wait(&sh.full[n % C::kStages], n / C::kStages);
-      tc_fence_after();
-    };
-    // By one thread: scores of tile t (into its buffer) with key tile i, its sums with the values of key tile i.
-    auto score = [&](int t, int buffer, int i) {
-      const uint32_t k_at = stage_of(2 * i);
-#pragma unroll
-      for (int s = 0; s < C::kSlabs; ++s)
-        mma_ss_x4<2, 2>(tmem + buffer * C::kKeys, desc_sw128(q_at + t * C::kQBytes + s * 16384, 16, 1024),
-                        desc_sw128(k_at + s * C::kKeys * 128, 16, 1024), product_desc(C::kKeys, false, kHalf), s > 0);
-      mma_commit(&sh.scores[buffer]);
-    };
-    auto accumulate = [&](int t, int buffer, int i) {
-      const uint32_t v_at = stage_of(2 * i + 1);
-#pragma unroll
-      for (int c = 0; c < C::kKeys / 64; ++c)
-        mma_ts_x4_step<128>(tmem + C::kOCol + t * kDim, tmem + buffer * C::kKeys + 32 * c, desc_sw128(v_at + c * 64 * 128, C::kKeys * 128, 1024),
-                            product_desc(kDim, true, kHalf), c > 0 || i > 0);
-    };
-    if (count > 0) {
-      wait(&sh.queries, 0);
-      landed(0);
-      if (elect_one()) {
+  if (warp >= C::kLoadWarp) {
+    // 384 threads have 168 registers; 128 x 80 and 256 x 208 are fewer.
+    if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == C::kLoadWarp) {
+      if (count > 0 && elect_one()) {
+        mbar_arrive_expect_tx(&sh.queries, present * C::kSlabs * tile_tokens * a.group * 128);
         for (int t = 0; t < present; ++t)
-          if (n_of[t] > 0) score(t, t, 0);
-        mma_commit(&sh.empty[0]);
+          for (int s = 0; s < C::kSlabs; ++s)
+            load_box(&maps.q, q_at + t * C::kQBytes + s * 16384, 64 * s, kv * a.group, it.q0 + t * tile_tokens, &sh.queries);
       }
       __syncwarp();
-    }
-    if constexpr (C::kTiles == 2) {
-      for (int i = 0; i < count; ++i) {
-        landed(2 * i + 1);
-        if (i + 1 < count) landed(2 * i + 2);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (i >= n_of[t]) continue;
-          wait(&sh.weights[t], i);
-          tc_fence_after();
-          if (elect_one()) {
-            accumulate(t, t, i);
-            if (t == present - 1) mma_commit(&sh.empty[(2 * i + 1) % C::kStages]);
-            if (i + 1 < n_of[t]) score(t, t, i + 1);
-            else mma_commit(&sh.result[t]);
-            if (t == present - 1 && i + 1 < count) mma_commit(&sh.empty[(2 * i + 2) % C::kStages]);
-          }
-          __syncwarp();
-        }
-      }
-    } else {
-      for (int i = 0; i < count; ++i) {
-        if (i + 1 < count) {
-          landed(2 * i + 2);
-          if (elect_one()) {
-            score(0, (i + 1) & 1, i + 1);
-            mma_commit(&sh.empty[(2 * i + 2) % C::kStages]);
-          }
-          __syncwarp();
-        }
-        landed(2 * i + 1);
-        wait(&sh.weights[i & 1], i >> 1);
-        tc_fence_after();
+      int n = 0;
+      for (; n < 2 * count; ++n) {  // K of tile 0, V of tile 0, K of tile 1, ...
+        const int stage = n % C::kStages;
+        if (n >= C::kStages) wait(&sh.empty[stage], n / C::kStages - 1);
+        if (late) break;  // a stage that may be on its way is not filled again
         if (elect_one()) {
-          accumulate(0, i & 1, i);
-          mma_commit(&sh.empty[(2 * i + 1) % C::kStages]);
-          mma_commit(&sh.products);
-          if (i + 1 == count) mma_commit(&sh.result[0]);
+          mbar_arrive_expect_tx(&sh.full[stage], C::kStageBytes);
+          const int row = it.k0 + start_of(n >> 1);
+#pragma unroll
+          for (int s = 0; s < C::kSlabs; ++s)
+            load_box(n & 1 ? &maps.v : &maps.k, ring + stage * C::kStageBytes + s * C::kKeys * 128, 64 * s, kv, row, &sh.full[stage]);
         }
         __syncwarp();
       }
+      // Nothing of this may be on its way when the CTA ends.
+      if (count > 0) mbar_wait(&sh.queries, 0, kDrainNs);
+      for (int i = max(0, n - C::kStages); i < n; ++i) mbar_wait(&sh.full[i % C::kStages], (i / C::kStages) & 1, kDrainNs);
     }
-    // After an expired wait products may be in flight still.
-    if (elect_one()) {
-      mma_commit(&sh.drained);
-      mbar_wait(&sh.drained, 0, kDrainNs);
+    if (warp == C::kIssueWarp) {
+      // ---- products: one warp for both tiles.  With one for each, the tiles' products
+      // interleave and their softmaxes meet (16,384 tokens x 16 heads of 128: 1,050 us
+      // instead of 750).
+      auto stage_of = [&](int n) { return ring + (n % C::kStages) * C::kStageBytes; };
+      auto s_of = [&](int t, int i) { return tmem + (C::kBuffers == 2 ? i & 1 : t) * C::kKeys; };
+      auto landed = [&](int n) {
+        wait(&sh.full[n % C::kStages], n / C::kStages);
+        tc_fence_after();
+      };
+      // By one thread: S of tile t and key tile i; 64 keys of its O += P V.
+      auto score = [&](int t, int i) {
+        const uint32_t k_at = stage_of(2 * i);
+#pragma unroll
+        for (int s = 0; s < C::kSlabs; ++s)
+          mma_ss_x4<2, 2>(s_of(t, i), desc_sw128(q_at + t * C::kQBytes + s * 16384, 16, 1024), desc_sw128(k_at + s * C::kKeys * 128, 16, 1024),
+                          product_desc(C::kKeys, false, kHalf), s > 0);
+        mma_commit(&sh.scores[C::kBuffers == 2 ? i & 1 : t]);
+      };
+      auto accumulate = [&](int t, int i, int h) {
+        mma_ts_x4_step<128>(tmem + C::kOCol + t * kDim, s_of(t, i) + 32 * h, desc_sw128(stage_of(2 * i + 1) + h * 64 * 128, C::kKeys * 128, 1024),
+                            product_desc(kDim, true, kHalf), h > 0 || i > 0);
+      };
+      auto used = [&](int n) { mma_commit(&sh.empty[n % C::kStages]); };
+      if (count > 0) {
+        wait(&sh.queries, 0);
+        landed(0);
+        if (elect_one()) {
+          for (int t = 0; t < present; ++t)
+            if (n_of[t] > 0) score(t, 0);
+          used(0);
+        }
+        __syncwarp();
+      }
+      for (int i = 0; i < count; ++i) {
+        const bool more = i + 1 < count;
+        if (more) landed(2 * i + 2);
+        if (C::kBuffers == 2 && more) {  // the next scores go to the other buffer
+          if (elect_one()) {
+            score(0, i + 1);
+            used(2 * i + 2);
+          }
+          __syncwarp();
+        }
+        landed(2 * i + 1);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          if (i >= n_of[t]) continue;
+          const int w = C::kBuffers == 2 ? i & 1 : t;
+#pragma unroll
+          for (int h = 0; h < C::kKeys / 64; ++h) {
+            wait(&sh.weights[w][h], C::kBuffers == 2 ? i >> 1 : i);
+            tc_fence_after();
+            if (elect_one()) {
+              accumulate(t, i, h);
+              if (h == C::kKeys / 64 - 1) {
+                if (C::kBuffers == 2) mma_commit(&sh.products);
+                if (i + 1 == n_of[t]) mma_commit(&sh.result[t]);
+                else if (C::kBuffers == 1) score(t, i + 1);  // where P was
+              }
+            }
+            __syncwarp();
+          }
+        }
+        if (elect_one()) {
+          used(2 * i + 1);
+          if (C::kBuffers == 1 && more) used(2 * i + 2);
+        }
+        __syncwarp();
+      }
+      // After an expired wait products may be in flight still.
+      if (elect_one()) {
+        mma_commit(&sh.drained);
+        mbar_wait(&sh.drained, 0, kDrainNs);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
-    // ---- softmax: a row a thread
-    const int t = C::kTiles == 2 ? warp >> 2 : 0, quarter = warp & 3, row = quarter * 32 + lane;
+    if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---- softmax: a row a thread, or half a row's keys
+    const int t = warp / (4 * kSplit), quarter = warp & 3, half = kSplit == 2 ? (warp >> 2) & 1 : 0, row = quarter * 32 + lane;
     const int n = n_of[t], token = t * tile_tokens + row / a.group, head = kv * a.group + row % a.group;
     const bool valid = row < tile_tokens * a.group && token < it.tokens;
     // Rows that are none are computed like the last one, and not stored.
     const int pos = it.pos + (valid ? token : it.tokens - 1);
     const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    const uint32_t my_lane = (uint32_t)(quarter * 32) << 16, o_mem = tmem + C::kOCol + t * kDim + my_lane;
+    constexpr int kMine = kDim / kSplit;  // columns of O of this thread
+    const uint32_t my_lane = (uint32_t)(quarter * 32) << 16, o_mem = tmem + C::kOCol + t * kDim + half * kMine + my_lane;
     constexpr float kShift = kHalf ? 10.f : 0.f, kGrowth = kHalf ? 4.f : 8.f;
     const float scale = fmaxf(fabsf(a.scale_log2), 1.4e-45f);  // its sign goes to the scores; zero becomes the least number
+    const uint64_t scales = pair(scale, scale);
+    // What the other half of a row has to say, once a key tile.
+    auto exchange = [&](int i, float mine) {
+      if (kSplit == 1) return mine;
+      sh.tops[i & 1][t][half][row] = mine;
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * t + quarter) : "memory");
+      return sh.tops[i & 1][t][half ^ 1][row];
+    };
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < n; ++i) {
-      const int buffer = C::kTiles == 2 ? t : i & 1;
-      wait(&sh.scores[buffer], C::kTiles == 2 ? i : i >> 1);
+      const int buffer = C::kBuffers == 2 ? i & 1 : t;
+      wait(&sh.scores[buffer], C::kBuffers == 2 ? i >> 1 : i);
       tc_fence_after();
-      const uint32_t s_mem = tmem + buffer * C::kKeys + my_lane;
-      uint32_t x[C::kKeys];
-      if constexpr (C::kKeys == 128) tmem_ld128(s_mem, x);
+      const uint32_t s_mem = tmem + buffer * C::kKeys + C::kMyKeys * half + my_lane;
+      const uint32_t p_mem = tmem + buffer * C::kKeys + C::kMyKeys / 2 * half + my_lane;
+      uint32_t x[C::kMyKeys];
+      if constexpr (C::kMyKeys == 128) tmem_ld128(s_mem, x);
       else tmem_ld64(s_mem, x);
       if (a.scale_log2 < 0.f) {
 #pragma unroll
-        for (int c = 0; c < C::kKeys; ++c) x[c] ^= 0x80000000u;
+        for (int c = 0; c < C::kMyKeys; ++c) x[c] ^= 0x80000000u;
       }
       // Columns up to `high`, and of those the ones from `low` on or below `sink`.
-      const int start = start_of(i);
+      const int start = start_of(i) + C::kMyKeys * half;
       const int high = min(pos, (i < sink_tiles ? sinks : it.keys) - 1) - start;
       const int low = i < sink_tiles ? 0 : lo - start, sink = a.n_sinks - start;
-      if (__any_sync(0xffffffffu, high < C::kKeys - 1 || (low > 0 && sink < min(low, C::kKeys)))) {
+      if (__any_sync(0xffffffffu, high < C::kMyKeys - 1 || (low > 0 && sink < min(low, C::kMyKeys)))) {
 #pragma unroll
-        for (int w = 0; w < C::kKeys / 32; ++w) {
+        for (int w = 0; w < C::kMyKeys / 32; ++w) {
           const uint32_t seen = bits_to(high - 32 * w) & (~bits_to(low - 1 - 32 * w) | bits_to(max(sink, 0) - 1 - 32 * w));
 #pragma unroll
           for (int c = 0; c < 32; ++c)
@@ -318,11 +330,12 @@ __global__ void __launch_bounds__(Config<kDim>::kThreads, 1) prompt_kernel(const
       }
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < C::kKeys; c += 8) {
+      for (int c = 0; c < C::kMyKeys; c += 8) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
       }
-      const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      most = fmaxf(most, exchange(i, most));
       bool raised = false;
       float keep = 1.f;
       if (valid && (most - m) * scale > kGrowth) {  // also the first finite maximum
@@ -332,13 +345,13 @@ __global__ void __launch_bounds__(Config<kDim>::kThreads, 1) prompt_kernel(const
         l *= keep;
       }
       if (i > 0 && __any_sync(0xffffffffu, raised)) {
-        // Two tiles: these scores came after the last product, which is complete.
-        if constexpr (C::kTiles == 1) {
+        // With one buffer these scores came after the last product, which is complete.
+        if constexpr (C::kBuffers == 2) {
           wait(&sh.products, i - 1);
           tc_fence_after();
         }
 #pragma unroll 1
-        for (int c = 0; c < kDim; c += 32) {
+        for (int c = 0; c < kMine; c += 32) {
           uint32_t v[32];
           tmem_ld32(o_mem + c, v);
 #pragma unroll
@@ -347,40 +360,41 @@ __global__ void __launch_bounds__(Config<kDim>::kThreads, 1) prompt_kernel(const
         }
       }
       const float from = m == -INFINITY ? 0.f : kShift - m * scale;
+      const uint64_t froms = pair(from, from);
       // A tile's sum first, then the row's: tens of thousands of equal terms one by
       // one would lose four digits.
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t part[2] = {0, 0};
 #pragma unroll
-      for (int half = 0; half < C::kKeys / 64; ++half) {
+      for (int h = 0; h < C::kMyKeys / 64; ++h) {
         uint32_t p[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-          float u = __uint_as_float(x[64 * half + 2 * c]), w = __uint_as_float(x[64 * half + 2 * c + 1]);
-          fma_pair(u, w, scale, from);
-          u = ex2_approx(u);
-          w = ex2_approx(w);
-          add_pair(part[2 * (c & 1)], part[2 * (c & 1) + 1], u, w);
+          const float2 y = apart(fma2(pair(__uint_as_float(x[64 * h + 2 * c]), __uint_as_float(x[64 * h + 2 * c + 1])), scales, froms));
+          const float u = ex2_approx(y.x), w = ex2_approx(y.y);
+          part[c & 1] = add2(part[c & 1], pair(u, w));
           p[c] = pack2<kHalf>(u, w);
         }
-        tmem_st32(s_mem + 32 * half, p);
+        tmem_st32(p_mem + 32 * h, p);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.weights[buffer][half + h]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.weights[buffer]);
-      l += (part[0] + part[1]) + (part[2] + part[3]);
+      const float2 sums = apart(add2(part[0], part[1]));
+      l += sums.x + sums.y;
     }
+    l += kSplit == 1 ? 0.f : exchange(n, l);
     // ---- the rows
     const float by = l == 0.f ? 0.f : 1.f / l;
     const int64_t to = it.q0 + token;
-    uint16_t* out = a.out + to * a.out_stride + (int64_t)head * kDim;
+    uint16_t* out = a.out + to * a.out_stride + (int64_t)head * kDim + half * kMine;
     bool odd = !(fabsf(l) < INFINITY);
     if (n > 0) {
       wait(&sh.result[t], 0);
       tc_fence_after();
     }
 #pragma unroll 1
-    for (int c = 0; c < kDim; c += 32) {
+    for (int c = 0; c < kMine; c += 32) {
       uint32_t v[32];
       if (n > 0) {
         tmem_ld32(o_mem + c, v);
@@ -404,7 +418,7 @@ __global__ void __launch_bounds__(Config<kDim>::kThreads, 1) prompt_kernel(const
       __syncwarp();
     }
     if (valid) {
-      if (a.lse) a.lse[to * a.n_heads + head] = l == 0.f ? -INFINITY : (m * scale - kShift + log2f(l)) * 0.6931471805599453f;
+      if (a.lse && half == 0) a.lse[to * a.n_heads + head] = l == 0.f ? -INFINITY : (m * scale - kShift + log2f(l)) * 0.6931471805599453f;
       if (odd) atomicOr(&sh.word, kPromptAgain);
     }
     tc_fence_before();
@@ -412,7 +426,7 @@ __global__ void __launch_bounds__(Config<kDim>::kThreads, 1) prompt_kernel(const
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == C::kLoadWarp) tmem_dealloc(tmem, 512);
+  if (warp == C::kLoadWarp) tmem_dealloc(tmem, C::kColumns);
   if (tid == 0) a.words[blockIdx.x] = sh.word;
 }
 
@@ -449,12 +463,12 @@ bool make_map(CUtensorMap* map, const uint16_t* base, int dtype, int dim, int he
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kHalf, int kDim>
+template <bool kHalf, int kDim, int kTiles>
 cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
-  using C = Config<kDim>;
-  static_assert(C::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
+  using C = Config<kDim, kTiles>;
+  static_assert(C::kCtas * (C::kSmem + sizeof(Shared<kTiles, C::kSplit>) + 1024) <= 228 * 1024 && C::kStages <= 10, "shared memory");
   PromptMaps maps;
-  if (!make_map(&maps.q, a.q, a.dtype, kDim, a.n_heads, a.q_rows, a.q_stride, a.group, a.tile_tokens / C::kTiles) ||
+  if (!make_map(&maps.q, a.q, a.dtype, kDim, a.n_heads, a.q_rows, a.q_stride, a.group, a.tile_tokens / kTiles) ||
       !make_map(&maps.k, a.k, a.dtype, kDim, a.n_kv_heads, a.k_rows, a.k_stride, 1, C::kKeys) ||
       !make_map(&maps.v, a.v, a.dtype, kDim, a.n_kv_heads, a.k_rows, a.v_stride, 1, C::kKeys))
     return cudaErrorInvalidValue;
@@ -465,21 +479,29 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (device & 63);
   if (!(have.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(prompt_kernel<kHalf, kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(prompt_kernel<kHalf, kDim, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     have.fetch_or(bit, std::memory_order_release);
   }
-  return launch_early(prompt_kernel<kHalf, kDim>, a.max_items, C::kThreads, C::kSmem, stream, a, maps);
+  return launch_early(prompt_kernel<kHalf, kDim, kTiles>, a.max_items, C::kThreads, C::kSmem, stream, a, maps);
 }
+
+// Whether sequences are short: rows of an average one.
+bool prompt_short(int batch, int q_rows, int group) { return (int64_t)q_rows * group < (int64_t)batch * kShortRows; }
 
 template <bool kHalf>
 cudaError_t launch_dim(const PromptArgs& a, cudaStream_t stream) {
-  return a.head_dim == 64 ? launch<kHalf, 64>(a, stream) : a.head_dim == 128 ? launch<kHalf, 128>(a, stream) : launch<kHalf, 256>(a, stream);
+  const bool two = a.tile_tokens > 128 / a.group;
+  return a.head_dim == 256   ? launch<kHalf, 256, 1>(a, stream)
+         : a.head_dim == 128 ? (two ? launch<kHalf, 128, 2>(a, stream) : launch<kHalf, 128, 1>(a, stream))
+                             : (two ? launch<kHalf, 64, 2>(a, stream) : launch<kHalf, 64, 1>(a, stream));
 }
 
 }  // namespace
 
-int prompt_tile_tokens(int group, int head_dim) { return 128 / group * (head_dim == 256 ? 1 : 2); }
+int prompt_tile_tokens(int batch, int q_rows, int group, int head_dim) {
+  return 128 / group * (head_dim == 256 || prompt_short(batch, q_rows, group) ? 1 : 2);
+}
 
 cudaError_t launch_prompt(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   const cudaError_t e = a.dtype == DDTREE_FP16 ? launch_dim<true>(a, stream) : launch_dim<false>(a, stream);

@@ -32,7 +32,7 @@ int64_t workspace_of(int64_t items) { return 256 + (items * 4 + 255) / 256 * 256
 bool plan_ok(const ddtree_prompt_plan_t* p) {
   if (!p || !sizes_ok(p->batch, p->q_rows, p->k_rows, p->n_heads, p->n_kv_heads, p->head_dim, p->dtype, p->window, p->n_sinks))
     return false;
-  if (p->tile_tokens != prompt_tile_tokens(p->n_heads / p->n_kv_heads, p->head_dim) || p->wait_limit_us < 0) return false;
+  if (p->tile_tokens != prompt_tile_tokens(p->batch, p->q_rows, p->n_heads / p->n_kv_heads, p->head_dim) || p->wait_limit_us < 0) return false;
   const int64_t items = items_of(p->batch, p->q_rows, p->n_kv_heads, p->tile_tokens);
   if (items > INT32_MAX || p->max_items != items || p->workspace_bytes != workspace_of(items)) return false;
   const int64_t width = (int64_t)p->n_heads * p->head_dim, kv_width = (int64_t)p->n_kv_heads * p->head_dim;
@@ -62,7 +62,7 @@ extern "C" int ddtree_prompt_attention_plan(int batch, int q_rows, int k_rows, i
   p.n_sinks = n_sinks;
   p.q_rows = q_rows;
   p.k_rows = k_rows;
-  p.tile_tokens = prompt_tile_tokens(n_heads / n_kv_heads, head_dim);
+  p.tile_tokens = prompt_tile_tokens(batch, q_rows, n_heads / n_kv_heads, head_dim);
   const int64_t items = items_of(batch, q_rows, n_kv_heads, p.tile_tokens);
   if (items > INT32_MAX) return DDTREE_EINVAL;
   p.max_items = (int32_t)items;

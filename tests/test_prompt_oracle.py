@@ -77,7 +77,7 @@ def test_plan_and_refusals(lib):
     with pytest.raises(TypeError):
         make(dtype=torch.float32)
     plan = make()
-    assert plan.tile_tokens * 4 <= 256 and plan.max_items == (100 // plan.tile_tokens + 3) * 2
+    assert 1 <= plan.tile_tokens <= 64 and plan.max_items == (100 // plan.tile_tokens + 3) * 2
     assert plan.workspace_bytes % 256 == 0 and plan.workspace_bytes >= 256 + 4 * plan.max_items
     assert lib.ddtree_prompt_attention_workspace_size(None) == 0
     far = ctypes.c_void_p(1 << 14)
