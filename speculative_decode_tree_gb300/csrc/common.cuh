@@ -340,8 +340,9 @@ struct Draft8ReadArgs {
   uint16_t *k_out, *v_out;   // rows *_stride apart; one may be null
   uint32_t* status;          // or null
   int64_t k_out_stride, v_out_stride, page_stride, token_stride, head_stride, total_slots;
-  Divider page, block;
-  int32_t n_rows, row_pieces, n_kv_heads, head_dim, page_size, blocks, dtype;
+  Divider page, block, piece;
+  int32_t n_rows, n_kv_heads, head_dim, page_size, blocks, dtype;
+  int32_t row_pieces, cta_rows;  // 16 codes each; rows of a CTA's turn
 };
 
 // Everything the attention over the 8-bit cache needs.

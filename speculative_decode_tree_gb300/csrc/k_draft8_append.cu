@@ -2,9 +2,10 @@
 // (include/ddtree_draft8.h): head norms, rotation, quantisation as the rows are
 // written; and rows read back.
 //
-// Queries go as in the 16-bit append: a warp per token or slice of its heads,
-// sines and cosines in registers.  So do keys and values where every token has
-// scales of its own (blocks of one token).
+// A CTA takes a chunk of up to 32 tokens, or a slice of its heads where tokens are
+// few, and puts the sines and cosines of its tokens into shared memory: every row
+// of a token needs the same.  Queries go row by row, and so do keys and values
+// where every token has scales of its own (blocks of one token).
 //
 // Keys and values: the rows that a call writes to one block (a run of the list)
 // share a scale, which depends on the largest magnitude of them all, so the
@@ -15,6 +16,8 @@
 // tokens; the warp at a run's first token takes the whole run, also what lies
 // behind its chunk.  A block that has to grow moves its other rows to the new
 // scale there and then: nobody else writes that block in the call.
+#include "../../include/ddtree_draft8.h"
+#include "f32x2.cuh"
 #include "rope.cuh"
 
 namespace ddtree {
@@ -22,7 +25,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 3;   // head steps of a query whose loads are in flight together
+constexpr int kUnroll = 4;   // head steps of a query whose loads are in flight together
 constexpr int kSteps = 4;    // row steps of a warp in a run
 
 __device__ __forceinline__ bool scale_ok(float s) { return s >= 0x1p-64f && s <= 0x1p96f; }
@@ -64,350 +67,481 @@ __device__ __forceinline__ void unpack_codes8(uint2 c, float (&x)[8]) {
     x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
   }
 }
-// x / s for eight numbers: a product where s is a power of two (also exact), else the quotient.
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s) {
-  float y[8];
+// Eight numbers of a row, two by two.
+struct Row {
+  uint64_t v[4];
+};
+template <bool kHalf>
+__device__ __forceinline__ Row unpack_row(const uint4& in) {
+  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+  Row r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = unpack2<kHalf>(w[j]);
+    r.v[j] = pair(x.x, x.y);
+  }
+  return r;
+}
+template <bool kHalf>
+__device__ __forceinline__ uint4 pack_row(const Row& r) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = apart(r.v[j]);
+    w[j] = pack2<kHalf>(x.x, x.y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// x / s: a product where s is a power of two (also exact), else the quotient.
+__device__ __forceinline__ uint2 quantise_row(const Row& r, float s) {
+  float2 y[4];
   if ((__float_as_uint(s) & 0x7fffffu) == 0) {
     const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = x[j] * inv;
+    for (int j = 0; j < 4; ++j) y[j] = apart(mul2(r.v[j], pair(inv, inv)));
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(x[j], s);
+    for (int j = 0; j < 4; ++j) {
+      y[j] = apart(r.v[j]);
+      y[j] = make_float2(__fdiv_rn(y[j].x, s), __fdiv_rn(y[j].y, s));
+    }
   }
-  return make_uint2(to_codes(y[0], y[1], y[2], y[3]), to_codes(y[4], y[5], y[6], y[7]));
+  return make_uint2(to_codes(y[0].x, y[0].y, y[1].x, y[1].y), to_codes(y[2].x, y[2].y, y[3].x, y[3].y));
 }
 
-// What a lane needs of the rotation: it has the columns 8 c .. 8 c + 7 of every
-// row.  Interleaved, those are four pairs of its own; in the half layout eight
-// pairs that it shares with the lane of the other half, and each computes four.
+// A row lies over kDim / 8 lanes.  A lane has two pieces of four columns: where the
+// rotation is on halves the same place of both, so that a pair's elements meet in
+// one lane; else (interleaved pairs, columns that are not rotated) eight next to
+// each other.
 template <int kDim, bool kInterleaved>
-struct Turner {
-  static constexpr int kLanes = kDim / 8, kTurns = kInterleaved ? 4 : 8;
-  uint64_t turns[4];
-  int other_lane;
-  bool turned, first;
-  __device__ __forceinline__ Turner(const RopeArgs& rope, int lane) {
-    const int c = lane % kLanes, half = rope.rot_dim / 16;
-    turned = 8 * c < rope.rot_dim;
-    first = c < half;
-    const int other = !turned ? c : first ? c + half : c - half;
-    other_lane = (lane & ~(kLanes - 1)) + other;
-    const int pair = !turned ? 0 : kInterleaved ? 4 * c : first ? 8 * c : 8 * other + 4;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) turns[j] = rope.turns[pair + j];
+struct Lane {
+  int a, b;      // first column of each piece
+  int pair;      // first of the lane's four pairs
+  bool turned;
+  __device__ __forceinline__ Lane(int rot_dim, int c) {
+    turned = 8 * c < rot_dim;
+    pair = turned ? 4 * c : 0;
+    a = kInterleaved || !turned ? 8 * c : 4 * c;
+    b = kInterleaved || !turned ? 8 * c + 4 : rot_dim / 2 + 4 * c;
   }
-  __device__ __forceinline__ void at(int pos, float mscale, float2 (&cs)[kTurns]) const {
-    float2 mine[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) mine[j] = turn(turns[j], pos, mscale);
-    if constexpr (kInterleaved) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) cs[j] = mine[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 theirs = make_float2(__shfl_sync(0xffffffffu, mine[j].x, other_lane), __shfl_sync(0xffffffffu, mine[j].y, other_lane));
-        // x cos - y sin for a first element, x cos + y sin for a second one, y its partner.
-        cs[j] = first ? make_float2(mine[j].x, -mine[j].y) : theirs;
-        cs[j + 4] = first ? make_float2(theirs.x, -theirs.y) : mine[j];
-      }
-    }
+  __device__ __forceinline__ uint4 load(const uint16_t* row) const {
+    const uint2 u = *reinterpret_cast<const uint2*>(row + a), v = *reinterpret_cast<const uint2*>(row + b);
+    return make_uint4(u.x, u.y, v.x, v.y);
   }
-  __device__ __forceinline__ void apply(float (&x)[8], const float2 (&cs)[kTurns]) const {
-    if constexpr (kInterleaved) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float e = x[2 * j], o = x[2 * j + 1];
-        x[2 * j] = turned ? e * cs[j].x - o * cs[j].y : e;
-        x[2 * j + 1] = turned ? e * cs[j].y + o * cs[j].x : o;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float y = __shfl_sync(0xffffffffu, x[j], other_lane);
-        if (turned) x[j] = x[j] * cs[j].x + y * cs[j].y;
-      }
-    }
+  __device__ __forceinline__ void store(uint16_t* row, const uint4& v) const {
+    *reinterpret_cast<uint2*>(row + a) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(row + b) = make_uint2(v.z, v.w);
+  }
+  __device__ __forceinline__ uint2 load_codes(const uint8_t* row) const {
+    return make_uint2(*reinterpret_cast<const uint32_t*>(row + a), *reinterpret_cast<const uint32_t*>(row + b));
+  }
+  __device__ __forceinline__ void store_codes(uint8_t* row, uint2 v) const {
+    *reinterpret_cast<uint32_t*>(row + a) = v.x;
+    *reinterpret_cast<uint32_t*>(row + b) = v.y;
   }
 };
 
-// The norm of a row that kDim / 8 lanes hold.
-template <bool kHalf, int kDim>
-__device__ __forceinline__ void norm_row(float (&x)[8], const uint4& weight, float eps) {
-  float sum = 0.f;
+// A token's rotation of a lane's four pairs: v = v * same + other elements of the pairs * across.
+template <bool kInterleaved>
+struct Turn {
+  uint64_t same[4], across[4];
+  // cosines and sines of the pairs, one behind the other
+  __device__ __forceinline__ Turn(const float* cosines, const float* sines) {
+    const float4 c = *reinterpret_cast<const float4*>(cosines), s = *reinterpret_cast<const float4*>(sines);
+    if constexpr (kInterleaved) {
+      same[0] = pair(c.x, c.x); same[1] = pair(c.y, c.y); same[2] = pair(c.z, c.z); same[3] = pair(c.w, c.w);
+      across[0] = pair(-s.x, s.x); across[1] = pair(-s.y, s.y); across[2] = pair(-s.z, s.z); across[3] = pair(-s.w, s.w);
+    } else {
+      same[0] = same[2] = pair(c.x, c.y);
+      same[1] = same[3] = pair(c.z, c.w);
+      across[0] = pair(-s.x, -s.y); across[1] = pair(-s.z, -s.w);
+      across[2] = pair(s.x, s.y); across[3] = pair(s.z, s.w);
+    }
+  }
+  __device__ __forceinline__ void apply(Row& r) const {
+    Row o;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (kInterleaved) {
+        const float2 x = apart(r.v[j]);
+        o.v[j] = pair(x.y, x.x);
+      } else {
+        o.v[j] = r.v[j ^ 2];
+      }
+    }
 #pragma unroll
-  for (int d = kDim / 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  const float scale = rsqrtf(sum * (1.f / kDim) + eps);
-  float w[8];
-  unpack8<kHalf>(weight, w);
+    for (int j = 0; j < 4; ++j) r.v[j] = fma2(o.v[j], across[j], mul2(r.v[j], same[j]));
+  }
+};
+
+// 1 / root mean square of rows that kDim / 8 lanes hold each, side by side.
+template <int kDim, int kCount>
+__device__ __forceinline__ void row_norms(const Row (&r)[kCount], float eps, float (&by)[kCount]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = x[j] * scale * w[j];
+  for (int i = 0; i < kCount; ++i) {
+    const uint64_t* v = r[i].v;
+    const float2 s = apart(fma2(v[3], v[3], fma2(v[2], v[2], fma2(v[1], v[1], mul2(v[0], v[0])))));
+    by[i] = s.x + s.y;
+  }
+#pragma unroll
+  for (int d = kDim / 16; d > 0; d >>= 1) {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) by[i] += __shfl_xor_sync(0xffffffffu, by[i], d);
+  }
+#pragma unroll
+  for (int i = 0; i < kCount; ++i) by[i] = rsqrtf(by[i] * (1.f / kDim) + eps);
+}
+__device__ __forceinline__ void scale_row(Row& r, float by, const Row& weight) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r.v[j] = mul2(mul2(r.v[j], pair(by, by)), weight.v[j]);
+}
+// Largest magnitude; NaN is passed over, and so are infinities where kFinite.
+template <bool kFinite>
+__device__ __forceinline__ float row_top(const Row& r, float top) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = apart(r.v[j]);
+    const float a = fabsf(x.x), b = fabsf(x.y);
+    if (!kFinite || a < INFINITY) top = fmaxf(top, a);
+    if (!kFinite || b < INFINITY) top = fmaxf(top, b);
+  }
+  return top;
 }
 
-// Grid: chunks of `chunk` tokens (a power of two), slices of their heads.
-// team: warps of a run.
-template <bool kHalf, int kDim, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 4) draft8_append_kernel(const __grid_constant__ Draft8AppendArgs a, int chunk, int team) {
+// Grid: chunks of `chunk` tokens (a power of two), slices of their heads: the first
+// row_slices for rows on their own and the others for runs, or one for both.
+// team: warps of a run.  kByRow: every token has its own scale, all rows are on their own.
+template <bool kHalf, int kDim, bool kInterleaved, bool kByRow>
+__global__ void __launch_bounds__(kThreads, 4) draft8_append_kernel(const __grid_constant__ Draft8AppendArgs a, int chunk, int team, int row_slices) {
   constexpr int kLanes = kDim / 8;        // lanes of a row
   constexpr int kRows = 32 / kLanes;      // rows of a warp's step
-  using Turn = Turner<kDim, kInterleaved>;
+  // Of the chunk's tokens, and of those behind it that end its last run: cosines, then sines.
+  extern __shared__ __align__(16) float turns[];
   __shared__ float tops[2][kWarps];
   await_grid();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = lane % kLanes, sub = lane / kLanes;
-  const int slice = blockIdx.y, slices = gridDim.y;
+  const Lane<kDim, kInterleaved> mine(a.rope.rot_dim, c);
+  const bool both = !kByRow && gridDim.y == 1, rows_on = both || blockIdx.y < row_slices, runs_on = !kByRow && (both || !rows_on);
+  const int slice = rows_on ? blockIdx.y : blockIdx.y - row_slices, slices = both ? 1 : rows_on ? row_slices : gridDim.y - row_slices;
   const int n0 = blockIdx.x * chunk, n_end = min(n0 + chunk, a.n_tokens);
-  const Turn rotation(a.rope, lane);
   const uint4 none = make_uint4(0, 0, 0, 0);
-  const uint4 wq = a.q_weight ? __ldg(reinterpret_cast<const uint4*>(a.q_weight) + c) : none;
-  const uint4 wk = a.k_weight ? __ldg(reinterpret_cast<const uint4*>(a.k_weight) + c) : none;
-  if (slice == 0 && warp == 0 && a.status && n0 + lane < n_end) {
+
+  // ---- the chunk's runs: lane i has token n0 + i, and the i-th and i + 32-th behind the chunk
+  struct Spot {
+    int block, place;  // number of the token's block, its place there; -1 where nothing is written
+  };
+  auto spot_of = [&](int n) {
+    Spot s = {-1, 0};
+    if (n < 0 || n >= a.n_tokens) return s;
+    const int pos = __ldg(a.positions + n), slot = __ldg(a.slots + n);
+    if (pos < 0 || slot < 0 || slot >= a.total_slots) return s;
+    const int page = a.page.quotient(slot), in_page = slot - page * a.page_size, b = a.block.quotient(in_page);
+    s.block = page * a.blocks + b;
+    s.place = in_page - b * a.block_tokens;
+    return s;
+  };
+  Spot here = {-1, 0}, behind[2] = {{-1, 0}, {-1, 0}};
+  uint32_t leaders = 0;
+  int tail = 0;
+  if (runs_on) {
+    // All loads at once.
+    if (n0 + lane < n_end) here = spot_of(n0 + lane);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (32 * k + lane < a.block_tokens - 1) behind[k] = spot_of(n_end + 32 * k + lane);
+    const int first_before = spot_of(n0 - 1).block;
+    const int last = __shfl_sync(0xffffffffu, here.block, n_end - 1 - n0);
+    uint32_t same[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) same[k] = __ballot_sync(0xffffffffu, last >= 0 && behind[k].block == last);
+    tail = ~same[0] ? __ffs(~same[0]) - 1 : ~same[1] ? 31 + __ffs(~same[1]) : 64;
+    int before = __shfl_up_sync(0xffffffffu, here.block, 1);
+    if (lane == 0) before = first_before;
+    leaders = __ballot_sync(0xffffffffu, here.block >= 0 && here.block != before);
+    if (!leaders) {
+      if (!rows_on) return;  // the whole CTA: nothing begins here
+      tail = 0;
+    }
+  }
+  if (blockIdx.y == 0 && warp == 0 && a.status && n0 + lane < n_end) {
     const int pos = __ldg(a.positions + n0 + lane), slot = __ldg(a.slots + n0 + lane);
     if (pos < -1) atomicOr(a.status, DDTREE_ST_BAD_LENGTH);
     else if (pos >= 0 && (slot < -1 || slot >= a.total_slots)) atomicOr(a.status, DDTREE_ST_BAD_INDEX);
   }
+  const int pairs = a.rope.rot_dim / 2;
+  Row wq = {}, wk = {};
+  if (a.q_weight) wq = unpack_row<kHalf>(mine.load(a.q_weight));
+  if (kByRow && a.k_weight) wk = unpack_row<kHalf>(mine.load(a.k_weight));
 
-  // ---- rows on their own: queries, and where every token has its own scale keys and values too
-  const bool by_row = a.block_tokens == 1;
-  const int nq = a.n_heads, nk = a.n_kv_heads, row_heads = by_row ? nq + 2 * nk : nq;
-  {
-    const int per_token = chunk < kWarps ? kWarps / chunk : 1;  // warps of a token
-    const int steps = (row_heads + kRows - 1) / kRows, parts = slices * per_token;
-    const int part = slice * per_token + warp % per_token, part_steps = (steps + parts - 1) / parts;
-    const int h_begin = part * part_steps * kRows, h_end = min(h_begin + part_steps * kRows, row_heads);
-    for (int n = n0 + warp / per_token; n < n_end && h_begin < h_end; n += kWarps / per_token) {
-      const int pos = __ldg(a.positions + n), slot = __ldg(a.slots + n);
-      const uint16_t *q = a.q + n * a.q_stride, *k = a.k + n * a.k_stride, *v = a.v + n * a.v_stride;
-      uint16_t* out = a.q_out + n * a.q_out_stride;
+  // ---- rows on their own: a warp has tokens of the chunk, or some heads of one.  A
+  // batch is kUnroll steps; the next one, of whatever token, is loaded before this
+  // one is computed, and the first one before the sines are ready.
+  const int nq = a.n_heads, nk = a.n_kv_heads, heads = kByRow ? nq + 2 * nk : nq;
+  const int per_token = chunk < kWarps ? kWarps / chunk : 1;  // warps of a token
+  const int row_parts = slices * per_token, part_steps = ((heads + kRows - 1) / kRows + row_parts - 1) / row_parts;
+  const int h_begin = (slice * per_token + warp % per_token) * part_steps * kRows, h_end = min(h_begin + part_steps * kRows, heads);
+  const int n_step = kWarps / per_token;
+  auto load_batch = [&](int n, int h, uint4 (&in)[kUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int at = h + u * kRows + sub;
+      in[u] = none;
+      if (n < n_end && at < h_end) {  // plain loads: q_out may be q
+        const uint16_t* src = !kByRow || at < nq ? a.q + n * a.q_stride + at * kDim
+                              : at < nq + nk     ? a.k + n * a.k_stride + (at - nq) * kDim
+                                                 : a.v + n * a.v_stride + (at - nq - nk) * kDim;
+        in[u] = mine.load(src);
+      }
+    }
+  };
+  uint4 next[kUnroll];
+  int n = rows_on && h_begin < h_end ? n0 + warp / per_token : n_end, h = h_begin;
+  load_batch(n, h, next);
+  for (int t = warp; t < n_end - n0 + tail; t += kWarps) {
+    const int pos = __ldg(a.positions + n0 + t);
+    for (int p = lane; p < pairs; p += 32) {
+      const float2 cs = turn(a.rope.turns[p], pos, a.rope.mscale);
+      turns[2 * t * pairs + p] = cs.x;
+      turns[(2 * t + 1) * pairs + p] = cs.y;
+    }
+  }
+  __syncthreads();
+  while (n < n_end) {
+    Row x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) x[u] = unpack_row<kHalf>(next[u]);
+    const int n_now = n, h_now = h;
+    h += kRows * kUnroll;
+    if (h >= h_end) {
+      h = h_begin;
+      n += n_step;
+    }
+    load_batch(n, h, next);
+    if (__ldg(a.positions + n_now) < 0) continue;
+    const float* cs = turns + 2 * (n_now - n0) * pairs + mine.pair;
+    const Turn<kInterleaved> rotation(cs, cs + pairs);
+    if constexpr (!kByRow) {
+      if (a.q_weight) {
+        float by[kUnroll];
+        row_norms<kDim>(x, a.eps, by);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) scale_row(x[u], by[u], wq);
+      }
+      if (mine.turned) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) rotation.apply(x[u]);
+      }
+      uint16_t* out = a.q_out + n_now * a.q_out_stride + (h_now + sub) * kDim;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (h_now + u * kRows + sub < h_end) mine.store(out + u * kRows * kDim, pack_row<kHalf>(x[u]));
+    } else {
+      const int slot = __ldg(a.slots + n_now);
       const bool write_kv = slot >= 0 && slot < a.total_slots;
       const int page = write_kv ? a.page.quotient(slot) : 0;
       const int64_t row = page * a.page_stride + (write_kv ? slot - page * a.page_size : 0) * a.token_stride;
-      float2 cs[Turn::kTurns];
-      for (int base = h_begin; base < h_end; base += kRows * kUnroll) {
-        uint4 in[kUnroll];
+      float by[kUnroll], top[kUnroll];
+      if (a.q_weight || a.k_weight) row_norms<kDim>(x, a.eps, by);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int h = base + u * kRows + sub;
-          const uint16_t* src = h < nq ? q + h * kDim : h < nq + nk ? k + (h - nq) * kDim : v + (h - nq - nk) * kDim;
-          in[u] = h < h_end ? reinterpret_cast<const uint4*>(src)[c] : none;  // plain loads: q_out may be q
-        }
-        if (pos < 0) break;
-        if (base == h_begin) rotation.at(pos, a.rope.mscale, cs);
+      for (int u = 0; u < kUnroll; ++u) {
+        const int at = h_now + u * kRows + sub;
+        if (at < nq ? a.q_weight != nullptr : at < nq + nk && a.k_weight) scale_row(x[u], by[u], at < nq ? wq : wk);
+        if (mine.turned && at < nq + nk) rotation.apply(x[u]);
+        top[u] = row_top<true>(x[u], 0.f);
+      }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          if (base + u * kRows >= h_end) break;  // the same in the whole warp
-          const int h = base + u * kRows + sub;
-          const bool is_q = h < nq, is_v = h >= nq + nk;
-          float x[8];
-          unpack8<kHalf>(in[u], x);
-          if (a.q_weight || a.k_weight) {
-            float y[8];
+      for (int d = kLanes / 2; d > 0; d >>= 1) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = x[j];
-            norm_row<kHalf, kDim>(y, is_q ? wq : wk, a.eps);
-            if (!is_v && (is_q ? a.q_weight : a.k_weight)) {
+        for (int u = 0; u < kUnroll; ++u) top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], d));
+      }
 #pragma unroll
-              for (int j = 0; j < 8; ++j) x[j] = y[j];
-            }
-          }
-          float y[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = x[j];
-          rotation.apply(y, cs);
-          if (!is_v) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = y[j];
-          }
-          if (by_row) {
-            float top = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float m = fabsf(x[j]);
-              if (m < INFINITY) top = fmaxf(top, m);
-            }
-#pragma unroll
-            for (int d = kLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            if (!is_q && h < h_end && write_kv) {
-              const float scale = scale_for(top);
-              const int kh = is_v ? h - nq - nk : h - nq;
-              *reinterpret_cast<uint2*>((is_v ? a.v_cache : a.k_cache) + row + kh * a.head_stride + 8 * c) = quantise8(x, scale);
-              if (c == 0) (is_v ? a.v_scale : a.k_scale)[(int64_t)slot * nk + kh] = scale;
-            }
-          }
-          if (is_q && h < h_end) reinterpret_cast<uint4*>(out + h * kDim)[c] = pack8<kHalf>(x);
+      for (int u = 0; u < kUnroll; ++u) {
+        const int at = h_now + u * kRows + sub;
+        if (at >= h_end) continue;
+        if (at < nq) {
+          mine.store(a.q_out + n_now * a.q_out_stride + at * kDim, pack_row<kHalf>(x[u]));
+        } else if (write_kv) {
+          const bool is_v = at >= nq + nk;
+          const int kh = is_v ? at - nq - nk : at - nq;
+          const float scale = scale_for(top[u]);
+          mine.store_codes((is_v ? a.v_cache : a.k_cache) + row + kh * a.head_stride, quantise_row(x[u], scale));
+          if (c == 0) (is_v ? a.v_scale : a.k_scale)[(int64_t)slot * nk + kh] = scale;
         }
       }
     }
   }
-  if (by_row) return;
+  if (!runs_on) return;
+  if (a.k_weight) wk = unpack_row<kHalf>(mine.load(a.k_weight));
 
-  // ---- keys and values: the chunk's runs, each key head's keys and values an item
-  auto block_of = [&](int n) {  // number of the token's block, -1 where nothing is written
-    if (n < 0 || n >= a.n_tokens) return -1;
-    const int pos = __ldg(a.positions + n), slot = __ldg(a.slots + n);
-    if (pos < 0 || slot < 0 || slot >= a.total_slots) return -1;
-    const int page = a.page.quotient(slot);
-    return page * a.blocks + a.block.quotient(slot - page * a.page_size);
-  };
-  const int mine = n0 + lane < n_end ? block_of(n0 + lane) : -1;
-  int before = __shfl_up_sync(0xffffffffu, mine, 1);
-  if (lane == 0) before = block_of(n0 - 1);
-  const uint32_t leaders = __ballot_sync(0xffffffffu, mine >= 0 && mine != before);
+  // ---- keys and values: run by run, each key head's keys and values for a team
   const int teams = kWarps / team, my_team = warp / team, rank = warp % team;
-  const uint32_t per_run = 2 * nk, items = __popc(leaders) * per_run;
+  const int r0 = rank * kRows + sub;  // this lane's first row of a run; the next is team * kRows behind
   int round = 0;
-  for (uint32_t at = slice * teams; at < items; at += slices * teams, ++round) {  // the same in the whole CTA
-    const uint32_t item = at + my_team;
-    const bool work = item < items;
-    float x[kSteps][8], top = 0.f, old = 0.f;
-    int n = 0, block = 0, run = 0, head = 0;
-    bool is_v = false;
-    uint64_t written = 0;  // tokens of the block that the run writes
-    float* scale_at = nullptr;
-    if (work) {
-      const uint32_t which = item / per_run, part = item - which * per_run;
-      head = part >> 1;
-      is_v = part & 1;
-      uint32_t left = leaders;
-      for (uint32_t k = 0; k < which; ++k) left &= left - 1;
-      const int first = __ffs(left) - 1;
-      n = n0 + first;
-      block = __shfl_sync(0xffffffffu, mine, first);
-      scale_at = (is_v ? a.v_scale : a.k_scale) + (int64_t)block * nk + head;
-      old = *scale_at;  // in every warp of the team before the exchange below, and so before it changes
-      // The run: the tokens from n on that lie in this block, as many as it has places.
-      uint32_t same[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        same[k] = __ballot_sync(0xffffffffu, 32 * k + lane < a.block_tokens && block_of(n + 32 * k + lane) == block);
-      run = ~same[0] ? __ffs(~same[0]) - 1 : ~same[1] ? 31 + __ffs(~same[1]) : 64;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t lo = 0, hi = 0;
-        if (32 * k + lane < run) {
-          const int slot = __ldg(a.slots + n + 32 * k + lane), in_page = slot - a.page.quotient(slot) * a.page_size;
-          const int t = in_page - a.block.quotient(in_page) * a.block_tokens;
-          (t < 32 ? lo : hi) = 1u << (t & 31);
-        }
-        written |= (uint64_t)__reduce_or_sync(0xffffffffu, hi) << 32 | __reduce_or_sync(0xffffffffu, lo);
-      }
-      const uint16_t* src = is_v ? a.v + head * kDim : a.k + head * kDim;
-      const int64_t stride = is_v ? a.v_stride : a.k_stride;
-      uint4 in[kSteps];
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int r = (s * team + rank) * kRows + sub;
-        in[s] = r < run ? __ldg(reinterpret_cast<const uint4*>(src + (n + r) * stride) + c) : none;
-      }
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int r0 = (s * team + rank) * kRows;
-        unpack8<kHalf>(in[s], x[s]);
-        if (!is_v && r0 < run) {  // the same in the whole warp
-          if (a.k_weight) norm_row<kHalf, kDim>(x[s], wk, a.eps);
-          float2 cs[Turn::kTurns];
-          rotation.at(__ldg(a.positions + n + min(r0 + sub, run - 1)), a.rope.mscale, cs);
-          rotation.apply(x[s], cs);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float m = fabsf(x[s][j]);
-          if (m < INFINITY) top = fmaxf(top, m);
-        }
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    }
-    if (team > 1) {
-      if (lane == 0) tops[round & 1][warp] = top;
-      __syncthreads();  // once a round: the other buffer is read before anyone writes it again
-      for (int k = 0; k < team; ++k) top = fmaxf(top, tops[round & 1][my_team * team + k]);
-    }
-    if (!work) continue;
-    const bool begun = !(written & 1) && scale_ok(old);
-    const float scale = begun && top <= old * 448.f ? old : scale_for(top);
-    const int page = block / a.blocks, b = block - page * a.blocks;
-    uint8_t* rows = (is_v ? a.v_cache : a.k_cache) + page * a.page_stride + (int64_t)b * a.block_tokens * a.token_stride +
-                    head * a.head_stride + 8 * c;
-    if (begun && scale != old) {
-      // What the block holds already, to the new scale.
-      const int tokens = min(a.block_tokens, a.page_size - b * a.block_tokens);
-      for (int t = rank * kRows + sub; t < tokens; t += team * kRows) {
-        if (written >> t & 1) continue;
-        uint2* p = reinterpret_cast<uint2*>(rows + t * a.token_stride);
-        float held[8];
-        unpack_codes8(*p, held);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) held[j] *= old;
-        *p = quantise8(held, scale);
-      }
-    }
-    const int slot0 = page * a.page_size + b * a.block_tokens;
+  for (uint32_t left = leaders; left; left &= left - 1) {
+    const int first = __ffs(left) - 1, n = n0 + first;  // its first token
+    const int block = __shfl_sync(0xffffffffu, here.block, first);
+    // The run: the tokens from n on that lie in this block, as many as it has places.
+    const uint32_t other = ~__ballot_sync(0xffffffffu, here.block == block) >> first;
+    const int inside = other ? min(__ffs(other) - 1, 32 - first) : 32 - first;
+    const int run = min(a.block_tokens, n + inside == n_end ? inside + tail : inside);
+    const bool tailed = run > inside;
+    uint64_t bit = 0;
+    if (lane >= first && lane < first + inside && lane - first < run) bit = 1ull << here.place;
+    if (tailed && lane < run - inside) bit |= 1ull << behind[0].place;
+    if (tailed && 32 + lane < run - inside) bit |= 1ull << behind[1].place;
+    // Tokens of the block that the run writes.
+    const uint64_t written = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(bit >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)bit);
+    const int page = block / a.blocks, b = block - page * a.blocks, slot0 = page * a.page_size + b * a.block_tokens;
+    const int64_t block_at = page * a.page_stride + (int64_t)b * a.block_tokens * a.token_stride;
+    // Where this lane's rows go.
+    int64_t to[kSteps];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const int r = (s * team + rank) * kRows + sub;
-      if (r < run) *reinterpret_cast<uint2*>(rows + (__ldg(a.slots + n + r) - slot0) * a.token_stride) = quantise8(x[s], scale);
+      const int r = r0 + s * team * kRows;
+      to[s] = r < run ? block_at + (__ldg(a.slots + n + r) - slot0) * a.token_stride : 0;
     }
-    if (rank == 0 && lane == 0 && scale != old) *scale_at = scale;
+    auto load = [&](int part, uint4 (&in)[kSteps]) {
+      const int head = part >> 1;
+      const uint16_t* src = (part & 1 ? a.v + (n + r0) * a.v_stride : a.k + (n + r0) * a.k_stride) + head * kDim;
+      const int64_t stride = (part & 1 ? a.v_stride : a.k_stride) * (team * kRows);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) in[s] = part < 2 * nk && r0 + s * team * kRows < run ? mine.load(src + s * stride) : none;
+    };
+    uint4 ahead[kSteps];
+    load(slice * teams + my_team, ahead);
+    for (int at = slice * teams; at < 2 * nk; at += slices * teams, ++round) {  // the same in the whole CTA
+      const int part = at + my_team, head = part >> 1;
+      const bool work = part < 2 * nk, is_v = part & 1;
+      Row x[kSteps];
+      float top = 0.f, old = 0.f;
+      float* scale_at = (is_v ? a.v_scale : a.k_scale) + (int64_t)block * nk + head;
+      if (work) old = *scale_at;  // in every warp of the team before the exchange below, and so before it changes
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) x[s] = unpack_row<kHalf>(ahead[s]);
+      load(part + slices * teams, ahead);
+      if (work) {
+        if (!is_v) {
+          if (a.k_weight) {
+            float by[kSteps];
+            row_norms<kDim>(x, a.eps, by);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) scale_row(x[s], by[s], wk);
+          }
+          if (mine.turned) {
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+              const float* cs = turns + 2 * (first + min(r0 + s * team * kRows, run - 1)) * pairs + mine.pair;
+              Turn<kInterleaved>(cs, cs + pairs).apply(x[s]);
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            if (r0 + s * team * kRows >= run) x[s] = Row{};  // no row
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) top = row_top<false>(x[s], top);
+        if (__any_sync(0xffffffffu, top == INFINITY)) {
+          top = 0.f;
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) top = row_top<true>(x[s], top);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      }
+      if (team > 1) {
+        if (lane == 0) tops[round & 1][warp] = top;
+        __syncthreads();  // once a round: the other buffer is read before anyone writes it again
+        for (int k = 0; k < team; ++k) top = fmaxf(top, tops[round & 1][my_team * team + k]);
+      }
+      if (!work) continue;
+      const bool begun = !(written & 1) && scale_ok(old);
+      const float scale = begun && top <= old * 448.f ? old : scale_for(top);
+      uint8_t* rows = (is_v ? a.v_cache : a.k_cache) + head * a.head_stride;
+      if (begun && scale != old) {
+        // What the block holds already, to the new scale.
+        const int tokens = min(a.block_tokens, a.page_size - b * a.block_tokens);
+        for (int t = r0; t < tokens; t += team * kRows) {
+          if (written >> t & 1) continue;
+          uint8_t* p = rows + block_at + t * a.token_stride;
+          float held[8];
+          unpack_codes8(mine.load_codes(p), held);
+          Row r;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r.v[j] = pair(held[2 * j] * old, held[2 * j + 1] * old);
+          mine.store_codes(p, quantise_row(r, scale));
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        if (r0 + s * team * kRows < run) mine.store_codes(rows + to[s], quantise_row(x[s], scale));
+      if (rank == 0 && lane == 0 && scale != old) *scale_at = scale;
+    }
   }
 }
 
-// Rows read back: eight codes a thread and step, of keys and of values.
+// Rows read back: sixteen codes a thread and step, of keys and of values.  A CTA
+// takes `rows` rows at a time; their pieces are numbered together.
 template <bool kHalf>
 __global__ void __launch_bounds__(256) draft8_read_kernel(const __grid_constant__ Draft8ReadArgs a) {
-  constexpr int kTogether = 4;
+  constexpr int kTogether = 2;
   await_grid();
-  const int64_t pieces = (int64_t)a.n_rows * a.row_pieces, stride = (int64_t)gridDim.x * 256;
-  const int per_head = a.head_dim / 8;
+  const int per_head = a.head_dim / 16;  // 4, 8 or 16
+  const int head_log2 = a.head_dim == 64 ? 2 : a.head_dim == 128 ? 3 : 4;
   uint32_t bad = 0;
-  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < pieces; at += stride * kTogether) {
-    uint2 code[kTogether][2];
-    float scale[kTogether][2];
-    int64_t to[kTogether];
-    int row[kTogether];
+  for (int64_t n0 = (int64_t)blockIdx.x * a.cta_rows; n0 < a.n_rows; n0 += (int64_t)gridDim.x * a.cta_rows) {
+    const int pieces = min(a.cta_rows, (int)(a.n_rows - n0)) * a.row_pieces;
+    for (int at = threadIdx.x; at < pieces; at += 256 * kTogether) {
+      uint4 code[kTogether][2];
+      float scale[kTogether][2];
+      int64_t row[kTogether];
+      int to[kTogether];
 #pragma unroll
-    for (int u = 0; u < kTogether; ++u) {
-      const int64_t i = at + u * stride;
-      row[u] = -1;
-      if (i >= pieces) continue;
-      const int n = (int)(i / a.row_pieces), piece = (int)(i - (int64_t)n * a.row_pieces);
-      const int slot = __ldg(a.slots + n);
-      if (slot < 0 || slot >= a.total_slots) {
-        if (slot != -1) bad |= DDTREE_ST_BAD_INDEX;
-        continue;
+      for (int u = 0; u < kTogether; ++u) {
+        const int i = at + 256 * u;
+        row[u] = -1;
+        if (i >= pieces) continue;
+        const int n = a.piece.quotient(i), piece = i - n * a.row_pieces;
+        const int slot = __ldg(a.slots + n0 + n);
+        if (slot < 0 || slot >= a.total_slots) {
+          if (slot != -1) bad |= DDTREE_ST_BAD_INDEX;
+          continue;
+        }
+        const int head = piece >> head_log2, col = (piece & (per_head - 1)) * 16;
+        const int page = a.page.quotient(slot), token = slot - page * a.page_size;
+        const int64_t from = page * a.page_stride + token * a.token_stride + head * a.head_stride + col;
+        const int64_t s = ((int64_t)page * a.blocks + a.block.quotient(token)) * a.n_kv_heads + head;
+        row[u] = n0 + n;
+        to[u] = head * a.head_dim + col;
+        if (a.k_out) {
+          code[u][0] = *reinterpret_cast<const uint4*>(a.k_cache + from);
+          scale[u][0] = a.k_scale[s];
+        }
+        if (a.v_out) {
+          code[u][1] = *reinterpret_cast<const uint4*>(a.v_cache + from);
+          scale[u][1] = a.v_scale[s];
+        }
       }
-      const int head = piece / per_head, col = (piece - head * per_head) * 8;
-      const int page = a.page.quotient(slot), token = slot - page * a.page_size;
-      const int64_t from = page * a.page_stride + token * a.token_stride + head * a.head_stride + col;
-      const int64_t s = ((int64_t)page * a.blocks + a.block.quotient(token)) * a.n_kv_heads + head;
-      row[u] = n;
-      to[u] = head * a.head_dim + col;
-      if (a.k_out) {
-        code[u][0] = *reinterpret_cast<const uint2*>(a.k_cache + from);
-        scale[u][0] = a.k_scale[s];
-      }
-      if (a.v_out) {
-        code[u][1] = *reinterpret_cast<const uint2*>(a.v_cache + from);
-        scale[u][1] = a.v_scale[s];
-      }
-    }
 #pragma unroll
-    for (int u = 0; u < kTogether; ++u) {
-      if (row[u] < 0) continue;
+      for (int u = 0; u < kTogether; ++u) {
+        if (row[u] < 0) continue;
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        uint16_t* out = w ? a.v_out : a.k_out;
-        if (!out) continue;
-        float x[8];
-        unpack_codes8(code[u][w], x);
-        const bool ok = scale_ok(scale[u][w]);
-        if (!ok) bad |= DDTREE_ST_BAD_SCALE;
+        for (int w = 0; w < 2; ++w) {
+          uint16_t* out = w ? a.v_out : a.k_out;
+          if (!out) continue;
+          const bool ok = scale_ok(scale[u][w]);
+          if (!ok) bad |= DDTREE_ST_BAD_SCALE;
+          const uint2 part[2] = {make_uint2(code[u][w].x, code[u][w].y), make_uint2(code[u][w].z, code[u][w].w)};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = ok ? x[j] * scale[u][w] : 0.f;
-        *reinterpret_cast<uint4*>(out + row[u] * (w ? a.v_out_stride : a.k_out_stride) + to[u]) = pack8<kHalf>(x);
+          for (int h = 0; h < 2; ++h) {
+            float x[8];
+            unpack_codes8(part[h], x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = ok ? x[j] * scale[u][w] : 0.f;
+            *reinterpret_cast<uint4*>(out + row[u] * (w ? a.v_out_stride : a.k_out_stride) + to[u] + 8 * h) = pack8<kHalf>(x);
+          }
+        }
       }
     }
   }
@@ -417,18 +551,24 @@ __global__ void __launch_bounds__(256) draft8_read_kernel(const __grid_constant_
 template <bool kHalf, int kDim>
 cudaError_t launch(const Draft8AppendArgs& a, int num_sms, cudaStream_t stream) {
   constexpr int kRows = 256 / kDim;
+  const bool by_row = a.block_tokens == 1;
   const int elements = a.block_tokens * kDim, team = elements <= 1024 ? 1 : elements <= 2048 ? 2 : 4;
-  // Chunks of up to 32 tokens; fewer tokens take smaller chunks and slices of
-  // the heads, until there are some CTAs for each SM.
-  const int items = a.block_tokens == 1 ? 0 : 2 * a.n_kv_heads * team;  // warps of a run
-  const int steps = (a.n_heads + (a.block_tokens == 1 ? 2 * a.n_kv_heads : 0) + kRows - 1) / kRows;
-  const int most = std::max(1, std::max((items + kWarps - 1) / kWarps, steps / kWarps));
-  int chunk = 32;
-  while (chunk > 1 && (int64_t)((a.n_tokens + chunk - 1) / chunk) * most < num_sms * 4) chunk /= 2;
+  // One wave of CTAs where tokens are few: chunks of fewer than eight tokens, down to
+  // one, then slices of its heads, in which rows and runs go side by side.
+  const int64_t slots = (int64_t)num_sms * 4;
+  int chunk = 8;
+  while (chunk > 1 && (a.n_tokens + chunk / 2 - 1) / (chunk / 2) <= slots) chunk /= 2;
   const int64_t chunks = (a.n_tokens + chunk - 1) / chunk;
-  const int slices = (int)std::max<int64_t>(1, std::min<int64_t>(most, (num_sms * 4 + chunks - 1) / chunks));
-  return launch_early(a.rope.interleaved ? draft8_append_kernel<kHalf, kDim, true> : draft8_append_kernel<kHalf, kDim, false>,
-                      dim3((unsigned)chunks, slices), kThreads, 0, stream, a, chunk, team);
+  const int steps = (a.n_heads + (by_row ? 2 * a.n_kv_heads : 0) + kRows - 1) / kRows;
+  const int rows_most = (steps + kWarps - 1) / kWarps, runs_most = by_row ? 0 : (2 * a.n_kv_heads * team + kWarps - 1) / kWarps;
+  const int slices = (int)std::max<int64_t>(1, std::min<int64_t>(rows_most + runs_most, slots / chunks));
+  const int row_slices = by_row || slices == 1 ? slices : a.n_heads == 0 ? 0 : std::max(1, std::min(slices - 1, slices * rows_most / (rows_most + runs_most)));
+  // Cosines and sines of a chunk's tokens, and of a block's behind it.
+  const size_t smem = (size_t)(chunk + a.block_tokens - 1) * a.rope.rot_dim * sizeof(float);
+  static_assert((8 + DDTREE_DRAFT8_MAX_BLOCK / kDim - 1) * (size_t)kDim * sizeof(float) + 64 <= 48 * 1024, "shared memory");
+  auto* kernel = a.rope.interleaved ? (by_row ? draft8_append_kernel<kHalf, kDim, true, true> : draft8_append_kernel<kHalf, kDim, true, false>)
+                                    : (by_row ? draft8_append_kernel<kHalf, kDim, false, true> : draft8_append_kernel<kHalf, kDim, false, false>);
+  return launch_early(kernel, dim3((unsigned)chunks, slices), kThreads, smem, stream, a, chunk, team, row_slices);
 }
 
 }  // namespace
@@ -444,8 +584,11 @@ cudaError_t launch_draft8_append(const Draft8AppendArgs& a, int num_sms, cudaStr
                              : launch<false, 256>(a, num_sms, stream);
 }
 
-cudaError_t launch_draft8_read(const Draft8ReadArgs& a, int num_sms, cudaStream_t stream) {
-  const int64_t blocks = ((int64_t)a.n_rows * a.row_pieces + 255) / 256;
+cudaError_t launch_draft8_read(const Draft8ReadArgs& args, int num_sms, cudaStream_t stream) {
+  Draft8ReadArgs a = args;
+  a.cta_rows = std::max(1, 512 / a.row_pieces);
+  a.piece = make_divider(a.row_pieces);
+  const int64_t blocks = ((int64_t)a.n_rows + a.cta_rows - 1) / a.cta_rows;
   const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)num_sms * 8);
   return launch_early(a.dtype == DDTREE_FP16 ? draft8_read_kernel<true> : draft8_read_kernel<false>, grid, 256, 0, stream, a);
 }
