@@ -342,7 +342,7 @@ struct Draft8ReadArgs {
   int64_t k_out_stride, v_out_stride, page_stride, token_stride, head_stride, total_slots;
   Divider page, block, piece;
   int32_t n_rows, n_kv_heads, head_dim, page_size, blocks, dtype;
-  int32_t row_pieces, cta_rows;  // 16 codes each; rows of a CTA's turn
+  int32_t row_pieces, cta_rows;  // 8 codes each; rows of a CTA's turn
 };
 
 // Everything the attention over the 8-bit cache needs.

@@ -172,7 +172,7 @@ extern "C" int ddtree_draft8_read(int64_t n_rows, int dtype, const ddtree_draft8
   a.page = make_divider(cache->page_size);
   a.block = make_divider(cache->block_tokens);
   a.n_rows = (int32_t)n_rows;
-  a.row_pieces = (int32_t)(width / 16);
+  a.row_pieces = (int32_t)(width / 8);
   a.n_kv_heads = cache->n_kv_heads;
   a.head_dim = cache->head_dim;
   a.page_size = cache->page_size;

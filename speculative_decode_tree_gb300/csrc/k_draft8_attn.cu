@@ -659,14 +659,15 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
   if (tid == 0) words[share] = bits;
 }
 
-// Joins the parts of the units that go on across shares, as the 16-bit kernel's
-// join does: a CTA per record (x) and slice of its rows (y); one more x gathers
-// the status words.  Eight teams of kDim / 4 threads take rows of their own, or
-// several share a row's parts.
-template <bool kHalf, int kDim>
-__global__ void __launch_bounds__(2 * kDim) draft8_join_kernel(const __grid_constant__ Draft8AttnArgs a, int slice_rows) {
-  constexpr int kTeams = 8, kLanes = kDim / 4, kTogether = 8;
-  constexpr int kThreads = kTeams * kLanes;
+// Joins the parts of the units that go on across shares: a CTA per record (x),
+// slice of its rows (y) and kSplit-th of the columns (z); one more x gathers the
+// status words.  kTeams teams of kDim / 4 / kSplit threads, a float4 each, take rows
+// of their own, or several share a row's parts; every team keeps its own running
+// maximum, so sums and rows are loaded together.  Few records have many parts
+// each, and more CTAs (kSplit) load them.
+template <bool kHalf, int kDim, int kSplit>
+__global__ void __launch_bounds__(256) draft8_join_kernel(const __grid_constant__ Draft8AttnArgs a, int slice_rows) {
+  constexpr int kLanes = kDim / 4 / kSplit, kTeams = 256 / kLanes, kTogether = 8;
   __shared__ float4 acc[kTeams][kLanes];
   __shared__ float2 team_sum[kTeams];
   __shared__ uint32_t all;
@@ -676,9 +677,9 @@ __global__ void __launch_bounds__(2 * kDim) draft8_join_kernel(const __grid_cons
   const int records = by_unit(a) ? a.n_tokens * a.unit_heads : a.n_shares;
   await_grid();
   if (x == records) {
-    if (slice > 0) return;
+    if (slice > 0 || blockIdx.z > 0) return;
     uint32_t b = 0;
-    for (int s = tid; s < a.n_shares; s += kThreads) b |= reinterpret_cast<const uint32_t*>(a.ws + ws.words)[s];
+    for (int s = tid; s < a.n_shares; s += 256) b |= reinterpret_cast<const uint32_t*>(a.ws + ws.words)[s];
     if (tid == 0) all = 0;
     __syncthreads();
     if (b) atomicOr(&all, b);
@@ -700,9 +701,11 @@ __global__ void __launch_bounds__(2 * kDim) draft8_join_kernel(const __grid_cons
   const float4* rows = reinterpret_cast<const float4*>(a.ws + ws.rows);
   // Part p of the unit, in every bundle-th share: the second place of the first one, the first place of the others.
   auto place = [&](int p, int row) { return ((int64_t)2 * (first + (p << a.bundle_log2)) + (p == 0)) * kRows + row; };
-  const int team = tid / kLanes, c = tid - team * kLanes;
+  const int team = tid / kLanes, lane = tid - team * kLanes, c = blockIdx.z * kLanes + lane;
   const int row_begin = slice * slice_rows, row_end = min(row_begin + slice_rows, rows_here);
-  const int per_row = parts <= kTogether || slice_rows > 4 ? 1 : slice_rows > 2 ? 2 : slice_rows > 1 ? 4 : 8;
+  // Teams of a row: as many as the CTA's rows leave, where it has more parts than one team loads at once.
+  int per_row = 1;
+  while (parts > per_row * kTogether && 2 * per_row * slice_rows <= kTeams) per_row *= 2;
   for (int row0 = row_begin; row0 < row_end; row0 += kTeams / per_row) {
     const int row = row0 + team / per_row;
     float high = -INFINITY, total = 0.f;
@@ -717,7 +720,7 @@ __global__ void __launch_bounds__(2 * kDim) draft8_join_kernel(const __grid_cons
         v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p < parts) {
           s[u] = sums[place(p, row)];
-          v[u] = rows[place(p, row) * kLanes + c];
+          v[u] = rows[place(p, row) * (kDim / 4) + c];
         }
       }
       float top = high;
@@ -735,8 +738,8 @@ __global__ void __launch_bounds__(2 * kDim) draft8_join_kernel(const __grid_cons
       }
     }
     if (per_row > 1) {  // the same in the whole CTA
-      acc[team][c] = o;
-      if (c == 0) team_sum[team] = make_float2(high, total);
+      acc[team][lane] = o;
+      if (lane == 0) team_sum[team] = make_float2(high, total);
       __syncthreads();
       if (team % per_row == 0) {
         for (int k = 0; k < per_row; ++k) high = fmaxf(high, team_sum[team + k].x);
@@ -745,7 +748,7 @@ __global__ void __launch_bounds__(2 * kDim) draft8_join_kernel(const __grid_cons
         total = 0.f;
         for (int k = 0; k < per_row; ++k) {
           const float w = power2(team_sum[team + k].x - from);
-          const float4 v = acc[team + k][c];
+          const float4 v = acc[team + k][lane];
           total += w * team_sum[team + k].y;
           o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
         }
@@ -778,13 +781,17 @@ cudaError_t launch(const Draft8AttnArgs& a, cudaStream_t stream) {
   }
   e = launch_early(draft8_attn_kernel<kHalf, kDim>, a.n_shares, kThreads, C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
-  // Rows get CTAs of their own where records are few, for their units have many parts.
+  // Rows get CTAs of their own where records are few, for their units have many
+  // parts, and where units may have a hundred, a row's columns too (185k single
+  // 51.9 -> 46.1 us; a window of 2,048, with 17 parts, 9.3 -> 9.6, so not there).
   const int records = by_unit(a) ? a.n_tokens * a.unit_heads : a.n_shares;
   const int rows = std::min(kRows, a.group);
   const int slices = std::max(1, std::min(rows, a.n_shares / records));
-  const int slice_rows = (rows + slices - 1) / slices;
-  return launch_early(draft8_join_kernel<kHalf, kDim>, dim3(records + 1, (rows + slice_rows - 1) / slice_rows), 2 * kDim, 0, stream, a,
-                      slice_rows);
+  const int slice_rows = (rows + slices - 1) / slices, slice_count = (rows + slice_rows - 1) / slice_rows;
+  constexpr int kSplit = kDim / 32;  // 128 bytes of a row
+  if (64 * records <= a.n_shares && (int64_t)records * slice_count * kSplit <= a.n_shares)
+    return launch_early(draft8_join_kernel<kHalf, kDim, kSplit>, dim3(records + 1, slice_count, kSplit), 256, 0, stream, a, slice_rows);
+  return launch_early(draft8_join_kernel<kHalf, kDim, 1>, dim3(records + 1, slice_count, 1), 256, 0, stream, a, slice_rows);
 }
 
 template <bool kHalf>
