@@ -304,6 +304,25 @@ def test_equal_bits_on_other_streams_without_lse_and_in_a_replay():
     c.compare()
 
 
+def test_pages_far_into_a_large_cache():
+    # 2 x 4.6 GB: offsets pass 32 bits.
+    c = Case([300, 90], 8, 1, 256, page=16, block=16, seed=22)
+    n, far = c.codes[0].shape[0], 1130000 - c.codes[0].shape[0]
+    big = [torch.empty(1130000, 16, 1, 256, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros(1130000, 1, 1, device="cuda") for _ in range(2)]
+    for b, codes, s, own in zip(big, c.codes, scales, c.scales):
+        b[far:].copy_(codes)
+        s[far:].copy_(own)
+    c.device()
+    cache = B.Draft8Cache(*big, *scales, 16)
+    assert big[0].numel() > 2 ** 32
+    table = torch.where(c.table >= 0, c.table + far, c.table).cuda()
+    B.ddtree_draft8_attention(c.plan, c.q_dev, cache, table, *c.args[4:], **c.kw)
+    torch.cuda.synchronize()
+    assert B.ddtree_verify_mla_check(c.ws) == 0
+    c.compare()
+
+
 def test_refusals():
     c = Case([5, 6], 8, 2, 64, seed=21)
     c.device()

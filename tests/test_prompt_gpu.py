@@ -186,6 +186,38 @@ def test_what_a_row_does_not_see_has_no_part_in_it(dim, heads, kvh):
         assert bool(torch.isfinite(c.out[:129]).all()) and bool(torch.isfinite(c.out[130:258]).all())
 
 
+def test_rows_far_apart():
+    # Keys and values 4 MB apart: offsets pass 32 bits; with a NaN the rows go one by one.
+    for bad in (False, True):
+        c = Case([40, 1100], 2, 1, 64, seed=15)
+        if bad:
+            c.v[c.kp[2] - 1, 0, 3] = float("nan")
+        c.device()
+        n, step = c.k.shape[0], 1 << 21
+        far = torch.empty(n * step, dtype=torch.bfloat16, device="cuda")
+        k, v = (torch.as_strided(far, (n, 1, 64), (step, 64, 1), at) for at in (0, 4096))
+        k.copy_(c.k), v.copy_(c.v)
+        B.ddtree_prompt_attention(c.plan, c.args[1], k, v, *c.args[4:], **c.kw)
+        torch.cuda.synchronize()
+        assert B.ddtree_verify_mla_check(c.ws) == 0
+        c.compare()
+
+
+def test_two_streams_with_a_workspace_each():
+    cases = [Case([700, 30, 5], 8, 2, 128, seed=16 + i) for i in range(2)] + [Case([90] * 9, 4, 2, 64, seed=18)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for c in cases:
+        c.device()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, s in zip(cases, streams):
+            B.ddtree_prompt_attention(*c.args, **c.kw, stream=s)
+    torch.cuda.synchronize()
+    for c in cases:
+        assert B.ddtree_verify_mla_check(c.ws) == 0
+        c.compare()
+
+
 def test_bad_sequences_write_nothing():
     base = Case([30, 50], 4, 2, 64, seed=11)
     for which, values in (("qp", [0, 40, 30]), ("qp", [-1, 30, 80]), ("qp", [0, 30, 84]), ("kp", [0, 90, 80]), ("kp", [0, 30, 90]), ("kp", [-5, 30, 80]),
