@@ -33,84 +33,92 @@ __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const __grid_cons
     if (tid == 0) *a.status = all;
     return;
   }
-  for (int id = blockIdx.x; id < items; id += gridDim.x - 1) {
-    if (!(a.words[id] & kPromptAgain)) continue;
-    __syncthreads();
-    PromptItem it;
-    if (find_prompt_item<kThreads>(a, id / a.n_kv_heads, scratch, it)) continue;
-    const int kv = id % a.n_kv_heads;
-    const uint16_t* k = a.k + it.k0 * a.k_stride + kv * kDim;
-    const uint16_t* v = a.v + it.k0 * a.v_stride + kv * kDim;
-    for (int r = warp; r < it.tokens * a.group; r += kThreads / 32) {
-      const int token = r / a.group, head = kv * a.group + r - token * a.group;
-      const int64_t row = it.q0 + token;
-      const int pos = it.pos + token;  // below 0: sees nothing
-      const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0, first = min(a.n_sinks, lo);
-      const int seen = pos < 0 ? 0 : first + pos - lo + 1;
-      const uint16_t* q = a.q + row * a.q_stride + head * kDim;
-      __syncwarp();
+  // Thread t looks at every gridDim-th item, from t gridDim on; those that are marked
+  // are done one after the other.
+  const int ctas = gridDim.x - 1;
+  for (int64_t base = blockIdx.x; base < items; base += (int64_t)ctas * kThreads) {
+    const int64_t look = base + (int64_t)ctas * tid;
+    const bool marked = look < items && (a.words[look] & kPromptAgain);
+    if (!__syncthreads_or(marked)) continue;
+    for (int slot = 0; slot < kThreads; ++slot) {
+      if (!__syncthreads_or(marked && tid == slot)) continue;
+      const int id = (int)(base + (int64_t)ctas * slot);
+      PromptItem it;
+      if (find_prompt_item<kThreads>(a, id / a.n_kv_heads, scratch, it)) continue;
+      const int kv = id % a.n_kv_heads;
+      const uint16_t* k = a.k + it.k0 * a.k_stride + kv * kDim;
+      const uint16_t* v = a.v + it.k0 * a.v_stride + kv * kDim;
+      for (int r = warp; r < it.tokens * a.group; r += kThreads / 32) {
+        const int token = r / a.group, head = kv * a.group + r - token * a.group;
+        const int64_t row = it.q0 + token;
+        const int pos = it.pos + token;  // below 0: sees nothing
+        const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0, first = min(a.n_sinks, lo);
+        const int seen = pos < 0 ? 0 : first + pos - lo + 1;
+        const uint16_t* q = a.q + row * a.q_stride + head * kDim;
+        __syncwarp();
 #pragma unroll
-      for (int c = 0; c < kCols / 2; ++c) {
-        const float2 x = unpack2<kHalf>(reinterpret_cast<const uint32_t*>(q)[c * 32 + lane]);
-        query[warp][2 * (c * 32 + lane)] = x.x;
-        query[warp][2 * (c * 32 + lane) + 1] = x.y;
-      }
-      __syncwarp();
-      float o[kCols], top = -INFINITY, sum = 0.f;
+        for (int c = 0; c < kCols / 2; ++c) {
+          const float2 x = unpack2<kHalf>(reinterpret_cast<const uint32_t*>(q)[c * 32 + lane]);
+          query[warp][2 * (c * 32 + lane)] = x.x;
+          query[warp][2 * (c * 32 + lane) + 1] = x.y;
+        }
+        __syncwarp();
+        float o[kCols], top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) o[c] = 0.f;
-      for (int base = 0; base < seen; base += 32) {
-        const int x = base + lane, j = x < first ? x : x - first + lo;
-        float s = -INFINITY;
-        if (x < seen) {
-          const uint4* key = reinterpret_cast<const uint4*>(k + j * a.k_stride);
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < kCols; ++c) o[c] = 0.f;
+        for (int base = 0; base < seen; base += 32) {
+          const int x = base + lane, j = x < first ? x : x - first + lo;
+          float s = -INFINITY;
+          if (x < seen) {
+            const uint4* key = reinterpret_cast<const uint4*>(k + j * a.k_stride);
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-          for (int c = 0; c < kDim / 8; ++c) {
-            float y[8];
-            unpack8<kHalf>(key[c], y);
+            for (int c = 0; c < kDim / 8; ++c) {
+              float y[8];
+              unpack8<kHalf>(key[c], y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) part[e & 3] = fmaf(y[e], query[warp][8 * c + e], part[e & 3]);
+              for (int e = 0; e < 8; ++e) part[e & 3] = fmaf(y[e], query[warp][8 * c + e], part[e & 3]);
+            }
+            s = (part[0] + part[1] + part[2] + part[3]) * a.scale_log2;
           }
-          s = (part[0] + part[1] + part[2] + part[3]) * a.scale_log2;
-        }
-        float high = s;
+          float high = s;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
-        high = fmaxf(high, top);
-        const float from = high == -INFINITY ? 0.f : high, keep = ptx::ex2_approx(top - from);
-        const float p = x < seen ? ptx::ex2_approx(s - from) : 0.f;
-        sum = sum * keep + p;
-        top = high;
+          for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+          high = fmaxf(high, top);
+          const float from = high == -INFINITY ? 0.f : high, keep = ptx::ex2_approx(top - from);
+          const float p = x < seen ? ptx::ex2_approx(s - from) : 0.f;
+          sum = sum * keep + p;
+          top = high;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) o[c] *= keep;
-        const int n = min(32, seen - base);
-        for (int i = 0; i < n; ++i) {
-          const float w = __shfl_sync(0xffffffffu, p, i);
-          const int jj = __shfl_sync(0xffffffffu, j, i);
-          const uint32_t* val = reinterpret_cast<const uint32_t*>(v + jj * a.v_stride);
+          for (int c = 0; c < kCols; ++c) o[c] *= keep;
+          const int n = min(32, seen - base);
+          for (int i = 0; i < n; ++i) {
+            const float w = __shfl_sync(0xffffffffu, p, i);
+            const int jj = __shfl_sync(0xffffffffu, j, i);
+            const uint32_t* val = reinterpret_cast<const uint32_t*>(v + jj * a.v_stride);
 #pragma unroll
-          for (int c = 0; c < kCols / 2; ++c) {
-            const float2 y = unpack2<kHalf>(__ldg(val + c * 32 + lane));
-            o[2 * c] = fmaf(w, y.x, o[2 * c]);
-            o[2 * c + 1] = fmaf(w, y.y, o[2 * c + 1]);
+            for (int c = 0; c < kCols / 2; ++c) {
+              const float2 y = unpack2<kHalf>(__ldg(val + c * 32 + lane));
+              o[2 * c] = fmaf(w, y.x, o[2 * c]);
+              o[2 * c + 1] = fmaf(w, y.y, o[2 * c + 1]);
+            }
           }
         }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const float by = sum == 0.f ? 0.f : 1.f / sum;
+        uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * a.out_stride + head * kDim);
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) out[c * 32 + lane] = pack2<kHalf>(o[2 * c] * by, o[2 * c + 1] * by);
+        if (a.lse && lane == 0) a.lse[row * a.n_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
       }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      const float by = sum == 0.f ? 0.f : 1.f / sum;
-      uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * a.out_stride + head * kDim);
-#pragma unroll
-      for (int c = 0; c < kCols / 2; ++c) out[c * 32 + lane] = pack2<kHalf>(o[2 * c] * by, o[2 * c + 1] * by);
-      if (a.lse && lane == 0) a.lse[row * a.n_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
   }
 }
 
 template <bool kHalf>
 cudaError_t launch_dim(const PromptArgs& a, int num_sms, cudaStream_t stream) {
-  const unsigned grid = (unsigned)std::min<int64_t>(a.max_items, (int64_t)num_sms * 8) + 1;
+  const unsigned grid = (unsigned)std::min<int64_t>(a.max_items, (int64_t)num_sms * 2) + 1;
   return launch_early(a.head_dim == 64    ? prompt_rows_kernel<kHalf, 64>
                       : a.head_dim == 128 ? prompt_rows_kernel<kHalf, 128>
                                           : prompt_rows_kernel<kHalf, 256>,

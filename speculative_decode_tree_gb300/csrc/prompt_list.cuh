@@ -24,11 +24,16 @@ __device__ __forceinline__ int find_prompt_item(const PromptArgs& a, int tile, i
   int* found = scratch + kWarps;
   const int per = (a.batch + kThreads - 1) / kThreads;
   int mine = 0;
+  int q_at = 0, q_end = 0, k_at = 0, k_end = 0;  // of the thread's last sequence, its only one where they are few
   bool bad = false;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b >= a.batch) break;
     const int q0 = __ldg(a.q_indptr + b), q1 = __ldg(a.q_indptr + b + 1), k0 = __ldg(a.k_indptr + b), k1 = __ldg(a.k_indptr + b + 1);
+    q_at = q0;
+    q_end = q1;
+    k_at = k0;
+    k_end = k1;
     bad |= q0 < 0 || q1 < q0 || q1 > a.q_rows || k0 < 0 || k1 < k0 || k1 > a.k_rows;
     if (!bad) mine += (q1 - q0 + a.tile_tokens - 1) / a.tile_tokens;
   }
@@ -48,11 +53,11 @@ __device__ __forceinline__ int find_prompt_item(const PromptArgs& a, int tile, i
   if (before <= tile && tile < before + mine) {
     int left = tile - before;
     for (int b = tid * per;; ++b) {
-      const int q0 = __ldg(a.q_indptr + b), q1 = __ldg(a.q_indptr + b + 1);
+      const int q0 = per == 1 ? q_at : __ldg(a.q_indptr + b), q1 = per == 1 ? q_end : __ldg(a.q_indptr + b + 1);
       const int tiles = (q1 - q0 + a.tile_tokens - 1) / a.tile_tokens;
       if (left < tiles) {
         const int first = (tiles - 1 - left) * a.tile_tokens;
-        const int k0 = __ldg(a.k_indptr + b), k1 = __ldg(a.k_indptr + b + 1);
+        const int k0 = per == 1 ? k_at : __ldg(a.k_indptr + b), k1 = per == 1 ? k_end : __ldg(a.k_indptr + b + 1);
         found[0] = q0 + first;
         found[1] = min(a.tile_tokens, q1 - q0 - first);
         found[2] = k0;
