@@ -302,6 +302,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       return sh.tops[i & 1][t][half ^ 1][row];
     };
     float m = -INFINITY, l = 0.f;
+    // Key tiles that every row of the warp sees whole start here to there.
+    const int lo_most = __reduce_max_sync(0xffffffffu, lo), start_last = __reduce_min_sync(0xffffffffu, pos) - C::kMyKeys + 1;
     for (int i = 0; i < n; ++i) {
       const int buffer = C::kBuffers == 2 ? i & 1 : t;
       wait(&sh.scores[buffer], C::kBuffers == 2 ? i >> 1 : i);
@@ -317,9 +319,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       }
       // Columns up to `high`, and of those the ones from `low` on or below `sink`.
       const int start = start_of(i) + C::kMyKeys * half;
-      const int high = min(pos, (i < sink_tiles ? sinks : it.keys) - 1) - start;
-      const int low = i < sink_tiles ? 0 : lo - start, sink = a.n_sinks - start;
-      if (__any_sync(0xffffffffu, high < C::kMyKeys - 1 || (low > 0 && sink < min(low, C::kMyKeys)))) {
+      if (i < sink_tiles || start > start_last || start < lo_most) {
+        const int high = min(pos, (i < sink_tiles ? sinks : it.keys) - 1) - start;
+        const int low = i < sink_tiles ? 0 : lo - start, sink = a.n_sinks - start;
 #pragma unroll
         for (int w = 0; w < C::kMyKeys / 32; ++w) {
           const uint32_t seen = bits_to(high - 32 * w) & (~bits_to(low - 1 - 32 * w) | bits_to(max(sink, 0) - 1 - 32 * w));
