@@ -389,33 +389,49 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     // ---- the rows
     const float by = l == 0.f ? 0.f : 1.f / l;
     const int64_t to = it.q0 + token;
-    uint16_t* out = a.out + to * a.out_stride + (int64_t)head * kDim + half * kMine;
+    const int64_t out_at = valid ? to * a.out_stride + (int64_t)head * kDim + half * kMine : -1;
     bool odd = !(fabsf(l) < INFINITY);
+    // A row's columns lie in one lane; they go through where the queries were, so that
+    // a warp stores whole lines (64 short prompts of 128 columns: 37.2 -> 35.7 us).
+    constexpr int kPiece = kMine < 64 ? kMine : 64, kChunks = kPiece / 8, kTurn = kChunks == 8 ? 0 : 1;
+    const uint32_t mine = q_at + t * C::kQBytes + (half * 4 + quarter) * (32 * kPiece * 2);
     if (n > 0) {
       wait(&sh.result[t], 0);
       tc_fence_after();
     }
 #pragma unroll 1
-    for (int c = 0; c < kMine; c += 32) {
-      uint32_t v[32];
+    for (int c = 0; c < kMine; c += kPiece) {
       if (n > 0) {
-        tmem_ld32(o_mem + c, v);
-      } else {
+        uint32_t v[kPiece];
+        if constexpr (kPiece == 64) tmem_ld64(o_mem + c, v);
+        else tmem_ld32(o_mem + c, v);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0;
-      }
-      if (valid) {
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
+        for (int e = 0; e < kChunks; ++e) {
           float y[8];
 #pragma unroll
           for (int d = 0; d < 8; ++d) {
-            y[d] = __uint_as_float(v[e + d]);
+            y[d] = __uint_as_float(v[8 * e + d]);
             odd |= !(fabsf(y[d]) < INFINITY);
             y[d] *= by;
           }
-          *reinterpret_cast<uint4*>(out + c + e) = pack8<kHalf>(y);
+          const uint4 w = pack8<kHalf>(y);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(mine + lane * (kPiece * 2) + ((e ^ (lane >> kTurn & (kChunks - 1))) << 4)),
+                       "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                       : "memory");
         }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < kChunks; ++e) {
+        const int from = (e * 32 + lane) / kChunks, chunk = lane % kChunks;
+        const int64_t at = __shfl_sync(0xffffffffu, out_at, from);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (n > 0)
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                       : "r"(mine + from * (kPiece * 2) + ((chunk ^ (from >> kTurn & (kChunks - 1))) << 4))
+                       : "memory");
+        if (at >= 0) *reinterpret_cast<uint4*>(a.out + at + c + 8 * chunk) = w;
       }
       __syncwarp();
     }
