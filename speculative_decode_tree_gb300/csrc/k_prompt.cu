@@ -26,9 +26,25 @@
 //    infinity in V is a NaN: a row whose result is no number marks its item, and a
 //    second grid, placed ahead of time, does marked items row by row
 //    (k_prompt_rows.cu).  So only inputs that hold such values pay for them.
+//  - A short sequence is mostly a CTA's start and end: one tile a CTA then, two CTAs
+//    an SM, and two threads for a row.  Where an average sequence has fewer than
+//    1,024 rows (64 prompts of 1 to 251 tokens, 32 + 8 heads of 128: 46 us with two
+//    tiles, 36 so); long ones want the two tiles (16,384 tokens, 16 + 2 heads of 128:
+//    765 us with one, 660 with two; chunks of 64 columns behind a context 398 and 253).
 //  - Waits are bounded (the plan's wait_limit_us).  A role whose wait expires sets
 //    TIMEOUT, goes on without waiting and comes to its end; products in flight are
 //    waited for before the tensor memory is given back, copies before the CTA ends.
+//
+// Measured: 16,384 tokens of 16 + 2 heads of 128 columns (1.1 Tflop) 650 to 700 us,
+// 1.6 to 1.7 Pflop/s, by the card's power; the products alone take 583.  A pair of
+// tiles goes around in 2,600 clocks, of which its products are 2,048: S ready to P
+// stored 1,380, and the rest is P to its products to the next S.  With 64 columns the
+// products are 1,024 of 2,250, and that chain is the bound (16,384 tokens 500 us;
+// without any arithmetic in the softmax still 475).  Tried there: P in columns of its
+// own, so that the next S is made beside the softmax (560: the two tiles' softmaxes
+// meet, and one issuing warp's waits are in each other's way), an issuing thread
+// without elections (544, for the same reason), the maximum found beside the
+// exponentials (532), one tile a CTA (581).
 #include <cuda.h>
 #include <string.h>
 
@@ -71,7 +87,7 @@ struct Config {
   static constexpr int kLoadWarp = 4 * kTiles * kSplit, kIssueWarp = kLoadWarp + 1;
   static constexpr int kThreads = 32 * (kTiles == 2 ? kLoadWarp + 4 : kIssueWarp + 1);
 };
-constexpr int kShortRows = 1024;
+constexpr int kShortRows = 1024;  // of an average sequence: above
 constexpr uint64_t kDrainNs = 2000000000ull;  // for products and copies in flight where the kernel ends
 
 __host__ __device__ constexpr uint32_t product_desc(int n, bool b_mn_major, bool half) {
@@ -248,6 +264,18 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
           __syncwarp();
         }
         landed(2 * i + 1);
+        // Values of keys that no row of the item sees become zeros.
+        if (!more || i < sink_tiles) {
+          const int unseen = (i < sink_tiles ? sinks : it.pos + it.tokens) - start_of(i);
+#pragma unroll 1
+          for (int at = lane * 16; at < (C::kKeys - unseen) * 128; at += 512) {
+#pragma unroll
+            for (int s = 0; s < C::kSlabs; ++s)
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(stage_of(2 * i + 1) + (s + 1) * C::kKeys * 128 - 16 - at), "r"(0) : "memory");
+          }
+          fence_async_smem();
+          __syncwarp();
+        }
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           if (i >= n_of[t]) continue;

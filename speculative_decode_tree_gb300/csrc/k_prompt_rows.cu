@@ -11,13 +11,13 @@
 namespace ddtree {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 template <bool kHalf, int kDim>
 __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const __grid_constant__ PromptArgs a) {
   constexpr int kCols = kDim / 32;  // columns of a lane
-  __shared__ int scratch[kThreads / 32 + 8];
-  __shared__ __align__(16) float query[kThreads / 32][kDim];
+  __shared__ int scratch[kWarps + 8];
+  __shared__ __align__(16) float query[kWarps][kDim];
   __shared__ uint32_t all;
   await_grid();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -33,22 +33,24 @@ __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const __grid_cons
     if (tid == 0) *a.status = all;
     return;
   }
-  // Thread t looks at every gridDim-th item, from t gridDim on; those that are marked
-  // are done one after the other.
-  const int ctas = gridDim.x - 1;
-  for (int64_t base = blockIdx.x; base < items; base += (int64_t)ctas * kThreads) {
+  // A unit is a row for each warp of an item.  Thread t looks at every gridDim-th
+  // one, from t gridDim on; those of marked items are done one after the other.
+  const int ctas = gridDim.x - 1, parts = (a.tile_tokens * a.group + kWarps - 1) / kWarps;
+  const int64_t units = (int64_t)items * parts;
+  for (int64_t base = blockIdx.x; base < units; base += (int64_t)ctas * kThreads) {
     const int64_t look = base + (int64_t)ctas * tid;
-    const bool marked = look < items && (a.words[look] & kPromptAgain);
+    const bool marked = look < units && (a.words[look / parts] & kPromptAgain);
     if (!__syncthreads_or(marked)) continue;
     for (int slot = 0; slot < kThreads; ++slot) {
       if (!__syncthreads_or(marked && tid == slot)) continue;
-      const int id = (int)(base + (int64_t)ctas * slot);
+      const int64_t unit = base + (int64_t)ctas * slot;
+      const int id = (int)(unit / parts), r = (int)(unit - (int64_t)id * parts) * kWarps + warp;
       PromptItem it;
       if (find_prompt_item<kThreads>(a, id / a.n_kv_heads, scratch, it)) continue;
       const int kv = id % a.n_kv_heads;
       const uint16_t* k = a.k + it.k0 * a.k_stride + kv * kDim;
       const uint16_t* v = a.v + it.k0 * a.v_stride + kv * kDim;
-      for (int r = warp; r < it.tokens * a.group; r += kThreads / 32) {
+      if (r < it.tokens * a.group) {
         const int token = r / a.group, head = kv * a.group + r - token * a.group;
         const int64_t row = it.q0 + token;
         const int pos = it.pos + token;  // below 0: sees nothing
