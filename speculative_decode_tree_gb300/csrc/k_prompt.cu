@@ -23,9 +23,12 @@
 //    the softmax warps.
 //  - Key tiles that no row sees are skipped; those that some rows see in part are
 //    masked by bits.  What is masked has probability 0, and 0 times a NaN or an
-//    infinity in V is a NaN: a row whose result is no number marks its item, and a
-//    second grid, placed ahead of time, does marked items row by row
-//    (k_prompt_rows.cu).  So only inputs that hold such values pay for them.
+//    infinity in V is a NaN.  Values that no row of the item sees (behind its last
+//    token, between sinks and window: other sequences, memory that nobody wrote)
+//    become zeros in shared memory.  What is left are values that other rows of the
+//    item see: a row whose result is no number marks its item, and a second grid,
+//    placed ahead of time, does marked items row by row (k_prompt_rows.cu).  So only
+//    prompts that hold such values pay for them.
 //  - A short sequence is mostly a CTA's start and end: one tile a CTA then, two CTAs
 //    an SM, and two threads for a row.  Where an average sequence has fewer than
 //    1,024 rows (64 prompts of 1 to 251 tokens, 32 + 8 heads of 128: 46 us with two

@@ -186,6 +186,28 @@ def test_what_a_row_does_not_see_has_no_part_in_it(dim, heads, kvh):
         assert bool(torch.isfinite(c.out[:129]).all()) and bool(torch.isfinite(c.out[130:258]).all())
 
 
+@pytest.mark.parametrize("dim,heads,kvh", [(64, 4, 2), (128, 4, 2), (256, 2, 2)])
+def test_old_context_that_was_not_read_back(dim, heads, kvh):
+    # Between the sinks and the first row's window anything may lie; 130 sinks end inside a key tile.
+    for sinks, n in ((3, 90), (130, 300)):
+        for bad in (float("nan"), float("inf")):
+            c = Case([n, 7], heads, kvh, dim, ctx=[1000, 700], window=64, sinks=sinks, seed=sinks)
+            for b in range(2):
+                first = c.kp[b + 1] - (c.qp[b + 1] - c.qp[b]) - 64 + 1
+                c.k[c.kp[b] + sinks:first], c.v[c.kp[b] + sinks:first] = bad, bad
+            assert c.run() == 0
+            c.compare()
+            assert bool(torch.isfinite(c.out[c.qp[0]:c.qp[-1]]).all())
+
+
+def test_more_rows_done_again_than_one_round_takes():
+    # 8,000 items of which every second one has a NaN in a value that its rows see.
+    c = Case([2] * 1000, 8, 8, 64, seed=19, same=True)
+    c.v[0:2000:2, ::2, 1] = float("nan")
+    assert c.run() == 0
+    c.compare()
+
+
 def test_rows_far_apart():
     # Keys and values 4 MB apart: offsets pass 32 bits; with a NaN the rows go one by one.
     for bad in (False, True):
