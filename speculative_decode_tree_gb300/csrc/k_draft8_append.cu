@@ -18,13 +18,15 @@
 // scale there and then: nobody else writes that block in the call.
 //
 // To read and write: 2 + 2 bytes a query element, 2 + 1 a key's or value's.  32,749
-// tokens of 32 + 8 heads of 128 columns (738 MB): 161 us, 4.6 TB/s, 0.68 of the copy
+// tokens of 32 + 8 heads of 128 columns (738 MB): 170 us, 4.3 TB/s, 0.65 of the copy
 // rate.  Of some 104 M warp instructions (the issue slots are 55 % busy) norms,
 // rotation and conversions are the most, and the next rows' loads have to hide
 // behind them in 16 warps an SM: 128 registers hold four rows a lane and the four
-// behind them.  Five CTAs an SM spill (207 us) and six more (230); chunks of 4 and
-// 16 tokens take 175 and 169; queries and runs as launches of their own 238.  Small
-// calls (8 tokens): 3.1 us in a graph, launch and three loads that wait for each other.
+// behind them.  With the rows read back as well 203 us; there five CTAs an SM, which
+// spill, take 251 and six 274, chunks of 4 and 16 tokens 218 and 211, queries and runs
+// as launches of their own 280.  Small calls (8 tokens of the same heads, one for
+// each block): 5.3 us in a graph, launch and three loads that wait for each other
+// (places, rows and scales, the block's old rows).
 #include "../../include/ddtree_draft8.h"
 #include "f32x2.cuh"
 #include "rope.cuh"

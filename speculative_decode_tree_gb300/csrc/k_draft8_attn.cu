@@ -41,8 +41,8 @@
 // eight requests above (738 MB) 117 us, 0.94; 61 requests of 0.5k to 16k, 8 x 64
 // columns of fp16 (292 MB) 64 us, 0.68: the issue slots of an SM are 60 % busy and
 // the conversions' pipe is the next; one of 185k with 2 x 256 columns (194 MB)
-// 45.7, 0.63: the stream takes 38, the join behind it the rest; a window of 2,048 at
-// 65k 9.0: steps that wait for each other, in two grids.
+// 45.8, 0.63: some 8 us of it the lists, the joins and the launches; a window of
+// 2,048 at 65k 9.0: steps that wait for each other, in two grids.
 #include <atomic>
 
 #include "f32x2.cuh"

@@ -46,6 +46,29 @@ def test_blocks_start_grow_and_keep():
     assert float(scales[0, 1, 0]) == 2.0 ** -9 and O.read_rows(codes, scales, 2, [3, -1], torch.full((2, 1, 2), 7.0)).tolist() == [[[0.5, 0.0]], [[7.0, 7.0]]]
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (5, 2)])
+def test_attention_equals_sdpa_over_the_values(window, sinks):
+    g = torch.Generator().manual_seed(window)
+    pages, page, kvh, d, block = 6, 4, 2, 8, 3
+    k, v = (torch.randint(0, 120, (pages, page, kvh, d), generator=g).to(torch.uint8) for _ in range(2))
+    ks, vs = (2.0 ** torch.randint(-3, 3, (pages, 2, kvh), generator=g).double() for _ in range(2))
+    vs[4, 0, 1] = float("nan")  # tokens 0 to 2 of page 4, of one key head
+    q, table = torch.randn(2, 4, d, generator=g), torch.tensor([[3, 1, 4], [0, 5, 2]], dtype=torch.int32)
+    out, lse, _, _ = O.attention(q, k, v, ks, vs, block, table, [1, 0], [6, 9], window, sinks, 0.1, torch.zeros(2, 4, d), torch.zeros(2, 4))
+    at = torch.arange(page) // block
+    kx, vx = ((k if c is ks else v).view(torch.float8_e4m3fn).double() * c[:, at][..., None] for c in (ks, vs))
+    for n, (row, pos) in enumerate(((1, 6), (0, 9))):
+        kk, vv = (c[table[row].long()].reshape(3 * page, kvh, d) for c in (kx, vx))
+        j = torch.arange(3 * page)
+        seen = (j <= pos) & ((j > pos - window) | (j < sinks) | (window == 0))
+        for h in range(4):
+            here = seen & ~torch.isnan(vv[:, h // 2, 0])
+            assert bool((here != seen).any()) == (row == 0 and h // 2 == 1)
+            ref = torch.nn.functional.scaled_dot_product_attention(q[n, h].double()[None], kk[here, h // 2], vv[here, h // 2], scale=0.1)[0]
+            assert torch.allclose(out[n, h], ref, rtol=1e-12)
+            assert torch.allclose(lse[n, h], torch.logsumexp(0.1 * kk[here, h // 2] @ q[n, h].double(), 0), rtol=1e-12)
+
+
 @pytest.fixture(scope="module")
 def lib():
     from speculative_decode_tree_gb300.build import build
