@@ -116,7 +116,8 @@ extern "C" int ddtree_prompt_attention(const ddtree_prompt_plan_t* plan, const v
   a.group = plan->n_heads / plan->n_kv_heads;
   a.head_dim = plan->head_dim;
   a.dtype = plan->dtype;
-  a.window = plan->window;
+  // A window of all rows is none; positions may be below 0, and less a larger one they would pass 32 bits.
+  a.window = plan->window >= DDTREE_PROMPT_MAX_ROWS ? 0 : plan->window;
   a.n_sinks = plan->n_sinks;
   a.q_rows = plan->q_rows;
   a.k_rows = plan->k_rows;

@@ -131,6 +131,13 @@ def test_contexts(dim):
     _check([3, 5], 8, 2, dim, ctx=[-3, -9], window=4, sinks=2, seed=3)
 
 
+@pytest.mark.parametrize("window", [2 ** 24 - 1, 2 ** 24, 2 ** 31 - 1])
+@pytest.mark.parametrize("sinks", [0, 2 ** 31 - 1])
+def test_largest_windows_with_queries_that_see_nothing(window, sinks):
+    for dim in (64, 128, 256):
+        _check([200, 70], 4, 2, dim, ctx=[-60, -69], window=window, sinks=sinks, seed=dim)
+
+
 @pytest.mark.parametrize("kw", [dict(packed=True), dict(lse=False), dict(q_scale=30.0), dict(q_scale=30.0, dtype=torch.float16), dict(scale=-0.2),
                                 dict(scale=0.0), dict(scale=-0.2, window=50, sinks=3), dict(before=9, behind=70), dict(behind=0)])
 @pytest.mark.parametrize("dim", [64, 128, 256])
