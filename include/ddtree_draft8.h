@@ -130,8 +130,9 @@ DDTREE_API size_t ddtree_draft8_attention_workspace_size(const ddtree_draft8_pla
  * 2^-39 of it or less is lost), scores, maxima and sums are in 32 bits, and the
  * weight p_j vscale_j of a value row is rounded to fp16 (half a step of it,
  * 2^-11) relative to the unit's largest: a row counts down to 2^-34 of that.
- * The sums take p_j unrounded, and an output is rounded once.  Equal inputs
- * give equal bits.
+ * The sums take p_j unrounded, but lose a key whose weight is below 2^-130 of the
+ * largest: value scales of a request's keys are to lie within 2^100 of each
+ * other.  An output is rounded once.  Equal inputs give equal bits.
  * Errors: as ddtree_draft_attention.
  */
 DDTREE_API int ddtree_draft8_attention(const ddtree_draft8_plan_t* plan, const void* q,

@@ -195,6 +195,16 @@ def test_value_blocks_of_very_different_scales():
         c.compare()
 
 
+def test_sums_see_value_blocks_2_to_the_100_apart():
+    for dim in (64, 128, 256):
+        c = Case([900, 20000], 8, 2, dim, seed=10)
+        c.scales[1].fill_(2.0 ** -50)
+        for n in range(2):
+            c.scales[1][int(c.table[c.token_rows[n], 20])] = 2.0 ** 50
+        assert c.run() == 0
+        c.compare()
+
+
 def test_one_large_score_among_many_keys_keeps_the_small_ones():
     c = Case([60000], 4, 1, 64, page=16, seed=13, scale=1.0)
     for codes, number in ((c.codes[0], 0.0), (c.codes[1], 1.0)):
