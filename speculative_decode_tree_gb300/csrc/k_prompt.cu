@@ -77,7 +77,7 @@ struct Config {
   static constexpr int kSlabs = kDim / 64;                  // of 64 columns
   static constexpr int kQBytes = 128 * kDim * 2;
   static constexpr int kStageBytes = kKeys * kDim * 2;      // a tile of K or of V
-  static constexpr int kStages = kDim == 64 ? (kSmall ? 4 : 10) : kSmall ? 2 : kDim == 128 ? 4 : 5;
+  static constexpr int kStages = kDim == 64 ? (kSmall ? 4 : 10) : kSmall ? 2 : 4;
   static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStageBytes;
   // Tensor memory: S of each tile (256 columns: two buffers), O of each tile.
   static constexpr int kBuffers = kDim == 256 ? 2 : 1;      // of S, for each tile
@@ -89,6 +89,7 @@ struct Config {
   static constexpr int kSplit = kSmall ? 2 : 1, kMyKeys = kKeys / kSplit;
   static constexpr int kLoadWarp = 4 * kTiles * kSplit, kIssueWarp = kLoadWarp + 1;
   static constexpr int kThreads = 32 * (kTiles == 2 ? kLoadWarp + 4 : kIssueWarp + 1);
+  static constexpr int kList = (DDTREE_MAX_BATCH + 1) * 4;  // of sequences
 };
 constexpr int kShortRows = 1024;  // of an average sequence: above
 constexpr uint64_t kDrainNs = 2000000000ull;  // for products and copies in flight where the kernel ends
@@ -110,15 +111,20 @@ __device__ __forceinline__ uint32_t bits_to(int h) { return h < 0 ? 0u : h >= 31
 template <int kTiles, int kSplit>
 struct Shared {
   uint64_t full[10], empty[10];      // stages: landed, used by every tile
-  uint64_t queries;
+  uint64_t item[2], known[2];        // items (even, odd): written, read by every role
+  uint64_t queries, asked;           // landed, multiplied by all keys
   uint64_t scores[2];                // S of a tile (256 columns: of a buffer) is complete
   uint64_t weights[2][2];            // 64 keys of P are written, by each half's threads
   uint64_t products;                 // 256 columns: PV of a key tile is complete
-  uint64_t result[2];                // O of a tile is complete
+  uint64_t result[2], stored[2];     // O of a tile is complete, read
   uint64_t drained;
   float tops[2][kTiles][2][kSplit == 2 ? 128 : 1];  // of even and odd key tiles, of both halves: the rows' maxima; at the end their sums
   uint32_t base, word;
   int scratch[28];
+  struct {
+    PromptItem it;
+    int id;  // -1: there are no more
+  } items[2];
 };
 
 template <bool kHalf, int kDim, int kTiles>
@@ -129,7 +135,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
   extern __shared__ uint8_t smem[];
   __shared__ Shared<kTiles, kSplit> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-  const int kv = blockIdx.x % a.n_kv_heads;
   // What needs no data comes before the wait for the stream's last kernel.
   if (warp == C::kLoadWarp) {
     if (elect_one()) {
@@ -142,47 +147,63 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
   if (tid == 0) {
     sh.word = 0;
     mbar_init(&sh.queries, 1);
+    mbar_init(&sh.asked, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.scores[i], 1);
       for (int h = 0; h < 2; ++h) mbar_init(&sh.weights[i][h], 4);
       mbar_init(&sh.result[i], 1);
+      mbar_init(&sh.stored[i], 4 * kSplit);
+      mbar_init(&sh.item[i], 1);
+      mbar_init(&sh.known[i], 1 + 4 * kTiles * kSplit);
     }
-    mbar_init(&sh.products, 1);
-    mbar_init(&sh.drained, 1);
-  }
-  release_grid();
-  await_grid();
-  tc_fence_before();
-  PromptItem it;
-  const int got = find_prompt_item<C::kThreads>(a, blockIdx.x / a.n_kv_heads, sh.scratch, it);
-  tc_fence_after();
-  const uint32_t tmem = sh.base;
-  if (got) {
-    if (tid == 0) a.words[blockIdx.x] = got == 2 ? DDTREE_ST_BAD_LENGTH : 0;
-    if (warp == C::kLoadWarp) tmem_dealloc(tmem, C::kColumns);
-    return;
-  }
-
-  // ---- the key tiles: sinks before every row's window, then from the first row's window on
-  const int tile_tokens = a.tile_tokens / kTiles;
-  const int lo_min = a.window > 0 ? max(0, it.pos - a.window + 1) : 0, sinks = min(a.n_sinks, lo_min);
-  const int sink_tiles = (sinks + C::kKeys - 1) / C::kKeys;
-  auto tiles_of = [&](int t) {  // key tiles of product tile t
-    const int last = it.pos + min((t + 1) * tile_tokens, it.tokens) - 1;
-    return t * tile_tokens >= it.tokens || last < 0 ? 0 : sink_tiles + (last - lo_min + C::kKeys) / C::kKeys;
-  };
-  auto start_of = [&](int i) { return i < sink_tiles ? i * C::kKeys : lo_min + (i - sink_tiles) * C::kKeys; };
-  const int n_of[2] = {tiles_of(0), kTiles == 2 ? tiles_of(1) : 0};
-  const int count = max(n_of[0], n_of[1]), present = n_of[1] > 0 ? 2 : 1;
-  if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
+    mbar_init(&sh.products, 1);
+    mbar_init(&sh.drained, 1);
     fence_mbar_init();
   }
-  __syncthreads();
+  release_grid();
+  await_grid();
+  tc_fence_before();
   const uint32_t q_at = (smem_u32(smem) + 1023) & ~1023u, ring = q_at + kTiles * C::kQBytes;
+  // Items of this CTA: in every second round from the other end, since a sequence's items are longest first.
+  auto number = [&](int round) { return (int64_t)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); };
+  for (int round = tid; number(round) < a.max_items || (int64_t)round * gridDim.x < a.max_items; round += C::kThreads)
+    if (number(round) < a.max_items) a.words[number(round)] = 0;
+  int* starts = reinterpret_cast<int*>(smem + (ring - smem_u32(smem)) + C::kStages * C::kStageBytes);
+  const int tiles = list_prompt_items<C::kThreads>(a, starts, sh.scratch);
+  const bool bad = tiles < 0;
+  const int64_t items = (int64_t)tiles * a.n_kv_heads;
+  tc_fence_after();
+  const uint32_t tmem = sh.base;
+  if (bad || number(0) >= items) {
+    if (tid == 0 && bad) a.words[blockIdx.x] = DDTREE_ST_BAD_LENGTH;
+    if (warp == C::kLoadWarp) tmem_dealloc(tmem, C::kColumns);
+    return;
+  }
+
+  __syncthreads();
+  // ---- an item's key tiles: sinks before every row's window, then from the first row's window on
+  const int tile_tokens = a.tile_tokens / kTiles;
+  struct Work {
+    PromptItem it;
+    int kv, lo_min, sinks, sink_tiles, n_of[2], count, present;
+    __device__ __forceinline__ Work(const PromptArgs& a, const PromptItem& item, int id, int tile_tokens) : it(item) {
+      kv = id % a.n_kv_heads;
+      lo_min = a.window > 0 ? max(0, it.pos - a.window + 1) : 0;
+      sinks = min(a.n_sinks, lo_min);
+      sink_tiles = (sinks + C::kKeys - 1) / C::kKeys;
+      for (int t = 0; t < 2; ++t) {  // key tiles of product tile t
+        const int last = it.pos + min((t + 1) * tile_tokens, it.tokens) - 1;
+        n_of[t] = t >= kTiles || t * tile_tokens >= it.tokens || last < 0 ? 0 : sink_tiles + (last - lo_min + C::kKeys) / C::kKeys;
+      }
+      count = max(n_of[0], n_of[1]);
+      present = n_of[1] > 0 ? 2 : 1;
+    }
+    __device__ __forceinline__ int start(int i) const { return i < sink_tiles ? i * C::kKeys : lo_min + (i - sink_tiles) * C::kKeys; }
+  };
   bool late = false;
   auto wait = [&](uint64_t* bar, int phase) {  // by a whole warp
     if (late) return;
@@ -192,34 +213,65 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       atomicOr(&sh.word, DDTREE_ST_TIMEOUT);
     }
   };
+  // The item of a round, by every role but the one that writes it: its number, -1 where there is none.
+  auto take = [&](int round, PromptItem& it) {
+    wait(&sh.item[round & 1], round >> 1);
+    if (late) return -1;
+    it = sh.items[round & 1].it;
+    const int id = sh.items[round & 1].id;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.known[round & 1]);
+    return id;
+  };
 
   if (warp >= C::kLoadWarp) {
     // 384 threads have 168 registers; 128 x 80 and 256 x 208 are fewer.
     if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == C::kLoadWarp) {
-      if (count > 0 && elect_one()) {
-        mbar_arrive_expect_tx(&sh.queries, present * C::kSlabs * tile_tokens * a.group * 128);
-        for (int t = 0; t < present; ++t)
-          for (int s = 0; s < C::kSlabs; ++s)
-            load_box(&maps.q, q_at + t * C::kQBytes + s * 16384, 64 * s, kv * a.group, it.q0 + t * tile_tokens, &sh.queries);
-      }
-      __syncwarp();
-      int n = 0;
-      for (; n < 2 * count; ++n) {  // K of tile 0, V of tile 0, K of tile 1, ...
-        const int stage = n % C::kStages;
-        if (n >= C::kStages) wait(&sh.empty[stage], n / C::kStages - 1);
-        if (late) break;  // a stage that may be on its way is not filled again
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&sh.full[stage], C::kStageBytes);
-          const int row = it.k0 + start_of(n >> 1);
-#pragma unroll
-          for (int s = 0; s < C::kSlabs; ++s)
-            load_box(n & 1 ? &maps.v : &maps.k, ring + stage * C::kStageBytes + s * C::kKeys * 128, 64 * s, kv, row, &sh.full[stage]);
+      int n = 0, asked = 0;  // stages filled, items that had queries
+      for (int round = 0;; ++round) {
+        const bool more = number(round) < items;
+        const int id = more ? (int)number(round) : -1;
+        PromptItem it = {};
+        if (more) it = prompt_item_at(a, starts, id / a.n_kv_heads);
+        if (round > 1) wait(&sh.known[round & 1], (round >> 1) - 1);
+        if (late) break;  // the others' waits for the item expire
+        if (lane == 0) {
+          sh.items[round & 1].it = it;
+          sh.items[round & 1].id = id;
+          mbar_arrive(&sh.item[round & 1]);
         }
         __syncwarp();
+        if (!more) break;
+        const Work w(a, it, id, tile_tokens);
+        if (w.count == 0) continue;
+        if (asked > 0) wait(&sh.asked, asked - 1);
+        if (late) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sh.queries, w.present * C::kSlabs * tile_tokens * a.group * 128);
+          for (int t = 0; t < w.present; ++t)
+            for (int s = 0; s < C::kSlabs; ++s)
+              load_box(&maps.q, q_at + t * C::kQBytes + s * 16384, 64 * s, w.kv * a.group, it.q0 + t * tile_tokens, &sh.queries);
+        }
+        __syncwarp();
+        ++asked;
+        for (int i = 0; i < 2 * w.count; ++i, ++n) {  // K of tile 0, V of tile 0, K of tile 1, ...
+          const int stage = n % C::kStages;
+          if (n >= C::kStages) wait(&sh.empty[stage], n / C::kStages - 1);
+          if (late) break;  // a stage that may be on its way is not filled again
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&sh.full[stage], C::kStageBytes);
+            const int row = it.k0 + w.start(i >> 1);
+#pragma unroll
+            for (int s = 0; s < C::kSlabs; ++s)
+              load_box(i & 1 ? &maps.v : &maps.k, ring + stage * C::kStageBytes + s * C::kKeys * 128, 64 * s, w.kv, row, &sh.full[stage]);
+          }
+          __syncwarp();
+        }
+        if (late) break;
       }
       // Nothing of this may be on its way when the CTA ends.
-      if (count > 0) mbar_wait(&sh.queries, 0, kDrainNs);
+      if (asked > 0) mbar_wait(&sh.queries, (asked - 1) & 1, kDrainNs);
       for (int i = max(0, n - C::kStages); i < n; ++i) mbar_wait(&sh.full[i % C::kStages], (i / C::kStages) & 1, kDrainNs);
     }
     if (warp == C::kIssueWarp) {
@@ -227,82 +279,101 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       // interleave and their softmaxes meet (16,384 tokens x 16 heads of 128: 1,050 us
       // instead of 750).
       auto stage_of = [&](int n) { return ring + (n % C::kStages) * C::kStageBytes; };
-      auto s_of = [&](int t, int i) { return tmem + (C::kBuffers == 2 ? i & 1 : t) * C::kKeys; };
+      auto s_of = [&](int t, int g) { return tmem + (C::kBuffers == 2 ? g & 1 : t) * C::kKeys; };
       auto landed = [&](int n) {
         wait(&sh.full[n % C::kStages], n / C::kStages);
         tc_fence_after();
       };
-      // By one thread: S of tile t and key tile i; 64 keys of its O += P V.
-      auto score = [&](int t, int i) {
-        const uint32_t k_at = stage_of(2 * i);
+      // By one thread: S of tile t, its g-th key tile; 64 keys of its O += P V.
+      auto score = [&](int t, int g, uint32_t k_at) {
 #pragma unroll
         for (int s = 0; s < C::kSlabs; ++s)
-          mma_ss_x4<2, 2>(s_of(t, i), desc_sw128(q_at + t * C::kQBytes + s * 16384, 16, 1024), desc_sw128(k_at + s * C::kKeys * 128, 16, 1024),
+          mma_ss_x4<2, 2>(s_of(t, g), desc_sw128(q_at + t * C::kQBytes + s * 16384, 16, 1024), desc_sw128(k_at + s * C::kKeys * 128, 16, 1024),
                           product_desc(C::kKeys, false, kHalf), s > 0);
-        mma_commit(&sh.scores[C::kBuffers == 2 ? i & 1 : t]);
+        mma_commit(&sh.scores[C::kBuffers == 2 ? g & 1 : t]);
       };
-      auto accumulate = [&](int t, int i, int h) {
-        mma_ts_x4_step<128>(tmem + C::kOCol + t * kDim, s_of(t, i) + 32 * h, desc_sw128(stage_of(2 * i + 1) + h * 64 * 128, C::kKeys * 128, 1024),
-                            product_desc(kDim, true, kHalf), h > 0 || i > 0);
+      auto accumulate = [&](int t, int g, int h, uint32_t v_at, bool more) {
+        mma_ts_x4_step<128>(tmem + C::kOCol + t * kDim, s_of(t, g) + 32 * h, desc_sw128(v_at + h * 64 * 128, C::kKeys * 128, 1024),
+                            product_desc(kDim, true, kHalf), more);
       };
       auto used = [&](int n) { mma_commit(&sh.empty[n % C::kStages]); };
-      if (count > 0) {
-        wait(&sh.queries, 0);
-        landed(0);
+      int n = 0, asked = 0;                      // stages used, items that had queries
+      int before[2] = {0, 0}, had[2] = {0, 0};   // key tiles of product tiles, items with any
+      for (int round = 0;; ++round) {
+        PromptItem it;
+        const int id = take(round, it);
+        if (id < 0) break;
+        const Work k(a, it, id, tile_tokens);
+        if (k.count == 0) continue;
+        wait(&sh.queries, asked);
+        landed(n);
         if (elect_one()) {
-          for (int t = 0; t < present; ++t)
-            if (n_of[t] > 0) score(t, 0);
-          used(0);
+          for (int t = 0; t < k.present; ++t)
+            if (k.n_of[t] > 0) score(t, before[t], stage_of(n));
+          used(n);
+          if (k.count == 1) mma_commit(&sh.asked);
         }
         __syncwarp();
-      }
-      for (int i = 0; i < count; ++i) {
-        const bool more = i + 1 < count;
-        if (more) landed(2 * i + 2);
-        if (C::kBuffers == 2 && more) {  // the next scores go to the other buffer
-          if (elect_one()) {
-            score(0, i + 1);
-            used(2 * i + 2);
-          }
-          __syncwarp();
-        }
-        landed(2 * i + 1);
-        // Values of keys that no row of the item sees become zeros.
-        if (!more || i < sink_tiles) {
-          const int unseen = (i < sink_tiles ? sinks : it.pos + it.tokens) - start_of(i);
-#pragma unroll 1
-          for (int at = lane * 16; at < (C::kKeys - unseen) * 128; at += 512) {
-#pragma unroll
-            for (int s = 0; s < C::kSlabs; ++s)
-              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(stage_of(2 * i + 1) + (s + 1) * C::kKeys * 128 - 16 - at), "r"(0) : "memory");
-          }
-          fence_async_smem();
-          __syncwarp();
-        }
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          if (i >= n_of[t]) continue;
-          const int w = C::kBuffers == 2 ? i & 1 : t;
-#pragma unroll
-          for (int h = 0; h < C::kKeys / 64; ++h) {
-            wait(&sh.weights[w][h], C::kBuffers == 2 ? i >> 1 : i);
-            tc_fence_after();
+        for (int i = 0; i < k.count; ++i) {
+          const int nk = n + 2 * i + 2, nv = n + 2 * i + 1;  // stages of the next K and of this V
+          const uint32_t k_at = stage_of(nk), v_at = stage_of(nv);
+          const bool more = i + 1 < k.count;
+          if (more) landed(nk);
+          if (C::kBuffers == 2 && more) {  // the next scores go to the other buffer
             if (elect_one()) {
-              accumulate(t, i, h);
-              if (h == C::kKeys / 64 - 1) {
-                if (C::kBuffers == 2) mma_commit(&sh.products);
-                if (i + 1 == n_of[t]) mma_commit(&sh.result[t]);
-                else if (C::kBuffers == 1) score(t, i + 1);  // where P was
-              }
+              score(0, before[0] + i + 1, k_at);
+              used(nk);
             }
             __syncwarp();
           }
+          landed(nv);
+          // Values of keys that no row of the item sees become zeros.
+          if (!more || i < k.sink_tiles) {
+            const int unseen = (i < k.sink_tiles ? k.sinks : it.pos + it.tokens) - k.start(i);
+#pragma unroll 1
+            for (int at = lane * 16; at < (C::kKeys - unseen) * 128; at += 512) {
+#pragma unroll
+              for (int s = 0; s < C::kSlabs; ++s)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_at + (s + 1) * C::kKeys * 128 - 16 - at), "r"(0) : "memory");
+            }
+            fence_async_smem();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            if (i >= k.n_of[t]) continue;
+            const int g = before[t] + i, w = C::kBuffers == 2 ? g & 1 : t;
+            if (i == 0 && had[t] > 0) wait(&sh.stored[t], had[t] - 1);  // O of the item before
+#pragma unroll
+            for (int h = 0; h < C::kKeys / 64; ++h) {
+              wait(&sh.weights[w][h], C::kBuffers == 2 ? g >> 1 : g);
+              tc_fence_after();
+              if (elect_one()) {
+                accumulate(t, g, h, v_at, h > 0 || i > 0);
+                if (h == C::kKeys / 64 - 1) {
+                  if (C::kBuffers == 2) mma_commit(&sh.products);
+                  if (i + 1 == k.n_of[t]) mma_commit(&sh.result[t]);
+                  else if (C::kBuffers == 1) score(t, g + 1, k_at);  // where P was
+                }
+              }
+              __syncwarp();
+            }
+          }
+          if (elect_one()) {
+            used(nv);
+            if (C::kBuffers == 1 && more) used(nk);
+            if (i + 2 == k.count) mma_commit(&sh.asked);
+          }
+          __syncwarp();
         }
-        if (elect_one()) {
-          used(2 * i + 1);
-          if (C::kBuffers == 1 && more) used(2 * i + 2);
+        if (late) break;
+        n += 2 * k.count;
+        ++asked;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          before[t] += k.n_of[t];
+          had[t] += k.n_of[t] > 0;
         }
-        __syncwarp();
       }
       // After an expired wait products may be in flight still.
       if (elect_one()) {
@@ -315,29 +386,38 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---- softmax: a row a thread, or half a row's keys
     const int t = warp / (4 * kSplit), quarter = warp & 3, half = kSplit == 2 ? (warp >> 2) & 1 : 0, row = quarter * 32 + lane;
-    const int n = n_of[t], token = t * tile_tokens + row / a.group, head = kv * a.group + row % a.group;
-    const bool valid = row < tile_tokens * a.group && token < it.tokens;
-    // Rows that are none are computed like the last one, and not stored.
-    const int pos = it.pos + (valid ? token : it.tokens - 1);
-    const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
     constexpr int kMine = kDim / kSplit;  // columns of O of this thread
     const uint32_t my_lane = (uint32_t)(quarter * 32) << 16, o_mem = tmem + C::kOCol + t * kDim + half * kMine + my_lane;
     constexpr float kShift = kHalf ? 10.f : 0.f, kGrowth = kHalf ? 4.f : 8.f;
     const float scale = fmaxf(fabsf(a.scale_log2), 1.4e-45f);  // its sign goes to the scores; zero becomes the least number
     const uint64_t scales = pair(scale, scale);
     // What the other half of a row has to say, once a key tile.
-    auto exchange = [&](int i, float mine) {
+    int turn = 0;
+    auto exchange = [&](float mine) {
       if (kSplit == 1) return mine;
-      sh.tops[i & 1][t][half][row] = mine;
+      turn ^= 1;
+      sh.tops[turn][t][half][row] = mine;
       asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * t + quarter) : "memory");
-      return sh.tops[i & 1][t][half ^ 1][row];
+      return sh.tops[turn][t][half ^ 1][row];
     };
+    const int row_token = t * tile_tokens + row / a.group, row_head = row % a.group;
+    int before = 0, had = 0;  // key tiles of the items before, items with any
+    for (int round = 0;; ++round) {
+    PromptItem it;
+    const int id = take(round, it);
+    if (id < 0) break;
+    const Work k(a, it, id, tile_tokens);
+    const int n = k.n_of[t], token = row_token, head = k.kv * a.group + row_head;
+    const bool valid = row < tile_tokens * a.group && token < it.tokens;
+    // Rows that are none are computed like the last one, and not stored.
+    const int pos = it.pos + (valid ? token : it.tokens - 1);
+    const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
     float m = -INFINITY, l = 0.f;
     // Key tiles that every row of the warp sees whole start here to there.
     const int lo_most = __reduce_max_sync(0xffffffffu, lo), start_last = __reduce_min_sync(0xffffffffu, pos) - C::kMyKeys + 1;
     for (int i = 0; i < n; ++i) {
-      const int buffer = C::kBuffers == 2 ? i & 1 : t;
-      wait(&sh.scores[buffer], C::kBuffers == 2 ? i >> 1 : i);
+      const int g = before + i, buffer = C::kBuffers == 2 ? g & 1 : t;
+      wait(&sh.scores[buffer], C::kBuffers == 2 ? g >> 1 : g);
       tc_fence_after();
       const uint32_t s_mem = tmem + buffer * C::kKeys + C::kMyKeys * half + my_lane;
       const uint32_t p_mem = tmem + buffer * C::kKeys + C::kMyKeys / 2 * half + my_lane;
@@ -349,10 +429,10 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
         for (int c = 0; c < C::kMyKeys; ++c) x[c] ^= 0x80000000u;
       }
       // Columns up to `high`, and of those the ones from `low` on or below `sink`.
-      const int start = start_of(i) + C::kMyKeys * half;
-      if (i < sink_tiles || start > start_last || start < lo_most) {
-        const int high = min(pos, (i < sink_tiles ? sinks : it.keys) - 1) - start;
-        const int low = i < sink_tiles ? 0 : lo - start, sink = a.n_sinks - start;
+      const int start = k.start(i) + C::kMyKeys * half;
+      if (i < k.sink_tiles || start > start_last || start < lo_most) {
+        const int high = min(pos, (i < k.sink_tiles ? k.sinks : it.keys) - 1) - start;
+        const int low = i < k.sink_tiles ? 0 : lo - start, sink = a.n_sinks - start;
 #pragma unroll
         for (int w = 0; w < C::kMyKeys / 32; ++w) {
           const uint32_t seen = bits_to(high - 32 * w) & (~bits_to(low - 1 - 32 * w) | bits_to(max(sink, 0) - 1 - 32 * w));
@@ -368,7 +448,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
         for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
       }
       float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      most = fmaxf(most, exchange(i, most));
+      most = fmaxf(most, exchange(most));
       bool raised = false;
       float keep = 1.f;
       if (valid && (most - m) * scale > kGrowth) {  // also the first finite maximum
@@ -380,7 +460,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       if (i > 0 && __any_sync(0xffffffffu, raised)) {
         // With one buffer these scores came after the last product, which is complete.
         if constexpr (C::kBuffers == 2) {
-          wait(&sh.products, i - 1);
+          wait(&sh.products, g - 1);
           tc_fence_after();
         }
 #pragma unroll 1
@@ -416,59 +496,52 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       const float2 sums = apart(add2(part[0], part[1]));
       l += sums.x + sums.y;
     }
-    l += kSplit == 1 ? 0.f : exchange(n, l);
+    l += kSplit == 1 ? 0.f : exchange(l);
     // ---- the rows
     const float by = l == 0.f ? 0.f : 1.f / l;
     const int64_t to = it.q0 + token;
-    const int64_t out_at = valid ? to * a.out_stride + (int64_t)head * kDim + half * kMine : -1;
+    uint16_t* out = a.out + to * a.out_stride + (int64_t)head * kDim + half * kMine;
     bool odd = !(fabsf(l) < INFINITY);
-    // A row's columns lie in one lane; they go through where the queries were, so that
-    // a warp stores whole lines (64 short prompts of 128 columns: 37.2 -> 35.7 us).
-    constexpr int kPiece = kMine < 64 ? kMine : 64, kChunks = kPiece / 8, kTurn = kChunks == 8 ? 0 : 1;
-    const uint32_t mine = q_at + t * C::kQBytes + (half * 4 + quarter) * (32 * kPiece * 2);
     if (n > 0) {
-      wait(&sh.result[t], 0);
+      wait(&sh.result[t], had);
       tc_fence_after();
     }
 #pragma unroll 1
-    for (int c = 0; c < kMine; c += kPiece) {
+    for (int c = 0; c < kMine; c += 32) {
+      uint32_t v[32];
       if (n > 0) {
-        uint32_t v[kPiece];
-        if constexpr (kPiece == 64) tmem_ld64(o_mem + c, v);
-        else tmem_ld32(o_mem + c, v);
+        tmem_ld32(o_mem + c, v);
+        if (c + 32 == kMine) {  // the next item may have it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.stored[t]);
+        }
+      } else {
 #pragma unroll
-        for (int e = 0; e < kChunks; ++e) {
+        for (int e = 0; e < 32; ++e) v[e] = 0;
+      }
+      if (valid) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
           float y[8];
 #pragma unroll
           for (int d = 0; d < 8; ++d) {
-            y[d] = __uint_as_float(v[8 * e + d]);
+            y[d] = __uint_as_float(v[e + d]);
             odd |= !(fabsf(y[d]) < INFINITY);
             y[d] *= by;
           }
-          const uint4 w = pack8<kHalf>(y);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(mine + lane * (kPiece * 2) + ((e ^ (lane >> kTurn & (kChunks - 1))) << 4)),
-                       "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
-                       : "memory");
+          *reinterpret_cast<uint4*>(out + c + e) = pack8<kHalf>(y);
         }
-      }
-      __syncwarp();
-#pragma unroll
-      for (int e = 0; e < kChunks; ++e) {
-        const int from = (e * 32 + lane) / kChunks, chunk = lane % kChunks;
-        const int64_t at = __shfl_sync(0xffffffffu, out_at, from);
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (n > 0)
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                       : "r"(mine + from * (kPiece * 2) + ((chunk ^ (from >> kTurn & (kChunks - 1))) << 4))
-                       : "memory");
-        if (at >= 0) *reinterpret_cast<uint4*>(a.out + at + c + 8 * chunk) = w;
       }
       __syncwarp();
     }
     if (valid) {
       if (a.lse && half == 0) a.lse[to * a.n_heads + head] = l == 0.f ? -INFINITY : (m * scale - kShift + log2f(l)) * 0.6931471805599453f;
-      if (odd) atomicOr(&sh.word, kPromptAgain);
+      if (odd) atomicOr(a.words + id, kPromptAgain);
+    }
+    before += n;
+    had += n > 0;
+    if (late) break;
     }
     tc_fence_before();
     __syncwarp();
@@ -476,7 +549,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
   __syncthreads();
   tc_fence_after();
   if (warp == C::kLoadWarp) tmem_dealloc(tmem, C::kColumns);
-  if (tid == 0) a.words[blockIdx.x] = sh.word;
+  if (tid == 0 && sh.word) atomicOr(a.words + blockIdx.x, sh.word);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -513,9 +586,9 @@ bool make_map(CUtensorMap* map, const uint16_t* base, int dtype, int dim, int he
 }
 
 template <bool kHalf, int kDim, int kTiles>
-cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
+cudaError_t launch(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   using C = Config<kDim, kTiles>;
-  static_assert(C::kCtas * (C::kSmem + sizeof(Shared<kTiles, C::kSplit>) + 1024) <= 228 * 1024 && C::kStages <= 10, "shared memory");
+  static_assert(C::kCtas * (C::kSmem + C::kList + sizeof(Shared<kTiles, C::kSplit>) + 1024) <= 228 * 1024 && C::kStages <= 10, "shared memory");
   PromptMaps maps;
   if (!make_map(&maps.q, a.q, a.dtype, kDim, a.n_heads, a.q_rows, a.q_stride, a.group, a.tile_tokens / kTiles) ||
       !make_map(&maps.k, a.k, a.dtype, kDim, a.n_kv_heads, a.k_rows, a.k_stride, 1, C::kKeys) ||
@@ -528,22 +601,23 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (device & 63);
   if (!(have.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(prompt_kernel<kHalf, kDim, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(prompt_kernel<kHalf, kDim, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem + C::kList);
     if (e != cudaSuccess) return e;
     have.fetch_or(bit, std::memory_order_release);
   }
-  return launch_early(prompt_kernel<kHalf, kDim, kTiles>, a.max_items, C::kThreads, C::kSmem, stream, a, maps);
+  const unsigned grid = (unsigned)std::min<int64_t>(a.max_items, (int64_t)num_sms * C::kCtas);
+  return launch_early(prompt_kernel<kHalf, kDim, kTiles>, grid, C::kThreads, C::kSmem + (a.batch + 1) * 4, stream, a, maps);
 }
 
 // Whether sequences are short: rows of an average one.
 bool prompt_short(int batch, int q_rows, int group) { return (int64_t)q_rows * group < (int64_t)batch * kShortRows; }
 
 template <bool kHalf>
-cudaError_t launch_dim(const PromptArgs& a, cudaStream_t stream) {
+cudaError_t launch_dim(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   const bool two = a.tile_tokens > 128 / a.group;
-  return a.head_dim == 256   ? launch<kHalf, 256, 1>(a, stream)
-         : a.head_dim == 128 ? (two ? launch<kHalf, 128, 2>(a, stream) : launch<kHalf, 128, 1>(a, stream))
-                             : (two ? launch<kHalf, 64, 2>(a, stream) : launch<kHalf, 64, 1>(a, stream));
+  return a.head_dim == 256   ? launch<kHalf, 256, 1>(a, num_sms, stream)
+         : a.head_dim == 128 ? (two ? launch<kHalf, 128, 2>(a, num_sms, stream) : launch<kHalf, 128, 1>(a, num_sms, stream))
+                             : (two ? launch<kHalf, 64, 2>(a, num_sms, stream) : launch<kHalf, 64, 1>(a, num_sms, stream));
 }
 
 }  // namespace
@@ -553,7 +627,7 @@ int prompt_tile_tokens(int batch, int q_rows, int group, int head_dim) {
 }
 
 cudaError_t launch_prompt(const PromptArgs& a, int num_sms, cudaStream_t stream) {
-  const cudaError_t e = a.dtype == DDTREE_FP16 ? launch_dim<true>(a, stream) : launch_dim<false>(a, stream);
+  const cudaError_t e = a.dtype == DDTREE_FP16 ? launch_dim<true>(a, num_sms, stream) : launch_dim<false>(a, num_sms, stream);
   return e != cudaSuccess ? e : launch_prompt_rows(a, num_sms, stream);
 }
 

@@ -78,4 +78,60 @@ __device__ __forceinline__ int find_prompt_item(const PromptArgs& a, int tile, i
   return 0;
 }
 
+// All items: starts[b] is the number of the first one of sequence b (without the key
+// head), starts[batch] that of the whole list, which is returned; -1: the sequences
+// are no good.  By a whole CTA; `scratch` as above.
+template <int kThreads>
+__device__ __forceinline__ int list_prompt_items(const PromptArgs& a, int* starts, int* scratch) {
+  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.batch + kThreads - 1) / kThreads;
+  int mine = 0;
+  bool bad = false;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b >= a.batch) break;
+    const int q0 = __ldg(a.q_indptr + b), q1 = __ldg(a.q_indptr + b + 1), k0 = __ldg(a.k_indptr + b), k1 = __ldg(a.k_indptr + b + 1);
+    bad |= q0 < 0 || q1 < q0 || q1 > a.q_rows || k0 < 0 || k1 < k0 || k1 > a.k_rows;
+    starts[b] = mine;
+    if (!bad) mine += (q1 - q0 + a.tile_tokens - 1) / a.tile_tokens;
+  }
+  int inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  if (__syncthreads_or(bad)) return -1;
+  int before = inc - mine, total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  for (int i = 0; i < per && tid * per + i < a.batch; ++i) starts[tid * per + i] += before;
+  if (tid == 0) starts[a.batch] = total;
+  __syncthreads();
+  return total;
+}
+
+// Item `tile` of that list.
+__device__ __forceinline__ PromptItem prompt_item_at(const PromptArgs& a, const int* starts, int tile) {
+  int b = 0, end = a.batch;  // starts[b] <= tile < starts[end]
+  while (end - b > 1) {
+    const int mid = (b + end) >> 1;
+    if (starts[mid] <= tile) b = mid;
+    else end = mid;
+  }
+  const int q0 = __ldg(a.q_indptr + b), q1 = __ldg(a.q_indptr + b + 1), k0 = __ldg(a.k_indptr + b), k1 = __ldg(a.k_indptr + b + 1);
+  const int first = (starts[b + 1] - 1 - tile) * a.tile_tokens;
+  PromptItem item;
+  item.q0 = q0 + first;
+  item.tokens = min(a.tile_tokens, q1 - q0 - first);
+  item.k0 = k0;
+  item.keys = k1 - k0;
+  item.pos = k1 - k0 - (q1 - q0) + first;
+  return item;
+}
+
 }  // namespace ddtree
