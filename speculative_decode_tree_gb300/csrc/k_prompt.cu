@@ -105,6 +105,24 @@ __device__ __forceinline__ void load_box(const CUtensorMap* map, uint32_t dst, i
       : "memory");
 }
 
+// Four lanes with four pieces of a row each: lane j gets piece j of the four rows.
+__device__ __forceinline__ void turn_pieces(uint4 (&c)[4], int lane) {
+#pragma unroll
+  for (int step = 1; step < 4; step *= 2) {
+    const bool upper = lane & step;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & step) continue;
+      uint4 &a = c[i], &b = c[i + step];
+      const uint4 give = upper ? a : b;
+      const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, step), __shfl_xor_sync(0xffffffffu, give.y, step),
+                                   __shfl_xor_sync(0xffffffffu, give.z, step), __shfl_xor_sync(0xffffffffu, give.w, step));
+      if (upper) a = got;
+      else b = got;
+    }
+  }
+}
+
 // Bits 0 .. h of a word of 32.
 __device__ __forceinline__ uint32_t bits_to(int h) { return h < 0 ? 0u : h >= 31 ? 0xffffffffu : (2u << h) - 1u; }
 
@@ -500,7 +518,13 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     // ---- the rows
     const float by = l == 0.f ? 0.f : 1.f / l;
     const int64_t to = it.q0 + token;
-    uint16_t* out = a.out + to * a.out_stride + (int64_t)head * kDim + half * kMine;
+    // A lane has a row; where it stores, eight rows of 64 bytes at once, it has a piece of
+    // four neighbouring rows (32 rows of 16 bytes at once keep the loads and stores of a
+    // whole SM waiting: 64 short prompts 33.0 -> 28.7 us).
+    const int64_t out_at = valid ? to * a.out_stride + (int64_t)head * kDim + half * kMine : -1;
+    int64_t four[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, out_at, (lane & ~3) + i);
     bool odd = !(fabsf(l) < INFINITY);
     if (n > 0) {
       wait(&sh.result[t], had);
@@ -520,20 +544,22 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = 0;
       }
-      if (valid) {
+      uint4 piece[4];
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          float y[8];
+      for (int e = 0; e < 4; ++e) {
+        float y[8];
 #pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            y[d] = __uint_as_float(v[e + d]);
-            odd |= !(fabsf(y[d]) < INFINITY);
-            y[d] *= by;
-          }
-          *reinterpret_cast<uint4*>(out + c + e) = pack8<kHalf>(y);
+        for (int d = 0; d < 8; ++d) {
+          y[d] = __uint_as_float(v[8 * e + d]);
+          odd |= !(fabsf(y[d]) < INFINITY);
+          y[d] *= by;
         }
+        piece[e] = pack8<kHalf>(y);
       }
-      __syncwarp();
+      turn_pieces(piece, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (four[i] >= 0) *reinterpret_cast<uint4*>(a.out + four[i] + c + 8 * (lane & 3)) = piece[i];
     }
     if (valid) {
       if (a.lse && half == 0) a.lse[to * a.n_heads + head] = l == 0.f ? -INFINITY : (m * scale - kShift + log2f(l)) * 0.6931471805599453f;
