@@ -126,6 +126,31 @@ __device__ __forceinline__ void turn_pieces(uint4 (&c)[4], int lane) {
 // Bits 0 .. h of a word of 32.
 __device__ __forceinline__ uint32_t bits_to(int h) { return h < 0 ? 0u : h >= 31 ? 0xffffffffu : (2u << h) - 1u; }
 
+// An item with its key tiles: sinks before every row's window, then from the first
+// row's window on.
+struct Work {
+  PromptItem it;
+  int id, kv;  // id -1: there are no more items
+  int lo_min, sinks, sink_tiles, n_of[2];  // key tiles of each product tile
+
+  template <int kTiles, int kKeys>
+  __device__ __forceinline__ void fill(const PromptArgs& a, const PromptItem& item, int number, int tile_tokens) {
+    it = item;
+    id = number;
+    kv = number % a.n_kv_heads;
+    lo_min = a.window > 0 ? max(0, it.pos - a.window + 1) : 0;
+    sinks = min(a.n_sinks, lo_min);
+    sink_tiles = (sinks + kKeys - 1) / kKeys;
+    for (int t = 0; t < 2; ++t) {
+      const int last = it.pos + min((t + 1) * tile_tokens, it.tokens) - 1;
+      n_of[t] = t >= kTiles || t * tile_tokens >= it.tokens || last < 0 ? 0 : sink_tiles + (last - lo_min + kKeys) / kKeys;
+    }
+  }
+  __device__ __forceinline__ int count() const { return max(n_of[0], n_of[1]); }
+  template <int kKeys>
+  __device__ __forceinline__ int start(int i) const { return i < sink_tiles ? i * kKeys : lo_min + (i - sink_tiles) * kKeys; }
+};
+
 template <int kTiles, int kSplit>
 struct Shared {
   uint64_t full[10], empty[10];      // stages: landed, used by every tile
@@ -139,10 +164,7 @@ struct Shared {
   float tops[2][kTiles][2][kSplit == 2 ? 128 : 1];  // of even and odd key tiles, of both halves: the rows' maxima; at the end their sums
   uint32_t base, word;
   int scratch[28];
-  struct {
-    PromptItem it;
-    int id;  // -1: there are no more
-  } items[2];
+  Work items[2];
 };
 
 template <bool kHalf, int kDim, int kTiles>
@@ -203,25 +225,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
   }
 
   __syncthreads();
-  // ---- an item's key tiles: sinks before every row's window, then from the first row's window on
   const int tile_tokens = a.tile_tokens / kTiles;
-  struct Work {
-    PromptItem it;
-    int kv, lo_min, sinks, sink_tiles, n_of[2], count, present;
-    __device__ __forceinline__ Work(const PromptArgs& a, const PromptItem& item, int id, int tile_tokens) : it(item) {
-      kv = id % a.n_kv_heads;
-      lo_min = a.window > 0 ? max(0, it.pos - a.window + 1) : 0;
-      sinks = min(a.n_sinks, lo_min);
-      sink_tiles = (sinks + C::kKeys - 1) / C::kKeys;
-      for (int t = 0; t < 2; ++t) {  // key tiles of product tile t
-        const int last = it.pos + min((t + 1) * tile_tokens, it.tokens) - 1;
-        n_of[t] = t >= kTiles || t * tile_tokens >= it.tokens || last < 0 ? 0 : sink_tiles + (last - lo_min + C::kKeys) / C::kKeys;
-      }
-      count = max(n_of[0], n_of[1]);
-      present = n_of[1] > 0 ? 2 : 1;
-    }
-    __device__ __forceinline__ int start(int i) const { return i < sink_tiles ? i * C::kKeys : lo_min + (i - sink_tiles) * C::kKeys; }
-  };
   bool late = false;
   auto wait = [&](uint64_t* bar, int phase) {  // by a whole warp
     if (late) return;
@@ -231,15 +235,14 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       atomicOr(&sh.word, DDTREE_ST_TIMEOUT);
     }
   };
-  // The item of a round, by every role but the one that writes it: its number, -1 where there is none.
-  auto take = [&](int round, PromptItem& it) {
+  // The item of a round, by every role but the one that writes it.
+  auto take = [&](int round, Work& w) {
     wait(&sh.item[round & 1], round >> 1);
-    if (late) return -1;
-    it = sh.items[round & 1].it;
-    const int id = sh.items[round & 1].id;
+    if (late) return false;
+    w = sh.items[round & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.known[round & 1]);
-    return id;
+    return w.id >= 0;
   };
 
   if (warp >= C::kLoadWarp) {
@@ -250,36 +253,37 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       for (int round = 0;; ++round) {
         const bool more = number(round) < items;
         const int id = more ? (int)number(round) : -1;
-        PromptItem it = {};
-        if (more) it = prompt_item_at(a, starts, id / a.n_kv_heads);
+        Work w = {};
+        w.id = -1;
+        if (more) w.fill<kTiles, C::kKeys>(a, prompt_item_at(a, starts, id / a.n_kv_heads), id, tile_tokens);
+        const PromptItem& it = w.it;
+        const int tiles_here = w.count(), present = w.n_of[1] > 0 ? 2 : 1;
         if (round > 1) wait(&sh.known[round & 1], (round >> 1) - 1);
         if (late) break;  // the others' waits for the item expire
         if (lane == 0) {
-          sh.items[round & 1].it = it;
-          sh.items[round & 1].id = id;
+          sh.items[round & 1] = w;
           mbar_arrive(&sh.item[round & 1]);
         }
         __syncwarp();
         if (!more) break;
-        const Work w(a, it, id, tile_tokens);
-        if (w.count == 0) continue;
+        if (tiles_here == 0) continue;
         if (asked > 0) wait(&sh.asked, asked - 1);
         if (late) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&sh.queries, w.present * C::kSlabs * tile_tokens * a.group * 128);
-          for (int t = 0; t < w.present; ++t)
+          mbar_arrive_expect_tx(&sh.queries, present * C::kSlabs * tile_tokens * a.group * 128);
+          for (int t = 0; t < present; ++t)
             for (int s = 0; s < C::kSlabs; ++s)
               load_box(&maps.q, q_at + t * C::kQBytes + s * 16384, 64 * s, w.kv * a.group, it.q0 + t * tile_tokens, &sh.queries);
         }
         __syncwarp();
         ++asked;
-        for (int i = 0; i < 2 * w.count; ++i, ++n) {  // K of tile 0, V of tile 0, K of tile 1, ...
+        for (int i = 0; i < 2 * tiles_here; ++i, ++n) {  // K of tile 0, V of tile 0, K of tile 1, ...
           const int stage = n % C::kStages;
           if (n >= C::kStages) wait(&sh.empty[stage], n / C::kStages - 1);
           if (late) break;  // a stage that may be on its way is not filled again
           if (elect_one()) {
             mbar_arrive_expect_tx(&sh.full[stage], C::kStageBytes);
-            const int row = it.k0 + w.start(i >> 1);
+            const int row = it.k0 + w.start<C::kKeys>(i >> 1);
 #pragma unroll
             for (int s = 0; s < C::kSlabs; ++s)
               load_box(i & 1 ? &maps.v : &maps.k, ring + stage * C::kStageBytes + s * C::kKeys * 128, 64 * s, w.kv, row, &sh.full[stage]);
@@ -318,24 +322,24 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       int n = 0, asked = 0;                      // stages used, items that had queries
       int before[2] = {0, 0}, had[2] = {0, 0};   // key tiles of product tiles, items with any
       for (int round = 0;; ++round) {
-        PromptItem it;
-        const int id = take(round, it);
-        if (id < 0) break;
-        const Work k(a, it, id, tile_tokens);
-        if (k.count == 0) continue;
+        Work k;
+        if (!take(round, k)) break;
+        const PromptItem& it = k.it;
+        const int count = k.count(), present = k.n_of[1] > 0 ? 2 : 1;
+        if (count == 0) continue;
         wait(&sh.queries, asked);
         landed(n);
         if (elect_one()) {
-          for (int t = 0; t < k.present; ++t)
+          for (int t = 0; t < present; ++t)
             if (k.n_of[t] > 0) score(t, before[t], stage_of(n));
           used(n);
-          if (k.count == 1) mma_commit(&sh.asked);
+          if (count == 1) mma_commit(&sh.asked);
         }
         __syncwarp();
-        for (int i = 0; i < k.count; ++i) {
+        for (int i = 0; i < count; ++i) {
           const int nk = n + 2 * i + 2, nv = n + 2 * i + 1;  // stages of the next K and of this V
           const uint32_t k_at = stage_of(nk), v_at = stage_of(nv);
-          const bool more = i + 1 < k.count;
+          const bool more = i + 1 < count;
           if (more) landed(nk);
           if (C::kBuffers == 2 && more) {  // the next scores go to the other buffer
             if (elect_one()) {
@@ -347,7 +351,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
           landed(nv);
           // Values of keys that no row of the item sees become zeros.
           if (!more || i < k.sink_tiles) {
-            const int unseen = (i < k.sink_tiles ? k.sinks : it.pos + it.tokens) - k.start(i);
+            const int unseen = (i < k.sink_tiles ? k.sinks : it.pos + it.tokens) - k.start<C::kKeys>(i);
 #pragma unroll 1
             for (int at = lane * 16; at < (C::kKeys - unseen) * 128; at += 512) {
 #pragma unroll
@@ -380,12 +384,12 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
           if (elect_one()) {
             used(nv);
             if (C::kBuffers == 1 && more) used(nk);
-            if (i + 2 == k.count) mma_commit(&sh.asked);
+            if (i + 2 == count) mma_commit(&sh.asked);
           }
           __syncwarp();
         }
         if (late) break;
-        n += 2 * k.count;
+        n += 2 * count;
         ++asked;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -421,10 +425,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     const int row_token = t * tile_tokens + row / a.group, row_head = row % a.group;
     int before = 0, had = 0;  // key tiles of the items before, items with any
     for (int round = 0;; ++round) {
-    PromptItem it;
-    const int id = take(round, it);
-    if (id < 0) break;
-    const Work k(a, it, id, tile_tokens);
+    Work k;
+    if (!take(round, k)) break;
+    const PromptItem& it = k.it;
     const int n = k.n_of[t], token = row_token, head = k.kv * a.group + row_head;
     const bool valid = row < tile_tokens * a.group && token < it.tokens;
     // Rows that are none are computed like the last one, and not stored.
@@ -447,7 +450,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
         for (int c = 0; c < C::kMyKeys; ++c) x[c] ^= 0x80000000u;
       }
       // Columns up to `high`, and of those the ones from `low` on or below `sink`.
-      const int start = k.start(i) + C::kMyKeys * half;
+      const int start = k.start<C::kKeys>(i) + C::kMyKeys * half;
       if (i < k.sink_tiles || start > start_last || start < lo_most) {
         const int high = min(pos, (i < k.sink_tiles ? k.sinks : it.keys) - 1) - start;
         const int low = i < k.sink_tiles ? 0 : lo - start, sink = a.n_sinks - start;
@@ -525,7 +528,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     int64_t four[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, out_at, (lane & ~3) + i);
-    bool odd = !(fabsf(l) < INFINITY);
+    // l and O times zero, added up: no number if one of them is none or no end.
+    uint64_t none = pair(l * 0.f, 0.f);
+    const uint64_t by2 = pair(by, by), zero = pair(0.f, 0.f);
     if (n > 0) {
       wait(&sh.result[t], had);
       tc_fence_after();
@@ -547,14 +552,15 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       uint4 piece[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float y[8];
+        uint32_t w[4];
 #pragma unroll
-        for (int d = 0; d < 8; ++d) {
-          y[d] = __uint_as_float(v[8 * e + d]);
-          odd |= !(fabsf(y[d]) < INFINITY);
-          y[d] *= by;
+        for (int d = 0; d < 4; ++d) {
+          const uint64_t y = pair(__uint_as_float(v[8 * e + 2 * d]), __uint_as_float(v[8 * e + 2 * d + 1]));
+          none = fma2(y, zero, none);
+          const float2 z = apart(mul2(y, by2));
+          w[d] = pack2<kHalf>(z.x, z.y);
         }
-        piece[e] = pack8<kHalf>(y);
+        piece[e] = make_uint4(w[0], w[1], w[2], w[3]);
       }
       turn_pieces(piece, lane);
 #pragma unroll
@@ -563,7 +569,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     }
     if (valid) {
       if (a.lse && half == 0) a.lse[to * a.n_heads + head] = l == 0.f ? -INFINITY : (m * scale - kShift + log2f(l)) * 0.6931471805599453f;
-      if (odd) atomicOr(a.words + id, kPromptAgain);
+      const float2 both = apart(none);
+      if (!(both.x + both.y == 0.f)) atomicOr(a.words + k.id, kPromptAgain);
     }
     before += n;
     had += n > 0;
