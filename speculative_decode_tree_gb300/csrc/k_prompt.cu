@@ -29,11 +29,15 @@
 //    item see: a row whose result is no number marks its item, and a second grid,
 //    placed ahead of time, does marked items row by row (k_prompt_rows.cu).  So only
 //    prompts that hold such values pay for them.
-//  - A short sequence is mostly a CTA's start and end: one tile a CTA then, two CTAs
-//    an SM, and two threads for a row.  Where an average sequence has fewer than
-//    1,024 rows (64 prompts of 1 to 251 tokens, 32 + 8 heads of 128: 46 us with two
-//    tiles, 36 so); long ones want the two tiles (16,384 tokens, 16 + 2 heads of 128:
-//    765 us with one, 660 with two; chunks of 64 columns behind a context 398 and 253).
+//  - A CTA goes through many items, one launch's worth of CTAs through all: the loading
+//    warp reads the list ahead and hands each item to the others, and loads and first
+//    products of the next one run beside this one's stores (a CTA for each item: 64
+//    prompts of 1 to 251 tokens 36.3 us, chunks 252; so 33.0 and 237).
+//  - Short sequences take one tile a CTA, two CTAs an SM, and two threads for a row,
+//    where an average sequence has fewer than 1,024 rows (32 + 8 heads of 128: 200
+//    prompts of 20 to 30 tokens 31 us, with two tiles 40; 64 of 150 47 and 48);
+//    long ones want the two tiles (64 of 300 to 500 tokens 129 us, with one 154;
+//    16,384 tokens, 16 + 2 heads of 128, 660 and 765).
 //  - Waits are bounded (the plan's wait_limit_us).  A role whose wait expires sets
 //    TIMEOUT, goes on without waiting and comes to its end; products in flight are
 //    waited for before the tensor memory is given back, copies before the CTA ends.
@@ -42,12 +46,12 @@
 // 1.6 to 1.7 Pflop/s, by the card's power; the products alone take 583.  A pair of
 // tiles goes around in 2,600 clocks, of which its products are 2,048: S ready to P
 // stored 1,380, and the rest is P to its products to the next S.  With 64 columns the
-// products are 1,024 of 2,250, and that chain is the bound (16,384 tokens 500 us;
-// without any arithmetic in the softmax still 475).  Tried there: P in columns of its
-// own, so that the next S is made beside the softmax (560: the two tiles' softmaxes
-// meet, and one issuing warp's waits are in each other's way), an issuing thread
-// without elections (544, for the same reason), the maximum found beside the
-// exponentials (532), one tile a CTA (581).
+// products are 1,024 of 2,250, and that chain is the bound (16,384 tokens 490 us).
+// With a CTA for each item it took 517, without any arithmetic in the softmax still
+// 475, with P in columns of its own, so that the next S is made beside the softmax,
+// 560 (the two tiles' softmaxes meet, and one issuing warp's waits are in each
+// other's way), with an issuing thread without elections 544 (for the same reason),
+// with the maximum found beside the exponentials 532.
 #include <cuda.h>
 #include <string.h>
 
@@ -121,6 +125,13 @@ __device__ __forceinline__ void turn_pieces(uint4 (&c)[4], int lane) {
       else b = got;
     }
   }
+}
+
+// Whether `p` holds in a thread of two warps that meet at barrier `id`.
+__device__ __forceinline__ bool any_of_two_warps(int id, bool p) {
+  uint32_t any;
+  asm volatile("{ .reg .pred a, b; setp.ne.u32 a, %1, 0; barrier.cta.red.or.pred b, %2, 64, a; selp.u32 %0, 1, 0, b; }" : "=r"(any) : "r"((uint32_t)p), "r"(id) : "memory");
+  return any != 0;
 }
 
 // Bits 0 .. h of a word of 32.
@@ -235,10 +246,24 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       atomicOr(&sh.word, DDTREE_ST_TIMEOUT);
     }
   };
-  // The item of a round, by every role but the one that writes it.
+  // The item of a round, by every role but the one that writes it.  Warps of a tile that
+  // an item leaves empty wait here for as long as the item takes, so this wait goes on
+  // (2 s at most) as long as no other one has expired.
   auto take = [&](int round, Work& w) {
-    wait(&sh.item[round & 1], round >> 1);
     if (late) return false;
+    bool done = mbar_wait(&sh.item[round & 1], (round >> 1) & 1, a.wait_ns);
+    if (!__all_sync(0xffffffffu, done)) {
+      const uint64_t until = global_timer_ns() + kDrainNs;
+      do {
+        const bool expired = *reinterpret_cast<volatile uint32_t*>(&sh.word) & DDTREE_ST_TIMEOUT || global_timer_ns() > until;
+        if (__any_sync(0xffffffffu, expired)) {
+          late = true;
+          atomicOr(&sh.word, DDTREE_ST_TIMEOUT);
+          return false;
+        }
+        done = mbar_wait(&sh.item[round & 1], (round >> 1) & 1, a.wait_ns);
+      } while (!__all_sync(0xffffffffu, done));
+    }
     w = sh.items[round & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.known[round & 1]);
@@ -425,156 +450,157 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     const int row_token = t * tile_tokens + row / a.group, row_head = row % a.group;
     int before = 0, had = 0;  // key tiles of the items before, items with any
     for (int round = 0;; ++round) {
-    Work k;
-    if (!take(round, k)) break;
-    const PromptItem& it = k.it;
-    const int n = k.n_of[t], token = row_token, head = k.kv * a.group + row_head;
-    const bool valid = row < tile_tokens * a.group && token < it.tokens;
-    // Rows that are none are computed like the last one, and not stored.
-    const int pos = it.pos + (valid ? token : it.tokens - 1);
-    const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    float m = -INFINITY, l = 0.f;
-    // Key tiles that every row of the warp sees whole start here to there.
-    const int lo_most = __reduce_max_sync(0xffffffffu, lo), start_last = __reduce_min_sync(0xffffffffu, pos) - C::kMyKeys + 1;
-    for (int i = 0; i < n; ++i) {
-      const int g = before + i, buffer = C::kBuffers == 2 ? g & 1 : t;
-      wait(&sh.scores[buffer], C::kBuffers == 2 ? g >> 1 : g);
-      tc_fence_after();
-      const uint32_t s_mem = tmem + buffer * C::kKeys + C::kMyKeys * half + my_lane;
-      const uint32_t p_mem = tmem + buffer * C::kKeys + C::kMyKeys / 2 * half + my_lane;
-      uint32_t x[C::kMyKeys];
-      if constexpr (C::kMyKeys == 128) tmem_ld128(s_mem, x);
-      else tmem_ld64(s_mem, x);
-      if (a.scale_log2 < 0.f) {
+      Work k;
+      bool ends = !take(round, k);
+      if (kSplit == 2) ends = any_of_two_warps(1 + 4 * t + quarter, ends);  // both or none
+      if (ends) break;
+      const PromptItem& it = k.it;
+      const int n = k.n_of[t], token = row_token, head = k.kv * a.group + row_head;
+      const bool valid = row < tile_tokens * a.group && token < it.tokens;
+      // Rows that are none are computed like the last one, and not stored.
+      const int pos = it.pos + (valid ? token : it.tokens - 1);
+      const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      float m = -INFINITY, l = 0.f;
+      // Key tiles that every row of the warp sees whole start here to there.
+      const int lo_most = __reduce_max_sync(0xffffffffu, lo), start_last = __reduce_min_sync(0xffffffffu, pos) - C::kMyKeys + 1;
+      for (int i = 0; i < n; ++i) {
+        const int g = before + i, buffer = C::kBuffers == 2 ? g & 1 : t;
+        wait(&sh.scores[buffer], C::kBuffers == 2 ? g >> 1 : g);
+        tc_fence_after();
+        const uint32_t s_mem = tmem + buffer * C::kKeys + C::kMyKeys * half + my_lane;
+        const uint32_t p_mem = tmem + buffer * C::kKeys + C::kMyKeys / 2 * half + my_lane;
+        uint32_t x[C::kMyKeys];
+        if constexpr (C::kMyKeys == 128) tmem_ld128(s_mem, x);
+        else tmem_ld64(s_mem, x);
+        if (a.scale_log2 < 0.f) {
 #pragma unroll
-        for (int c = 0; c < C::kMyKeys; ++c) x[c] ^= 0x80000000u;
-      }
-      // Columns up to `high`, and of those the ones from `low` on or below `sink`.
-      const int start = k.start<C::kKeys>(i) + C::kMyKeys * half;
-      if (i < k.sink_tiles || start > start_last || start < lo_most) {
-        const int high = min(pos, (i < k.sink_tiles ? k.sinks : it.keys) - 1) - start;
-        const int low = i < k.sink_tiles ? 0 : lo - start, sink = a.n_sinks - start;
-#pragma unroll
-        for (int w = 0; w < C::kMyKeys / 32; ++w) {
-          const uint32_t seen = bits_to(high - 32 * w) & (~bits_to(low - 1 - 32 * w) | bits_to(max(sink, 0) - 1 - 32 * w));
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (!(seen >> c & 1)) x[32 * w + c] = 0xff800000u;  // -inf
+          for (int c = 0; c < C::kMyKeys; ++c) x[c] ^= 0x80000000u;
         }
-      }
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // Columns up to `high`, and of those the ones from `low` on or below `sink`.
+        const int start = k.start<C::kKeys>(i) + C::kMyKeys * half;
+        if (i < k.sink_tiles || start > start_last || start < lo_most) {
+          const int high = min(pos, (i < k.sink_tiles ? k.sinks : it.keys) - 1) - start;
+          const int low = i < k.sink_tiles ? 0 : lo - start, sink = a.n_sinks - start;
 #pragma unroll
-      for (int c = 0; c < C::kMyKeys; c += 8) {
+          for (int w = 0; w < C::kMyKeys / 32; ++w) {
+            const uint32_t seen = bits_to(high - 32 * w) & (~bits_to(low - 1 - 32 * w) | bits_to(max(sink, 0) - 1 - 32 * w));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
-      }
-      float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      most = fmaxf(most, exchange(most));
-      bool raised = false;
-      float keep = 1.f;
-      if (valid && (most - m) * scale > kGrowth) {  // also the first finite maximum
-        keep = m == -INFINITY ? 0.f : ex2_approx((m - most) * scale);
-        raised = true;
-        m = most;
-        l *= keep;
-      }
-      if (i > 0 && __any_sync(0xffffffffu, raised)) {
-        // With one buffer these scores came after the last product, which is complete.
-        if constexpr (C::kBuffers == 2) {
-          wait(&sh.products, g - 1);
-          tc_fence_after();
+            for (int c = 0; c < 32; ++c)
+              if (!(seen >> c & 1)) x[32 * w + c] = 0xff800000u;  // -inf
+          }
         }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < C::kMyKeys; c += 8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
+        }
+        float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        most = fmaxf(most, exchange(most));
+        bool raised = false;
+        float keep = 1.f;
+        if (valid && (most - m) * scale > kGrowth) {  // also the first finite maximum
+          keep = m == -INFINITY ? 0.f : ex2_approx((m - most) * scale);
+          raised = true;
+          m = most;
+          l *= keep;
+        }
+        if (i > 0 && __any_sync(0xffffffffu, raised)) {
+          // With one buffer these scores came after the last product, which is complete.
+          if constexpr (C::kBuffers == 2) {
+            wait(&sh.products, g - 1);
+            tc_fence_after();
+          }
 #pragma unroll 1
-        for (int c = 0; c < kMine; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(o_mem + c, v);
+          for (int c = 0; c < kMine; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(o_mem + c, v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * keep);
-          tmem_st32(o_mem + c, v);
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * keep);
+            tmem_st32(o_mem + c, v);
+          }
         }
-      }
-      const float from = m == -INFINITY ? 0.f : kShift - m * scale;
-      const uint64_t froms = pair(from, from);
-      // A tile's sum first, then the row's: tens of thousands of equal terms one by
-      // one would lose four digits.
-      uint64_t part[2] = {0, 0};
+        const float from = m == -INFINITY ? 0.f : kShift - m * scale;
+        const uint64_t froms = pair(from, from);
+        // A tile's sum first, then the row's: tens of thousands of equal terms one by
+        // one would lose four digits.
+        uint64_t part[2] = {0, 0};
 #pragma unroll
-      for (int h = 0; h < C::kMyKeys / 64; ++h) {
-        uint32_t p[32];
+        for (int h = 0; h < C::kMyKeys / 64; ++h) {
+          uint32_t p[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 y = apart(fma2(pair(__uint_as_float(x[64 * h + 2 * c]), __uint_as_float(x[64 * h + 2 * c + 1])), scales, froms));
-          const float u = ex2_approx(y.x), w = ex2_approx(y.y);
-          part[c & 1] = add2(part[c & 1], pair(u, w));
-          p[c] = pack2<kHalf>(u, w);
-        }
-        tmem_st32(p_mem + 32 * h, p);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.weights[buffer][half + h]);
-      }
-      const float2 sums = apart(add2(part[0], part[1]));
-      l += sums.x + sums.y;
-    }
-    l += kSplit == 1 ? 0.f : exchange(l);
-    // ---- the rows
-    const float by = l == 0.f ? 0.f : 1.f / l;
-    const int64_t to = it.q0 + token;
-    // A lane has a row; where it stores, eight rows of 64 bytes at once, it has a piece of
-    // four neighbouring rows (32 rows of 16 bytes at once keep the loads and stores of a
-    // whole SM waiting: 64 short prompts 33.0 -> 28.7 us).
-    const int64_t out_at = valid ? to * a.out_stride + (int64_t)head * kDim + half * kMine : -1;
-    int64_t four[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, out_at, (lane & ~3) + i);
-    // l and O times zero, added up: no number if one of them is none or no end.
-    uint64_t none = pair(l * 0.f, 0.f);
-    const uint64_t by2 = pair(by, by), zero = pair(0.f, 0.f);
-    if (n > 0) {
-      wait(&sh.result[t], had);
-      tc_fence_after();
-    }
-#pragma unroll 1
-    for (int c = 0; c < kMine; c += 32) {
-      uint32_t v[32];
-      if (n > 0) {
-        tmem_ld32(o_mem + c, v);
-        if (c + 32 == kMine) {  // the next item may have it
+          for (int c = 0; c < 32; ++c) {
+            const float2 y = apart(fma2(pair(__uint_as_float(x[64 * h + 2 * c]), __uint_as_float(x[64 * h + 2 * c + 1])), scales, froms));
+            const float u = ex2_approx(y.x), w = ex2_approx(y.y);
+            part[c & 1] = add2(part[c & 1], pair(u, w));
+            p[c] = pack2<kHalf>(u, w);
+          }
+          tmem_st32(p_mem + 32 * h, p);
+          tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.stored[t]);
+          if (lane == 0) mbar_arrive(&sh.weights[buffer][half + h]);
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0;
+        const float2 sums = apart(add2(part[0], part[1]));
+        l += sums.x + sums.y;
       }
-      uint4 piece[4];
+      l += kSplit == 1 ? 0.f : exchange(l);
+      // ---- the rows
+      const float by = l == 0.f ? 0.f : 1.f / l;
+      const int64_t to = it.q0 + token;
+      // A lane has a row; where it stores, eight rows of 64 bytes at once, it has a piece of
+      // four neighbouring rows (32 rows of 16 bytes at once keep the loads and stores of a
+      // whole SM waiting: 64 short prompts 33.0 -> 28.7 us).
+      const int64_t out_at = valid ? to * a.out_stride + (int64_t)head * kDim + half * kMine : -1;
+      int64_t four[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t w[4];
+      for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, out_at, (lane & ~3) + i);
+      // l and O times zero, added up: no number if one of them is none or no end.
+      uint64_t none = pair(l * 0.f, 0.f);
+      const uint64_t by2 = pair(by, by), zero = pair(0.f, 0.f);
+      if (n > 0) {
+        wait(&sh.result[t], had);
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int c = 0; c < kMine; c += 32) {
+        uint32_t v[32];
+        if (n > 0) {
+          tmem_ld32(o_mem + c, v);
+          if (c + 32 == kMine) {  // the next item may have it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.stored[t]);
+          }
+        } else {
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const uint64_t y = pair(__uint_as_float(v[8 * e + 2 * d]), __uint_as_float(v[8 * e + 2 * d + 1]));
-          none = fma2(y, zero, none);
-          const float2 z = apart(mul2(y, by2));
-          w[d] = pack2<kHalf>(z.x, z.y);
+          for (int e = 0; e < 32; ++e) v[e] = 0;
         }
-        piece[e] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      turn_pieces(piece, lane);
+        uint4 piece[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (four[i] >= 0) *reinterpret_cast<uint4*>(a.out + four[i] + c + 8 * (lane & 3)) = piece[i];
-    }
-    if (valid) {
-      if (a.lse && half == 0) a.lse[to * a.n_heads + head] = l == 0.f ? -INFINITY : (m * scale - kShift + log2f(l)) * 0.6931471805599453f;
-      const float2 both = apart(none);
-      if (!(both.x + both.y == 0.f)) atomicOr(a.words + k.id, kPromptAgain);
-    }
-    before += n;
-    had += n > 0;
-    if (late) break;
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[4];
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const uint64_t y = pair(__uint_as_float(v[8 * e + 2 * d]), __uint_as_float(v[8 * e + 2 * d + 1]));
+            none = fma2(y, zero, none);
+            const float2 z = apart(mul2(y, by2));
+            w[d] = pack2<kHalf>(z.x, z.y);
+          }
+          piece[e] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        turn_pieces(piece, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (four[i] >= 0) *reinterpret_cast<uint4*>(a.out + four[i] + c + 8 * (lane & 3)) = piece[i];
+      }
+      if (valid) {
+        if (a.lse && half == 0) a.lse[to * a.n_heads + head] = l == 0.f ? -INFINITY : (m * scale - kShift + log2f(l)) * 0.6931471805599453f;
+        const float2 both = apart(none);
+        if (!(both.x + both.y == 0.f)) atomicOr(a.words + k.id, kPromptAgain);
+      }
+      before += n;
+      had += n > 0;
     }
     tc_fence_before();
     __syncwarp();

@@ -138,6 +138,26 @@ def test_largest_windows_with_queries_that_see_nothing(window, sinks):
         _check([200, 70], 4, 2, dim, ctx=[-60, -69], window=window, sinks=sinks, seed=dim)
 
 
+@pytest.mark.parametrize("lens,ctx", [([3] * 900, None), ([1, 40, 0, 90] * 60, [0, 300, 5, -70] * 60), ([260, 700] * 20, [900, 0] * 20)])
+@pytest.mark.parametrize("dim,heads,kvh", [(64, 16, 8), (128, 16, 8), (256, 8, 8)])
+def test_many_items_for_each_cta(lens, ctx, dim, heads, kvh):
+    _check(lens, heads, kvh, dim, ctx=ctx, window=600, sinks=2, seed=dim)
+
+
+def test_one_short_chunk_behind_a_long_context_with_a_small_bound():
+    # One product tile has no rows and waits for the next item all the while.
+    c = Case([70], 8, 8, 64, ctx=[200000], seed=20, window=150000)
+    c.device()
+    c.plan.wait_limit_us = 200
+    B.ddtree_prompt_attention(*c.args, **c.kw)
+    torch.cuda.synchronize()
+    assert B.ddtree_verify_mla_check(c.ws) == 0
+    want = c.out.clone()
+    c.plan.wait_limit_us = 0
+    B.ddtree_prompt_attention(*c.args, **c.kw)
+    assert torch.equal(c.out, want)
+
+
 @pytest.mark.parametrize("kw", [dict(packed=True), dict(lse=False), dict(q_scale=30.0), dict(q_scale=30.0, dtype=torch.float16), dict(scale=-0.2),
                                 dict(scale=0.0), dict(scale=-0.2, window=50, sinks=3), dict(before=9, behind=70), dict(behind=0)])
 @pytest.mark.parametrize("dim", [64, 128, 256])

@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("dim", [64, 128, 256])
-@pytest.mark.parametrize("lens", [[4000], [30] * 40, [5, 900, 0, 300]])
+@pytest.mark.parametrize("lens", [[4000], [30] * 40, [5, 900, 0, 300], [30] * 1000, [700] * 40])
 def test_short_bounds_end_the_call(lens, dim, dtype):
     c = Case(lens, 8, 2, dim, dtype=dtype, seed=61)
     c.device()
