@@ -127,13 +127,6 @@ __device__ __forceinline__ void turn_pieces(uint4 (&c)[4], int lane) {
   }
 }
 
-// Whether `p` holds in a thread of two warps that meet at barrier `id`.
-__device__ __forceinline__ bool any_of_two_warps(int id, bool p) {
-  uint32_t any;
-  asm volatile("{ .reg .pred a, b; setp.ne.u32 a, %1, 0; barrier.cta.red.or.pred b, %2, 64, a; selp.u32 %0, 1, 0, b; }" : "=r"(any) : "r"((uint32_t)p), "r"(id) : "memory");
-  return any != 0;
-}
-
 // Bits 0 .. h of a word of 32.
 __device__ __forceinline__ uint32_t bits_to(int h) { return h < 0 ? 0u : h >= 31 ? 0xffffffffu : (2u << h) - 1u; }
 
@@ -172,6 +165,7 @@ struct Shared {
   uint64_t products;                 // 256 columns: PV of a key tile is complete
   uint64_t result[2], stored[2];     // O of a tile is complete, read
   uint64_t drained;
+  uint64_t pairs[4];                 // what a row's halves have to say is written
   float tops[2][kTiles][2][kSplit == 2 ? 128 : 1];  // of even and odd key tiles, of both halves: the rows' maxima; at the end their sums
   uint32_t base, word;
   int scratch[28];
@@ -211,6 +205,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.pairs[i], 2);
     mbar_init(&sh.products, 1);
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
@@ -442,18 +437,17 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     int turn = 0;
     auto exchange = [&](float mine) {
       if (kSplit == 1) return mine;
-      turn ^= 1;
-      sh.tops[turn][t][half][row] = mine;
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * t + quarter) : "memory");
-      return sh.tops[turn][t][half ^ 1][row];
+      sh.tops[turn & 1][t][half][row] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.pairs[quarter]);
+      wait(&sh.pairs[quarter], turn);  // bounded, for one of the two may have left after an expired wait
+      return sh.tops[turn++ & 1][t][half ^ 1][row];
     };
     const int row_token = t * tile_tokens + row / a.group, row_head = row % a.group;
     int before = 0, had = 0;  // key tiles of the items before, items with any
     for (int round = 0;; ++round) {
       Work k;
-      bool ends = !take(round, k);
-      if (kSplit == 2) ends = any_of_two_warps(1 + 4 * t + quarter, ends);  // both or none
-      if (ends) break;
+      if (!take(round, k)) break;
       const PromptItem& it = k.it;
       const int n = k.n_of[t], token = row_token, head = k.kv * a.group + row_head;
       const bool valid = row < tile_tokens * a.group && token < it.tokens;
