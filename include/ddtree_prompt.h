@@ -42,8 +42,10 @@ typedef struct ddtree_prompt_plan {
   int32_t batch, n_heads, n_kv_heads, head_dim, dtype;
   int32_t window, n_sinks;
   int32_t q_rows, k_rows;      /* rows of the packed buffers                       */
-  int32_t wait_limit_us;       /* bound of each wait inside the kernel; one that expires
-                                  sets DDTREE_ST_TIMEOUT, and the call ends without it */
+  int32_t wait_limit_us;       /* bound of each wait inside the kernel for a copy, a
+                                  product or another warp; one that expires sets
+                                  DDTREE_ST_TIMEOUT, and the call ends without it (a
+                                  CTA within a few such bounds, and 2 s at most)  */
   int32_t tile_tokens;         /* query tokens of a work item                      */
   int32_t max_items;           /* work items of the fullest batch                  */
   int64_t q_stride, k_stride, v_stride, out_stride;  /* elements between rows, multiples of 8 */

@@ -32,15 +32,18 @@
 //  - A CTA goes through many items, one launch's worth of CTAs through all: the loading
 //    warp reads the list ahead and hands each item to the others, and loads and first
 //    products of the next one run beside this one's stores (a CTA for each item: 64
-//    prompts of 1 to 251 tokens 36.3 us, chunks 252; so 33.0 and 237).
+//    prompts of 1 to 251 tokens 36.3 us, chunks 252; so 33.0 and 237, and with rows
+//    that leave as 64-byte pieces 29.1 and 228).
 //  - Short sequences take one tile a CTA, two CTAs an SM, and two threads for a row,
-//    where an average sequence has fewer than 1,024 rows (32 + 8 heads of 128: 200
+//    where an average sequence has fewer than 1,024 rows (32 + 8 heads of 128; 200
 //    prompts of 20 to 30 tokens 31 us, with two tiles 40; 64 of 150 47 and 48);
 //    long ones want the two tiles (64 of 300 to 500 tokens 129 us, with one 154;
 //    16,384 tokens, 16 + 2 heads of 128, 660 and 765).
-//  - Waits are bounded (the plan's wait_limit_us).  A role whose wait expires sets
-//    TIMEOUT, goes on without waiting and comes to its end; products in flight are
-//    waited for before the tensor memory is given back, copies before the CTA ends.
+//  - Waits are bounded (the plan's wait_limit_us; for the next item 2 s, since a warp
+//    without rows waits there while others work).  A role whose wait expires sets
+//    TIMEOUT, goes on without waiting to the end of its item and leaves; products in
+//    flight are waited for before the tensor memory is given back, copies before the
+//    CTA ends.
 //
 // Measured: 16,384 tokens of 16 + 2 heads of 128 columns (1.1 Tflop) 650 to 700 us,
 // 1.6 to 1.7 Pflop/s, by the card's power; the products alone take 583.  A pair of
