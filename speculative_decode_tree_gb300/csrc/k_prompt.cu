@@ -164,7 +164,7 @@ struct Shared {
   uint64_t item[2], known[2];        // items (even, odd): written, read by every role
   uint64_t queries, asked;           // landed, multiplied by all keys
   uint64_t scores[2];                // S of a tile (256 columns: of a buffer) is complete
-  uint64_t weights[2][2];            // 64 keys of P are written, by each half's threads
+  uint64_t weights[2][2];            // 64 keys of P are written, by each half's threads; the first: O is scaled too, by both
   uint64_t products;                 // 256 columns: PV of a key tile is complete
   uint64_t result[2], stored[2];     // O of a tile is complete, read
   uint64_t drained;
@@ -198,7 +198,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     mbar_init(&sh.asked, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.scores[i], 1);
-      for (int h = 0; h < 2; ++h) mbar_init(&sh.weights[i][h], 4);
+      for (int h = 0; h < 2; ++h) mbar_init(&sh.weights[i][h], h == 0 ? 4 * kSplit : 4);
       mbar_init(&sh.result[i], 1);
       mbar_init(&sh.stored[i], 4 * kSplit);
       mbar_init(&sh.item[i], 1);
@@ -442,9 +442,11 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     auto exchange = [&](float mine) {
       if (kSplit == 1) return mine;
       sh.tops[turn & 1][t][half][row] = mine;
+      tc_fence_before();  // the second half's P goes where the first half's scores were
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.pairs[quarter]);
       wait(&sh.pairs[quarter], turn);  // bounded, for one of the two may have left after an expired wait
+      tc_fence_after();
       return sh.tops[turn++ & 1][t][half ^ 1][row];
     };
     const int row_token = t * tile_tokens + row / a.group, row_head = row % a.group;
@@ -517,6 +519,13 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
             for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * keep);
             tmem_st32(o_mem + c, v);
           }
+        }
+        // The first half's product goes to all columns of O, the second half's among them.
+        if (half == 1) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.weights[buffer][0]);
         }
         const float from = m == -INFINITY ? 0.f : kShift - m * scale;
         const uint64_t froms = pair(from, from);

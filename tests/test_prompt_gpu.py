@@ -334,3 +334,25 @@ def test_refusals():
         B.ddtree_prompt_attention(plan, q, k, v, c.q_indptr, c.k_indptr, float("inf"), c.out, c.ws)
     with pytest.raises(B.DDTreeError):
         B.ddtree_prompt_attention(plan, q, k, v, c.q_indptr, c.k_indptr, 1.0, q, c.ws)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,ctx", [([3] * 90, 700), ([200] * 40, 0), ([1, 60, 129, 250] * 12, 300)])
+def test_rising_scores_of_short_sequences(lens, ctx, dim, dtype):
+    # Short sequences take two threads for a row, each with half of its keys and half of its columns of O: where the
+    # maximum rises at every key tile, both halves have to be scaled before a product goes on top of them.  More items
+    # than two for each SM, many times over: equal bits each time.
+    c = Case(lens, 8, 4, dim, ctx=[ctx] * len(lens), seed=22, scale=1.0, dtype=dtype)
+    c.q[:, :, 0] = 1.0
+    c.q[:, :, 1:] *= 0.01
+    for a, b in zip(c.kp, c.kp[1:]):
+        c.k[a:b, :, 0] = torch.linspace(-60, 60, b - a).to(dtype)[:, None]
+    assert c.run() == 0
+    c.compare()
+    out, lse = c.out.clone(), c.lse.clone()
+    for _ in range(50):
+        c.out.copy_(c.out0), c.lse.copy_(c.lse0)
+        B.ddtree_prompt_attention(*c.args, **c.kw)
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+    assert B.ddtree_verify_mla_check(c.ws) == 0
