@@ -254,6 +254,13 @@ __global__ void __launch_bounds__(kThreads, 4) draft8_append_kernel(const __grid
   const int n0 = blockIdx.x * chunk, n_end = min(n0 + chunk, a.n_tokens);
   const uint4 none = make_uint4(0, 0, 0, 0);
 
+  // Before a CTA in which no run begins leaves: without queries there may be no other one for its tokens.
+  if (blockIdx.y == 0 && warp == 0 && a.status && n0 + lane < n_end) {
+    const int pos = __ldg(a.positions + n0 + lane), slot = __ldg(a.slots + n0 + lane);
+    if (pos < -1) atomicOr(a.status, DDTREE_ST_BAD_LENGTH);
+    else if (pos >= 0 && (slot < -1 || slot >= a.total_slots)) atomicOr(a.status, DDTREE_ST_BAD_INDEX);
+  }
+
   // ---- the chunk's runs: lane i has token n0 + i, and the i-th and i + 32-th behind the chunk
   struct Spot {
     int block, place;  // number of the token's block, its place there; -1 where nothing is written
@@ -290,11 +297,6 @@ __global__ void __launch_bounds__(kThreads, 4) draft8_append_kernel(const __grid
       if (!rows_on) return;  // the whole CTA: nothing begins here
       tail = 0;
     }
-  }
-  if (blockIdx.y == 0 && warp == 0 && a.status && n0 + lane < n_end) {
-    const int pos = __ldg(a.positions + n0 + lane), slot = __ldg(a.slots + n0 + lane);
-    if (pos < -1) atomicOr(a.status, DDTREE_ST_BAD_LENGTH);
-    else if (pos >= 0 && (slot < -1 || slot >= a.total_slots)) atomicOr(a.status, DDTREE_ST_BAD_INDEX);
   }
   const int pairs = a.rope.rot_dim / 2;
   Row wq = {}, wk = {};

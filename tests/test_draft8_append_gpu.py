@@ -180,6 +180,26 @@ def test_padding_and_bad_slots():
         _check([-1] * 12, 4, 2, 64, positions=[-1] * 12, **kw)
 
 
+@pytest.mark.parametrize("heads,kvh", [(0, 1), (0, 5), (0, 8), (32, 8)])
+@pytest.mark.parametrize("n", [1, 12, 300, 2500])
+@pytest.mark.parametrize("block", [1, 8, 16])
+def test_bad_tokens_are_reported_with_and_without_queries(block, n, heads, kvh):
+    # Few tokens are spread over CTAs by their heads, and without queries every CTA looks for runs alone.
+    pages = -(-n // 16) + 1
+    good = _laid(n, 16, pages, 0)
+    last = n - 1
+    for slots, pos, status in ((dict([(last, pages * 16)]), {}, B.DDTREE_ST_BAD_INDEX), (dict([(0, -2)]), {}, B.DDTREE_ST_BAD_INDEX),
+                               ({}, dict([(last, -2)]), B.DDTREE_ST_BAD_LENGTH), ({}, dict([(0, -2 ** 31)]), B.DDTREE_ST_BAD_LENGTH),
+                               (dict([(0, 2 ** 31 - 1)]), dict([(last, -9)]) if n > 1 else {},
+                                B.DDTREE_ST_BAD_INDEX | (B.DDTREE_ST_BAD_LENGTH if n > 1 else 0)),
+                               ({i: -5 for i in range(n)}, {}, B.DDTREE_ST_BAD_INDEX), ({i: -5 for i in range(n)}, {i: -1 for i in range(n)}, 0)):
+        c = Case([slots.get(i, s) for i, s in enumerate(good)], heads, kvh, 128, block=block, page=16, pages=pages, seed=n,
+                 positions=[pos.get(i, 40 + i) for i in range(n)])
+        assert c.run() == status
+        if n <= 12:
+            c.compare()
+
+
 def test_values_that_are_no_numbers():
     for block in (1, 16):
         c = Case(_laid(20, 16, 2, 0), 2, 2, 64, block=block, page=16, pages=2, norm=False, positions=[0] * 20, seed=5)
