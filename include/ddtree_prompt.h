@@ -21,7 +21,9 @@
  * inputs' type (half a step of it) where it meets V, while the sums take it
  * unrounded, and fp16 probabilities carry a factor of 2^10, so that keys down
  * to 2^-34 of the largest count.  An output is rounded once.  Equal inputs give
- * equal bits.
+ * equal bits.  The tensor cores cut their sums off at 32 bits, which takes 6e-9 of
+ * sum p |v| for each key: rows of many keys are summed in parts of 16,384 (where
+ * rows of the plan may see more than 32,768), so that this stays below 2e-4.
  *
  * Conventions as in ddtree_verify.h.
  */
@@ -63,8 +65,9 @@ DDTREE_API int ddtree_prompt_attention_plan(int batch, int q_rows, int k_rows, i
                                             int dtype, int window, int n_sinks, ddtree_prompt_plan_t* plan);
 
 /* Workspace bytes for a plan (a multiple of 256; 256-byte aligned buffer): the
- * 256-byte status block (read with ddtree_verify_mla_check) and a word for
- * each work item.  It keeps nothing between calls; calls that may overlap on
+ * 256-byte status block (read with ddtree_verify_mla_check), a word for each
+ * work item, and where rows may see more than 32,768 keys 64 or 128 KB for each
+ * of up to 320 thread blocks (20 MB at most).  It keeps nothing between calls; calls that may overlap on
  * the GPU need a workspace each.  0 for a null plan. */
 DDTREE_API size_t ddtree_prompt_attention_workspace_size(const ddtree_prompt_plan_t* plan);
 

@@ -381,6 +381,7 @@ struct PromptArgs {
   uint64_t wait_ns;            // bound of every wait
   int32_t batch, n_heads, n_kv_heads, group, head_dim, dtype, window, n_sinks;
   int32_t q_rows, k_rows, tile_tokens, max_items;
+  float* folds;                // sums of earlier keys, for each CTA; null where no row sees so many
 };
 constexpr uint32_t kPromptAgain = 0x80000000u;  // the item goes row by row
 
@@ -424,6 +425,7 @@ int draft8_shares(int head_dim, int num_sms);
 int64_t draft8_workspace_bytes(int head_dim, int n_shares);
 cudaError_t launch_draft8_attention(const Draft8AttnArgs& a, cudaStream_t stream);
 int prompt_tile_tokens(int batch, int q_rows, int group, int head_dim);
+int64_t prompt_fold_bytes(int k_rows, int head_dim, int group, int window, int n_sinks, int tile_tokens, int64_t max_items);
 cudaError_t launch_prompt(const PromptArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_prompt_rows(const PromptArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_maps(const MapsArgs& a, int num_sms, cudaStream_t stream);

@@ -74,6 +74,17 @@ struct PromptMaps {
   CUtensorMap q, k, v;
 };
 
+// The products cut a sum off where it does not fit into 32 bits, always towards zero:
+// 6.3e-9 of it for every key (values of one sign, 2^16 to 2^22 keys), so that a million
+// keys in one sum lost 0.7 %.  Where rows may see more than kLongKeys keys, the form
+// kLong ends the sum in the tensor memory after every kFoldKeys and joins the parts in
+// the workspace, in 32 bits: 1e-4 of a part at most, 2e-4 where the other form still
+// serves, below half a step of an fp16 probability.  A row's part is 512 bytes or so,
+// and the form's other instructions cost 1.7 % (16,384 tokens of 16 + 2 heads of 128:
+// 714 us for 702 in turn), hence two forms.  Parts of 4,096, 8,192 and 16,384 keys: 748,
+// 728 and 721 us there.  kMostSms: SMs that a plan has room for.
+constexpr int kFoldKeys = 16384, kLongKeys = 32768, kMostSms = 160;
+
 // kTiles: product tiles of a CTA.  One tile of 64 or 128 columns leaves room for two
 // CTAs on an SM: short sequences, where a CTA's start and end are most of its time.
 template <int kDim, int kTiles>
@@ -97,6 +108,8 @@ struct Config {
   static constexpr int kLoadWarp = 4 * kTiles * kSplit, kIssueWarp = kLoadWarp + 1;
   static constexpr int kThreads = 32 * (kTiles == 2 ? kLoadWarp + 4 : kIssueWarp + 1);
   static constexpr int kList = (DDTREE_MAX_BATCH + 1) * 4;  // of sequences
+  static constexpr int kFold = kFoldKeys / kKeys;           // key tiles of one sum in the tensor memory
+  static constexpr int64_t kFoldBytes = (int64_t)kTiles * 128 * kDim * 4;
 };
 constexpr int kShortRows = 1024;  // of an average sequence: above
 constexpr uint64_t kDrainNs = 2000000000ull;  // for products and copies in flight where the kernel ends
@@ -175,7 +188,7 @@ struct Shared {
   Work items[2];
 };
 
-template <bool kHalf, int kDim, int kTiles>
+template <bool kHalf, int kDim, int kTiles, bool kLong>
 __global__ void __launch_bounds__(Config<kDim, kTiles>::kThreads, Config<kDim, kTiles>::kCtas)
 prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps) {
   using C = Config<kDim, kTiles>;
@@ -395,7 +408,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
               wait(&sh.weights[w][h], C::kBuffers == 2 ? g >> 1 : g);
               tc_fence_after();
               if (elect_one()) {
-                accumulate(t, g, h, v_at, h > 0 || i > 0);
+                accumulate(t, g, h, v_at, h > 0 || (kLong ? i % C::kFold > 0 : i > 0));
                 if (h == C::kKeys / 64 - 1) {
                   if (C::kBuffers == 2) mma_commit(&sh.products);
                   if (i + 1 == k.n_of[t]) mma_commit(&sh.result[t]);
@@ -451,6 +464,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     };
     const int row_token = t * tile_tokens + row / a.group, row_head = row % a.group;
     int before = 0, had = 0;  // key tiles of the items before, items with any
+    float4* const folds = reinterpret_cast<float4*>(a.folds) + (((int64_t)blockIdx.x * kTiles + t) * kDim + half * kMine) / 4 * 128 + row;
     for (int round = 0;; ++round) {
       Work k;
       if (!take(round, k)) break;
@@ -461,12 +475,41 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       const int pos = it.pos + (valid ? token : it.tokens - 1);
       const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       float m = -INFINITY, l = 0.f;
+      float m_fold = -INFINITY, l_fold = 0.f;  // of what lies in the workspace
       // Key tiles that every row of the warp sees whole start here to there.
       const int lo_most = __reduce_max_sync(0xffffffffu, lo), start_last = __reduce_min_sync(0xffffffffu, pos) - C::kMyKeys + 1;
       for (int i = 0; i < n; ++i) {
         const int g = before + i, buffer = C::kBuffers == 2 ? g & 1 : t;
         wait(&sh.scores[buffer], C::kBuffers == 2 ? g >> 1 : g);
         tc_fence_after();
+        // With one buffer these scores came after the last product, which is complete.
+        const bool anew = kLong && i > 0 && i % C::kFold == 0;
+        if (anew) {
+          // What O is goes to the workspace, and O starts anew.
+          if constexpr (C::kBuffers == 2) {  // as below
+            wait(&sh.products, g - 1);
+            tc_fence_after();
+          }
+          const float by = m_fold == -INFINITY ? 0.f : ex2_approx((m_fold - m) * scale);
+#pragma unroll 1
+          for (int c = 0; c < kMine; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(o_mem + c, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float4* at = folds + (c / 4 + e) * 128;
+              float4 u = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+              if (i > C::kFold) {  // not the first time
+                const float4 w = *at;
+                u.x += w.x * by; u.y += w.y * by; u.z += w.z * by; u.w += w.w * by;
+              }
+              *at = u;
+            }
+          }
+          l_fold = l_fold * by + l;
+          l = 0.f;
+          m_fold = m;
+        }
         const uint32_t s_mem = tmem + buffer * C::kKeys + C::kMyKeys * half + my_lane;
         const uint32_t p_mem = tmem + buffer * C::kKeys + C::kMyKeys / 2 * half + my_lane;
         uint32_t x[C::kMyKeys];
@@ -505,7 +548,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
           m = most;
           l *= keep;
         }
-        if (i > 0 && __any_sync(0xffffffffu, raised)) {
+        if (i > 0 && !anew && __any_sync(0xffffffffu, raised)) {
           // With one buffer these scores came after the last product, which is complete.
           if constexpr (C::kBuffers == 2) {
             wait(&sh.products, g - 1);
@@ -551,6 +594,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
         const float2 sums = apart(add2(part[0], part[1]));
         l += sums.x + sums.y;
       }
+      const float fold_by = m_fold == -INFINITY ? 0.f : ex2_approx((m_fold - m) * scale);
+      if constexpr (kLong) l += l_fold * fold_by;
       l += kSplit == 1 ? 0.f : exchange(l);
       // ---- the rows
       const float by = l == 0.f ? 0.f : 1.f / l;
@@ -582,6 +627,16 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = 0;
+        }
+        if (kLong && n > C::kFold) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 w = folds[(c / 4 + e) * 128];
+            v[4 * e] = __float_as_uint(__uint_as_float(v[4 * e]) + w.x * fold_by);
+            v[4 * e + 1] = __float_as_uint(__uint_as_float(v[4 * e + 1]) + w.y * fold_by);
+            v[4 * e + 2] = __float_as_uint(__uint_as_float(v[4 * e + 2]) + w.z * fold_by);
+            v[4 * e + 3] = __float_as_uint(__uint_as_float(v[4 * e + 3]) + w.w * fold_by);
+          }
         }
         uint4 piece[4];
 #pragma unroll
@@ -651,8 +706,8 @@ bool make_map(CUtensorMap* map, const uint16_t* base, int dtype, int dim, int he
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kHalf, int kDim, int kTiles>
-cudaError_t launch(const PromptArgs& a, int num_sms, cudaStream_t stream) {
+template <bool kHalf, int kDim, int kTiles, bool kLong>
+cudaError_t launch_one(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   using C = Config<kDim, kTiles>;
   static_assert(C::kCtas * (C::kSmem + C::kList + sizeof(Shared<kTiles, C::kSplit>) + 1024) <= 228 * 1024 && C::kStages <= 10, "shared memory");
   PromptMaps maps;
@@ -667,12 +722,17 @@ cudaError_t launch(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (device & 63);
   if (!(have.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(prompt_kernel<kHalf, kDim, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem + C::kList);
+    e = cudaFuncSetAttribute(prompt_kernel<kHalf, kDim, kTiles, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem + C::kList);
     if (e != cudaSuccess) return e;
     have.fetch_or(bit, std::memory_order_release);
   }
-  const unsigned grid = (unsigned)std::min<int64_t>(a.max_items, (int64_t)num_sms * C::kCtas);
-  return launch_early(prompt_kernel<kHalf, kDim, kTiles>, grid, C::kThreads, C::kSmem + (a.batch + 1) * 4, stream, a, maps);
+  const unsigned grid = (unsigned)std::min<int64_t>(a.max_items, (int64_t)std::min(num_sms, kMostSms) * C::kCtas);
+  return launch_early(prompt_kernel<kHalf, kDim, kTiles, kLong>, grid, C::kThreads, C::kSmem + (a.batch + 1) * 4, stream, a, maps);
+}
+
+template <bool kHalf, int kDim, int kTiles>
+cudaError_t launch(const PromptArgs& a, int num_sms, cudaStream_t stream) {
+  return a.folds ? launch_one<kHalf, kDim, kTiles, true>(a, num_sms, stream) : launch_one<kHalf, kDim, kTiles, false>(a, num_sms, stream);
 }
 
 // Whether sequences are short: rows of an average one.
@@ -690,6 +750,20 @@ cudaError_t launch_dim(const PromptArgs& a, int num_sms, cudaStream_t stream) {
 
 int prompt_tile_tokens(int batch, int q_rows, int group, int head_dim) {
   return 128 / group * (head_dim == 256 || prompt_short(batch, q_rows, group) ? 1 : 2);
+}
+
+// Bytes for sums that go on beyond what stays in the tensor memory; 0 where no row sees that many keys.
+int64_t prompt_fold_bytes(int k_rows, int head_dim, int group, int window, int n_sinks, int tile_tokens, int64_t max_items) {
+  const int64_t keys = window > 0 ? std::min<int64_t>(k_rows, (int64_t)n_sinks + window + tile_tokens) : k_rows;
+  if (keys <= kLongKeys) return 0;
+  const bool two = tile_tokens > 128 / group;
+  auto bytes = [&](auto config) -> int64_t {
+    using C = decltype(config);
+    return std::min<int64_t>(max_items, kMostSms * C::kCtas) * C::kFoldBytes;
+  };
+  return head_dim == 256   ? bytes(Config<256, 1>{})
+         : head_dim == 128 ? (two ? bytes(Config<128, 2>{}) : bytes(Config<128, 1>{}))
+                           : (two ? bytes(Config<64, 2>{}) : bytes(Config<64, 1>{}));
 }
 
 cudaError_t launch_prompt(const PromptArgs& a, int num_sms, cudaStream_t stream) {

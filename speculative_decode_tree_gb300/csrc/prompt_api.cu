@@ -27,14 +27,18 @@ int64_t items_of(int batch, int q_rows, int n_kv_heads, int tile_tokens) {
   return ((int64_t)q_rows / tile_tokens + batch) * n_kv_heads;
 }
 
-int64_t workspace_of(int64_t items) { return 256 + (items * 4 + 255) / 256 * 256; }
+int64_t words_end(int64_t items) { return 256 + (items * 4 + 255) / 256 * 256; }
+
+int64_t workspace_of(const ddtree_prompt_plan_t& p, int64_t items) {
+  return words_end(items) + prompt_fold_bytes(p.k_rows, p.head_dim, p.n_heads / p.n_kv_heads, p.window, p.n_sinks, p.tile_tokens, items);
+}
 
 bool plan_ok(const ddtree_prompt_plan_t* p) {
   if (!p || !sizes_ok(p->batch, p->q_rows, p->k_rows, p->n_heads, p->n_kv_heads, p->head_dim, p->dtype, p->window, p->n_sinks))
     return false;
   if (p->tile_tokens != prompt_tile_tokens(p->batch, p->q_rows, p->n_heads / p->n_kv_heads, p->head_dim) || p->wait_limit_us < 0) return false;
   const int64_t items = items_of(p->batch, p->q_rows, p->n_kv_heads, p->tile_tokens);
-  if (items > INT32_MAX || p->max_items != items || p->workspace_bytes != workspace_of(items)) return false;
+  if (items > INT32_MAX || p->max_items != items || p->workspace_bytes != workspace_of(*p, items)) return false;
   const int64_t width = (int64_t)p->n_heads * p->head_dim, kv_width = (int64_t)p->n_kv_heads * p->head_dim;
   for (int64_t s : {p->q_stride, p->out_stride})
     if (s != 0 && (s < width || s % 8 || s > kMaxStride)) return false;
@@ -66,7 +70,7 @@ extern "C" int ddtree_prompt_attention_plan(int batch, int q_rows, int k_rows, i
   const int64_t items = items_of(batch, q_rows, n_kv_heads, p.tile_tokens);
   if (items > INT32_MAX) return DDTREE_EINVAL;
   p.max_items = (int32_t)items;
-  p.workspace_bytes = workspace_of(items);
+  p.workspace_bytes = workspace_of(p, items);
   *plan = p;
   return DDTREE_OK;
 }
@@ -104,6 +108,8 @@ extern "C" int ddtree_prompt_attention(const ddtree_prompt_plan_t* plan, const v
   a.lse = lse;
   a.status = static_cast<uint32_t*>(workspace);
   a.words = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + 256);
+  const int64_t folds_at = words_end(plan->max_items);
+  if (plan->workspace_bytes > folds_at) a.folds = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + folds_at);
   a.q_stride = plan->q_stride ? plan->q_stride : width;
   a.k_stride = plan->k_stride ? plan->k_stride : kv_width;
   a.v_stride = plan->v_stride ? plan->v_stride : kv_width;

@@ -356,3 +356,44 @@ def test_rising_scores_of_short_sequences(lens, ctx, dim, dtype):
         B.ddtree_prompt_attention(*c.args, **c.kw)
         assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
     assert B.ddtree_verify_mla_check(c.ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim,tokens,heads,log_keys", [(64, 2, 8, 20), (128, 2, 8, 20), (256, 2, 8, 20), (64, 300, 4, 19), (128, 300, 4, 19)])
+@pytest.mark.parametrize("rising,window", [(False, 0), (True, 0), (False, 300000)])
+def test_sums_over_very_many_keys(dim, tokens, heads, log_keys, rising, window, dtype):
+    # Values of one sign, so that whatever a long sum loses adds up.  Bound: half a step of the output; half a step of
+    # every probability; and in the tensor cores, which cut sums off where they do not fit into 32 bits, 2^-23 of the sum
+    # for every four keys of the 16,384 that one sum goes over.  lse: 64 units for sums that are halves of halves.
+    g = torch.Generator(device="cuda").manual_seed(dim + tokens)
+    n, sinks = 1 << log_keys, 5000 if window else 0
+    q, k = (torch.randn(*s, generator=g, device="cuda").to(dtype) for s in ((tokens, heads, dim), (n, 1, dim)))
+    v = (torch.rand(n, 1, dim, generator=g, device="cuda") + 1).to(dtype)
+    if rising:
+        q[:, :, 0] = 1.0
+        k[:, 0, 0] = (torch.linspace(-40, 40, n, device="cuda")).to(dtype)
+    plan = B.ddtree_prompt_attention_plan(1, tokens, n, heads, 1, dim, dtype, window, sinks)
+    ws = torch.full((B.ddtree_prompt_attention_workspace_size(plan),), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(tokens, heads, device="cuda")
+    indptr = [torch.tensor([0, m], dtype=I32, device="cuda") for m in (tokens, n)]
+    B.ddtree_prompt_attention(plan, q, k, v, *indptr, dim ** -0.5, out, ws, lse=lse)
+    assert B.ddtree_verify_mla_check(ws) == 0
+    half, kd, vd = torch.finfo(dtype).eps / 2, k[:, 0].double(), v[:, 0].double()
+    j = torch.arange(n, device="cuda")[None, :]
+    for first in range(0, tokens, 50):
+        rows = slice(first, min(tokens, first + 50))
+        p = torch.arange(n - tokens + first, n - tokens + rows.stop, device="cuda")[:, None]
+        seen = j <= p
+        if window:
+            seen &= (j > p - window) | (j < sinks)
+        for h in range(heads):
+            s = (q[rows, h].double() @ kd.T) * dim ** -0.5
+            terms = (q[rows, h].double().abs() @ kd.abs().T).amax(-1) * dim ** -0.5
+            s.masked_fill_(~seen, -float("inf"))
+            ref_lse = torch.logsumexp(s, -1)
+            ref = torch.exp(s - ref_lse[:, None]) @ vd
+            bound = ref * (half + half + 4096 * 2.0 ** -23 + (2 * dim * U * terms + 64 * U)[:, None] * 2)
+            over = ((out[rows, h].double() - ref).abs() - bound).max()
+            assert float(over) <= 0, f"out {float(over):.3e} over its bound"
+            over = ((lse[rows, h].double() - ref_lse).abs() - (dim * U * terms + 8 * U * ref_lse.abs() + 64 * U)).max()
+            assert float(over) <= 0, f"lse {float(over):.3e} over its bound"

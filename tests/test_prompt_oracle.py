@@ -97,3 +97,15 @@ def test_plan_and_refusals(lib):
         setattr(plan, field, value)
         assert call() == B.DDTREE_EINVAL, field
         setattr(plan, field, kept)
+
+
+def test_workspace_of_long_sums(lib):
+    # Room for sums that go on beyond 16,384 keys, in plans of more than 32,768, and none where no row sees as many.
+    def extra(q, k, h, kvh, dim, window=0, n_sinks=0, batch=1):
+        p = B.ddtree_prompt_attention_plan(batch, q, k, h, kvh, dim, torch.bfloat16, window, n_sinks)
+        return p.workspace_bytes - 256 - (4 * p.max_items + 255) // 256 * 256
+    for dim in (64, 128, 256):
+        assert extra(5000, 32768, 8, 2, dim) == 0 and extra(5000, 1 << 24, 8, 2, dim, window=30000, n_sinks=2000) == 0
+        rows = 128 * (1 if dim == 256 else 2)
+        assert extra(100000, 32769, 8, 2, dim) == extra(100000, 1 << 24, 8, 2, dim, 2 ** 31 - 1, 2 ** 31 - 1) == 160 * rows * dim * 4
+        assert extra(100, 1 << 24, 8, 2, dim, window=4096, n_sinks=30000, batch=3) == (100 // 32 + 3) * 2 * 128 * dim * 4
