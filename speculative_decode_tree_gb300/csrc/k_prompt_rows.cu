@@ -8,9 +8,10 @@
 // It runs behind the tensor-core kernel for the items that one has marked, and
 // costs a call without any 1 to 2 us, most of them beside the other's end.  A key
 // row is read by one lane alone, 16 bytes after 16 bytes, so what bounds it is the
-// latency of those loads: a NaN in the last value of 16,384 (16 + 2 heads of 128
-// columns), which marks 512 rows, takes 7 ms.  Spreading an item's rows over the
-// CTAs, one for each warp, took it there from 98.
+// latency of those loads, with as many in flight as 120 registers hold (64: 8.1 ms): a
+// NaN in the last value of 16,384 (16 + 2 heads of 128 columns), which marks 512 rows,
+// takes 5.6 ms.  Spreading an item's rows over the CTAs, one for each warp, took it
+// there from 98.
 #include "prompt_list.cuh"
 #include "rope.cuh"
 #include "tc_ptx.cuh"
@@ -19,9 +20,13 @@ namespace ddtree {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+// A row may have 2^24 keys, and a sum of n numbers one by one is up to n half steps of 32
+// bits off where they are alike (262,144 keys: 0.4 to 0.6 %).  In three levels no sum has
+// more than 725 terms.
+constexpr int kChain = 724;
 
 template <bool kHalf, int kDim>
-__global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const __grid_constant__ PromptArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) prompt_rows_kernel(const __grid_constant__ PromptArgs a) {
   constexpr int kCols = kDim / 32;  // columns of a lane
   __shared__ int scratch[kWarps + 8];
   __shared__ __align__(16) float query[kWarps][kDim];
@@ -72,9 +77,10 @@ __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const __grid_cons
           query[warp][2 * (c * 32 + lane) + 1] = x.y;
         }
         __syncwarp();
-        float o[kCols], top = -INFINITY, sum = 0.f;
+        // Sums of 32 keys (`part`), of kChain of those, and of all.
+        float o[kCols], chain[kCols], top = -INFINITY, sum = 0.f, chain_sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) o[c] = 0.f;
+        for (int c = 0; c < kCols; ++c) o[c] = chain[c] = 0.f;
         for (int base = 0; base < seen; base += 32) {
           const int x = base + lane, j = x < first ? x : x - first + lo;
           float s = -INFINITY;
@@ -96,10 +102,20 @@ __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const __grid_cons
           high = fmaxf(high, top);
           const float from = high == -INFINITY ? 0.f : high, keep = ptx::ex2_approx(top - from);
           const float p = x < seen ? ptx::ex2_approx(s - from) : 0.f;
-          sum = sum * keep + p;
           top = high;
+          if (keep != 1.f) {  // the same in the whole warp
+            sum *= keep;
+            chain_sum *= keep;
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) o[c] *= keep;
+            for (int c = 0; c < kCols; ++c) {
+              o[c] *= keep;
+              chain[c] *= keep;
+            }
+          }
+          chain_sum += p;
+          float part[kCols];
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) part[c] = 0.f;
           const int n = min(32, seen - base);
           for (int i = 0; i < n; ++i) {
             const float w = __shfl_sync(0xffffffffu, p, i);
@@ -108,9 +124,20 @@ __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const __grid_cons
 #pragma unroll
             for (int c = 0; c < kCols / 2; ++c) {
               const float2 y = unpack2<kHalf>(__ldg(val + c * 32 + lane));
-              o[2 * c] = fmaf(w, y.x, o[2 * c]);
-              o[2 * c + 1] = fmaf(w, y.y, o[2 * c + 1]);
+              part[2 * c] = fmaf(w, y.x, part[2 * c]);
+              part[2 * c + 1] = fmaf(w, y.y, part[2 * c + 1]);
             }
+          }
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) chain[c] += part[c];
+          if (base / 32 % kChain == kChain - 1 || base + 32 >= seen) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+              o[c] += chain[c];
+              chain[c] = 0.f;
+            }
+            sum += chain_sum;
+            chain_sum = 0.f;
           }
         }
 #pragma unroll

@@ -397,3 +397,34 @@ def test_sums_over_very_many_keys(dim, tokens, heads, log_keys, rising, window, 
             assert float(over) <= 0, f"out {float(over):.3e} over its bound"
             over = ((lse[rows, h].double() - ref_lse).abs() - (dim * U * terms + 8 * U * ref_lse.abs() + 64 * U)).max()
             assert float(over) <= 0, f"lse {float(over):.3e} over its bound"
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("flat", [True, False])
+def test_sums_over_many_keys_row_by_row(flat, dim, dtype):
+    # The last value is no number, so the rows before it are done again one by one: constant values (no powers of two)
+    # and, where flat, equal weights.  Bound: half a step of the output, and of 32-bit sums that go over 32 + 724 + 12 terms.
+    n, heads = 1 << 18, 4
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    q = torch.zeros(2, heads, dim, device="cuda", dtype=dtype) if flat else torch.randn(2, heads, dim, generator=g, device="cuda").to(dtype)
+    k = torch.randn(n, 1, dim, generator=g, device="cuda").to(dtype)
+    value = (1 + torch.arange(dim, device="cuda") / dim).to(dtype)
+    v = value.expand(n, 1, dim).contiguous()
+    v[n - 1] = float("nan")
+    plan = B.ddtree_prompt_attention_plan(1, 2, n, heads, 1, dim, dtype)
+    ws = torch.full((B.ddtree_prompt_attention_workspace_size(plan),), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(2, heads, device="cuda")
+    B.ddtree_prompt_attention(plan, q, k, v, torch.tensor([0, 2], dtype=I32, device="cuda"), torch.tensor([0, n], dtype=I32, device="cuda"),
+                              dim ** -0.5, out, ws, lse=lse)
+    assert B.ddtree_verify_mla_check(ws) == 0
+    half = torch.finfo(dtype).eps / 2
+    assert bool(torch.isnan(out[1]).all())
+    # Numerator and denominator each lose at most 768 half steps of 32 bits, and 64 more for the exponentials.
+    over = ((out[0].double() / value.double() - 1).abs() - half - 2 * (768 + 64) * U).max()
+    assert float(over) <= 0, f"{float(over):.3e} over its bound"
+    s = (q[0].double() @ k[:n - 1, 0].double().T) * dim ** -0.5
+    terms = (q[0].double().abs() @ k[:n - 1, 0].double().abs().T).amax(-1) * dim ** -0.5
+    ref = torch.logsumexp(s, -1)
+    over = ((lse[0].double() - ref).abs() - (dim * U * terms + 8 * U * ref.abs() + (768 + 64) * U)).max()
+    assert float(over) <= 0, f"lse {float(over):.3e} over its bound"
