@@ -598,7 +598,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       if constexpr (kLong) l += l_fold * fold_by;
       l += kSplit == 1 ? 0.f : exchange(l);
       // ---- the rows
-      const float by = l == 0.f ? 0.f : 1.f / l;
+      // A row that sees no key (pos < 0) is zero; with nothing but scores of -inf it is 0 / 0.
+      const float by = l == 0.f ? (pos < 0 ? 0.f : NAN) : 1.f / l;
       const int64_t to = it.q0 + token;
       // A lane has a row; where it stores, eight rows of 64 bytes at once, it has a piece of
       // four neighbouring rows (32 rows of 16 bytes at once keep the loads and stores of a
@@ -657,7 +658,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
           if (four[i] >= 0) *reinterpret_cast<uint4*>(a.out + four[i] + c + 8 * (lane & 3)) = piece[i];
       }
       if (valid) {
-        if (a.lse && half == 0) a.lse[to * a.n_heads + head] = l == 0.f ? -INFINITY : (m * scale - kShift + log2f(l)) * 0.6931471805599453f;
+        if (a.lse && half == 0) a.lse[to * a.n_heads + head] = l == 0.f ? (pos < 0 ? -INFINITY : NAN) : (m * scale - kShift + log2f(l)) * 0.6931471805599453f;
         const float2 both = apart(none);
         if (!(both.x + both.y == 0.f)) atomicOr(a.words + k.id, kPromptAgain);
       }

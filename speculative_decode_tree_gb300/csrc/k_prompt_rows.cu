@@ -142,11 +142,12 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_rows_kernel(const __grid_c
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float by = sum == 0.f ? 0.f : 1.f / sum;
+        // As in the other kernel: without a key zero, with nothing but scores of -inf 0 / 0.
+        const float by = sum == 0.f ? (pos < 0 ? 0.f : NAN) : 1.f / sum;
         uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * a.out_stride + head * kDim);
 #pragma unroll
         for (int c = 0; c < kCols / 2; ++c) out[c * 32 + lane] = pack2<kHalf>(o[2 * c] * by, o[2 * c + 1] * by);
-        if (a.lse && lane == 0) a.lse[row * a.n_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        if (a.lse && lane == 0) a.lse[row * a.n_heads + head] = sum == 0.f ? (pos < 0 ? -INFINITY : NAN) : (top + log2f(sum)) * 0.6931471805599453f;
       }
     }
   }

@@ -428,3 +428,22 @@ def test_sums_over_many_keys_row_by_row(flat, dim, dtype):
     ref = torch.logsumexp(s, -1)
     over = ((lse[0].double() - ref).abs() - (dim * U * terms + 8 * U * ref.abs() + (768 + 64) * U)).max()
     assert float(over) <= 0, f"lse {float(over):.3e} over its bound"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("values", [False, True])
+def test_rows_whose_scores_are_all_minus_infinity(values, dim, dtype):
+    # exp(-inf) / 0 is no number; a row that sees no key at all is zero (queries before the first key).
+    for lens, ctx in (([30, 5], [-2, 0]), ([700], [-3])):
+        c = Case(lens, 4, 2, dim, ctx=ctx, dtype=dtype, seed=33)
+        c.q[:, :, 0] = -1.0
+        c.k[c.kp[0]:c.kp[0] + 9, 0, 0] = float("inf")   # the first rows see nothing but such keys
+        c.k[c.kp[0]:c.kp[0] + 9, 0, 1:] = 0.5
+        if values:
+            c.v[c.kp[0] + 12, 0, 3] = float("nan")      # row by row
+        assert c.run() == 0
+        c.compare()
+        first = c.qp[0] - ctx[0]
+        assert bool(torch.isnan(c.out[first:first + 9, :2]).all()) and bool((c.out[c.qp[0]:first] == 0).all())
+        assert bool(torch.isneginf(c.lse[c.qp[0]:first]).all()) and bool(torch.isfinite(c.lse[first + 9:c.qp[1]]).all())
