@@ -26,9 +26,11 @@
 //    infinity in V is a NaN.  Values that no row of the item sees (behind its last
 //    token, between sinks and window: other sequences, memory that nobody wrote)
 //    become zeros in shared memory.  What is left are values that other rows of the
-//    item see: a row whose result is no number marks its item, and a second grid,
-//    placed ahead of time, does marked items row by row (k_prompt_rows.cu).  So only
-//    prompts that hold such values pay for them.
+//    item see: a row whose sum of probabilities is a number and whose result is none
+//    marks its item, and a second grid, placed ahead of time, does marked items row by
+//    row (k_prompt_rows.cu).  So only prompts that hold such values pay for them, and
+//    not for what keys and queries hold: a score that is no number and that a row sees
+//    makes all its outputs so.
 //  - A CTA goes through many items, one launch's worth of CTAs through all: the loading
 //    warp reads the list ahead and hands each item to the others, and loads and first
 //    products of the next one run beside this one's stores (a CTA for each item: 64
@@ -608,8 +610,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       int64_t four[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, out_at, (lane & ~3) + i);
-      // l and O times zero, added up: no number if one of them is none or no end.
-      uint64_t none = pair(l * 0.f, 0.f);
+      // O times zero, added up: no number if one of them is none or no end.
+      uint64_t none = 0;
       const uint64_t by2 = pair(by, by), zero = pair(0.f, 0.f);
       if (n > 0) {
         wait(&sh.result[t], had);
@@ -660,7 +662,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       if (valid) {
         if (a.lse && half == 0) a.lse[to * a.n_heads + head] = l == 0.f ? (pos < 0 ? -INFINITY : NAN) : (m * scale - kShift + log2f(l)) * 0.6931471805599453f;
         const float2 both = apart(none);
-        if (!(both.x + both.y == 0.f)) atomicOr(a.words + k.id, kPromptAgain);
+        // Where l is no number, a score that the row sees is none, and so are all its outputs:
+        // masked keys add zeros to l.
+        if (l * 0.f == 0.f && !(both.x + both.y == 0.f)) atomicOr(a.words + k.id, kPromptAgain);
       }
       before += n;
       had += n > 0;

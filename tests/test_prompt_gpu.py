@@ -447,3 +447,24 @@ def test_rows_whose_scores_are_all_minus_infinity(values, dim, dtype):
         first = c.qp[0] - ctx[0]
         assert bool(torch.isnan(c.out[first:first + 9, :2]).all()) and bool((c.out[c.qp[0]:first] == 0).all())
         assert bool(torch.isneginf(c.lse[c.qp[0]:first]).all()) and bool(torch.isfinite(c.lse[first + 9:c.qp[1]]).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("lens", [[700, 90], [40] * 30])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_keys_and_queries_that_are_no_numbers_cost_no_second_pass(dim, lens, bad):
+    # Rows that see such a key are none, whatever the values are; only values that some rows of an item do not see
+    # have their items done again (a bit in the words behind the status block).
+    def marked(c):
+        words = c.ws[256:256 + 4 * c.plan.max_items].view(I32)
+        return int((words < 0).sum())
+    c = Case(lens, 8, 2, dim, seed=30)
+    c.k[c.kp[0], 0, 3], c.k[c.kp[1] + 20, 1], c.q[c.qp[1] + 5] = bad, bad, bad
+    assert c.run() == 0
+    c.compare()
+    assert marked(c) == 0
+    c = Case(lens, 8, 2, dim, seed=31)
+    c.v[c.kp[0] + 7, 0, 3] = bad
+    assert c.run() == 0
+    c.compare()
+    assert marked(c) > 0
