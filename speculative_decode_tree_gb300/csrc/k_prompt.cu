@@ -43,9 +43,9 @@
 //    16,384 tokens, 16 + 2 heads of 128, 660 and 765).
 //  - Waits are bounded (the plan's wait_limit_us; for the next item 2 s, since a warp
 //    without rows waits there while others work).  A role whose wait expires sets
-//    TIMEOUT, goes on without waiting to the end of its item and leaves; products in
-//    flight are waited for before the tensor memory is given back, copies before the
-//    CTA ends.
+//    TIMEOUT and leaves, the softmax warps at the end of their item, to which they go
+//    on without waiting; products in flight are waited for before the tensor memory is
+//    given back, copies before the CTA ends.
 //
 // Measured: 16,384 tokens of 16 + 2 heads of 128 columns (1.1 Tflop) 650 to 700 us,
 // 1.6 to 1.7 Pflop/s, by the card's power; the products alone take 583.  A pair of
@@ -360,14 +360,18 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
       auto used = [&](int n) { mma_commit(&sh.empty[n % C::kStages]); };
       int n = 0, asked = 0;                      // stages used, items that had queries
       int before[2] = {0, 0}, had[2] = {0, 0};   // key tiles of product tiles, items with any
+      // It leaves where a wait expires: a stage or queries that it gave back without having
+      // waited for them would be filled again while they are on their way.
+      auto all_items = [&] {
       for (int round = 0;; ++round) {
         Work k;
-        if (!take(round, k)) break;
+        if (!take(round, k)) return;
         const PromptItem& it = k.it;
         const int count = k.count(), present = k.n_of[1] > 0 ? 2 : 1;
         if (count == 0) continue;
         wait(&sh.queries, asked);
         landed(n);
+        if (late) return;
         if (elect_one()) {
           for (int t = 0; t < present; ++t)
             if (k.n_of[t] > 0) score(t, before[t], stage_of(n));
@@ -380,6 +384,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
           const uint32_t k_at = stage_of(nk), v_at = stage_of(nv);
           const bool more = i + 1 < count;
           if (more) landed(nk);
+          if (late) return;
           if (C::kBuffers == 2 && more) {  // the next scores go to the other buffer
             if (elect_one()) {
               score(0, before[0] + i + 1, k_at);
@@ -388,6 +393,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
             __syncwarp();
           }
           landed(nv);
+          if (late) return;
           // Values of keys that no row of the item sees become zeros.
           if (!more || i < k.sink_tiles) {
             const int unseen = (i < k.sink_tiles ? k.sinks : it.pos + it.tokens) - k.start<C::kKeys>(i);
@@ -408,6 +414,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
 #pragma unroll
             for (int h = 0; h < C::kKeys / 64; ++h) {
               wait(&sh.weights[w][h], C::kBuffers == 2 ? g >> 1 : g);
+              if (late) return;
               tc_fence_after();
               if (elect_one()) {
                 accumulate(t, g, h, v_at, h > 0 || (kLong ? i % C::kFold > 0 : i > 0));
@@ -427,7 +434,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
           }
           __syncwarp();
         }
-        if (late) break;
         n += 2 * count;
         ++asked;
 #pragma unroll
@@ -436,6 +442,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
           had[t] += k.n_of[t] > 0;
         }
       }
+      };
+      all_items();
       // After an expired wait products may be in flight still.
       if (elect_one()) {
         mma_commit(&sh.drained);
