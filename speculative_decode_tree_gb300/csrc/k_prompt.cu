@@ -79,12 +79,15 @@ struct PromptMaps {
 // The products cut a sum off where it does not fit into 32 bits, always towards zero:
 // 6.3e-9 of it for every key (values of one sign, 2^16 to 2^22 keys), so that a million
 // keys in one sum lost 0.7 %.  Where rows may see more than kLongKeys keys, the form
-// kLong ends the sum in the tensor memory after every kFoldKeys and joins the parts in
+// kRare ends the sum in the tensor memory after every kFoldKeys and joins the parts in
 // the workspace, in 32 bits: 1e-4 of a part at most, 2e-4 where the other form still
 // serves, below half a step of an fp16 probability.  A row's part is 512 bytes or so,
 // and the form's other instructions cost 1.7 % (16,384 tokens of 16 + 2 heads of 128:
 // 714 us for 702 in turn), hence two forms.  Parts of 4,096, 8,192 and 16,384 keys: 748,
 // 728 and 721 us there.  kMostSms: SMs that a plan has room for.
+// kRare serves bounds of waits below kShortNs too: there waits poll, since a try may
+// suspend a thread for longer than such a bound.
+constexpr uint64_t kShortNs = 1000000ull;
 constexpr int kFoldKeys = 16384, kLongKeys = 32768, kMostSms = 160;
 
 // kTiles: product tiles of a CTA.  One tile of 64 or 128 columns leaves room for two
@@ -190,7 +193,7 @@ struct Shared {
   Work items[2];
 };
 
-template <bool kHalf, int kDim, int kTiles, bool kLong>
+template <bool kHalf, int kDim, int kTiles, bool kRare>
 __global__ void __launch_bounds__(Config<kDim, kTiles>::kThreads, Config<kDim, kTiles>::kCtas)
 prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps) {
   using C = Config<kDim, kTiles>;
@@ -252,9 +255,12 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
   __syncthreads();
   const int tile_tokens = a.tile_tokens / kTiles;
   bool late = false;
+  auto try_for = [&](uint64_t* bar, int phase) {
+    return kRare && a.wait_ns < kShortNs ? mbar_poll(bar, phase & 1, a.wait_ns) : mbar_wait(bar, phase & 1, a.wait_ns);
+  };
   auto wait = [&](uint64_t* bar, int phase) {  // by a whole warp
     if (late) return;
-    const bool done = mbar_wait(bar, phase & 1, a.wait_ns);
+    const bool done = try_for(bar, phase);
     if (!__all_sync(0xffffffffu, done)) {
       late = true;
       atomicOr(&sh.word, DDTREE_ST_TIMEOUT);
@@ -265,7 +271,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
   // (2 s at most) as long as no other one has expired.
   auto take = [&](int round, Work& w) {
     if (late) return false;
-    bool done = mbar_wait(&sh.item[round & 1], (round >> 1) & 1, a.wait_ns);
+    bool done = try_for(&sh.item[round & 1], round >> 1);
     if (!__all_sync(0xffffffffu, done)) {
       const uint64_t until = global_timer_ns() + kDrainNs;
       do {
@@ -275,7 +281,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
           atomicOr(&sh.word, DDTREE_ST_TIMEOUT);
           return false;
         }
-        done = mbar_wait(&sh.item[round & 1], (round >> 1) & 1, a.wait_ns);
+        done = try_for(&sh.item[round & 1], round >> 1);
       } while (!__all_sync(0xffffffffu, done));
     }
     w = sh.items[round & 1];
@@ -417,7 +423,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
               if (late) return;
               tc_fence_after();
               if (elect_one()) {
-                accumulate(t, g, h, v_at, h > 0 || (kLong ? i % C::kFold > 0 : i > 0));
+                accumulate(t, g, h, v_at, h > 0 || (kRare && a.folds ? i % C::kFold > 0 : i > 0));
                 if (h == C::kKeys / 64 - 1) {
                   if (C::kBuffers == 2) mma_commit(&sh.products);
                   if (i + 1 == k.n_of[t]) mma_commit(&sh.result[t]);
@@ -493,7 +499,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
         wait(&sh.scores[buffer], C::kBuffers == 2 ? g >> 1 : g);
         tc_fence_after();
         // With one buffer these scores came after the last product, which is complete.
-        const bool anew = kLong && i > 0 && i % C::kFold == 0;
+        const bool anew = kRare && a.folds && i > 0 && i % C::kFold == 0;
         if (anew) {
           // What O is goes to the workspace, and O starts anew.
           if constexpr (C::kBuffers == 2) {  // as below
@@ -605,7 +611,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
         l += sums.x + sums.y;
       }
       const float fold_by = m_fold == -INFINITY ? 0.f : ex2_approx((m_fold - m) * scale);
-      if constexpr (kLong) l += l_fold * fold_by;
+      if constexpr (kRare) l += l_fold * fold_by;
       l += kSplit == 1 ? 0.f : exchange(l);
       // ---- the rows
       // A row that sees no key (pos < 0) is zero; with nothing but scores of -inf it is 0 / 0.
@@ -639,7 +645,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = 0;
         }
-        if (kLong && n > C::kFold) {
+        if (kRare && a.folds && n > C::kFold) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 w = folds[(c / 4 + e) * 128];
@@ -719,7 +725,7 @@ bool make_map(CUtensorMap* map, const uint16_t* base, int dtype, int dim, int he
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kHalf, int kDim, int kTiles, bool kLong>
+template <bool kHalf, int kDim, int kTiles, bool kRare>
 cudaError_t launch_one(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   using C = Config<kDim, kTiles>;
   static_assert(C::kCtas * (C::kSmem + C::kList + sizeof(Shared<kTiles, C::kSplit>) + 1024) <= 228 * 1024 && C::kStages <= 10, "shared memory");
@@ -735,17 +741,17 @@ cudaError_t launch_one(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (device & 63);
   if (!(have.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(prompt_kernel<kHalf, kDim, kTiles, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem + C::kList);
+    e = cudaFuncSetAttribute(prompt_kernel<kHalf, kDim, kTiles, kRare>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem + C::kList);
     if (e != cudaSuccess) return e;
     have.fetch_or(bit, std::memory_order_release);
   }
   const unsigned grid = (unsigned)std::min<int64_t>(a.max_items, (int64_t)std::min(num_sms, kMostSms) * C::kCtas);
-  return launch_early(prompt_kernel<kHalf, kDim, kTiles, kLong>, grid, C::kThreads, C::kSmem + (a.batch + 1) * 4, stream, a, maps);
+  return launch_early(prompt_kernel<kHalf, kDim, kTiles, kRare>, grid, C::kThreads, C::kSmem + (a.batch + 1) * 4, stream, a, maps);
 }
 
 template <bool kHalf, int kDim, int kTiles>
 cudaError_t launch(const PromptArgs& a, int num_sms, cudaStream_t stream) {
-  return a.folds ? launch_one<kHalf, kDim, kTiles, true>(a, num_sms, stream) : launch_one<kHalf, kDim, kTiles, false>(a, num_sms, stream);
+  return a.folds || a.wait_ns < kShortNs ? launch_one<kHalf, kDim, kTiles, true>(a, num_sms, stream) : launch_one<kHalf, kDim, kTiles, false>(a, num_sms, stream);
 }
 
 // Whether sequences are short: rows of an average one.

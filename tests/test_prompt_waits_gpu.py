@@ -35,3 +35,32 @@ def test_short_bounds_end_the_call(lens, dim, dtype):
     c.out, c.lse = out, lse
     if sum(lens) < 2000:
         c.compare()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_expired_waits_are_reported(dim, dtype):
+    # A call whose status is 0 has the bits of a call without a bound, whatever the bound was; of 1 us some do not hold.
+    seen = 0
+    for lens, ctx in (([4000], [0]), ([30] * 40, [0] * 40), ([5, 900, 0, 300], [40] * 4), ([30] * 1000, [0] * 1000), ([2, 70], [40000, 300])):
+        c = Case(lens, 8, 2, dim, ctx=ctx, dtype=dtype, seed=62)
+        c.device()
+        B.ddtree_prompt_attention(*c.args, **c.kw)
+        assert B.ddtree_verify_mla_check(c.ws) == 0
+        out, lse = c.out.clone(), c.lse.clone()
+        for limit in (1, 2, 5, 20, 100, 999, 1000):
+            c.plan.wait_limit_us = limit
+            for _ in range(3):
+                c.out.copy_(c.out0), c.lse.copy_(c.lse0)
+                B.ddtree_prompt_attention(*c.args, **c.kw)
+                bits = B.ddtree_verify_mla_check(c.ws)
+                assert bits in (0, B.DDTREE_ST_TIMEOUT)
+                seen |= bits
+                if bits == 0:
+                    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+        c.plan.wait_limit_us = 0
+        c.out.copy_(c.out0), c.lse.copy_(c.lse0)
+        B.ddtree_prompt_attention(*c.args, **c.kw)
+        assert B.ddtree_verify_mla_check(c.ws) == 0
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+    assert seen == B.DDTREE_ST_TIMEOUT
