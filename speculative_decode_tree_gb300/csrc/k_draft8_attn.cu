@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
         }
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        // The largest element to [2^14, 2^15).
-        const int up = most == 0.f ? 0 : max(-110, min(120, 14 + 127 - (int)(__float_as_uint(most) >> 23)));
+        // The largest element to [2^14, 2^15); of bf16 they reach 2^128.
+        const int up = most == 0.f ? 0 : max(-114, min(120, 14 + 127 - (int)(__float_as_uint(most) >> 23)));
         const float by = __uint_as_float((uint32_t)(up + 127) << 23);
         factor[r] = __uint_as_float((uint32_t)(127 - up) << 23) * a.scale_log2;
 #pragma unroll

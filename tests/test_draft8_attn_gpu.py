@@ -222,6 +222,23 @@ def test_one_large_score_among_many_keys_keeps_the_small_ones():
     assert float(c.out.float().mean()) > 6e-3
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_largest_and_smallest_queries(dim):
+    # Rows are moved into fp16's range by a power of two, from either end of bf16's.
+    for q_scale, scale in ((4e37, 4e-40), (8e37, -2e-40), (1e-36, 1e35)):
+        c = Case([700, 3, 64, 1], 12, 3, dim, seed=dim, q_scale=q_scale, scale=scale)
+        c.q[0, 0, 5] = 3.3e38 if q_scale > 1 else 2.0 ** -126
+        c.q_dev.copy_(c.q)
+        assert c.run() == 0
+        # 256 columns of 8e37 hold one number beyond bf16's range, an infinity: that row is none, and is compared as zero.
+        odd = torch.isinf(c.q).any(-1)
+        assert int(odd.sum()) == (dim == 256 and q_scale == 8e37) and bool(torch.isnan(c.out.cpu()[odd]).all())
+        c.q[odd] = 0
+        c.q_dev.copy_(c.q)
+        assert c.run() == 0
+        c.compare()
+
+
 def test_bad_positions_rows_pages_and_scales():
     c = Case([100, 50, 20, 77], 8, 2, 64, seed=14)
     c.positions[0] = -5
