@@ -132,7 +132,10 @@ DDTREE_API size_t ddtree_draft8_attention_workspace_size(const ddtree_draft8_pla
  * 2^-11) relative to the unit's largest: a row counts down to 2^-34 of that.
  * The sums take p_j unrounded, but lose a key whose weight is below 2^-130 of the
  * largest: value scales of a request's keys are to lie within 2^100 of each
- * other.  An output is rounded once.  Equal inputs give equal bits.
+ * other.  The products cut their sums off at 32 bits, which takes some 4e-9 of
+ * sum p |v| for each key: a warp's sums start anew every 8,192 keys and are added
+ * up, so that this stays below 5e-5.  An output is rounded once.  Equal inputs
+ * give equal bits.
  * Errors: as ddtree_draft_attention.
  */
 DDTREE_API int ddtree_draft8_attention(const ddtree_draft8_plan_t* plan, const void* q,

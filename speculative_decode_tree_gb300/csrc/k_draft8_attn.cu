@@ -59,6 +59,13 @@ constexpr int kRows = 16;       // query heads of a unit
 // relative to moves only when it has grown by more than 2^kGrowth: 2^15 is the
 // largest weight, and one counts down to 2^-34 of it.
 constexpr float kShift = 10.f, kGrowth = 5.f;
+// Products cut their sums off where they do not fit into 32 bits, always towards zero:
+// 4e-9 of it for every key of a warp (values of one sign), which with a million keys in
+// one share was 0.1 % (0.23 % with 256 columns).  So after this many tiles, 8,192 keys of
+// a warp, the sums start anew, and what they were is added up in the workspace.  Where
+// no unit has more tiles, another form leaves that out (61 requests of 0.5k to 16k, 8 x
+// 64 columns: 64.5 us for 66.1 in turn).
+constexpr int kChain = 256;
 
 template <int kDim>
 struct Config {
@@ -83,9 +90,10 @@ struct Record {
 __host__ __device__ inline bool by_unit(const Draft8AttnArgs& a) { return (int64_t)a.n_tokens * a.unit_heads <= a.n_shares; }
 
 // Workspace: status block, per share a status word and a record, then the
-// (maximum, sum) pairs and the rows of two partial units per share.
+// (maximum, sum) pairs and the rows of two partial units per share; and of what a
+// share holds of a long unit (pairs twice, taken in turn).
 struct Layout {
-  int64_t words, records, sums, rows, total;
+  int64_t words, records, sums, rows, held_sums, held_rows, total;
 };
 __host__ __device__ inline Layout layout_of(int dim, int shares) {
   Layout l;
@@ -93,7 +101,9 @@ __host__ __device__ inline Layout layout_of(int dim, int shares) {
   l.records = l.words + ((int64_t)shares * 4 + 255) / 256 * 256;
   l.sums = l.records + ((int64_t)shares * 16 + 255) / 256 * 256;
   l.rows = l.sums + ((int64_t)shares * 2 * kRows * 8 + 255) / 256 * 256;
-  l.total = l.rows + (int64_t)shares * 2 * kRows * dim * 4;
+  l.held_sums = l.rows + (int64_t)shares * 2 * kRows * dim * 4;
+  l.held_rows = l.held_sums + (int64_t)shares * 2 * kRows * 8;
+  l.total = l.held_rows + (int64_t)shares * kRows * dim * 4;
   return l;
 }
 
@@ -165,7 +175,7 @@ __device__ __forceinline__ int first_head(const Draft8AttnArgs& a, int head, int
   return kv * a.group + part * kRows;
 }
 
-template <bool kHalf, int kDim>
+template <bool kHalf, int kDim, bool kLong>
 __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_kernel(const __grid_constant__ Draft8AttnArgs a) {
   using C = Config<kDim>;
   constexpr int kStages = C::kStages, kWarpKeys = C::kWarpKeys, kCols = C::kCols;
@@ -386,11 +396,12 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
   float o[kTilesN][4], top[2], factor[2];
   uint64_t sum[2];
   bool first = true;
-  int rows = 0, head0 = 0;
+  int rows = 0, head0 = 0, chain = 0, held = 0;  // tiles in the sums, times that the unit's sums have gone to the workspace
 
   for (int i = 0; i < count; ++i) {
     const int slot = i % kStages;
     const bool unit_ends = tile + 1 == now.tiles, last = unit_ends || i + 1 == count;
+    const bool joins = last || (kLong && ++chain == kChain);
     if (first) {
       // Queries: columns 16 q4 .. 16 q4 + 15 of every 64, of rows g and g + 8, four of them an instruction.
       head0 = first_head(a, head, rows);
@@ -565,12 +576,12 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
         for (int e = 0; e < 4; ++e) mma(o[4 * w + e], p, b0[e], b1[e]);
       }
     }
-    if (last) {
-      // ---- the unit ends here: the warps' rows are joined through this tile's stages
+    if (joins) {
+      // ---- the unit or a chain ends here: the warps' rows are joined through this tile's stages
       const bool whole = unit_ends && !begun;
       const int64_t piece = 2 * share + (begun ? 0 : 1);
       // The unit's record, where it starts; without units' own, the share's, where the share ends.
-      if (tid == 0 && (unit_records ? !begun : i + 1 == count)) {
+      if (tid == 0 && last && (unit_records ? !begun : i + 1 == count)) {
         Record r;
         r.token = !unit_ends && !begun ? token : -1;
         r.head = head;
@@ -626,6 +637,24 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
           l += w * sum_s[k][row];
           x.x += w * u.x; x.y += w * u.y; x.z += w * u.z; x.w += w * u.w;
         }
+        if (kLong && (held || !last)) {
+          // A long unit's sums so far, the same thread's each time but for the pair.
+          float2* pairs = reinterpret_cast<float2*>(a.ws + ws.held_sums) + (int64_t)share * 2 * kRows + row;
+          float4* at = reinterpret_cast<float4*>(a.ws + ws.held_rows) + ((int64_t)share * kRows + row) * (kDim / 4) + vec;
+          if (held) {
+            const float2 s = pairs[(held & 1) * kRows];
+            const float4 u = *at;
+            const float high = fmaxf(m, s.x), from = high == -INFINITY ? 0.f : high, w = power2(m - from), v = power2(s.x - from);
+            m = high;
+            l = w * l + v * s.y;
+            x.x = w * x.x + v * u.x; x.y = w * x.y + v * u.y; x.z = w * x.z + v * u.z; x.w = w * x.w + v * u.w;
+          }
+          if (!last) {
+            *at = x;
+            if (col == 0) pairs[(held + 1 & 1) * kRows] = make_float2(m, l);
+            continue;
+          }
+        }
         if (whole) {
           const float by = l == 0.f ? 0.f : 1.f / l;
           *reinterpret_cast<uint2*>(a.out + token * a.out_stride + (int64_t)(head0 + row) * kDim + col) =
@@ -638,10 +667,12 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
         }
       }
       all_warps();  // the stages are free again
+      chain = 0;
+      held = last ? 0 : held + 1;
     }
     // ---- the next tile of this stage
     if constexpr (C::kHalves == 2) {
-      if (!last) pair_of_warps();  // the other one has read the scores
+      if (!joins) pair_of_warps();  // the other one has read the scores
     }
 #pragma unroll
     for (int k = 0; k + 1 < kStages; ++k) {
@@ -653,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, Config<kDim>::kCtas) draft8_attn_ker
     commit();
     if (i + kStages + 1 < count) find();
     // ---- and the tile after this one
-    first = last;
+    first = joins;
     if (unit_ends) {
       tile = 0;
       begun = false;
@@ -779,8 +810,8 @@ __global__ void __launch_bounds__(256) draft8_join_kernel(const __grid_constant_
   }
 }
 
-template <bool kHalf, int kDim>
-cudaError_t launch(const Draft8AttnArgs& a, cudaStream_t stream) {
+template <bool kHalf, int kDim, bool kLong>
+cudaError_t launch_form(const Draft8AttnArgs& a, cudaStream_t stream) {
   using C = Config<kDim>;
   // The shared-memory limit belongs to the kernel on a device: set once on each.
   static std::atomic<uint64_t> have{0};
@@ -789,11 +820,11 @@ cudaError_t launch(const Draft8AttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (device & 63);
   if (!(have.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(draft8_attn_kernel<kHalf, kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(draft8_attn_kernel<kHalf, kDim, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     have.fetch_or(bit, std::memory_order_release);
   }
-  e = launch_early(draft8_attn_kernel<kHalf, kDim>, a.n_shares, kThreads, C::kSmem, stream, a);
+  e = launch_early(draft8_attn_kernel<kHalf, kDim, kLong>, a.n_shares, kThreads, C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
   // Rows get CTAs of their own where records are few, for their units have many
   // parts, and where units may have a hundred, a row's columns too (185k single
@@ -806,6 +837,13 @@ cudaError_t launch(const Draft8AttnArgs& a, cudaStream_t stream) {
   if (64 * records <= a.n_shares && (int64_t)records * slice_count * kSplit <= a.n_shares)
     return launch_early(draft8_join_kernel<kHalf, kDim, kSplit>, dim3(records + 1, slice_count, kSplit), 256, 0, stream, a, slice_rows);
   return launch_early(draft8_join_kernel<kHalf, kDim, 1>, dim3(records + 1, slice_count, 1), 256, 0, stream, a, slice_rows);
+}
+
+template <bool kHalf, int kDim>
+cudaError_t launch(const Draft8AttnArgs& a, cudaStream_t stream) {
+  const int64_t of_table = (int64_t)a.table_stride * a.page_size;
+  const int64_t keys = a.window > 0 ? std::min(of_table, (int64_t)a.window + a.n_sinks) : of_table;
+  return keys > (int64_t)kChain * Config<kDim>::kKeys ? launch_form<kHalf, kDim, true>(a, stream) : launch_form<kHalf, kDim, false>(a, stream);
 }
 
 template <bool kHalf>

@@ -239,6 +239,52 @@ def test_largest_and_smallest_queries(dim):
         c.compare()
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim,heads", [(64, 8), (128, 8), (256, 8), (64, 24)])
+@pytest.mark.parametrize("rising", [False, True])
+def test_sums_over_very_many_keys(rising, dim, heads, dtype):
+    # A plan of one SM, so that a share has a million keys.  Values of one sign, so that whatever a long sum loses adds
+    # up.  Bound: half a step of the output; half a step of fp16 of every weight; the products, which cut sums off where
+    # they do not fit into 32 bits, 2^-23 of the sum for every four of the 8,192 keys that a warp sums before they start
+    # anew; 32-bit work as above.
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    n, page, block = 1 << 22, 64, 16
+    pages = n // page
+    k = (torch.randn(pages, page, 1, dim, generator=g, device="cuda", dtype=torch.float16)).to(torch.float8_e4m3fn)
+    v = (torch.rand(pages, page, 1, dim, generator=g, device="cuda", dtype=torch.float16) + 1).to(torch.float8_e4m3fn)
+    scales = [torch.exp2(torch.randint(-1, 2, (pages, page // block, 1), generator=g, device="cuda").float()) for _ in range(2)]
+    q = torch.randn(1, heads, dim, generator=g, device="cuda").to(dtype)
+    order = torch.randperm(pages, generator=g, device="cuda")
+    if rising:
+        q[:, :, 0] = 1.0
+        k.view(torch.uint8)[order, :, 0, 0] = torch.linspace(-400, 400, pages, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)[:, None]
+    cache = B.Draft8Cache(k, v, *scales, block)
+    plan = B.ddtree_draft8_attention_plan(1, heads, cache, dtype, num_sms=1)
+    ws = torch.full((B.ddtree_draft8_attention_workspace_size(plan),), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse, outs = torch.empty_like(q), torch.empty(1, heads, device="cuda"), []
+    for _ in range(2):
+        B.ddtree_draft8_attention(plan, q, cache, order.to(I32)[None].contiguous(), torch.tensor([n - 1], dtype=I32, device="cuda"),
+                                  dim ** -0.5, out, ws, lse=lse)
+        assert B.ddtree_verify_mla_check(ws) == 0
+        outs.append(out.clone())
+    assert torch.equal(*outs)
+    kf, vf = ((c[order, :, 0].float() * s[order].repeat_interleave(block, 1)).view(n, dim) for c, s in ((k, scales[0]), (v, scales[1])))
+    half = torch.finfo(dtype).eps / 2
+    for h in range(heads):
+        s, terms, ref = [], 0.0, 0.0
+        for part in kf.split(1 << 19):
+            s.append((part.double() @ q[0, h].double()) * dim ** -0.5)
+            terms = max(terms, float((part.double().abs() @ q[0, h].double().abs()).max()) * dim ** -0.5)
+        s = torch.cat(s)
+        ref_lse = torch.logsumexp(s, 0)
+        for part, x in zip(vf.split(1 << 19), s.split(1 << 19)):
+            ref = ref + torch.exp(x - ref_lse) @ part.double()
+        score = dim * U * terms + 8 * U
+        over = ((out[0, h].double() - ref).abs() - ref * (half + 2.0 ** -11 + 2048 * 2.0 ** -23 + 2 * (2 * score + 64 * U))).max()
+        assert float(over) <= 0, f"out {float(over):.3e} over its bound"
+        assert abs(float(lse[0, h]) - float(ref_lse)) <= score + 8 * U * abs(float(ref_lse)) + 64 * U
+
+
 def test_bad_positions_rows_pages_and_scales():
     c = Case([100, 50, 20, 77], 8, 2, 64, seed=14)
     c.positions[0] = -5
