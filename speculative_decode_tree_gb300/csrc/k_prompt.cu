@@ -79,16 +79,17 @@ struct PromptMaps {
 // The products cut a sum off where it does not fit into 32 bits, always towards zero:
 // 6.3e-9 of it for every key (values of one sign, 2^16 to 2^22 keys), so that a million
 // keys in one sum lost 0.7 %.  Where rows may see more than kLongKeys keys, the form
-// kRare ends the sum in the tensor memory after every kFoldKeys and joins the parts in
-// the workspace, in 32 bits: 1e-4 of a part at most, 2e-4 where the other form still
-// serves, below half a step of an fp16 probability.  A row's part is 512 bytes or so,
-// and the form's other instructions cost 1.7 % (16,384 tokens of 16 + 2 heads of 128:
-// 714 us for 702 in turn), hence two forms.  Parts of 4,096, 8,192 and 16,384 keys: 748,
-// 728 and 721 us there.  kMostSms: SMs that a plan has room for.
-// kRare serves bounds of waits below kShortNs too: there waits poll, since a try may
-// suspend a thread for longer than such a bound.
-constexpr uint64_t kShortNs = 1000000ull;
+// kLong ends the sum in the tensor memory after every kFoldKeys and joins the parts in
+// the workspace, in 32 bits: 1e-4 of a part at most, 2e-4 where the plain form still
+// serves, below half a step of an fp16 probability.  The form's other instructions cost
+// 1.7 % (16,384 tokens of 16 + 2 heads of 128: 714 us for 702 in turn), hence the plain
+// one.  Parts of 4,096, 8,192 and 16,384 keys: 748, 728 and 721 us there.  kMostSms: SMs
+// that a plan has room for.
 constexpr int kFoldKeys = 16384, kLongKeys = 32768, kMostSms = 160;
+// Bounds of waits below this one take the form kPolls, whose waits never suspend a
+// thread, since a try may do so for longer than such a bound.
+constexpr uint64_t kShortNs = 1000000ull;
+constexpr int kPlain = 0, kLong = 1, kPolls = 2;
 
 // kTiles: product tiles of a CTA.  One tile of 64 or 128 columns leaves room for two
 // CTAs on an SM: short sequences, where a CTA's start and end are most of its time.
@@ -193,7 +194,7 @@ struct Shared {
   Work items[2];
 };
 
-template <bool kHalf, int kDim, int kTiles, bool kRare>
+template <bool kHalf, int kDim, int kTiles, int kForm>
 __global__ void __launch_bounds__(Config<kDim, kTiles>::kThreads, Config<kDim, kTiles>::kCtas)
 prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps) {
   using C = Config<kDim, kTiles>;
@@ -254,9 +255,11 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
   // prompts, and 16,384 tokens of 256 columns took 2,030 in place of 1,680).
   __syncthreads();
   const int tile_tokens = a.tile_tokens / kTiles;
+  // Whether O starts anew every kFold key tiles, and what it was goes to the workspace.
+  const bool folds = kForm == kLong || (kForm == kPolls && a.folds);
   bool late = false;
   auto try_for = [&](uint64_t* bar, int phase) {
-    return kRare && a.wait_ns < kShortNs ? mbar_poll(bar, phase & 1, a.wait_ns) : mbar_wait(bar, phase & 1, a.wait_ns);
+    return kForm == kPolls ? mbar_poll(bar, phase & 1, a.wait_ns) : mbar_wait(bar, phase & 1, a.wait_ns);
   };
   auto wait = [&](uint64_t* bar, int phase) {  // by a whole warp
     if (late) return;
@@ -423,7 +426,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
               if (late) return;
               tc_fence_after();
               if (elect_one()) {
-                accumulate(t, g, h, v_at, h > 0 || (kRare && a.folds ? i % C::kFold > 0 : i > 0));
+                accumulate(t, g, h, v_at, h > 0 || (folds ? i % C::kFold > 0 : i > 0));
                 if (h == C::kKeys / 64 - 1) {
                   if (C::kBuffers == 2) mma_commit(&sh.products);
                   if (i + 1 == k.n_of[t]) mma_commit(&sh.result[t]);
@@ -480,7 +483,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
     };
     const int row_token = t * tile_tokens + row / a.group, row_head = row % a.group;
     int before = 0, had = 0;  // key tiles of the items before, items with any
-    float4* const folds = reinterpret_cast<float4*>(a.folds) + (((int64_t)blockIdx.x * kTiles + t) * kDim + half * kMine) / 4 * 128 + row;
+    float4* const parts = reinterpret_cast<float4*>(a.folds) + (((int64_t)blockIdx.x * kTiles + t) * kDim + half * kMine) / 4 * 128 + row;
     for (int round = 0;; ++round) {
       Work k;
       if (!take(round, k)) break;
@@ -499,7 +502,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
         wait(&sh.scores[buffer], C::kBuffers == 2 ? g >> 1 : g);
         tc_fence_after();
         // With one buffer these scores came after the last product, which is complete.
-        const bool anew = kRare && a.folds && i > 0 && i % C::kFold == 0;
+        const bool anew = folds && i > 0 && i % C::kFold == 0;
         if (anew) {
           // What O is goes to the workspace, and O starts anew.
           if constexpr (C::kBuffers == 2) {  // as below
@@ -513,7 +516,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
             tmem_ld16(o_mem + c, v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float4* at = folds + (c / 4 + e) * 128;
+              float4* at = parts + (c / 4 + e) * 128;
               float4 u = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
               if (i > C::kFold) {  // not the first time
                 const float4 w = *at;
@@ -611,7 +614,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
         l += sums.x + sums.y;
       }
       const float fold_by = m_fold == -INFINITY ? 0.f : ex2_approx((m_fold - m) * scale);
-      if constexpr (kRare) l += l_fold * fold_by;
+      if (folds) l += l_fold * fold_by;
       l += kSplit == 1 ? 0.f : exchange(l);
       // ---- the rows
       // A row that sees no key (pos < 0) is zero; with nothing but scores of -inf it is 0 / 0.
@@ -645,10 +648,10 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Prom
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = 0;
         }
-        if (kRare && a.folds && n > C::kFold) {
+        if (folds && n > C::kFold) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float4 w = folds[(c / 4 + e) * 128];
+            const float4 w = parts[(c / 4 + e) * 128];
             v[4 * e] = __float_as_uint(__uint_as_float(v[4 * e]) + w.x * fold_by);
             v[4 * e + 1] = __float_as_uint(__uint_as_float(v[4 * e + 1]) + w.y * fold_by);
             v[4 * e + 2] = __float_as_uint(__uint_as_float(v[4 * e + 2]) + w.z * fold_by);
@@ -725,7 +728,7 @@ bool make_map(CUtensorMap* map, const uint16_t* base, int dtype, int dim, int he
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kHalf, int kDim, int kTiles, bool kRare>
+template <bool kHalf, int kDim, int kTiles, int kForm>
 cudaError_t launch_one(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   using C = Config<kDim, kTiles>;
   static_assert(C::kCtas * (C::kSmem + C::kList + sizeof(Shared<kTiles, C::kSplit>) + 1024) <= 228 * 1024 && C::kStages <= 10, "shared memory");
@@ -741,17 +744,19 @@ cudaError_t launch_one(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (device & 63);
   if (!(have.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(prompt_kernel<kHalf, kDim, kTiles, kRare>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem + C::kList);
+    e = cudaFuncSetAttribute(prompt_kernel<kHalf, kDim, kTiles, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem + C::kList);
     if (e != cudaSuccess) return e;
     have.fetch_or(bit, std::memory_order_release);
   }
   const unsigned grid = (unsigned)std::min<int64_t>(a.max_items, (int64_t)std::min(num_sms, kMostSms) * C::kCtas);
-  return launch_early(prompt_kernel<kHalf, kDim, kTiles, kRare>, grid, C::kThreads, C::kSmem + (a.batch + 1) * 4, stream, a, maps);
+  return launch_early(prompt_kernel<kHalf, kDim, kTiles, kForm>, grid, C::kThreads, C::kSmem + (a.batch + 1) * 4, stream, a, maps);
 }
 
 template <bool kHalf, int kDim, int kTiles>
 cudaError_t launch(const PromptArgs& a, int num_sms, cudaStream_t stream) {
-  return a.folds || a.wait_ns < kShortNs ? launch_one<kHalf, kDim, kTiles, true>(a, num_sms, stream) : launch_one<kHalf, kDim, kTiles, false>(a, num_sms, stream);
+  return a.wait_ns < kShortNs ? launch_one<kHalf, kDim, kTiles, kPolls>(a, num_sms, stream)
+         : a.folds            ? launch_one<kHalf, kDim, kTiles, kLong>(a, num_sms, stream)
+                              : launch_one<kHalf, kDim, kTiles, kPlain>(a, num_sms, stream);
 }
 
 // Whether sequences are short: rows of an average one.
