@@ -8,10 +8,12 @@
 // It runs behind the tensor-core kernel for the items that one has marked, and
 // costs a call without any 1 to 2 us, most of them beside the other's end.  A key
 // row is read by one lane alone, 16 bytes after 16 bytes, so what bounds it is the
-// latency of those loads, with as many in flight as 120 registers hold (64: 8.1 ms): a
-// NaN in the last value of 16,384 (16 + 2 heads of 128 columns), which marks 512 rows,
-// takes 5.6 ms.  Spreading an item's rows over the CTAs, one for each warp, took it
-// there from 98.
+// latency of those loads: a NaN in the last value of 16,384 (16 + 2 heads of 128
+// columns), which marks 512 rows, takes 6.0 ms, one in the first value, which marks
+// all, 149.  Spreading an item's rows over the CTAs, one for each warp, took the former
+// from 98 to 7.  More registers hold more loads (64, 80 and 118: 8.9, 6.0 and 5.4 ms),
+// but with 118 the CTAs find room later, where the other kernel ends (200 prompts of 20
+// to 30 tokens 31.3 us, with 80 30.7).
 #include "prompt_list.cuh"
 #include "rope.cuh"
 #include "tc_ptx.cuh"
@@ -26,7 +28,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kChain = 724;
 
 template <bool kHalf, int kDim>
-__global__ void __launch_bounds__(kThreads, 2) prompt_rows_kernel(const __grid_constant__ PromptArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) prompt_rows_kernel(const __grid_constant__ PromptArgs a) {
   constexpr int kCols = kDim / 32;  // columns of a lane
   __shared__ int scratch[kWarps + 8];
   __shared__ __align__(16) float query[kWarps][kDim];
