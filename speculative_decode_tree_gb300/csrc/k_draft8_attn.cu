@@ -39,10 +39,15 @@
 //
 // Measured (calls back to back; the share is of the copy rate of 6.7 TB/s): the
 // eight requests above (738 MB) 117 us, 0.94; 61 requests of 0.5k to 16k, 8 x 64
-// columns of fp16 (292 MB) 64 us, 0.68: the issue slots of an SM are 60 % busy and
-// the conversions' pipe is the next; one of 185k with 2 x 256 columns (194 MB)
-// 45.8, 0.63: some 8 us of it the lists, the joins and the launches; a window of
-// 2,048 at 65k 9.0: steps that wait for each other, in two grids.
+// columns of fp16 (292 MB) 64 to 66 us, 0.67: the issue slots of an SM are 60 % busy
+// and the conversions' pipe is the next, and rows 8 to 15 of a product, empty here,
+// are computed as well; one of 185k with 2 x 256 columns (194 MB) 46, 0.63: some 8 us
+// of it the lists, the joins and the launches; a window of 2,048 at 65k 9.1, where the
+// 16-bit kernel takes 8.3: steps that wait for each other, in two grids, and no bytes
+// to save.  Every 16 query heads of a key head convert its codes again: eight requests
+// of 65,536, 32,768 and 16,384 keys (8 x 64, 8 x 128 and 4 x 256 columns) take 106, 96
+// and 62 us with 16 heads a key head (16 bits 161, 158, 89), 199, 154 and 91 with 32
+// (181, 168, 97) and 385, 293 and 165 with 64 (195, 172, 100, on tensor memory).
 #include <atomic>
 
 #include "f32x2.cuh"
@@ -826,9 +831,13 @@ cudaError_t launch_form(const Draft8AttnArgs& a, cudaStream_t stream) {
   }
   e = launch_early(draft8_attn_kernel<kHalf, kDim, kLong>, a.n_shares, kThreads, C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
-  // Rows get CTAs of their own where records are few, for their units have many
-  // parts, and where units may have a hundred, a row's columns too (185k single
-  // 51.9 -> 46.1 us; a window of 2,048, with 17 parts, 9.3 -> 9.6, so not there).
+  // Rows get CTAs of their own where records are few, for their units may have many
+  // parts, and where they may have 64, a row's columns too: 185k single, 2 x 256
+  // columns, 51.9 -> 46.1 us.  How many there are depends on lengths, which are on the
+  // device, so the rule goes by the units: one request of 1 or 2 key heads of 128
+  // columns loses 0.3 to 0.5 us by it with a window of 2,048 (7.4 -> 7.7 to 8.0), none
+  // with 8,192 (8.6 and 9.0 -> 8.3 and 8.9), and gains at 65,536 keys (16.6 and 15.6 ->
+  // 12.4 and 13.5); 256 columns gain from 2,048 keys on.
   const int records = by_unit(a) ? a.n_tokens * a.unit_heads : a.n_shares;
   const int rows = std::min(kRows, a.group);
   const int slices = std::max(1, std::min(rows, a.n_shares / records));

@@ -35,23 +35,26 @@
 //    warp reads the list ahead and hands each item to the others, and loads and first
 //    products of the next one run beside this one's stores (a CTA for each item: 64
 //    prompts of 1 to 251 tokens 36.3 us, chunks 252; so 33.0 and 237, and with rows
-//    that leave as 64-byte pieces 29.1 and 228).
+//    that leave as 64-byte pieces 29.1 and 228; by now 25 to 27 and 219 to 233).
 //  - Short sequences take one tile a CTA, two CTAs an SM, and two threads for a row,
-//    where an average sequence has fewer than 1,024 rows (32 + 8 heads of 128; 200
-//    prompts of 20 to 30 tokens 31 us, with two tiles 40; 64 of 150 47 and 48);
-//    long ones want the two tiles (64 of 300 to 500 tokens 129 us, with one 154;
-//    16,384 tokens, 16 + 2 heads of 128, 660 and 765).
+//    where the plan's buffer has fewer than 1,024 rows (tokens times group) for each of
+//    its sequences; how many come is known on the device alone (32 + 8 heads of 128; 200
+//    prompts of 20 to 30 tokens 31 us, with two tiles, as in a buffer of 65,536 tokens,
+//    40 to 43; 64 of 150 47 and 48).  Long ones want the two tiles (64 of 300 to 500
+//    tokens 129 us, with one 154; 16,384 tokens, 16 + 2 heads of 128, 660 and 765).
 //  - Waits are bounded (the plan's wait_limit_us; for the next item 2 s, since a warp
 //    without rows waits there while others work).  A role whose wait expires sets
 //    TIMEOUT and leaves, the softmax warps at the end of their item, to which they go
 //    on without waiting; products in flight are waited for before the tensor memory is
 //    given back, copies before the CTA ends.
 //
-// Measured: 16,384 tokens of 16 + 2 heads of 128 columns (1.1 Tflop) 650 to 700 us,
-// 1.6 to 1.7 Pflop/s, by the card's power; the products alone take 583.  A pair of
+// Measured: 16,384 tokens of 16 + 2 heads of 128 columns (1.1 Tflop) 689 to 696 us where
+// inputs change, 1.6 Pflop/s, 638 with the same ones again, by the card's power; the
+// products alone take 583.  256 columns take 1,560 to 1,590 us (2.2 Tflop; floor 1,093):
+// one product tile an SM, with nothing but the next scores beside its softmax.  A pair of
 // tiles goes around in 2,600 clocks, of which its products are 2,048: S ready to P
 // stored 1,380, and the rest is P to its products to the next S.  With 64 columns the
-// products are 1,024 of 2,250, and that chain is the bound (16,384 tokens 490 us).
+// products are 1,024 of 2,250, and that chain is the bound (16,384 tokens 473 us).
 // With a CTA for each item it took 517, without any arithmetic in the softmax still
 // 475, with P in columns of its own, so that the next S is made beside the softmax,
 // 560 (the two tiles' softmaxes meet, and one issuing warp's waits are in each
@@ -759,7 +762,7 @@ cudaError_t launch(const PromptArgs& a, int num_sms, cudaStream_t stream) {
                               : launch_one<kHalf, kDim, kTiles, kPlain>(a, num_sms, stream);
 }
 
-// Whether sequences are short: rows of an average one.
+// Whether sequences are short: rows that the buffer has for each.
 bool prompt_short(int batch, int q_rows, int group) { return (int64_t)q_rows * group < (int64_t)batch * kShortRows; }
 
 template <bool kHalf>
